@@ -57,6 +57,8 @@ typedef enum {
 #define IRS_DEVERR_CU_SEQLENS 0x2 /* cu_seqlens not strictly increasing from 0 to T, or a
                                      document longer than max_doc_len; no route was written  */
 #define IRS_DEVERR_TIMEOUT 0x4    /* a bounded on-device wait gave up; outputs are undefined */
+#define IRS_DEVERR_PAGE 0x8       /* a cache length, or a page of the page table, outside the pool; what lies
+                                     there was neither read nor written */
 
 /* Version of this ABI (incremented on incompatible change). */
 int irs_abi_version(void);
@@ -485,6 +487,159 @@ irs_status irs_sparse_gqa_attn_bwd(const void* q, int64_t q_stride_t, int64_t q_
                                    const void* out, const float* lse, const void* dout, int T, int Tk, int Hq,
                                    int Hkv, int Dqk, int Dv, int W, float scale, float* dq, float* dk, float* dv,
                                    int32_t* err_flag, irs_stream_t stream);
+
+/*
+ * Rotary positions of attention heads.
+ *
+ * QSA page, `apply_qsa_rope` (rotary values on a part of the head, the remainder passes
+ * through), here for the attention's own queries and keys, with the angles computed on the
+ * device. For token t at position p = positions[t] and pair i of the rotated part
+ * [start, start + rope_dims) of every head, with the angle a = p * inv_freq[i]:
+ *   y_1 = amplitude * (x_1 cos a - x_2 sin a)
+ *   y_2 = amplitude * (x_2 cos a + x_1 sin a)
+ * layout IRS_ROPE_HALF pairs dims (i, i + rope_dims/2) of the part, IRS_ROPE_INTERLEAVED
+ * (2i, 2i + 1). The other dims are copied. transpose != 0 flips the sign of the sine: the
+ * transposed map, which takes an output gradient to the input gradient. Angles are exact
+ * fractions of a turn (64-bit integers), so positions far beyond 2^24 keep full accuracy;
+ * products are FP32, rounded once to bf16.
+ *
+ * x         bf16, element (t,h,d) at x + t*x_stride_t + h*x_stride_h + d
+ * positions int32 [T] DEVICE, any value
+ * inv_freq  fp64 [rope_dims / 2] DEVICE, radians per token (finite)
+ * out       bf16 by strides; out may be x with x's strides, and no other overlap
+ * sizes: D % 8 == 0, rope_dims a multiple of 16 in [0, D], start % 8 == 0, start + rope_dims
+ *        <= D; strides and pointers keep rows 16-byte aligned; T = 0 does nothing
+ */
+#define IRS_ROPE_HALF 0
+#define IRS_ROPE_INTERLEAVED 1
+irs_status irs_rope(const void* x, int64_t x_stride_t, int64_t x_stride_h, const int32_t* positions,
+                    const double* inv_freq, int T, int H, int D, int rope_dims, int start, int layout,
+                    float amplitude, int transpose, void* out, int64_t out_stride_t, int64_t out_stride_h,
+                    irs_stream_t stream);
+
+/*
+ * New tokens into a paged cache: queries and keys are rotated (as irs_rope), keys and values
+ * written to the tokens' pages.
+ *
+ * The cache is a pool of pages. Page g holds page_size tokens; element (token, head, d) of
+ * the keys is at k_cache + g*kc_stride_p + token*kc_stride_t + head*kc_stride_h + d (values
+ * alike), so both [pages, page_size, Hkv, D] and [pages, Hkv, page_size, D] pools work.
+ * Sequence b's position p lives in page page_table[b*table_stride + p / page_size] at token
+ * p % page_size. The new tokens are rows of q, k and v: sequence b's are
+ * [cu_new[b], cu_new[b+1]) at the positions cache_lens[b], cache_lens[b] + 1, ...
+ * (cu_new NULL: row b is sequence b's only new token, T == B). cache_lens holds the lengths
+ * BEFORE the call and is not changed. Rows behind cu_new[B] are left as they were, in q_out
+ * and k_out too.
+ *
+ * q          bf16 [T, Hq, Dqk] by strides, q_out likewise (may be q); Hq = 0: no queries
+ * k, v       bf16 [T, Hkv, Dqk], [T, Hkv, Dv] by strides
+ * cu_new     NULL or int32 [B + 1] DEVICE, from 0, never falling, at most T
+ * page_table int32 [B, max_pages] DEVICE; only the new tokens' entries are read
+ * rope_dims  0: nothing is rotated (inv_freq may be NULL)
+ * k_out      NULL, or bf16 by strides: the rotated keys a second time, contiguous use
+ * A token whose length or page lies outside the pool (IRS_DEVERR_PAGE) is not written to the
+ * cache. Two tokens of one call must not share a slot: a page that new tokens fall in
+ * belongs to one sequence. A cu_new that falls or passes T sets IRS_DEVERR_CU_SEQLENS.
+ * max_pages * page_size <= 2^30.
+ */
+irs_status irs_paged_rope_append(const void* q, int64_t q_stride_t, int64_t q_stride_h, const void* k,
+                                 int64_t k_stride_t, int64_t k_stride_h, const void* v, int64_t v_stride_t,
+                                 int64_t v_stride_h, const int32_t* cu_new, int T, int B, int Hq, int Hkv, int Dqk,
+                                 int Dv, const int32_t* page_table, int64_t table_stride, int max_pages,
+                                 int num_pages, int page_size, const int32_t* cache_lens, const double* inv_freq,
+                                 int rope_dims, int start, int layout, float amplitude, void* k_cache,
+                                 int64_t kc_stride_p, int64_t kc_stride_t, int64_t kc_stride_h, void* v_cache,
+                                 int64_t vc_stride_p, int64_t vc_stride_t, int64_t vc_stride_h, void* q_out,
+                                 int64_t qo_stride_t, int64_t qo_stride_h, void* k_out, int64_t ko_stride_t,
+                                 int64_t ko_stride_h, int32_t* err_flag, irs_stream_t stream);
+
+/*
+ * paged_gqa_attn_decode: attention of one new token per sequence over a paged cache.
+ *
+ * QSA page, `gathered_qsa_gqa_attention` (attention over routed positions), Step-5 layers
+ * page, `Step5Attention` (keys from a sliding window or from the selection), for the token
+ * at position L - 1 of sequence b, L = cache_lens[b], whose own key and value are already
+ * in the cache (irs_paged_rope_append; lengths AFTER it). It attends
+ *   - route_ids NULL, window 0: every position in [0, L);
+ *   - window > 0: the last `window` positions, and the first `sinks` positions;
+ *   - route_ids: positions of this sequence, -1 padding, next to the window and the first
+ *     tokens where these are not 0 (an entry inside them does not count again; without a
+ *     window the routes stand alone).
+ * With KV head g = h / (Hq/Hkv) and that set R:
+ *   s_r = scale * q[b,h,:] . k_r[g,:],  out = sum_r e^{s_r - m} v_r[g,:] / sum_r e^{s_r - m},
+ *   lse = m + ln sum_r e^{s_r - m}
+ * A sequence with no position (L = 0, or all routes padding) gives out = 0, lse = -inf.
+ * Route entries other than -1 outside [0, L) are padding and set IRS_DEVERR_ROUTE_ID; entries
+ * must be distinct. A length below 0 or past max_pages * page_size reads as 0 and a position
+ * whose page lies outside the pool is skipped; both set IRS_DEVERR_PAGE. Rows of the pool
+ * that no position points at are never read.
+ *
+ * q          bf16 [B, Hq, Dqk] by strides;  caches and page_table as for irs_paged_rope_append
+ * route_ids  NULL or int32 [B, W], row stride route_stride >= W; W = 0 without routes
+ * sizes: Hq % Hkv == 0, Dqk in {64, 128, 192, 256}, Dv in {64, 128, 256}, rows 16-byte
+ *        aligned, max_pages * page_size <= 2^30, W <= 2^24, window and sinks >= 0 (sinks
+ *        need a window or routes), scale > 0 (finite)
+ * out        bf16 [B, Hq, Dv] contiguous;  lse  fp32 [B, Hq] contiguous (may be NULL)
+ * workspace  irs_paged_gqa_attn_decode_workspace_bytes(...) bytes, 256-byte aligned; nothing
+ *            in it outlives the call, and calls that may overlap need one each
+ * Results do not depend on the run: the split over a sequence is fixed by the sizes and the
+ * lengths, and its parts are joined in order.
+ */
+size_t irs_paged_gqa_attn_decode_workspace_bytes(int B, int Hq, int Hkv, int Dv);
+irs_status irs_paged_gqa_attn_decode(const void* q, int64_t q_stride_b, int64_t q_stride_h, const void* k_cache,
+                                     int64_t kc_stride_p, int64_t kc_stride_t, int64_t kc_stride_h,
+                                     const void* v_cache, int64_t vc_stride_p, int64_t vc_stride_t,
+                                     int64_t vc_stride_h, const int32_t* page_table, int64_t table_stride,
+                                     int max_pages, int num_pages, int page_size, const int32_t* cache_lens,
+                                     const int32_t* route_ids, int64_t route_stride, int W, int window, int sinks,
+                                     int B, int Hq, int Hkv, int Dqk, int Dv, float scale, void* out, float* lse,
+                                     void* workspace, size_t workspace_bytes, int32_t* err_flag,
+                                     irs_stream_t stream);
+
+/*
+ * window_gqa_attn_fwd(q, k, v, cu_seqlens, window, sinks, scale) -> out, lse
+ *
+ * Step-5 layers page, `Step5Attention` (layers whose keys come from a sliding window alone),
+ * with the first tokens of each document kept visible. Query t of document [s_d, e_d)
+ * attends the keys s of its document with t - window < s <= t, and those with
+ * s < s_d + sinks, s <= t:
+ *   out = softmax(scale * q.k) v,   lse natural log, as irs_sparse_gqa_attn_fwd.
+ * A masked key or value does not reach a row, whatever it holds (infinities and NaN too).
+ *
+ * q, k, v     bf16 [T, Hq, Dqk], [T, Hkv, Dqk], [T, Hkv, Dv] by strides (rows 16-byte aligned)
+ * cu_seqlens  int32 [ndocs + 1] DEVICE, strictly increasing from 0 to T (IRS_DEVERR_CU_SEQLENS
+ *             otherwise: outputs are then undefined)
+ * sizes: Hq % Hkv == 0, Hq / Hkv <= 128, Dqk in {64, 128, 192}, Dv in {64, 128}, window >= 1,
+ *        0 <= sinks <= 128, scale > 0 (finite); T = 0 does nothing
+ * out  bf16 [T, Hq, Dv] contiguous;  lse  fp32 [T, Hq] contiguous (may be NULL)
+ */
+irs_status irs_window_gqa_attn_fwd(const void* q, int64_t q_stride_t, int64_t q_stride_h, const void* k,
+                                   int64_t k_stride_t, int64_t k_stride_h, const void* v, int64_t v_stride_t,
+                                   int64_t v_stride_h, const int32_t* cu_seqlens, int ndocs, int window, int sinks,
+                                   int T, int Hq, int Hkv, int Dqk, int Dv, float scale, void* out, float* lse,
+                                   int32_t* err_flag, irs_stream_t stream);
+
+/*
+ * window_gqa_attn_bwd: gradients of irs_window_gqa_attn_fwd for the loss sum(out * dout),
+ * from its out and lse (formulas as irs_sparse_gqa_attn_bwd, D = dout . out from the bf16
+ * output). dk and dv sum over the query heads of a KV head and over every query that sees
+ * the key. No atomics: results are the same in every run.
+ *
+ * out, dout  bf16 [T, Hq, Dv] contiguous;  lse  fp32 [T, Hq] contiguous
+ * dq  bf16 [T, Hq, Dqk], dk  bf16 [T, Hkv, Dqk], dv  bf16 [T, Hkv, Dv]: contiguous, 16-byte
+ *     aligned, overwritten (sums in FP32, rounded once)
+ * workspace  irs_window_gqa_attn_bwd_workspace_bytes(...) bytes, 256-byte aligned; nothing
+ *            in it outlives the call, and calls that may overlap need one each
+ * Other arguments as for the forward.
+ */
+size_t irs_window_gqa_attn_bwd_workspace_bytes(int T, int Hq, int Hkv, int Dqk, int Dv, int ndocs, int window,
+                                               int sinks);
+irs_status irs_window_gqa_attn_bwd(const void* q, int64_t q_stride_t, int64_t q_stride_h, const void* k,
+                                   int64_t k_stride_t, int64_t k_stride_h, const void* v, int64_t v_stride_t,
+                                   int64_t v_stride_h, const int32_t* cu_seqlens, int ndocs, int window, int sinks,
+                                   const void* out, const float* lse, const void* dout, int T, int Hq, int Hkv,
+                                   int Dqk, int Dv, float scale, void* dq, void* dk, void* dv, void* workspace,
+                                   size_t workspace_bytes, int32_t* err_flag, irs_stream_t stream);
 
 /*
  * Failure-detection self-test (no counterpart on the reference pages). Launches one

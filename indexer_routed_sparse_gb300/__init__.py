@@ -12,9 +12,15 @@ this package is its thin Python binding. Names follow the C entry points:
 * ``indexer_projection(hidden, weight, Hi, Di) -> (qI, kI, w)``: the indexer's projections
 * ``region_summaries(kI, z, cu_seqlens, c)`` and ``sparse_index_score_topk_summaries``:
   Step-5 learned-logit region summaries and the indexer that scores them
+* ``window_gqa_attn_fwd`` / ``window_gqa_attn_bwd``: attention over a sliding window and the
+  documents' first tokens, and its gradients
+* ``rope`` / ``rope_frequencies``: rotary positions of the attention heads
+* ``paged_rope_append``: new tokens, rotated, into a paged key/value cache
+* ``paged_gqa_attn_decode``: one new token per sequence over that cache
 """
 from ._binding import (  # noqa: F401
     DEVERR_CU_SEQLENS,
+    DEVERR_PAGE,
     DEVERR_ROUTE_ID,
     DEVERR_TIMEOUT,
     LIB_PATH,
@@ -27,8 +33,12 @@ from ._binding import (  # noqa: F401
     index_workspace_bytes,
     indexer_projection,
     lib,
+    paged_gqa_attn_decode,
+    paged_rope_append,
     read_device_errors,
     region_summaries,
+    rope,
+    rope_frequencies,
     sparse_gqa_attn_bwd,
     sparse_gqa_attn_fwd,
     sparse_gqa_attn_fwd_grouped,
@@ -36,4 +46,6 @@ from ._binding import (  # noqa: F401
     sparse_index_score_topk_grouped,
     sparse_index_score_topk_summaries,
     topk_from_scores,
+    window_gqa_attn_bwd,
+    window_gqa_attn_fwd,
 )

@@ -18,7 +18,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libirs.so")
 
 IRS_OK, IRS_ERR_TYPE, IRS_ERR_VALUE, IRS_ERR_RUNTIME = 0, 1, 2, 3
-DEVERR_ROUTE_ID, DEVERR_CU_SEQLENS, DEVERR_TIMEOUT = 0x1, 0x2, 0x4
+DEVERR_ROUTE_ID, DEVERR_CU_SEQLENS, DEVERR_TIMEOUT, DEVERR_PAGE = 0x1, 0x2, 0x4, 0x8
 
 _lib = None
 _lock = threading.Lock()
@@ -65,6 +65,18 @@ _SIGNATURES = {
                                               _I, _I, _I, _I, _I, _I, _I, _F, _P, _P, _P, _P]),
     "irs_sparse_gqa_attn_bwd": (_I, [_P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _P, _P, _P, _I, _I,
                                      _I, _I, _I, _I, _I, _F, _P, _P, _P, _P, _P]),
+    "irs_rope": (_I, [_P, _I64, _I64, _P, _P, _I, _I, _I, _I, _I, _I, _F, _I, _P, _I64, _I64, _P]),
+    "irs_paged_rope_append": (_I, [_P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _I, _I, _I, _I, _I, _I, _P, _I64,
+                                   _I, _I, _I, _P, _P, _I, _I, _I, _F, _P, _I64, _I64, _I64, _P, _I64, _I64, _I64, _P,
+                                   _I64, _I64, _P, _I64, _I64, _P, _P]),
+    "irs_paged_gqa_attn_decode_workspace_bytes": (_SZ, [_I, _I, _I, _I]),
+    "irs_paged_gqa_attn_decode": (_I, [_P, _I64, _I64, _P, _I64, _I64, _I64, _P, _I64, _I64, _I64, _P, _I64, _I, _I, _I,
+                                       _P, _P, _I64, _I, _I, _I, _I, _I, _I, _I, _I, _F, _P, _P, _P, _SZ, _P, _P]),
+    "irs_window_gqa_attn_fwd": (_I, [_P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _I, _I, _I, _I, _I, _I, _I, _I,
+                                     _F, _P, _P, _P, _P]),
+    "irs_window_gqa_attn_bwd_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I, _I, _I, _I]),
+    "irs_window_gqa_attn_bwd": (_I, [_P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _I, _I, _I, _P, _P, _P, _I, _I,
+                                     _I, _I, _I, _F, _P, _P, _P, _P, _SZ, _P, _P]),
     "irs_check_bounded_wait": (_I, [ctypes.c_uint64, _P, _P]),
 }
 
@@ -143,7 +155,8 @@ def check_device_errors(device=None) -> None:
     if v:
         names = [n for b, n in ((DEVERR_ROUTE_ID, "route id out of range"),
                                 (DEVERR_CU_SEQLENS, "malformed cu_seqlens"),
-                                (DEVERR_TIMEOUT, "on-device wait timed out")) if v & b]
+                                (DEVERR_TIMEOUT, "on-device wait timed out"),
+                                (DEVERR_PAGE, "cache length or page outside the pool")) if v & b]
         raise RuntimeError("device reported: " + ", ".join(names))
 
 
@@ -676,3 +689,333 @@ def sparse_gqa_attn_fwd_grouped(q: torch.Tensor, k: torch.Tensor, v: torch.Tenso
         _ptr(out), _ptr(lse), _ptr(err), _stream(dev))
     _check(st, "sparse_gqa_attn_fwd_grouped")
     return out, lse
+
+
+# ---------------------------------------------------------------------------------------
+# Rotary positions, the paged cache and window attention
+# ---------------------------------------------------------------------------------------
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+
+
+def _on(dev: torch.device, fn, *args):
+    """fn(*args) with `dev` as the current device (the library launches on the current one)."""
+    if torch.cuda.current_device() == dev.index:
+        return fn(*args)
+    with torch.cuda.device(dev):
+        return fn(*args)
+
+
+def _st(t: torch.Tensor, dim: int) -> int:
+    """The stride of a dim in elements; 0 where the dim has one entry (its stride is arbitrary)."""
+    return 0 if t.shape[dim] == 1 else t.stride(dim)
+
+
+def _rows(t: torch.Tensor, name: str, ndim: int, dev: torch.device) -> None:
+    """A bf16 tensor whose last dim is contiguous, on `dev`."""
+    _need(t, name, torch.bfloat16, ndim)
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, not {dev}")
+    if t.stride(-1) != 1 and t.shape[-1] != 1:
+        raise ValueError(f"{name} must have unit inner stride")
+
+
+def _ints(t: torch.Tensor, name: str, shape: tuple, dev: torch.device) -> None:
+    """An int32 tensor of this shape (None: any size) with unit inner stride, on `dev`."""
+    _need(t, name, torch.int32, len(shape))
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, not {dev}")
+    if any(n is not None and n != m for n, m in zip(shape, t.shape)) or (t.stride(-1) != 1 and t.shape[-1] > 1):
+        raise ValueError(f"{name} must have shape {tuple('*' if n is None else n for n in shape)} and unit inner "
+                         f"stride, got {tuple(t.shape)}")
+
+
+def _result(t: torch.Tensor | None, name: str, shape: tuple, dtype: torch.dtype, dev: torch.device) -> torch.Tensor:
+    """An output: a fresh contiguous tensor, or the caller's, checked."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    if tuple(t.shape) != shape or t.dtype != dtype or t.device != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {shape} on {dev}")
+    return t
+
+
+def _scratch(t: torch.Tensor | None, nbytes: int, dev: torch.device) -> torch.Tensor:
+    """Scratch of at least nbytes: the caller's where it is large enough, else fresh."""
+    if t is not None:
+        if t.dtype != torch.uint8 or t.device != dev or not t.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous uint8 tensor on {dev}")
+        if t.numel() >= nbytes:
+            return t
+    return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+
+
+def rope_frequencies(rope_dims: int, base: float = 10000.0, *, scaling: str | None = None, factor: float = 1.0,
+                     trained_len: int | None = None, beta_fast: float = 32.0, beta_slow: float = 1.0,
+                     device=None) -> tuple[torch.Tensor, float]:
+    """(inv_freq, amplitude) of rotary positions: inv_freq fp64 [rope_dims / 2], radians per
+    token, and the factor that the rotated values take.
+
+    inv_freq[i] = base^(-2 i / rope_dims). For contexts `factor` times the trained length:
+    scaling "linear" divides every frequency by the factor; "base" raises the base by
+    factor^(n / (n - 2)), n = rope_dims, so that the slowest pair slows by the factor and the
+    fastest keeps its pace; "by_parts" divides the frequency of pairs that turn at most
+    beta_slow times over trained_len tokens, keeps that of pairs that turn at least beta_fast
+    times, goes over linearly in between, and has the amplitude 0.1 ln(factor) + 1.
+    """
+    if rope_dims < 16 or rope_dims % 16:
+        raise ValueError("rope_dims must be a positive multiple of 16")
+    if not (base > 0 and math.isfinite(base)) or not (factor >= 1 and math.isfinite(factor)):
+        raise ValueError("base must be positive and factor at least 1, both finite")
+    if scaling not in (None, "linear", "base", "by_parts"):
+        raise ValueError("scaling must be None, 'linear', 'base' or 'by_parts'")
+    if scaling is None and factor != 1.0:
+        raise ValueError("a factor needs a scaling")
+    n = rope_dims // 2
+    if scaling == "base":
+        base = base * factor ** (rope_dims / (rope_dims - 2))
+    f = torch.tensor([base ** (-i / n) for i in range(n)], dtype=torch.float64)
+    amplitude = 1.0
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "by_parts":
+        if trained_len is None or trained_len < 1 or not beta_fast > beta_slow:
+            raise ValueError("'by_parts' needs trained_len >= 1 and beta_fast > beta_slow")
+        keep = ((trained_len * f / (2 * math.pi) - beta_slow) / (beta_fast - beta_slow)).clamp(0.0, 1.0)
+        f = f * (keep + (1.0 - keep) / factor)
+        amplitude = 0.1 * math.log(factor) + 1.0
+    return f.to(device if device is not None else "cpu"), amplitude
+
+
+def _rope_table(inv_freq: torch.Tensor | None, dev: torch.device) -> int:
+    if inv_freq is None:
+        return 0
+    _need(inv_freq, "inv_freq", torch.float64, 1)
+    if inv_freq.device != dev or not inv_freq.is_contiguous():
+        raise ValueError(f"inv_freq must be a contiguous fp64 [rope_dims / 2] on {dev}")
+    return 2 * inv_freq.numel()
+
+
+def _layout(layout: str) -> int:
+    if layout not in ROPE_LAYOUTS:
+        raise ValueError("layout must be 'half' or 'interleaved'")
+    return ROPE_LAYOUTS[layout]
+
+
+def rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, *, layout: str = "half", start: int = 0,
+         amplitude: float = 1.0, transpose: bool = False, out: torch.Tensor | None = None) -> torch.Tensor:
+    """Rotary positions on the part [start, start + 2 len(inv_freq)) of every head of x.
+
+    x bf16 [T, H, D], positions int32 [T], inv_freq fp64 radians per token of each pair
+    (`rope_frequencies`). layout "half" pairs dims i and i + n/2 of the part, "interleaved"
+    2i and 2i + 1. transpose=True applies the transposed map: the gradient with respect to x
+    from the gradient of the result. out may be x.
+    """
+    _need(x, "x", torch.bfloat16, 3)
+    dev = x.device
+    _rows(x, "x", 3, dev)
+    T, H, D = x.shape
+    _ints(positions, "positions", (T,), dev)
+    if inv_freq is None:
+        raise ValueError("inv_freq is needed")
+    n = _rope_table(inv_freq, dev)
+    if out is None:
+        out = torch.empty((T, H, D), dtype=torch.bfloat16, device=dev)
+    else:
+        _rows(out, "out", 3, dev)
+        if out.shape != x.shape:
+            raise ValueError(f"out must have x's shape {tuple(x.shape)}")
+    st = _on(dev, lib().irs_rope, _ptr(x), _st(x, 0), _st(x, 1), _ptr(positions), _ptr(inv_freq), T, H, D, n, int(start),
+             _layout(layout), float(amplitude), int(bool(transpose)), _ptr(out), _st(out, 0), _st(out, 1), _stream(dev))
+    _check(st, "rope")
+    return out
+
+
+def _pool(k_cache, v_cache, page_table, cache_lens, dev):
+    """(Hkv, Dqk, Dv, B) of a paged cache, its tensors checked."""
+    _rows(k_cache, "k_cache", 4, dev)
+    _rows(v_cache, "v_cache", 4, dev)
+    if k_cache.shape[:3] != v_cache.shape[:3]:
+        raise ValueError(f"shape mismatch: k_cache {tuple(k_cache.shape)} v_cache {tuple(v_cache.shape)}")
+    _ints(page_table, "page_table", (None, None), dev)
+    B = page_table.shape[0]
+    _ints(cache_lens, "cache_lens", (B,), dev)
+    return k_cache.shape[2], k_cache.shape[3], v_cache.shape[3], B
+
+
+def paged_rope_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
+                      v_cache: torch.Tensor, page_table: torch.Tensor, cache_lens: torch.Tensor,
+                      inv_freq: torch.Tensor | None = None, *, cu_new: torch.Tensor | None = None,
+                      layout: str = "half", start: int = 0, amplitude: float = 1.0, q_out: torch.Tensor | None = None,
+                      k_out: torch.Tensor | None = None, err: torch.Tensor | None = None) -> torch.Tensor | None:
+    """Rotate new tokens' queries and keys and write keys and values into a paged cache.
+
+    q bf16 [T, Hq, Dqk] (or None), k [T, Hkv, Dqk], v [T, Hkv, Dv]; k_cache bf16 [pages,
+    page_size, Hkv, Dqk] and v_cache [pages, page_size, Hkv, Dv] by any strides with a
+    contiguous last dim (a [pages, Hkv, page_size, D] pool: pass its transpose(1, 2));
+    page_table int32 [B, max_pages]; cache_lens int32 [B], the lengths BEFORE these tokens
+    (not changed here). cu_new int32 [B + 1]: sequence b's tokens are the rows cu_new[b] ..
+    cu_new[b+1]; without it row b is sequence b's only new token. Rows behind cu_new[B] are
+    left alone. inv_freq None: no rotation. Returns the rotated queries (q_out, which may be
+    q); k_out, if given, also receives the rotated keys.
+    """
+    _need(k, "k", torch.bfloat16, 3)
+    dev = k.device
+    Hkv, Dqk, Dv, B = _pool(k_cache, v_cache, page_table, cache_lens, dev)
+    T = k.shape[0]
+    _rows(k, "k", 3, dev)
+    _rows(v, "v", 3, dev)
+    if tuple(k.shape) != (T, Hkv, Dqk) or tuple(v.shape) != (T, Hkv, Dv):
+        raise ValueError(f"shape mismatch: k {tuple(k.shape)} v {tuple(v.shape)} for a cache of {Hkv} heads of {Dqk} "
+                         f"and {Dv}")
+    Hq, qs, qos, kos = 0, (0, 0), (0, 0), (0, 0)
+    if q is not None:
+        _rows(q, "q", 3, dev)
+        Hq = q.shape[1]
+        if tuple(q.shape) != (T, Hq, Dqk) or Hq < 1:
+            raise ValueError(f"shape mismatch: q {tuple(q.shape)} for {T} tokens of head dim {Dqk}")
+        if q_out is None:
+            q_out = torch.empty((T, Hq, Dqk), dtype=torch.bfloat16, device=dev)
+        _rows(q_out, "q_out", 3, dev)
+        if q_out.shape != q.shape:
+            raise ValueError(f"q_out must have q's shape {tuple(q.shape)}")
+        qs, qos = (_st(q, 0), _st(q, 1)), (_st(q_out, 0), _st(q_out, 1))
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    if k_out is not None:
+        _rows(k_out, "k_out", 3, dev)
+        if k_out.shape != k.shape:
+            raise ValueError(f"k_out must have k's shape {tuple(k.shape)}")
+        kos = (_st(k_out, 0), _st(k_out, 1))
+    if cu_new is not None:
+        _ints(cu_new, "cu_new", (B + 1,), dev)
+    n = _rope_table(inv_freq, dev)
+    if err is None:
+        err = device_error_flag(dev)
+    st = _on(dev, lib().irs_paged_rope_append, _ptr(q), *qs, _ptr(k), _st(k, 0), _st(k, 1), _ptr(v), _st(v, 0),
+             _st(v, 1), _ptr(cu_new), T, B, Hq, Hkv, Dqk, Dv, _ptr(page_table),
+             page_table.stride(0) if B > 1 else page_table.shape[1], page_table.shape[1], k_cache.shape[0],
+             k_cache.shape[1], _ptr(cache_lens), _ptr(inv_freq), n, int(start), _layout(layout), float(amplitude),
+             _ptr(k_cache), _st(k_cache, 0), _st(k_cache, 1), _st(k_cache, 2), _ptr(v_cache), _st(v_cache, 0),
+             _st(v_cache, 1), _st(v_cache, 2), _ptr(q_out), *qos, _ptr(k_out), *kos, _ptr(err), _stream(dev))
+    _check(st, "paged_rope_append")
+    return q_out
+
+
+def paged_gqa_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor,
+                          cache_lens: torch.Tensor, scale: float | None = None, *, window: int = 0, sinks: int = 0,
+                          route_ids: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                          lse: torch.Tensor | None = None, want_lse: bool = True,
+                          workspace: torch.Tensor | None = None,
+                          err: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor | None]:
+    """Attention of one new token per sequence over a paged cache: (out bf16 [B, Hq, Dv],
+    lse fp32 [B, Hq]).
+
+    q bf16 [B, Hq, Dqk]; the cache as for `paged_rope_append`; cache_lens int32 [B], the
+    lengths with the new token (its key and value are in the cache). By default every
+    position is attended; window > 0 keeps the last `window` positions and the first `sinks`;
+    route_ids int32 [B, W] (positions of the sequence, -1 padding) attends those, next to the
+    window and first tokens where they are given. A sequence with nothing to attend gives
+    out = 0 and lse = -inf.
+    """
+    _need(q, "q", torch.bfloat16, 3)
+    dev = q.device
+    _rows(q, "q", 3, dev)
+    Hkv, Dqk, Dv, B = _pool(k_cache, v_cache, page_table, cache_lens, dev)
+    Hq = q.shape[1]
+    if tuple(q.shape) != (B, Hq, Dqk):
+        raise ValueError(f"shape mismatch: q {tuple(q.shape)} for {B} sequences of head dim {Dqk}")
+    W, rs = 0, 0
+    if route_ids is not None:
+        _ints(route_ids, "route_ids", (B, None), dev)
+        W = route_ids.shape[1]
+        rs = route_ids.stride(0) if B > 1 else W
+    if scale is None:
+        scale = 1.0 / math.sqrt(Dqk)
+    out = _result(out, "out", (B, Hq, Dv), torch.bfloat16, dev)
+    if lse is not None or want_lse:
+        lse = _result(lse, "lse", (B, Hq), torch.float32, dev)
+    L = lib()
+    workspace = _scratch(workspace, int(L.irs_paged_gqa_attn_decode_workspace_bytes(B, Hq, Hkv, Dv)), dev)
+    if err is None:
+        err = device_error_flag(dev)
+    st = _on(dev, L.irs_paged_gqa_attn_decode, _ptr(q), _st(q, 0), _st(q, 1), _ptr(k_cache), _st(k_cache, 0),
+             _st(k_cache, 1), _st(k_cache, 2), _ptr(v_cache), _st(v_cache, 0), _st(v_cache, 1), _st(v_cache, 2),
+             _ptr(page_table), page_table.stride(0) if B > 1 else page_table.shape[1], page_table.shape[1],
+             k_cache.shape[0], k_cache.shape[1], _ptr(cache_lens), _ptr(route_ids), rs, W, int(window), int(sinks), B,
+             Hq, Hkv, Dqk, Dv, float(scale), _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(), _ptr(err),
+             _stream(dev))
+    _check(st, "paged_gqa_attn_decode")
+    return out, lse
+
+
+def _window_shapes(q, k, v, cu_seqlens):
+    _need(q, "q", torch.bfloat16, 3)
+    dev = q.device
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        _rows(t, name, 3, dev)
+    T, Hq, Dqk = q.shape
+    Hkv, Dv = k.shape[1], v.shape[2]
+    if tuple(k.shape) != (T, Hkv, Dqk) or tuple(v.shape) != (T, Hkv, Dv):
+        raise ValueError(f"shape mismatch: q {tuple(q.shape)} k {tuple(k.shape)} v {tuple(v.shape)}")
+    _ints(cu_seqlens, "cu_seqlens", (None,), dev)
+    return dev, T, Hq, Hkv, Dqk, Dv
+
+
+def window_gqa_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor, window: int,
+                        scale: float | None = None, *, sinks: int = 0, out: torch.Tensor | None = None,
+                        lse: torch.Tensor | None = None, want_lse: bool = True,
+                        err: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor | None]:
+    """Attention of packed documents over a causal sliding window and the documents' first
+    tokens: (out bf16 [T, Hq, Dv], lse fp32 [T, Hq]).
+
+    q bf16 [T, Hq, Dqk], k [T, Hkv, Dqk], v [T, Hkv, Dv]; cu_seqlens int32 [ndocs + 1]. Query
+    t attends the last `window` tokens of its document up to itself and the document's first
+    `sinks` tokens.
+    """
+    dev, T, Hq, Hkv, Dqk, Dv = _window_shapes(q, k, v, cu_seqlens)
+    if scale is None:
+        scale = 1.0 / math.sqrt(Dqk)
+    out = _result(out, "out", (T, Hq, Dv), torch.bfloat16, dev)
+    if lse is not None or want_lse:
+        lse = _result(lse, "lse", (T, Hq), torch.float32, dev)
+    if err is None:
+        err = device_error_flag(dev)
+    st = _on(dev, lib().irs_window_gqa_attn_fwd, _ptr(q), _st(q, 0), _st(q, 1), _ptr(k), _st(k, 0), _st(k, 1), _ptr(v),
+             _st(v, 0), _st(v, 1), _ptr(cu_seqlens), cu_seqlens.numel() - 1, int(window), int(sinks), T, Hq, Hkv, Dqk,
+             Dv, float(scale), _ptr(out), _ptr(lse), _ptr(err), _stream(dev))
+    _check(st, "window_gqa_attn_fwd")
+    return out, lse
+
+
+def window_gqa_attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor, window: int,
+                        out: torch.Tensor, lse: torch.Tensor, dout: torch.Tensor, scale: float | None = None, *,
+                        sinks: int = 0, dq: torch.Tensor | None = None, dk: torch.Tensor | None = None,
+                        dv: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                        err: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """Gradients of `window_gqa_attn_fwd` for the loss sum(out * dout): (dq, dk, dv), bf16.
+
+    out and lse are the forward's outputs, dout bf16 [T, Hq, Dv] contiguous. The gradients
+    are overwritten, summed in FP32 and rounded once, and equal in every run.
+    """
+    dev, T, Hq, Hkv, Dqk, Dv = _window_shapes(q, k, v, cu_seqlens)
+    for name, t, shape, dtype in (("out", out, (T, Hq, Dv), torch.bfloat16), ("dout", dout, (T, Hq, Dv), torch.bfloat16),
+                                  ("lse", lse, (T, Hq), torch.float32)):
+        _need(t, name, dtype, len(shape))
+        if tuple(t.shape) != shape or t.device != dev or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous with shape {shape} on {dev}")
+    if scale is None:
+        scale = 1.0 / math.sqrt(Dqk)
+    dq = _result(dq, "dq", (T, Hq, Dqk), torch.bfloat16, dev)
+    dk = _result(dk, "dk", (T, Hkv, Dqk), torch.bfloat16, dev)
+    dv = _result(dv, "dv", (T, Hkv, Dv), torch.bfloat16, dev)
+    L = lib()
+    ndocs = cu_seqlens.numel() - 1
+    workspace = _scratch(workspace, int(L.irs_window_gqa_attn_bwd_workspace_bytes(T, Hq, Hkv, Dqk, Dv, ndocs,
+                                                                                  int(window), int(sinks))), dev)
+    if err is None:
+        err = device_error_flag(dev)
+    st = _on(dev, L.irs_window_gqa_attn_bwd, _ptr(q), _st(q, 0), _st(q, 1), _ptr(k), _st(k, 0), _st(k, 1), _ptr(v),
+             _st(v, 0), _st(v, 1), _ptr(cu_seqlens), ndocs, int(window), int(sinks), _ptr(out), _ptr(lse), _ptr(dout), T,
+             Hq, Hkv, Dqk, Dv, float(scale), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(workspace), workspace.numel(), _ptr(err),
+             _stream(dev))
+    _check(st, "window_gqa_attn_bwd")
+    return dq, dk, dv

@@ -7,6 +7,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 
 #include "irs_internal.h"
@@ -822,3 +823,269 @@ extern "C" irs_status irs_check_bounded_wait(uint64_t limit_ns, int32_t* err_fla
   bounded_wait_probe_kernel<<<1, 32, 0, reinterpret_cast<cudaStream_t>(stream)>>>(err_flag, limit_ns);
   return launch_status(cudaGetLastError(), "launching the bounded-wait check");
 }
+
+// =====================================================================================
+// Rotary positions, the paged cache and window attention.
+// =====================================================================================
+namespace {
+
+const __nv_bfloat16* bf(const void* p) { return static_cast<const __nv_bfloat16*>(p); }
+__nv_bfloat16* bf(void* p) { return static_cast<__nv_bfloat16*>(p); }
+
+bool bad_stride(std::initializer_list<int64_t> strides) {
+  for (int64_t s : strides)
+    if (s < 0 || s % 8 != 0) return true;
+  return false;
+}
+
+irs_status check_rope(const double* inv_freq, int D, int rope_dims, int start, int layout, float amplitude) {
+  if (D < 8 || D % 8 != 0 || D > 4096) return fail(IRS_ERR_VALUE, "the head dim must be a multiple of 8 in [8, 4096] (got %d)", D);
+  if (rope_dims < 0 || rope_dims % 16 != 0) return fail(IRS_ERR_VALUE, "rope_dims must be a multiple of 16 (got %d)", rope_dims);
+  if (start < 0 || start % 8 != 0 || rope_dims > D - start)
+    return fail(IRS_ERR_VALUE, "the rotated part [%d, %d + %d) must start at a multiple of 8 inside the head", start, start, rope_dims);
+  if (layout != IRS_ROPE_HALF && layout != IRS_ROPE_INTERLEAVED) return fail(IRS_ERR_VALUE, "unknown rotary layout %d", layout);
+  if (!std::isfinite(amplitude)) return fail(IRS_ERR_VALUE, "amplitude must be finite");
+  if (rope_dims > 0 && (inv_freq == nullptr || (reinterpret_cast<uintptr_t>(inv_freq) & 7u) != 0))
+    return fail(IRS_ERR_VALUE, "inv_freq must be an 8-byte aligned device table");
+  return IRS_OK;
+}
+
+irs_status check_pool(const void* k_cache, const void* v_cache, const int32_t* page_table, const int32_t* cache_lens,
+                      int64_t table_stride, int max_pages, int num_pages, int page_size) {
+  if (max_pages < 1 || num_pages < 1 || page_size < 1)
+    return fail(IRS_ERR_VALUE, "bad pool sizes (max_pages=%d num_pages=%d page_size=%d)", max_pages, num_pages, page_size);
+  if ((long long)max_pages * page_size > (1LL << 30)) return fail(IRS_ERR_VALUE, "max_pages * page_size must be at most 2^30");
+  if (table_stride < max_pages) return fail(IRS_ERR_VALUE, "table_stride must be >= max_pages");
+  if (!k_cache || !v_cache || !page_table || !cache_lens) return fail(IRS_ERR_VALUE, "NULL cache pointer");
+  if (!aligned16(k_cache) || !aligned16(v_cache)) return fail(IRS_ERR_VALUE, "the caches must be 16-byte aligned");
+  return IRS_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+irs_status irs_rope(const void* x, int64_t x_stride_t, int64_t x_stride_h, const int32_t* positions,
+                    const double* inv_freq, int T, int H, int D, int rope_dims, int start, int layout,
+                    float amplitude, int transpose, void* out, int64_t out_stride_t, int64_t out_stride_h,
+                    irs_stream_t stream) {
+  if (T < 0 || H < 1) return fail(IRS_ERR_VALUE, "bad sizes (T=%d H=%d)", T, H);
+  irs_status s = check_rope(inv_freq, D, rope_dims, start, layout, amplitude);
+  if (s != IRS_OK || T == 0) return s;
+  if (!x || !positions || !out) return fail(IRS_ERR_VALUE, "NULL tensor pointer");
+  if (!aligned16(x) || !aligned16(out)) return fail(IRS_ERR_VALUE, "x and out must be 16-byte aligned");
+  if (bad_stride({x_stride_t, x_stride_h, out_stride_t, out_stride_h}))
+    return fail(IRS_ERR_VALUE, "strides must be non-negative multiples of 8 elements (16 bytes)");
+  if (x == out && (x_stride_t != out_stride_t || x_stride_h != out_stride_h))
+    return fail(IRS_ERR_VALUE, "out may be x only with x's strides");
+  DeviceInfo* dev = nullptr;
+  if ((s = current_device(&dev)) != IRS_OK) return s;
+  irs::RopeArgs a{};
+  a.q = bf(x); a.q_st = x_stride_t; a.q_sh = x_stride_h;
+  a.q_out = bf(out); a.qo_st = out_stride_t; a.qo_sh = out_stride_h;
+  a.positions = positions;
+  a.inv_freq = inv_freq;
+  a.T = T; a.Hq = H; a.D = D; a.rope_dims = rope_dims; a.start = start;
+  a.amplitude = amplitude;
+  a.transpose = transpose != 0;
+  a.in_place = x == out;
+  return launch_status(irs::launch_rope(a, layout == IRS_ROPE_HALF, dev->num_sms, reinterpret_cast<cudaStream_t>(stream)),
+                       "launching the rotation");
+}
+
+irs_status irs_paged_rope_append(const void* q, int64_t q_stride_t, int64_t q_stride_h, const void* k,
+                                 int64_t k_stride_t, int64_t k_stride_h, const void* v, int64_t v_stride_t,
+                                 int64_t v_stride_h, const int32_t* cu_new, int T, int B, int Hq, int Hkv, int Dqk,
+                                 int Dv, const int32_t* page_table, int64_t table_stride, int max_pages,
+                                 int num_pages, int page_size, const int32_t* cache_lens, const double* inv_freq,
+                                 int rope_dims, int start, int layout, float amplitude, void* k_cache,
+                                 int64_t kc_stride_p, int64_t kc_stride_t, int64_t kc_stride_h, void* v_cache,
+                                 int64_t vc_stride_p, int64_t vc_stride_t, int64_t vc_stride_h, void* q_out,
+                                 int64_t qo_stride_t, int64_t qo_stride_h, void* k_out, int64_t ko_stride_t,
+                                 int64_t ko_stride_h, int32_t* err_flag, irs_stream_t stream) {
+  if (T < 0 || B < 1 || Hq < 0 || Hkv < 1) return fail(IRS_ERR_VALUE, "bad sizes (T=%d B=%d Hq=%d Hkv=%d)", T, B, Hq, Hkv);
+  if (cu_new == nullptr && T != B) return fail(IRS_ERR_VALUE, "without cu_new every sequence has one row: T (%d) must be B (%d)", T, B);
+  irs_status s = check_rope(inv_freq, Dqk, rope_dims, start, layout, amplitude);
+  if (s != IRS_OK) return s;
+  if (Dv < 8 || Dv % 8 != 0 || Dv > 4096) return fail(IRS_ERR_VALUE, "Dv must be a multiple of 8 in [8, 4096] (got %d)", Dv);
+  if (T == 0) return IRS_OK;
+  if ((s = check_pool(k_cache, v_cache, page_table, cache_lens, table_stride, max_pages, num_pages, page_size)) != IRS_OK)
+    return s;
+  if (!k || !v || (Hq > 0 && (!q || !q_out))) return fail(IRS_ERR_VALUE, "NULL tensor pointer");
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || !aligned16(k_out))
+    return fail(IRS_ERR_VALUE, "q, k, v, q_out and k_out must be 16-byte aligned");
+  if (bad_stride({q_stride_t, q_stride_h, k_stride_t, k_stride_h, v_stride_t, v_stride_h, kc_stride_p, kc_stride_t,
+                  kc_stride_h, vc_stride_p, vc_stride_t, vc_stride_h, qo_stride_t, qo_stride_h, ko_stride_t, ko_stride_h}))
+    return fail(IRS_ERR_VALUE, "strides must be non-negative multiples of 8 elements (16 bytes)");
+  if (Hq > 0 && q == q_out && (q_stride_t != qo_stride_t || q_stride_h != qo_stride_h))
+    return fail(IRS_ERR_VALUE, "q_out may be q only with q's strides");
+  DeviceInfo* dev = nullptr;
+  if ((s = current_device(&dev)) != IRS_OK) return s;
+  irs::RopeArgs a{};
+  a.q = bf(q); a.q_st = q_stride_t; a.q_sh = q_stride_h;
+  a.k = bf(k); a.k_st = k_stride_t; a.k_sh = k_stride_h;
+  a.v = bf(v); a.v_st = v_stride_t; a.v_sh = v_stride_h;
+  a.inv_freq = inv_freq;
+  a.cu_new = cu_new;
+  a.cache_lens = cache_lens;
+  a.page_table = page_table; a.table_stride = table_stride;
+  a.q_out = bf(q_out); a.qo_st = qo_stride_t; a.qo_sh = qo_stride_h;
+  a.k_out = bf(k_out); a.ko_st = ko_stride_t; a.ko_sh = ko_stride_h;
+  a.k_cache = bf(k_cache); a.kc_sp = kc_stride_p; a.kc_st = kc_stride_t; a.kc_sh = kc_stride_h;
+  a.v_cache = bf(v_cache); a.vc_sp = vc_stride_p; a.vc_st = vc_stride_t; a.vc_sh = vc_stride_h;
+  a.err = err_flag;
+  a.T = T; a.B = B; a.Hq = Hq; a.Hkv = Hkv; a.D = Dqk; a.Dv = Dv;
+  a.rope_dims = rope_dims; a.start = start;
+  a.max_pages = max_pages; a.num_pages = num_pages; a.page_size = page_size;
+  a.amplitude = amplitude;
+  return launch_status(irs::launch_rope(a, layout == IRS_ROPE_HALF, dev->num_sms, reinterpret_cast<cudaStream_t>(stream)),
+                       "launching the cache append");
+}
+
+size_t irs_paged_gqa_attn_decode_workspace_bytes(int B, int Hq, int Hkv, int Dv) {
+  if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Dv < 64) return 0;
+  return irs::paged_workspace_bytes(Dv);
+}
+
+irs_status irs_paged_gqa_attn_decode(const void* q, int64_t q_stride_b, int64_t q_stride_h, const void* k_cache,
+                                     int64_t kc_stride_p, int64_t kc_stride_t, int64_t kc_stride_h,
+                                     const void* v_cache, int64_t vc_stride_p, int64_t vc_stride_t,
+                                     int64_t vc_stride_h, const int32_t* page_table, int64_t table_stride,
+                                     int max_pages, int num_pages, int page_size, const int32_t* cache_lens,
+                                     const int32_t* route_ids, int64_t route_stride, int W, int window, int sinks,
+                                     int B, int Hq, int Hkv, int Dqk, int Dv, float scale, void* out, float* lse,
+                                     void* workspace, size_t workspace_bytes, int32_t* err_flag,
+                                     irs_stream_t stream) {
+  if (B < 0 || Hq < 1 || Hkv < 1) return fail(IRS_ERR_VALUE, "bad sizes (B=%d Hq=%d Hkv=%d)", B, Hq, Hkv);
+  if (Hq % Hkv != 0) return fail(IRS_ERR_VALUE, "Hq (%d) must be a multiple of Hkv (%d)", Hq, Hkv);
+  if (Dqk != 64 && Dqk != 128 && Dqk != 192 && Dqk != 256) return fail(IRS_ERR_VALUE, "Dqk must be 64, 128, 192 or 256 (got %d)", Dqk);
+  if (Dv != 64 && Dv != 128 && Dv != 256) return fail(IRS_ERR_VALUE, "Dv must be 64, 128 or 256 (got %d)", Dv);
+  if ((long long)B * Hq >= (1LL << 24)) return fail(IRS_ERR_VALUE, "B * Hq must be below 2^24");
+  if (window < 0 || sinks < 0 || window > (1 << 30) || sinks > (1 << 30)) return fail(IRS_ERR_VALUE, "window and sinks must be in [0, 2^30]");
+  if (route_ids == nullptr && W != 0) return fail(IRS_ERR_VALUE, "W must be 0 without routes");
+  if (route_ids != nullptr && (W < 1 || W > (1 << 24) || route_stride < W))
+    return fail(IRS_ERR_VALUE, "routes need 1 <= W <= 2^24 and route_stride >= W");
+  if (sinks > 0 && window == 0 && route_ids == nullptr) return fail(IRS_ERR_VALUE, "sinks need a window or routes");
+  if (!(scale > 0.f) || !std::isfinite(scale)) return fail(IRS_ERR_VALUE, "scale must be positive and finite");
+  if (B == 0) return IRS_OK;
+  irs_status s = check_pool(k_cache, v_cache, page_table, cache_lens, table_stride, max_pages, num_pages, page_size);
+  if (s != IRS_OK) return s;
+  if (!q || !out || !workspace) return fail(IRS_ERR_VALUE, "NULL tensor pointer");
+  if (!aligned16(q) || !aligned16(out)) return fail(IRS_ERR_VALUE, "q and out must be 16-byte aligned");
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return fail(IRS_ERR_VALUE, "workspace must be 256-byte aligned");
+  if (workspace_bytes < irs::paged_workspace_bytes(Dv))
+    return fail(IRS_ERR_VALUE, "workspace too small: %zu < %zu bytes", workspace_bytes, irs::paged_workspace_bytes(Dv));
+  if (bad_stride({q_stride_b, q_stride_h, kc_stride_p, kc_stride_t, kc_stride_h, vc_stride_p, vc_stride_t, vc_stride_h}))
+    return fail(IRS_ERR_VALUE, "strides must be non-negative multiples of 8 elements (16 bytes)");
+  DeviceInfo* dev = nullptr;
+  if ((s = current_device(&dev)) != IRS_OK) return s;
+  irs::PagedArgs a{};
+  a.q = bf(q); a.q_sb = q_stride_b; a.q_sh = q_stride_h;
+  a.k = bf(k_cache); a.k_sp = kc_stride_p; a.k_st = kc_stride_t; a.k_sh = kc_stride_h;
+  a.v = bf(v_cache); a.v_sp = vc_stride_p; a.v_st = vc_stride_t; a.v_sh = vc_stride_h;
+  a.page_table = page_table; a.table_stride = table_stride;
+  a.cache_lens = cache_lens;
+  a.route = route_ids; a.route_stride = route_stride;
+  a.out = bf(out);
+  a.lse = lse;
+  a.ws = static_cast<uint8_t*>(workspace);
+  a.err = err_flag;
+  a.B = B; a.Hq = Hq; a.Hkv = Hkv; a.G = Hq / Hkv; a.Dqk = Dqk; a.Dv = Dv;
+  a.W = W; a.window = window; a.sinks = sinks;
+  a.max_pages = max_pages; a.num_pages = num_pages; a.page_size = page_size;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  return launch_status(irs::launch_paged_decode(a, dev->num_sms, reinterpret_cast<cudaStream_t>(stream)),
+                       "launching paged attention");
+}
+
+}  // extern "C"
+
+namespace {
+
+// Checks shared by the window forward and backward; fills the arguments both need.
+irs_status window_args(irs::WinArgs* a, const void* q, int64_t q_stride_t, int64_t q_stride_h, const void* k,
+                       int64_t k_stride_t, int64_t k_stride_h, const void* v, int64_t v_stride_t, int64_t v_stride_h,
+                       const int32_t* cu_seqlens, int ndocs, int window, int sinks, int T, int Hq, int Hkv, int Dqk,
+                       int Dv, float scale, int32_t* err_flag) {
+  if (T < 0 || Hq < 1 || Hkv < 1) return fail(IRS_ERR_VALUE, "bad sizes (T=%d Hq=%d Hkv=%d)", T, Hq, Hkv);
+  if (Hq % Hkv != 0) return fail(IRS_ERR_VALUE, "Hq (%d) must be a multiple of Hkv (%d)", Hq, Hkv);
+  if (Hq / Hkv > 128) return fail(IRS_ERR_VALUE, "at most 128 query heads share a KV head (got %d)", Hq / Hkv);
+  if (Dqk != 64 && Dqk != 128 && Dqk != 192) return fail(IRS_ERR_VALUE, "Dqk must be 64, 128 or 192 (got %d)", Dqk);
+  if (Dv != 64 && Dv != 128) return fail(IRS_ERR_VALUE, "Dv must be 64 or 128 (got %d)", Dv);
+  if (window < 1 || window > (1 << 30)) return fail(IRS_ERR_VALUE, "window must be in [1, 2^30] (got %d)", window);
+  if (sinks < 0 || sinks > 128) return fail(IRS_ERR_VALUE, "sinks must be in [0, 128] (got %d)", sinks);
+  if (!(scale > 0.f) || !std::isfinite(scale)) return fail(IRS_ERR_VALUE, "scale must be positive and finite");
+  if (T > (1 << 30) || (long long)T * Hq >= (1LL << 31)) return fail(IRS_ERR_VALUE, "T * Hq must be below 2^31");
+  if (T == 0) return IRS_OK;
+  if (ndocs < 1 || ndocs > T) return fail(IRS_ERR_VALUE, "ndocs must be in [1, T] (got %d)", ndocs);
+  if (!q || !k || !v || !cu_seqlens) return fail(IRS_ERR_VALUE, "NULL tensor pointer");
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v)) return fail(IRS_ERR_VALUE, "q, k and v must be 16-byte aligned");
+  if (bad_stride({q_stride_t, q_stride_h, k_stride_t, k_stride_h, v_stride_t, v_stride_h}))
+    return fail(IRS_ERR_VALUE, "strides must be non-negative multiples of 8 elements (16 bytes)");
+  a->q = bf(q); a->q_st = q_stride_t; a->q_sh = q_stride_h;
+  a->k = bf(k); a->k_st = k_stride_t; a->k_sh = k_stride_h;
+  a->v = bf(v); a->v_st = v_stride_t; a->v_sh = v_stride_h;
+  a->cu = cu_seqlens; a->ndocs = ndocs;
+  a->T = T; a->Hq = Hq; a->Hkv = Hkv; a->G = Hq / Hkv; a->Dqk = Dqk; a->Dv = Dv;
+  a->window = window; a->sinks = sinks;
+  a->scale = scale;
+  a->scale_log2 = scale * 1.4426950408889634f;
+  a->err = err_flag;
+  return IRS_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+irs_status irs_window_gqa_attn_fwd(const void* q, int64_t q_stride_t, int64_t q_stride_h, const void* k,
+                                   int64_t k_stride_t, int64_t k_stride_h, const void* v, int64_t v_stride_t,
+                                   int64_t v_stride_h, const int32_t* cu_seqlens, int ndocs, int window, int sinks,
+                                   int T, int Hq, int Hkv, int Dqk, int Dv, float scale, void* out, float* lse,
+                                   int32_t* err_flag, irs_stream_t stream) {
+  irs::WinArgs a{};
+  irs_status s = window_args(&a, q, q_stride_t, q_stride_h, k, k_stride_t, k_stride_h, v, v_stride_t, v_stride_h,
+                             cu_seqlens, ndocs, window, sinks, T, Hq, Hkv, Dqk, Dv, scale, err_flag);
+  if (s != IRS_OK || T == 0) return s;
+  if (!out || !aligned16(out)) return fail(IRS_ERR_VALUE, "out must be a 16-byte aligned buffer");
+  DeviceInfo* dev = nullptr;
+  if ((s = current_device(&dev)) != IRS_OK) return s;
+  a.out = bf(out);
+  a.lse = lse;
+  return launch_status(irs::launch_window_fwd(a, reinterpret_cast<cudaStream_t>(stream)), "launching window attention");
+}
+
+size_t irs_window_gqa_attn_bwd_workspace_bytes(int T, int Hq, int Hkv, int Dqk, int Dv, int ndocs, int window,
+                                               int sinks) {
+  if (T < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Dqk < 64 || Dv < 64 || ndocs < 0 || window < 1 || sinks < 0) return 0;
+  return irs::window_bwd_workspace_bytes(T, Hq, Hkv, Dqk, Dv, ndocs, window, sinks);
+}
+
+irs_status irs_window_gqa_attn_bwd(const void* q, int64_t q_stride_t, int64_t q_stride_h, const void* k,
+                                   int64_t k_stride_t, int64_t k_stride_h, const void* v, int64_t v_stride_t,
+                                   int64_t v_stride_h, const int32_t* cu_seqlens, int ndocs, int window, int sinks,
+                                   const void* out, const float* lse, const void* dout, int T, int Hq, int Hkv,
+                                   int Dqk, int Dv, float scale, void* dq, void* dk, void* dv, void* workspace,
+                                   size_t workspace_bytes, int32_t* err_flag, irs_stream_t stream) {
+  irs::WinArgs a{};
+  irs_status s = window_args(&a, q, q_stride_t, q_stride_h, k, k_stride_t, k_stride_h, v, v_stride_t, v_stride_h,
+                             cu_seqlens, ndocs, window, sinks, T, Hq, Hkv, Dqk, Dv, scale, err_flag);
+  if (s != IRS_OK || T == 0) return s;
+  if (!out || !lse || !dout || !dq || !dk || !dv || !workspace) return fail(IRS_ERR_VALUE, "NULL tensor pointer");
+  if (!aligned16(out) || !aligned16(dout) || !aligned16(dq) || !aligned16(dk) || !aligned16(dv))
+    return fail(IRS_ERR_VALUE, "out, dout, dq, dk and dv must be 16-byte aligned");
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return fail(IRS_ERR_VALUE, "workspace must be 256-byte aligned");
+  const size_t need = irs::window_bwd_workspace_bytes(T, Hq, Hkv, Dqk, Dv, ndocs, window, sinks);
+  if (workspace_bytes < need) return fail(IRS_ERR_VALUE, "workspace too small: %zu < %zu bytes", workspace_bytes, need);
+  DeviceInfo* dev = nullptr;
+  if ((s = current_device(&dev)) != IRS_OK) return s;
+  a.out = bf(const_cast<void*>(out));
+  a.lse_in = lse;
+  a.dout = bf(dout);
+  a.delta = static_cast<float*>(workspace);
+  a.dq = bf(dq); a.dk = bf(dk); a.dv = bf(dv);
+  return launch_status(irs::launch_window_bwd(a, reinterpret_cast<cudaStream_t>(stream)),
+                       "launching the window attention backward");
+}
+
+}  // extern "C"

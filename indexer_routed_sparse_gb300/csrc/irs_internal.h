@@ -181,4 +181,123 @@ cudaError_t launch_bwd(const BwdArgs& a, cudaStream_t stream);
 bool bwd_tc_supported(const BwdArgs& a);
 cudaError_t launch_bwd_tc(const BwdArgs& a, unsigned items, cudaStream_t stream);
 
+// Rotary positions, on their own (k_cache == nullptr: H = Hq heads of q) or while new
+// tokens are appended to a paged cache.
+struct RopeArgs {
+  const __nv_bfloat16* q;
+  const __nv_bfloat16* k;
+  const __nv_bfloat16* v;
+  int64_t q_st, q_sh, k_st, k_sh, v_st, v_sh;
+  const int32_t* positions;   // [T] (rope alone)
+  const double* inv_freq;     // [rope_dims / 2] radians per token
+  const int32_t* cu_new;      // [B + 1] or nullptr: token i is sequence i's only new token
+  const int32_t* cache_lens;  // [B] lengths before the new tokens
+  const int32_t* page_table;  // [B, max_pages]
+  int64_t table_stride;
+  __nv_bfloat16* q_out;
+  __nv_bfloat16* k_out;       // nullptr: keys go to the cache only
+  __nv_bfloat16* k_cache;
+  __nv_bfloat16* v_cache;
+  int64_t qo_st, qo_sh, ko_st, ko_sh;
+  int64_t kc_sp, kc_st, kc_sh, vc_sp, vc_st, vc_sh;   // page, token in page, head
+  int32_t* err;
+  int T, B, Hq, Hkv, D, Dv;   // D: head dim of q and k
+  int rope_dims, start;
+  int max_pages, num_pages, page_size;
+  float amplitude;
+  int transpose, in_place;
+  int units, groups;          // set by launch_rope: 16-element units of a token's heads, head groups
+};
+cudaError_t launch_rope(RopeArgs a, bool half, int num_sms, cudaStream_t stream);
+
+// Attention of one new token per sequence over a paged cache.
+struct PagedArgs {
+  const __nv_bfloat16* q;
+  const __nv_bfloat16* k;     // pool [num_pages, page_size, Hkv, Dqk] by strides
+  const __nv_bfloat16* v;
+  int64_t q_sb, q_sh, k_sp, k_st, k_sh, v_sp, v_st, v_sh;
+  const int32_t* page_table;
+  int64_t table_stride;
+  const int32_t* cache_lens;
+  const int32_t* route;       // [B, W] positions or nullptr
+  int64_t route_stride;
+  __nv_bfloat16* out;         // [B, Hq, Dv]
+  float* lse;                 // [B, Hq] or nullptr
+  uint8_t* ws;
+  int32_t* err;
+  int B, Hq, Hkv, G, Dqk, Dv, W, window, sinks;
+  int max_pages, num_pages, page_size;
+  float scale_log2;
+};
+size_t paged_workspace_bytes(int Dv);
+cudaError_t launch_paged_decode(const PagedArgs& a, int num_sms, cudaStream_t stream);
+
+// Attention of packed documents over a sliding window and the documents' first tokens.
+struct WinArgs {
+  const __nv_bfloat16* q;
+  const __nv_bfloat16* k;
+  const __nv_bfloat16* v;
+  int64_t q_st, q_sh, k_st, k_sh, v_st, v_sh;
+  const int32_t* cu;          // [ndocs + 1]
+  int ndocs, T, Hq, Hkv, G, Dqk, Dv, window, sinks;
+  float scale, scale_log2;
+  __nv_bfloat16* out;         // [T, Hq, Dv] (forward: written; backward: read)
+  float* lse;                 // [T, Hq] or nullptr (forward)
+  const float* lse_in;        // [T, Hq] (backward)
+  const __nv_bfloat16* dout;
+  float* delta;               // [T, Hq] scratch: dout . out
+  __nv_bfloat16* dq;
+  __nv_bfloat16* dk;
+  __nv_bfloat16* dv;
+  int32_t* err;
+};
+size_t window_bwd_workspace_bytes(int T, int Hq, int Hkv, int Dqk, int Dv, int ndocs, int window, int sinks);
+cudaError_t launch_window_fwd(const WinArgs& a, cudaStream_t stream);
+cudaError_t launch_window_bwd(const WinArgs& a, cudaStream_t stream);
+
+#ifdef __CUDACC__
+// The document of token t, kept inside [0, T) even where cu is malformed.
+struct WinDoc {
+  int start, end;
+};
+__device__ __forceinline__ WinDoc window_doc(const int32_t* cu, int ndocs, int T, int t) {
+  int lo = 0, hi = ndocs;   // cu[lo] <= t < cu[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (cu[mid] <= t) lo = mid; else hi = mid;
+  }
+  return WinDoc{min(max(cu[lo], 0), t), max(min(cu[lo + 1], T), t + 1)};
+}
+
+// The positions that sequence b's new token attends, in order: `early` first tokens, then
+// `recent` tokens from `first` on, then W routed entries (those inside the first two parts
+// do not count again). A length below 0 or past the page table's reach is reported and read
+// as an empty cache.
+struct PagedSet {
+  int L, early, first, recent, n;
+};
+__device__ __forceinline__ PagedSet paged_set(const PagedArgs& a, int L) {
+  PagedSet s;
+  s.L = (L < 0 || L > a.max_pages * a.page_size) ? 0 : L;   // the product is at most 2^30
+  s.first = (a.window == 0 && a.route == nullptr) ? 0 : a.window > 0 ? max(0, s.L - a.window) : s.L;
+  s.early = min(a.sinks, s.first);
+  s.recent = s.L - s.first;
+  s.n = s.early + s.recent + (s.L > 0 ? a.W : 0);
+  return s;
+}
+// The position of entry j < n, or -1 where it does not count; *bad: a route entry that is
+// neither -1 nor inside [0, L).
+__device__ __forceinline__ int paged_position(const PagedArgs& a, const PagedSet& s, int b, int j, bool* bad) {
+  if (j < s.early) return j;
+  j -= s.early;
+  if (j < s.recent) return s.first + j;
+  const int r = a.route[(int64_t)b * a.route_stride + (j - s.recent)];
+  if (r < 0 || r >= s.L) {
+    if (r != -1) *bad = true;
+    return -1;
+  }
+  return r >= s.early && r < s.first ? r : -1;
+}
+#endif
+
 }  // namespace irs

@@ -1,0 +1,176 @@
+"""Attention over a sliding window and the documents' first tokens, forward and backward, on
+the GPU (through the C ABI), against the 64-bit definition."""
+import math
+
+import pytest
+import torch
+
+import serving_ref as R
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda", 0)
+
+
+@pytest.fixture(scope="module")
+def irs():
+    import indexer_routed_sparse_gb300 as m
+
+    m.lib()
+    return m
+
+
+def _inputs(T, Hq, Hkv, Dqk, Dv, docs, seed=0):
+    g = torch.Generator().manual_seed(seed + T + Hq)
+    n = lambda *s: torch.randn(*s, generator=g).to(torch.bfloat16)  # noqa: E731
+    cu = torch.tensor([0] + docs).cumsum(0).to(torch.int32)
+    assert int(cu[-1]) == T
+    return n(T, Hq, Dqk), n(T, Hkv, Dqk), n(T, Hkv, Dv), n(T, Hq, Dv), cu
+
+
+def _case(irs, q, k, v, do, cu, window, sinks, scale=None, gpu=None):
+    scale = 1 / math.sqrt(q.shape[2]) if scale is None else scale
+    ref = R.window_fwd(q, k, v, cu, window, sinks, scale)
+    qd, kd, vd = gpu if gpu is not None else (q.to(DEV), k.to(DEV), v.to(DEV))
+    cd, dd = cu.to(DEV), do.to(DEV)
+    out, lse = irs.window_gqa_attn_fwd(qd, kd, vd, cd, window, scale, sinks=sinks)
+    irs.check_device_errors(DEV)
+    R.check(out, ref[0], ref[2], "out")
+    R.check(lse, ref[1], ref[3], "lse")
+    got = irs.window_gqa_attn_bwd(qd, kd, vd, cd, window, out, lse, dd, scale, sinks=sinks)
+    irs.check_device_errors(DEV)
+    want = R.window_bwd(q, k, v, cu, window, sinks, scale, out.cpu(), lse.cpu(), do)
+    for name, t in zip(("dq", "dk", "dv"), got):
+        R.check(t, *want[name], name)
+    again = irs.window_gqa_attn_fwd(qd, kd, vd, cd, window, scale, sinks=sinks)
+    grads = irs.window_gqa_attn_bwd(qd, kd, vd, cd, window, out, lse, dd, scale, sinks=sinks)
+    assert all(torch.equal(a, b) for a, b in zip((out, lse) + tuple(got), tuple(again) + tuple(grads)))
+    return out, lse, got
+
+
+@pytest.mark.parametrize("Hq,Hkv,Dqk,Dv", [(1, 1, 64, 64), (8, 2, 128, 128), (6, 2, 192, 128), (3, 3, 128, 64),
+                                           (16, 1, 192, 128), (5, 1, 64, 128), (32, 2, 192, 64), (40, 1, 128, 128)])
+def test_head_shapes(irs, Hq, Hkv, Dqk, Dv):
+    _case(irs, *_inputs(203, Hq, Hkv, Dqk, Dv, [90, 1, 112]), window=37, sinks=3)
+
+
+@pytest.mark.parametrize("docs", [[1], [2], [63], [64], [65], [127, 1], [128, 129], [1] * 40, [500], [3, 400, 7, 90]])
+def test_document_lengths(irs, docs):
+    _case(irs, *_inputs(sum(docs), 4, 2, 128, 128, docs), window=50, sinks=4)
+
+
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (2, 128), (16, 0), (64, 5), (100, 64), (128, 0), (200, 128),
+                                          (299, 1), (300, 4), (5000, 4), (1 << 30, 0)])
+def test_windows_and_first_tokens(irs, window, sinks):
+    _case(irs, *_inputs(420, 4, 2, 128, 128, [120, 300]), window=window, sinks=sinks)
+
+
+def test_long_document_with_first_tokens(irs):
+    """First tokens seen by thousands of queries: their gradients are sums over all of them."""
+    _case(irs, *_inputs(1500, 8, 1, 64, 64, [1490, 10]), window=64, sinks=4)
+
+
+def test_strides_and_broadcast_heads(irs):
+    q, k, v, do, cu = _inputs(150, 8, 2, 128, 128, [100, 50])
+    big = torch.zeros(150, 14, 256, dtype=torch.bfloat16, device=DEV)   # one packed tensor of all heads
+    big[:, :8, :128], big[:, 8:10, 64:192], big[:, 11:13, 128:] = q.to(DEV), k.to(DEV), v.to(DEV)
+    _case(irs, q, k, v, do, cu, 40, 2, gpu=(big[:, :8, :128], big[:, 8:10, 64:192], big[:, 11:13, 128:]))
+    hm = tuple(t.to(DEV).transpose(0, 1).contiguous().transpose(0, 1) for t in (q, k, v))   # head-major rows
+    _case(irs, q, k, v, do, cu, 40, 2, gpu=hm)
+    one_k, one_v = k[:, :1].expand(150, 2, 128), v[:, :1].expand(150, 2, 128)   # stride 0 over the heads
+    _case(irs, q, one_k, one_v, do, cu, 40, 2, gpu=(q.to(DEV), k.to(DEV)[:, :1].expand(150, 2, 128),
+                                                    v.to(DEV)[:, :1].expand(150, 2, 128)))
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_masked_rows_may_hold_anything(irs, bad):
+    """A key, value or output gradient reaches only the rows that see it: all others are within
+    their bounds of the definition on clean inputs."""
+    T, docs, window, sinks = 330, [130, 90, 110], 30, 2
+    q, k, v, do, cu = _inputs(T, 4, 2, 128, 128, docs)
+    dev = lambda *a: [t.to(DEV) for t in a]  # noqa: E731
+    qd, kd, vd, dd, cd = dev(q, k, v, do, cu)
+    scale = 1 / math.sqrt(128)
+    out, lse = irs.window_gqa_attn_fwd(qd, kd, vd, cd, window, sinks=sinks)
+    ref = R.window_fwd(q, k, v, cu, window, sinks, scale)
+    want = R.window_bwd(q, k, v, cu, window, sinks, scale, out.cpu(), lse.cpu(), do)
+    seen = R.window_mask(cu, T, window, sinks)
+
+    def same(t, r, e, rows, what):
+        R.check(t.cpu()[rows], r[rows], e[rows], what)
+
+    for at in (60, 135, 329):                                # mid-document, near a document's start, the last row
+        for which in ("k", "v"):
+            kb, vb = k.clone(), v.clone()
+            (kb if which == "k" else vb)[at] = bad
+            kb, vb = dev(kb, vb)
+            o, l = irs.window_gqa_attn_fwd(qd, kb, vb, cd, window, sinks=sinks)
+            clean = ~seen[:, at]                             # queries that do not see the row
+            same(o, ref[0], ref[2], clean, (at, which, "out"))
+            same(l, ref[1], ref[3], clean, (at, which, "lse"))
+            g = irs.window_gqa_attn_bwd(qd, kb, vb, cd, window, out, lse, dd, sinks=sinks)
+            same(g[0], *want["dq"], clean, (at, which, "dq"))
+            hit = seen[~clean].any(0)                        # keys that share a query with the row
+            same(g[1], *want["dk"], ~hit, (at, which, "dk"))
+            same(g[2], *want["dv"], ~hit, (at, which, "dv"))
+        dob = do.clone()
+        dob[at] = bad
+        g = irs.window_gqa_attn_bwd(qd, kd, vd, cd, window, out, lse, dob.to(DEV), sinks=sinks)
+        same(g[0], *want["dq"], torch.arange(T) != at, (at, "dout", "dq"))
+        same(g[1], *want["dk"], ~seen[at], (at, "dout", "dk"))
+        same(g[2], *want["dv"], ~seen[at], (at, "dout", "dv"))
+
+
+def test_large_scores(irs):
+    q, k, v, do, cu = _inputs(200, 4, 2, 128, 128, [200])
+    _case(irs, q * 20, k, v * 50, do, cu, 70, 4, scale=1.0)
+
+
+def test_malformed_documents_are_reported(irs):
+    q, k, v, do, _ = _inputs(40, 2, 1, 64, 64, [40])
+    dev = [t.to(DEV) for t in (q, k, v)]
+    for cu in ([0, 20, 20, 40], [0, 41], [1, 40], [0, 30, 20, 40], [0, 39]):
+        irs.read_device_errors(DEV)
+        irs.window_gqa_attn_fwd(*dev, torch.tensor(cu, dtype=torch.int32, device=DEV), 8, sinks=2)
+        assert irs.read_device_errors(DEV) & irs.DEVERR_CU_SEQLENS, cu
+
+
+def test_given_outputs_no_lse_and_no_tokens(irs):
+    q, k, v, do, cu = _inputs(100, 4, 2, 64, 64, [60, 40])
+    dev = [t.to(DEV) for t in (q, k, v, cu)]
+    out, lse = irs.window_gqa_attn_fwd(*dev, 20)
+    mine = torch.empty_like(out)
+    o, l = irs.window_gqa_attn_fwd(*dev, 20, out=mine, want_lse=False)
+    assert o is mine and l is None and torch.equal(mine, out)
+    e = torch.empty(0, 4, 64, dtype=torch.bfloat16, device=DEV)
+    o, l = irs.window_gqa_attn_fwd(e, e[:, :2], e[:, :2], torch.zeros(1, dtype=torch.int32, device=DEV), 5)
+    assert o.shape == (0, 4, 64) and l.shape == (0, 4)
+
+
+def test_training_step_captured(irs):
+    """Rotation, attention, its gradients and the rotation's gradient in one graph, replayed on
+    new inputs, equal the same calls made eagerly."""
+    q, k, v, do, cu = _inputs(300, 8, 2, 128, 128, [170, 130])
+    qd, kd, vd, dd, cd = (t.to(DEV) for t in (q, k, v, do, cu))
+    f = irs.rope_frequencies(128)[0].to(DEV)
+    pos = torch.cat([torch.arange(n, dtype=torch.int32) for n in (170, 130)]).to(DEV)
+
+    def step():
+        qr, kr = irs.rope(qd, pos, f), irs.rope(kd, pos, f)
+        out, lse = irs.window_gqa_attn_fwd(qr, kr, vd, cd, 50, sinks=4)
+        dq, dk, dv = irs.window_gqa_attn_bwd(qr, kr, vd, cd, 50, out, lse, dd, sinks=4)
+        return out, irs.rope(dq, pos, f, transpose=True), irs.rope(dk, pos, f, transpose=True), dv
+
+    eager = step()
+    torch.cuda.synchronize()
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        got = step()
+    gr.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, eager))
+    for t in (qd, kd, vd, dd):
+        t.copy_(t.flip(0))
+    gr.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, step()))
+    irs.check_device_errors(DEV)
