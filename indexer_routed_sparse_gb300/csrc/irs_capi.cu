@@ -35,6 +35,7 @@ struct DeviceInfo {
   size_t l2_bytes = 0;
   size_t score_smem = 0, topk_smem = 0, attn_smem = 0, mla_smem = 0, bwd_smem = 0;   // largest configured so far
   bool proj_configured = false;
+  bool paged_configured[irs::kPagedKinds] = {};
 };
 constexpr int kMaxDevices = 64;
 DeviceInfo g_dev[kMaxDevices];
@@ -944,7 +945,7 @@ irs_status irs_paged_rope_append(const void* q, int64_t q_stride_t, int64_t q_st
 
 size_t irs_paged_gqa_attn_decode_workspace_bytes(int B, int Hq, int Hkv, int Dv) {
   if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Dv < 64) return 0;
-  return irs::paged_workspace_bytes(Dv);
+  return irs::paged_workspace_bytes(B, Dv);
 }
 
 irs_status irs_paged_gqa_attn_decode(const void* q, int64_t q_stride_b, int64_t q_stride_h, const void* k_cache,
@@ -973,8 +974,8 @@ irs_status irs_paged_gqa_attn_decode(const void* q, int64_t q_stride_b, int64_t 
   if (!q || !out || !workspace) return fail(IRS_ERR_VALUE, "NULL tensor pointer");
   if (!aligned16(q) || !aligned16(out)) return fail(IRS_ERR_VALUE, "q and out must be 16-byte aligned");
   if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return fail(IRS_ERR_VALUE, "workspace must be 256-byte aligned");
-  if (workspace_bytes < irs::paged_workspace_bytes(Dv))
-    return fail(IRS_ERR_VALUE, "workspace too small: %zu < %zu bytes", workspace_bytes, irs::paged_workspace_bytes(Dv));
+  if (workspace_bytes < irs::paged_workspace_bytes(B, Dv))
+    return fail(IRS_ERR_VALUE, "workspace too small: %zu < %zu bytes", workspace_bytes, irs::paged_workspace_bytes(B, Dv));
   if (bad_stride({q_stride_b, q_stride_h, kc_stride_p, kc_stride_t, kc_stride_h, vc_stride_p, vc_stride_t, vc_stride_h}))
     return fail(IRS_ERR_VALUE, "strides must be non-negative multiples of 8 elements (16 bytes)");
   DeviceInfo* dev = nullptr;
@@ -994,7 +995,8 @@ irs_status irs_paged_gqa_attn_decode(const void* q, int64_t q_stride_b, int64_t 
   a.W = W; a.window = window; a.sinks = sinks;
   a.max_pages = max_pages; a.num_pages = num_pages; a.page_size = page_size;
   a.scale_log2 = scale * 1.4426950408889634f;
-  return launch_status(irs::launch_paged_decode(a, dev->num_sms, reinterpret_cast<cudaStream_t>(stream)),
+  std::lock_guard<std::mutex> lk(g_dev_mu);
+  return launch_status(irs::launch_paged_decode(a, dev->num_sms, dev->paged_configured, reinterpret_cast<cudaStream_t>(stream)),
                        "launching paged attention");
 }
 

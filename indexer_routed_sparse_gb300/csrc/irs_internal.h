@@ -229,8 +229,10 @@ struct PagedArgs {
   int max_pages, num_pages, page_size;
   float scale_log2;
 };
-size_t paged_workspace_bytes(int Dv);
-cudaError_t launch_paged_decode(const PagedArgs& a, int num_sms, cudaStream_t stream);
+constexpr int kPagedKinds = 12;   // kernels, by head dims
+size_t paged_workspace_bytes(int B, int Dv);
+// configured[kPagedKinds]: whose shared-memory limit has been raised on this device
+cudaError_t launch_paged_decode(const PagedArgs& a, int num_sms, bool* configured, cudaStream_t stream);
 
 // Attention of packed documents over a sliding window and the documents' first tokens.
 struct WinArgs {
@@ -284,19 +286,6 @@ __device__ __forceinline__ PagedSet paged_set(const PagedArgs& a, int L) {
   s.recent = s.L - s.first;
   s.n = s.early + s.recent + (s.L > 0 ? a.W : 0);
   return s;
-}
-// The position of entry j < n, or -1 where it does not count; *bad: a route entry that is
-// neither -1 nor inside [0, L).
-__device__ __forceinline__ int paged_position(const PagedArgs& a, const PagedSet& s, int b, int j, bool* bad) {
-  if (j < s.early) return j;
-  j -= s.early;
-  if (j < s.recent) return s.first + j;
-  const int r = a.route[(int64_t)b * a.route_stride + (j - s.recent)];
-  if (r < 0 || r >= s.L) {
-    if (r != -1) *bad = true;
-    return -1;
-  }
-  return r >= s.early && r < s.first ? r : -1;
 }
 #endif
 

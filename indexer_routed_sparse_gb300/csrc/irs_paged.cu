@@ -5,7 +5,31 @@
 // routed positions, with the window and the first tokens where they are asked for. With
 // x_j = scale * q.k_j, m = max x_j and l = sum e^{x_j - m}:
 //   out = sum e^{x_j - m} v_j / l,   lse = m + ln l   (no position: out = 0, lse = -inf)
-// Position j lives in row (page_table[b, j / page_size], j % page_size) of the pool.
+// Position j lives in row (page_table[b, j / page_size], j % page_size) of the pool. Parts
+// of a sequence join exactly: with M = max m_i, out = sum e^{m_i - M} o_i / sum e^{m_i - M} l_i.
+//
+// What bounds it. 2 (Dqk + Dv) bytes a position and KV head against 2 G (Dqk + Dv) flops: G
+// flops a byte, so HBM; the tensor cores are used (mma.sync, 16 query heads a tile) because
+// at G = 8 and above FP32 cores would be the bound.
+//
+// Design.
+// * A tile is 16 positions of one KV head. All tiles of the batch (sequence by sequence, head
+//   by head) form one list, and every CTA (one an SM) takes the same number of neighbouring
+//   tiles, so ragged lengths load the SMs equally and one long sequence spreads over all of
+//   them. The list's shape comes from the lengths on the device; nothing is read back.
+// * A warp owns its tiles from load to product: every NW-th tile of the CTA's run, through
+//   its own ring of cp.async stages, with its own running maximum, sum and output in
+//   registers. No barrier stands between tiles, and the copies run on into the next
+//   sequence. Positions, routes and page numbers are looked up two tiles ahead.
+// * At the end of a sequence's run the warps join their parts in shared memory, in warp
+//   order. A run that holds the whole (sequence, head) writes the result; one cut by a CTA
+//   border leaves its part in the workspace, and a second kernel (launched early, waiting for
+//   the first) joins those, in CTA order. No atomics: every run gives the same bits.
+// * The maximum is raised, and the output rescaled, only where a score passes it by 2^8:
+//   weights then stay below 2^8 and sums below 2^8 n, harmless in FP32, and the rescaling of
+//   Dv/2 registers a thread leaves the loop almost entirely.
+// * A weight enters the second product as two bf16 terms (its rounding and the rest), which
+//   keeps 16 bits of it; the extra product costs tensor time that HBM-bound code has.
 #include "irs_internal.h"
 #include "irs_ptx.cuh"
 
@@ -13,73 +37,554 @@ namespace irs {
 
 namespace {
 
-constexpr int kPagedThreads = 128;
+constexpr int kTile = 16;              // positions a tile (two 8-column halves of the score product)
+constexpr int kHeads = 16;             // query heads a tile (rows of the products)
+constexpr int kMaxPagedCtas = 160;
+constexpr float kRaise = 8.f;          // raise the maximum only where a score passes it by 2^8
 
-__device__ __forceinline__ float warp_sum(float x) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
+struct PagedLayout {
+  int warps, stages;
+  uint32_t stage_bytes, mask_off, ml_off, o_off, total;
+};
+
+// Warps and stages for head dims: 8 warps where two stages each fit, 4 otherwise.
+__host__ __device__ constexpr PagedLayout paged_layout(int Dqk, int Dv) {
+  PagedLayout L{};
+  L.stage_bytes = (uint32_t)(kTile * (Dqk + Dv) * 2);
+  L.warps = L.stage_bytes * 16u <= 204800u ? 8 : 4;
+  const int fit = (int)(204800u / (L.stage_bytes * (uint32_t)L.warps));
+  L.stages = fit > 4 ? 4 : fit;
+  L.mask_off = L.stage_bytes * (uint32_t)(L.warps * L.stages);
+  L.ml_off = L.mask_off + 4u * (uint32_t)(L.warps * L.stages);
+  L.o_off = (L.ml_off + 4u * 2u * kHeads * (uint32_t)L.warps + 15u) & ~15u;
+  L.total = L.o_off + 4u * kHeads * 40u * (uint32_t)L.warps;   // 32 columns a warp and round, rows 40 floats apart
+  return L;
 }
 
-// One warp per (sequence, query head).
-__global__ void __launch_bounds__(kPagedThreads) paged_decode_rows_kernel(PagedArgs a) {
-  const int lane = threadIdx.x & 31;
-  const int row = blockIdx.x * (kPagedThreads / 32) + (threadIdx.x >> 5);
-  if (row >= a.B * a.Hq) return;
-  const int b = row / a.Hq, h = row % a.Hq, g = h / a.G;
-  const int L = a.cache_lens[b];
-  const PagedSet set = paged_set(a, L);
-  if (L != set.L && lane == 0) record_error(a.err, IRS_DEVERR_PAGE);
-  bool bad = false;
-  const int nq = a.Dqk >> 6, nv = a.Dv >> 6;
-  float2 q[4], o[4];
-  for (int i = 0; i < nq; ++i)
-    q[i] = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(a.q + (int64_t)b * a.q_sb + (int64_t)h * a.q_sh + 64 * i + 2 * lane));
-  for (int i = 0; i < 4; ++i) o[i] = make_float2(0.f, 0.f);
-  float m = -INFINITY, l = 0.f;
-  for (int j = 0; j < set.n; ++j) {
-    const int pos = paged_position(a, set, b, j, &bad);
-    if (pos < 0) continue;
-    const int pg = pos / a.page_size, off = pos - pg * a.page_size;
-    const int page = a.page_table[(int64_t)b * a.table_stride + pg];
-    if (page < 0 || page >= a.num_pages) {
-      if (lane == 0) record_error(a.err, IRS_DEVERR_PAGE);
-      continue;
-    }
-    const __nv_bfloat16* k = a.k + (int64_t)page * a.k_sp + (int64_t)off * a.k_st + (int64_t)g * a.k_sh;
-    const __nv_bfloat16* v = a.v + (int64_t)page * a.v_sp + (int64_t)off * a.v_st + (int64_t)g * a.v_sh;
-    float s = 0.f;
-    for (int i = 0; i < nq; ++i) {
-      const float2 x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(k + 64 * i + 2 * lane));
-      s = fmaf(q[i].x, x.x, fmaf(q[i].y, x.y, s));
-    }
-    s = warp_sum(s) * a.scale_log2;
-    const float mn = fmaxf(m, s), c = ex2_approx(m - mn), p = ex2_approx(s - mn);
-    m = mn;
-    l = fmaf(l, c, p);
-    for (int i = 0; i < nv; ++i) {
-      const float2 x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(v + 64 * i + 2 * lane));
-      o[i].x = fmaf(p, x.x, o[i].x * c);
-      o[i].y = fmaf(p, x.y, o[i].y * c);
+// Workspace: prefix sums of the sequences' tile counts, then two parts for every CTA.
+__host__ __device__ inline size_t paged_prefix_bytes(int B) { return ((size_t)(B + 1) * 8 + 255) & ~size_t(255); }
+__host__ __device__ inline size_t paged_part_floats(int Dv) { return (size_t)kHeads * (Dv + 2); }
+
+__device__ __forceinline__ int tiles_of(const PagedArgs& a, int L) {
+  const PagedSet s = paged_set(a, L);
+  return (s.n + kTile - 1) / kTile;
+}
+
+// Tiles every CTA takes: an equal share, but at least one for each warp.
+__device__ __forceinline__ int64_t paged_share(int64_t total, int ctas, int warps) {
+  const int64_t q = (total + ctas - 1) / ctas;
+  return q < warps ? warps : q;
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// x and y as bf16 pairs: the rounded values, and what the rounding left.
+__device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+  const float2 f = __bfloat1622float2(h);
+  const __nv_bfloat162 l = __floats2bfloat162_rn(x - f.x, y - f.y);
+  hi = *reinterpret_cast<const uint32_t*>(&h);
+  lo = *reinterpret_cast<const uint32_t*>(&l);
+}
+
+// One place in the list of tiles.
+struct Cursor {
+  int b, hk, tile, nt;   // sequence, (KV head, head block), tile of it, its tile count
+  PagedSet set;
+};
+__device__ __forceinline__ void cursor_open(const PagedArgs& a, Cursor& c) {
+  c.set = paged_set(a, __ldg(a.cache_lens + c.b));
+  c.nt = (c.set.n + kTile - 1) / kTile;
+}
+// Move on to the (sequence, head) that holds c.tile; the list must go on that far.
+__device__ __forceinline__ void cursor_settle(const PagedArgs& a, Cursor& c, int HK) {
+  while (c.tile >= c.nt) {
+    c.tile -= c.nt;
+    if (c.nt == 0 || ++c.hk == HK) {
+      c.hk = 0;
+      if (++c.b >= a.B) { c.b = a.B - 1; c.tile = 0; return; }   // not reached on a list of the right length
+      cursor_open(a, c);
     }
   }
-  if (bad && lane == 0) record_error(a.err, IRS_DEVERR_ROUTE_ID);
-  const float f = l > 0.f ? 1.f / l : l;   // an empty row gives 0; a NaN sum stays NaN
-  for (int i = 0; i < nv; ++i)
-    *reinterpret_cast<__nv_bfloat162*>(a.out + (int64_t)row * a.Dv + 64 * i + 2 * lane) =
-        __floats2bfloat162_rn(o[i].x * f, o[i].y * f);
-  if (a.lse != nullptr && lane == 0) a.lse[row] = fmaf(m, 0.6931471805599453f, logf(l));
+}
+
+template <int DQK, int DV>
+__global__ void __launch_bounds__(32 * paged_layout(DQK, DV).warps, 1) paged_decode_kernel(PagedArgs a, int nhb) {
+  constexpr PagedLayout LY = paged_layout(DQK, DV);
+  constexpr int NW = LY.warps, S = LY.stages, KS = DQK / 16, NV = DV / 8;
+  constexpr int KCH = DQK / 8, VCH = DV / 8;          // 16-byte chunks a row
+  constexpr bool QREG = DQK + DV <= 384;              // the queries stay in registers
+  extern __shared__ __align__(128) uint8_t smem[];
+  uint32_t* masks = reinterpret_cast<uint32_t*>(smem + LY.mask_off);
+  float* sm_ml = reinterpret_cast<float*>(smem + LY.ml_off);
+  float* sm_o = reinterpret_cast<float*>(smem + LY.o_off);
+  __shared__ int64_t scan[32 * NW + 1];
+  __shared__ int64_t start_pre;
+  __shared__ int start_b;
+
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int HK = a.Hkv * nhb;
+
+  // ---- the list of tiles: its length and where this CTA's run starts ----
+  const int per = (a.B + 32 * NW - 1) / (32 * NW);
+  const int bs = min(a.B, tid * per), be = min(a.B, bs + per);
+  {
+    int64_t n = 0;
+    for (int b = bs; b < be; ++b) {
+      const int L = __ldg(a.cache_lens + b);
+      if (blockIdx.x == 0 && (L < 0 || L > a.max_pages * a.page_size)) record_error(a.err, IRS_DEVERR_PAGE);
+      n += tiles_of(a, L);
+    }
+    int64_t x = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) scan[warp] = x;
+    __syncthreads();
+    int64_t base = 0, total = 0;
+    for (int w = 0; w < NW; ++w) {
+      if (w < warp) base += scan[w];
+      total += scan[w];
+    }
+    __syncthreads();
+    scan[tid] = base + x - n;
+    if (tid == 0) { scan[32 * NW] = total; start_b = -1; }
+    __syncthreads();
+  }
+  const int64_t total = scan[32 * NW] * HK;
+  const int64_t share = paged_share(total, (int)gridDim.x, NW);
+  const int64_t f0 = min(total, (int64_t)blockIdx.x * share), f1 = min(total, f0 + share);
+  {
+    int64_t* pre = reinterpret_cast<int64_t*>(a.ws);
+    int64_t n = scan[tid];
+    for (int b = bs; b < be; ++b) {
+      const int64_t next = n + tiles_of(a, __ldg(a.cache_lens + b));
+      if (blockIdx.x == 0) pre[b] = n;
+      if (f0 >= n * HK && f0 < next * HK) { start_b = b; start_pre = n; }
+      n = next;
+    }
+    if (blockIdx.x == 0 && tid == 0) pre[a.B] = scan[32 * NW];
+  }
+  __syncthreads();
+  if (f0 >= f1 || start_b < 0) return;
+
+  Cursor cc;                                            // the segment being computed
+  cc.b = start_b;
+  cursor_open(a, cc);
+  {
+    const int64_t in = f0 - start_pre * HK;
+    cc.hk = (int)(in / cc.nt);
+    cc.tile = (int)(in - (int64_t)cc.hk * cc.nt);
+  }
+
+  // ---- loads: A looks up positions or routes, B pages, C issues the copies ----
+  Cursor lc = cc;
+  int64_t lf = f0 + warp;
+  lc.tile += warp;
+  bool a_route = false;
+  int a_pos = -1, a_b = 0, a_hk = 0, a_lo = 0, a_hi = 0, a_L = 0;
+  int b_pos = -1, b_page = -1, b_off = 0, b_hk = 0;
+  bool a_live = false, b_live = false, bad_route = false, bad_page = false;
+  const int key = lane & 15;
+  auto step_a = [&]() {
+    a_live = lf < f1;
+    a_pos = -1;
+    a_route = false;
+    if (a_live) {
+      cursor_settle(a, lc, HK);
+      a_b = lc.b;
+      a_hk = lc.hk;
+      int j = lc.tile * kTile + key;
+      if (j < lc.set.n) {
+        if (j < lc.set.early) a_pos = j;
+        else if ((j -= lc.set.early) < lc.set.recent) a_pos = lc.set.first + j;
+        else {
+          a_route = true;
+          a_pos = __ldg(a.route + (int64_t)a_b * a.route_stride + (j - lc.set.recent));
+          a_lo = lc.set.early;
+          a_hi = lc.set.first;
+          a_L = lc.set.L;
+        }
+      }
+      lf += NW;
+      lc.tile += NW;
+    }
+  };
+  auto step_b = [&]() {
+    b_live = a_live;
+    b_hk = a_hk;
+    b_pos = a_pos;
+    if (a_route) {
+      if (b_pos < 0 || b_pos >= a_L) {
+        bad_route |= b_pos != -1;
+        b_pos = -1;
+      } else if (b_pos < a_lo || b_pos >= a_hi) {
+        b_pos = -1;
+      }
+    }
+    b_page = -1;
+    if (b_pos >= 0) {
+      const int pg = b_pos / a.page_size;
+      b_off = b_pos - pg * a.page_size;
+      b_page = __ldg(a.page_table + (int64_t)a_b * a.table_stride + pg);
+    }
+  };
+  const uint32_t ring = smem_u32(smem) + (uint32_t)warp * S * LY.stage_bytes;
+  auto step_c = [&](int slot) {
+    if (b_live) {
+      bool ok = b_pos >= 0;
+      if (ok && (b_page < 0 || b_page >= a.num_pages)) { bad_page = true; ok = false; }
+      const int g = b_hk / nhb;
+      const int64_t ko = ok ? (int64_t)b_page * a.k_sp + (int64_t)b_off * a.k_st + (int64_t)g * a.k_sh : 0;
+      const int64_t vo = ok ? (int64_t)b_page * a.v_sp + (int64_t)b_off * a.v_st + (int64_t)g * a.v_sh : 0;
+      const uint32_t m = __ballot_sync(0xffffffffu, ok) & 0xffffu;
+      if (lane == 0) masks[warp * S + slot] = m;
+      const uint32_t kd = ring + (uint32_t)slot * LY.stage_bytes, vd = kd + kTile * DQK * 2;
+#pragma unroll
+      for (int i = 0; i < KCH / 2; ++i) {
+        const int x = i * 32 + lane, row = x / KCH, ch = x % KCH;
+        const int64_t o = __shfl_sync(0xffffffffu, ko, row);
+        cp_async_16(kd + (uint32_t)(row * DQK * 2 + ((ch ^ (row & 7)) << 4)), a.k + o + ch * 8, (m >> row) & 1u ? 16u : 0u);
+      }
+#pragma unroll
+      for (int i = 0; i < VCH / 2; ++i) {
+        const int x = i * 32 + lane, row = x / VCH, ch = x % VCH;
+        const int64_t o = __shfl_sync(0xffffffffu, vo, row);
+        cp_async_16(vd + (uint32_t)(row * DV * 2 + ((ch ^ (row & 7)) << 4)), a.v + o + ch * 8, (m >> row) & 1u ? 16u : 0u);
+      }
+    }
+    cp_async_commit();
+  };
+
+  step_a();
+  step_b();
+  step_a();
+  for (int s = 0; s < S - 1; ++s) {
+    step_c(s);
+    step_b();
+    step_a();
+  }
+
+  // ---- segments: the tiles of one (sequence, head) inside this CTA's run ----
+  const int g4 = lane >> 2, t4 = lane & 3;
+  int64_t cf = f0 + warp;   // this warp's next tile
+  int slot = 0;
+  int64_t seg0 = f0;
+  bool first_seg = true;
+  while (seg0 < f1) {
+    cursor_settle(a, cc, HK);
+    const int64_t left = cc.nt - cc.tile;
+    const int64_t seg1 = min(f1, seg0 + left);
+    const int g = cc.hk / nhb, hb = cc.hk % nhb;
+    const int h0 = g * a.G + hb * kHeads, nh = min(kHeads, a.G - hb * kHeads);
+    const __nv_bfloat16* qrow = a.q + (int64_t)cc.b * a.q_sb;
+    auto load_q = [&](uint32_t (&f)[4], int ks) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = g4 + (i & 1) * 8, d = ks * 16 + 2 * t4 + (i >> 1) * 8;
+        f[i] = r < nh ? *reinterpret_cast<const uint32_t*>(qrow + (int64_t)(h0 + r) * a.q_sh + d) : 0u;
+      }
+    };
+    uint32_t qf[QREG ? KS : 1][4];
+    if (QREG) {
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) load_q(qf[QREG ? ks : 0], ks);
+    }
+    float o[NV][4];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
+    float mx[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};   // rows g4 and g4 + 8
+
+    for (; cf < seg1; cf += NW) {
+      cp_async_wait_pending(S - 2);
+      __syncwarp();
+      step_c(slot == 0 ? S - 1 : slot - 1);
+      step_b();
+      step_a();
+      const uint32_t kd = ring + (uint32_t)slot * LY.stage_bytes, vd = kd + kTile * DQK * 2;
+      const uint32_t mask = masks[warp * S + slot];
+      slot = slot + 1 == S ? 0 : slot + 1;
+      // S = Q K^T: two halves of 8 positions
+      float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+      {
+        const int mtx = lane >> 3, r = (mtx >> 1) * 8 + (lane & 7);
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          uint32_t kf[4];
+          ldsm4(kf, kd + (uint32_t)(r * DQK * 2 + (((2 * ks + (mtx & 1)) ^ (r & 7)) << 4)));
+          if (QREG) {
+            mma16816(s[0], qf[QREG ? ks : 0], kf[0], kf[1]);
+            mma16816(s[1], qf[QREG ? ks : 0], kf[2], kf[3]);
+          } else {
+            uint32_t f[4];
+            load_q(f, ks);
+            mma16816(s[0], f, kf[0], kf[1]);
+            mma16816(s[1], f, kf[2], kf[3]);
+          }
+        }
+      }
+      float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int c = 8 * j + 2 * t4 + (i & 1);
+          s[j][i] = (mask >> c) & 1u ? s[j][i] * a.scale_log2 : -INFINITY;
+          top[i >> 1] = fmaxf(top[i >> 1], s[j][i]);
+        }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
+        top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2));
+      }
+      if (__any_sync(0xffffffffu, top[0] > mx[0] + kRaise || top[1] > mx[1] + kRaise)) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float nm = fmaxf(mx[i], top[i]);
+          const float c = nm == -INFINITY ? 1.f : ex2_approx(mx[i] - nm);
+          mx[i] = nm;
+          l[i] *= c;
+#pragma unroll
+          for (int n = 0; n < NV; ++n) { o[n][2 * i] *= c; o[n][2 * i + 1] *= c; }
+        }
+      }
+      uint32_t ph[4], pl[4];
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float m = mx[i] == -INFINITY ? 0.f : mx[i];
+          const float p0 = ex2_approx(s[j][2 * i] - m), p1 = ex2_approx(s[j][2 * i + 1] - m);
+          l[i] += p0 + p1;
+          split2(p0, p1, ph[2 * j + i], pl[2 * j + i]);
+        }
+      {
+        const int mtx = lane >> 3, r = (mtx & 1) * 8 + (lane & 7);
+#pragma unroll
+        for (int n = 0; n < NV; n += 2) {
+          uint32_t vf[4];
+          ldsm4_t(vf, vd + (uint32_t)(r * DV * 2 + (((n + (mtx >> 1)) ^ (r & 7)) << 4)));
+          mma16816(o[n], ph, vf[0], vf[1]);
+          mma16816(o[n + 1], ph, vf[2], vf[3]);
+          mma16816(o[n], pl, vf[0], vf[1]);
+          mma16816(o[n + 1], pl, vf[2], vf[3]);
+        }
+      }
+    }
+
+    // ---- join the warps' parts, 32 output columns a round ----
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+      if (t4 == 0) {
+        sm_ml[warp * 2 * kHeads + g4 + 8 * i] = mx[i];
+        sm_ml[warp * 2 * kHeads + kHeads + g4 + 8 * i] = l[i];
+      }
+    }
+    __syncthreads();
+    float f[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float M = -INFINITY;
+      for (int w = 0; w < NW; ++w) M = fmaxf(M, sm_ml[w * 2 * kHeads + g4 + 8 * i]);
+      f[i] = M == -INFINITY ? 0.f : ex2_approx(mx[i] - M);
+    }
+    const bool whole = cc.tile == 0 && seg1 - seg0 == cc.nt;
+    float* part = reinterpret_cast<float*>(a.ws + paged_prefix_bytes(a.B)) +
+                  ((size_t)blockIdx.x * 2 + (first_seg ? 0 : 1)) * paged_part_floats(DV);
+    // thread: row `row`, columns col, col + 1 of the round's 32 (and so on for 4 warps)
+#pragma unroll 1
+    for (int c0 = 0; c0 < DV; c0 += 32) {
+#pragma unroll
+      for (int n = 0; n < NV; ++n) {
+        if (n * 8 >= c0 && n * 8 < c0 + 32) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            *reinterpret_cast<float2*>(sm_o + (warp * kHeads + g4 + 8 * i) * 40 + n * 8 - c0 + 2 * t4) =
+                make_float2(o[n][2 * i] * f[i], o[n][2 * i + 1] * f[i]);
+        }
+      }
+      __syncthreads();
+      for (int e = tid; e < kHeads * 16; e += 32 * NW) {
+        const int row = e >> 4, col = (e & 15) * 2;
+        float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+          const float2 x = *reinterpret_cast<const float2*>(sm_o + (w * kHeads + row) * 40 + col);
+          sum.x += x.x;
+          sum.y += x.y;
+        }
+        float M = -INFINITY, ls = 0.f;
+        for (int w = 0; w < NW; ++w) M = fmaxf(M, sm_ml[w * 2 * kHeads + row]);
+        for (int w = 0; w < NW; ++w)
+          ls += sm_ml[w * 2 * kHeads + kHeads + row] * (M == -INFINITY ? 0.f : ex2_approx(sm_ml[w * 2 * kHeads + row] - M));
+        if (whole) {
+          if (row < nh) {
+            const float inv = ls == 0.f ? 0.f : 1.f / ls;   // no position: 0; a NaN sum stays NaN
+            const int64_t r = (int64_t)cc.b * a.Hq + h0 + row;
+            *reinterpret_cast<__nv_bfloat162*>(a.out + r * DV + c0 + col) = __floats2bfloat162_rn(sum.x * inv, sum.y * inv);
+            if (c0 == 0 && col == 0 && a.lse != nullptr) a.lse[r] = fmaf(M, 0.6931471805599453f, logf(ls));
+          }
+        } else {
+          *reinterpret_cast<float2*>(part + row * DV + c0 + col) = sum;
+          if (c0 == 0 && col == 0) {
+            part[kHeads * DV + row] = M;
+            part[kHeads * DV + kHeads + row] = ls;
+          }
+        }
+      }
+      __syncthreads();
+    }
+    cc.tile += (int)(seg1 - seg0);
+    seg0 = seg1;
+    first_seg = false;
+  }
+  cp_async_wait_pending(0);
+  if (bad_route) record_error(a.err, IRS_DEVERR_ROUTE_ID);
+  if (bad_page) record_error(a.err, IRS_DEVERR_PAGE);
+}
+
+// Joins the parts of the (sequence, head) pairs that CTA borders cut, and writes the empty
+// ones. A block takes rows blockIdx.y, + gridDim.y, ... of a pair; its threads are Dv/4
+// column groups by `pg` groups of parts by rows.
+template <int DV>
+__global__ void __launch_bounds__(256) paged_join_kernel(PagedArgs a, int nhb, int ctas, int warps, int pg) {
+  constexpr int CL = DV / 4, RG = 256 / CL;   // column lanes; row-and-part groups
+  __shared__ float4 sm_o[256];
+  __shared__ float sm_l[256];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int HK = a.Hkv * nhb;
+  const int b = blockIdx.x / HK, hk = blockIdx.x % HK;
+  const int64_t* pre = reinterpret_cast<const int64_t*>(a.ws);
+  const int64_t p0 = pre[b], nt = pre[b + 1] - p0, total = pre[a.B] * HK;
+  const int64_t share = paged_share(total, ctas, warps);
+  const int64_t F0 = p0 * HK + hk * nt, F1 = F0 + nt;
+  const int g = hk / nhb, hb = hk % nhb;
+  const int h0 = g * a.G + hb * kHeads, nh = min(kHeads, a.G - hb * kHeads);
+  const int cl = threadIdx.x % CL, grp = threadIdx.x / CL;
+  const int part_grp = grp % pg, row_grp = grp / pg, rows = RG / pg;
+  int c0 = 0, c1 = -1;
+  if (nt > 0) {
+    c0 = (int)(F0 / share);
+    c1 = (int)((F1 - 1) / share);
+    if (c0 == c1) return;
+  }
+  const float* parts = reinterpret_cast<const float*>(a.ws + paged_prefix_bytes(a.B));
+  for (int rb = blockIdx.y * rows; rb < nh; rb += gridDim.y * rows) {
+    const int row = rb + row_grp;
+    float M = -INFINITY, ls = 0.f;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto part_of = [&](int c) { return parts + ((size_t)c * 2 + (c == c0 && F0 != (int64_t)c0 * share ? 1 : 0)) * paged_part_floats(DV); };
+    if (row < nh) {
+#pragma unroll 8
+      for (int c = c0; c <= c1; ++c) M = fmaxf(M, part_of(c)[kHeads * DV + row]);
+#pragma unroll 4
+      for (int c = c0 + part_grp; c <= c1; c += pg) {
+        const float* p = part_of(c);
+        const float f = M == -INFINITY ? 0.f : ex2_approx(p[kHeads * DV + row] - M);
+        const float4 x = *reinterpret_cast<const float4*>(p + row * DV + 4 * cl);
+        ls = fmaf(f, p[kHeads * DV + kHeads + row], ls);
+        s.x = fmaf(f, x.x, s.x);
+        s.y = fmaf(f, x.y, s.y);
+        s.z = fmaf(f, x.z, s.z);
+        s.w = fmaf(f, x.w, s.w);
+      }
+    }
+    if (pg > 1) {
+      sm_o[threadIdx.x] = s;
+      sm_l[threadIdx.x] = ls;
+      __syncthreads();
+      if (part_grp == 0)
+        for (int i = 1; i < pg; ++i) {
+          const float4 x = sm_o[threadIdx.x + i * CL];
+          s.x += x.x;
+          s.y += x.y;
+          s.z += x.z;
+          s.w += x.w;
+          ls += sm_l[threadIdx.x + i * CL];
+        }
+      __syncthreads();
+    }
+    if (part_grp == 0 && row < nh) {
+      const float inv = ls == 0.f ? 0.f : 1.f / ls;
+      const int64_t r = (int64_t)b * a.Hq + h0 + row;
+      __nv_bfloat162 y[2] = {__floats2bfloat162_rn(s.x * inv, s.y * inv), __floats2bfloat162_rn(s.z * inv, s.w * inv)};
+      *reinterpret_cast<uint2*>(a.out + r * DV + 4 * cl) = *reinterpret_cast<const uint2*>(y);
+      if (cl == 0 && a.lse != nullptr) a.lse[r] = fmaf(M, 0.6931471805599453f, logf(ls));
+    }
+  }
+}
+
+template <int DQK, int DV>
+cudaError_t launch_decode(const PagedArgs& a, int num_sms, bool* configured, cudaStream_t stream) {
+  constexpr PagedLayout LY = paged_layout(DQK, DV);
+  if (!*configured) {
+    const cudaError_t e = cudaFuncSetAttribute(paged_decode_kernel<DQK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)LY.total);
+    if (e != cudaSuccess) return e;
+    *configured = true;
+  }
+  const int nhb = (a.G + kHeads - 1) / kHeads;
+  const int ctas = num_sms < kMaxPagedCtas ? num_sms : kMaxPagedCtas;
+  paged_decode_kernel<DQK, DV><<<ctas, 32 * LY.warps, LY.total, stream>>>(a, nhb);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  // few pairs have many parts each: a row a block, the parts over the groups; many pairs have
+  // a few parts: rows over the groups
+  const int pairs = a.B * a.Hkv * nhb;
+  constexpr int RG = 256 / (DV / 4);
+  const bool few = pairs < num_sms;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)pairs, few ? kHeads : 1);
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_join_kernel<DV>, a, nhb, ctas, LY.warps, few ? RG : 1);
 }
 
 }  // namespace
 
-size_t paged_workspace_bytes(int) { return 256; }
+size_t paged_workspace_bytes(int B, int Dv) {
+  return paged_prefix_bytes(B) + (size_t)kMaxPagedCtas * 2 * paged_part_floats(Dv) * 4;
+}
 
-cudaError_t launch_paged_decode(const PagedArgs& a, int, cudaStream_t stream) {
-  const int64_t rows = (int64_t)a.B * a.Hq;
-  paged_decode_rows_kernel<<<(unsigned)((rows + kPagedThreads / 32 - 1) / (kPagedThreads / 32)), kPagedThreads, 0,
-                             stream>>>(a);
-  return cudaGetLastError();
+cudaError_t launch_paged_decode(const PagedArgs& a, int num_sms, bool* configured, cudaStream_t stream) {
+  const int i = (a.Dqk / 64 - 1) * 3 + (a.Dv == 64 ? 0 : a.Dv == 128 ? 1 : 2);
+  switch (i) {
+    case 0: return launch_decode<64, 64>(a, num_sms, configured + i, stream);
+    case 1: return launch_decode<64, 128>(a, num_sms, configured + i, stream);
+    case 2: return launch_decode<64, 256>(a, num_sms, configured + i, stream);
+    case 3: return launch_decode<128, 64>(a, num_sms, configured + i, stream);
+    case 4: return launch_decode<128, 128>(a, num_sms, configured + i, stream);
+    case 5: return launch_decode<128, 256>(a, num_sms, configured + i, stream);
+    case 6: return launch_decode<192, 64>(a, num_sms, configured + i, stream);
+    case 7: return launch_decode<192, 128>(a, num_sms, configured + i, stream);
+    case 8: return launch_decode<192, 256>(a, num_sms, configured + i, stream);
+    case 9: return launch_decode<256, 64>(a, num_sms, configured + i, stream);
+    case 10: return launch_decode<256, 128>(a, num_sms, configured + i, stream);
+    default: return launch_decode<256, 256>(a, num_sms, configured + i, stream);
+  }
 }
 
 }  // namespace irs
