@@ -14,17 +14,17 @@
 //
 // Design.
 // * A tile is 16 positions of one KV head. All tiles of the batch (sequence by sequence, head
-//   by head) form one list, and every CTA (one an SM) takes the same number of neighbouring
+//   by head) form one list, and every warp of the GPU takes the same number of neighbouring
 //   tiles, so ragged lengths load the SMs equally and one long sequence spreads over all of
 //   them. The list's shape comes from the lengths on the device; nothing is read back.
-// * A warp owns its tiles from load to product: every NW-th tile of the CTA's run, through
-//   its own ring of cp.async stages, with its own running maximum, sum and output in
-//   registers. No barrier stands between tiles, and the copies run on into the next
-//   sequence. Positions, routes and page numbers are looked up two tiles ahead.
-// * At the end of a sequence's run the warps join their parts in shared memory, in warp
-//   order. A run that holds the whole (sequence, head) writes the result; one cut by a CTA
-//   border leaves its part in the workspace, and a second kernel (launched early, waiting for
-//   the first) joins those, in CTA order. No atomics: every run gives the same bits.
+// * A warp works alone: its own ring of cp.async stages, its own running maximum, sum and
+//   output in registers, no barrier anywhere in the loop, and its copies run on into the
+//   next sequence. Positions, routes and page numbers are looked up two tiles ahead.
+// * A run that holds a whole (sequence, head) writes the result. One that a warp border cuts
+//   leaves its part in the workspace, and a second kernel (launched early, waiting for the
+//   first) joins the parts in list order. No atomics: every run gives the same bits.
+//   Joining the eight warps of a CTA in shared memory at every sequence's end instead cost
+//   18 us a sequence (128 windows of 516 positions: 80 us where this takes a quarter).
 // * The maximum is raised, and the output rescaled, only where a score passes it by 2^8:
 //   weights then stay below 2^8 and sums below 2^8 n, harmless in FP32, and the rescaling of
 //   Dv/2 registers a thread leaves the loop almost entirely.
@@ -42,26 +42,29 @@ constexpr int kHeads = 16;             // query heads a tile (rows of the produc
 constexpr int kMaxPagedCtas = 160;
 constexpr float kRaise = 8.f;          // raise the maximum only where a score passes it by 2^8
 
+constexpr int kMinTiles = 4;           // a warp's run has at least this many: a part is as large as two tiles
+constexpr uint32_t kRingBytes = 226u * 1024u;
+
 struct PagedLayout {
   int warps, stages;
-  uint32_t stage_bytes, mask_off, ml_off, o_off, total;
+  uint32_t stage_bytes, mask_off, total;
 };
 
-// Warps and stages for head dims: 8 warps where two stages each fit, 4 otherwise.
+// Warps and stages for head dims: as many warps (up to 8) as can have three stages each.
 __host__ __device__ constexpr PagedLayout paged_layout(int Dqk, int Dv) {
   PagedLayout L{};
   L.stage_bytes = (uint32_t)(kTile * (Dqk + Dv) * 2);
-  L.warps = L.stage_bytes * 16u <= 204800u ? 8 : 4;
-  const int fit = (int)(204800u / (L.stage_bytes * (uint32_t)L.warps));
-  L.stages = fit > 4 ? 4 : fit;
+  const int w = (int)(kRingBytes / (3u * L.stage_bytes));
+  L.warps = w > 8 ? 8 : w;
+  const int fit = (int)(kRingBytes / (L.stage_bytes * (uint32_t)L.warps));
+  L.stages = fit > 6 ? 6 : fit;
   L.mask_off = L.stage_bytes * (uint32_t)(L.warps * L.stages);
-  L.ml_off = L.mask_off + 4u * (uint32_t)(L.warps * L.stages);
-  L.o_off = (L.ml_off + 4u * 2u * kHeads * (uint32_t)L.warps + 15u) & ~15u;
-  L.total = L.o_off + 4u * kHeads * 40u * (uint32_t)L.warps;   // 32 columns a warp and round, rows 40 floats apart
+  L.total = L.mask_off + 4u * (uint32_t)(L.warps * L.stages);
   return L;
 }
 
-// Workspace: prefix sums of the sequences' tile counts, then two parts for every CTA.
+// Workspace: prefix sums of the sequences' tile counts, then two parts for every warp (the
+// pair its run starts in, the pair it ends in): rows of Dv sums, then maxima, then sums.
 __host__ __device__ inline size_t paged_prefix_bytes(int B) { return ((size_t)(B + 1) * 8 + 255) & ~size_t(255); }
 __host__ __device__ inline size_t paged_part_floats(int Dv) { return (size_t)kHeads * (Dv + 2); }
 
@@ -70,10 +73,10 @@ __device__ __forceinline__ int tiles_of(const PagedArgs& a, int L) {
   return (s.n + kTile - 1) / kTile;
 }
 
-// Tiles every CTA takes: an equal share, but at least one for each warp.
-__device__ __forceinline__ int64_t paged_share(int64_t total, int ctas, int warps) {
-  const int64_t q = (total + ctas - 1) / ctas;
-  return q < warps ? warps : q;
+// Tiles every warp takes.
+__device__ __forceinline__ int64_t paged_share(int64_t total, int warps) {
+  const int64_t q = (total + warps - 1) / warps;
+  return q < kMinTiles ? kMinTiles : q;
 }
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
@@ -127,11 +130,9 @@ __global__ void __launch_bounds__(32 * paged_layout(DQK, DV).warps, 1) paged_dec
   constexpr bool QREG = DQK + DV <= 384;              // the queries stay in registers
   extern __shared__ __align__(128) uint8_t smem[];
   uint32_t* masks = reinterpret_cast<uint32_t*>(smem + LY.mask_off);
-  float* sm_ml = reinterpret_cast<float*>(smem + LY.ml_off);
-  float* sm_o = reinterpret_cast<float*>(smem + LY.o_off);
   __shared__ int64_t scan[32 * NW + 1];
-  __shared__ int64_t start_pre;
-  __shared__ int start_b;
+  __shared__ int64_t start_pre[NW];
+  __shared__ int start_b[NW];
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -162,39 +163,43 @@ __global__ void __launch_bounds__(32 * paged_layout(DQK, DV).warps, 1) paged_dec
     }
     __syncthreads();
     scan[tid] = base + x - n;
-    if (tid == 0) { scan[32 * NW] = total; start_b = -1; }
+    if (tid == 0) scan[32 * NW] = total;
+    if (tid < NW) start_b[tid] = -1;
     __syncthreads();
   }
   const int64_t total = scan[32 * NW] * HK;
-  const int64_t share = paged_share(total, (int)gridDim.x, NW);
-  const int64_t f0 = min(total, (int64_t)blockIdx.x * share), f1 = min(total, f0 + share);
+  const int64_t share = paged_share(total, (int)gridDim.x * NW);
+  const int64_t wf0 = (int64_t)blockIdx.x * NW * share;   // the CTA's first warp's run
   {
     int64_t* pre = reinterpret_cast<int64_t*>(a.ws);
     int64_t n = scan[tid];
     for (int b = bs; b < be; ++b) {
       const int64_t next = n + tiles_of(a, __ldg(a.cache_lens + b));
       if (blockIdx.x == 0) pre[b] = n;
-      if (f0 >= n * HK && f0 < next * HK) { start_b = b; start_pre = n; }
+      for (int w = 0; w < NW; ++w) {
+        const int64_t f = wf0 + w * share;
+        if (f >= n * HK && f < next * HK) { start_b[w] = b; start_pre[w] = n; }
+      }
       n = next;
     }
     if (blockIdx.x == 0 && tid == 0) pre[a.B] = scan[32 * NW];
   }
   __syncthreads();
-  if (f0 >= f1 || start_b < 0) return;
+  const int64_t f0 = wf0 + warp * share, f1 = min(total, f0 + share);
+  if (f0 >= f1 || start_b[warp] < 0) return;
 
-  Cursor cc;                                            // the segment being computed
-  cc.b = start_b;
+  Cursor cc;                                            // the tile being computed
+  cc.b = start_b[warp];
   cursor_open(a, cc);
   {
-    const int64_t in = f0 - start_pre * HK;
+    const int64_t in = f0 - start_pre[warp] * HK;
     cc.hk = (int)(in / cc.nt);
     cc.tile = (int)(in - (int64_t)cc.hk * cc.nt);
   }
 
   // ---- loads: A looks up positions or routes, B pages, C issues the copies ----
   Cursor lc = cc;
-  int64_t lf = f0 + warp;
-  lc.tile += warp;
+  int64_t lf = f0;
   bool a_route = false;
   int a_pos = -1, a_b = 0, a_hk = 0, a_lo = 0, a_hi = 0, a_L = 0;
   int b_pos = -1, b_page = -1, b_off = 0, b_hk = 0;
@@ -220,8 +225,8 @@ __global__ void __launch_bounds__(32 * paged_layout(DQK, DV).warps, 1) paged_dec
           a_L = lc.set.L;
         }
       }
-      lf += NW;
-      lc.tile += NW;
+      ++lf;
+      ++lc.tile;
     }
   };
   auto step_b = [&]() {
@@ -279,16 +284,13 @@ __global__ void __launch_bounds__(32 * paged_layout(DQK, DV).warps, 1) paged_dec
     step_a();
   }
 
-  // ---- segments: the tiles of one (sequence, head) inside this CTA's run ----
+  // ---- the run, a (sequence, head) pair at a time ----
   const int g4 = lane >> 2, t4 = lane & 3;
-  int64_t cf = f0 + warp;   // this warp's next tile
   int slot = 0;
-  int64_t seg0 = f0;
-  bool first_seg = true;
-  while (seg0 < f1) {
+  int64_t f = f0;
+  while (f < f1) {
     cursor_settle(a, cc, HK);
-    const int64_t left = cc.nt - cc.tile;
-    const int64_t seg1 = min(f1, seg0 + left);
+    const int tiles = (int)min(f1 - f, (int64_t)(cc.nt - cc.tile));
     const int g = cc.hk / nhb, hb = cc.hk % nhb;
     const int h0 = g * a.G + hb * kHeads, nh = min(kHeads, a.G - hb * kHeads);
     const __nv_bfloat16* qrow = a.q + (int64_t)cc.b * a.q_sb;
@@ -311,7 +313,7 @@ __global__ void __launch_bounds__(32 * paged_layout(DQK, DV).warps, 1) paged_dec
       for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
     float mx[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};   // rows g4 and g4 + 8
 
-    for (; cf < seg1; cf += NW) {
+    for (int it = 0; it < tiles; ++it) {
       cp_async_wait_pending(S - 2);
       __syncwarp();
       step_c(slot == 0 ? S - 1 : slot - 1);
@@ -388,98 +390,70 @@ __global__ void __launch_bounds__(32 * paged_layout(DQK, DV).warps, 1) paged_dec
       }
     }
 
-    // ---- join the warps' parts, 32 output columns a round ----
+    // ---- the pair's result, or this run's part of it ----
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
       l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-      if (t4 == 0) {
-        sm_ml[warp * 2 * kHeads + g4 + 8 * i] = mx[i];
-        sm_ml[warp * 2 * kHeads + kHeads + g4 + 8 * i] = l[i];
-      }
     }
-    __syncthreads();
-    float f[2];
+    if (tiles == cc.nt) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float M = -INFINITY;
-      for (int w = 0; w < NW; ++w) M = fmaxf(M, sm_ml[w * 2 * kHeads + g4 + 8 * i]);
-      f[i] = M == -INFINITY ? 0.f : ex2_approx(mx[i] - M);
-    }
-    const bool whole = cc.tile == 0 && seg1 - seg0 == cc.nt;
-    float* part = reinterpret_cast<float*>(a.ws + paged_prefix_bytes(a.B)) +
-                  ((size_t)blockIdx.x * 2 + (first_seg ? 0 : 1)) * paged_part_floats(DV);
-    // thread: row `row`, columns col, col + 1 of the round's 32 (and so on for 4 warps)
-#pragma unroll 1
-    for (int c0 = 0; c0 < DV; c0 += 32) {
+      for (int i = 0; i < 2; ++i) {
+        const int row = g4 + 8 * i;
+        if (row < nh) {
+          const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];   // no position: 0; a NaN sum stays NaN
+          const int64_t r = (int64_t)cc.b * a.Hq + h0 + row;
 #pragma unroll
-      for (int n = 0; n < NV; ++n) {
-        if (n * 8 >= c0 && n * 8 < c0 + 32) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            *reinterpret_cast<float2*>(sm_o + (warp * kHeads + g4 + 8 * i) * 40 + n * 8 - c0 + 2 * t4) =
-                make_float2(o[n][2 * i] * f[i], o[n][2 * i + 1] * f[i]);
+          for (int n = 0; n < NV; ++n)
+            *reinterpret_cast<__nv_bfloat162*>(a.out + r * DV + n * 8 + 2 * t4) =
+                __floats2bfloat162_rn(o[n][2 * i] * inv, o[n][2 * i + 1] * inv);
+          if (t4 == 0 && a.lse != nullptr) a.lse[r] = fmaf(mx[i], 0.6931471805599453f, logf(l[i]));
         }
       }
-      __syncthreads();
-      for (int e = tid; e < kHeads * 16; e += 32 * NW) {
-        const int row = e >> 4, col = (e & 15) * 2;
-        float2 sum = make_float2(0.f, 0.f);
+    } else {
+      float* part = reinterpret_cast<float*>(a.ws + paged_prefix_bytes(a.B)) +
+                    (((size_t)blockIdx.x * NW + warp) * 2 + (f == f0 ? 0 : 1)) * paged_part_floats(DV);
 #pragma unroll
-        for (int w = 0; w < NW; ++w) {
-          const float2 x = *reinterpret_cast<const float2*>(sm_o + (w * kHeads + row) * 40 + col);
-          sum.x += x.x;
-          sum.y += x.y;
-        }
-        float M = -INFINITY, ls = 0.f;
-        for (int w = 0; w < NW; ++w) M = fmaxf(M, sm_ml[w * 2 * kHeads + row]);
-        for (int w = 0; w < NW; ++w)
-          ls += sm_ml[w * 2 * kHeads + kHeads + row] * (M == -INFINITY ? 0.f : ex2_approx(sm_ml[w * 2 * kHeads + row] - M));
-        if (whole) {
-          if (row < nh) {
-            const float inv = ls == 0.f ? 0.f : 1.f / ls;   // no position: 0; a NaN sum stays NaN
-            const int64_t r = (int64_t)cc.b * a.Hq + h0 + row;
-            *reinterpret_cast<__nv_bfloat162*>(a.out + r * DV + c0 + col) = __floats2bfloat162_rn(sum.x * inv, sum.y * inv);
-            if (c0 == 0 && col == 0 && a.lse != nullptr) a.lse[r] = fmaf(M, 0.6931471805599453f, logf(ls));
-          }
-        } else {
-          *reinterpret_cast<float2*>(part + row * DV + c0 + col) = sum;
-          if (c0 == 0 && col == 0) {
-            part[kHeads * DV + row] = M;
-            part[kHeads * DV + kHeads + row] = ls;
+      for (int i = 0; i < 2; ++i) {
+        const int row = g4 + 8 * i;
+        if (row < nh) {
+#pragma unroll
+          for (int n = 0; n < NV; ++n)
+            *reinterpret_cast<float2*>(part + row * DV + n * 8 + 2 * t4) = make_float2(o[n][2 * i], o[n][2 * i + 1]);
+          if (t4 == 0) {
+            part[kHeads * DV + row] = mx[i];
+            part[kHeads * DV + kHeads + row] = l[i];
           }
         }
       }
-      __syncthreads();
     }
-    cc.tile += (int)(seg1 - seg0);
-    seg0 = seg1;
-    first_seg = false;
+    cc.tile += tiles;
+    f += tiles;
   }
   cp_async_wait_pending(0);
   if (bad_route) record_error(a.err, IRS_DEVERR_ROUTE_ID);
   if (bad_page) record_error(a.err, IRS_DEVERR_PAGE);
 }
 
-// Joins the parts of the (sequence, head) pairs that CTA borders cut, and writes the empty
-// ones. A block takes rows blockIdx.y, + gridDim.y, ... of a pair; its threads are Dv/4
-// column groups by `pg` groups of parts by rows.
+// Joins the parts of the (sequence, head) pairs that warp borders cut, and writes the empty
+// ones. A block has Dv/4 column lanes and row-and-part groups: `pg` groups share a row, each
+// taking every pg-th part with its own running maximum; they are then joined in order.
 template <int DV>
-__global__ void __launch_bounds__(256) paged_join_kernel(PagedArgs a, int nhb, int ctas, int warps, int pg) {
-  constexpr int CL = DV / 4, RG = 256 / CL;   // column lanes; row-and-part groups
-  __shared__ float4 sm_o[256];
-  __shared__ float sm_l[256];
+__global__ void __launch_bounds__(1024) paged_join_kernel(PagedArgs a, int nhb, int workers, int pg) {
+  constexpr int CL = DV / 4;
+  __shared__ float4 sm_o[1024];
+  __shared__ float2 sm_ml[1024 / CL];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int HK = a.Hkv * nhb;
   const int b = blockIdx.x / HK, hk = blockIdx.x % HK;
   const int64_t* pre = reinterpret_cast<const int64_t*>(a.ws);
   const int64_t p0 = pre[b], nt = pre[b + 1] - p0, total = pre[a.B] * HK;
-  const int64_t share = paged_share(total, ctas, warps);
+  const int64_t share = paged_share(total, workers);
   const int64_t F0 = p0 * HK + hk * nt, F1 = F0 + nt;
   const int g = hk / nhb, hb = hk % nhb;
   const int h0 = g * a.G + hb * kHeads, nh = min(kHeads, a.G - hb * kHeads);
   const int cl = threadIdx.x % CL, grp = threadIdx.x / CL;
-  const int part_grp = grp % pg, row_grp = grp / pg, rows = RG / pg;
+  const int part_grp = grp % pg, row_grp = grp / pg, rows = (int)blockDim.x / CL / pg;
   int c0 = 0, c1 = -1;
   if (nt > 0) {
     c0 = (int)(F0 / share);
@@ -491,35 +465,45 @@ __global__ void __launch_bounds__(256) paged_join_kernel(PagedArgs a, int nhb, i
     const int row = rb + row_grp;
     float M = -INFINITY, ls = 0.f;
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto part_of = [&](int c) { return parts + ((size_t)c * 2 + (c == c0 && F0 != (int64_t)c0 * share ? 1 : 0)) * paged_part_floats(DV); };
+    auto add = [&](float m, float l, const float4& x) {   // a part with its own maximum
+      const float n = fmaxf(M, m);
+      const float u = n == -INFINITY ? 0.f : ex2_approx(M - n), v = n == -INFINITY ? 0.f : ex2_approx(m - n);
+      M = n;
+      ls = fmaf(ls, u, l * v);
+      s.x = fmaf(s.x, u, x.x * v);
+      s.y = fmaf(s.y, u, x.y * v);
+      s.z = fmaf(s.z, u, x.z * v);
+      s.w = fmaf(s.w, u, x.w * v);
+    };
     if (row < nh) {
-#pragma unroll 8
-      for (int c = c0; c <= c1; ++c) M = fmaxf(M, part_of(c)[kHeads * DV + row]);
-#pragma unroll 4
-      for (int c = c0 + part_grp; c <= c1; c += pg) {
-        const float* p = part_of(c);
-        const float f = M == -INFINITY ? 0.f : ex2_approx(p[kHeads * DV + row] - M);
-        const float4 x = *reinterpret_cast<const float4*>(p + row * DV + 4 * cl);
-        ls = fmaf(f, p[kHeads * DV + kHeads + row], ls);
-        s.x = fmaf(f, x.x, s.x);
-        s.y = fmaf(f, x.y, s.y);
-        s.z = fmaf(f, x.z, s.z);
-        s.w = fmaf(f, x.w, s.w);
+      constexpr int U = 4;
+      for (int c = c0 + part_grp; c <= c1; c += U * pg) {
+        float m[U], l[U];
+        float4 x[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          const int ci = c + i * pg;
+          m[i] = -INFINITY;
+          l[i] = 0.f;
+          x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (ci <= c1) {
+            // the pair's first part is its warp's second, unless the warp starts with the pair
+            const float* p = parts + ((size_t)ci * 2 + (ci == c0 && F0 != (int64_t)c0 * share ? 1 : 0)) * paged_part_floats(DV);
+            m[i] = p[kHeads * DV + row];
+            l[i] = p[kHeads * DV + kHeads + row];
+            x[i] = *reinterpret_cast<const float4*>(p + row * DV + 4 * cl);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) add(m[i], l[i], x[i]);
       }
     }
     if (pg > 1) {
       sm_o[threadIdx.x] = s;
-      sm_l[threadIdx.x] = ls;
+      if (cl == 0) sm_ml[grp] = make_float2(M, ls);
       __syncthreads();
       if (part_grp == 0)
-        for (int i = 1; i < pg; ++i) {
-          const float4 x = sm_o[threadIdx.x + i * CL];
-          s.x += x.x;
-          s.y += x.y;
-          s.z += x.z;
-          s.w += x.w;
-          ls += sm_l[threadIdx.x + i * CL];
-        }
+        for (int i = 1; i < pg; ++i) add(sm_ml[grp + i].x, sm_ml[grp + i].y, sm_o[threadIdx.x + i * CL]);
       __syncthreads();
     }
     if (part_grp == 0 && row < nh) {
@@ -546,27 +530,26 @@ cudaError_t launch_decode(const PagedArgs& a, int num_sms, bool* configured, cud
   paged_decode_kernel<DQK, DV><<<ctas, 32 * LY.warps, LY.total, stream>>>(a, nhb);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  // few pairs have many parts each: a row a block, the parts over the groups; many pairs have
-  // a few parts: rows over the groups
+  // few pairs may have hundreds of parts each: a row a block, the parts over 1024 threads;
+  // many pairs have a few parts: rows over the threads
   const int pairs = a.B * a.Hkv * nhb;
-  constexpr int RG = 256 / (DV / 4);
   const bool few = pairs < num_sms;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)pairs, few ? kHeads : 1);
-  cfg.blockDim = dim3(256);
+  cfg.gridDim = dim3((unsigned)pairs, few ? (unsigned)(a.G < kHeads ? a.G : kHeads) : 1u);
+  cfg.blockDim = dim3(few ? 1024 : 256);
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_join_kernel<DV>, a, nhb, ctas, LY.warps, few ? RG : 1);
+  return cudaLaunchKernelEx(&cfg, paged_join_kernel<DV>, a, nhb, ctas * LY.warps, few ? 1024 / (DV / 4) : 1);
 }
 
 }  // namespace
 
 size_t paged_workspace_bytes(int B, int Dv) {
-  return paged_prefix_bytes(B) + (size_t)kMaxPagedCtas * 2 * paged_part_floats(Dv) * 4;
+  return paged_prefix_bytes(B) + (size_t)kMaxPagedCtas * 8 * 2 * paged_part_floats(Dv) * 4;
 }
 
 cudaError_t launch_paged_decode(const PagedArgs& a, int num_sms, bool* configured, cudaStream_t stream) {
