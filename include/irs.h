@@ -576,8 +576,8 @@ irs_status irs_paged_rope_append(const void* q, int64_t q_stride_t, int64_t q_st
  *
  * q          bf16 [B, Hq, Dqk] by strides;  caches and page_table as for irs_paged_rope_append
  * route_ids  NULL or int32 [B, W], row stride route_stride >= W; W = 0 without routes
- * sizes: Hq % Hkv == 0, Dqk in {64, 128, 192, 256}, Dv in {64, 128, 256}, rows 16-byte
- *        aligned, max_pages * page_size <= 2^30, W <= 2^24, window and sinks >= 0 (sinks
+ * sizes: Hq % Hkv == 0, Hkv * ceil(Hq / Hkv / 16) <= 1024, B * Hq < 2^24, Dqk in {64, 128,
+ *        192, 256}, Dv in {64, 128, 256}, rows 16-byte aligned, max_pages * page_size <= 2^30, W <= 2^24, window and sinks >= 0 (sinks
  *        need a window or routes), scale > 0 (finite)
  * out        bf16 [B, Hq, Dv] contiguous;  lse  fp32 [B, Hq] contiguous (may be NULL)
  * workspace  irs_paged_gqa_attn_decode_workspace_bytes(...) bytes, 256-byte aligned; nothing

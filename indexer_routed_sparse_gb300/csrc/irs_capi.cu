@@ -962,6 +962,7 @@ irs_status irs_paged_gqa_attn_decode(const void* q, int64_t q_stride_b, int64_t 
   if (Dqk != 64 && Dqk != 128 && Dqk != 192 && Dqk != 256) return fail(IRS_ERR_VALUE, "Dqk must be 64, 128, 192 or 256 (got %d)", Dqk);
   if (Dv != 64 && Dv != 128 && Dv != 256) return fail(IRS_ERR_VALUE, "Dv must be 64, 128 or 256 (got %d)", Dv);
   if ((long long)B * Hq >= (1LL << 24)) return fail(IRS_ERR_VALUE, "B * Hq must be below 2^24");
+  if ((long long)Hkv * ((Hq / Hkv + 15) / 16) > 1024) return fail(IRS_ERR_VALUE, "at most 1024 KV heads times blocks of 16 query heads");
   if (window < 0 || sinks < 0 || window > (1 << 30) || sinks > (1 << 30)) return fail(IRS_ERR_VALUE, "window and sinks must be in [0, 2^30]");
   if (route_ids == nullptr && W != 0) return fail(IRS_ERR_VALUE, "W must be 0 without routes");
   if (route_ids != nullptr && (W < 1 || W > (1 << 24) || route_stride < W))

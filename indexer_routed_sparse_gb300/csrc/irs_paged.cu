@@ -13,10 +13,12 @@
 // at G = 8 and above FP32 cores would be the bound.
 //
 // Design.
-// * A tile is 16 positions of one KV head. All tiles of the batch (sequence by sequence, head
-//   by head) form one list, and every warp of the GPU takes the same number of neighbouring
-//   tiles, so ragged lengths load the SMs equally and one long sequence spreads over all of
-//   them. The list's shape comes from the lengths on the device; nothing is read back.
+// * A tile is 16 positions of one KV head. The tiles of the batch, sequence by sequence, form
+//   one list per head, and the lists are cut into runs of equal length, one a warp, so ragged
+//   lengths load the SMs equally and one long sequence spreads over all of them. The list's
+//   shape comes from the lengths on the device; nothing is read back. The warps of a CTA take
+//   the same run for different heads: a token's heads lie next to one another in the pool,
+//   and fetching them together is what keeps DRAM pages open (routed positions).
 // * A warp works alone: its own ring of cp.async stages, its own running maximum, sum and
 //   output in registers, no barrier anywhere in the loop, and its copies run on into the
 //   next sequence. Positions, routes and page numbers are looked up two tiles ahead.
@@ -24,7 +26,7 @@
 //   leaves its part in the workspace, and a second kernel (launched early, waiting for the
 //   first) joins the parts in list order. No atomics: every run gives the same bits.
 //   Joining the eight warps of a CTA in shared memory at every sequence's end instead cost
-//   18 us a sequence (128 windows of 516 positions: 80 us where this takes a quarter).
+//   18 us a sequence.
 // * The maximum is raised, and the output rescaled, only where a score passes it by 2^8:
 //   weights then stay below 2^8 and sums below 2^8 n, harmless in FP32, and the rescaling of
 //   Dv/2 registers a thread leaves the loop almost entirely.
@@ -40,31 +42,42 @@ namespace {
 constexpr int kTile = 16;              // positions a tile (two 8-column halves of the score product)
 constexpr int kHeads = 16;             // query heads a tile (rows of the products)
 constexpr int kMaxPagedCtas = 160;
+constexpr int kMaxWarps = 8;
 constexpr float kRaise = 8.f;          // raise the maximum only where a score passes it by 2^8
 
 constexpr int kMinTiles = 4;           // a warp's run has at least this many: a part is as large as two tiles
-constexpr uint32_t kRingBytes = 226u * 1024u;
+constexpr uint32_t kRingBytes = 223u * 1024u;
 
-struct PagedLayout {
-  int warps, stages;
-  uint32_t stage_bytes, mask_off, total;
+// How a launch lays out its warps: `groups` groups of CTAs take `heads` heads each; `per_head`
+// warps of a CTA share a head's list.
+struct PagedGrid {
+  int groups, heads, per_head, warps, stages, ctas, workers;   // workers: runs of a head's list
+  uint32_t mask_off, smem;
 };
 
-// Warps and stages for head dims: as many warps (up to 8) as can have three stages each.
-__host__ __device__ constexpr PagedLayout paged_layout(int Dqk, int Dv) {
-  PagedLayout L{};
-  L.stage_bytes = (uint32_t)(kTile * (Dqk + Dv) * 2);
-  const int w = (int)(kRingBytes / (3u * L.stage_bytes));
-  L.warps = w > 8 ? 8 : w;
-  const int fit = (int)(kRingBytes / (L.stage_bytes * (uint32_t)L.warps));
-  L.stages = fit > 6 ? 6 : fit;
-  L.mask_off = L.stage_bytes * (uint32_t)(L.warps * L.stages);
-  L.total = L.mask_off + 4u * (uint32_t)(L.warps * L.stages);
-  return L;
+inline PagedGrid paged_grid(int Dqk, int Dv, int HK, int num_sms) {
+  PagedGrid g{};
+  const uint32_t stage = (uint32_t)(kTile * (Dqk + Dv) * 2);
+  int most = (int)(kRingBytes / (3u * stage));   // as many warps (up to 8) as can have three stages each
+  most = most > kMaxWarps ? kMaxWarps : most;
+  g.groups = (HK + most - 1) / most;
+  g.heads = (HK + g.groups - 1) / g.groups;
+  g.groups = (HK + g.heads - 1) / g.heads;
+  g.per_head = most / g.heads;
+  g.warps = g.heads * g.per_head;
+  const int fit = (int)(kRingBytes / (stage * (uint32_t)g.warps));
+  g.stages = fit > 6 ? 6 : fit;
+  g.mask_off = stage * (uint32_t)(g.warps * g.stages);
+  g.smem = g.mask_off + 4u * (uint32_t)(g.warps * g.stages);
+  int c = (num_sms < kMaxPagedCtas ? num_sms : kMaxPagedCtas) / g.groups;   // CTAs a group
+  c = c < 1 ? 1 : c;
+  g.ctas = c * g.groups;
+  g.workers = c * g.per_head;
+  return g;
 }
 
-// Workspace: prefix sums of the sequences' tile counts, then two parts for every warp (the
-// pair its run starts in, the pair it ends in): rows of Dv sums, then maxima, then sums.
+// Workspace: prefix sums of the sequences' tile counts, then two parts for every run and head
+// (the sequence it starts in, the one it ends in): rows of Dv sums, then maxima, then sums.
 __host__ __device__ inline size_t paged_prefix_bytes(int B) { return ((size_t)(B + 1) * 8 + 255) & ~size_t(255); }
 __host__ __device__ inline size_t paged_part_floats(int Dv) { return (size_t)kHeads * (Dv + 2); }
 
@@ -73,9 +86,9 @@ __device__ __forceinline__ int tiles_of(const PagedArgs& a, int L) {
   return (s.n + kTile - 1) / kTile;
 }
 
-// Tiles every warp takes.
-__device__ __forceinline__ int64_t paged_share(int64_t total, int warps) {
-  const int64_t q = (total + warps - 1) / warps;
+// Tiles of a run.
+__device__ __forceinline__ int64_t paged_share(int64_t total, int workers) {
+  const int64_t q = (total + workers - 1) / workers;
   return q < kMinTiles ? kMinTiles : q;
 }
 
@@ -103,42 +116,42 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t&
 
 // One place in the list of tiles.
 struct Cursor {
-  int b, hk, tile, nt;   // sequence, (KV head, head block), tile of it, its tile count
+  int b, tile, nt;   // sequence, tile of it, its tile count
   PagedSet set;
 };
 __device__ __forceinline__ void cursor_open(const PagedArgs& a, Cursor& c) {
   c.set = paged_set(a, __ldg(a.cache_lens + c.b));
   c.nt = (c.set.n + kTile - 1) / kTile;
 }
-// Move on to the (sequence, head) that holds c.tile; the list must go on that far.
-__device__ __forceinline__ void cursor_settle(const PagedArgs& a, Cursor& c, int HK) {
+// Move on to the sequence that holds c.tile; the list must go on that far.
+__device__ __forceinline__ void cursor_settle(const PagedArgs& a, Cursor& c) {
   while (c.tile >= c.nt) {
     c.tile -= c.nt;
-    if (c.nt == 0 || ++c.hk == HK) {
-      c.hk = 0;
-      if (++c.b >= a.B) { c.b = a.B - 1; c.tile = 0; return; }   // not reached on a list of the right length
-      cursor_open(a, c);
-    }
+    if (++c.b >= a.B) { c.b = a.B - 1; c.tile = 0; return; }   // not reached on a list of the right length
+    cursor_open(a, c);
   }
 }
 
 template <int DQK, int DV>
-__global__ void __launch_bounds__(32 * paged_layout(DQK, DV).warps, 1) paged_decode_kernel(PagedArgs a, int nhb) {
-  constexpr PagedLayout LY = paged_layout(DQK, DV);
-  constexpr int NW = LY.warps, S = LY.stages, KS = DQK / 16, NV = DV / 8;
+__global__ void __launch_bounds__(32 * kMaxWarps, 1) paged_decode_kernel(PagedArgs a, PagedGrid pg, int nhb) {
+  constexpr int KS = DQK / 16, NV = DV / 8;
+  constexpr uint32_t kStage = kTile * (DQK + DV) * 2;
+  const int NW = pg.warps, S = pg.stages;
   constexpr int KCH = DQK / 8, VCH = DV / 8;          // 16-byte chunks a row
   constexpr bool QREG = DQK + DV <= 384;              // the queries stay in registers
   extern __shared__ __align__(128) uint8_t smem[];
-  uint32_t* masks = reinterpret_cast<uint32_t*>(smem + LY.mask_off);
-  __shared__ int64_t scan[32 * NW + 1];
-  __shared__ int64_t start_pre[NW];
-  __shared__ int start_b[NW];
+  uint32_t* masks = reinterpret_cast<uint32_t*>(smem + pg.mask_off);
+  __shared__ int64_t scan[32 * kMaxWarps + 1];
+  __shared__ int64_t start_pre[kMaxWarps];
+  __shared__ int start_b[kMaxWarps];
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int HK = a.Hkv * nhb;
+  const int hk = (int)(blockIdx.x % (unsigned)pg.groups) * pg.heads + warp / pg.per_head;   // KV head and block of query heads
+  const int worker0 = (int)(blockIdx.x / (unsigned)pg.groups) * pg.per_head;   // the CTA's first run of each head's list
 
-  // ---- the list of tiles: its length and where this CTA's run starts ----
+  // ---- the list of tiles: its length and where this CTA's runs start ----
   const int per = (a.B + 32 * NW - 1) / (32 * NW);
   const int bs = min(a.B, tid * per), be = min(a.B, bs + per);
   {
@@ -163,46 +176,44 @@ __global__ void __launch_bounds__(32 * paged_layout(DQK, DV).warps, 1) paged_dec
     }
     __syncthreads();
     scan[tid] = base + x - n;
-    if (tid == 0) scan[32 * NW] = total;
+    if (tid == 0) scan[32 * kMaxWarps] = total;
     if (tid < NW) start_b[tid] = -1;
     __syncthreads();
   }
-  const int64_t total = scan[32 * NW] * HK;
-  const int64_t share = paged_share(total, (int)gridDim.x * NW);
-  const int64_t wf0 = (int64_t)blockIdx.x * NW * share;   // the CTA's first warp's run
+  const int64_t total = scan[32 * kMaxWarps];
+  const int64_t share = paged_share(total, pg.workers);
   {
     int64_t* pre = reinterpret_cast<int64_t*>(a.ws);
     int64_t n = scan[tid];
     for (int b = bs; b < be; ++b) {
       const int64_t next = n + tiles_of(a, __ldg(a.cache_lens + b));
       if (blockIdx.x == 0) pre[b] = n;
-      for (int w = 0; w < NW; ++w) {
-        const int64_t f = wf0 + w * share;
-        if (f >= n * HK && f < next * HK) { start_b[w] = b; start_pre[w] = n; }
+      for (int w = 0; w < pg.per_head; ++w) {
+        const int64_t f = (worker0 + w) * share;
+        if (f >= n && f < next) { start_b[w] = b; start_pre[w] = n; }
       }
       n = next;
     }
-    if (blockIdx.x == 0 && tid == 0) pre[a.B] = scan[32 * NW];
+    if (blockIdx.x == 0 && tid == 0) pre[a.B] = total;
   }
   __syncthreads();
-  const int64_t f0 = wf0 + warp * share, f1 = min(total, f0 + share);
-  if (f0 >= f1 || start_b[warp] < 0) return;
+  const int sub = warp % pg.per_head, worker = worker0 + sub;
+  const int64_t f0 = worker * share, f1 = min(total, f0 + share);
+  if (f0 >= f1 || start_b[sub] < 0 || hk >= HK) return;
+  const int g = hk / nhb, hb = hk % nhb;
+  const int h0 = g * a.G + hb * kHeads, nh = min(kHeads, a.G - hb * kHeads);
 
   Cursor cc;                                            // the tile being computed
-  cc.b = start_b[warp];
+  cc.b = start_b[sub];
   cursor_open(a, cc);
-  {
-    const int64_t in = f0 - start_pre[warp] * HK;
-    cc.hk = (int)(in / cc.nt);
-    cc.tile = (int)(in - (int64_t)cc.hk * cc.nt);
-  }
+  cc.tile = (int)(f0 - start_pre[sub]);
 
   // ---- loads: A looks up positions or routes, B pages, C issues the copies ----
   Cursor lc = cc;
   int64_t lf = f0;
   bool a_route = false;
-  int a_pos = -1, a_b = 0, a_hk = 0, a_lo = 0, a_hi = 0, a_L = 0;
-  int b_pos = -1, b_page = -1, b_off = 0, b_hk = 0;
+  int a_pos = -1, a_b = 0, a_lo = 0, a_hi = 0, a_L = 0;
+  int b_pos = -1, b_page = -1, b_off = 0;
   bool a_live = false, b_live = false, bad_route = false, bad_page = false;
   const int key = lane & 15;
   auto step_a = [&]() {
@@ -210,9 +221,8 @@ __global__ void __launch_bounds__(32 * paged_layout(DQK, DV).warps, 1) paged_dec
     a_pos = -1;
     a_route = false;
     if (a_live) {
-      cursor_settle(a, lc, HK);
+      cursor_settle(a, lc);
       a_b = lc.b;
-      a_hk = lc.hk;
       int j = lc.tile * kTile + key;
       if (j < lc.set.n) {
         if (j < lc.set.early) a_pos = j;
@@ -231,7 +241,6 @@ __global__ void __launch_bounds__(32 * paged_layout(DQK, DV).warps, 1) paged_dec
   };
   auto step_b = [&]() {
     b_live = a_live;
-    b_hk = a_hk;
     b_pos = a_pos;
     if (a_route) {
       if (b_pos < 0 || b_pos >= a_L) {
@@ -248,17 +257,16 @@ __global__ void __launch_bounds__(32 * paged_layout(DQK, DV).warps, 1) paged_dec
       b_page = __ldg(a.page_table + (int64_t)a_b * a.table_stride + pg);
     }
   };
-  const uint32_t ring = smem_u32(smem) + (uint32_t)warp * S * LY.stage_bytes;
+  const uint32_t ring = smem_u32(smem) + (uint32_t)warp * S * kStage;
   auto step_c = [&](int slot) {
     if (b_live) {
       bool ok = b_pos >= 0;
       if (ok && (b_page < 0 || b_page >= a.num_pages)) { bad_page = true; ok = false; }
-      const int g = b_hk / nhb;
       const int64_t ko = ok ? (int64_t)b_page * a.k_sp + (int64_t)b_off * a.k_st + (int64_t)g * a.k_sh : 0;
       const int64_t vo = ok ? (int64_t)b_page * a.v_sp + (int64_t)b_off * a.v_st + (int64_t)g * a.v_sh : 0;
       const uint32_t m = __ballot_sync(0xffffffffu, ok) & 0xffffu;
       if (lane == 0) masks[warp * S + slot] = m;
-      const uint32_t kd = ring + (uint32_t)slot * LY.stage_bytes, vd = kd + kTile * DQK * 2;
+      const uint32_t kd = ring + (uint32_t)slot * kStage, vd = kd + kTile * DQK * 2;
 #pragma unroll
       for (int i = 0; i < KCH / 2; ++i) {
         const int x = i * 32 + lane, row = x / KCH, ch = x % KCH;
@@ -284,15 +292,13 @@ __global__ void __launch_bounds__(32 * paged_layout(DQK, DV).warps, 1) paged_dec
     step_a();
   }
 
-  // ---- the run, a (sequence, head) pair at a time ----
+  // ---- the run, a sequence at a time ----
   const int g4 = lane >> 2, t4 = lane & 3;
   int slot = 0;
   int64_t f = f0;
   while (f < f1) {
-    cursor_settle(a, cc, HK);
+    cursor_settle(a, cc);
     const int tiles = (int)min(f1 - f, (int64_t)(cc.nt - cc.tile));
-    const int g = cc.hk / nhb, hb = cc.hk % nhb;
-    const int h0 = g * a.G + hb * kHeads, nh = min(kHeads, a.G - hb * kHeads);
     const __nv_bfloat16* qrow = a.q + (int64_t)cc.b * a.q_sb;
     auto load_q = [&](uint32_t (&f)[4], int ks) {
 #pragma unroll
@@ -319,7 +325,7 @@ __global__ void __launch_bounds__(32 * paged_layout(DQK, DV).warps, 1) paged_dec
       step_c(slot == 0 ? S - 1 : slot - 1);
       step_b();
       step_a();
-      const uint32_t kd = ring + (uint32_t)slot * LY.stage_bytes, vd = kd + kTile * DQK * 2;
+      const uint32_t kd = ring + (uint32_t)slot * kStage, vd = kd + kTile * DQK * 2;
       const uint32_t mask = masks[warp * S + slot];
       slot = slot + 1 == S ? 0 : slot + 1;
       // S = Q K^T: two halves of 8 positions
@@ -412,7 +418,7 @@ __global__ void __launch_bounds__(32 * paged_layout(DQK, DV).warps, 1) paged_dec
       }
     } else {
       float* part = reinterpret_cast<float*>(a.ws + paged_prefix_bytes(a.B)) +
-                    (((size_t)blockIdx.x * NW + warp) * 2 + (f == f0 ? 0 : 1)) * paged_part_floats(DV);
+                    (((size_t)worker * HK + hk) * 2 + (f == f0 ? 0 : 1)) * paged_part_floats(DV);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int row = g4 + 8 * i;
@@ -447,9 +453,9 @@ __global__ void __launch_bounds__(1024) paged_join_kernel(PagedArgs a, int nhb, 
   const int HK = a.Hkv * nhb;
   const int b = blockIdx.x / HK, hk = blockIdx.x % HK;
   const int64_t* pre = reinterpret_cast<const int64_t*>(a.ws);
-  const int64_t p0 = pre[b], nt = pre[b + 1] - p0, total = pre[a.B] * HK;
-  const int64_t share = paged_share(total, workers);
-  const int64_t F0 = p0 * HK + hk * nt, F1 = F0 + nt;
+  const int64_t p0 = pre[b], nt = pre[b + 1] - p0;
+  const int64_t share = paged_share(pre[a.B], workers);
+  const int64_t F0 = p0, F1 = p0 + nt;
   const int g = hk / nhb, hb = hk % nhb;
   const int h0 = g * a.G + hb * kHeads, nh = min(kHeads, a.G - hb * kHeads);
   const int cl = threadIdx.x % CL, grp = threadIdx.x / CL;
@@ -487,8 +493,8 @@ __global__ void __launch_bounds__(1024) paged_join_kernel(PagedArgs a, int nhb, 
           l[i] = 0.f;
           x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
           if (ci <= c1) {
-            // the pair's first part is its warp's second, unless the warp starts with the pair
-            const float* p = parts + ((size_t)ci * 2 + (ci == c0 && F0 != (int64_t)c0 * share ? 1 : 0)) * paged_part_floats(DV);
+            // the sequence's first part is its run's second, unless the run starts with it
+            const float* p = parts + (((size_t)ci * HK + hk) * 2 + (ci == c0 && F0 != (int64_t)c0 * share ? 1 : 0)) * paged_part_floats(DV);
             m[i] = p[kHeads * DV + row];
             l[i] = p[kHeads * DV + kHeads + row];
             x[i] = *reinterpret_cast<const float4*>(p + row * DV + 4 * cl);
@@ -518,16 +524,15 @@ __global__ void __launch_bounds__(1024) paged_join_kernel(PagedArgs a, int nhb, 
 
 template <int DQK, int DV>
 cudaError_t launch_decode(const PagedArgs& a, int num_sms, bool* configured, cudaStream_t stream) {
-  constexpr PagedLayout LY = paged_layout(DQK, DV);
   if (!*configured) {
     const cudaError_t e = cudaFuncSetAttribute(paged_decode_kernel<DQK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)LY.total);
+                                               (int)(kRingBytes + 256));
     if (e != cudaSuccess) return e;
     *configured = true;
   }
   const int nhb = (a.G + kHeads - 1) / kHeads;
-  const int ctas = num_sms < kMaxPagedCtas ? num_sms : kMaxPagedCtas;
-  paged_decode_kernel<DQK, DV><<<ctas, 32 * LY.warps, LY.total, stream>>>(a, nhb);
+  const PagedGrid pg = paged_grid(DQK, DV, a.Hkv * nhb, num_sms);
+  paged_decode_kernel<DQK, DV><<<pg.ctas, 32 * pg.warps, pg.smem, stream>>>(a, pg, nhb);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // few pairs may have hundreds of parts each: a row a block, the parts over 1024 threads;
@@ -543,13 +548,13 @@ cudaError_t launch_decode(const PagedArgs& a, int num_sms, bool* configured, cud
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_join_kernel<DV>, a, nhb, ctas * LY.warps, few ? 1024 / (DV / 4) : 1);
+  return cudaLaunchKernelEx(&cfg, paged_join_kernel<DV>, a, nhb, pg.workers, few ? 1024 / (DV / 4) : 1);
 }
 
 }  // namespace
 
 size_t paged_workspace_bytes(int B, int Dv) {
-  return paged_prefix_bytes(B) + (size_t)kMaxPagedCtas * 8 * 2 * paged_part_floats(Dv) * 4;
+  return paged_prefix_bytes(B) + (size_t)kMaxPagedCtas * kMaxWarps * 2 * paged_part_floats(Dv) * 4;
 }
 
 cudaError_t launch_paged_decode(const PagedArgs& a, int num_sms, bool* configured, cudaStream_t stream) {

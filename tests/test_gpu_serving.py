@@ -217,7 +217,8 @@ def _decode_case(irs, lens, Hq, Hkv, Dqk, Dv, page, window=0, sinks=0, W=0, seed
 
 
 @pytest.mark.parametrize("Hq,Hkv,Dqk,Dv", [(1, 1, 64, 64), (8, 8, 128, 128), (6, 2, 192, 128), (16, 1, 128, 64),
-                                           (64, 4, 192, 128), (20, 1, 64, 128), (40, 2, 256, 256), (3, 1, 64, 256)])
+                                           (64, 4, 192, 128), (20, 1, 64, 128), (40, 2, 256, 256), (3, 1, 64, 256),
+                                           (12, 12, 64, 64), (3, 3, 192, 128), (48, 16, 128, 128), (90, 5, 256, 64)])
 @pytest.mark.parametrize("page", [1, 16, 48])
 def test_decode_head_shapes_and_lengths(irs, Hq, Hkv, Dqk, Dv, page):
     _decode_case(irs, [1, 0, 15, 16, 17, 64, 333, 700], Hq, Hkv, Dqk, Dv, page, heads_first=page == 16)

@@ -93,7 +93,7 @@ def _decode(lib, p, **kw):
     (dict(route=256, W=0), b"routes need"), (dict(route=256, W=4, rs=3), b"routes need"), (dict(scale=0.0), b"scale"),
     (dict(scale=math.inf), b"scale"), (dict(ts=2), b"table_stride"), (dict(ps=0), b"pool"), (dict(q=None), b"NULL"),
     (dict(out=None), b"NULL"), (dict(ws=None), b"NULL"), (dict(ws=16), b"256-byte"), (dict(wb=16), b"too small"),
-    (dict(st=4), b"multiples of 8"), (dict(B=1 << 23), b"2^24"),
+    (dict(st=4), b"multiples of 8"), (dict(B=1 << 23), b"2^24"), (dict(Hq=2000, Hkv=1025), b"multiple"), (dict(Hq=1025, Hkv=1025), b"1024"),
 ])
 def test_decode_refusals(lib, p, kw, word):
     kw = {n: (p + x if n in ("ws", "route") and x else x) for n, x in kw.items()}
