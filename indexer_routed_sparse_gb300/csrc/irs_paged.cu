@@ -58,7 +58,10 @@ struct PagedGrid {
 inline PagedGrid paged_grid(int Dqk, int Dv, int HK, int num_sms) {
   PagedGrid g{};
   const uint32_t stage = (uint32_t)(kTile * (Dqk + Dv) * 2);
-  int most = (int)(kRingBytes / (3u * stage));   // as many warps (up to 8) as can have three stages each
+  // As many warps (up to 8) as can have two stages each: a warp alone issues an instruction in
+  // four cycles, so two a scheduler count for more than a third stage (192/128 with 4 KV heads,
+  // 450k positions: 183 us with 8 warps of 2 stages, 198 us with 4 warps of 5).
+  int most = (int)(kRingBytes / (2u * stage));
   most = most > kMaxWarps ? kMaxWarps : most;
   g.groups = (HK + most - 1) / most;
   g.heads = (HK + g.groups - 1) / g.groups;
@@ -137,7 +140,6 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) paged_decode_kernel(PagedAr
   constexpr int KS = DQK / 16, NV = DV / 8;
   constexpr uint32_t kStage = kTile * (DQK + DV) * 2;
   const int NW = pg.warps, S = pg.stages;
-  constexpr int KCH = DQK / 8, VCH = DV / 8;          // 16-byte chunks a row
   constexpr bool QREG = DQK + DV <= 384;              // the queries stay in registers
   extern __shared__ __align__(128) uint8_t smem[];
   uint32_t* masks = reinterpret_cast<uint32_t*>(smem + pg.mask_off);
@@ -266,18 +268,22 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) paged_decode_kernel(PagedAr
       const int64_t vo = ok ? (int64_t)b_page * a.v_sp + (int64_t)b_off * a.v_st + (int64_t)g * a.v_sh : 0;
       const uint32_t m = __ballot_sync(0xffffffffu, ok) & 0xffffu;
       if (lane == 0) masks[warp * S + slot] = m;
-      const uint32_t kd = ring + (uint32_t)slot * kStage, vd = kd + kTile * DQK * 2;
+      // eight lanes a row: lane l takes the 16-byte chunks l % 8 + 8 j of the rows l / 8 + 4 i,
+      // so that an address is worked out once a row and the chunks are constant offsets
+      const int c8 = lane & 7;
 #pragma unroll
-      for (int i = 0; i < KCH / 2; ++i) {
-        const int x = i * 32 + lane, row = x / KCH, ch = x % KCH;
-        const int64_t o = __shfl_sync(0xffffffffu, ko, row);
-        cp_async_16(kd + (uint32_t)(row * DQK * 2 + ((ch ^ (row & 7)) << 4)), a.k + o + ch * 8, (m >> row) & 1u ? 16u : 0u);
-      }
+      for (int i = 0; i < 4; ++i) {
+        const int row = 4 * i + (lane >> 3);
+        const __nv_bfloat16* ks = a.k + __shfl_sync(0xffffffffu, ko, row) + c8 * 8;
+        const __nv_bfloat16* vs = a.v + __shfl_sync(0xffffffffu, vo, row) + c8 * 8;
+        const uint32_t n = (m >> row) & 1u ? 16u : 0u;
+        const uint32_t sw = (uint32_t)((c8 ^ (row & 7)) << 4);
+        const uint32_t kd = ring + (uint32_t)slot * kStage + (uint32_t)row * (DQK * 2) + sw;
+        const uint32_t vd = ring + (uint32_t)slot * kStage + kTile * DQK * 2 + (uint32_t)row * (DV * 2) + sw;
 #pragma unroll
-      for (int i = 0; i < VCH / 2; ++i) {
-        const int x = i * 32 + lane, row = x / VCH, ch = x % VCH;
-        const int64_t o = __shfl_sync(0xffffffffu, vo, row);
-        cp_async_16(vd + (uint32_t)(row * DV * 2 + ((ch ^ (row & 7)) << 4)), a.v + o + ch * 8, (m >> row) & 1u ? 16u : 0u);
+        for (int j = 0; j < DQK / 64; ++j) cp_async_16(kd + 128 * j, ks + 64 * j, n);
+#pragma unroll
+        for (int j = 0; j < DV / 64; ++j) cp_async_16(vd + 128 * j, vs + 64 * j, n);
       }
     }
     cp_async_commit();
