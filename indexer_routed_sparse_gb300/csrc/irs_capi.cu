@@ -36,6 +36,7 @@ struct DeviceInfo {
   size_t score_smem = 0, topk_smem = 0, attn_smem = 0, mla_smem = 0, bwd_smem = 0;   // largest configured so far
   bool proj_configured = false;
   bool paged_configured[irs::kPagedKinds] = {};
+  bool window_fwd_configured[irs::kWindowKinds] = {};
 };
 constexpr int kMaxDevices = 64;
 DeviceInfo g_dev[kMaxDevices];
@@ -1005,6 +1006,33 @@ irs_status irs_paged_gqa_attn_decode(const void* q, int64_t q_stride_b, int64_t 
 
 namespace {
 
+// 3-D bf16 map of a packed tensor [T][heads][D] by strides (elements), boxes of 64 dims x
+// box_heads x box_tokens.
+irs_status make_packed_map(CUtensorMap* m, const void* base, int D, int heads, int T, int64_t stride_h, int64_t stride_t,
+                           int box_heads, int box_tokens) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return fail(IRS_ERR_RUNTIME, "cuTensorMapEncodeTiled is unavailable");
+  cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)T};
+  // the stride of a dim with one entry is never used, but has to be a valid one
+  cuuint64_t strides[2] = {(cuuint64_t)(heads > 1 ? stride_h : D) * 2, (cuuint64_t)(T > 1 ? stride_t : (int64_t)D * heads) * 2};
+  cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_tokens};
+  cuuint32_t es[3] = {1, 1, 1};
+  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(IRS_ERR_RUNTIME, "cuTensorMapEncodeTiled (packed heads) failed (%d)", (int)r);
+  return IRS_OK;
+}
+
+// Tensors with a stride of 0 over tokens or heads (broadcast) have no tensor map; they take
+// the kernels that read rows by address.
+bool window_has_maps(const irs::WinArgs& a) {
+  auto ok = [&](int64_t st, int64_t sh, int heads) {
+    return (a.T == 1 || (st > 0 && st < (1LL << 38))) && (heads == 1 || (sh > 0 && sh < (1LL << 38)));
+  };
+  return ok(a.q_st, a.q_sh, a.Hq) && ok(a.k_st, a.k_sh, a.Hkv) && ok(a.v_st, a.v_sh, a.Hkv);
+}
+
 // Checks shared by the window forward and backward; fills the arguments both need.
 irs_status window_args(irs::WinArgs* a, const void* q, int64_t q_stride_t, int64_t q_stride_h, const void* k,
                        int64_t k_stride_t, int64_t k_stride_h, const void* v, int64_t v_stride_t, int64_t v_stride_h,
@@ -1055,7 +1083,15 @@ irs_status irs_window_gqa_attn_fwd(const void* q, int64_t q_stride_t, int64_t q_
   if ((s = current_device(&dev)) != IRS_OK) return s;
   a.out = bf(out);
   a.lse = lse;
-  return launch_status(irs::launch_window_fwd(a, reinterpret_cast<cudaStream_t>(stream)), "launching window attention");
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (!window_has_maps(a)) return launch_status(irs::launch_window_fwd_rows(a, st), "launching window attention (rows)");
+  irs::WinMaps m;
+  if ((s = make_packed_map(&m.q, q, Dqk, Hq, T, q_stride_h, q_stride_t, a.G, 128 / a.G)) != IRS_OK) return s;
+  if ((s = make_packed_map(&m.k, k, Dqk, Hkv, T, k_stride_h, k_stride_t, 1, 128)) != IRS_OK) return s;
+  if ((s = make_packed_map(&m.v, v, Dv, Hkv, T, v_stride_h, v_stride_t, 1, 128)) != IRS_OK) return s;
+  std::lock_guard<std::mutex> lk(g_dev_mu);
+  return launch_status(irs::launch_window_fwd_tc(m, a, dev->num_sms, dev->window_fwd_configured, st),
+                       "launching window attention");
 }
 
 size_t irs_window_gqa_attn_bwd_workspace_bytes(int T, int Hq, int Hkv, int Dqk, int Dv, int ndocs, int window,

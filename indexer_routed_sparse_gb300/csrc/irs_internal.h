@@ -254,7 +254,16 @@ struct WinArgs {
   int32_t* err;
 };
 size_t window_bwd_workspace_bytes(int T, int Hq, int Hkv, int Dqk, int Dv, int ndocs, int window, int sinks);
-cudaError_t launch_window_fwd(const WinArgs& a, cudaStream_t stream);
+// TMA maps [T][heads][D] of the packed tensors: queries in boxes of 64 dims x G heads x 128/G
+// tokens, keys and values in boxes of 64 dims x one head x 128 tokens.
+struct WinMaps {
+  CUtensorMap q, k, v;
+};
+constexpr int kWindowKinds = 6;   // kernels, by head dims
+// configured[kWindowKinds]: whose shared-memory limit has been raised on this device
+cudaError_t launch_window_fwd_tc(const WinMaps& m, const WinArgs& a, int num_sms, bool* configured, cudaStream_t stream);
+// A warp a row; takes strides of 0 too.
+cudaError_t launch_window_fwd_rows(const WinArgs& a, cudaStream_t stream);
 cudaError_t launch_window_bwd(const WinArgs& a, cudaStream_t stream);
 
 #ifdef __CUDACC__

@@ -12,135 +12,13 @@
 // same in every run. Only visible keys are read: what a masked row holds does not matter.
 #include "irs_internal.h"
 #include "irs_ptx.cuh"
+#include "irs_window_rows.cuh"
 
 namespace irs {
 
 namespace {
 
 constexpr int kWinThreads = 256;
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-
-__device__ __forceinline__ float warp_sum(float x) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
-}
-
-// Lane l of a row holds the element pairs 2l, 2l + 1 of every 64 elements.
-template <int N>
-__device__ __forceinline__ void load_row(float2 (&r)[N], const __nv_bfloat16* p, int lane) {
-#pragma unroll
-  for (int i = 0; i < N; ++i) r[i] = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(p + 64 * i + 2 * lane));
-}
-template <int N>
-__device__ __forceinline__ void store_row(const float2 (&r)[N], float f, __nv_bfloat16* p, int lane) {
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-    *reinterpret_cast<__nv_bfloat162*>(p + 64 * i + 2 * lane) = __floats2bfloat162_rn(r[i].x * f, r[i].y * f);
-}
-template <int N>
-__device__ __forceinline__ float dot_row(const float2 (&x)[N], const float2 (&y)[N]) {
-  float s = 0.f;
-#pragma unroll
-  for (int i = 0; i < N; ++i) s = fmaf(x[i].x, y[i].x, fmaf(x[i].y, y[i].y, s));
-  return warp_sum(s);
-}
-template <int N>
-__device__ __forceinline__ void axpy_row(float2 (&acc)[N], float f, const float2 (&x)[N]) {
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    acc[i].x = fmaf(f, x[i].x, acc[i].x);
-    acc[i].y = fmaf(f, x[i].y, acc[i].y);
-  }
-}
-
-__device__ __forceinline__ void check_documents(const WinArgs& a) {
-  if (blockIdx.x != 0) return;
-  bool bad = threadIdx.x == 0 && (a.cu[0] != 0 || a.cu[a.ndocs] != a.T);
-  for (int i = threadIdx.x; i < a.ndocs; i += blockDim.x) bad |= a.cu[i + 1] <= a.cu[i];
-  if (bad) record_error(a.err, IRS_DEVERR_CU_SEQLENS);
-}
-
-template <int NQ, int NV>
-__device__ void fwd_row(const WinArgs& a, int t, int h, int lane) {
-  const int g = h / a.G;
-  const WinDoc doc = window_doc(a.cu, a.ndocs, a.T, t);
-  const int lo = max(doc.start, t - a.window + 1);
-  const int early = min(doc.start + a.sinks, lo);
-  float2 q[NQ], o[NV];
-  load_row<NQ>(q, a.q + (int64_t)t * a.q_st + (int64_t)h * a.q_sh, lane);
-#pragma unroll
-  for (int i = 0; i < NV; ++i) o[i] = make_float2(0.f, 0.f);
-  float m = -INFINITY, l = 0.f;
-  for (int s = doc.start < early ? doc.start : lo; s <= t; s = s + 1 == early ? lo : s + 1) {
-    float2 x[NQ], y[NV];
-    load_row<NQ>(x, a.k + (int64_t)s * a.k_st + (int64_t)g * a.k_sh, lane);
-    load_row<NV>(y, a.v + (int64_t)s * a.v_st + (int64_t)g * a.v_sh, lane);
-    const float sc = dot_row<NQ>(q, x) * a.scale_log2;
-    const float mn = fmaxf(m, sc);
-    const float c = ex2_approx(m - mn), p = ex2_approx(sc - mn);
-    m = mn;
-    l = fmaf(l, c, p);
-#pragma unroll
-    for (int i = 0; i < NV; ++i) { o[i].x *= c; o[i].y *= c; }
-    axpy_row<NV>(o, p, y);
-  }
-  store_row<NV>(o, 1.f / l, a.out + ((int64_t)t * a.Hq + h) * (64 * NV), lane);
-  if (a.lse != nullptr && lane == 0) a.lse[(int64_t)t * a.Hq + h] = fmaf(m, kLn2, logf(l));
-}
-
-template <int NQ, int NV>
-__device__ void dq_row(const WinArgs& a, int t, int h, int lane) {
-  const int g = h / a.G;
-  const WinDoc doc = window_doc(a.cu, a.ndocs, a.T, t);
-  const int lo = max(doc.start, t - a.window + 1);
-  const int early = min(doc.start + a.sinks, lo);
-  const int64_t row = (int64_t)t * a.Hq + h;
-  float2 q[NQ], d[NV], acc[NQ];
-  load_row<NQ>(q, a.q + (int64_t)t * a.q_st + (int64_t)h * a.q_sh, lane);
-  load_row<NV>(d, a.dout + row * (64 * NV), lane);
-#pragma unroll
-  for (int i = 0; i < NQ; ++i) acc[i] = make_float2(0.f, 0.f);
-  const float l2 = a.lse_in[row] * kLog2e, D = a.delta[row];
-  for (int s = doc.start < early ? doc.start : lo; s <= t; s = s + 1 == early ? lo : s + 1) {
-    float2 x[NQ], y[NV];
-    load_row<NQ>(x, a.k + (int64_t)s * a.k_st + (int64_t)g * a.k_sh, lane);
-    load_row<NV>(y, a.v + (int64_t)s * a.v_st + (int64_t)g * a.v_sh, lane);
-    const float p = ex2_approx(fmaf(dot_row<NQ>(q, x), a.scale_log2, -l2));
-    axpy_row<NQ>(acc, p * (dot_row<NV>(d, y) - D), x);
-  }
-  store_row<NQ>(acc, a.scale, a.dq + row * (64 * NQ), lane);
-}
-
-template <int NQ, int NV>
-__device__ void dkv_row(const WinArgs& a, int s, int g, int lane) {
-  const WinDoc doc = window_doc(a.cu, a.ndocs, a.T, s);
-  const int64_t last = (int64_t)s + a.window;   // first query past the window
-  const int end = s - doc.start < a.sinks || last > doc.end ? doc.end : (int)last;
-  float2 k[NQ], v[NV], dk[NQ], dv[NV];
-  load_row<NQ>(k, a.k + (int64_t)s * a.k_st + (int64_t)g * a.k_sh, lane);
-  load_row<NV>(v, a.v + (int64_t)s * a.v_st + (int64_t)g * a.v_sh, lane);
-#pragma unroll
-  for (int i = 0; i < NQ; ++i) dk[i] = make_float2(0.f, 0.f);
-#pragma unroll
-  for (int i = 0; i < NV; ++i) dv[i] = make_float2(0.f, 0.f);
-  for (int t = s; t < end; ++t) {
-    for (int h = g * a.G; h < (g + 1) * a.G; ++h) {
-      const int64_t row = (int64_t)t * a.Hq + h;
-      float2 q[NQ], d[NV];
-      load_row<NQ>(q, a.q + (int64_t)t * a.q_st + (int64_t)h * a.q_sh, lane);
-      load_row<NV>(d, a.dout + row * (64 * NV), lane);
-      const float p = ex2_approx(fmaf(dot_row<NQ>(q, k), a.scale_log2, -a.lse_in[row] * kLog2e));
-      const float ds = p * (dot_row<NV>(d, v) - a.delta[row]);
-      axpy_row<NQ>(dk, ds, q);
-      axpy_row<NV>(dv, p, d);
-    }
-  }
-  const int64_t row = (int64_t)s * a.Hkv + g;
-  store_row<NQ>(dk, a.scale, a.dk + row * (64 * NQ), lane);
-  store_row<NV>(dv, 1.f, a.dv + row * (64 * NV), lane);
-}
 
 // MODE 0: forward rows, 1: dq rows, 2: dk/dv rows, 3: D = dout.out rows.
 template <int NQ, int NV, int MODE>
@@ -193,7 +71,7 @@ size_t window_bwd_workspace_bytes(int T, int Hq, int, int, int, int, int, int) {
   return (((size_t)T * Hq * 4 + 255) & ~size_t(255)) + 256;
 }
 
-cudaError_t launch_window_fwd(const WinArgs& a, cudaStream_t stream) { return launch_rows_any(a, 0, stream); }
+cudaError_t launch_window_fwd_rows(const WinArgs& a, cudaStream_t stream) { return launch_rows_any(a, 0, stream); }
 
 cudaError_t launch_window_bwd(const WinArgs& a, cudaStream_t stream) {
   for (int mode : {3, 1, 2}) {

@@ -1,0 +1,457 @@
+// Window attention on the tensor cores (tcgen05 + TMEM + TMA): the forward.
+//
+// Mathematics as in irs_window.cu: query t of document [s_d, e_d) sees lo <= s <= t, lo =
+// max(s_d, t - window + 1), and the first tokens s_d <= s < min(s_d + sinks, lo).
+//
+// What bounds it. 2 (Dqk + Dv) flops a (query, head, key) pair on operands that stay in L2:
+// the tensor cores, with the exponentials (one a pair) close behind.
+//
+// Design.
+// * The 128 rows of a product are the G query heads of a KV head for 128 / G queries, so a
+//   tile spans few queries and the keys it needs beyond one window are few: window 512 and
+//   G = 16 give tiles of 8 queries over 519 keys.
+// * An item is two such tiles of neighbouring queries over the same key blocks (128 keys, by
+//   TMA): while one tile's scores go through the softmax (a warpgroup, one row a thread), the
+//   tensor cores work for the other. A persistent CTA an SM walks the items; the next item's
+//   queries and keys load while the last one drains.
+// * S[128 x 128] = Q K^T lies in TMEM; the weights return over it as bf16 and are the first
+//   operand of O += P V straight from TMEM (V read MN-major from its [key][dim] tile).
+// * The running maximum is raised only where a score passes it by 2^8 (weights stay below
+//   2^8, sums in FP32), so O in TMEM is rescaled almost never.
+// * Documents are not aligned to tiles: a tile's keys are one range of the packed sequence,
+//   and each row masks by its own document's start. Only blocks at a border of the range are
+//   masked element by element. First tokens before the range are one more (narrow) block.
+// * A masked weight is 0, but 0 times an infinity or NaN in a masked value row is NaN. Rows
+//   whose sum or output is not finite are computed again from their visible keys alone.
+#include "irs_internal.h"
+#include "irs_ptx.cuh"
+#include "irs_window_rows.cuh"
+
+namespace irs {
+
+namespace {
+
+constexpr int kBlk = 128;            // keys a block
+constexpr int kRows = 128;           // rows a tile
+constexpr uint32_t kAtom = 128 * 128;   // 128 rows x 64 bf16
+constexpr int kFwdThreads = 320;     // warps 0-3, 4-7: softmax of the two tiles; 8: TMA; 9: MMA
+constexpr float kRaise = 8.f;
+
+template <int DQK, int DV>
+struct FwdCfg {
+  static constexpr int QA = DQK / 64, VA = DV / 64;
+  static constexpr uint32_t q_bytes = QA * kAtom;          // one tile's queries
+  static constexpr uint32_t k_bytes = QA * kAtom, v_bytes = VA * kAtom;
+  static constexpr uint32_t budget = 226u * 1024u;
+  static constexpr int KS = 2;
+  static constexpr int VS = 2 * q_bytes + 2 * k_bytes + 2 * v_bytes <= budget ? 2 : 1;
+  static constexpr uint32_t k_off = 2 * q_bytes, v_off = k_off + KS * k_bytes, bar_off = v_off + VS * v_bytes;
+  static constexpr uint32_t total = bar_off + 32 * 8 + 16 + 1024;
+  static constexpr uint32_t S0 = 0, O0 = 256;              // TMEM: S of tile x at 128 x, O at 256 + x DV
+};
+
+// The keys of one item: two tiles of `qt` queries from t0 on.
+struct Item {
+  int t0, last;          // first query; last query of the item
+  int lastA;             // last query of the first tile
+  int ds0, dsB;          // document starts of the tiles' first queries
+  int loB;               // first key of the second tile's first query
+  int klo, nb, ns;       // first key of the range, its blocks; first tokens before it
+  int nbt;               // blocks with the first-token block (which is block 0 when ns > 0)
+  bool hasB;
+};
+__device__ __forceinline__ Item window_item(const WinArgs& a, int t0, int qt) {
+  Item m;
+  m.t0 = t0;
+  m.last = min(t0 + 2 * qt, a.T) - 1;
+  m.lastA = min(t0 + qt, a.T) - 1;
+  m.hasB = t0 + qt < a.T;
+  m.ds0 = window_doc(a.cu, a.ndocs, a.T, t0).start;
+  const int tb = m.hasB ? t0 + qt : t0;
+  m.dsB = window_doc(a.cu, a.ndocs, a.T, tb).start;
+  m.loB = max(m.dsB, tb - a.window + 1);
+  m.klo = max(m.ds0, t0 - a.window + 1);
+  m.nb = (m.last - m.klo) / kBlk + 1;
+  m.ns = max(0, min(m.ds0 + a.sinks, m.klo) - m.ds0);
+  m.nbt = m.nb + (m.ns > 0 ? 1 : 0);
+  return m;
+}
+__device__ __forceinline__ int item_key(const Item& m, int j) {   // first key of block j
+  return m.ns > 0 ? (j == 0 ? m.ds0 : m.klo + kBlk * (j - 1)) : m.klo + kBlk * j;
+}
+__device__ __forceinline__ int item_cols(const Item& m, int j) {  // its keys, up to a multiple of 32
+  const int n = (m.ns > 0 && j == 0) ? m.ns : min(kBlk, m.last - item_key(m, j) + 1);
+  return (n + 31) & ~31;
+}
+__device__ __forceinline__ bool item_active(const WinArgs& a, const Item& m, int x, int j) {
+  if (m.ns > 0 && j == 0) return x == 0 || (m.hasB && m.dsB == m.ds0);
+  const int kb = item_key(m, j);
+  if (x == 0) return kb <= m.lastA;
+  if (!m.hasB) return false;
+  // before the tile's window, and without first tokens of its document
+  return !(kb + kBlk <= m.loB && (kb >= m.dsB + a.sinks || kb + kBlk <= m.dsB));
+}
+__device__ __forceinline__ int item_last(const Item& m, int x) {   // the last active block
+  return x == 0 ? (m.lastA - m.klo) / kBlk + (m.ns > 0 ? 1 : 0) : m.nbt - 1;
+}
+
+// D[128 x DV] (+)= P . V: P bf16 in TMEM, V a [key][dim] tile read MN-major; NK steps of 16 keys.
+template <int NK>
+__device__ __forceinline__ void pv_run(uint32_t d, uint32_t p, uint32_t vb, uint32_t idesc, bool accumulate) {
+  const uint64_t b0 = sdesc_sw128(vb, kAtom, 1024);
+#pragma unroll
+  for (int ks = 0; ks < NK; ++ks)
+    umma_bf16_ts(d, p + 8 * ks, b0 + (uint64_t)((ks * 2048) >> 4), idesc, (accumulate || ks > 0) ? 1u : 0u);
+}
+__device__ __forceinline__ void pv_any(int cols, uint32_t d, uint32_t p, uint32_t vb, uint32_t idesc, bool accumulate) {
+  switch (cols >> 5) {
+    case 1: pv_run<2>(d, p, vb, idesc, accumulate); break;
+    case 2: pv_run<4>(d, p, vb, idesc, accumulate); break;
+    case 3: pv_run<6>(d, p, vb, idesc, accumulate); break;
+    default: pv_run<8>(d, p, vb, idesc, accumulate); break;
+  }
+}
+
+template <int DQK, int DV>
+__global__ void __launch_bounds__(kFwdThreads, 1)
+    window_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                      const __grid_constant__ CUtensorMap tm_v, WinArgs a, int qt, int pairs) {
+  using C = FwdCfg<DQK, DV>;
+  constexpr int KS = C::KS, VS = C::VS;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::bar_off);   // [2]
+  uint64_t* q_empty = q_full + 2;     // [2]
+  uint64_t* k_full = q_empty + 2;     // [KS]
+  uint64_t* k_empty = k_full + 2;
+  uint64_t* v_full = k_empty + 2;     // [VS]
+  uint64_t* v_empty = v_full + 2;
+  uint64_t* s_full = v_empty + 2;     // [2] scores of the tile's next block
+  uint64_t* p_full = s_full + 2;      // [2] its weights
+  uint64_t* o_full = p_full + 2;      // [2] the tile's output
+  uint64_t* o_empty = o_full + 2;     // [2]
+  uint64_t* drain = o_empty + 2;
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], 1); mbar_init(&q_empty[i], 1);
+      mbar_init(&k_full[i], 1); mbar_init(&k_empty[i], 1);
+      mbar_init(&v_full[i], 1); mbar_init(&v_empty[i], 1);
+      mbar_init(&s_full[i], 1); mbar_init(&p_full[i], 4);
+      mbar_init(&o_full[i], 1); mbar_init(&o_empty[i], 4);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(tslot, 512);
+    tmem_relinquish();
+  }
+  check_documents(a);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = *tslot;
+  const int items = pairs * a.Hkv;
+
+  if (warp == 8) {
+    // ---------------- TMA producer ----------------
+    if (lane == 0) {
+      tma_prefetch_map(&tm_q);
+      tma_prefetch_map(&tm_k);
+      tma_prefetch_map(&tm_v);
+      const uint32_t q_box = (uint32_t)(qt * a.G) * 128u * C::QA;
+      uint32_t nq[2] = {0, 0}, nk = 0, nv = 0;
+      bool ok = true;
+      auto load_q = [&](int x, const Item& m, int g) {
+        if (nq[x] > 0 && !mbar_wait(&q_empty[x], (nq[x] - 1) & 1, abort_flag, a.err)) return false;
+        mbar_arrive_expect_tx(&q_full[x], q_box);
+        for (int c = 0; c < C::QA; ++c)
+          tma_load_3d(smem + x * C::q_bytes + c * kAtom, &tm_q, c * 64, g * a.G, m.t0 + x * qt, &q_full[x]);
+        ++nq[x];
+        return true;
+      };
+      for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
+        const int pair = item / a.Hkv, g = item - pair * a.Hkv;
+        const Item m = window_item(a, pair * 2 * qt, qt);
+        if (!(ok = load_q(0, m, g))) break;
+        for (int j = 0; j < m.nbt && ok; ++j) {
+          const int kb = item_key(m, j);
+          const uint32_t ks = nk % KS, vs = nv % VS;
+          if (nk >= KS && !mbar_wait(&k_empty[ks], (nk / KS - 1) & 1, abort_flag, a.err)) { ok = false; break; }
+          mbar_arrive_expect_tx(&k_full[ks], C::k_bytes);
+          for (int c = 0; c < C::QA; ++c)
+            tma_load_3d(smem + C::k_off + ks * C::k_bytes + c * kAtom, &tm_k, c * 64, g, kb, &k_full[ks]);
+          ++nk;
+          if (j == 0 && m.hasB && !(ok = load_q(1, m, g))) break;
+          if (nv >= VS && !mbar_wait(&v_empty[vs], (nv / VS - 1) & 1, abort_flag, a.err)) { ok = false; break; }
+          mbar_arrive_expect_tx(&v_full[vs], C::v_bytes);
+          for (int c = 0; c < C::VA; ++c)
+            tma_load_3d(smem + C::v_off + vs * C::v_bytes + c * kAtom, &tm_v, c * 64, g, kb, &v_full[vs]);
+          ++nv;
+        }
+      }
+      if (*abort_flag) {
+        // copies still in flight land before the CTA leaves
+        auto landed = [&](uint64_t* bar, uint32_t parity) {
+          const unsigned long long w0 = globaltimer_ns();
+          while (!mbar_try_wait(bar, parity) && globaltimer_ns() - w0 < kWaitLimitNs) {}
+        };
+        for (int x = 0; x < 2; ++x) if (nq[x] > 0) landed(&q_full[x], (nq[x] - 1) & 1);
+        for (uint32_t i = nk > KS ? nk - KS : 0; i < nk; ++i) landed(&k_full[i % KS], (i / KS) & 1);
+        for (uint32_t i = nv > VS ? nv - VS : 0; i < nv; ++i) landed(&v_full[i % VS], (i / VS) & 1);
+      }
+    }
+  } else if (warp == 9) {
+    // ---------------- MMA issuer ----------------
+    if (lane == 0) {
+      constexpr uint32_t PV_IDESC = idesc_bf16(kRows, DV, false, true);
+      uint32_t nk = 0, nv = 0, np[2] = {0, 0}, nq[2] = {0, 0}, no[2] = {0, 0};
+      bool alive = true;
+      for (int item = blockIdx.x; item < items && alive; item += gridDim.x) {
+        const Item m = window_item(a, item / a.Hkv * 2 * qt, qt);
+        bool pend[2] = {false, false}, first[2] = {true, true}, begun[2] = {false, false};
+        int pcols = 0;
+        for (int j = 0; j <= m.nbt && alive; ++j) {
+          const bool more = j < m.nbt;
+          const int cols = more ? item_cols(m, j) : 0;
+          const uint32_t kst = nk % KS, vst = nv % VS;
+          if (more && !mbar_wait(&k_full[kst], (nk / KS) & 1, abort_flag, a.err)) { alive = false; break; }
+          if (j > 0 && !mbar_wait(&v_full[vst], (nv / VS) & 1, abort_flag, a.err)) { alive = false; break; }
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const bool act = more && item_active(a, m, x, j);
+            if (pend[x]) {
+              if (!mbar_wait(&p_full[x], np[x] & 1, abort_flag, a.err)) { alive = false; break; }
+              ++np[x];
+              if (first[x] && no[x] > 0 && !mbar_wait(&o_empty[x], (no[x] - 1) & 1, abort_flag, a.err)) { alive = false; break; }
+              tc_fence_after();
+              pv_any(pcols, tbase + C::O0 + x * DV, tbase + C::S0 + 128 * x, smem_u32(smem) + C::v_off + vst * C::v_bytes,
+                     PV_IDESC, !first[x]);
+              first[x] = false;
+              if (j - 1 == item_last(m, x)) { umma_commit(&o_full[x]); ++no[x]; }
+            }
+            if (act) {
+              if (!begun[x]) {
+                if (!mbar_wait(&q_full[x], nq[x] & 1, abort_flag, a.err)) { alive = false; break; }
+                ++nq[x];
+                begun[x] = true;
+              }
+              tc_fence_after();
+              const uint32_t idesc = idesc_bf16(kRows, cols, false, false);
+              const uint64_t a0 = sdesc_sw128(smem_u32(smem) + x * C::q_bytes, 16, 1024);
+              const uint64_t b0 = sdesc_sw128(smem_u32(smem) + C::k_off + kst * C::k_bytes, 16, 1024);
+#pragma unroll
+              for (int ks = 0; ks < 4 * C::QA; ++ks) {
+                const uint64_t off = (uint64_t)(((ks >> 2) * kAtom + (ks & 3) * 32) >> 4);
+                umma_bf16(tbase + C::S0 + 128 * x, a0 + off, b0 + off, idesc, ks > 0);
+              }
+              umma_commit(&s_full[x]);
+              if (j == item_last(m, x)) umma_commit(&q_empty[x]);
+            }
+            pend[x] = act;
+          }
+          if (!alive) break;
+          if (more) { umma_commit(&k_empty[kst]); ++nk; }
+          if (j > 0) { umma_commit(&v_empty[vst]); ++nv; }
+          pcols = cols;
+        }
+      }
+      // every issued product completes before the CTA releases its tensor memory
+      umma_commit(drain);
+      const unsigned long long w0 = globaltimer_ns();
+      while (!mbar_try_wait(drain, 0) && globaltimer_ns() - w0 < kWaitLimitNs) {}
+    }
+  } else {
+    // ---------------- softmax: warps 0-3 the first tile, 4-7 the second ----------------
+    const int x = warp >> 2;
+    const int r = (warp & 3) * 32 + lane;                 // row of the tile = TMEM lane
+    const int rq = r / a.G, rh = r - rq * a.G;            // its query and head
+    const uint32_t s_addr = tbase + C::S0 + 128 * x + tmem_lane_base(warp);
+    const uint32_t o_addr = tbase + C::O0 + x * DV + tmem_lane_base(warp);
+    uint32_t nsf = 0, nof = 0;
+    bool alive = true;
+    for (int item = blockIdx.x; item < items && alive; item += gridDim.x) {
+      const int pair = item / a.Hkv, g = item - pair * a.Hkv;
+      const Item m = window_item(a, pair * 2 * qt, qt);
+      if (x == 1 && !m.hasB) continue;
+      const int t = m.t0 + x * qt + rq;
+      const bool live = rq < qt && t < a.T;
+      const int t_first = m.t0 + x * qt, t_last = x == 0 ? m.lastA : m.last;
+      const int ds = window_doc(a.cu, a.ndocs, a.T, min(t, a.T - 1)).start;
+      const int lo = max(ds, t - a.window + 1);
+      const int early = min(ds + a.sinks, lo);            // first tokens: [ds, early)
+      const int lo_last = max(window_doc(a.cu, a.ndocs, a.T, t_last).start, t_last - a.window + 1);
+      float mx = -INFINITY, l = 0.f;
+      bool started = false;
+      const int jl = item_last(m, x);
+      for (int j = 0; j <= jl; ++j) {
+        if (!item_active(a, m, x, j)) continue;
+        const int kb = item_key(m, j), cols = item_cols(m, j);
+        const bool sink_blk = m.ns > 0 && j == 0;
+        if (!__all_sync(0xffffffffu, mbar_wait(&s_full[x], nsf & 1, abort_flag, a.err))) { alive = false; break; }
+        ++nsf;
+        tc_fence_after();
+        float v[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (32 * c < cols) tmem_ld32(s_addr + 32 * c, v[c]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld_wait_regs(v[c]);
+        if (sink_blk || kb < lo_last || kb + cols - 1 > t_first) {
+          // border: key kb + i is seen for i in [w0, w1] (the window) or [e0, e1) (first tokens)
+          int w0 = lo - kb, w1 = t - kb, e0 = ds - kb, e1 = early - kb;
+          if (sink_blk) { w0 = 1; w1 = 0; e0 = 0; e1 = ds == m.ds0 ? m.ns : 0; }
+          if (!live) { w0 = 1; w1 = 0; e1 = e0 = 0; }
+          const unsigned wn = (unsigned)max(w1 - w0 + 1, 0), en = (unsigned)max(e1 - e0, 0);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            if (32 * c < cols) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                const int k = 32 * c + i;
+                const bool seen = (unsigned)(k - w0) < wn || (unsigned)(k - e0) < en;
+                v[c][i] = seen ? v[c][i] : -INFINITY;
+              }
+            }
+          }
+        }
+        float top = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if (32 * c < cols) {
+            float t0 = v[c][0], t1 = v[c][1];
+#pragma unroll
+            for (int i = 2; i < 32; i += 2) { t0 = fmaxf(t0, v[c][i]); t1 = fmaxf(t1, v[c][i + 1]); }
+            top = fmaxf(top, fmaxf(t0, t1));
+          }
+        }
+        top *= a.scale_log2;
+        if (__any_sync(0xffffffffu, top > mx + kRaise)) {
+          const float nm = fmaxf(mx, top);
+          const float c = nm == -INFINITY ? 1.f : ex2_approx(mx - nm);
+          mx = nm;
+          l *= c;
+          if (started) {
+            // the scores' barrier also covers the products before them: O is complete so far
+#pragma unroll 1
+            for (int d = 0; d < DV; d += 32) {
+              float o[32];
+              tmem_ld32(o_addr + d, o);
+              tmem_ld_wait_regs(o);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] *= c;
+              tmem_st32(o_addr + d, o);
+            }
+          }
+        }
+        started = true;
+        const float off = mx == -INFINITY ? 0.f : -mx;
+        float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if (32 * c < cols) {
+            float w[16];
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              const float p0 = ex2_approx(fmaf(v[c][i], a.scale_log2, off));
+              const float p1 = ex2_approx(fmaf(v[c][i + 1], a.scale_log2, off));
+              l0 += p0;
+              l1 += p1;
+              const __nv_bfloat162 b = __floats2bfloat162_rn(p0, p1);
+              w[i >> 1] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&b));
+            }
+            tmem_st16(s_addr + 16 * c, w);
+          }
+        }
+        l += l0 + l1;
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[x]);
+      }
+      if (!alive) break;
+      // ---- the tile's rows ----
+      if (!__all_sync(0xffffffffu, mbar_wait(&o_full[x], nof & 1, abort_flag, a.err))) break;
+      ++nof;
+      tc_fence_after();
+      const float inv = 1.f / l;
+      const int h = g * a.G + rh;
+      const int64_t row = (int64_t)t * a.Hq + h;
+      float odd = fmaf(mx, 0.f, l * 0.f);                 // NaN where anything is not finite
+#pragma unroll 1
+      for (int d = 0; d < DV; d += 32) {
+        float o[32];
+        tmem_ld32(o_addr + d, o);
+        tmem_ld_wait_regs(o);
+        uint32_t w[16];
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+          odd = fmaf(o[i], 0.f, odd);
+          odd = fmaf(o[i + 1], 0.f, odd);
+          const __nv_bfloat162 b = __floats2bfloat162_rn(o[i] * inv, o[i + 1] * inv);
+          w[i >> 1] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+        if (live) {
+          uint4* dst = reinterpret_cast<uint4*>(a.out + row * DV + d);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) dst[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&o_empty[x]);
+      if (live && a.lse != nullptr) a.lse[row] = fmaf(mx, 0.6931471805599453f, logf(l));
+      __syncwarp();   // the stores above come before those of the rows done again
+      unsigned again = __ballot_sync(0xffffffffu, live && odd != 0.f);   // NaN compares unequal
+      while (again) {
+        const int src = __ffs((int)again) - 1;
+        again &= again - 1;
+        fwd_row<DQK / 64, DV / 64>(a, __shfl_sync(0xffffffffu, t, src), __shfl_sync(0xffffffffu, h, src), lane);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tbase, 512);
+  }
+}
+
+template <int DQK, int DV>
+cudaError_t launch_fwd(const WinMaps& m, const WinArgs& a, int num_sms, bool* configured, cudaStream_t stream) {
+  using C = FwdCfg<DQK, DV>;
+  if (!*configured) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(window_fwd_kernel<DQK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::total);
+    if (e != cudaSuccess) return e;
+    *configured = true;
+  }
+  const int qt = kRows / a.G;
+  const int pairs = (a.T + 2 * qt - 1) / (2 * qt);
+  const int64_t items = (int64_t)pairs * a.Hkv;
+  const int grid = items < num_sms ? (int)items : num_sms;
+  window_fwd_kernel<DQK, DV><<<grid, kFwdThreads, C::total, stream>>>(m.q, m.k, m.v, a, qt, pairs);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_window_fwd_tc(const WinMaps& m, const WinArgs& a, int num_sms, bool* configured, cudaStream_t stream) {
+  const int i = (a.Dqk / 64 - 1) * 2 + (a.Dv / 64 - 1);
+  switch (i) {
+    case 0: return launch_fwd<64, 64>(m, a, num_sms, configured + i, stream);
+    case 1: return launch_fwd<64, 128>(m, a, num_sms, configured + i, stream);
+    case 2: return launch_fwd<128, 64>(m, a, num_sms, configured + i, stream);
+    case 3: return launch_fwd<128, 128>(m, a, num_sms, configured + i, stream);
+    case 4: return launch_fwd<192, 64>(m, a, num_sms, configured + i, stream);
+    default: return launch_fwd<192, 128>(m, a, num_sms, configured + i, stream);
+  }
+}
+
+}  // namespace irs
