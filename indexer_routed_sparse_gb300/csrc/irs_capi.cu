@@ -36,7 +36,7 @@ struct DeviceInfo {
   size_t score_smem = 0, topk_smem = 0, attn_smem = 0, mla_smem = 0, bwd_smem = 0;   // largest configured so far
   bool proj_configured = false;
   bool paged_configured[irs::kPagedKinds] = {};
-  bool window_fwd_configured[irs::kWindowKinds] = {};
+  bool window_fwd_configured[irs::kWindowKinds] = {}, window_bwd_configured[irs::kWindowKinds] = {};
 };
 constexpr int kMaxDevices = 64;
 DeviceInfo g_dev[kMaxDevices];
@@ -1123,7 +1123,20 @@ irs_status irs_window_gqa_attn_bwd(const void* q, int64_t q_stride_t, int64_t q_
   a.dout = bf(dout);
   a.delta = static_cast<float*>(workspace);
   a.dq = bf(dq); a.dk = bf(dk); a.dv = bf(dv);
-  return launch_status(irs::launch_window_bwd(a, reinterpret_cast<cudaStream_t>(stream)),
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (!window_has_maps(a)) return launch_status(irs::launch_window_bwd_rows(a, st), "launching the window backward (rows)");
+  irs::WinSinks sk;
+  irs::window_bwd_layout(static_cast<uint8_t*>(workspace), T, Hq, Hkv, Dqk, Dv, ndocs, window, sinks, &sk);
+  const int hc = a.G < 64 ? a.G : 64;
+  irs::WinBwdMaps m;
+  if ((s = make_packed_map(&m.q, q, Dqk, Hq, T, q_stride_h, q_stride_t, a.G, 128 / a.G)) != IRS_OK) return s;
+  if ((s = make_packed_map(&m.q2, q, Dqk, Hq, T, q_stride_h, q_stride_t, hc, 64 / hc)) != IRS_OK) return s;
+  if ((s = make_packed_map(&m.dout, dout, Dv, Hq, T, Dv, (int64_t)Hq * Dv, a.G, 128 / a.G)) != IRS_OK) return s;
+  if ((s = make_packed_map(&m.dout2, dout, Dv, Hq, T, Dv, (int64_t)Hq * Dv, hc, 64 / hc)) != IRS_OK) return s;
+  if ((s = make_packed_map(&m.k, k, Dqk, Hkv, T, k_stride_h, k_stride_t, 1, 128)) != IRS_OK) return s;
+  if ((s = make_packed_map(&m.v, v, Dv, Hkv, T, v_stride_h, v_stride_t, 1, 128)) != IRS_OK) return s;
+  std::lock_guard<std::mutex> lk(g_dev_mu);
+  return launch_status(irs::launch_window_bwd_tc(m, a, sk, dev->num_sms, dev->window_bwd_configured, st),
                        "launching the window attention backward");
 }
 

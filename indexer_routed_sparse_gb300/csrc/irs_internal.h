@@ -264,19 +264,39 @@ constexpr int kWindowKinds = 6;   // kernels, by head dims
 cudaError_t launch_window_fwd_tc(const WinMaps& m, const WinArgs& a, int num_sms, bool* configured, cudaStream_t stream);
 // A warp a row; takes strides of 0 too.
 cudaError_t launch_window_fwd_rows(const WinArgs& a, cudaStream_t stream);
-cudaError_t launch_window_bwd(const WinArgs& a, cudaStream_t stream);
+cudaError_t launch_window_bwd_rows(const WinArgs& a, cudaStream_t stream);
+
+// First tokens with queries beyond the window (backward): the documents that have them, cut
+// into stretches of queries, and FP32 sums [Dqk | Dv] of each first token and KV head.
+struct WinSinks {
+  int slots, chunks;   // upper bounds of the documents and stretches
+  int* slot;           // [ndocs] document -> slot
+  int* chunk0;         // [ndocs + 1] document -> first stretch
+  int* doc;            // [slots] slot -> document, then the number of slots used
+  float* base;         // [slots][Hkv][sinks][Dqk + Dv]: from the window
+  float* part;         // [chunks][Hkv][sinks][Dqk + Dv]: from a stretch
+};
+// Maps of the backward: q and dout in boxes as the forward's queries (q, dout) and in boxes
+// of 64 rows (q2, dout2); k and v as in the forward.
+struct WinBwdMaps {
+  CUtensorMap q, dout, q2, dout2, k, v;
+};
+size_t window_bwd_layout(uint8_t* ws, int T, int Hq, int Hkv, int Dqk, int Dv, int ndocs, int window, int sinks, WinSinks* s);
+cudaError_t launch_window_bwd_tc(const WinBwdMaps& m, const WinArgs& a, const WinSinks& sk, int num_sms, bool* configured,
+                                 cudaStream_t stream);
 
 #ifdef __CUDACC__
 // The document of token t, kept inside [0, T) even where cu is malformed.
 struct WinDoc {
   int start, end;
 };
-__device__ __forceinline__ WinDoc window_doc(const int32_t* cu, int ndocs, int T, int t) {
+__device__ __forceinline__ WinDoc window_doc(const int32_t* cu, int ndocs, int T, int t, int* index = nullptr) {
   int lo = 0, hi = ndocs;   // cu[lo] <= t < cu[hi]
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (cu[mid] <= t) lo = mid; else hi = mid;
   }
+  if (index != nullptr) *index = lo;
   return WinDoc{min(max(cu[lo], 0), t), max(min(cu[lo + 1], T), t + 1)};
 }
 

@@ -67,13 +67,9 @@ cudaError_t launch_rows_any(const WinArgs& a, int mode, cudaStream_t stream) {
 
 }  // namespace
 
-size_t window_bwd_workspace_bytes(int T, int Hq, int, int, int, int, int, int) {
-  return (((size_t)T * Hq * 4 + 255) & ~size_t(255)) + 256;
-}
-
 cudaError_t launch_window_fwd_rows(const WinArgs& a, cudaStream_t stream) { return launch_rows_any(a, 0, stream); }
 
-cudaError_t launch_window_bwd(const WinArgs& a, cudaStream_t stream) {
+cudaError_t launch_window_bwd_rows(const WinArgs& a, cudaStream_t stream) {
   for (int mode : {3, 1, 2}) {
     const cudaError_t e = launch_rows_any(a, mode, stream);
     if (e != cudaSuccess) return e;

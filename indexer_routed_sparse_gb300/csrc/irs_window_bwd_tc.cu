@@ -1,0 +1,893 @@
+// Window attention on the tensor cores (tcgen05 + TMEM + TMA): the backward.
+//
+// Mathematics as in irs_window.cu, from the saved out and lse:
+//   p = e^{scale q.k - lse},  ds = p (dout.v - D),  D = dout.out
+//   dq = scale sum_s ds k,    dk = scale sum ds q,    dv = sum p dout
+//
+// Two kernels, each with its own sums in TMEM, so that nothing is added in memory and every
+// run gives the same bits; the price is computing the scores and dout.v twice (7 products
+// for 5). Adding dq tiles in memory instead would move an FP32 dq once for every key tile of
+// the window: at window 512 about 8 GB against 1.6 GB of other traffic (T 32768, 64 heads of
+// 192), four times the cost of the two products.
+//
+// * dq (also D): rows of a product are the query heads of 128 / G queries, as in the forward.
+//   S = Q K^T and dP = dO V^T for a block of 128 keys; two warpgroups (64 keys each, one row
+//   a thread) form dS and leave it in TMEM as bf16, the first operand of dQ += dS K (K read
+//   MN-major). S and dP are read out early, so the next block's products run meanwhile.
+// * dk, dv: rows are 128 keys, columns the rows (query, head) that see them, 64 at a time:
+//   S^T = K Q^T, dP^T = V dO^T; P^T and dS^T return to TMEM as bf16, first operands of
+//   dV += P^T dO and dK += dS^T Q. With Dqk = 192 and Dv = 128 the TMEM is full to the last
+//   column: 64 + 64 scores, 32 + 32 weights, 128 + 192 sums.
+// * First tokens are seen by every later query of their document, so their sums are long.
+//   Queries beyond the window are cut into stretches, each an item of its own (one tile of
+//   first-token keys) with FP32 partial sums in the workspace; a small kernel adds a first
+//   token's window part and its stretches in order.
+// * 0 times an infinity or NaN of a masked row is NaN: rows and keys whose result is not
+//   finite are computed again from what they see alone.
+#include "irs_internal.h"
+#include "irs_ptx.cuh"
+#include "irs_window_rows.cuh"
+
+namespace irs {
+
+namespace {
+
+constexpr int kBlk = 128;               // keys a block (dq), keys a tile (dk, dv)
+constexpr int kCols = 64;               // (query, head) rows a block (dk, dv)
+constexpr uint32_t kAtom = 128 * 128;   // 128 rows x 64 bf16
+constexpr uint32_t kAtom64 = 64 * 128;  // 64 rows x 64 bf16
+constexpr int kBwdThreads = 320;        // warps 0-7: score warps; 8: TMA; 9: MMA
+
+__device__ __forceinline__ void wait_landed(uint64_t* bar, uint32_t parity) {
+  const unsigned long long t0 = globaltimer_ns();
+  while (!mbar_try_wait(bar, parity) && globaltimer_ns() - t0 < kWaitLimitNs) {}
+}
+
+// D (+)= A . B with A (bf16, one row a lane) in TMEM and B a [row][dim] tile read MN-major:
+// NK steps of 16 rows, 64-dim atoms `atom` bytes apart.
+template <int NK>
+__device__ __forceinline__ void ts_run(uint32_t d, uint32_t at, uint32_t bb, uint32_t atom, uint32_t idesc, bool accumulate) {
+  const uint64_t b0 = sdesc_sw128(bb, atom, 1024);
+#pragma unroll
+  for (int ks = 0; ks < NK; ++ks)
+    umma_bf16_ts(d, at + 8 * ks, b0 + (uint64_t)((ks * 2048) >> 4), idesc, (accumulate || ks > 0) ? 1u : 0u);
+}
+// D = A . B^T, both K-major over NA 64-dim atoms.
+template <int NA>
+__device__ __forceinline__ void ss_run(uint32_t d, uint32_t ab, uint32_t a_atom, uint32_t bb, uint32_t b_atom, uint32_t idesc) {
+  const uint64_t a0 = sdesc_sw128(ab, 16, 1024), b0 = sdesc_sw128(bb, 16, 1024);
+#pragma unroll
+  for (int ks = 0; ks < 4 * NA; ++ks)
+    umma_bf16(d, a0 + (uint64_t)(((ks >> 2) * a_atom + (ks & 3) * 32) >> 4),
+              b0 + (uint64_t)(((ks >> 2) * b_atom + (ks & 3) * 32) >> 4), idesc, ks > 0);
+}
+
+// ---------------------------------------------------------------------------------------
+// dq
+// ---------------------------------------------------------------------------------------
+template <int DQK, int DV>
+struct DqCfg {
+  static constexpr int QA = DQK / 64, VA = DV / 64;
+  static constexpr uint32_t q_bytes = QA * kAtom, do_bytes = VA * kAtom, k_bytes = QA * kAtom, v_bytes = VA * kAtom;
+  static constexpr uint32_t do_off = q_bytes, k_off = q_bytes + do_bytes;
+  static constexpr int KS = 2;
+  static constexpr uint32_t v_off = k_off + KS * k_bytes;
+  static constexpr int VS = v_off + 2 * v_bytes <= 222u * 1024u ? 2 : 1;
+  static constexpr uint32_t x_off = v_off + VS * v_bytes;     // halves of D, then flags of rows to do again
+  static constexpr uint32_t bar_off = x_off + 3 * 128 * 4;
+  static constexpr uint32_t total = bar_off + 32 * 8 + 16 + 1024;
+  static constexpr uint32_t S0 = 0, P0 = 128, DS0 = 256, DQ0 = 320;
+};
+
+struct DqItem {
+  int t0, last, ds0, klo, nb, ns, nbt;
+};
+__device__ __forceinline__ DqItem dq_item(const WinArgs& a, int t0, int qt) {
+  DqItem m;
+  m.t0 = t0;
+  m.last = min(t0 + qt, a.T) - 1;
+  m.ds0 = window_doc(a.cu, a.ndocs, a.T, t0).start;
+  m.klo = max(m.ds0, t0 - a.window + 1);
+  m.nb = (m.last - m.klo) / kBlk + 1;
+  m.ns = max(0, min(m.ds0 + a.sinks, m.klo) - m.ds0);
+  m.nbt = m.nb + (m.ns > 0 ? 1 : 0);
+  return m;
+}
+__device__ __forceinline__ int dq_key(const DqItem& m, int j) {
+  return m.ns > 0 ? (j == 0 ? m.ds0 : m.klo + kBlk * (j - 1)) : m.klo + kBlk * j;
+}
+__device__ __forceinline__ int dq_cols(const DqItem& m, int j) {
+  const int n = (m.ns > 0 && j == 0) ? m.ns : min(kBlk, m.last - dq_key(m, j) + 1);
+  return (n + 31) & ~31;
+}
+
+template <int DQK, int DV>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+    window_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
+                     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, WinArgs a, int qt,
+                     int tiles) {
+  using C = DqCfg<DQK, DV>;
+  constexpr int KS = C::KS, VS = C::VS;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  float* xd = reinterpret_cast<float*>(smem + C::x_off);
+  int* odd_rows = reinterpret_cast<int*>(xd + 256);
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::bar_off);
+  uint64_t* q_empty = q_full + 1;
+  uint64_t* k_full = q_empty + 1;    // [2]
+  uint64_t* k_empty = k_full + 2;
+  uint64_t* v_full = k_empty + 2;    // [2]
+  uint64_t* v_empty = v_full + 2;
+  uint64_t* sp_full = v_empty + 2;   // scores and dP of a block
+  uint64_t* sp_empty = sp_full + 1;  // ... have been read
+  uint64_t* ds_full = sp_empty + 1;
+  uint64_t* dq_full = ds_full + 1;
+  uint64_t* dq_empty = dq_full + 1;
+  uint64_t* drain = dq_empty + 1;
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    mbar_init(q_full, 1); mbar_init(q_empty, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&k_full[i], 1); mbar_init(&k_empty[i], 1);
+      mbar_init(&v_full[i], 1); mbar_init(&v_empty[i], 1);
+    }
+    mbar_init(sp_full, 1); mbar_init(sp_empty, 8);
+    mbar_init(ds_full, 8);
+    mbar_init(dq_full, 1); mbar_init(dq_empty, 8);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(tslot, 512);
+    tmem_relinquish();
+  }
+  check_documents(a);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = *tslot;
+  const int items = tiles * a.Hkv;
+
+  if (warp == 8) {
+    // ---------------- TMA producer ----------------
+    if (lane == 0) {
+      tma_prefetch_map(&tm_q);
+      tma_prefetch_map(&tm_do);
+      tma_prefetch_map(&tm_k);
+      tma_prefetch_map(&tm_v);
+      const uint32_t box = (uint32_t)(qt * a.G) * 128u;
+      uint32_t nq = 0, nk = 0, nv = 0;
+      bool ok = true;
+      for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
+        const int tile = item / a.Hkv, g = item - tile * a.Hkv;
+        const DqItem m = dq_item(a, tile * qt, qt);
+        if (nq > 0 && !mbar_wait(q_empty, (nq - 1) & 1, abort_flag, a.err)) break;
+        mbar_arrive_expect_tx(q_full, box * (C::QA + C::VA));
+        for (int c = 0; c < C::QA; ++c) tma_load_3d(smem + c * kAtom, &tm_q, c * 64, g * a.G, m.t0, q_full);
+        for (int c = 0; c < C::VA; ++c) tma_load_3d(smem + C::do_off + c * kAtom, &tm_do, c * 64, g * a.G, m.t0, q_full);
+        ++nq;
+        for (int j = 0; j < m.nbt; ++j) {
+          const int kb = dq_key(m, j);
+          const uint32_t ks = nk % KS, vs = nv % VS;
+          if (nk >= KS && !mbar_wait(&k_empty[ks], (nk / KS - 1) & 1, abort_flag, a.err)) { ok = false; break; }
+          mbar_arrive_expect_tx(&k_full[ks], C::k_bytes);
+          for (int c = 0; c < C::QA; ++c)
+            tma_load_3d(smem + C::k_off + ks * C::k_bytes + c * kAtom, &tm_k, c * 64, g, kb, &k_full[ks]);
+          ++nk;
+          if (nv >= VS && !mbar_wait(&v_empty[vs], (nv / VS - 1) & 1, abort_flag, a.err)) { ok = false; break; }
+          mbar_arrive_expect_tx(&v_full[vs], C::v_bytes);
+          for (int c = 0; c < C::VA; ++c)
+            tma_load_3d(smem + C::v_off + vs * C::v_bytes + c * kAtom, &tm_v, c * 64, g, kb, &v_full[vs]);
+          ++nv;
+        }
+      }
+      if (*abort_flag) {
+        if (nq > 0) wait_landed(q_full, (nq - 1) & 1);
+        for (uint32_t i = nk > KS ? nk - KS : 0; i < nk; ++i) wait_landed(&k_full[i % KS], (i / KS) & 1);
+        for (uint32_t i = nv > VS ? nv - VS : 0; i < nv; ++i) wait_landed(&v_full[i % VS], (i / VS) & 1);
+      }
+    }
+  } else if (warp == 9) {
+    // ---------------- MMA issuer ----------------
+    if (lane == 0) {
+      constexpr uint32_t DQ_IDESC = idesc_bf16(128, DQK, false, true);
+      const uint32_t sb = smem_u32(smem);
+      uint32_t nk = 0, nv = 0, nsp = 0, nds = 0, ni = 0;   // blocks scored; dS taken; items
+      bool alive = true;
+      auto scores = [&](int cols) {
+        const uint32_t ks = nk % KS, vs = nv % VS;
+        if (!mbar_wait(&k_full[ks], (nk / KS) & 1, abort_flag, a.err)) return false;
+        if (!mbar_wait(&v_full[vs], (nv / VS) & 1, abort_flag, a.err)) return false;
+        if (nsp > 0 && !mbar_wait(sp_empty, (nsp - 1) & 1, abort_flag, a.err)) return false;
+        tc_fence_after();
+        const uint32_t idesc = idesc_bf16(128, cols, false, false);
+        ss_run<C::QA>(tbase + C::S0, sb, kAtom, sb + C::k_off + ks * C::k_bytes, kAtom, idesc);
+        ss_run<C::VA>(tbase + C::P0, sb + C::do_off, kAtom, sb + C::v_off + vs * C::v_bytes, kAtom, idesc);
+        umma_commit(sp_full);
+        umma_commit(&v_empty[vs]);
+        ++nk; ++nv; ++nsp;
+        return true;
+      };
+      for (int item = blockIdx.x; item < items && alive; item += gridDim.x, ++ni) {
+        const DqItem m = dq_item(a, item / a.Hkv * qt, qt);
+        if (!mbar_wait(q_full, ni & 1, abort_flag, a.err)) break;
+        if (!scores(dq_cols(m, 0))) break;
+        if (m.nbt == 1) umma_commit(q_empty);
+        for (int j = 0; j < m.nbt; ++j) {
+          const uint32_t ks = (nk - 1) % KS;   // block j's keys (nk counts block j, not yet j + 1)
+          if (j + 1 < m.nbt) {
+            if (!scores(dq_cols(m, j + 1))) { alive = false; break; }
+            if (j + 2 == m.nbt) umma_commit(q_empty);
+          }
+          if (!mbar_wait(ds_full, nds & 1, abort_flag, a.err)) { alive = false; break; }
+          ++nds;
+          if (j == 0 && ni > 0 && !mbar_wait(dq_empty, (ni - 1) & 1, abort_flag, a.err)) { alive = false; break; }
+          tc_fence_after();
+          const uint32_t kb = sb + C::k_off + ks * C::k_bytes;
+          switch (dq_cols(m, j) >> 5) {
+            case 1: ts_run<2>(tbase + C::DQ0, tbase + C::DS0, kb, kAtom, DQ_IDESC, j > 0); break;
+            case 2: ts_run<4>(tbase + C::DQ0, tbase + C::DS0, kb, kAtom, DQ_IDESC, j > 0); break;
+            case 3: ts_run<6>(tbase + C::DQ0, tbase + C::DS0, kb, kAtom, DQ_IDESC, j > 0); break;
+            default: ts_run<8>(tbase + C::DQ0, tbase + C::DS0, kb, kAtom, DQ_IDESC, j > 0); break;
+          }
+          umma_commit(&k_empty[ks]);   // also: dS has been read (the score warps wait for it below)
+        }
+        if (!alive) break;
+        umma_commit(dq_full);
+      }
+      umma_commit(drain);
+      wait_landed(drain, 0);
+    }
+  } else {
+    // ---------------- score warps: row = TMEM lane, 64 keys of the block each ----------------
+    const int half = warp >> 2;
+    const int r = (warp & 3) * 32 + lane;
+    const int rq = r / a.G, rh = r - rq * a.G;
+    const uint32_t lanes = tmem_lane_base(warp);
+    uint32_t nsp = 0, ni = 0, nkb = 0;
+    bool alive = true;
+    for (int item = blockIdx.x; item < items && alive; item += gridDim.x, ++ni) {
+      const int tile = item / a.Hkv, g = item - tile * a.Hkv;
+      const DqItem m = dq_item(a, tile * qt, qt);
+      const int t = m.t0 + rq, h = g * a.G + rh;
+      const bool live = rq < qt && t < a.T;
+      const int64_t row = (int64_t)t * a.Hq + h;
+      const int ds = window_doc(a.cu, a.ndocs, a.T, min(t, a.T - 1)).start;
+      const int lo = max(ds, t - a.window + 1);
+      const int early = min(ds + a.sinks, lo);
+      const int lo_last = max(window_doc(a.cu, a.ndocs, a.T, m.last).start, m.last - a.window + 1);
+      // D = dout . out: half the dims a thread, joined through shared memory
+      float l2 = 0.f;
+      {
+        float s = 0.f;
+        if (live) {
+          l2 = a.lse_in[row] * kLog2e;
+          const uint4* x = reinterpret_cast<const uint4*>(a.dout + row * DV + half * (DV / 2));
+          const uint4* y = reinterpret_cast<const uint4*>(a.out + row * DV + half * (DV / 2));
+#pragma unroll
+          for (int i = 0; i < DV / 16; ++i) {
+            const uint4 u = x[i], w = y[i];
+            const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              s = fmaf(__uint_as_float(uu[k] << 16), __uint_as_float(ww[k] << 16), s);
+              s = fmaf(__uint_as_float(uu[k] & 0xffff0000u), __uint_as_float(ww[k] & 0xffff0000u), s);
+            }
+          }
+        }
+        xd[half * 128 + r] = s;
+      }
+      if (half == 0) odd_rows[r] = 0;
+      named_bar_sync(1, 256);
+      const float D = xd[r] + xd[128 + r];
+      if (live && half == 0) a.delta[row] = D;
+      for (int j = 0; j < m.nbt; ++j, ++nkb) {
+        const int kb = dq_key(m, j), cols = dq_cols(m, j);
+        const bool sink_blk = m.ns > 0 && j == 0;
+        if (!__all_sync(0xffffffffu, mbar_wait(sp_full, nsp & 1, abort_flag, a.err))) { alive = false; break; }
+        ++nsp;
+        tc_fence_after();
+        const bool border = sink_blk || kb < lo_last || kb + cols - 1 > m.t0;
+        int w0 = lo - kb, w1 = t - kb, e0 = ds - kb, e1 = early - kb;
+        if (sink_blk) { w0 = 1; w1 = 0; e0 = 0; e1 = ds == m.ds0 ? m.ns : 0; }
+        if (!live) { w0 = 1; w1 = 0; e1 = e0 = 0; }
+        const unsigned wn = (unsigned)max(w1 - w0 + 1, 0), en = (unsigned)max(e1 - e0, 0);
+        const int mine = min(max((cols >> 5) - 2 * half, 0), 2);   // 32-key pieces of this half
+        // dS of the block before must have been read by its product before it is replaced
+        bool taken = nkb == 0;
+        auto wait_taken = [&]() {
+          if (!taken && !__all_sync(0xffffffffu, mbar_wait(&k_empty[(nkb - 1) % KS], ((nkb - 1) / KS) & 1, abort_flag, a.err)))
+            alive = false;
+          taken = true;
+        };
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          if (c < mine) {
+            const int k0 = 64 * half + 32 * c;
+            float s[32], p[32];
+            tmem_ld32(tbase + C::S0 + lanes + k0, s);
+            tmem_ld32(tbase + C::P0 + lanes + k0, p);
+            tmem_ld_wait_regs(s);
+            tmem_ld_wait_regs(p);
+            if (c == mine - 1) {   // the last of the block's scores are in registers
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(sp_empty);
+            }
+#pragma unroll
+            for (int i = 0; i < 32; ++i) s[i] = ex2_approx(fmaf(s[i], a.scale_log2, -l2)) * (p[i] - D);
+            if (border) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                const int k = k0 + i;
+                s[i] = (unsigned)(k - w0) < wn || (unsigned)(k - e0) < en ? s[i] : 0.f;
+              }
+            }
+            float w[16];
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              const __nv_bfloat162 b = __floats2bfloat162_rn(s[i], s[i + 1]);
+              w[i >> 1] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&b));
+            }
+            wait_taken();
+            tmem_st16(tbase + C::DS0 + lanes + (k0 >> 1), w);
+          }
+        }
+        if (mine == 0 && lane == 0) mbar_arrive(sp_empty);
+        wait_taken();
+        if (!alive) break;
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ds_full);
+      }
+      if (alive && !__all_sync(0xffffffffu, mbar_wait(dq_full, ni & 1, abort_flag, a.err))) alive = false;
+      tc_fence_after();
+      float odd = 0.f;
+#pragma unroll 1
+      for (int d = 32 * half; alive && d < DQK; d += 64) {
+        float o[32];
+        tmem_ld32(tbase + C::DQ0 + lanes + d, o);
+        tmem_ld_wait_regs(o);
+        uint32_t w[16];
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+          odd = fmaf(o[i], 0.f, fmaf(o[i + 1], 0.f, odd));
+          const __nv_bfloat162 b = __floats2bfloat162_rn(o[i] * a.scale, o[i + 1] * a.scale);
+          w[i >> 1] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+        if (live) {
+          uint4* dst = reinterpret_cast<uint4*>(a.dq + row * DQK + d);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) dst[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(dq_empty);
+      if (live && odd != 0.f) odd_rows[r] = 1;   // NaN compares unequal
+      // both halves have stored their columns; after a wait that gave up all leave together
+      alive = named_bar_and(1, 256, alive);
+      if (alive && half == 0) {
+        unsigned again = __ballot_sync(0xffffffffu, odd_rows[r] != 0);
+        while (again) {
+          const int src = __ffs((int)again) - 1;
+          again &= again - 1;
+          dq_row<DQK / 64, DV / 64>(a, __shfl_sync(0xffffffffu, t, src), __shfl_sync(0xffffffffu, h, src), lane);
+        }
+      }
+      named_bar_sync(1, 256);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tbase, 512);
+  }
+}
+
+// ---------------------------------------------------------------------------------------
+// dk, dv
+// ---------------------------------------------------------------------------------------
+template <int DQK, int DV>
+struct DkvCfg {
+  static constexpr int QA = DQK / 64, VA = DV / 64;
+  static constexpr uint32_t k_bytes = QA * kAtom, v_bytes = VA * kAtom;
+  static constexpr uint32_t q_bytes = QA * kAtom64, do_bytes = VA * kAtom64, st_bytes = q_bytes + do_bytes;
+  static constexpr uint32_t st_off = k_bytes + v_bytes;
+  static constexpr int ST = st_off + 4 * st_bytes <= 220u * 1024u ? 4 : 3;
+  static constexpr uint32_t ld_off = st_off + ST * st_bytes;              // lse (base 2) and D of each stage's rows
+  static constexpr uint32_t bar_off = ld_off + ST * 2 * kCols * 4;
+  static constexpr uint32_t total = bar_off + 32 * 8 + 16 + 1024;
+  static constexpr uint32_t S0 = 0, P0 = 64, PW0 = 128, DS0 = 160, DV0 = 192, DK0 = 192 + DV;
+};
+
+struct DkvItem {
+  int s0, keys;     // first key, number of keys
+  int t0, t1;       // queries
+  int g, chunk;     // KV head; stretch of far queries of first tokens, or -1
+  int nblk;
+};
+
+// Queries of one stretch beyond the window.
+__host__ __device__ inline int sink_stretch(int window) { return window < 256 ? 256 : window > 4096 ? 4096 : window; }
+
+__device__ __forceinline__ DkvItem dkv_item(const WinArgs& a, const WinSinks& sk, int item, int tiles, int qt, int nhc) {
+  DkvItem m;
+  const int u = item / a.Hkv;
+  m.g = item - u * a.Hkv;
+  if (u < tiles) {
+    m.chunk = -1;
+    m.s0 = u * kBlk;
+    m.keys = min(kBlk, a.T - m.s0);
+    m.t0 = m.s0;
+    const int sl = m.s0 + m.keys - 1;
+    const WinDoc d = window_doc(a.cu, a.ndocs, a.T, sl);
+    m.t1 = (int)min((int64_t)sl + a.window, (int64_t)d.end);
+  } else {
+    m.chunk = u - tiles;
+    int lo = 0, hi = a.ndocs;   // chunk0[lo] <= chunk < chunk0[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (sk.chunk0[mid] <= m.chunk) lo = mid; else hi = mid;
+    }
+    const int start = min(max(a.cu[lo], 0), a.T - 1), end = max(min(a.cu[lo + 1], a.T), start + 1);
+    m.s0 = start;
+    m.keys = min(a.sinks, end - start);
+    const int n = sink_stretch(a.window);
+    m.t0 = (int)min((int64_t)end, (int64_t)start + a.window + (int64_t)(m.chunk - sk.chunk0[lo]) * n);
+    m.t1 = min(end, m.t0 + n);
+  }
+  m.t1 = max(m.t1, m.t0 + 1);   // only where cu_seqlens is malformed
+  m.nblk = (m.t1 - m.t0 + qt - 1) / qt * nhc;
+  return m;
+}
+
+template <int DQK, int DV>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+    window_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
+                      const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, WinArgs a,
+                      WinSinks sk, int tiles) {
+  using C = DkvCfg<DQK, DV>;
+  constexpr int ST = C::ST;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  float* ld = reinterpret_cast<float*>(smem + C::ld_off);
+  uint64_t* kv_full = reinterpret_cast<uint64_t*>(smem + C::bar_off);
+  uint64_t* kv_empty = kv_full + 1;
+  uint64_t* st_full = kv_empty + 1;    // [4]
+  uint64_t* st_empty = st_full + 4;    // [4]
+  uint64_t* sp_full = st_empty + 4;
+  uint64_t* sp_empty = sp_full + 1;
+  uint64_t* pd_full = sp_empty + 1;    // weights and dS of a block
+  uint64_t* pd_empty = pd_full + 1;    // ... have been read by the products
+  uint64_t* acc_full = pd_empty + 1;
+  uint64_t* acc_empty = acc_full + 1;
+  uint64_t* drain = acc_empty + 1;
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int hc = a.G < kCols ? a.G : kCols;      // heads a block
+  const int qt = kCols / hc;                     // queries a block
+  const int nhc = (a.G + kCols - 1) / kCols;     // blocks that share their queries
+  // stage rows that no copy writes (64 not a multiple of the heads) meet weights of 0
+  if (qt * hc < kCols) {
+    for (uint32_t i = tid; i < ST * C::st_bytes / 16u; i += kBwdThreads)
+      reinterpret_cast<uint4*>(smem + C::st_off)[i] = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+  }
+  if (tid == 0) {
+    mbar_init(kv_full, 1); mbar_init(kv_empty, 1);
+    for (int i = 0; i < 4; ++i) { mbar_init(&st_full[i], 33); mbar_init(&st_empty[i], 1); }
+    mbar_init(sp_full, 1); mbar_init(sp_empty, 8);
+    mbar_init(pd_full, 8); mbar_init(pd_empty, 1);
+    mbar_init(acc_full, 1); mbar_init(acc_empty, 8);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(tslot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = *tslot;
+  const int units = tiles + (a.sinks > 0 && sk.slots > 0 ? min(sk.chunk0[a.ndocs], sk.chunks) : 0);
+  const int items = units * a.Hkv;
+
+  if (warp == 8) {
+    // ---------------- producer: TMA by lane 0, lse and D by all ----------------
+    if (lane == 0) {
+      tma_prefetch_map(&tm_q);
+      tma_prefetch_map(&tm_do);
+      tma_prefetch_map(&tm_k);
+      tma_prefetch_map(&tm_v);
+    }
+    const uint32_t box = (uint32_t)(qt * hc) * 128u * (C::QA + C::VA);
+    uint32_t ni = 0, ns = 0;
+    bool ok = true;
+    for (int item = blockIdx.x; item < items && ok; item += gridDim.x, ++ni) {
+      const DkvItem m = dkv_item(a, sk, item, tiles, qt, nhc);
+      if (ni > 0 && !__all_sync(0xffffffffu, mbar_wait(kv_empty, (ni - 1) & 1, abort_flag, a.err))) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(kv_full, C::k_bytes + C::v_bytes);
+        for (int c = 0; c < C::QA; ++c) tma_load_3d(smem + c * kAtom, &tm_k, c * 64, m.g, m.s0, kv_full);
+        for (int c = 0; c < C::VA; ++c) tma_load_3d(smem + C::k_bytes + c * kAtom, &tm_v, c * 64, m.g, m.s0, kv_full);
+      }
+      for (int b = 0; b < m.nblk; ++b, ++ns) {
+        const uint32_t st = ns % ST;
+        const int tb = m.t0 + b / nhc * qt, hb = b % nhc * hc;
+        float v[4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int c = lane + 32 * i, t = tb + c / hc, h = hb + c % hc;
+          const bool in = c < qt * hc && t < a.T && h < a.G;
+          const int64_t row = (int64_t)t * a.Hq + m.g * a.G + h;
+          v[2 * i] = in ? a.lse_in[row] * kLog2e : 0.f;
+          v[2 * i + 1] = in ? a.delta[row] : 0.f;
+        }
+        if (ns >= ST && !__all_sync(0xffffffffu, mbar_wait(&st_empty[st], (ns / ST - 1) & 1, abort_flag, a.err))) { ok = false; break; }
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&st_full[st], box);
+          uint8_t* dst = smem + C::st_off + st * C::st_bytes;
+          for (int c = 0; c < C::QA; ++c) tma_load_3d(dst + c * kAtom64, &tm_q, c * 64, m.g * a.G + hb, tb, &st_full[st]);
+          for (int c = 0; c < C::VA; ++c)
+            tma_load_3d(dst + C::q_bytes + c * kAtom64, &tm_do, c * 64, m.g * a.G + hb, tb, &st_full[st]);
+        }
+        float* l = ld + st * 2 * kCols;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          l[lane + 32 * i] = v[2 * i];
+          l[kCols + lane + 32 * i] = v[2 * i + 1];
+        }
+        mbar_arrive(&st_full[st]);
+      }
+    }
+    if (*abort_flag && lane == 0) {
+      if (ni > 0) wait_landed(kv_full, (ni - 1) & 1);
+      for (uint32_t i = ns > ST ? ns - ST : 0; i < ns; ++i) wait_landed(&st_full[i % ST], (i / ST) & 1);
+    }
+  } else if (warp == 9) {
+    // ---------------- MMA issuer ----------------
+    if (lane == 0) {
+      constexpr uint32_t S_IDESC = idesc_bf16(128, kCols, false, false);
+      constexpr uint32_t DV_IDESC = idesc_bf16(128, DV, false, true), DK_IDESC = idesc_bf16(128, DQK, false, true);
+      const uint32_t sb = smem_u32(smem);
+      uint32_t nsc = 0, npd = 0, ni = 0;   // blocks scored, blocks summed, items
+      bool alive = true;
+      auto scores = [&]() {
+        const uint32_t st = nsc % ST;
+        if (!mbar_wait(&st_full[st], (nsc / ST) & 1, abort_flag, a.err)) return false;
+        if (nsc > 0 && !mbar_wait(sp_empty, (nsc - 1) & 1, abort_flag, a.err)) return false;
+        tc_fence_after();
+        const uint32_t q = sb + C::st_off + st * C::st_bytes;
+        ss_run<C::QA>(tbase + C::S0, sb, kAtom, q, kAtom64, S_IDESC);
+        ss_run<C::VA>(tbase + C::P0, sb + C::k_bytes, kAtom, q + C::q_bytes, kAtom64, S_IDESC);
+        umma_commit(sp_full);
+        ++nsc;
+        return true;
+      };
+      for (int item = blockIdx.x; item < items && alive; item += gridDim.x, ++ni) {
+        const DkvItem m = dkv_item(a, sk, item, tiles, qt, nhc);
+        if (!mbar_wait(kv_full, ni & 1, abort_flag, a.err)) break;
+        if (!scores()) break;
+        if (m.nblk == 1) umma_commit(kv_empty);
+        for (int b = 0; b < m.nblk; ++b) {
+          if (b + 1 < m.nblk) {
+            if (!scores()) { alive = false; break; }
+            if (b + 2 == m.nblk) umma_commit(kv_empty);
+          }
+          if (!mbar_wait(pd_full, npd & 1, abort_flag, a.err)) { alive = false; break; }
+          if (b == 0 && ni > 0 && !mbar_wait(acc_empty, (ni - 1) & 1, abort_flag, a.err)) { alive = false; break; }
+          tc_fence_after();
+          const uint32_t st = npd % ST, q = sb + C::st_off + st * C::st_bytes;
+          ts_run<4>(tbase + C::DV0, tbase + C::PW0, q + C::q_bytes, kAtom64, DV_IDESC, b > 0);
+          ts_run<4>(tbase + C::DK0, tbase + C::DS0, q, kAtom64, DK_IDESC, b > 0);
+          umma_commit(pd_empty);
+          umma_commit(&st_empty[st]);
+          ++npd;
+        }
+        if (!alive) break;
+        umma_commit(acc_full);
+      }
+      umma_commit(drain);
+      wait_landed(drain, 0);
+    }
+  } else {
+    // ---------------- score warps: key = TMEM lane, 32 of a block's 64 rows each ----------------
+    const int half = warp >> 2;
+    const int r = (warp & 3) * 32 + lane;
+    const uint32_t lanes = tmem_lane_base(warp);
+    uint32_t nb = 0, ni = 0;
+    bool alive = true;
+    for (int item = blockIdx.x; item < items && alive; item += gridDim.x, ++ni) {
+      const DkvItem m = dkv_item(a, sk, item, tiles, qt, nhc);
+      const int s = m.s0 + r;
+      const bool live = r < m.keys;
+      int di = 0;
+      const WinDoc doc = window_doc(a.cu, a.ndocs, a.T, min(s, a.T - 1), &di);
+      // this key's queries of the item: [from, to)
+      const int64_t past = (int64_t)s + a.window;
+      const int from = m.chunk < 0 ? s : (int)min(past, (int64_t)m.t1);
+      const int to = m.chunk < 0 ? (int)min(past, (int64_t)doc.end) : m.t1;
+      // a block is whole when every key of the tile sees every row
+      int all0, all1;
+      if (m.chunk < 0) {
+        const WinDoc d0 = window_doc(a.cu, a.ndocs, a.T, m.s0);
+        all0 = m.s0 + m.keys - 1;
+        all1 = (int)min((int64_t)m.s0 + a.window, (int64_t)d0.end);
+      } else {
+        all0 = (int)min((int64_t)m.s0 + m.keys - 1 + a.window, (int64_t)m.t1);
+        all1 = m.t1;
+      }
+      for (int b = 0; b < m.nblk; ++b, ++nb) {
+        const uint32_t st = nb % ST;
+        const int tb = m.t0 + b / nhc * qt, valid = min(qt * hc, a.G - b % nhc * hc < hc ? a.G - b % nhc * hc : qt * hc);
+        const bool whole = tb >= all0 && tb + qt <= all1 && valid == kCols;
+        int c0 = 0, c1 = kCols;
+        if (!whole) {
+          c0 = max(from - tb, 0) * hc;
+          c1 = min(valid, max(min(to - tb, qt), 0) * hc);
+        }
+        if (!__all_sync(0xffffffffu, mbar_wait(&st_full[st], (nb / ST) & 1, abort_flag, a.err) &&
+                                         mbar_wait(sp_full, nb & 1, abort_flag, a.err))) {
+          alive = false;
+          break;
+        }
+        tc_fence_after();
+        float sc[32], dp[32];
+        tmem_ld32(tbase + C::S0 + lanes + 32 * half, sc);
+        tmem_ld32(tbase + C::P0 + lanes + 32 * half, dp);
+        tmem_ld_wait_regs(sc);
+        tmem_ld_wait_regs(dp);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sp_empty);
+        const float4* l4 = reinterpret_cast<const float4*>(ld + st * 2 * kCols + 32 * half);
+        const float4* d4 = reinterpret_cast<const float4*>(ld + st * 2 * kCols + kCols + 32 * half);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float4 l = l4[i], d = d4[i];
+          const float lv[4] = {l.x, l.y, l.z, l.w}, dv[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int c = 4 * i + k;
+            sc[c] = ex2_approx(fmaf(sc[c], a.scale_log2, -lv[k]));
+            dp[c] = sc[c] * (dp[c] - dv[k]);
+          }
+        }
+        if (!whole) {
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            const bool in = c + 32 * half >= c0 && c + 32 * half < c1;
+            sc[c] = in ? sc[c] : 0.f;
+            dp[c] = in ? dp[c] : 0.f;
+          }
+        }
+        float w[16], x[16];
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) {
+          const __nv_bfloat162 p = __floats2bfloat162_rn(sc[c], sc[c + 1]), q = __floats2bfloat162_rn(dp[c], dp[c + 1]);
+          w[c >> 1] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&p));
+          x[c >> 1] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&q));
+        }
+        if (nb > 0 && !__all_sync(0xffffffffu, mbar_wait(pd_empty, (nb - 1) & 1, abort_flag, a.err))) { alive = false; break; }
+        tmem_st16(tbase + C::PW0 + lanes + 16 * half, w);
+        tmem_st16(tbase + C::DS0 + lanes + 16 * half, x);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(pd_full);
+      }
+      if (!alive) break;
+      if (!__all_sync(0xffffffffu, mbar_wait(acc_full, ni & 1, abort_flag, a.err))) break;
+      tc_fence_after();
+      // ---- this key's sums: half 0 dv, half 1 dk ----
+      const bool far = m.chunk >= 0 || (s - doc.start < a.sinks && doc.end - doc.start > a.window && sk.slots > 0);
+      float* part = nullptr;   // FP32 rows [DQK | DV] of first tokens
+      if (m.chunk >= 0) part = sk.part + (((int64_t)m.chunk * a.Hkv + m.g) * a.sinks + r) * (DQK + DV);
+      else if (live && far) part = sk.base + (((int64_t)sk.slot[di] * a.Hkv + m.g) * a.sinks + (s - doc.start)) * (DQK + DV);
+      const int64_t row = (int64_t)s * a.Hkv + m.g;
+      float odd = 0.f;
+#pragma unroll 1
+      for (int d = 0; d < (half == 0 ? DV : DQK); d += 32) {
+        float o[32];
+        tmem_ld32(tbase + (half == 0 ? C::DV0 : C::DK0) + lanes + d, o);
+        tmem_ld_wait_regs(o);
+        const float f = half == 0 ? 1.f : a.scale;
+        if (live && far) {
+          float* dst = part + (half == 0 ? DQK : 0) + d;
+#pragma unroll
+          for (int i = 0; i < 32; i += 4)
+            *reinterpret_cast<float4*>(dst + i) = make_float4(o[i] * f, o[i + 1] * f, o[i + 2] * f, o[i + 3] * f);
+        } else {
+          uint32_t w[16];
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            odd = fmaf(o[i], 0.f, fmaf(o[i + 1], 0.f, odd));
+            const __nv_bfloat162 b = __floats2bfloat162_rn(o[i] * f, o[i + 1] * f);
+            w[i >> 1] = *reinterpret_cast<const uint32_t*>(&b);
+          }
+          if (live) {
+            uint4* dst = reinterpret_cast<uint4*>(half == 0 ? a.dv + row * DV + d : a.dk + row * DQK + d);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) dst[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(acc_empty);
+      // a key is done again by the half whose sums are not finite, each its own output
+      unsigned again = __ballot_sync(0xffffffffu, live && !far && odd != 0.f);
+      while (again) {
+        const int src = __ffs((int)again) - 1;
+        again &= again - 1;
+        dkv_row<DQK / 64, DV / 64>(a, __shfl_sync(0xffffffffu, s, src), m.g, lane, half == 1, half == 0);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tbase, 512);
+  }
+}
+
+// ---------------------------------------------------------------------------------------
+// First tokens: which documents have far queries, and the joining of their sums
+// ---------------------------------------------------------------------------------------
+constexpr int kPlanThreads = 1024;
+
+// slot[d]: the document's place among those longer than the window; chunk0[d]: its first
+// stretch; doc[slot]. One block.
+__global__ void __launch_bounds__(kPlanThreads) window_plan_kernel(WinArgs a, WinSinks sk) {
+  __shared__ int s_slot[kPlanThreads], s_chunk[kPlanThreads];
+  const int tid = threadIdx.x;
+  const int per = (a.ndocs + kPlanThreads - 1) / kPlanThreads;
+  const int b = min(a.ndocs, tid * per), e = min(a.ndocs, b + per);
+  const int n = sink_stretch(a.window);
+  auto chunks_of = [&](int d) {
+    const int start = min(max(a.cu[d], 0), a.T - 1), end = max(min(a.cu[d + 1], a.T), start + 1);
+    const int far = end - start - a.window;
+    return far > 0 ? (far + n - 1) / n : 0;
+  };
+  int slots = 0, chunks = 0;
+  for (int d = b; d < e; ++d) {
+    const int c = chunks_of(d);
+    slots += c > 0;
+    chunks += c;
+  }
+  s_slot[tid] = slots;
+  s_chunk[tid] = chunks;
+  __syncthreads();
+  for (int o = 1; o < kPlanThreads; o <<= 1) {
+    const int x = tid >= o ? s_slot[tid - o] : 0, y = tid >= o ? s_chunk[tid - o] : 0;
+    __syncthreads();
+    s_slot[tid] += x;
+    s_chunk[tid] += y;
+    __syncthreads();
+  }
+  int slot = s_slot[tid] - slots, chunk = s_chunk[tid] - chunks;
+  for (int d = b; d < e; ++d) {
+    const int c = chunks_of(d);
+    // the clamps only matter where cu_seqlens is malformed
+    sk.slot[d] = min(slot, sk.slots - 1);
+    sk.chunk0[d] = min(chunk, sk.chunks);
+    if (c > 0 && slot < sk.slots) sk.doc[slot] = d;
+    slot += c > 0;
+    chunk += c;
+  }
+  if (tid == kPlanThreads - 1) {
+    sk.chunk0[a.ndocs] = min(s_chunk[tid], sk.chunks);
+    sk.doc[sk.slots] = min(s_slot[tid], sk.slots);   // how many slots are used
+  }
+}
+
+template <int DQK, int DV>
+__global__ void __launch_bounds__(128) window_join_kernel(WinArgs a, WinSinks sk) {
+  const int slot = blockIdx.x / (a.Hkv * a.sinks), gi = blockIdx.x % (a.Hkv * a.sinks), g = gi / a.sinks, i = gi % a.sinks;
+  if (slot >= sk.doc[sk.slots]) return;
+  const int d = sk.doc[slot];
+  const int start = min(max(a.cu[d], 0), a.T - 1), end = max(min(a.cu[d + 1], a.T), start + 1);
+  if (i >= end - start) return;
+  constexpr int D = DQK + DV;
+  const int c0 = sk.chunk0[d], c1 = sk.chunk0[d + 1];
+  const int64_t row = (int64_t)(start + i) * a.Hkv + g;
+  const float* base = sk.base + (((int64_t)slot * a.Hkv + g) * a.sinks + i) * D;
+  const float* part = sk.part + ((int64_t)g * a.sinks + i) * D;
+  const int64_t step = (int64_t)a.Hkv * a.sinks * D;
+  float odd = 0.f;
+  for (int x = threadIdx.x; x < D; x += 128) {
+    float s = base[x];
+#pragma unroll 8
+    for (int c = c0; c < c1; ++c) s += part[c * step + x];
+    odd = fmaf(s, 0.f, odd);
+    if (x < DQK) a.dk[row * DQK + x] = __float2bfloat16_rn(s);
+    else a.dv[row * DV + x - DQK] = __float2bfloat16_rn(s);
+  }
+  if (__syncthreads_or(odd != 0.f) && threadIdx.x < 32) dkv_row<DQK / 64, DV / 64>(a, start + i, g, threadIdx.x, true, true);
+}
+
+template <int DQK, int DV>
+cudaError_t launch_bwd(const WinBwdMaps& m, const WinArgs& a, const WinSinks& sk, int num_sms, bool* configured,
+                       cudaStream_t stream) {
+  using Q = DqCfg<DQK, DV>;
+  using K = DkvCfg<DQK, DV>;
+  cudaError_t e;
+  if (!*configured) {
+    if ((e = cudaFuncSetAttribute(window_dq_kernel<DQK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Q::total)) != cudaSuccess)
+      return e;
+    if ((e = cudaFuncSetAttribute(window_dkv_kernel<DQK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)K::total)) != cudaSuccess)
+      return e;
+    *configured = true;
+  }
+  const int qt = 128 / a.G, tiles = (a.T + qt - 1) / qt, ktiles = (a.T + kBlk - 1) / kBlk;
+  const int64_t items = (int64_t)tiles * a.Hkv;
+  window_dq_kernel<DQK, DV><<<items < num_sms ? (int)items : num_sms, kBwdThreads, Q::total, stream>>>(m.q, m.dout, m.k, m.v, a, qt, tiles);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if (sk.slots > 0) {
+    window_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a, sk);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  const int64_t kitems = ((int64_t)ktiles + sk.chunks) * a.Hkv;
+  window_dkv_kernel<DQK, DV><<<kitems < num_sms ? (int)kitems : num_sms, kBwdThreads, K::total, stream>>>(m.q2, m.dout2, m.k, m.v, a, sk, ktiles);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if (sk.slots > 0)
+    window_join_kernel<DQK, DV><<<(unsigned)(sk.slots * a.Hkv * a.sinks), 128, 0, stream>>>(a, sk);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+// Workspace: D of every row; then, with first tokens, the plan and the FP32 sums.
+size_t window_bwd_workspace_bytes(int T, int Hq, int Hkv, int Dqk, int Dv, int ndocs, int window, int sinks) {
+  WinSinks s;
+  return window_bwd_layout(nullptr, T, Hq, Hkv, Dqk, Dv, ndocs, window, sinks, &s);
+}
+
+size_t window_bwd_layout(uint8_t* ws, int T, int Hq, int Hkv, int Dqk, int Dv, int ndocs, int window, int sinks, WinSinks* s) {
+  size_t off = ((size_t)T * Hq * 4 + 255) & ~size_t(255);
+  auto take = [&](size_t bytes) {
+    uint8_t* p = ws + off;
+    off += (bytes + 255) & ~size_t(255);
+    return p;
+  };
+  *s = WinSinks{};
+  const int64_t longer = (int64_t)T / ((int64_t)window + 1);   // documents that can be longer than the window
+  s->slots = sinks > 0 ? (int)(longer < ndocs ? longer : ndocs) : 0;
+  if (s->slots > 0) {
+    s->chunks = T / sink_stretch(window) + s->slots;
+    s->slot = reinterpret_cast<int*>(take((size_t)ndocs * 4));
+    s->chunk0 = reinterpret_cast<int*>(take((size_t)(ndocs + 1) * 4));
+    s->doc = reinterpret_cast<int*>(take((size_t)(s->slots + 1) * 4));
+    const size_t rows = (size_t)Hkv * sinks * (Dqk + Dv) * 4;
+    s->base = reinterpret_cast<float*>(take((size_t)s->slots * rows));
+    s->part = reinterpret_cast<float*>(take((size_t)s->chunks * rows));
+  }
+  return off + 256;
+}
+
+cudaError_t launch_window_bwd_tc(const WinBwdMaps& m, const WinArgs& a, const WinSinks& sk, int num_sms, bool* configured,
+                                 cudaStream_t stream) {
+  const int i = (a.Dqk / 64 - 1) * 2 + (a.Dv / 64 - 1);
+  switch (i) {
+    case 0: return launch_bwd<64, 64>(m, a, sk, num_sms, configured + i, stream);
+    case 1: return launch_bwd<64, 128>(m, a, sk, num_sms, configured + i, stream);
+    case 2: return launch_bwd<128, 64>(m, a, sk, num_sms, configured + i, stream);
+    case 3: return launch_bwd<128, 128>(m, a, sk, num_sms, configured + i, stream);
+    case 4: return launch_bwd<192, 64>(m, a, sk, num_sms, configured + i, stream);
+    default: return launch_bwd<192, 128>(m, a, sk, num_sms, configured + i, stream);
+  }
+}
+
+}  // namespace irs

@@ -105,7 +105,7 @@ __device__ void dq_row(const WinArgs& a, int t, int h, int lane) {
 }
 
 template <int NQ, int NV>
-__device__ void dkv_row(const WinArgs& a, int s, int g, int lane) {
+__device__ void dkv_row(const WinArgs& a, int s, int g, int lane, bool want_dk = true, bool want_dv = true) {
   const WinDoc doc = window_doc(a.cu, a.ndocs, a.T, s);
   const int64_t last = (int64_t)s + a.window;   // first query past the window
   const int end = s - doc.start < a.sinks || last > doc.end ? doc.end : (int)last;
@@ -129,8 +129,8 @@ __device__ void dkv_row(const WinArgs& a, int s, int g, int lane) {
     }
   }
   const int64_t row = (int64_t)s * a.Hkv + g;
-  store_row<NQ>(dk, a.scale, a.dk + row * (64 * NQ), lane);
-  store_row<NV>(dv, 1.f, a.dv + row * (64 * NV), lane);
+  if (want_dk) store_row<NQ>(dk, a.scale, a.dk + row * (64 * NQ), lane);
+  if (want_dv) store_row<NV>(dv, 1.f, a.dv + row * (64 * NV), lane);
 }
 
 }  // namespace
