@@ -8,6 +8,7 @@ library is missing or the device is not an sm_103 GPU, the calls raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import threading
@@ -84,6 +85,8 @@ _SIGNATURES = {
 def lib() -> ctypes.CDLL:
     """The loaded library (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -695,57 +698,81 @@ def sparse_gqa_attn_fwd_grouped(q: torch.Tensor, k: torch.Tensor, v: torch.Tenso
 # Rotary positions, the paged cache and window attention
 # ---------------------------------------------------------------------------------------
 ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+_raw_stream = torch._C._cuda_getCurrentRawStream   # current_stream() without its Python object: 0.1 us for 2
+_BF16, _F32, _F64, _I32 = torch.bfloat16, torch.float32, torch.float64, torch.int32
 
 
-def _on(dev: torch.device, fn, *args):
-    """fn(*args) with `dev` as the current device (the library launches on the current one)."""
-    if torch.cuda.current_device() == dev.index:
-        return fn(*args)
-    with torch.cuda.device(dev):
-        return fn(*args)
+def _call(index: int, what: str, fn, *args) -> None:
+    """fn(*args, current stream) with GPU `index` current (the library launches on the current one)."""
+    if torch.cuda.current_device() == index:
+        st = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            st = fn(*args, _raw_stream(index))
+    if st:
+        _check(st, what)
 
 
-def _st(t: torch.Tensor, dim: int) -> int:
-    """The stride of a dim in elements; 0 where the dim has one entry (its stride is arbitrary)."""
-    return 0 if t.shape[dim] == 1 else t.stride(dim)
+def _first(t: torch.Tensor, name: str, dtype: torch.dtype) -> int:
+    """The GPU index of the tensor that decides where a call runs."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return index
 
 
-def _rows(t: torch.Tensor, name: str, ndim: int, dev: torch.device) -> None:
-    """A bf16 tensor whose last dim is contiguous, on `dev`."""
-    _need(t, name, torch.bfloat16, ndim)
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, not {dev}")
-    if t.stride(-1) != 1 and t.shape[-1] != 1:
+def _look(t: torch.Tensor, name: str, dtype: torch.dtype, ndim: int, index: int):
+    """(shape, strides) of a tensor whose last dim is contiguous, its type and place checked."""
+    if _first(t, name, dtype) != index:
+        raise ValueError(f"{name} is on {t.device}, not cuda:{index}")
+    shape, strides = t.shape, t.stride()
+    if len(shape) != ndim:
+        raise ValueError(f"{name} must have {ndim} dims, got shape {tuple(shape)}")
+    if strides[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name} must have unit inner stride")
+    return shape, strides
 
 
-def _ints(t: torch.Tensor, name: str, shape: tuple, dev: torch.device) -> None:
-    """An int32 tensor of this shape (None: any size) with unit inner stride, on `dev`."""
-    _need(t, name, torch.int32, len(shape))
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, not {dev}")
-    if any(n is not None and n != m for n, m in zip(shape, t.shape)) or (t.stride(-1) != 1 and t.shape[-1] > 1):
-        raise ValueError(f"{name} must have shape {tuple('*' if n is None else n for n in shape)} and unit inner "
-                         f"stride, got {tuple(t.shape)}")
-
-
-def _result(t: torch.Tensor | None, name: str, shape: tuple, dtype: torch.dtype, dev: torch.device) -> torch.Tensor:
+def _result(t: torch.Tensor | None, name: str, shape: tuple, dtype: torch.dtype, index: int) -> torch.Tensor:
     """An output: a fresh contiguous tensor, or the caller's, checked."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    if tuple(t.shape) != shape or t.dtype != dtype or t.device != dev or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor {shape} on {dev}")
+        return torch.empty(shape, dtype=dtype, device=index)
+    if _first(t, name, dtype) != index or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {shape} on cuda:{index}")
     return t
 
 
-def _scratch(t: torch.Tensor | None, nbytes: int, dev: torch.device) -> torch.Tensor:
+def _scratch(t: torch.Tensor | None, nbytes: int, index: int) -> torch.Tensor:
     """Scratch of at least nbytes: the caller's where it is large enough, else fresh."""
     if t is not None:
-        if t.dtype != torch.uint8 or t.device != dev or not t.is_contiguous():
-            raise ValueError(f"workspace must be a contiguous uint8 tensor on {dev}")
+        if _first(t, "workspace", torch.uint8) != index or not t.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous uint8 tensor on cuda:{index}")
         if t.numel() >= nbytes:
             return t
-    return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    return torch.empty(nbytes, dtype=torch.uint8, device=index)
+
+
+def _err(err: torch.Tensor | None, index: int) -> int:
+    """The address of the device error word."""
+    if err is None:
+        err = _err_flags.get(index)
+        if err is None:
+            err = device_error_flag(torch.device("cuda", index))
+    return err.data_ptr()
+
+
+@functools.lru_cache(maxsize=4096)
+def _decode_bytes(B: int, Hq: int, Hkv: int, Dv: int) -> int:
+    return int(lib().irs_paged_gqa_attn_decode_workspace_bytes(B, Hq, Hkv, Dv))
+
+
+@functools.lru_cache(maxsize=4096)
+def _window_bwd_bytes(*sizes: int) -> int:
+    return int(lib().irs_window_gqa_attn_bwd_workspace_bytes(*sizes))
 
 
 def rope_frequencies(rope_dims: int, base: float = 10000.0, *, scaling: str | None = None, factor: float = 1.0,
@@ -785,19 +812,17 @@ def rope_frequencies(rope_dims: int, base: float = 10000.0, *, scaling: str | No
     return f.to(device if device is not None else "cpu"), amplitude
 
 
-def _rope_table(inv_freq: torch.Tensor | None, dev: torch.device) -> int:
-    if inv_freq is None:
-        return 0
-    _need(inv_freq, "inv_freq", torch.float64, 1)
-    if inv_freq.device != dev or not inv_freq.is_contiguous():
-        raise ValueError(f"inv_freq must be a contiguous fp64 [rope_dims / 2] on {dev}")
-    return 2 * inv_freq.numel()
+def _rope_table(inv_freq: torch.Tensor, index: int) -> tuple[int, int]:
+    """(address, rotated dims) of a frequency table."""
+    shape, _ = _look(inv_freq, "inv_freq", _F64, 1, index)
+    return inv_freq.data_ptr(), 2 * shape[0]
 
 
 def _layout(layout: str) -> int:
-    if layout not in ROPE_LAYOUTS:
+    code = ROPE_LAYOUTS.get(layout)
+    if code is None:
         raise ValueError("layout must be 'half' or 'interleaved'")
-    return ROPE_LAYOUTS[layout]
+    return code
 
 
 def rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, *, layout: str = "half", start: int = 0,
@@ -809,36 +834,34 @@ def rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, *, la
     2i and 2i + 1. transpose=True applies the transposed map: the gradient with respect to x
     from the gradient of the result. out may be x.
     """
-    _need(x, "x", torch.bfloat16, 3)
-    dev = x.device
-    _rows(x, "x", 3, dev)
-    T, H, D = x.shape
-    _ints(positions, "positions", (T,), dev)
-    if inv_freq is None:
-        raise ValueError("inv_freq is needed")
-    n = _rope_table(inv_freq, dev)
+    index = _first(x, "x", _BF16)
+    shape, (xt, xh, _) = _look(x, "x", _BF16, 3, index)
+    T, H, D = shape
+    if _look(positions, "positions", _I32, 1, index)[0][0] != T:
+        raise ValueError(f"positions must have shape ({T},)")
+    table, n = _rope_table(inv_freq, index)
     if out is None:
-        out = torch.empty((T, H, D), dtype=torch.bfloat16, device=dev)
+        out = torch.empty((T, H, D), dtype=_BF16, device=index)
+        ot, oh = H * D, D
     else:
-        _rows(out, "out", 3, dev)
-        if out.shape != x.shape:
-            raise ValueError(f"out must have x's shape {tuple(x.shape)}")
-    st = _on(dev, lib().irs_rope, _ptr(x), _st(x, 0), _st(x, 1), _ptr(positions), _ptr(inv_freq), T, H, D, n, int(start),
-             _layout(layout), float(amplitude), int(bool(transpose)), _ptr(out), _st(out, 0), _st(out, 1), _stream(dev))
-    _check(st, "rope")
+        oshape, (ot, oh, _) = _look(out, "out", _BF16, 3, index)
+        if oshape != shape:
+            raise ValueError(f"out must have x's shape {tuple(shape)}")
+    _call(index, "rope", lib().irs_rope, x.data_ptr(), xt, xh, positions.data_ptr(), table, T, H, D, n, start,
+          _layout(layout), amplitude, 1 if transpose else 0, out.data_ptr(), ot, oh)
     return out
 
 
-def _pool(k_cache, v_cache, page_table, cache_lens, dev):
-    """(Hkv, Dqk, Dv, B) of a paged cache, its tensors checked."""
-    _rows(k_cache, "k_cache", 4, dev)
-    _rows(v_cache, "v_cache", 4, dev)
-    if k_cache.shape[:3] != v_cache.shape[:3]:
-        raise ValueError(f"shape mismatch: k_cache {tuple(k_cache.shape)} v_cache {tuple(v_cache.shape)}")
-    _ints(page_table, "page_table", (None, None), dev)
-    B = page_table.shape[0]
-    _ints(cache_lens, "cache_lens", (B,), dev)
-    return k_cache.shape[2], k_cache.shape[3], v_cache.shape[3], B
+def _pool(k_cache, v_cache, page_table, cache_lens, index: int):
+    """(shape of the key pool, Dv, its strides, the value pool's, page table shape, row stride)."""
+    ks, kst = _look(k_cache, "k_cache", _BF16, 4, index)
+    vs, vst = _look(v_cache, "v_cache", _BF16, 4, index)
+    if ks[:3] != vs[:3]:
+        raise ValueError(f"shape mismatch: k_cache {tuple(ks)} v_cache {tuple(vs)}")
+    ts, tst = _look(page_table, "page_table", _I32, 2, index)
+    if _look(cache_lens, "cache_lens", _I32, 1, index)[0][0] != ts[0]:
+        raise ValueError(f"cache_lens must have shape ({ts[0]},)")
+    return ks, vs[3], kst, vst, ts, tst[0] if ts[0] > 1 else ts[1]
 
 
 def paged_rope_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
@@ -857,46 +880,45 @@ def paged_rope_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, 
     left alone. inv_freq None: no rotation. Returns the rotated queries (q_out, which may be
     q); k_out, if given, also receives the rotated keys.
     """
-    _need(k, "k", torch.bfloat16, 3)
-    dev = k.device
-    Hkv, Dqk, Dv, B = _pool(k_cache, v_cache, page_table, cache_lens, dev)
-    T = k.shape[0]
-    _rows(k, "k", 3, dev)
-    _rows(v, "v", 3, dev)
-    if tuple(k.shape) != (T, Hkv, Dqk) or tuple(v.shape) != (T, Hkv, Dv):
-        raise ValueError(f"shape mismatch: k {tuple(k.shape)} v {tuple(v.shape)} for a cache of {Hkv} heads of {Dqk} "
+    index = _first(k, "k", _BF16)
+    (pages, page, Hkv, Dqk), Dv, kcs, vcs, (B, max_pages), ts = _pool(k_cache, v_cache, page_table, cache_lens, index)
+    kshape, (kt, kh, _) = _look(k, "k", _BF16, 3, index)
+    vshape, (vt, vh, _) = _look(v, "v", _BF16, 3, index)
+    T = kshape[0]
+    if kshape != (T, Hkv, Dqk) or vshape != (T, Hkv, Dv):
+        raise ValueError(f"shape mismatch: k {tuple(kshape)} v {tuple(vshape)} for a cache of {Hkv} heads of {Dqk} "
                          f"and {Dv}")
-    Hq, qs, qos, kos = 0, (0, 0), (0, 0), (0, 0)
+    Hq = qp = qt = qh = op = ot = oh = kop = kot = koh = 0
     if q is not None:
-        _rows(q, "q", 3, dev)
-        Hq = q.shape[1]
-        if tuple(q.shape) != (T, Hq, Dqk) or Hq < 1:
-            raise ValueError(f"shape mismatch: q {tuple(q.shape)} for {T} tokens of head dim {Dqk}")
+        qshape, (qt, qh, _) = _look(q, "q", _BF16, 3, index)
+        Hq = qshape[1]
+        if qshape != (T, Hq, Dqk) or Hq < 1:
+            raise ValueError(f"shape mismatch: q {tuple(qshape)} for {T} tokens of head dim {Dqk}")
         if q_out is None:
-            q_out = torch.empty((T, Hq, Dqk), dtype=torch.bfloat16, device=dev)
-        _rows(q_out, "q_out", 3, dev)
-        if q_out.shape != q.shape:
-            raise ValueError(f"q_out must have q's shape {tuple(q.shape)}")
-        qs, qos = (_st(q, 0), _st(q, 1)), (_st(q_out, 0), _st(q_out, 1))
+            q_out = torch.empty((T, Hq, Dqk), dtype=_BF16, device=index)
+            ot, oh = Hq * Dqk, Dqk
+        else:
+            oshape, (ot, oh, _) = _look(q_out, "q_out", _BF16, 3, index)
+            if oshape != qshape:
+                raise ValueError(f"q_out must have q's shape {tuple(qshape)}")
+        qp, op = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out needs q")
     if k_out is not None:
-        _rows(k_out, "k_out", 3, dev)
-        if k_out.shape != k.shape:
-            raise ValueError(f"k_out must have k's shape {tuple(k.shape)}")
-        kos = (_st(k_out, 0), _st(k_out, 1))
+        oshape, (kot, koh, _) = _look(k_out, "k_out", _BF16, 3, index)
+        if oshape != kshape:
+            raise ValueError(f"k_out must have k's shape {tuple(kshape)}")
+        kop = k_out.data_ptr()
+    cu = 0
     if cu_new is not None:
-        _ints(cu_new, "cu_new", (B + 1,), dev)
-    n = _rope_table(inv_freq, dev)
-    if err is None:
-        err = device_error_flag(dev)
-    st = _on(dev, lib().irs_paged_rope_append, _ptr(q), *qs, _ptr(k), _st(k, 0), _st(k, 1), _ptr(v), _st(v, 0),
-             _st(v, 1), _ptr(cu_new), T, B, Hq, Hkv, Dqk, Dv, _ptr(page_table),
-             page_table.stride(0) if B > 1 else page_table.shape[1], page_table.shape[1], k_cache.shape[0],
-             k_cache.shape[1], _ptr(cache_lens), _ptr(inv_freq), n, int(start), _layout(layout), float(amplitude),
-             _ptr(k_cache), _st(k_cache, 0), _st(k_cache, 1), _st(k_cache, 2), _ptr(v_cache), _st(v_cache, 0),
-             _st(v_cache, 1), _st(v_cache, 2), _ptr(q_out), *qos, _ptr(k_out), *kos, _ptr(err), _stream(dev))
-    _check(st, "paged_rope_append")
+        if _look(cu_new, "cu_new", _I32, 1, index)[0][0] != B + 1:
+            raise ValueError(f"cu_new must have shape ({B + 1},)")
+        cu = cu_new.data_ptr()
+    table, n = (0, 0) if inv_freq is None else _rope_table(inv_freq, index)
+    _call(index, "paged_rope_append", lib().irs_paged_rope_append, qp, qt, qh, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh,
+          cu, T, B, Hq, Hkv, Dqk, Dv, page_table.data_ptr(), ts, max_pages, pages, page, cache_lens.data_ptr(), table, n,
+          start, _layout(layout), amplitude, k_cache.data_ptr(), kcs[0], kcs[1], kcs[2], v_cache.data_ptr(), vcs[0], vcs[1],
+          vcs[2], op, ot, oh, kop, kot, koh, _err(err, index))
     return q_out
 
 
@@ -916,48 +938,44 @@ def paged_gqa_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
     window and first tokens where they are given. A sequence with nothing to attend gives
     out = 0 and lse = -inf.
     """
-    _need(q, "q", torch.bfloat16, 3)
-    dev = q.device
-    _rows(q, "q", 3, dev)
-    Hkv, Dqk, Dv, B = _pool(k_cache, v_cache, page_table, cache_lens, dev)
-    Hq = q.shape[1]
-    if tuple(q.shape) != (B, Hq, Dqk):
-        raise ValueError(f"shape mismatch: q {tuple(q.shape)} for {B} sequences of head dim {Dqk}")
-    W, rs = 0, 0
+    index = _first(q, "q", _BF16)
+    qshape, (qb, qh, _) = _look(q, "q", _BF16, 3, index)
+    (pages, page, Hkv, Dqk), Dv, kcs, vcs, (B, max_pages), ts = _pool(k_cache, v_cache, page_table, cache_lens, index)
+    Hq = qshape[1]
+    if qshape != (B, Hq, Dqk):
+        raise ValueError(f"shape mismatch: q {tuple(qshape)} for {B} sequences of head dim {Dqk}")
+    W = rs = rp = 0
     if route_ids is not None:
-        _ints(route_ids, "route_ids", (B, None), dev)
-        W = route_ids.shape[1]
-        rs = route_ids.stride(0) if B > 1 else W
+        (rb, W), (rs, _) = _look(route_ids, "route_ids", _I32, 2, index)
+        if rb != B or W < 1:
+            raise ValueError(f"route_ids must have shape ({B}, W >= 1), got {tuple(route_ids.shape)}")
+        rp, rs = route_ids.data_ptr(), rs if B > 1 else W
     if scale is None:
         scale = 1.0 / math.sqrt(Dqk)
-    out = _result(out, "out", (B, Hq, Dv), torch.bfloat16, dev)
+    out = _result(out, "out", (B, Hq, Dv), _BF16, index)
+    lp = 0
     if lse is not None or want_lse:
-        lse = _result(lse, "lse", (B, Hq), torch.float32, dev)
-    L = lib()
-    workspace = _scratch(workspace, int(L.irs_paged_gqa_attn_decode_workspace_bytes(B, Hq, Hkv, Dv)), dev)
-    if err is None:
-        err = device_error_flag(dev)
-    st = _on(dev, L.irs_paged_gqa_attn_decode, _ptr(q), _st(q, 0), _st(q, 1), _ptr(k_cache), _st(k_cache, 0),
-             _st(k_cache, 1), _st(k_cache, 2), _ptr(v_cache), _st(v_cache, 0), _st(v_cache, 1), _st(v_cache, 2),
-             _ptr(page_table), page_table.stride(0) if B > 1 else page_table.shape[1], page_table.shape[1],
-             k_cache.shape[0], k_cache.shape[1], _ptr(cache_lens), _ptr(route_ids), rs, W, int(window), int(sinks), B,
-             Hq, Hkv, Dqk, Dv, float(scale), _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(), _ptr(err),
-             _stream(dev))
-    _check(st, "paged_gqa_attn_decode")
+        lse = _result(lse, "lse", (B, Hq), _F32, index)
+        lp = lse.data_ptr()
+    workspace = _scratch(workspace, _decode_bytes(B, Hq, Hkv, Dv), index)
+    _call(index, "paged_gqa_attn_decode", lib().irs_paged_gqa_attn_decode, q.data_ptr(), qb, qh, k_cache.data_ptr(),
+          kcs[0], kcs[1], kcs[2], v_cache.data_ptr(), vcs[0], vcs[1], vcs[2], page_table.data_ptr(), ts, max_pages, pages,
+          page, cache_lens.data_ptr(), rp, rs, W, window, sinks, B, Hq, Hkv, Dqk, Dv, scale, out.data_ptr(), lp,
+          workspace.data_ptr(), workspace.numel(), _err(err, index))
     return out, lse
 
 
 def _window_shapes(q, k, v, cu_seqlens):
-    _need(q, "q", torch.bfloat16, 3)
-    dev = q.device
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        _rows(t, name, 3, dev)
-    T, Hq, Dqk = q.shape
-    Hkv, Dv = k.shape[1], v.shape[2]
-    if tuple(k.shape) != (T, Hkv, Dqk) or tuple(v.shape) != (T, Hkv, Dv):
-        raise ValueError(f"shape mismatch: q {tuple(q.shape)} k {tuple(k.shape)} v {tuple(v.shape)}")
-    _ints(cu_seqlens, "cu_seqlens", (None,), dev)
-    return dev, T, Hq, Hkv, Dqk, Dv
+    """(GPU, sizes T Hq Hkv Dqk Dv, strides, documents), checked."""
+    index = _first(q, "q", _BF16)
+    (T, Hq, Dqk), qst = _look(q, "q", _BF16, 3, index)
+    kshape, kst = _look(k, "k", _BF16, 3, index)
+    vshape, vst = _look(v, "v", _BF16, 3, index)
+    Hkv, Dv = kshape[1], vshape[2]
+    if kshape != (T, Hkv, Dqk) or vshape != (T, Hkv, Dv):
+        raise ValueError(f"shape mismatch: q {tuple(q.shape)} k {tuple(kshape)} v {tuple(vshape)}")
+    ndocs = _look(cu_seqlens, "cu_seqlens", _I32, 1, index)[0][0] - 1
+    return index, (T, Hq, Hkv, Dqk, Dv), (qst[0], qst[1], kst[0], kst[1], vst[0], vst[1]), ndocs
 
 
 def window_gqa_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor, window: int,
@@ -971,18 +989,17 @@ def window_gqa_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_se
     t attends the last `window` tokens of its document up to itself and the document's first
     `sinks` tokens.
     """
-    dev, T, Hq, Hkv, Dqk, Dv = _window_shapes(q, k, v, cu_seqlens)
+    index, (T, Hq, Hkv, Dqk, Dv), st, ndocs = _window_shapes(q, k, v, cu_seqlens)
     if scale is None:
         scale = 1.0 / math.sqrt(Dqk)
-    out = _result(out, "out", (T, Hq, Dv), torch.bfloat16, dev)
+    out = _result(out, "out", (T, Hq, Dv), _BF16, index)
+    lp = 0
     if lse is not None or want_lse:
-        lse = _result(lse, "lse", (T, Hq), torch.float32, dev)
-    if err is None:
-        err = device_error_flag(dev)
-    st = _on(dev, lib().irs_window_gqa_attn_fwd, _ptr(q), _st(q, 0), _st(q, 1), _ptr(k), _st(k, 0), _st(k, 1), _ptr(v),
-             _st(v, 0), _st(v, 1), _ptr(cu_seqlens), cu_seqlens.numel() - 1, int(window), int(sinks), T, Hq, Hkv, Dqk,
-             Dv, float(scale), _ptr(out), _ptr(lse), _ptr(err), _stream(dev))
-    _check(st, "window_gqa_attn_fwd")
+        lse = _result(lse, "lse", (T, Hq), _F32, index)
+        lp = lse.data_ptr()
+    _call(index, "window_gqa_attn_fwd", lib().irs_window_gqa_attn_fwd, q.data_ptr(), st[0], st[1], k.data_ptr(), st[2],
+          st[3], v.data_ptr(), st[4], st[5], cu_seqlens.data_ptr(), ndocs, window, sinks, T, Hq, Hkv, Dqk, Dv, scale,
+          out.data_ptr(), lp, _err(err, index))
     return out, lse
 
 
@@ -996,26 +1013,20 @@ def window_gqa_attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_se
     out and lse are the forward's outputs, dout bf16 [T, Hq, Dv] contiguous. The gradients
     are overwritten, summed in FP32 and rounded once, and equal in every run.
     """
-    dev, T, Hq, Hkv, Dqk, Dv = _window_shapes(q, k, v, cu_seqlens)
-    for name, t, shape, dtype in (("out", out, (T, Hq, Dv), torch.bfloat16), ("dout", dout, (T, Hq, Dv), torch.bfloat16),
-                                  ("lse", lse, (T, Hq), torch.float32)):
-        _need(t, name, dtype, len(shape))
-        if tuple(t.shape) != shape or t.device != dev or not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous with shape {shape} on {dev}")
+    index, (T, Hq, Hkv, Dqk, Dv), st, ndocs = _window_shapes(q, k, v, cu_seqlens)
+    for name, t, shape, dtype in (("out", out, (T, Hq, Dv), _BF16), ("dout", dout, (T, Hq, Dv), _BF16),
+                                  ("lse", lse, (T, Hq), _F32)):
+        if t is None:
+            raise TypeError(f"{name} must be a torch.Tensor")
+        _result(t, name, shape, dtype, index)
     if scale is None:
         scale = 1.0 / math.sqrt(Dqk)
-    dq = _result(dq, "dq", (T, Hq, Dqk), torch.bfloat16, dev)
-    dk = _result(dk, "dk", (T, Hkv, Dqk), torch.bfloat16, dev)
-    dv = _result(dv, "dv", (T, Hkv, Dv), torch.bfloat16, dev)
-    L = lib()
-    ndocs = cu_seqlens.numel() - 1
-    workspace = _scratch(workspace, int(L.irs_window_gqa_attn_bwd_workspace_bytes(T, Hq, Hkv, Dqk, Dv, ndocs,
-                                                                                  int(window), int(sinks))), dev)
-    if err is None:
-        err = device_error_flag(dev)
-    st = _on(dev, L.irs_window_gqa_attn_bwd, _ptr(q), _st(q, 0), _st(q, 1), _ptr(k), _st(k, 0), _st(k, 1), _ptr(v),
-             _st(v, 0), _st(v, 1), _ptr(cu_seqlens), ndocs, int(window), int(sinks), _ptr(out), _ptr(lse), _ptr(dout), T,
-             Hq, Hkv, Dqk, Dv, float(scale), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(workspace), workspace.numel(), _ptr(err),
-             _stream(dev))
-    _check(st, "window_gqa_attn_bwd")
+    dq = _result(dq, "dq", (T, Hq, Dqk), _BF16, index)
+    dk = _result(dk, "dk", (T, Hkv, Dqk), _BF16, index)
+    dv = _result(dv, "dv", (T, Hkv, Dv), _BF16, index)
+    workspace = _scratch(workspace, _window_bwd_bytes(T, Hq, Hkv, Dqk, Dv, ndocs, window, sinks), index)
+    _call(index, "window_gqa_attn_bwd", lib().irs_window_gqa_attn_bwd, q.data_ptr(), st[0], st[1], k.data_ptr(), st[2],
+          st[3], v.data_ptr(), st[4], st[5], cu_seqlens.data_ptr(), ndocs, window, sinks, out.data_ptr(), lse.data_ptr(),
+          dout.data_ptr(), T, Hq, Hkv, Dqk, Dv, scale, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), workspace.data_ptr(),
+          workspace.numel(), _err(err, index))
     return dq, dk, dv

@@ -834,6 +834,11 @@ namespace {
 const __nv_bfloat16* bf(const void* p) { return static_cast<const __nv_bfloat16*>(p); }
 __nv_bfloat16* bf(void* p) { return static_cast<__nv_bfloat16*>(p); }
 
+// The stride of a dim with one entry is never used: 0, whatever the caller's says.
+void one_entry(int n, int64_t& stride) {
+  if (n <= 1) stride = 0;
+}
+
 bool bad_stride(std::initializer_list<int64_t> strides) {
   for (int64_t s : strides)
     if (s < 0 || s % 8 != 0) return true;
@@ -875,6 +880,8 @@ irs_status irs_rope(const void* x, int64_t x_stride_t, int64_t x_stride_h, const
   irs_status s = check_rope(inv_freq, D, rope_dims, start, layout, amplitude);
   if (s != IRS_OK || T == 0) return s;
   if (!x || !positions || !out) return fail(IRS_ERR_VALUE, "NULL tensor pointer");
+  one_entry(T, x_stride_t); one_entry(H, x_stride_h);
+  one_entry(T, out_stride_t); one_entry(H, out_stride_h);
   if (!aligned16(x) || !aligned16(out)) return fail(IRS_ERR_VALUE, "x and out must be 16-byte aligned");
   if (bad_stride({x_stride_t, x_stride_h, out_stride_t, out_stride_h}))
     return fail(IRS_ERR_VALUE, "strides must be non-negative multiples of 8 elements (16 bytes)");
@@ -914,6 +921,11 @@ irs_status irs_paged_rope_append(const void* q, int64_t q_stride_t, int64_t q_st
   if ((s = check_pool(k_cache, v_cache, page_table, cache_lens, table_stride, max_pages, num_pages, page_size)) != IRS_OK)
     return s;
   if (!k || !v || (Hq > 0 && (!q || !q_out))) return fail(IRS_ERR_VALUE, "NULL tensor pointer");
+  for (int64_t* st : {&q_stride_t, &k_stride_t, &v_stride_t, &qo_stride_t, &ko_stride_t}) one_entry(T, *st);
+  for (int64_t* st : {&k_stride_h, &v_stride_h, &ko_stride_h, &kc_stride_h, &vc_stride_h}) one_entry(Hkv, *st);
+  one_entry(Hq, q_stride_h); one_entry(Hq, qo_stride_h);
+  one_entry(num_pages, kc_stride_p); one_entry(num_pages, vc_stride_p);
+  one_entry(page_size, kc_stride_t); one_entry(page_size, vc_stride_t);
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || !aligned16(k_out))
     return fail(IRS_ERR_VALUE, "q, k, v, q_out and k_out must be 16-byte aligned");
   if (bad_stride({q_stride_t, q_stride_h, k_stride_t, k_stride_h, v_stride_t, v_stride_h, kc_stride_p, kc_stride_t,
@@ -978,6 +990,10 @@ irs_status irs_paged_gqa_attn_decode(const void* q, int64_t q_stride_b, int64_t 
   if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return fail(IRS_ERR_VALUE, "workspace must be 256-byte aligned");
   if (workspace_bytes < irs::paged_workspace_bytes(B, Dv))
     return fail(IRS_ERR_VALUE, "workspace too small: %zu < %zu bytes", workspace_bytes, irs::paged_workspace_bytes(B, Dv));
+  one_entry(B, q_stride_b); one_entry(Hq, q_stride_h);
+  one_entry(num_pages, kc_stride_p); one_entry(num_pages, vc_stride_p);
+  one_entry(page_size, kc_stride_t); one_entry(page_size, vc_stride_t);
+  one_entry(Hkv, kc_stride_h); one_entry(Hkv, vc_stride_h);
   if (bad_stride({q_stride_b, q_stride_h, kc_stride_p, kc_stride_t, kc_stride_h, vc_stride_p, vc_stride_t, vc_stride_h}))
     return fail(IRS_ERR_VALUE, "strides must be non-negative multiples of 8 elements (16 bytes)");
   DeviceInfo* dev = nullptr;
@@ -1049,6 +1065,9 @@ irs_status window_args(irs::WinArgs* a, const void* q, int64_t q_stride_t, int64
   if (T > (1 << 30) || (long long)T * Hq >= (1LL << 31)) return fail(IRS_ERR_VALUE, "T * Hq must be below 2^31");
   if (T == 0) return IRS_OK;
   if (ndocs < 1 || ndocs > T) return fail(IRS_ERR_VALUE, "ndocs must be in [1, T] (got %d)", ndocs);
+  for (int64_t* st : {&q_stride_t, &k_stride_t, &v_stride_t}) one_entry(T, *st);
+  for (int64_t* st : {&k_stride_h, &v_stride_h}) one_entry(Hkv, *st);
+  one_entry(Hq, q_stride_h);
   if (!q || !k || !v || !cu_seqlens) return fail(IRS_ERR_VALUE, "NULL tensor pointer");
   if (!aligned16(q) || !aligned16(k) || !aligned16(v)) return fail(IRS_ERR_VALUE, "q, k and v must be 16-byte aligned");
   if (bad_stride({q_stride_t, q_stride_h, k_stride_t, k_stride_h, v_stride_t, v_stride_h}))
