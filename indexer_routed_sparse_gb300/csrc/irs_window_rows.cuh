@@ -54,7 +54,7 @@ __device__ __forceinline__ void check_documents(const WinArgs& a) {
 }
 
 template <int NQ, int NV>
-__device__ void fwd_row(const WinArgs& a, int t, int h, int lane) {
+__device__ __noinline__ void fwd_row(const WinArgs& a, int t, int h, int lane) {
   const int g = h / a.G;
   const WinDoc doc = window_doc(a.cu, a.ndocs, a.T, t);
   const int lo = max(doc.start, t - a.window + 1);
@@ -82,7 +82,7 @@ __device__ void fwd_row(const WinArgs& a, int t, int h, int lane) {
 }
 
 template <int NQ, int NV>
-__device__ void dq_row(const WinArgs& a, int t, int h, int lane) {
+__device__ __noinline__ void dq_row(const WinArgs& a, int t, int h, int lane) {
   const int g = h / a.G;
   const WinDoc doc = window_doc(a.cu, a.ndocs, a.T, t);
   const int lo = max(doc.start, t - a.window + 1);
@@ -105,7 +105,7 @@ __device__ void dq_row(const WinArgs& a, int t, int h, int lane) {
 }
 
 template <int NQ, int NV>
-__device__ void dkv_row(const WinArgs& a, int s, int g, int lane, bool want_dk = true, bool want_dv = true) {
+__device__ __noinline__ void dkv_row(const WinArgs& a, int s, int g, int lane, bool want_dk = true, bool want_dv = true) {
   const WinDoc doc = window_doc(a.cu, a.ndocs, a.T, s);
   const int64_t last = (int64_t)s + a.window;   // first query past the window
   const int end = s - doc.start < a.sinks || last > doc.end ? doc.end : (int)last;

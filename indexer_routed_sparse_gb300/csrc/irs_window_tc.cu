@@ -11,9 +11,13 @@
 //   tile spans few queries and the keys it needs beyond one window are few: window 512 and
 //   G = 16 give tiles of 8 queries over 519 keys.
 // * An item is two such tiles of neighbouring queries over the same key blocks (128 keys, by
-//   TMA): while one tile's scores go through the softmax (a warpgroup, one row a thread), the
-//   tensor cores work for the other. A persistent CTA an SM walks the items; the next item's
-//   queries and keys load while the last one drains.
+//   TMA): while one tile's scores go through the softmax, the tensor cores work for the
+//   other. A persistent CTA an SM walks the items; the next item's queries and keys load
+//   while the last one drains.
+// * Two threads share a row, 64 keys of a block each (16 softmax warps). With one thread a
+//   row (8 warps of 128 values) a warp's own latency was the bound: 4 to 5 cycles an
+//   instruction, 2.72 ms at T 65536 where two take less. They hold the same maximum; one
+//   barrier of the two warps a block carries their vote whether to raise it.
 // * S[128 x 128] = Q K^T lies in TMEM; the weights return over it as bf16 and are the first
 //   operand of O += P V straight from TMEM (V read MN-major from its [key][dim] tile).
 // * The running maximum is raised only where a score passes it by 2^8 (weights stay below
@@ -34,7 +38,7 @@ namespace {
 constexpr int kBlk = 128;            // keys a block
 constexpr int kRows = 128;           // rows a tile
 constexpr uint32_t kAtom = 128 * 128;   // 128 rows x 64 bf16
-constexpr int kFwdThreads = 320;     // warps 0-3, 4-7: softmax of the two tiles; 8: TMA; 9: MMA
+constexpr int kFwdThreads = 576;     // warps 0-7, 8-15: softmax of the two tiles; 16: TMA; 17: MMA
 constexpr float kRaise = 8.f;
 
 template <int DQK, int DV>
@@ -45,8 +49,9 @@ struct FwdCfg {
   static constexpr uint32_t budget = 226u * 1024u;
   static constexpr int KS = 2;
   static constexpr int VS = 2 * q_bytes + 2 * k_bytes + 2 * v_bytes <= budget ? 2 : 1;
-  static constexpr uint32_t k_off = 2 * q_bytes, v_off = k_off + KS * k_bytes, bar_off = v_off + VS * v_bytes;
-  static constexpr uint32_t total = bar_off + 32 * 8 + 16 + 1024;
+  static constexpr uint32_t k_off = 2 * q_bytes, v_off = k_off + KS * k_bytes, x_off = v_off + VS * v_bytes;
+  static constexpr uint32_t bar_off = x_off + 2 * 2 * kRows * 4;   // a word a row, half and tile
+  static constexpr uint32_t total = bar_off + 32 * 8 + 16;   // 226.3 KB at 192/128: none to spare for aligning
   static constexpr uint32_t S0 = 0, O0 = 256;              // TMEM: S of tile x at 128 x, O at 256 + x DV
 };
 
@@ -95,13 +100,27 @@ __device__ __forceinline__ int item_last(const Item& m, int x) {   // the last a
   return x == 0 ? (m.lastA - m.klo) / kBlk + (m.ns > 0 ? 1 : 0) : m.nbt - 1;
 }
 
-// D[128 x DV] (+)= P . V: P bf16 in TMEM, V a [key][dim] tile read MN-major; NK steps of 16 keys.
+// Bits [from, to) of a 64-bit word, both clamped to [0, 64].
+__device__ __forceinline__ uint64_t bit_range(int from, int to) {
+  from = max(from, 0);
+  to = min(to, 64);
+  if (from >= to) return 0ull;
+  return (~0ull >> (64 - (to - from))) << from;
+}
+
+__device__ __forceinline__ void mask32(float (&v)[32], uint32_t bits) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = (bits >> i) & 1u ? v[i] : -INFINITY;
+}
+
+// D[128 x DV] (+)= P . V: P bf16 in TMEM (32 columns for 64 keys at the first of their 64 score
+// columns), V a [key][dim] tile read MN-major; NK steps of 16 keys.
 template <int NK>
 __device__ __forceinline__ void pv_run(uint32_t d, uint32_t p, uint32_t vb, uint32_t idesc, bool accumulate) {
   const uint64_t b0 = sdesc_sw128(vb, kAtom, 1024);
 #pragma unroll
   for (int ks = 0; ks < NK; ++ks)
-    umma_bf16_ts(d, p + 8 * ks, b0 + (uint64_t)((ks * 2048) >> 4), idesc, (accumulate || ks > 0) ? 1u : 0u);
+    umma_bf16_ts(d, p + 8 * ks + (ks >= 4 ? 32 : 0), b0 + (uint64_t)((ks * 2048) >> 4), idesc, (accumulate || ks > 0) ? 1u : 0u);
 }
 __device__ __forceinline__ void pv_any(int cols, uint32_t d, uint32_t p, uint32_t vb, uint32_t idesc, bool accumulate) {
   switch (cols >> 5) {
@@ -118,8 +137,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                       const __grid_constant__ CUtensorMap tm_v, WinArgs a, int qt, int pairs) {
   using C = FwdCfg<DQK, DV>;
   constexpr int KS = C::KS, VS = C::VS;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if ((smem_u32(smem) & 1023u) != 0) {   // the attribute asks for it; the tiles need it
+    record_error(a.err, IRS_DEVERR_TIMEOUT);
+    return;
+  }
   uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::bar_off);   // [2]
   uint64_t* q_empty = q_full + 2;     // [2]
   uint64_t* k_full = q_empty + 2;     // [KS]
@@ -140,14 +162,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       mbar_init(&q_full[i], 1); mbar_init(&q_empty[i], 1);
       mbar_init(&k_full[i], 1); mbar_init(&k_empty[i], 1);
       mbar_init(&v_full[i], 1); mbar_init(&v_empty[i], 1);
-      mbar_init(&s_full[i], 1); mbar_init(&p_full[i], 4);
-      mbar_init(&o_full[i], 1); mbar_init(&o_empty[i], 4);
+      mbar_init(&s_full[i], 1); mbar_init(&p_full[i], 8);
+      mbar_init(&o_full[i], 1); mbar_init(&o_empty[i], 8);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 9) {
+  if (warp == 17) {
     tmem_alloc(tslot, 512);
     tmem_relinquish();
   }
@@ -158,7 +180,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   const uint32_t tbase = *tslot;
   const int items = pairs * a.Hkv;
 
-  if (warp == 8) {
+  if (warp == 16) {
     // ---------------- TMA producer ----------------
     if (lane == 0) {
       tma_prefetch_map(&tm_q);
@@ -206,7 +228,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         for (uint32_t i = nv > VS ? nv - VS : 0; i < nv; ++i) landed(&v_full[i % VS], (i / VS) & 1);
       }
     }
-  } else if (warp == 9) {
+  } else if (warp == 17) {
     // ---------------- MMA issuer ----------------
     if (lane == 0) {
       constexpr uint32_t PV_IDESC = idesc_bf16(kRows, DV, false, true);
@@ -267,12 +289,15 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       while (!mbar_try_wait(drain, 0) && globaltimer_ns() - w0 < kWaitLimitNs) {}
     }
   } else {
-    // ---------------- softmax: warps 0-3 the first tile, 4-7 the second ----------------
-    const int x = warp >> 2;
+    // ---------------- softmax: warps 0-7 the first tile, 8-15 the second ----------------
+    const int x = warp >> 3, half = (warp >> 2) & 1;
+    const int bar_id = 1 + x * 4 + (warp & 3);            // the two warps of these rows
     const int r = (warp & 3) * 32 + lane;                 // row of the tile = TMEM lane
     const int rq = r / a.G, rh = r - rq * a.G;            // its query and head
     const uint32_t s_addr = tbase + C::S0 + 128 * x + tmem_lane_base(warp);
     const uint32_t o_addr = tbase + C::O0 + x * DV + tmem_lane_base(warp);
+    volatile float* mine = reinterpret_cast<volatile float*>(smem + C::x_off) + (x * 2 + half) * kRows + r;
+    volatile float* other = reinterpret_cast<volatile float*>(smem + C::x_off) + (x * 2 + (half ^ 1)) * kRows + r;
     uint32_t nsf = 0, nof = 0;
     bool alive = true;
     for (int item = blockIdx.x; item < items && alive; item += gridDim.x) {
@@ -289,57 +314,54 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       float mx = -INFINITY, l = 0.f;
       bool started = false;
       const int jl = item_last(m, x);
-      for (int j = 0; j <= jl; ++j) {
+      for (int j = 0; j <= jl && alive; ++j) {
         if (!item_active(a, m, x, j)) continue;
         const int kb = item_key(m, j), cols = item_cols(m, j);
         const bool sink_blk = m.ns > 0 && j == 0;
-        if (!__all_sync(0xffffffffu, mbar_wait(&s_full[x], nsf & 1, abort_flag, a.err))) { alive = false; break; }
+        const int pieces = min(max((cols >> 5) - 2 * half, 0), 2);   // 32-key pieces of this half
+        alive = __all_sync(0xffffffffu, mbar_wait(&s_full[x], nsf & 1, abort_flag, a.err));
         ++nsf;
         tc_fence_after();
-        float v[4][32];
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (32 * c < cols) tmem_ld32(s_addr + 32 * c, v[c]);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld_wait_regs(v[c]);
-        if (sink_blk || kb < lo_last || kb + cols - 1 > t_first) {
-          // border: key kb + i is seen for i in [w0, w1] (the window) or [e0, e1) (first tokens)
-          int w0 = lo - kb, w1 = t - kb, e0 = ds - kb, e1 = early - kb;
-          if (sink_blk) { w0 = 1; w1 = 0; e0 = 0; e1 = ds == m.ds0 ? m.ns : 0; }
-          if (!live) { w0 = 1; w1 = 0; e1 = e0 = 0; }
-          const unsigned wn = (unsigned)max(w1 - w0 + 1, 0), en = (unsigned)max(e1 - e0, 0);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            if (32 * c < cols) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                const int k = 32 * c + i;
-                const bool seen = (unsigned)(k - w0) < wn || (unsigned)(k - e0) < en;
-                v[c][i] = seen ? v[c][i] : -INFINITY;
-              }
-            }
-          }
+        // border: key k0 + i is seen for i in [w0, w1) (the window) or [e0, e1) (first tokens)
+        const bool border = sink_blk || kb < lo_last || kb + cols - 1 > t_first;
+        uint64_t seen = ~0ull;
+        if (border) {
+          const int k0 = kb + 64 * half;
+          seen = bit_range(lo - k0, t + 1 - k0) | bit_range(ds - k0, early - k0);
+          if (sink_blk) seen = ds == m.ds0 ? bit_range(0, m.ns - 64 * half) : 0ull;
+          if (!live) seen = 0ull;
         }
+        // two passes over the scores in TMEM, the maximum and then the weights: 32 values at a
+        // time stay in registers (64 at once spilled at 96 registers a thread)
         float top = -INFINITY;
+        for (int c = 0; c < pieces; ++c) {
+          float v[32];
+          tmem_ld32(s_addr + 64 * half + 32 * c, v);
+          tmem_ld_wait_regs(v);
+          if (border) mask32(v, (uint32_t)(seen >> (32 * c)));
+          float u0 = v[0], u1 = v[1], u2 = v[2], u3 = v[3];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          if (32 * c < cols) {
-            float t0 = v[c][0], t1 = v[c][1];
-#pragma unroll
-            for (int i = 2; i < 32; i += 2) { t0 = fmaxf(t0, v[c][i]); t1 = fmaxf(t1, v[c][i + 1]); }
-            top = fmaxf(top, fmaxf(t0, t1));
+          for (int i = 4; i < 32; i += 4) {
+            u0 = fmaxf(u0, v[i]);
+            u1 = fmaxf(u1, v[i + 1]);
+            u2 = fmaxf(u2, v[i + 2]);
+            u3 = fmaxf(u3, v[i + 3]);
           }
+          top = fmaxf(top, fmaxf(fmaxf(u0, u1), fmaxf(u2, u3)));
         }
         top *= a.scale_log2;
-        if (__any_sync(0xffffffffu, top > mx + kRaise)) {
-          const float nm = fmaxf(mx, top);
+        // the two halves raise the maximum together, and leave together after a wait that gave up
+        if (named_bar_or(bar_id, 64, top > mx + kRaise || !alive)) {
+          *mine = top;
+          alive = named_bar_and(bar_id, 64, alive);
+          const float nm = fmaxf(mx, fmaxf(top, *other));
           const float c = nm == -INFINITY ? 1.f : ex2_approx(mx - nm);
           mx = nm;
           l *= c;
-          if (started) {
+          if (started && alive) {
             // the scores' barrier also covers the products before them: O is complete so far
 #pragma unroll 1
-            for (int d = 0; d < DV; d += 32) {
+            for (int d = half * (DV / 2); d < (half + 1) * (DV / 2); d += 32) {
               float o[32];
               tmem_ld32(o_addr + d, o);
               tmem_ld_wait_regs(o);
@@ -351,40 +373,48 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         }
         started = true;
         const float off = mx == -INFINITY ? 0.f : -mx;
-        float l0 = 0.f, l1 = 0.f;
+        float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
+        for (int c = 0; c < pieces; ++c) {
+          float v[32], w[16];
+          tmem_ld32(s_addr + 64 * half + 32 * c, v);
+          tmem_ld_wait_regs(v);
+          if (border) mask32(v, (uint32_t)(seen >> (32 * c)));
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          if (32 * c < cols) {
-            float w[16];
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              const float p0 = ex2_approx(fmaf(v[c][i], a.scale_log2, off));
-              const float p1 = ex2_approx(fmaf(v[c][i + 1], a.scale_log2, off));
-              l0 += p0;
-              l1 += p1;
-              const __nv_bfloat162 b = __floats2bfloat162_rn(p0, p1);
-              w[i >> 1] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&b));
-            }
-            tmem_st16(s_addr + 16 * c, w);
+          for (int i = 0; i < 32; i += 4) {
+            const float p0 = ex2_approx(fmaf(v[i], a.scale_log2, off));
+            const float p1 = ex2_approx(fmaf(v[i + 1], a.scale_log2, off));
+            const float p2 = ex2_approx(fmaf(v[i + 2], a.scale_log2, off));
+            const float p3 = ex2_approx(fmaf(v[i + 3], a.scale_log2, off));
+            l0 += p0;
+            l1 += p1;
+            l2 += p2;
+            l3 += p3;
+            const __nv_bfloat162 b0 = __floats2bfloat162_rn(p0, p1), b1 = __floats2bfloat162_rn(p2, p3);
+            w[i >> 1] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&b0));
+            w[(i >> 1) + 1] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&b1));
           }
+          tmem_st16(s_addr + 64 * half + 16 * c, w);   // over scores that have been read
         }
-        l += l0 + l1;
+        l += (l0 + l1) + (l2 + l3);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[x]);
       }
-      if (!alive) break;
-      // ---- the tile's rows ----
-      if (!__all_sync(0xffffffffu, mbar_wait(&o_full[x], nof & 1, abort_flag, a.err))) break;
+      // ---- the tile's rows, half the dims a thread ----
+      if (alive) alive = __all_sync(0xffffffffu, mbar_wait(&o_full[x], nof & 1, abort_flag, a.err));
       ++nof;
       tc_fence_after();
+      *mine = l;
+      alive = named_bar_and(bar_id, 64, alive);
+      if (!alive) break;
+      l += *other;
       const float inv = 1.f / l;
       const int h = g * a.G + rh;
       const int64_t row = (int64_t)t * a.Hq + h;
       float odd = fmaf(mx, 0.f, l * 0.f);                 // NaN where anything is not finite
 #pragma unroll 1
-      for (int d = 0; d < DV; d += 32) {
+      for (int d = half * (DV / 2); d < (half + 1) * (DV / 2); d += 32) {
         float o[32];
         tmem_ld32(o_addr + d, o);
         tmem_ld_wait_regs(o);
@@ -405,19 +435,23 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&o_empty[x]);
-      if (live && a.lse != nullptr) a.lse[row] = fmaf(mx, 0.6931471805599453f, logf(l));
-      __syncwarp();   // the stores above come before those of the rows done again
-      unsigned again = __ballot_sync(0xffffffffu, live && odd != 0.f);   // NaN compares unequal
-      while (again) {
-        const int src = __ffs((int)again) - 1;
-        again &= again - 1;
-        fwd_row<DQK / 64, DV / 64>(a, __shfl_sync(0xffffffffu, t, src), __shfl_sync(0xffffffffu, h, src), lane);
+      if (half == 0 && live && a.lse != nullptr) a.lse[row] = fmaf(mx, 0.6931471805599453f, logf(l));
+      // rows to do again: by the first half's warp, after both halves have stored
+      if (named_bar_or(bar_id, 64, live && odd != 0.f)) {   // NaN compares unequal
+        *mine = odd;
+        named_bar_sync(bar_id, 64);
+        unsigned again = __ballot_sync(0xffffffffu, live && half == 0 && (odd != 0.f || *other != 0.f));
+        while (again) {
+          const int src = __ffs((int)again) - 1;
+          again &= again - 1;
+          fwd_row<DQK / 64, DV / 64>(a, __shfl_sync(0xffffffffu, t, src), __shfl_sync(0xffffffffu, h, src), lane);
+        }
       }
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == 17) {
     tc_fence_after();
     tmem_dealloc(tbase, 512);
   }
