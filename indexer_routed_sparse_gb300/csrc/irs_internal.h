@@ -255,10 +255,11 @@ struct WinArgs {
 };
 size_t window_bwd_workspace_bytes(int T, int Hq, int Hkv, int Dqk, int Dv, int ndocs, int window, int sinks);
 // TMA maps [T][heads][D] of the packed tensors: queries in boxes of 64 dims x G heads x 128/G
-// tokens, keys and values in boxes of 64 dims x one head x 128 tokens.
+// tokens, keys and values in boxes of 64 dims x one head x a block of tokens.
 struct WinMaps {
   CUtensorMap q, k, v;
 };
+int window_fwd_block(int Dqk, int Dv);   // keys a block of the forward: the box of its k and v maps
 constexpr int kWindowKinds = 6;   // kernels, by head dims
 // configured[kWindowKinds]: whose shared-memory limit has been raised on this device
 cudaError_t launch_window_fwd_tc(const WinMaps& m, const WinArgs& a, int num_sms, bool* configured, cudaStream_t stream);

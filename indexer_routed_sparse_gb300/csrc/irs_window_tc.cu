@@ -11,7 +11,7 @@
 //   tile spans few queries and the keys it needs beyond one window are few: window 512 and
 //   G = 16 give tiles of 8 queries over 519 keys.
 // * An item is two such tiles of neighbouring queries over the same key blocks (128 keys, by
-//   TMA): while one tile's scores go through the softmax, the tensor cores work for the
+//   TMA, 96 where shared memory asks for it): while one tile's scores go through the softmax, the tensor cores work for the
 //   other. A persistent CTA an SM walks the items; the next item's queries and keys load
 //   while the last one drains.
 // * Two threads share a row, 64 keys of a block each (16 softmax warps). With one thread a
@@ -35,7 +35,6 @@ namespace irs {
 
 namespace {
 
-constexpr int kBlk = 128;            // keys a block
 constexpr int kRows = 128;           // rows a tile
 constexpr uint32_t kAtom = 128 * 128;   // 128 rows x 64 bf16
 constexpr int kFwdThreads = 576;     // warps 0-7, 8-15: softmax of the two tiles; 16: TMA; 17: MMA
@@ -45,26 +44,28 @@ template <int DQK, int DV>
 struct FwdCfg {
   static constexpr int QA = DQK / 64, VA = DV / 64;
   static constexpr uint32_t q_bytes = QA * kAtom;          // one tile's queries
-  static constexpr uint32_t k_bytes = QA * kAtom, v_bytes = VA * kAtom;
-  static constexpr uint32_t budget = 226u * 1024u;
-  static constexpr int KS = 2;
-  static constexpr int VS = 2 * q_bytes + 2 * k_bytes + 2 * v_bytes <= budget ? 2 : 1;
+  // Keys a block: 128 where two stages of keys and of values fit beside the queries, else 96
+  // (192/128). One stage of 128 values exposed its load every block: 2.45 ms for 65536 tokens.
+  static constexpr int BLK = 2 * q_bytes + 2 * (QA + VA) * kAtom <= 224u * 1024u ? 128 : 96;
+  static constexpr uint32_t kv_atom = BLK * 128;           // BLK rows x 64 bf16
+  static constexpr uint32_t k_bytes = QA * kv_atom, v_bytes = VA * kv_atom;
+  static constexpr int KS = 2, VS = 2;
   static constexpr uint32_t k_off = 2 * q_bytes, v_off = k_off + KS * k_bytes, x_off = v_off + VS * v_bytes;
   static constexpr uint32_t bar_off = x_off + 2 * 2 * kRows * 4;   // a word a row, half and tile
-  static constexpr uint32_t total = bar_off + 32 * 8 + 16;   // 226.3 KB at 192/128: none to spare for aligning
+  static constexpr uint32_t total = bar_off + 24 * 8 + 16 + 2 * 16;   // 226.3 KB at 192/128: none to spare for aligning
   static constexpr uint32_t S0 = 0, O0 = 256;              // TMEM: S of tile x at 128 x, O at 256 + x DV
 };
 
-// The keys of one item: two tiles of `qt` queries from t0 on.
+// The keys of one item: two tiles of `qt` queries from t0 on. Block 0 holds the first tokens
+// before the range where there are any; the first tile takes blocks [0, l0], the second [f1,
+// nbt).
 struct Item {
-  int t0, last;          // first query; last query of the item
-  int lastA;             // last query of the first tile
-  int ds0, dsB;          // document starts of the tiles' first queries
-  int loB;               // first key of the second tile's first query
-  int klo, nb, ns;       // first key of the range, its blocks; first tokens before it
-  int nbt;               // blocks with the first-token block (which is block 0 when ns > 0)
+  int t0, last, lastA;   // first query; last query of the item and of its first tile
+  int ds0, klo, ns;      // document start of the first query; first key of the range; first tokens before it
+  int nbt, l0, f1;
   bool hasB;
 };
+template <int kBlk>
 __device__ __forceinline__ Item window_item(const WinArgs& a, int t0, int qt) {
   Item m;
   m.t0 = t0;
@@ -72,32 +73,28 @@ __device__ __forceinline__ Item window_item(const WinArgs& a, int t0, int qt) {
   m.lastA = min(t0 + qt, a.T) - 1;
   m.hasB = t0 + qt < a.T;
   m.ds0 = window_doc(a.cu, a.ndocs, a.T, t0).start;
-  const int tb = m.hasB ? t0 + qt : t0;
-  m.dsB = window_doc(a.cu, a.ndocs, a.T, tb).start;
-  m.loB = max(m.dsB, tb - a.window + 1);
   m.klo = max(m.ds0, t0 - a.window + 1);
-  m.nb = (m.last - m.klo) / kBlk + 1;
   m.ns = max(0, min(m.ds0 + a.sinks, m.klo) - m.ds0);
-  m.nbt = m.nb + (m.ns > 0 ? 1 : 0);
+  const int s = m.ns > 0 ? 1 : 0;
+  m.nbt = (m.last - m.klo) / kBlk + 1 + s;
+  m.l0 = (m.lastA - m.klo) / kBlk + s;
+  m.f1 = 0;
+  if (m.hasB) {
+    const int tb = t0 + qt, dsB = window_doc(a.cu, a.ndocs, a.T, tb).start;
+    // blocks before the second tile's window are left out; with first tokens, only theirs
+    if (a.sinks == 0) m.f1 = (max(dsB, tb - a.window + 1) - m.klo) / kBlk;
+    else m.f1 = s != 0 && dsB != m.ds0 ? 1 : 0;
+  }
   return m;
 }
+template <int kBlk>
 __device__ __forceinline__ int item_key(const Item& m, int j) {   // first key of block j
   return m.ns > 0 ? (j == 0 ? m.ds0 : m.klo + kBlk * (j - 1)) : m.klo + kBlk * j;
 }
+template <int kBlk>
 __device__ __forceinline__ int item_cols(const Item& m, int j) {  // its keys, up to a multiple of 32
-  const int n = (m.ns > 0 && j == 0) ? m.ns : min(kBlk, m.last - item_key(m, j) + 1);
+  const int n = (m.ns > 0 && j == 0) ? m.ns : min(kBlk, m.last - item_key<kBlk>(m, j) + 1);
   return (n + 31) & ~31;
-}
-__device__ __forceinline__ bool item_active(const WinArgs& a, const Item& m, int x, int j) {
-  if (m.ns > 0 && j == 0) return x == 0 || (m.hasB && m.dsB == m.ds0);
-  const int kb = item_key(m, j);
-  if (x == 0) return kb <= m.lastA;
-  if (!m.hasB) return false;
-  // before the tile's window, and without first tokens of its document
-  return !(kb + kBlk <= m.loB && (kb >= m.dsB + a.sinks || kb + kBlk <= m.dsB));
-}
-__device__ __forceinline__ int item_last(const Item& m, int x) {   // the last active block
-  return x == 0 ? (m.lastA - m.klo) / kBlk + (m.ns > 0 ? 1 : 0) : m.nbt - 1;
 }
 
 // Bits [from, to) of a 64-bit word, both clamped to [0, 64].
@@ -108,26 +105,28 @@ __device__ __forceinline__ uint64_t bit_range(int from, int to) {
   return (~0ull >> (64 - (to - from))) << from;
 }
 
-__device__ __forceinline__ void mask32(float (&v)[32], uint32_t bits) {
+__device__ __forceinline__ void mask16(float (&v)[16], uint32_t bits) {
 #pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = (bits >> i) & 1u ? v[i] : -INFINITY;
+  for (int i = 0; i < 16; ++i) v[i] = (bits >> i) & 1u ? v[i] : -INFINITY;
 }
 
-// D[128 x DV] (+)= P . V: P bf16 in TMEM (32 columns for 64 keys at the first of their 64 score
-// columns), V a [key][dim] tile read MN-major; NK steps of 16 keys.
+// D[128 x DV] (+)= P . V: P bf16 in TMEM, V a [key][dim] tile read MN-major; NK steps of 16
+// keys. Each half of the keys has its weights at the first of its own score columns.
 template <int NK>
-__device__ __forceinline__ void pv_run(uint32_t d, uint32_t p, uint32_t vb, uint32_t idesc, bool accumulate) {
-  const uint64_t b0 = sdesc_sw128(vb, kAtom, 1024);
+__device__ __forceinline__ void pv_run(uint32_t d, uint32_t p, uint32_t vb, uint32_t atom, uint32_t idesc, bool accumulate) {
+  const uint64_t b0 = sdesc_sw128(vb, atom, 1024);
 #pragma unroll
   for (int ks = 0; ks < NK; ++ks)
-    umma_bf16_ts(d, p + 8 * ks + (ks >= 4 ? 32 : 0), b0 + (uint64_t)((ks * 2048) >> 4), idesc, (accumulate || ks > 0) ? 1u : 0u);
+    umma_bf16_ts_warp(d, p + (ks < NK / 2 ? 8 * ks : 8 * NK + 8 * (ks - NK / 2)), b0 + (uint64_t)((ks * 2048) >> 4), idesc,
+                 (accumulate || ks > 0) ? 1u : 0u);
 }
-__device__ __forceinline__ void pv_any(int cols, uint32_t d, uint32_t p, uint32_t vb, uint32_t idesc, bool accumulate) {
+__device__ __forceinline__ void pv_any(int cols, uint32_t d, uint32_t p, uint32_t vb, uint32_t atom, uint32_t idesc,
+                                       bool accumulate) {
   switch (cols >> 5) {
-    case 1: pv_run<2>(d, p, vb, idesc, accumulate); break;
-    case 2: pv_run<4>(d, p, vb, idesc, accumulate); break;
-    case 3: pv_run<6>(d, p, vb, idesc, accumulate); break;
-    default: pv_run<8>(d, p, vb, idesc, accumulate); break;
+    case 1: pv_run<2>(d, p, vb, atom, idesc, accumulate); break;
+    case 2: pv_run<4>(d, p, vb, atom, idesc, accumulate); break;
+    case 3: pv_run<6>(d, p, vb, atom, idesc, accumulate); break;
+    default: pv_run<8>(d, p, vb, atom, idesc, accumulate); break;
   }
 }
 
@@ -155,6 +154,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   uint64_t* drain = o_empty + 2;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
+  volatile int* plan = reinterpret_cast<volatile int*>(tslot + 4);     // [2][4]: an item's blocks, for the MMA warp
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
@@ -199,21 +199,27 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       };
       for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
         const int pair = item / a.Hkv, g = item - pair * a.Hkv;
-        const Item m = window_item(a, pair * 2 * qt, qt);
+        const Item m = window_item<C::BLK>(a, pair * 2 * qt, qt);
+        // two slots: this one was read before the first tile's last scores of two items ago
+        volatile int* pl = plan + 4 * (nq[0] & 1);
+        pl[0] = m.nbt;
+        pl[1] = m.l0;
+        pl[2] = m.hasB ? m.f1 : m.nbt;
+        pl[3] = (m.ns > 0 ? item_cols<C::BLK>(m, 0) : 0) | item_cols<C::BLK>(m, m.nbt - 1) << 16;
         if (!(ok = load_q(0, m, g))) break;
         for (int j = 0; j < m.nbt && ok; ++j) {
-          const int kb = item_key(m, j);
+          const int kb = item_key<C::BLK>(m, j);
           const uint32_t ks = nk % KS, vs = nv % VS;
           if (nk >= KS && !mbar_wait(&k_empty[ks], (nk / KS - 1) & 1, abort_flag, a.err)) { ok = false; break; }
           mbar_arrive_expect_tx(&k_full[ks], C::k_bytes);
           for (int c = 0; c < C::QA; ++c)
-            tma_load_3d(smem + C::k_off + ks * C::k_bytes + c * kAtom, &tm_k, c * 64, g, kb, &k_full[ks]);
+            tma_load_3d(smem + C::k_off + ks * C::k_bytes + c * C::kv_atom, &tm_k, c * 64, g, kb, &k_full[ks]);
           ++nk;
           if (j == 0 && m.hasB && !(ok = load_q(1, m, g))) break;
           if (nv >= VS && !mbar_wait(&v_empty[vs], (nv / VS - 1) & 1, abort_flag, a.err)) { ok = false; break; }
           mbar_arrive_expect_tx(&v_full[vs], C::v_bytes);
           for (int c = 0; c < C::VA; ++c)
-            tma_load_3d(smem + C::v_off + vs * C::v_bytes + c * kAtom, &tm_v, c * 64, g, kb, &v_full[vs]);
+            tma_load_3d(smem + C::v_off + vs * C::v_bytes + c * C::kv_atom, &tm_v, c * 64, g, kb, &v_full[vs]);
           ++nv;
         }
       }
@@ -229,65 +235,66 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       }
     }
   } else if (warp == 17) {
-    // ---------------- MMA issuer ----------------
-    if (lane == 0) {
-      constexpr uint32_t PV_IDESC = idesc_bf16(kRows, DV, false, true);
-      uint32_t nk = 0, nv = 0, np[2] = {0, 0}, nq[2] = {0, 0}, no[2] = {0, 0};
-      bool alive = true;
-      for (int item = blockIdx.x; item < items && alive; item += gridDim.x) {
-        const Item m = window_item(a, item / a.Hkv * 2 * qt, qt);
-        bool pend[2] = {false, false}, first[2] = {true, true}, begun[2] = {false, false};
-        int pcols = 0;
-        for (int j = 0; j <= m.nbt && alive; ++j) {
-          const bool more = j < m.nbt;
-          const int cols = more ? item_cols(m, j) : 0;
-          const uint32_t kst = nk % KS, vst = nv % VS;
-          if (more && !mbar_wait(&k_full[kst], (nk / KS) & 1, abort_flag, a.err)) { alive = false; break; }
-          if (j > 0 && !mbar_wait(&v_full[vst], (nv / VS) & 1, abort_flag, a.err)) { alive = false; break; }
+    // ---------------- MMA issuer (the whole warp; one elected lane issues) ----------------
+    constexpr uint32_t PV_IDESC = idesc_bf16(kRows, DV, false, true);
+    const uint32_t tb = (uint32_t)uniform((int)tbase);
+    const uint32_t sb = smem_u32(smem);
+    auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, a.err)); };
+    uint32_t nk = 0, nv = 0, np[2] = {0, 0}, nq[2] = {0, 0}, no[2] = {0, 0};
+    bool alive = true;
+    for (int item = blockIdx.x; item < items && alive; item += gridDim.x) {
+      if (!wait(&q_full[0], nq[0] & 1)) break;
+      const volatile int* pl = plan + 4 * (nq[0] & 1);
+      const int nbt = uniform(pl[0]), l0 = uniform(pl[1]), f1 = uniform(pl[2]), pc = uniform(pl[3]);
+      const int cols0 = pc & 0xffff, colsL = pc >> 16;   // columns of a first-token block (0: none), of the last
+      ++nq[0];
+      int pcols = 0;
+      for (int j = 0; j <= nbt && alive; ++j) {
+        const bool more = j < nbt;
+        const int cols = j == 0 && cols0 != 0 ? cols0 : j == nbt - 1 ? colsL : C::BLK;
+        const uint32_t kst = nk & 1, vst = nv & 1;
+        if (more && !wait(&k_full[kst], (nk >> 1) & 1)) { alive = false; break; }
+        if (j > 0 && !wait(&v_full[vst], (nv >> 1) & 1)) { alive = false; break; }
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const bool act = more && item_active(a, m, x, j);
-            if (pend[x]) {
-              if (!mbar_wait(&p_full[x], np[x] & 1, abort_flag, a.err)) { alive = false; break; }
-              ++np[x];
-              if (first[x] && no[x] > 0 && !mbar_wait(&o_empty[x], (no[x] - 1) & 1, abort_flag, a.err)) { alive = false; break; }
-              tc_fence_after();
-              pv_any(pcols, tbase + C::O0 + x * DV, tbase + C::S0 + 128 * x, smem_u32(smem) + C::v_off + vst * C::v_bytes,
-                     PV_IDESC, !first[x]);
-              first[x] = false;
-              if (j - 1 == item_last(m, x)) { umma_commit(&o_full[x]); ++no[x]; }
-            }
-            if (act) {
-              if (!begun[x]) {
-                if (!mbar_wait(&q_full[x], nq[x] & 1, abort_flag, a.err)) { alive = false; break; }
-                ++nq[x];
-                begun[x] = true;
-              }
-              tc_fence_after();
-              const uint32_t idesc = idesc_bf16(kRows, cols, false, false);
-              const uint64_t a0 = sdesc_sw128(smem_u32(smem) + x * C::q_bytes, 16, 1024);
-              const uint64_t b0 = sdesc_sw128(smem_u32(smem) + C::k_off + kst * C::k_bytes, 16, 1024);
-#pragma unroll
-              for (int ks = 0; ks < 4 * C::QA; ++ks) {
-                const uint64_t off = (uint64_t)(((ks >> 2) * kAtom + (ks & 3) * 32) >> 4);
-                umma_bf16(tbase + C::S0 + 128 * x, a0 + off, b0 + off, idesc, ks > 0);
-              }
-              umma_commit(&s_full[x]);
-              if (j == item_last(m, x)) umma_commit(&q_empty[x]);
-            }
-            pend[x] = act;
+        for (int x = 0; x < 2; ++x) {
+          const int fx = x == 0 ? 0 : f1, lx = x == 0 ? l0 : nbt - 1;
+          if (j - 1 >= fx && j - 1 <= lx) {   // the block before: its weights times its values
+            if (!wait(&p_full[x], np[x] & 1)) { alive = false; break; }
+            ++np[x];
+            if (j - 1 == fx && no[x] > 0 && !wait(&o_empty[x], (no[x] - 1) & 1)) { alive = false; break; }
+            tc_fence_after();
+            pv_any(pcols, tb + C::O0 + x * DV, tb + C::S0 + 128 * x, sb + C::v_off + vst * C::v_bytes, C::kv_atom, PV_IDESC,
+                   j - 1 > fx);
+            if (j - 1 == lx) { umma_commit_warp(&o_full[x]); ++no[x]; }
           }
-          if (!alive) break;
-          if (more) { umma_commit(&k_empty[kst]); ++nk; }
-          if (j > 0) { umma_commit(&v_empty[vst]); ++nv; }
-          pcols = cols;
+          if (more && j >= fx && j <= lx) {
+            if (x == 1 && j == fx) {
+              if (!wait(&q_full[1], nq[1] & 1)) { alive = false; break; }
+              ++nq[1];
+            }
+            tc_fence_after();
+            const uint32_t idesc = idesc_bf16(kRows, cols, false, false);
+            const uint64_t a0 = sdesc_sw128(sb + x * C::q_bytes, 16, 1024);
+            const uint64_t b0 = sdesc_sw128(sb + C::k_off + kst * C::k_bytes, 16, 1024);
+#pragma unroll
+            for (int ks = 0; ks < 4 * C::QA; ++ks)
+              umma_bf16_warp(tb + C::S0 + 128 * x, a0 + (uint64_t)(((ks >> 2) * kAtom + (ks & 3) * 32) >> 4),
+                             b0 + (uint64_t)(((ks >> 2) * C::kv_atom + (ks & 3) * 32) >> 4), idesc, ks > 0);
+            umma_commit_warp(&s_full[x]);
+            if (j == lx) umma_commit_warp(&q_empty[x]);
+          }
         }
+        if (!alive) break;
+        if (j > 0) { umma_commit_warp(&v_empty[vst]); ++nv; }
+        if (more) { umma_commit_warp(&k_empty[kst]); ++nk; }
+        pcols = cols;
       }
-      // every issued product completes before the CTA releases its tensor memory
-      umma_commit(drain);
-      const unsigned long long w0 = globaltimer_ns();
-      while (!mbar_try_wait(drain, 0) && globaltimer_ns() - w0 < kWaitLimitNs) {}
     }
+    // every issued product completes before the CTA releases its tensor memory
+    umma_commit_warp(drain);
+    const unsigned long long w0 = globaltimer_ns();
+    while (!mbar_try_wait(drain, 0) && globaltimer_ns() - w0 < kWaitLimitNs) {}
+    __syncwarp();
   } else {
     // ---------------- softmax: warps 0-7 the first tile, 8-15 the second ----------------
     const int x = warp >> 3, half = (warp >> 2) & 1;
@@ -302,7 +309,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     bool alive = true;
     for (int item = blockIdx.x; item < items && alive; item += gridDim.x) {
       const int pair = item / a.Hkv, g = item - pair * a.Hkv;
-      const Item m = window_item(a, pair * 2 * qt, qt);
+      const Item m = window_item<C::BLK>(a, pair * 2 * qt, qt);
       if (x == 1 && !m.hasB) continue;
       const int t = m.t0 + x * qt + rq;
       const bool live = rq < qt && t < a.T;
@@ -313,12 +320,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       const int lo_last = max(window_doc(a.cu, a.ndocs, a.T, t_last).start, t_last - a.window + 1);
       float mx = -INFINITY, l = 0.f;
       bool started = false;
-      const int jl = item_last(m, x);
-      for (int j = 0; j <= jl && alive; ++j) {
-        if (!item_active(a, m, x, j)) continue;
-        const int kb = item_key(m, j), cols = item_cols(m, j);
+      const int jf = x == 0 ? 0 : m.f1, jl = x == 0 ? m.l0 : m.nbt - 1;
+      for (int j = jf; j <= jl && alive; ++j) {
+        const int kb = item_key<C::BLK>(m, j), cols = item_cols<C::BLK>(m, j);
         const bool sink_blk = m.ns > 0 && j == 0;
-        const int pieces = min(max((cols >> 5) - 2 * half, 0), 2);   // 32-key pieces of this half
+        const int pieces = cols >> 5, c0 = half * (cols >> 1);   // 16-key pieces of this half, its first column
         alive = __all_sync(0xffffffffu, mbar_wait(&s_full[x], nsf & 1, abort_flag, a.err));
         ++nsf;
         tc_fence_after();
@@ -326,28 +332,35 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         const bool border = sink_blk || kb < lo_last || kb + cols - 1 > t_first;
         uint64_t seen = ~0ull;
         if (border) {
-          const int k0 = kb + 64 * half;
+          const int k0 = kb + c0;
           seen = bit_range(lo - k0, t + 1 - k0) | bit_range(ds - k0, early - k0);
-          if (sink_blk) seen = ds == m.ds0 ? bit_range(0, m.ns - 64 * half) : 0ull;
+          if (sink_blk) seen = ds == m.ds0 ? bit_range(0, m.ns - c0) : 0ull;
           if (!live) seen = 0ull;
         }
         // two passes over the scores in TMEM, the maximum and then the weights: 32 values at a
         // time stay in registers (64 at once spilled at 96 registers a thread)
         float top = -INFINITY;
-        for (int c = 0; c < pieces; ++c) {
-          float v[32];
-          tmem_ld32(s_addr + 64 * half + 32 * c, v);
-          tmem_ld_wait_regs(v);
-          if (border) mask32(v, (uint32_t)(seen >> (32 * c)));
-          float u0 = v[0], u1 = v[1], u2 = v[2], u3 = v[3];
+        for (int c = 0; c < pieces; c += 2) {
+          float v[2][16];
+          tmem_ld16(s_addr + c0 + 16 * c, v[0]);
+          if (c + 1 < pieces) tmem_ld16(s_addr + c0 + 16 * c + 16, v[1]);
+          tmem_ld_wait_regs(v[0]);
+          tmem_ld_wait_regs(v[1]);
 #pragma unroll
-          for (int i = 4; i < 32; i += 4) {
-            u0 = fmaxf(u0, v[i]);
-            u1 = fmaxf(u1, v[i + 1]);
-            u2 = fmaxf(u2, v[i + 2]);
-            u3 = fmaxf(u3, v[i + 3]);
+          for (int u = 0; u < 2; ++u) {
+            if (c + u < pieces) {
+              if (border) mask16(v[u], (uint32_t)(seen >> (16 * (c + u))));
+              float u0 = v[u][0], u1 = v[u][1], u2 = v[u][2], u3 = v[u][3];
+#pragma unroll
+              for (int i = 4; i < 16; i += 4) {
+                u0 = fmaxf(u0, v[u][i]);
+                u1 = fmaxf(u1, v[u][i + 1]);
+                u2 = fmaxf(u2, v[u][i + 2]);
+                u3 = fmaxf(u3, v[u][i + 3]);
+              }
+              top = fmaxf(top, fmaxf(fmaxf(u0, u1), fmaxf(u2, u3)));
+            }
           }
-          top = fmaxf(top, fmaxf(fmaxf(u0, u1), fmaxf(u2, u3)));
         }
         top *= a.scale_log2;
         // the two halves raise the maximum together, and leave together after a wait that gave up
@@ -374,26 +387,34 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         started = true;
         const float off = mx == -INFINITY ? 0.f : -mx;
         float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
-        for (int c = 0; c < pieces; ++c) {
-          float v[32], w[16];
-          tmem_ld32(s_addr + 64 * half + 32 * c, v);
-          tmem_ld_wait_regs(v);
-          if (border) mask32(v, (uint32_t)(seen >> (32 * c)));
+        for (int c = 0; c < pieces; c += 2) {
+          float v[2][16];
+          tmem_ld16(s_addr + c0 + 16 * c, v[0]);
+          if (c + 1 < pieces) tmem_ld16(s_addr + c0 + 16 * c + 16, v[1]);
+          tmem_ld_wait_regs(v[0]);
+          tmem_ld_wait_regs(v[1]);
 #pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            const float p0 = ex2_approx(fmaf(v[i], a.scale_log2, off));
-            const float p1 = ex2_approx(fmaf(v[i + 1], a.scale_log2, off));
-            const float p2 = ex2_approx(fmaf(v[i + 2], a.scale_log2, off));
-            const float p3 = ex2_approx(fmaf(v[i + 3], a.scale_log2, off));
-            l0 += p0;
-            l1 += p1;
-            l2 += p2;
-            l3 += p3;
-            const __nv_bfloat162 b0 = __floats2bfloat162_rn(p0, p1), b1 = __floats2bfloat162_rn(p2, p3);
-            w[i >> 1] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&b0));
-            w[(i >> 1) + 1] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&b1));
+          for (int u = 0; u < 2; ++u) {
+            if (c + u < pieces) {
+              if (border) mask16(v[u], (uint32_t)(seen >> (16 * (c + u))));
+              float w[8];
+#pragma unroll
+              for (int i = 0; i < 16; i += 4) {
+                const float p0 = ex2_approx(fmaf(v[u][i], a.scale_log2, off));
+                const float p1 = ex2_approx(fmaf(v[u][i + 1], a.scale_log2, off));
+                const float p2 = ex2_approx(fmaf(v[u][i + 2], a.scale_log2, off));
+                const float p3 = ex2_approx(fmaf(v[u][i + 3], a.scale_log2, off));
+                l0 += p0;
+                l1 += p1;
+                l2 += p2;
+                l3 += p3;
+                const __nv_bfloat162 b0 = __floats2bfloat162_rn(p0, p1), b1 = __floats2bfloat162_rn(p2, p3);
+                w[i >> 1] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&b0));
+                w[(i >> 1) + 1] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&b1));
+              }
+              tmem_st8(s_addr + c0 + 8 * (c + u), w);   // over scores that have been read
+            }
           }
-          tmem_st16(s_addr + 64 * half + 16 * c, w);   // over scores that have been read
         }
         l += (l0 + l1) + (l2 + l3);
         tmem_st_wait();
@@ -456,6 +477,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     tmem_dealloc(tbase, 512);
   }
 }
+
+}  // namespace
+
+int window_fwd_block(int Dqk, int Dv) { return Dqk == 192 && Dv == 128 ? FwdCfg<192, 128>::BLK : 128; }
+
+namespace {
+
+static_assert(FwdCfg<192, 64>::BLK == 128 && FwdCfg<128, 128>::BLK == 128, "window_fwd_block");
 
 template <int DQK, int DV>
 cudaError_t launch_fwd(const WinMaps& m, const WinArgs& a, int num_sms, bool* configured, cudaStream_t stream) {
