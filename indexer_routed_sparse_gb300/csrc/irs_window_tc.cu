@@ -20,8 +20,9 @@
 //   barrier of the two warps a block carries their vote whether to raise it.
 // * S[128 x 128] = Q K^T lies in TMEM; the weights return over it as bf16 and are the first
 //   operand of O += P V straight from TMEM (V read MN-major from its [key][dim] tile).
-// * The running maximum is raised only where a score passes it by 2^8 (weights stay below
-//   2^8, sums in FP32), so O in TMEM is rescaled almost never.
+// * The running maximum is raised only where a weight under it passes 2^8 (sums are FP32), so
+//   that after a tile's first block the scores are read once and O in TMEM is hardly ever
+//   rescaled.
 // * Documents are not aligned to tiles: a tile's keys are one range of the packed sequence,
 //   and each row masks by its own document's start. Only blocks at a border of the range are
 //   masked element by element. First tokens before the range are one more (narrow) block.
@@ -38,7 +39,7 @@ namespace {
 constexpr int kRows = 128;           // rows a tile
 constexpr uint32_t kAtom = 128 * 128;   // 128 rows x 64 bf16
 constexpr int kFwdThreads = 576;     // warps 0-7, 8-15: softmax of the two tiles; 16: TMA; 17: MMA
-constexpr float kRaise = 8.f;
+constexpr float kRaise = 256.f;      // a weight past this raises the maximum
 
 template <int DQK, int DV>
 struct FwdCfg {
@@ -52,7 +53,9 @@ struct FwdCfg {
   static constexpr int KS = 2, VS = 2;
   static constexpr uint32_t k_off = 2 * q_bytes, v_off = k_off + KS * k_bytes, x_off = v_off + VS * v_bytes;
   static constexpr uint32_t bar_off = x_off + 2 * 2 * kRows * 4;   // a word a row, half and tile
-  static constexpr uint32_t total = bar_off + 24 * 8 + 16 + 2 * 16;   // 226.3 KB at 192/128: none to spare for aligning
+  static constexpr uint32_t cu_off = bar_off + 24 * 8 + 16 + 2 * 16;
+  static constexpr int cu_cap = (int)((232448u - cu_off) / 4u) < 2048 ? (int)((232448u - cu_off) / 4u) : 2048;
+  static constexpr uint32_t total = cu_off + 4u * cu_cap;   // 226.3 KB at 192/128: none to spare for aligning
   static constexpr uint32_t S0 = 0, O0 = 256;              // TMEM: S of tile x at 128 x, O at 256 + x DV
 };
 
@@ -66,13 +69,13 @@ struct Item {
   bool hasB;
 };
 template <int kBlk>
-__device__ __forceinline__ Item window_item(const WinArgs& a, int t0, int qt) {
+__device__ __forceinline__ Item window_item(const WinArgs& a, const int32_t* cu, int t0, int qt) {
   Item m;
   m.t0 = t0;
   m.last = min(t0 + 2 * qt, a.T) - 1;
   m.lastA = min(t0 + qt, a.T) - 1;
   m.hasB = t0 + qt < a.T;
-  m.ds0 = window_doc(a.cu, a.ndocs, a.T, t0).start;
+  m.ds0 = window_doc(cu, a.ndocs, a.T, t0).start;
   m.klo = max(m.ds0, t0 - a.window + 1);
   m.ns = max(0, min(m.ds0 + a.sinks, m.klo) - m.ds0);
   const int s = m.ns > 0 ? 1 : 0;
@@ -80,7 +83,7 @@ __device__ __forceinline__ Item window_item(const WinArgs& a, int t0, int qt) {
   m.l0 = (m.lastA - m.klo) / kBlk + s;
   m.f1 = 0;
   if (m.hasB) {
-    const int tb = t0 + qt, dsB = window_doc(a.cu, a.ndocs, a.T, tb).start;
+    const int tb = t0 + qt, dsB = window_doc(cu, a.ndocs, a.T, tb).start;
     // blocks before the second tile's window are left out; with first tokens, only theirs
     if (a.sinks == 0) m.f1 = (max(dsB, tb - a.window + 1) - m.klo) / kBlk;
     else m.f1 = s != 0 && dsB != m.ds0 ? 1 : 0;
@@ -174,6 +177,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     tmem_relinquish();
   }
   check_documents(a);
+  // document borders are searched for every item by every row: in shared memory where they fit
+  // (from L2 the searches took 9,000 of an item's 40,000 cycles)
+  const int32_t* cu = a.cu;
+  if (a.ndocs < C::cu_cap) {
+    int32_t* near = reinterpret_cast<int32_t*>(smem + C::cu_off);
+    for (int i = tid; i <= a.ndocs; i += kFwdThreads) near[i] = a.cu[i];
+    cu = near;
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -199,7 +210,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       };
       for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
         const int pair = item / a.Hkv, g = item - pair * a.Hkv;
-        const Item m = window_item<C::BLK>(a, pair * 2 * qt, qt);
+        const Item m = window_item<C::BLK>(a, cu, pair * 2 * qt, qt);
         // two slots: this one was read before the first tile's last scores of two items ago
         volatile int* pl = plan + 4 * (nq[0] & 1);
         pl[0] = m.nbt;
@@ -309,17 +320,17 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     bool alive = true;
     for (int item = blockIdx.x; item < items && alive; item += gridDim.x) {
       const int pair = item / a.Hkv, g = item - pair * a.Hkv;
-      const Item m = window_item<C::BLK>(a, pair * 2 * qt, qt);
+      const Item m = window_item<C::BLK>(a, cu, pair * 2 * qt, qt);
       if (x == 1 && !m.hasB) continue;
       const int t = m.t0 + x * qt + rq;
       const bool live = rq < qt && t < a.T;
       const int t_first = m.t0 + x * qt, t_last = x == 0 ? m.lastA : m.last;
-      const int ds = window_doc(a.cu, a.ndocs, a.T, min(t, a.T - 1)).start;
+      const int ds = window_doc(cu, a.ndocs, a.T, min(t, a.T - 1)).start;
       const int lo = max(ds, t - a.window + 1);
       const int early = min(ds + a.sinks, lo);            // first tokens: [ds, early)
-      const int lo_last = max(window_doc(a.cu, a.ndocs, a.T, t_last).start, t_last - a.window + 1);
+      const int lo_last = max(window_doc(cu, a.ndocs, a.T, t_last).start, t_last - a.window + 1);
       float mx = -INFINITY, l = 0.f;
-      bool started = false;
+      bool settled = false;                               // every row of the warps has a maximum
       const int jf = x == 0 ? 0 : m.f1, jl = x == 0 ? m.l0 : m.nbt - 1;
       for (int j = jf; j <= jl && alive; ++j) {
         const int kb = item_key<C::BLK>(m, j), cols = item_cols<C::BLK>(m, j);
@@ -337,41 +348,62 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           if (sink_blk) seen = ds == m.ds0 ? bit_range(0, m.ns - c0) : 0ull;
           if (!live) seen = 0ull;
         }
-        // two passes over the scores in TMEM, the maximum and then the weights: 32 values at a
-        // time stay in registers (64 at once spilled at 96 registers a thread)
-        float top = -INFINITY;
-        for (int c = 0; c < pieces; c += 2) {
-          float v[2][16];
-          tmem_ld16(s_addr + c0 + 16 * c, v[0]);
-          if (c + 1 < pieces) tmem_ld16(s_addr + c0 + 16 * c + 16, v[1]);
-          tmem_ld_wait_regs(v[0]);
-          tmem_ld_wait_regs(v[1]);
+        // One pass: the weights under the present maximum, and whether one passes 2^8. They
+        // wait in registers for the two halves' vote; where it asks for it (and for the first
+        // blocks, before every row has a maximum) the scores are read again.
+        uint32_t w[C::BLK / 32][8];
+        float ln = 0.f;
+        auto weights = [&]() {
+          const float off = mx == -INFINITY ? 0.f : -mx;
+          float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f, big = 0.f;
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            if (c + u < pieces) {
-              if (border) mask16(v[u], (uint32_t)(seen >> (16 * (c + u))));
-              float u0 = v[u][0], u1 = v[u][1], u2 = v[u][2], u3 = v[u][3];
+          for (int c = 0; c < C::BLK / 32; ++c) {
+            if (c < pieces) {
+              float v[16];
+              tmem_ld16(s_addr + c0 + 16 * c, v);
+              tmem_ld_wait_regs(v);
+              if (border) mask16(v, (uint32_t)(seen >> (16 * c)));
 #pragma unroll
-              for (int i = 4; i < 16; i += 4) {
-                u0 = fmaxf(u0, v[u][i]);
-                u1 = fmaxf(u1, v[u][i + 1]);
-                u2 = fmaxf(u2, v[u][i + 2]);
-                u3 = fmaxf(u3, v[u][i + 3]);
+              for (int i = 0; i < 16; i += 4) {
+                const float p0 = ex2_approx(fmaf(v[i], a.scale_log2, off));
+                const float p1 = ex2_approx(fmaf(v[i + 1], a.scale_log2, off));
+                const float p2 = ex2_approx(fmaf(v[i + 2], a.scale_log2, off));
+                const float p3 = ex2_approx(fmaf(v[i + 3], a.scale_log2, off));
+                l0 += p0;
+                l1 += p1;
+                l2 += p2;
+                l3 += p3;
+                big = fmaxf(fmaxf(big, p0), p1);
+                big = fmaxf(fmaxf(big, p2), p3);
+                const __nv_bfloat162 b0 = __floats2bfloat162_rn(p0, p1), b1 = __floats2bfloat162_rn(p2, p3);
+                w[c][i >> 1] = *reinterpret_cast<const uint32_t*>(&b0);
+                w[c][(i >> 1) + 1] = *reinterpret_cast<const uint32_t*>(&b1);
               }
-              top = fmaxf(top, fmaxf(fmaxf(u0, u1), fmaxf(u2, u3)));
             }
           }
-        }
-        top *= a.scale_log2;
-        // the two halves raise the maximum together, and leave together after a wait that gave up
-        if (named_bar_or(bar_id, 64, top > mx + kRaise || !alive)) {
+          ln = (l0 + l1) + (l2 + l3);
+          return big;
+        };
+        bool slow = !settled;
+        if (!slow) slow = named_bar_or(bar_id, 64, weights() > kRaise || !alive);
+        if (slow) {
+          float top = -INFINITY;
+          for (int c = 0; c < pieces; ++c) {
+            float v[16];
+            tmem_ld16(s_addr + c0 + 16 * c, v);
+            tmem_ld_wait_regs(v);
+            if (border) mask16(v, (uint32_t)(seen >> (16 * c)));
+#pragma unroll
+            for (int i = 0; i < 16; ++i) top = fmaxf(top, v[i]);
+          }
+          top *= a.scale_log2;
           *mine = top;
-          alive = named_bar_and(bar_id, 64, alive);
+          alive = named_bar_and(bar_id, 64, alive);   // both halves leave together after a wait that gave up
           const float nm = fmaxf(mx, fmaxf(top, *other));
           const float c = nm == -INFINITY ? 1.f : ex2_approx(mx - nm);
           mx = nm;
           l *= c;
-          if (started && alive) {
+          if (j > jf && alive) {
             // the scores' barrier also covers the products before them: O is complete so far
 #pragma unroll 1
             for (int d = half * (DV / 2); d < (half + 1) * (DV / 2); d += 32) {
@@ -383,40 +415,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
               tmem_st32(o_addr + d, o);
             }
           }
+          weights();
+          settled = named_bar_and(bar_id, 64, !live || mx > -INFINITY);
         }
-        started = true;
-        const float off = mx == -INFINITY ? 0.f : -mx;
-        float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
-        for (int c = 0; c < pieces; c += 2) {
-          float v[2][16];
-          tmem_ld16(s_addr + c0 + 16 * c, v[0]);
-          if (c + 1 < pieces) tmem_ld16(s_addr + c0 + 16 * c + 16, v[1]);
-          tmem_ld_wait_regs(v[0]);
-          tmem_ld_wait_regs(v[1]);
+        l += ln;
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            if (c + u < pieces) {
-              if (border) mask16(v[u], (uint32_t)(seen >> (16 * (c + u))));
-              float w[8];
-#pragma unroll
-              for (int i = 0; i < 16; i += 4) {
-                const float p0 = ex2_approx(fmaf(v[u][i], a.scale_log2, off));
-                const float p1 = ex2_approx(fmaf(v[u][i + 1], a.scale_log2, off));
-                const float p2 = ex2_approx(fmaf(v[u][i + 2], a.scale_log2, off));
-                const float p3 = ex2_approx(fmaf(v[u][i + 3], a.scale_log2, off));
-                l0 += p0;
-                l1 += p1;
-                l2 += p2;
-                l3 += p3;
-                const __nv_bfloat162 b0 = __floats2bfloat162_rn(p0, p1), b1 = __floats2bfloat162_rn(p2, p3);
-                w[i >> 1] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&b0));
-                w[(i >> 1) + 1] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&b1));
-              }
-              tmem_st8(s_addr + c0 + 8 * (c + u), w);   // over scores that have been read
-            }
-          }
-        }
-        l += (l0 + l1) + (l2 + l3);
+        for (int c = 0; c < C::BLK / 32; ++c)
+          if (c < pieces) tmem_st8(s_addr + c0 + 8 * c, reinterpret_cast<const float(&)[8]>(w[c]));
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -447,11 +452,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           const __nv_bfloat162 b = __floats2bfloat162_rn(o[i] * inv, o[i + 1] * inv);
           w[i >> 1] = *reinterpret_cast<const uint32_t*>(&b);
         }
-        if (live) {
-          uint4* dst = reinterpret_cast<uint4*>(a.out + row * DV + d);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) dst[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-        }
+        store_rows32(w, live ? a.out + row * DV + d : nullptr, lane);
       }
       tc_fence_before();
       __syncwarp();
