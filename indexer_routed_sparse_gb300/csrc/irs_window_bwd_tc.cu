@@ -36,6 +36,7 @@ constexpr int kBlk = 128;               // keys a block (dq), keys a tile (dk, d
 constexpr int kCols = 64;               // (query, head) rows a block (dk, dv)
 constexpr uint32_t kAtom = 128 * 128;   // 128 rows x 64 bf16
 constexpr uint32_t kAtom64 = 64 * 128;  // 64 rows x 64 bf16
+constexpr int kDqThreads = 384;         // warps 0-7: score warps; 8: TMA; 9: MMA; 10, 11: D = dout.out
 constexpr int kBwdThreads = 320;        // warps 0-7: score warps; 8: TMA; 9: MMA
 
 __device__ __forceinline__ void wait_landed(uint64_t* bar, uint32_t parity) {
@@ -50,7 +51,7 @@ __device__ __forceinline__ void ts_run(uint32_t d, uint32_t at, uint32_t bb, uin
   const uint64_t b0 = sdesc_sw128(bb, atom, 1024);
 #pragma unroll
   for (int ks = 0; ks < NK; ++ks)
-    umma_bf16_ts(d, at + 8 * ks, b0 + (uint64_t)((ks * 2048) >> 4), idesc, (accumulate || ks > 0) ? 1u : 0u);
+    umma_bf16_ts_warp(d, at + 8 * ks, b0 + (uint64_t)((ks * 2048) >> 4), idesc, (accumulate || ks > 0) ? 1u : 0u);
 }
 // D = A . B^T, both K-major over NA 64-dim atoms.
 template <int NA>
@@ -58,7 +59,7 @@ __device__ __forceinline__ void ss_run(uint32_t d, uint32_t ab, uint32_t a_atom,
   const uint64_t a0 = sdesc_sw128(ab, 16, 1024), b0 = sdesc_sw128(bb, 16, 1024);
 #pragma unroll
   for (int ks = 0; ks < 4 * NA; ++ks)
-    umma_bf16(d, a0 + (uint64_t)(((ks >> 2) * a_atom + (ks & 3) * 32) >> 4),
+    umma_bf16_warp(d, a0 + (uint64_t)(((ks >> 2) * a_atom + (ks & 3) * 32) >> 4),
               b0 + (uint64_t)(((ks >> 2) * b_atom + (ks & 3) * 32) >> 4), idesc, ks > 0);
 }
 
@@ -73,20 +74,23 @@ struct DqCfg {
   static constexpr int KS = 2;
   static constexpr uint32_t v_off = k_off + KS * k_bytes;
   static constexpr int VS = v_off + 2 * v_bytes <= 222u * 1024u ? 2 : 1;
-  static constexpr uint32_t x_off = v_off + VS * v_bytes;     // halves of D, then flags of rows to do again
-  static constexpr uint32_t bar_off = x_off + 3 * 128 * 4;
-  static constexpr uint32_t total = bar_off + 32 * 8 + 16 + 1024;
+  static constexpr uint32_t x_off = v_off + VS * v_bytes;     // [2][2][128] D and lse of an item's rows; flags of rows to do again
+  static constexpr uint32_t bar_off = x_off + 5 * 128 * 4;
+  static constexpr uint32_t plan_off = bar_off + 24 * 8 + 16;  // [2][4] an item's blocks
+  static constexpr uint32_t cu_off = plan_off + 32;
+  static constexpr int cu_cap = 2048;
+  static constexpr uint32_t total = cu_off + 4 * cu_cap + 1024;
   static constexpr uint32_t S0 = 0, P0 = 128, DS0 = 256, DQ0 = 320;
 };
 
 struct DqItem {
   int t0, last, ds0, klo, nb, ns, nbt;
 };
-__device__ __forceinline__ DqItem dq_item(const WinArgs& a, int t0, int qt) {
+__device__ __forceinline__ DqItem dq_item(const WinArgs& a, const int32_t* cu, int t0, int qt) {
   DqItem m;
   m.t0 = t0;
   m.last = min(t0 + qt, a.T) - 1;
-  m.ds0 = window_doc(a.cu, a.ndocs, a.T, t0).start;
+  m.ds0 = window_doc(cu, a.ndocs, a.T, t0).start;
   m.klo = max(m.ds0, t0 - a.window + 1);
   m.nb = (m.last - m.klo) / kBlk + 1;
   m.ns = max(0, min(m.ds0 + a.sinks, m.klo) - m.ds0);
@@ -102,7 +106,7 @@ __device__ __forceinline__ int dq_cols(const DqItem& m, int j) {
 }
 
 template <int DQK, int DV>
-__global__ void __launch_bounds__(kBwdThreads, 1)
+__global__ void __launch_bounds__(kDqThreads, 1)
     window_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
                      const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, WinArgs a, int qt,
                      int tiles) {
@@ -110,8 +114,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   constexpr int KS = C::KS, VS = C::VS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  float* xd = reinterpret_cast<float*>(smem + C::x_off);
-  int* odd_rows = reinterpret_cast<int*>(xd + 256);
+  float* xd = reinterpret_cast<float*>(smem + C::x_off);      // [slot][D, lse (base 2)][row]
+  int* odd_rows = reinterpret_cast<int*>(xd + 512);
   uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::bar_off);
   uint64_t* q_empty = q_full + 1;
   uint64_t* k_full = q_empty + 1;    // [2]
@@ -123,9 +127,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   uint64_t* ds_full = sp_empty + 1;
   uint64_t* dq_full = ds_full + 1;
   uint64_t* dq_empty = dq_full + 1;
-  uint64_t* drain = dq_empty + 1;
+  uint64_t* d_full = dq_empty + 1;   // [2] D and lse of an item
+  uint64_t* d_empty = d_full + 2;    // [2]
+  uint64_t* drain = d_empty + 2;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
+  volatile int* plan = reinterpret_cast<volatile int*>(smem + C::plan_off);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
@@ -133,6 +140,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&k_full[i], 1); mbar_init(&k_empty[i], 1);
       mbar_init(&v_full[i], 1); mbar_init(&v_empty[i], 1);
+      mbar_init(&d_full[i], 2); mbar_init(&d_empty[i], 8);
     }
     mbar_init(sp_full, 1); mbar_init(sp_empty, 8);
     mbar_init(ds_full, 8);
@@ -146,6 +154,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     tmem_relinquish();
   }
   check_documents(a);
+  const int32_t* cu = a.cu;
+  if (a.ndocs < C::cu_cap) {   // searched for every item by every row
+    int32_t* near = reinterpret_cast<int32_t*>(smem + C::cu_off);
+    for (int i = tid; i <= a.ndocs; i += kDqThreads) near[i] = a.cu[i];
+    cu = near;
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -164,7 +178,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       bool ok = true;
       for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
         const int tile = item / a.Hkv, g = item - tile * a.Hkv;
-        const DqItem m = dq_item(a, tile * qt, qt);
+        const DqItem m = dq_item(a, cu, tile * qt, qt);
+        volatile int* pl = plan + 4 * (nq & 1);   // read before the last scores of two items ago
+        pl[0] = m.nbt;
+        pl[1] = (m.ns > 0 ? dq_cols(m, 0) : 0) | dq_cols(m, m.nbt - 1) << 16;
         if (nq > 0 && !mbar_wait(q_empty, (nq - 1) & 1, abort_flag, a.err)) break;
         mbar_arrive_expect_tx(q_full, box * (C::QA + C::VA));
         for (int c = 0; c < C::QA; ++c) tma_load_3d(smem + c * kAtom, &tm_q, c * 64, g * a.G, m.t0, q_full);
@@ -192,55 +209,104 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       }
     }
   } else if (warp == 9) {
-    // ---------------- MMA issuer ----------------
-    if (lane == 0) {
-      constexpr uint32_t DQ_IDESC = idesc_bf16(128, DQK, false, true);
-      const uint32_t sb = smem_u32(smem);
-      uint32_t nk = 0, nv = 0, nsp = 0, nds = 0, ni = 0;   // blocks scored; dS taken; items
-      bool alive = true;
-      auto scores = [&](int cols) {
-        const uint32_t ks = nk % KS, vs = nv % VS;
-        if (!mbar_wait(&k_full[ks], (nk / KS) & 1, abort_flag, a.err)) return false;
-        if (!mbar_wait(&v_full[vs], (nv / VS) & 1, abort_flag, a.err)) return false;
-        if (nsp > 0 && !mbar_wait(sp_empty, (nsp - 1) & 1, abort_flag, a.err)) return false;
-        tc_fence_after();
-        const uint32_t idesc = idesc_bf16(128, cols, false, false);
-        ss_run<C::QA>(tbase + C::S0, sb, kAtom, sb + C::k_off + ks * C::k_bytes, kAtom, idesc);
-        ss_run<C::VA>(tbase + C::P0, sb + C::do_off, kAtom, sb + C::v_off + vs * C::v_bytes, kAtom, idesc);
-        umma_commit(sp_full);
-        umma_commit(&v_empty[vs]);
-        ++nk; ++nv; ++nsp;
-        return true;
-      };
-      for (int item = blockIdx.x; item < items && alive; item += gridDim.x, ++ni) {
-        const DqItem m = dq_item(a, item / a.Hkv * qt, qt);
-        if (!mbar_wait(q_full, ni & 1, abort_flag, a.err)) break;
-        if (!scores(dq_cols(m, 0))) break;
-        if (m.nbt == 1) umma_commit(q_empty);
-        for (int j = 0; j < m.nbt; ++j) {
-          const uint32_t ks = (nk - 1) % KS;   // block j's keys (nk counts block j, not yet j + 1)
-          if (j + 1 < m.nbt) {
-            if (!scores(dq_cols(m, j + 1))) { alive = false; break; }
-            if (j + 2 == m.nbt) umma_commit(q_empty);
-          }
-          if (!mbar_wait(ds_full, nds & 1, abort_flag, a.err)) { alive = false; break; }
-          ++nds;
-          if (j == 0 && ni > 0 && !mbar_wait(dq_empty, (ni - 1) & 1, abort_flag, a.err)) { alive = false; break; }
-          tc_fence_after();
-          const uint32_t kb = sb + C::k_off + ks * C::k_bytes;
-          switch (dq_cols(m, j) >> 5) {
-            case 1: ts_run<2>(tbase + C::DQ0, tbase + C::DS0, kb, kAtom, DQ_IDESC, j > 0); break;
-            case 2: ts_run<4>(tbase + C::DQ0, tbase + C::DS0, kb, kAtom, DQ_IDESC, j > 0); break;
-            case 3: ts_run<6>(tbase + C::DQ0, tbase + C::DS0, kb, kAtom, DQ_IDESC, j > 0); break;
-            default: ts_run<8>(tbase + C::DQ0, tbase + C::DS0, kb, kAtom, DQ_IDESC, j > 0); break;
-          }
-          umma_commit(&k_empty[ks]);   // also: dS has been read (the score warps wait for it below)
+    // ---------------- MMA issuer (the whole warp; one elected lane issues) ----------------
+    constexpr uint32_t DQ_IDESC = idesc_bf16(128, DQK, false, true);
+    const uint32_t sb = smem_u32(smem), tb = (uint32_t)uniform((int)tbase);
+    auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, a.err)); };
+    uint32_t nk = 0, nv = 0, nsp = 0, nds = 0, ni = 0;   // blocks scored; dS taken; items
+    bool alive = true;
+    auto scores = [&](int cols) {
+      const uint32_t ks = nk % KS, vs = nv % VS;
+      if (!wait(&k_full[ks], (nk / KS) & 1)) return false;
+      if (nsp > 0 && !wait(sp_empty, (nsp - 1) & 1)) return false;
+      tc_fence_after();
+      const uint32_t idesc = idesc_bf16(128, cols, false, false);
+      ss_run<C::QA>(tb + C::S0, sb, kAtom, sb + C::k_off + ks * C::k_bytes, kAtom, idesc);
+      if (!wait(&v_full[vs], (nv / VS) & 1)) return false;
+      tc_fence_after();
+      ss_run<C::VA>(tb + C::P0, sb + C::do_off, kAtom, sb + C::v_off + vs * C::v_bytes, kAtom, idesc);
+      umma_commit_warp(sp_full);
+      umma_commit_warp(&v_empty[vs]);
+      ++nk; ++nv; ++nsp;
+      return true;
+    };
+    for (int item = blockIdx.x; item < items && alive; item += gridDim.x, ++ni) {
+      if (!wait(q_full, ni & 1)) break;
+      const volatile int* pl = plan + 4 * (ni & 1);
+      const int nbt = uniform(pl[0]), pc = uniform(pl[1]);
+      const int cols0 = pc & 0xffff, colsL = pc >> 16;
+      auto cols_of = [&](int j) { return j == 0 && cols0 != 0 ? cols0 : j == nbt - 1 ? colsL : kBlk; };
+      if (!scores(cols_of(0))) break;
+      if (nbt == 1) umma_commit_warp(q_empty);
+      for (int j = 0; j < nbt; ++j) {
+        const uint32_t ks = (nk - 1) % KS;   // block j's keys (nk counts block j, not yet j + 1)
+        if (j + 1 < nbt) {
+          if (!scores(cols_of(j + 1))) { alive = false; break; }
+          if (j + 2 == nbt) umma_commit_warp(q_empty);
         }
-        if (!alive) break;
-        umma_commit(dq_full);
+        if (!wait(ds_full, nds & 1)) { alive = false; break; }
+        ++nds;
+        if (j == 0 && ni > 0 && !wait(dq_empty, (ni - 1) & 1)) { alive = false; break; }
+        tc_fence_after();
+        const uint32_t kb = sb + C::k_off + ks * C::k_bytes;
+        switch (cols_of(j) >> 5) {
+          case 1: ts_run<2>(tb + C::DQ0, tb + C::DS0, kb, kAtom, DQ_IDESC, j > 0); break;
+          case 2: ts_run<4>(tb + C::DQ0, tb + C::DS0, kb, kAtom, DQ_IDESC, j > 0); break;
+          case 3: ts_run<6>(tb + C::DQ0, tb + C::DS0, kb, kAtom, DQ_IDESC, j > 0); break;
+          default: ts_run<8>(tb + C::DQ0, tb + C::DS0, kb, kAtom, DQ_IDESC, j > 0); break;
+        }
+        umma_commit_warp(&k_empty[ks]);   // also: dS has been read (the score warps wait for it below)
       }
-      umma_commit(drain);
-      wait_landed(drain, 0);
+      if (!alive) break;
+      umma_commit_warp(dq_full);
+    }
+    umma_commit_warp(drain);
+    wait_landed(drain, 0);
+    __syncwarp();
+  } else if (warp >= 10) {
+    // ---------------- D = dout . out and lse of the next item's rows: DV / 8 lanes a row ----------------
+    constexpr int LR = DV / 8, RW = 32 / LR;   // lanes a row, rows a warp and step
+    uint32_t ni = 0;
+    for (int item = blockIdx.x; item < items; item += gridDim.x, ++ni) {
+      const int tile = item / a.Hkv, g = item - tile * a.Hkv, t0 = tile * qt;
+      const uint32_t slot = ni & 1;
+      if (ni >= 2 && !__all_sync(0xffffffffu, mbar_wait(&d_empty[slot], (ni / 2 - 1) & 1, abort_flag, a.err))) break;
+      float* dst = xd + slot * 256;
+      constexpr int U = 32 / RW;   // steps whose loads are in flight together: half of the warp's 64 rows
+      for (int r0 = (warp - 10) * 64; r0 < (warp - 10) * 64 + 64; r0 += U * RW) {
+        uint4 u[U], w[U];
+        int64_t row[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          const int r = r0 + i * RW + lane / LR, rq = r / a.G, t = t0 + rq;
+          row[i] = rq < qt && t < a.T ? (int64_t)t * a.Hq + g * a.G + (r - rq * a.G) : -1;
+          u[i] = w[i] = make_uint4(0, 0, 0, 0);
+          if (row[i] >= 0) {
+            u[i] = *reinterpret_cast<const uint4*>(a.dout + row[i] * DV + 8 * (lane % LR));
+            w[i] = *reinterpret_cast<const uint4*>(a.out + row[i] * DV + 8 * (lane % LR));
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          const uint32_t uu[4] = {u[i].x, u[i].y, u[i].z, u[i].w}, ww[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+          float s = 0.f;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            s = fmaf(__uint_as_float(uu[k] << 16), __uint_as_float(ww[k] << 16), s);
+            s = fmaf(__uint_as_float(uu[k] & 0xffff0000u), __uint_as_float(ww[k] & 0xffff0000u), s);
+          }
+#pragma unroll
+          for (int o = LR / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+          if (lane % LR == 0) {
+            const int r = r0 + i * RW + lane / LR;
+            dst[r] = s;
+            dst[128 + r] = row[i] >= 0 ? a.lse_in[row[i]] * kLog2e : 0.f;
+            if (row[i] >= 0) a.delta[row[i]] = s;
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&d_full[slot]);
     }
   } else {
     // ---------------- score warps: row = TMEM lane, 64 keys of the block each ----------------
@@ -252,40 +318,21 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     bool alive = true;
     for (int item = blockIdx.x; item < items && alive; item += gridDim.x, ++ni) {
       const int tile = item / a.Hkv, g = item - tile * a.Hkv;
-      const DqItem m = dq_item(a, tile * qt, qt);
+      const DqItem m = dq_item(a, cu, tile * qt, qt);
       const int t = m.t0 + rq, h = g * a.G + rh;
       const bool live = rq < qt && t < a.T;
       const int64_t row = (int64_t)t * a.Hq + h;
-      const int ds = window_doc(a.cu, a.ndocs, a.T, min(t, a.T - 1)).start;
+      const int ds = window_doc(cu, a.ndocs, a.T, min(t, a.T - 1)).start;
       const int lo = max(ds, t - a.window + 1);
       const int early = min(ds + a.sinks, lo);
-      const int lo_last = max(window_doc(a.cu, a.ndocs, a.T, m.last).start, m.last - a.window + 1);
-      // D = dout . out: half the dims a thread, joined through shared memory
-      float l2 = 0.f;
-      {
-        float s = 0.f;
-        if (live) {
-          l2 = a.lse_in[row] * kLog2e;
-          const uint4* x = reinterpret_cast<const uint4*>(a.dout + row * DV + half * (DV / 2));
-          const uint4* y = reinterpret_cast<const uint4*>(a.out + row * DV + half * (DV / 2));
-#pragma unroll
-          for (int i = 0; i < DV / 16; ++i) {
-            const uint4 u = x[i], w = y[i];
-            const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              s = fmaf(__uint_as_float(uu[k] << 16), __uint_as_float(ww[k] << 16), s);
-              s = fmaf(__uint_as_float(uu[k] & 0xffff0000u), __uint_as_float(ww[k] & 0xffff0000u), s);
-            }
-          }
-        }
-        xd[half * 128 + r] = s;
-      }
+      const int lo_last = max(window_doc(cu, a.ndocs, a.T, m.last).start, m.last - a.window + 1);
+      const uint32_t slot = ni & 1;
+      if (!__all_sync(0xffffffffu, mbar_wait(&d_full[slot], (ni / 2) & 1, abort_flag, a.err))) alive = false;
+      const float D = xd[slot * 256 + r], l2 = xd[slot * 256 + 128 + r];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&d_empty[slot]);
       if (half == 0) odd_rows[r] = 0;
-      named_bar_sync(1, 256);
-      const float D = xd[r] + xd[128 + r];
-      if (live && half == 0) a.delta[row] = D;
-      for (int j = 0; j < m.nbt; ++j, ++nkb) {
+      for (int j = 0; alive && j < m.nbt; ++j, ++nkb) {
         const int kb = dq_key(m, j), cols = dq_cols(m, j);
         const bool sink_blk = m.ns > 0 && j == 0;
         if (!__all_sync(0xffffffffu, mbar_wait(sp_full, nsp & 1, abort_flag, a.err))) { alive = false; break; }
@@ -360,17 +407,16 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           const __nv_bfloat162 b = __floats2bfloat162_rn(o[i] * a.scale, o[i + 1] * a.scale);
           w[i >> 1] = *reinterpret_cast<const uint32_t*>(&b);
         }
-        if (live) {
-          uint4* dst = reinterpret_cast<uint4*>(a.dq + row * DQK + d);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) dst[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-        }
+        store_rows32(w, live ? a.dq + row * DQK + d : nullptr, lane);
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(dq_empty);
-      if (live && odd != 0.f) odd_rows[r] = 1;   // NaN compares unequal
-      // both halves have stored their columns; after a wait that gave up all leave together
+      // rows that are not finite (NaN compares unequal) are done again once both halves have
+      // stored; after a wait that gave up all leave together
+      const bool redo = named_bar_or(1, 256, (live && odd != 0.f) || !alive);
+      if (!redo) continue;
+      if (live && odd != 0.f) odd_rows[r] = 1;
       alive = named_bar_and(1, 256, alive);
       if (alive && half == 0) {
         unsigned again = __ballot_sync(0xffffffffu, odd_rows[r] != 0);
@@ -556,51 +602,52 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       for (uint32_t i = ns > ST ? ns - ST : 0; i < ns; ++i) wait_landed(&st_full[i % ST], (i / ST) & 1);
     }
   } else if (warp == 9) {
-    // ---------------- MMA issuer ----------------
-    if (lane == 0) {
-      constexpr uint32_t S_IDESC = idesc_bf16(128, kCols, false, false);
-      constexpr uint32_t DV_IDESC = idesc_bf16(128, DV, false, true), DK_IDESC = idesc_bf16(128, DQK, false, true);
-      const uint32_t sb = smem_u32(smem);
-      uint32_t nsc = 0, npd = 0, ni = 0;   // blocks scored, blocks summed, items
-      bool alive = true;
-      auto scores = [&]() {
-        const uint32_t st = nsc % ST;
-        if (!mbar_wait(&st_full[st], (nsc / ST) & 1, abort_flag, a.err)) return false;
-        if (nsc > 0 && !mbar_wait(sp_empty, (nsc - 1) & 1, abort_flag, a.err)) return false;
-        tc_fence_after();
-        const uint32_t q = sb + C::st_off + st * C::st_bytes;
-        ss_run<C::QA>(tbase + C::S0, sb, kAtom, q, kAtom64, S_IDESC);
-        ss_run<C::VA>(tbase + C::P0, sb + C::k_bytes, kAtom, q + C::q_bytes, kAtom64, S_IDESC);
-        umma_commit(sp_full);
-        ++nsc;
-        return true;
-      };
-      for (int item = blockIdx.x; item < items && alive; item += gridDim.x, ++ni) {
-        const DkvItem m = dkv_item(a, sk, item, tiles, qt, nhc);
-        if (!mbar_wait(kv_full, ni & 1, abort_flag, a.err)) break;
-        if (!scores()) break;
-        if (m.nblk == 1) umma_commit(kv_empty);
-        for (int b = 0; b < m.nblk; ++b) {
-          if (b + 1 < m.nblk) {
-            if (!scores()) { alive = false; break; }
-            if (b + 2 == m.nblk) umma_commit(kv_empty);
-          }
-          if (!mbar_wait(pd_full, npd & 1, abort_flag, a.err)) { alive = false; break; }
-          if (b == 0 && ni > 0 && !mbar_wait(acc_empty, (ni - 1) & 1, abort_flag, a.err)) { alive = false; break; }
-          tc_fence_after();
-          const uint32_t st = npd % ST, q = sb + C::st_off + st * C::st_bytes;
-          ts_run<4>(tbase + C::DV0, tbase + C::PW0, q + C::q_bytes, kAtom64, DV_IDESC, b > 0);
-          ts_run<4>(tbase + C::DK0, tbase + C::DS0, q, kAtom64, DK_IDESC, b > 0);
-          umma_commit(pd_empty);
-          umma_commit(&st_empty[st]);
-          ++npd;
+    // ---------------- MMA issuer (the whole warp; one elected lane issues) ----------------
+    constexpr uint32_t S_IDESC = idesc_bf16(128, kCols, false, false);
+    constexpr uint32_t DV_IDESC = idesc_bf16(128, DV, false, true), DK_IDESC = idesc_bf16(128, DQK, false, true);
+    const uint32_t sb = smem_u32(smem), tb = (uint32_t)uniform((int)tbase);
+    auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, a.err)); };
+    uint32_t nsc = 0, npd = 0, ni = 0, sst = 0, sph = 0, pst = 0;   // blocks scored, blocks summed, items; ring places
+    bool alive = true;
+    auto scores = [&]() {
+      if (!wait(&st_full[sst], sph)) return false;
+      if (nsc > 0 && !wait(sp_empty, (nsc - 1) & 1)) return false;
+      tc_fence_after();
+      const uint32_t q = sb + C::st_off + sst * C::st_bytes;
+      ss_run<C::QA>(tb + C::S0, sb, kAtom, q, kAtom64, S_IDESC);
+      ss_run<C::VA>(tb + C::P0, sb + C::k_bytes, kAtom, q + C::q_bytes, kAtom64, S_IDESC);
+      umma_commit_warp(sp_full);
+      ++nsc;
+      if (++sst == ST) { sst = 0; sph ^= 1u; }
+      return true;
+    };
+    for (int item = blockIdx.x; item < items && alive; item += gridDim.x, ++ni) {
+      const int nblk = uniform(dkv_item(a, sk, item, tiles, qt, nhc).nblk);
+      if (!wait(kv_full, ni & 1)) break;
+      if (!scores()) break;
+      if (nblk == 1) umma_commit_warp(kv_empty);
+      for (int b = 0; b < nblk; ++b) {
+        if (b + 1 < nblk) {
+          if (!scores()) { alive = false; break; }
+          if (b + 2 == nblk) umma_commit_warp(kv_empty);
         }
-        if (!alive) break;
-        umma_commit(acc_full);
+        if (!wait(pd_full, npd & 1)) { alive = false; break; }
+        if (b == 0 && ni > 0 && !wait(acc_empty, (ni - 1) & 1)) { alive = false; break; }
+        tc_fence_after();
+        const uint32_t q = sb + C::st_off + pst * C::st_bytes;
+        ts_run<4>(tb + C::DV0, tb + C::PW0, q + C::q_bytes, kAtom64, DV_IDESC, b > 0);
+        ts_run<4>(tb + C::DK0, tb + C::DS0, q, kAtom64, DK_IDESC, b > 0);
+        umma_commit_warp(pd_empty);
+        umma_commit_warp(&st_empty[pst]);
+        ++npd;
+        if (++pst == ST) pst = 0;
       }
-      umma_commit(drain);
-      wait_landed(drain, 0);
+      if (!alive) break;
+      umma_commit_warp(acc_full);
     }
+    umma_commit_warp(drain);
+    wait_landed(drain, 0);
+    __syncwarp();
   } else {
     // ---------------- score warps: key = TMEM lane, 32 of a block's 64 rows each ----------------
     const int half = warp >> 2;
@@ -833,7 +880,7 @@ cudaError_t launch_bwd(const WinBwdMaps& m, const WinArgs& a, const WinSinks& sk
   }
   const int qt = 128 / a.G, tiles = (a.T + qt - 1) / qt, ktiles = (a.T + kBlk - 1) / kBlk;
   const int64_t items = (int64_t)tiles * a.Hkv;
-  window_dq_kernel<DQK, DV><<<items < num_sms ? (int)items : num_sms, kBwdThreads, Q::total, stream>>>(m.q, m.dout, m.k, m.v, a, qt, tiles);
+  window_dq_kernel<DQK, DV><<<items < num_sms ? (int)items : num_sms, kDqThreads, Q::total, stream>>>(m.q, m.dout, m.k, m.v, a, qt, tiles);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if (sk.slots > 0) {
     window_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a, sk);
