@@ -1154,6 +1154,9 @@ irs_status irs_window_gqa_attn_bwd(const void* q, int64_t q_stride_t, int64_t q_
   if ((s = make_packed_map(&m.dout2, dout, Dv, Hq, T, Dv, (int64_t)Hq * Dv, hc, 64 / hc)) != IRS_OK) return s;
   if ((s = make_packed_map(&m.k, k, Dqk, Hkv, T, k_stride_h, k_stride_t, 1, 128)) != IRS_OK) return s;
   if ((s = make_packed_map(&m.v, v, Dv, Hkv, T, v_stride_h, v_stride_t, 1, 128)) != IRS_OK) return s;
+  const int blk = irs::window_dq_block(Dqk, Dv);
+  if ((s = make_packed_map(&m.kq, k, Dqk, Hkv, T, k_stride_h, k_stride_t, 1, blk)) != IRS_OK) return s;
+  if ((s = make_packed_map(&m.vq, v, Dv, Hkv, T, v_stride_h, v_stride_t, 1, blk)) != IRS_OK) return s;
   std::lock_guard<std::mutex> lk(g_dev_mu);
   return launch_status(irs::launch_window_bwd_tc(m, a, sk, dev->num_sms, dev->window_bwd_configured, st),
                        "launching the window attention backward");

@@ -278,10 +278,11 @@ struct WinSinks {
   float* part;         // [chunks][Hkv][sinks][Dqk + Dv]: from a stretch
 };
 // Maps of the backward: q and dout in boxes as the forward's queries (q, dout) and in boxes
-// of 64 rows (q2, dout2); k and v as in the forward.
+// of 64 rows (q2, dout2); k and v in boxes of 128 tokens, and (kq, vq) of a dq block.
 struct WinBwdMaps {
-  CUtensorMap q, dout, q2, dout2, k, v;
+  CUtensorMap q, dout, q2, dout2, k, v, kq, vq;
 };
+int window_dq_block(int Dqk, int Dv);
 size_t window_bwd_layout(uint8_t* ws, int T, int Hq, int Hkv, int Dqk, int Dv, int ndocs, int window, int sinks, WinSinks* s);
 cudaError_t launch_window_bwd_tc(const WinBwdMaps& m, const WinArgs& a, const WinSinks& sk, int num_sms, bool* configured,
                                  cudaStream_t stream);

@@ -11,9 +11,11 @@
 // 192), four times the cost of the two products.
 //
 // * dq (also D): rows of a product are the query heads of 128 / G queries, as in the forward.
-//   S = Q K^T and dP = dO V^T for a block of 128 keys; two warpgroups (64 keys each, one row
-//   a thread) form dS and leave it in TMEM as bf16, the first operand of dQ += dS K (K read
-//   MN-major). S and dP are read out early, so the next block's products run meanwhile.
+//   S = Q K^T and dP = dO V^T for a block of keys; two warpgroups (half the keys each, one
+//   row a thread) form dS and leave it in TMEM as bf16, the first operand of dQ += dS K (K
+//   read MN-major). S and dP are read out at once, so the next block's products run
+//   meanwhile. Four helper warps form D for the next item and store the last item's dq: done
+//   by the score warps these took 13,000 of an item's 34,000 cycles (192/128, window 512).
 // * dk, dv: rows are 128 keys, columns the rows (query, head) that see them, 64 at a time:
 //   S^T = K Q^T, dP^T = V dO^T; P^T and dS^T return to TMEM as bf16, first operands of
 //   dV += P^T dO and dK += dS^T Q. With Dqk = 192 and Dv = 128 the TMEM is full to the last
@@ -32,11 +34,11 @@ namespace irs {
 
 namespace {
 
-constexpr int kBlk = 128;               // keys a block (dq), keys a tile (dk, dv)
+constexpr int kBlk = 128;               // keys a tile (dk, dv)
 constexpr int kCols = 64;               // (query, head) rows a block (dk, dv)
 constexpr uint32_t kAtom = 128 * 128;   // 128 rows x 64 bf16
 constexpr uint32_t kAtom64 = 64 * 128;  // 64 rows x 64 bf16
-constexpr int kDqThreads = 384;         // warps 0-7: score warps; 8: TMA; 9: MMA; 10, 11: D = dout.out
+constexpr int kDqThreads = 448;         // warps 0-7: score warps; 8: TMA; 9: MMA; 10-13: helpers
 constexpr int kBwdThreads = 320;        // warps 0-7: score warps; 8: TMA; 9: MMA
 
 __device__ __forceinline__ void wait_landed(uint64_t* bar, uint32_t parity) {
@@ -69,39 +71,50 @@ __device__ __forceinline__ void ss_run(uint32_t d, uint32_t ab, uint32_t a_atom,
 template <int DQK, int DV>
 struct DqCfg {
   static constexpr int QA = DQK / 64, VA = DV / 64;
-  static constexpr uint32_t q_bytes = QA * kAtom, do_bytes = VA * kAtom, k_bytes = QA * kAtom, v_bytes = VA * kAtom;
-  static constexpr uint32_t do_off = q_bytes, k_off = q_bytes + do_bytes;
-  static constexpr int KS = 2;
-  static constexpr uint32_t v_off = k_off + KS * k_bytes;
-  static constexpr int VS = v_off + 2 * v_bytes <= 222u * 1024u ? 2 : 1;
-  static constexpr uint32_t x_off = v_off + VS * v_bytes;     // [2][2][128] D and lse of an item's rows; flags of rows to do again
-  static constexpr uint32_t bar_off = x_off + 5 * 128 * 4;
-  static constexpr uint32_t plan_off = bar_off + 24 * 8 + 16;  // [2][4] an item's blocks
-  static constexpr uint32_t cu_off = plan_off + 32;
+  static constexpr uint32_t q_bytes = QA * kAtom, do_bytes = VA * kAtom;
+  // Keys a block, stages of values: what fits beside a tile's queries and dout with three
+  // stages of keys (a block's keys stay until its dS K, two blocks' products later).
+  static constexpr bool fits(int blk, int vs) {
+    return q_bytes + do_bytes + (3 * QA + vs * VA) * blk * 128 <= 214u * 1024u;
+  }
+  static constexpr int BLK = fits(128, 2) ? 128 : 96;
+  static constexpr int KS = 3, VS = fits(BLK, 2) ? 2 : 1;
+  static constexpr uint32_t kv_atom = BLK * 128, k_bytes = QA * kv_atom, v_bytes = VA * kv_atom;
+  static constexpr uint32_t do_off = q_bytes, k_off = q_bytes + do_bytes, v_off = k_off + KS * k_bytes;
+  static constexpr uint32_t row_off = v_off + VS * v_bytes;     // [2][128] of an item's rows: D, lse (base 2), window, document
+  static constexpr uint32_t hdr_off = row_off + 2 * 128 * 16;   // [2][8] of an item: see DqHead
+  static constexpr uint32_t plan_off = hdr_off + 2 * 32;        // [2][4] its blocks, for the MMA warp
+  static constexpr uint32_t bar_off = plan_off + 2 * 16;
+  static constexpr uint32_t cu_off = bar_off + 24 * 8 + 16;
   static constexpr int cu_cap = 2048;
   static constexpr uint32_t total = cu_off + 4 * cu_cap + 1024;
-  static constexpr uint32_t S0 = 0, P0 = 128, DS0 = 256, DQ0 = 320;
+  static constexpr uint32_t S0 = 0, P0 = 128, DS0 = 256, DQ0 = 320;   // TMEM columns
 };
 
+// The keys of one tile of `qt` queries from t0 on: the first `sb` blocks hold the first tokens
+// before the range, where there are any.
 struct DqItem {
-  int t0, last, ds0, klo, nb, ns, nbt;
+  int t0, last, ds0, klo, ns, sb, nbt;
 };
+template <int kBlk>
 __device__ __forceinline__ DqItem dq_item(const WinArgs& a, const int32_t* cu, int t0, int qt) {
   DqItem m;
   m.t0 = t0;
   m.last = min(t0 + qt, a.T) - 1;
   m.ds0 = window_doc(cu, a.ndocs, a.T, t0).start;
   m.klo = max(m.ds0, t0 - a.window + 1);
-  m.nb = (m.last - m.klo) / kBlk + 1;
   m.ns = max(0, min(m.ds0 + a.sinks, m.klo) - m.ds0);
-  m.nbt = m.nb + (m.ns > 0 ? 1 : 0);
+  m.sb = (m.ns + kBlk - 1) / kBlk;
+  m.nbt = (m.last - m.klo) / kBlk + 1 + m.sb;
   return m;
 }
+template <int kBlk>
 __device__ __forceinline__ int dq_key(const DqItem& m, int j) {
-  return m.ns > 0 ? (j == 0 ? m.ds0 : m.klo + kBlk * (j - 1)) : m.klo + kBlk * j;
+  return j < m.sb ? m.ds0 + kBlk * j : m.klo + kBlk * (j - m.sb);
 }
+template <int kBlk>
 __device__ __forceinline__ int dq_cols(const DqItem& m, int j) {
-  const int n = (m.ns > 0 && j == 0) ? m.ns : min(kBlk, m.last - dq_key(m, j) + 1);
+  const int n = min(kBlk, j < m.sb ? m.ns - kBlk * j : m.last - dq_key<kBlk>(m, j) + 1);
   return (n + 31) & ~31;
 }
 
@@ -111,40 +124,41 @@ __global__ void __launch_bounds__(kDqThreads, 1)
                      const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, WinArgs a, int qt,
                      int tiles) {
   using C = DqCfg<DQK, DV>;
-  constexpr int KS = C::KS, VS = C::VS;
+  constexpr int KS = C::KS, VS = C::VS, BLK = C::BLK;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  float* xd = reinterpret_cast<float*>(smem + C::x_off);      // [slot][D, lse (base 2)][row]
-  int* odd_rows = reinterpret_cast<int*>(xd + 512);
+  float4* rows = reinterpret_cast<float4*>(smem + C::row_off);
+  volatile int* head = reinterpret_cast<volatile int*>(smem + C::hdr_off);
+  volatile int* plan = reinterpret_cast<volatile int*>(smem + C::plan_off);
   uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::bar_off);
   uint64_t* q_empty = q_full + 1;
-  uint64_t* k_full = q_empty + 1;    // [2]
-  uint64_t* k_empty = k_full + 2;
-  uint64_t* v_full = k_empty + 2;    // [2]
+  uint64_t* k_full = q_empty + 1;    // [3]
+  uint64_t* k_empty = k_full + 3;
+  uint64_t* v_full = k_empty + 3;    // [2]
   uint64_t* v_empty = v_full + 2;
   uint64_t* sp_full = v_empty + 2;   // scores and dP of a block
   uint64_t* sp_empty = sp_full + 1;  // ... have been read
   uint64_t* ds_full = sp_empty + 1;
-  uint64_t* dq_full = ds_full + 1;
+  uint64_t* ds_empty = ds_full + 1;  // dS has been read by its product
+  uint64_t* dq_full = ds_empty + 1;
   uint64_t* dq_empty = dq_full + 1;
-  uint64_t* d_full = dq_empty + 1;   // [2] D and lse of an item
-  uint64_t* d_empty = d_full + 2;    // [2]
+  uint64_t* d_full = dq_empty + 1;   // [2] an item's rows and head
+  uint64_t* d_empty = d_full + 2;
   uint64_t* drain = d_empty + 2;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
-  volatile int* plan = reinterpret_cast<volatile int*>(smem + C::plan_off);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     mbar_init(q_full, 1); mbar_init(q_empty, 1);
+    for (int i = 0; i < KS; ++i) { mbar_init(&k_full[i], 1); mbar_init(&k_empty[i], 1); }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&k_full[i], 1); mbar_init(&k_empty[i], 1);
       mbar_init(&v_full[i], 1); mbar_init(&v_empty[i], 1);
-      mbar_init(&d_full[i], 2); mbar_init(&d_empty[i], 8);
+      mbar_init(&d_full[i], 4); mbar_init(&d_empty[i], 8);
     }
     mbar_init(sp_full, 1); mbar_init(sp_empty, 8);
-    mbar_init(ds_full, 8);
-    mbar_init(dq_full, 1); mbar_init(dq_empty, 8);
+    mbar_init(ds_full, 8); mbar_init(ds_empty, 1);
+    mbar_init(dq_full, 1); mbar_init(dq_empty, 4);
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -174,31 +188,32 @@ __global__ void __launch_bounds__(kDqThreads, 1)
       tma_prefetch_map(&tm_k);
       tma_prefetch_map(&tm_v);
       const uint32_t box = (uint32_t)(qt * a.G) * 128u;
-      uint32_t nq = 0, nk = 0, nv = 0;
+      uint32_t nq = 0, nk = 0, nv = 0, ks = 0;
       bool ok = true;
       for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
         const int tile = item / a.Hkv, g = item - tile * a.Hkv;
-        const DqItem m = dq_item(a, cu, tile * qt, qt);
+        const DqItem m = dq_item<BLK>(a, cu, tile * qt, qt);
         volatile int* pl = plan + 4 * (nq & 1);   // read before the last scores of two items ago
         pl[0] = m.nbt;
-        pl[1] = (m.ns > 0 ? dq_cols(m, 0) : 0) | dq_cols(m, m.nbt - 1) << 16;
+        pl[1] = (m.sb > 0 ? dq_cols<BLK>(m, m.sb - 1) : 0) | dq_cols<BLK>(m, m.nbt - 1) << 8 | m.sb << 16;
         if (nq > 0 && !mbar_wait(q_empty, (nq - 1) & 1, abort_flag, a.err)) break;
         mbar_arrive_expect_tx(q_full, box * (C::QA + C::VA));
         for (int c = 0; c < C::QA; ++c) tma_load_3d(smem + c * kAtom, &tm_q, c * 64, g * a.G, m.t0, q_full);
         for (int c = 0; c < C::VA; ++c) tma_load_3d(smem + C::do_off + c * kAtom, &tm_do, c * 64, g * a.G, m.t0, q_full);
         ++nq;
         for (int j = 0; j < m.nbt; ++j) {
-          const int kb = dq_key(m, j);
-          const uint32_t ks = nk % KS, vs = nv % VS;
+          const int kb = dq_key<BLK>(m, j);
+          const uint32_t vs = nv % VS;
           if (nk >= KS && !mbar_wait(&k_empty[ks], (nk / KS - 1) & 1, abort_flag, a.err)) { ok = false; break; }
           mbar_arrive_expect_tx(&k_full[ks], C::k_bytes);
           for (int c = 0; c < C::QA; ++c)
-            tma_load_3d(smem + C::k_off + ks * C::k_bytes + c * kAtom, &tm_k, c * 64, g, kb, &k_full[ks]);
+            tma_load_3d(smem + C::k_off + ks * C::k_bytes + c * C::kv_atom, &tm_k, c * 64, g, kb, &k_full[ks]);
           ++nk;
+          if (++ks == KS) ks = 0;
           if (nv >= VS && !mbar_wait(&v_empty[vs], (nv / VS - 1) & 1, abort_flag, a.err)) { ok = false; break; }
           mbar_arrive_expect_tx(&v_full[vs], C::v_bytes);
           for (int c = 0; c < C::VA; ++c)
-            tma_load_3d(smem + C::v_off + vs * C::v_bytes + c * kAtom, &tm_v, c * 64, g, kb, &v_full[vs]);
+            tma_load_3d(smem + C::v_off + vs * C::v_bytes + c * C::kv_atom, &tm_v, c * 64, g, kb, &v_full[vs]);
           ++nv;
         }
       }
@@ -213,33 +228,33 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     constexpr uint32_t DQ_IDESC = idesc_bf16(128, DQK, false, true);
     const uint32_t sb = smem_u32(smem), tb = (uint32_t)uniform((int)tbase);
     auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, a.err)); };
-    uint32_t nk = 0, nv = 0, nsp = 0, nds = 0, ni = 0;   // blocks scored; dS taken; items
+    uint32_t nv = 0, nsp = 0, nds = 0, ni = 0, ks = 0, kph = 0, kd = 0;   // kd: stage of the block whose dS comes next
     bool alive = true;
     auto scores = [&](int cols) {
-      const uint32_t ks = nk % KS, vs = nv % VS;
-      if (!wait(&k_full[ks], (nk / KS) & 1)) return false;
+      const uint32_t vs = nv % VS;
+      if (!wait(&k_full[ks], kph)) return false;
       if (nsp > 0 && !wait(sp_empty, (nsp - 1) & 1)) return false;
       tc_fence_after();
       const uint32_t idesc = idesc_bf16(128, cols, false, false);
-      ss_run<C::QA>(tb + C::S0, sb, kAtom, sb + C::k_off + ks * C::k_bytes, kAtom, idesc);
+      ss_run<C::QA>(tb + C::S0, sb, kAtom, sb + C::k_off + ks * C::k_bytes, C::kv_atom, idesc);
       if (!wait(&v_full[vs], (nv / VS) & 1)) return false;
       tc_fence_after();
-      ss_run<C::VA>(tb + C::P0, sb + C::do_off, kAtom, sb + C::v_off + vs * C::v_bytes, kAtom, idesc);
+      ss_run<C::VA>(tb + C::P0, sb + C::do_off, kAtom, sb + C::v_off + vs * C::v_bytes, C::kv_atom, idesc);
       umma_commit_warp(sp_full);
       umma_commit_warp(&v_empty[vs]);
-      ++nk; ++nv; ++nsp;
+      ++nv; ++nsp;
+      if (++ks == KS) { ks = 0; kph ^= 1u; }
       return true;
     };
     for (int item = blockIdx.x; item < items && alive; item += gridDim.x, ++ni) {
       if (!wait(q_full, ni & 1)) break;
       const volatile int* pl = plan + 4 * (ni & 1);
       const int nbt = uniform(pl[0]), pc = uniform(pl[1]);
-      const int cols0 = pc & 0xffff, colsL = pc >> 16;
-      auto cols_of = [&](int j) { return j == 0 && cols0 != 0 ? cols0 : j == nbt - 1 ? colsL : kBlk; };
+      const int colsS = pc & 0xff, colsL = pc >> 8 & 0xff, sb1 = (pc >> 16) - 1;
+      auto cols_of = [&](int j) { return j == sb1 ? colsS : j == nbt - 1 ? colsL : BLK; };
       if (!scores(cols_of(0))) break;
       if (nbt == 1) umma_commit_warp(q_empty);
       for (int j = 0; j < nbt; ++j) {
-        const uint32_t ks = (nk - 1) % KS;   // block j's keys (nk counts block j, not yet j + 1)
         if (j + 1 < nbt) {
           if (!scores(cols_of(j + 1))) { alive = false; break; }
           if (j + 2 == nbt) umma_commit_warp(q_empty);
@@ -248,14 +263,16 @@ __global__ void __launch_bounds__(kDqThreads, 1)
         ++nds;
         if (j == 0 && ni > 0 && !wait(dq_empty, (ni - 1) & 1)) { alive = false; break; }
         tc_fence_after();
-        const uint32_t kb = sb + C::k_off + ks * C::k_bytes;
+        const uint32_t kb = sb + C::k_off + kd * C::k_bytes;
         switch (cols_of(j) >> 5) {
-          case 1: ts_run<2>(tb + C::DQ0, tb + C::DS0, kb, kAtom, DQ_IDESC, j > 0); break;
-          case 2: ts_run<4>(tb + C::DQ0, tb + C::DS0, kb, kAtom, DQ_IDESC, j > 0); break;
-          case 3: ts_run<6>(tb + C::DQ0, tb + C::DS0, kb, kAtom, DQ_IDESC, j > 0); break;
-          default: ts_run<8>(tb + C::DQ0, tb + C::DS0, kb, kAtom, DQ_IDESC, j > 0); break;
+          case 1: ts_run<2>(tb + C::DQ0, tb + C::DS0, kb, C::kv_atom, DQ_IDESC, j > 0); break;
+          case 2: ts_run<4>(tb + C::DQ0, tb + C::DS0, kb, C::kv_atom, DQ_IDESC, j > 0); break;
+          case 3: ts_run<6>(tb + C::DQ0, tb + C::DS0, kb, C::kv_atom, DQ_IDESC, j > 0); break;
+          default: ts_run<8>(tb + C::DQ0, tb + C::DS0, kb, C::kv_atom, DQ_IDESC, j > 0); break;
         }
-        umma_commit_warp(&k_empty[ks]);   // also: dS has been read (the score warps wait for it below)
+        umma_commit_warp(ds_empty);
+        umma_commit_warp(&k_empty[kd]);
+        if (++kd == KS) kd = 0;
       }
       if (!alive) break;
       umma_commit_warp(dq_full);
@@ -264,169 +281,196 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     wait_landed(drain, 0);
     __syncwarp();
   } else if (warp >= 10) {
-    // ---------------- D = dout . out and lse of the next item's rows: DV / 8 lanes a row ----------------
-    constexpr int LR = DV / 8, RW = 32 / LR;   // lanes a row, rows a warp and step
+    // ---------------- helpers: the next item's D, lse and borders; the last item's dq ----------------
+    constexpr int LR = DV / 8, RW = 32 / LR, U = 8;   // lanes a row; rows a step; steps in flight together (32 rows a warp)
+    const uint32_t lanes = tmem_lane_base(warp);
     uint32_t ni = 0;
-    for (int item = blockIdx.x; item < items; item += gridDim.x, ++ni) {
-      const int tile = item / a.Hkv, g = item - tile * a.Hkv, t0 = tile * qt;
-      const uint32_t slot = ni & 1;
-      if (ni >= 2 && !__all_sync(0xffffffffu, mbar_wait(&d_empty[slot], (ni / 2 - 1) & 1, abort_flag, a.err))) break;
-      float* dst = xd + slot * 256;
-      constexpr int U = 32 / RW;   // steps whose loads are in flight together: half of the warp's 64 rows
-      for (int r0 = (warp - 10) * 64; r0 < (warp - 10) * 64 + 64; r0 += U * RW) {
+    int prev = -1;
+    for (int item = blockIdx.x;; item += gridDim.x, ++ni) {
+      if (item < items) {
+        const int tile = item / a.Hkv, g = item - tile * a.Hkv;
+        const uint32_t slot = ni & 1;
+        if (ni >= 2 && !__all_sync(0xffffffffu, mbar_wait(&d_empty[slot], (ni / 2 - 1) & 1, abort_flag, a.err))) break;
+        const DqItem m = dq_item<BLK>(a, cu, tile * qt, qt);
+        if (warp == 10 && lane == 0) {
+          volatile int* h = head + 8 * slot;
+          h[0] = m.klo;
+          h[1] = m.ns;
+          h[2] = m.nbt;
+          h[3] = max(window_doc(cu, a.ndocs, a.T, m.last).start, m.last - a.window + 1);
+          h[4] = m.ds0;
+          h[5] = m.last;
+        }
+#pragma unroll 1
+        for (int r0 = (warp - 10) * 32; r0 < (warp - 10) * 32 + 32; r0 += U * RW) {
         uint4 u[U], w[U];
         int64_t row[U];
+        float l[U];
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-          const int r = r0 + i * RW + lane / LR, rq = r / a.G, t = t0 + rq;
+          const int r = r0 + i * RW + lane / LR, rq = r / a.G, t = m.t0 + rq;
           row[i] = rq < qt && t < a.T ? (int64_t)t * a.Hq + g * a.G + (r - rq * a.G) : -1;
           u[i] = w[i] = make_uint4(0, 0, 0, 0);
+          l[i] = 0.f;
           if (row[i] >= 0) {
             u[i] = *reinterpret_cast<const uint4*>(a.dout + row[i] * DV + 8 * (lane % LR));
             w[i] = *reinterpret_cast<const uint4*>(a.out + row[i] * DV + 8 * (lane % LR));
+            if (lane % LR == 0) l[i] = a.lse_in[row[i]];
           }
         }
 #pragma unroll
         for (int i = 0; i < U; ++i) {
           const uint32_t uu[4] = {u[i].x, u[i].y, u[i].z, u[i].w}, ww[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-          float s = 0.f;
+          float s = 0.f, s1 = 0.f;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             s = fmaf(__uint_as_float(uu[k] << 16), __uint_as_float(ww[k] << 16), s);
-            s = fmaf(__uint_as_float(uu[k] & 0xffff0000u), __uint_as_float(ww[k] & 0xffff0000u), s);
+            s1 = fmaf(__uint_as_float(uu[k] & 0xffff0000u), __uint_as_float(ww[k] & 0xffff0000u), s1);
           }
+          s += s1;
 #pragma unroll
           for (int o = LR / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
           if (lane % LR == 0) {
-            const int r = r0 + i * RW + lane / LR;
-            dst[r] = s;
-            dst[128 + r] = row[i] >= 0 ? a.lse_in[row[i]] * kLog2e : 0.f;
+            const int r = r0 + i * RW + lane / LR, t = min(m.t0 + r / a.G, a.T - 1);
+            const int ds = window_doc(cu, a.ndocs, a.T, t).start;
+            rows[slot * 128 + r] = make_float4(s, l[i] * kLog2e, __int_as_float(max(ds, t - a.window + 1)), __int_as_float(ds));
             if (row[i] >= 0) a.delta[row[i]] = s;
           }
         }
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&d_full[slot]);
-    }
-  } else {
-    // ---------------- score warps: row = TMEM lane, 64 keys of the block each ----------------
-    const int half = warp >> 2;
-    const int r = (warp & 3) * 32 + lane;
-    const int rq = r / a.G, rh = r - rq * a.G;
-    const uint32_t lanes = tmem_lane_base(warp);
-    uint32_t nsp = 0, ni = 0, nkb = 0;
-    bool alive = true;
-    for (int item = blockIdx.x; item < items && alive; item += gridDim.x, ++ni) {
-      const int tile = item / a.Hkv, g = item - tile * a.Hkv;
-      const DqItem m = dq_item(a, cu, tile * qt, qt);
-      const int t = m.t0 + rq, h = g * a.G + rh;
-      const bool live = rq < qt && t < a.T;
-      const int64_t row = (int64_t)t * a.Hq + h;
-      const int ds = window_doc(cu, a.ndocs, a.T, min(t, a.T - 1)).start;
-      const int lo = max(ds, t - a.window + 1);
-      const int early = min(ds + a.sinks, lo);
-      const int lo_last = max(window_doc(cu, a.ndocs, a.T, m.last).start, m.last - a.window + 1);
-      const uint32_t slot = ni & 1;
-      if (!__all_sync(0xffffffffu, mbar_wait(&d_full[slot], (ni / 2) & 1, abort_flag, a.err))) alive = false;
-      const float D = xd[slot * 256 + r], l2 = xd[slot * 256 + 128 + r];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&d_empty[slot]);
-      if (half == 0) odd_rows[r] = 0;
-      for (int j = 0; alive && j < m.nbt; ++j, ++nkb) {
-        const int kb = dq_key(m, j), cols = dq_cols(m, j);
-        const bool sink_blk = m.ns > 0 && j == 0;
-        if (!__all_sync(0xffffffffu, mbar_wait(sp_full, nsp & 1, abort_flag, a.err))) { alive = false; break; }
-        ++nsp;
-        tc_fence_after();
-        const bool border = sink_blk || kb < lo_last || kb + cols - 1 > m.t0;
-        int w0 = lo - kb, w1 = t - kb, e0 = ds - kb, e1 = early - kb;
-        if (sink_blk) { w0 = 1; w1 = 0; e0 = 0; e1 = ds == m.ds0 ? m.ns : 0; }
-        if (!live) { w0 = 1; w1 = 0; e1 = e0 = 0; }
-        const unsigned wn = (unsigned)max(w1 - w0 + 1, 0), en = (unsigned)max(e1 - e0, 0);
-        const int mine = min(max((cols >> 5) - 2 * half, 0), 2);   // 32-key pieces of this half
-        // dS of the block before must have been read by its product before it is replaced
-        bool taken = nkb == 0;
-        auto wait_taken = [&]() {
-          if (!taken && !__all_sync(0xffffffffu, mbar_wait(&k_empty[(nkb - 1) % KS], ((nkb - 1) / KS) & 1, abort_flag, a.err)))
-            alive = false;
-          taken = true;
-        };
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          if (c < mine) {
-            const int k0 = 64 * half + 32 * c;
-            float s[32], p[32];
-            tmem_ld32(tbase + C::S0 + lanes + k0, s);
-            tmem_ld32(tbase + C::P0 + lanes + k0, p);
-            tmem_ld_wait_regs(s);
-            tmem_ld_wait_regs(p);
-            if (c == mine - 1) {   // the last of the block's scores are in registers
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(sp_empty);
-            }
-#pragma unroll
-            for (int i = 0; i < 32; ++i) s[i] = ex2_approx(fmaf(s[i], a.scale_log2, -l2)) * (p[i] - D);
-            if (border) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                const int k = k0 + i;
-                s[i] = (unsigned)(k - w0) < wn || (unsigned)(k - e0) < en ? s[i] : 0.f;
-              }
-            }
-            float w[16];
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              const __nv_bfloat162 b = __floats2bfloat162_rn(s[i], s[i + 1]);
-              w[i >> 1] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&b));
-            }
-            wait_taken();
-            tmem_st16(tbase + C::DS0 + lanes + (k0 >> 1), w);
-          }
         }
-        if (mine == 0 && lane == 0) mbar_arrive(sp_empty);
-        wait_taken();
-        if (!alive) break;
-        tmem_st_wait();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&d_full[slot]);
+      }
+      if (prev >= 0) {
+        const int tile = prev / a.Hkv, g = prev - tile * a.Hkv;
+        const int r = (warp & 3) * 32 + lane, rq = r / a.G, t = tile * qt + rq, h = g * a.G + (r - rq * a.G);
+        const bool live = rq < qt && t < a.T;
+        const int64_t row = (int64_t)t * a.Hq + h;
+        if (!__all_sync(0xffffffffu, mbar_wait(dq_full, (ni - 1) & 1, abort_flag, a.err))) break;
+        tc_fence_after();
+        float odd = 0.f;
+#pragma unroll 1
+        for (int d = 0; d < DQK; d += 32) {
+          float o[32];
+          tmem_ld32(tbase + C::DQ0 + lanes + d, o);
+          tmem_ld_wait_regs(o);
+          uint32_t w[16];
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            odd = fmaf(o[i], 0.f, fmaf(o[i + 1], 0.f, odd));
+            const __nv_bfloat162 b = __floats2bfloat162_rn(o[i] * a.scale, o[i + 1] * a.scale);
+            w[i >> 1] = *reinterpret_cast<const uint32_t*>(&b);
+          }
+          store_rows32(w, live ? a.dq + row * DQK + d : nullptr, lane);
+        }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(ds_full);
-      }
-      if (alive && !__all_sync(0xffffffffu, mbar_wait(dq_full, ni & 1, abort_flag, a.err))) alive = false;
-      tc_fence_after();
-      float odd = 0.f;
-#pragma unroll 1
-      for (int d = 32 * half; alive && d < DQK; d += 64) {
-        float o[32];
-        tmem_ld32(tbase + C::DQ0 + lanes + d, o);
-        tmem_ld_wait_regs(o);
-        uint32_t w[16];
-#pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-          odd = fmaf(o[i], 0.f, fmaf(o[i + 1], 0.f, odd));
-          const __nv_bfloat162 b = __floats2bfloat162_rn(o[i] * a.scale, o[i + 1] * a.scale);
-          w[i >> 1] = *reinterpret_cast<const uint32_t*>(&b);
-        }
-        store_rows32(w, live ? a.dq + row * DQK + d : nullptr, lane);
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(dq_empty);
-      // rows that are not finite (NaN compares unequal) are done again once both halves have
-      // stored; after a wait that gave up all leave together
-      const bool redo = named_bar_or(1, 256, (live && odd != 0.f) || !alive);
-      if (!redo) continue;
-      if (live && odd != 0.f) odd_rows[r] = 1;
-      alive = named_bar_and(1, 256, alive);
-      if (alive && half == 0) {
-        unsigned again = __ballot_sync(0xffffffffu, odd_rows[r] != 0);
+        if (lane == 0) mbar_arrive(dq_empty);
+        unsigned again = __ballot_sync(0xffffffffu, live && odd != 0.f);   // NaN compares unequal
         while (again) {
           const int src = __ffs((int)again) - 1;
           again &= again - 1;
           dq_row<DQK / 64, DV / 64>(a, __shfl_sync(0xffffffffu, t, src), __shfl_sync(0xffffffffu, h, src), lane);
         }
       }
-      named_bar_sync(1, 256);
+      if (item >= items) break;
+      prev = item;
+    }
+  } else {
+    // ---------------- score warps: row = TMEM lane, half of the block's keys each ----------------
+    const int half = warp >> 2;
+    const int r = (warp & 3) * 32 + lane;
+    const int rq = r / a.G;
+    const uint32_t lanes = tmem_lane_base(warp);
+    uint32_t nsp = 0, ni = 0;
+    bool alive = true;
+    for (int item = blockIdx.x; item < items && alive; item += gridDim.x, ++ni) {
+      const uint32_t slot = ni & 1;
+      if (!__all_sync(0xffffffffu, mbar_wait(&d_full[slot], (ni / 2) & 1, abort_flag, a.err))) break;
+      const float4 mine = rows[slot * 128 + r];
+      const volatile int* hd = head + 8 * slot;
+      DqItem m;
+      m.klo = hd[0];
+      m.ns = hd[1];
+      m.nbt = hd[2];
+      m.sb = (m.ns + BLK - 1) / BLK;
+      const int lo_last = hd[3];
+      m.ds0 = hd[4];
+      m.last = hd[5];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&d_empty[slot]);
+      m.t0 = item / a.Hkv * qt;
+      const float D = mine.x, l2 = mine.y;
+      const int lo = __float_as_int(mine.z), ds = __float_as_int(mine.w), t = m.t0 + rq;
+      const int early = min(ds + a.sinks, lo);
+      const bool live = rq < qt && t < a.T;
+      for (int j = 0; j < m.nbt; ++j, ++nsp) {
+        const int kb = dq_key<BLK>(m, j), cols = dq_cols<BLK>(m, j);
+        const bool sink_blk = j < m.sb;
+        const int pieces = cols >> 5, c0 = half * (cols >> 1);   // 16-key pieces of this half, its first key
+        uint64_t seen = ~0ull;
+        const bool border = sink_blk || kb < lo_last || kb + cols - 1 > m.t0;
+        if (border) {
+          const int k0 = kb + c0;
+          seen = bit_range(lo - k0, t + 1 - k0) | bit_range(ds - k0, early - k0);
+          if (sink_blk) seen = ds == m.ds0 ? bit_range(0, m.ns - BLK * j - c0) : 0ull;
+          if (!live) seen = 0ull;
+        }
+        if (!__all_sync(0xffffffffu, mbar_wait(sp_full, nsp & 1, abort_flag, a.err))) { alive = false; break; }
+        tc_fence_after();
+        // three pieces (96 keys a block) are read at once, so that the next block's products can start
+#pragma unroll
+        for (int c1 = 0; c1 < BLK / 32; c1 += 3) {
+          float s[3][16], p[3][16];
+#pragma unroll
+          for (int c = 0; c < 3; ++c)
+            if (c1 + c < pieces) {
+              tmem_ld16(tbase + C::S0 + lanes + c0 + 16 * (c1 + c), s[c]);
+              tmem_ld16(tbase + C::P0 + lanes + c0 + 16 * (c1 + c), p[c]);
+            }
+#pragma unroll
+          for (int c = 0; c < 3; ++c) {
+            tmem_ld_wait_regs(s[c]);
+            tmem_ld_wait_regs(p[c]);
+          }
+          if (c1 + 3 >= BLK / 32) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(sp_empty);
+          }
+#pragma unroll
+          for (int c = 0; c < 3; ++c) {
+            if (c1 + c < pieces) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) s[c][i] = ex2_approx(fmaf(s[c][i], a.scale_log2, -l2)) * (p[c][i] - D);
+              if (border) {
+                const uint32_t bits = (uint32_t)(seen >> (16 * (c1 + c)));
+#pragma unroll
+                for (int i = 0; i < 16; ++i) s[c][i] = (bits >> i) & 1u ? s[c][i] : 0.f;
+              }
+            }
+          }
+          // dS of the block before must have been read by its product before it is replaced
+          if (c1 == 0 && nsp > 0 && !__all_sync(0xffffffffu, mbar_wait(ds_empty, (nsp - 1) & 1, abort_flag, a.err))) alive = false;
+#pragma unroll
+          for (int c = 0; c < 3; ++c) {
+            if (c1 + c < pieces) {
+              float w[8];
+#pragma unroll
+              for (int i = 0; i < 16; i += 2) {
+                const __nv_bfloat162 b = __floats2bfloat162_rn(s[c][i], s[c][i + 1]);
+                w[i >> 1] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&b));
+              }
+              tmem_st8(tbase + C::DS0 + lanes + ((c0 + 16 * (c1 + c)) >> 1), w);
+            }
+          }
+        }
+        if (!alive) break;
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ds_full);
+      }
     }
   }
   tc_fence_before();
@@ -865,6 +909,22 @@ __global__ void __launch_bounds__(128) window_join_kernel(WinArgs a, WinSinks sk
   if (__syncthreads_or(odd != 0.f) && threadIdx.x < 32) dkv_row<DQK / 64, DV / 64>(a, start + i, g, threadIdx.x, true, true);
 }
 
+}  // namespace
+
+// Keys a block of the dq kernel: the box of its k and v maps.
+int window_dq_block(int Dqk, int Dv) {
+  switch ((Dqk / 64 - 1) * 2 + (Dv / 64 - 1)) {
+    case 0: return DqCfg<64, 64>::BLK;
+    case 1: return DqCfg<64, 128>::BLK;
+    case 2: return DqCfg<128, 64>::BLK;
+    case 3: return DqCfg<128, 128>::BLK;
+    case 4: return DqCfg<192, 64>::BLK;
+    default: return DqCfg<192, 128>::BLK;
+  }
+}
+
+namespace {
+
 template <int DQK, int DV>
 cudaError_t launch_bwd(const WinBwdMaps& m, const WinArgs& a, const WinSinks& sk, int num_sms, bool* configured,
                        cudaStream_t stream) {
@@ -880,7 +940,7 @@ cudaError_t launch_bwd(const WinBwdMaps& m, const WinArgs& a, const WinSinks& sk
   }
   const int qt = 128 / a.G, tiles = (a.T + qt - 1) / qt, ktiles = (a.T + kBlk - 1) / kBlk;
   const int64_t items = (int64_t)tiles * a.Hkv;
-  window_dq_kernel<DQK, DV><<<items < num_sms ? (int)items : num_sms, kDqThreads, Q::total, stream>>>(m.q, m.dout, m.k, m.v, a, qt, tiles);
+  window_dq_kernel<DQK, DV><<<items < num_sms ? (int)items : num_sms, kDqThreads, Q::total, stream>>>(m.q, m.dout, m.kq, m.vq, a, qt, tiles);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if (sk.slots > 0) {
     window_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a, sk);

@@ -9,6 +9,14 @@ namespace irs {
 
 namespace {
 
+// Bits [from, to) of a 64-bit word, both clamped to [0, 64].
+__device__ __forceinline__ uint64_t bit_range(int from, int to) {
+  from = max(from, 0);
+  to = min(to, 64);
+  if (from >= to) return 0ull;
+  return (~0ull >> (64 - (to - from))) << from;
+}
+
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 

@@ -59,13 +59,13 @@ struct FwdCfg {
   static constexpr uint32_t S0 = 0, O0 = 256;              // TMEM: S of tile x at 128 x, O at 256 + x DV
 };
 
-// The keys of one item: two tiles of `qt` queries from t0 on. Block 0 holds the first tokens
-// before the range where there are any; the first tile takes blocks [0, l0], the second [f1,
-// nbt).
+// The keys of one item: two tiles of `qt` queries from t0 on. The first `sb` blocks hold the
+// first tokens before the range, where there are any; the first tile takes blocks [0, l0],
+// the second [f1, nbt).
 struct Item {
   int t0, last, lastA;   // first query; last query of the item and of its first tile
   int ds0, klo, ns;      // document start of the first query; first key of the range; first tokens before it
-  int nbt, l0, f1;
+  int sb, nbt, l0, f1;
   bool hasB;
 };
 template <int kBlk>
@@ -78,34 +78,26 @@ __device__ __forceinline__ Item window_item(const WinArgs& a, const int32_t* cu,
   m.ds0 = window_doc(cu, a.ndocs, a.T, t0).start;
   m.klo = max(m.ds0, t0 - a.window + 1);
   m.ns = max(0, min(m.ds0 + a.sinks, m.klo) - m.ds0);
-  const int s = m.ns > 0 ? 1 : 0;
-  m.nbt = (m.last - m.klo) / kBlk + 1 + s;
-  m.l0 = (m.lastA - m.klo) / kBlk + s;
+  m.sb = (m.ns + kBlk - 1) / kBlk;
+  m.nbt = (m.last - m.klo) / kBlk + 1 + m.sb;
+  m.l0 = (m.lastA - m.klo) / kBlk + m.sb;
   m.f1 = 0;
   if (m.hasB) {
     const int tb = t0 + qt, dsB = window_doc(cu, a.ndocs, a.T, tb).start;
     // blocks before the second tile's window are left out; with first tokens, only theirs
     if (a.sinks == 0) m.f1 = (max(dsB, tb - a.window + 1) - m.klo) / kBlk;
-    else m.f1 = s != 0 && dsB != m.ds0 ? 1 : 0;
+    else m.f1 = dsB != m.ds0 ? m.sb : 0;
   }
   return m;
 }
 template <int kBlk>
 __device__ __forceinline__ int item_key(const Item& m, int j) {   // first key of block j
-  return m.ns > 0 ? (j == 0 ? m.ds0 : m.klo + kBlk * (j - 1)) : m.klo + kBlk * j;
+  return j < m.sb ? m.ds0 + kBlk * j : m.klo + kBlk * (j - m.sb);
 }
 template <int kBlk>
 __device__ __forceinline__ int item_cols(const Item& m, int j) {  // its keys, up to a multiple of 32
-  const int n = (m.ns > 0 && j == 0) ? m.ns : min(kBlk, m.last - item_key<kBlk>(m, j) + 1);
+  const int n = min(kBlk, j < m.sb ? m.ns - kBlk * j : m.last - item_key<kBlk>(m, j) + 1);
   return (n + 31) & ~31;
-}
-
-// Bits [from, to) of a 64-bit word, both clamped to [0, 64].
-__device__ __forceinline__ uint64_t bit_range(int from, int to) {
-  from = max(from, 0);
-  to = min(to, 64);
-  if (from >= to) return 0ull;
-  return (~0ull >> (64 - (to - from))) << from;
 }
 
 __device__ __forceinline__ void mask16(float (&v)[16], uint32_t bits) {
@@ -216,7 +208,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         pl[0] = m.nbt;
         pl[1] = m.l0;
         pl[2] = m.hasB ? m.f1 : m.nbt;
-        pl[3] = (m.ns > 0 ? item_cols<C::BLK>(m, 0) : 0) | item_cols<C::BLK>(m, m.nbt - 1) << 16;
+        pl[3] = (m.sb > 0 ? item_cols<C::BLK>(m, m.sb - 1) : 0) | item_cols<C::BLK>(m, m.nbt - 1) << 8 | m.sb << 16;
         if (!(ok = load_q(0, m, g))) break;
         for (int j = 0; j < m.nbt && ok; ++j) {
           const int kb = item_key<C::BLK>(m, j);
@@ -257,12 +249,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       if (!wait(&q_full[0], nq[0] & 1)) break;
       const volatile int* pl = plan + 4 * (nq[0] & 1);
       const int nbt = uniform(pl[0]), l0 = uniform(pl[1]), f1 = uniform(pl[2]), pc = uniform(pl[3]);
-      const int cols0 = pc & 0xffff, colsL = pc >> 16;   // columns of a first-token block (0: none), of the last
+      const int colsS = pc & 0xff, colsL = pc >> 8 & 0xff, sb1 = (pc >> 16) - 1;   // columns of the last first-token block (sb1) and of the last
       ++nq[0];
       int pcols = 0;
       for (int j = 0; j <= nbt && alive; ++j) {
         const bool more = j < nbt;
-        const int cols = j == 0 && cols0 != 0 ? cols0 : j == nbt - 1 ? colsL : C::BLK;
+        const int cols = j == sb1 ? colsS : j == nbt - 1 ? colsL : C::BLK;
         const uint32_t kst = nk & 1, vst = nv & 1;
         if (more && !wait(&k_full[kst], (nk >> 1) & 1)) { alive = false; break; }
         if (j > 0 && !wait(&v_full[vst], (nv >> 1) & 1)) { alive = false; break; }
@@ -334,7 +326,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       const int jf = x == 0 ? 0 : m.f1, jl = x == 0 ? m.l0 : m.nbt - 1;
       for (int j = jf; j <= jl && alive; ++j) {
         const int kb = item_key<C::BLK>(m, j), cols = item_cols<C::BLK>(m, j);
-        const bool sink_blk = m.ns > 0 && j == 0;
+        const bool sink_blk = j < m.sb;
         const int pieces = cols >> 5, c0 = half * (cols >> 1);   // 16-key pieces of this half, its first column
         alive = __all_sync(0xffffffffu, mbar_wait(&s_full[x], nsf & 1, abort_flag, a.err));
         ++nsf;
@@ -345,7 +337,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         if (border) {
           const int k0 = kb + c0;
           seen = bit_range(lo - k0, t + 1 - k0) | bit_range(ds - k0, early - k0);
-          if (sink_blk) seen = ds == m.ds0 ? bit_range(0, m.ns - c0) : 0ull;
+          if (sink_blk) seen = ds == m.ds0 ? bit_range(0, m.ns - C::BLK * j - c0) : 0ull;
           if (!live) seen = 0ull;
         }
         // One pass: the weights under the present maximum, and whether one passes 2^8. They
@@ -481,6 +473,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 
 }  // namespace
 
+// Keys a block of the forward: the box of its k and v maps.
 int window_fwd_block(int Dqk, int Dv) { return Dqk == 192 && Dv == 128 ? FwdCfg<192, 128>::BLK : 128; }
 
 namespace {

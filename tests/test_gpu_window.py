@@ -64,6 +64,13 @@ def test_windows_and_first_tokens(irs, window, sinks):
     _case(irs, *_inputs(420, 4, 2, 128, 128, [120, 300]), window=window, sinks=sinks)
 
 
+@pytest.mark.parametrize("Dqk,Dv", [(64, 64), (64, 128), (128, 64), (192, 64), (192, 128)])
+@pytest.mark.parametrize("window,sinks", [(3, 128), (40, 97), (250, 33)])
+def test_many_first_tokens(irs, Dqk, Dv, window, sinks):
+    """More first tokens than one block of keys holds, at every pair of head dims."""
+    _case(irs, *_inputs(420, 6, 2, Dqk, Dv, [110, 10, 300]), window=window, sinks=sinks)
+
+
 def test_long_document_with_first_tokens(irs):
     """First tokens seen by thousands of queries: their gradients are sums over all of them."""
     _case(irs, *_inputs(1500, 8, 1, 64, 64, [1490, 10]), window=64, sinks=4)
