@@ -187,6 +187,13 @@ __device__ __forceinline__ uint64_t ffma2(uint64_t a, uint64_t b, uint64_t c) {
   return r;
 }
 
+// a + b on both halves
+__device__ __forceinline__ uint64_t fadd2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 // ---------------------------------------------------------------------------------
 // 16-byte cp.async (zero-fills the destination when src_bytes == 0)
 // ---------------------------------------------------------------------------------

@@ -11,9 +11,9 @@
 // 192), four times the cost of the two products.
 //
 // * dq (also D): rows of a product are the query heads of 128 / G queries, as in the forward.
-//   S = Q K^T and dP = dO V^T for a block of keys; two warpgroups (half the keys each, one
-//   row a thread) form dS and leave it in TMEM as bf16, the first operand of dQ += dS K (K
-//   read MN-major). S and dP are read out at once, so the next block's products run
+//   S = Q K^T and dP = dO V^T for a block of 96 keys; three warpgroups (32 keys each, one row
+//   a thread) form dS and leave it in TMEM as bf16, the first operand of dQ += dS K (K read
+//   MN-major). S and dP are read out at once, so the next block's products run
 //   meanwhile. Four helper warps form D for the next item and store the last item's dq: done
 //   by the score warps these took 13,000 of an item's 34,000 cycles (192/128, window 512).
 // * dk, dv: rows are 128 keys, columns the rows (query, head) that see them, 64 at a time:
@@ -38,7 +38,7 @@ constexpr int kBlk = 128;               // keys a tile (dk, dv)
 constexpr int kCols = 64;               // (query, head) rows a block (dk, dv)
 constexpr uint32_t kAtom = 128 * 128;   // 128 rows x 64 bf16
 constexpr uint32_t kAtom64 = 64 * 128;  // 64 rows x 64 bf16
-constexpr int kDqThreads = 448;         // warps 0-7: score warps; 8: TMA; 9: MMA; 10-13: helpers
+constexpr int kDqThreads = 576;         // warps 0-11: score warps; 12: TMA; 13: MMA; 14-17: helpers
 constexpr int kBwdThreads = 320;        // warps 0-7: score warps; 8: TMA; 9: MMA
 
 __device__ __forceinline__ void wait_landed(uint64_t* bar, uint32_t parity) {
@@ -72,17 +72,17 @@ template <int DQK, int DV>
 struct DqCfg {
   static constexpr int QA = DQK / 64, VA = DV / 64;
   static constexpr uint32_t q_bytes = QA * kAtom, do_bytes = VA * kAtom;
-  // Keys a block, stages of values: what fits beside a tile's queries and dout with three
-  // stages of keys (a block's keys stay until its dS K, two blocks' products later).
+  // Three stages of keys (a block's keys stay until its dS K, two blocks' products later) and as
+  // many of values as fit beside a tile's queries and dout.
   static constexpr bool fits(int blk, int vs) {
-    return q_bytes + do_bytes + (3 * QA + vs * VA) * blk * 128 <= 214u * 1024u;
+    return q_bytes + do_bytes + (3 * QA + vs * VA) * blk * 128 <= 212u * 1024u;
   }
-  static constexpr int BLK = fits(128, 2) ? 128 : 96;
+  static constexpr int BLK = 96;                                // a piece of 32 keys for each group of score warps
   static constexpr int KS = 3, VS = fits(BLK, 2) ? 2 : 1;
   static constexpr uint32_t kv_atom = BLK * 128, k_bytes = QA * kv_atom, v_bytes = VA * kv_atom;
   static constexpr uint32_t do_off = q_bytes, k_off = q_bytes + do_bytes, v_off = k_off + KS * k_bytes;
   static constexpr uint32_t row_off = v_off + VS * v_bytes;     // [2][128] of an item's rows: D, lse (base 2), window, document
-  static constexpr uint32_t hdr_off = row_off + 2 * 128 * 16;   // [2][8] of an item: see DqHead
+  static constexpr uint32_t hdr_off = row_off + 2 * 128 * 16;   // [2][8] of an item: range and borders
   static constexpr uint32_t plan_off = hdr_off + 2 * 32;        // [2][4] its blocks, for the MMA warp
   static constexpr uint32_t bar_off = plan_off + 2 * 16;
   static constexpr uint32_t cu_off = bar_off + 24 * 8 + 16;
@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
   constexpr int KS = C::KS, VS = C::VS, BLK = C::BLK;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  float4* rows = reinterpret_cast<float4*>(smem + C::row_off);
+  volatile float* rows = reinterpret_cast<volatile float*>(smem + C::row_off);
   volatile int* head = reinterpret_cast<volatile int*>(smem + C::hdr_off);
   volatile int* plan = reinterpret_cast<volatile int*>(smem + C::plan_off);
   uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::bar_off);
@@ -154,16 +154,16 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     for (int i = 0; i < KS; ++i) { mbar_init(&k_full[i], 1); mbar_init(&k_empty[i], 1); }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&v_full[i], 1); mbar_init(&v_empty[i], 1);
-      mbar_init(&d_full[i], 4); mbar_init(&d_empty[i], 8);
+      mbar_init(&d_full[i], 4); mbar_init(&d_empty[i], 12);
     }
-    mbar_init(sp_full, 1); mbar_init(sp_empty, 8);
-    mbar_init(ds_full, 8); mbar_init(ds_empty, 1);
+    mbar_init(sp_full, 1); mbar_init(sp_empty, 12);
+    mbar_init(ds_full, 12); mbar_init(ds_empty, 1);
     mbar_init(dq_full, 1); mbar_init(dq_empty, 4);
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 9) {
+  if (warp == 13) {
     tmem_alloc(tslot, 512);
     tmem_relinquish();
   }
@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
   const uint32_t tbase = *tslot;
   const int items = tiles * a.Hkv;
 
-  if (warp == 8) {
+  if (warp == 12) {
     // ---------------- TMA producer ----------------
     if (lane == 0) {
       tma_prefetch_map(&tm_q);
@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
         for (uint32_t i = nv > VS ? nv - VS : 0; i < nv; ++i) wait_landed(&v_full[i % VS], (i / VS) & 1);
       }
     }
-  } else if (warp == 9) {
+  } else if (warp == 13) {
     // ---------------- MMA issuer (the whole warp; one elected lane issues) ----------------
     constexpr uint32_t DQ_IDESC = idesc_bf16(128, DQK, false, true);
     const uint32_t sb = smem_u32(smem), tb = (uint32_t)uniform((int)tbase);
@@ -280,10 +280,13 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     umma_commit_warp(drain);
     wait_landed(drain, 0);
     __syncwarp();
-  } else if (warp >= 10) {
+  } else if (warp >= 14) {
     // ---------------- helpers: the next item's D, lse and borders; the last item's dq ----------------
-    constexpr int LR = DV / 8, RW = 32 / LR, U = 8;   // lanes a row; rows a step; steps in flight together (32 rows a warp)
+    constexpr int LR = DV / 8, RW = 32 / LR, U = 8;   // lanes a row; rows a step; steps in flight together
     const uint32_t lanes = tmem_lane_base(warp);
+    const int rb = (warp - 14) * 32;                  // D: the warp's rows
+    const int orq = (rb + lane) / a.G;                // the lane's own one
+    const int orow = orq * a.Hq + (rb + lane) - orq * a.G;
     uint32_t ni = 0;
     int prev = -1;
     for (int item = blockIdx.x;; item += gridDim.x, ++ni) {
@@ -292,7 +295,57 @@ __global__ void __launch_bounds__(kDqThreads, 1)
         const uint32_t slot = ni & 1;
         if (ni >= 2 && !__all_sync(0xffffffffu, mbar_wait(&d_empty[slot], (ni / 2 - 1) & 1, abort_flag, a.err))) break;
         const DqItem m = dq_item<BLK>(a, cu, tile * qt, qt);
-        if (warp == 10 && lane == 0) {
+        const int64_t base = (int64_t)m.t0 * a.Hq + g * a.G;
+        const int t = m.t0 + orq;
+        const bool in = orq < qt && t < a.T;
+        const int mine = in ? orow : -1;
+        const float l = in ? a.lse_in[base + orow] : 0.f;
+        volatile float* dst = rows + slot * 512;
+        // eight steps' loads in flight; their sums over a row's lanes are folded together, each
+        // exchange halving what a lane still holds (8 shuffles for 8 steps)
+#pragma unroll 1
+        for (int r0 = 0; r0 < 32; r0 += U * RW) {
+          uint4 u[U], w[U];
+#pragma unroll
+          for (int i = 0; i < U; ++i) {
+            const int o = __shfl_sync(0xffffffffu, mine, r0 + i * RW + lane / LR);
+            u[i] = w[i] = make_uint4(0, 0, 0, 0);
+            if (o >= 0) {
+              u[i] = *reinterpret_cast<const uint4*>(a.dout + (base + o) * DV + 8 * (lane % LR));
+              w[i] = *reinterpret_cast<const uint4*>(a.out + (base + o) * DV + 8 * (lane % LR));
+            }
+          }
+          float s[U];
+#pragma unroll
+          for (int i = 0; i < U; ++i) {
+            const uint32_t uu[4] = {u[i].x, u[i].y, u[i].z, u[i].w}, ww[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+            float x = 0.f, y = 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              x = fmaf(__uint_as_float(uu[k] << 16), __uint_as_float(ww[k] << 16), x);
+              y = fmaf(__uint_as_float(uu[k] & 0xffff0000u), __uint_as_float(ww[k] & 0xffff0000u), y);
+            }
+            s[i] = x + y;
+          }
+          int step = 0;
+#pragma unroll
+          for (int n = U / 2, o = LR / 2; n > 0; n >>= 1, o >>= 1) {
+            const bool hi = lane & o;
+#pragma unroll
+            for (int i = 0; i < n; ++i) {
+              const float keep = hi ? s[i + n] : s[i], send = hi ? s[i] : s[i + n];
+              s[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+            }
+            if (hi) step += n;
+          }
+          if (LR == 16) s[0] += __shfl_xor_sync(0xffffffffu, s[0], 1);   // two lanes hold the same step
+          dst[4 * (rb + r0 + step * RW + lane / LR)] = s[0];
+        }
+        const int ds = window_doc(cu, a.ndocs, a.T, min(t, a.T - 1)).start;
+        dst[4 * (rb + lane) + 1] = l * kLog2e;
+        dst[4 * (rb + lane) + 2] = __int_as_float(max(ds, t - a.window + 1));
+        dst[4 * (rb + lane) + 3] = __int_as_float(ds);
+        if (warp == 14 && lane == 0) {
           volatile int* h = head + 8 * slot;
           h[0] = m.klo;
           h[1] = m.ns;
@@ -301,44 +354,8 @@ __global__ void __launch_bounds__(kDqThreads, 1)
           h[4] = m.ds0;
           h[5] = m.last;
         }
-#pragma unroll 1
-        for (int r0 = (warp - 10) * 32; r0 < (warp - 10) * 32 + 32; r0 += U * RW) {
-        uint4 u[U], w[U];
-        int64_t row[U];
-        float l[U];
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-          const int r = r0 + i * RW + lane / LR, rq = r / a.G, t = m.t0 + rq;
-          row[i] = rq < qt && t < a.T ? (int64_t)t * a.Hq + g * a.G + (r - rq * a.G) : -1;
-          u[i] = w[i] = make_uint4(0, 0, 0, 0);
-          l[i] = 0.f;
-          if (row[i] >= 0) {
-            u[i] = *reinterpret_cast<const uint4*>(a.dout + row[i] * DV + 8 * (lane % LR));
-            w[i] = *reinterpret_cast<const uint4*>(a.out + row[i] * DV + 8 * (lane % LR));
-            if (lane % LR == 0) l[i] = a.lse_in[row[i]];
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-          const uint32_t uu[4] = {u[i].x, u[i].y, u[i].z, u[i].w}, ww[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-          float s = 0.f, s1 = 0.f;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            s = fmaf(__uint_as_float(uu[k] << 16), __uint_as_float(ww[k] << 16), s);
-            s1 = fmaf(__uint_as_float(uu[k] & 0xffff0000u), __uint_as_float(ww[k] & 0xffff0000u), s1);
-          }
-          s += s1;
-#pragma unroll
-          for (int o = LR / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-          if (lane % LR == 0) {
-            const int r = r0 + i * RW + lane / LR, t = min(m.t0 + r / a.G, a.T - 1);
-            const int ds = window_doc(cu, a.ndocs, a.T, t).start;
-            rows[slot * 128 + r] = make_float4(s, l[i] * kLog2e, __int_as_float(max(ds, t - a.window + 1)), __int_as_float(ds));
-            if (row[i] >= 0) a.delta[row[i]] = s;
-          }
-        }
-        }
         __syncwarp();
+        if (in) a.delta[base + orow] = dst[4 * (rb + lane)];
         if (lane == 0) mbar_arrive(&d_full[slot]);
       }
       if (prev >= 0) {
@@ -377,8 +394,8 @@ __global__ void __launch_bounds__(kDqThreads, 1)
       prev = item;
     }
   } else {
-    // ---------------- score warps: row = TMEM lane, half of the block's keys each ----------------
-    const int half = warp >> 2;
+    // ---------------- score warps: row = TMEM lane, a piece of 32 keys each ----------------
+    const int k32 = (warp >> 2) * 32;
     const int r = (warp & 3) * 32 + lane;
     const int rq = r / a.G;
     const uint32_t lanes = tmem_lane_base(warp);
@@ -387,7 +404,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     for (int item = blockIdx.x; item < items && alive; item += gridDim.x, ++ni) {
       const uint32_t slot = ni & 1;
       if (!__all_sync(0xffffffffu, mbar_wait(&d_full[slot], (ni / 2) & 1, abort_flag, a.err))) break;
-      const float4 mine = rows[slot * 128 + r];
+      const float4 mine = *reinterpret_cast<const float4*>(smem + C::row_off + (slot * 128 + r) * 16);
       const volatile int* hd = head + 8 * slot;
       DqItem m;
       m.klo = hd[0];
@@ -405,68 +422,54 @@ __global__ void __launch_bounds__(kDqThreads, 1)
       const int early = min(ds + a.sinks, lo);
       const bool live = rq < qt && t < a.T;
       for (int j = 0; j < m.nbt; ++j, ++nsp) {
-        const int kb = dq_key<BLK>(m, j), cols = dq_cols<BLK>(m, j);
+        const int kb = dq_key<BLK>(m, j) + k32, cols = dq_cols<BLK>(m, j);
+        const bool any = k32 < cols;                       // the block reaches this piece
         const bool sink_blk = j < m.sb;
-        const int pieces = cols >> 5, c0 = half * (cols >> 1);   // 16-key pieces of this half, its first key
-        uint64_t seen = ~0ull;
-        const bool border = sink_blk || kb < lo_last || kb + cols - 1 > m.t0;
+        const bool border = sink_blk || kb < lo_last || kb + 31 > m.t0;
+        uint32_t seen = ~0u;
         if (border) {
-          const int k0 = kb + c0;
-          seen = bit_range(lo - k0, t + 1 - k0) | bit_range(ds - k0, early - k0);
-          if (sink_blk) seen = ds == m.ds0 ? bit_range(0, m.ns - BLK * j - c0) : 0ull;
-          if (!live) seen = 0ull;
+          seen = bit_range32(lo - kb, t + 1 - kb) | bit_range32(ds - kb, early - kb);
+          if (sink_blk) seen = ds == m.ds0 ? bit_range32(0, m.ns - BLK * j - k32) : 0u;
+          if (!live) seen = 0u;
         }
         if (!__all_sync(0xffffffffu, mbar_wait(sp_full, nsp & 1, abort_flag, a.err))) { alive = false; break; }
         tc_fence_after();
-        // three pieces (96 keys a block) are read at once, so that the next block's products can start
+        float s[32], p[32];
+        if (any) {
+          tmem_ld32(tbase + C::S0 + lanes + k32, s);
+          tmem_ld32(tbase + C::P0 + lanes + k32, p);
+          tmem_ld_wait_regs(s);
+          tmem_ld_wait_regs(p);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sp_empty);   // the next block's products can start
+        float w[16];
+        if (any) {
+          const uint64_t sc2 = pack2(a.scale_log2, a.scale_log2), l22 = pack2(-l2, -l2), d2 = pack2(-D, -D);
 #pragma unroll
-        for (int c1 = 0; c1 < BLK / 32; c1 += 3) {
-          float s[3][16], p[3][16];
-#pragma unroll
-          for (int c = 0; c < 3; ++c)
-            if (c1 + c < pieces) {
-              tmem_ld16(tbase + C::S0 + lanes + c0 + 16 * (c1 + c), s[c]);
-              tmem_ld16(tbase + C::P0 + lanes + c0 + 16 * (c1 + c), p[c]);
-            }
-#pragma unroll
-          for (int c = 0; c < 3; ++c) {
-            tmem_ld_wait_regs(s[c]);
-            tmem_ld_wait_regs(p[c]);
+          for (int i = 0; i < 32; i += 2) {
+            const float2 e = unpack2(ffma2(pack2(s[i], s[i + 1]), sc2, l22));
+            const float2 y = unpack2(fadd2(pack2(p[i], p[i + 1]), d2));
+            s[i] = ex2_approx(e.x) * y.x;
+            s[i + 1] = ex2_approx(e.y) * y.y;
           }
-          if (c1 + 3 >= BLK / 32) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(sp_empty);
+          if (border) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) s[i] = (seen >> i) & 1u ? s[i] : 0.f;
           }
 #pragma unroll
-          for (int c = 0; c < 3; ++c) {
-            if (c1 + c < pieces) {
-#pragma unroll
-              for (int i = 0; i < 16; ++i) s[c][i] = ex2_approx(fmaf(s[c][i], a.scale_log2, -l2)) * (p[c][i] - D);
-              if (border) {
-                const uint32_t bits = (uint32_t)(seen >> (16 * (c1 + c)));
-#pragma unroll
-                for (int i = 0; i < 16; ++i) s[c][i] = (bits >> i) & 1u ? s[c][i] : 0.f;
-              }
-            }
-          }
-          // dS of the block before must have been read by its product before it is replaced
-          if (c1 == 0 && nsp > 0 && !__all_sync(0xffffffffu, mbar_wait(ds_empty, (nsp - 1) & 1, abort_flag, a.err))) alive = false;
-#pragma unroll
-          for (int c = 0; c < 3; ++c) {
-            if (c1 + c < pieces) {
-              float w[8];
-#pragma unroll
-              for (int i = 0; i < 16; i += 2) {
-                const __nv_bfloat162 b = __floats2bfloat162_rn(s[c][i], s[c][i + 1]);
-                w[i >> 1] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&b));
-              }
-              tmem_st8(tbase + C::DS0 + lanes + ((c0 + 16 * (c1 + c)) >> 1), w);
-            }
+          for (int i = 0; i < 32; i += 2) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(s[i], s[i + 1]);
+            w[i >> 1] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&b));
           }
         }
-        if (!alive) break;
-        tmem_st_wait();
+        // dS of the block before must have been read by its product before it is replaced
+        if (nsp > 0 && !__all_sync(0xffffffffu, mbar_wait(ds_empty, (nsp - 1) & 1, abort_flag, a.err))) { alive = false; break; }
+        if (any) {
+          tmem_st16(tbase + C::DS0 + lanes + (k32 >> 1), w);
+          tmem_st_wait();
+        }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(ds_full);
@@ -475,7 +478,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == 13) {
     tc_fence_after();
     tmem_dealloc(tbase, 512);
   }

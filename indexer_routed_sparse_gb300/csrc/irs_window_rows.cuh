@@ -17,6 +17,13 @@ __device__ __forceinline__ uint64_t bit_range(int from, int to) {
   return (~0ull >> (64 - (to - from))) << from;
 }
 
+__device__ __forceinline__ uint32_t bit_range32(int from, int to) {
+  from = max(from, 0);
+  to = min(to, 32);
+  if (from >= to) return 0u;
+  return (~0u >> (32 - (to - from))) << from;
+}
+
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
