@@ -11,8 +11,8 @@
 // 192), four times the cost of the two products.
 //
 // * dq (also D): rows of a product are the query heads of 128 / G queries, as in the forward.
-//   S = Q K^T and dP = dO V^T for a block of 96 keys; three warpgroups (32 keys each, one row
-//   a thread) form dS and leave it in TMEM as bf16, the first operand of dQ += dS K (K read
+//   S = Q K^T and dP = dO V^T for a block of 96 keys; two warpgroups (48 keys each, one row a
+//   thread) form dS and leave it in TMEM as bf16, the first operand of dQ += dS K (K read
 //   MN-major). S and dP are read out at once, so the next block's products run
 //   meanwhile. Four helper warps form D for the next item and store the last item's dq: done
 //   by the score warps these took 13,000 of an item's 34,000 cycles (192/128, window 512).
@@ -38,7 +38,7 @@ constexpr int kBlk = 128;               // keys a tile (dk, dv)
 constexpr int kCols = 64;               // (query, head) rows a block (dk, dv)
 constexpr uint32_t kAtom = 128 * 128;   // 128 rows x 64 bf16
 constexpr uint32_t kAtom64 = 64 * 128;  // 64 rows x 64 bf16
-constexpr int kDqThreads = 576;         // warps 0-11: score warps; 12: TMA; 13: MMA; 14-17: helpers
+constexpr int kDqThreads = 448;         // warps 0-7: score warps; 8: TMA; 9: MMA; 10-13: helpers
 constexpr int kBwdThreads = 320;        // warps 0-7: score warps; 8: TMA; 9: MMA
 
 __device__ __forceinline__ void wait_landed(uint64_t* bar, uint32_t parity) {
@@ -77,7 +77,7 @@ struct DqCfg {
   static constexpr bool fits(int blk, int vs) {
     return q_bytes + do_bytes + (3 * QA + vs * VA) * blk * 128 <= 212u * 1024u;
   }
-  static constexpr int BLK = 96;                                // a piece of 32 keys for each group of score warps
+  static constexpr int BLK = 96;                                // three pieces of 16 keys for each score warp
   static constexpr int KS = 3, VS = fits(BLK, 2) ? 2 : 1;
   static constexpr uint32_t kv_atom = BLK * 128, k_bytes = QA * kv_atom, v_bytes = VA * kv_atom;
   static constexpr uint32_t do_off = q_bytes, k_off = q_bytes + do_bytes, v_off = k_off + KS * k_bytes;
@@ -154,16 +154,16 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     for (int i = 0; i < KS; ++i) { mbar_init(&k_full[i], 1); mbar_init(&k_empty[i], 1); }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&v_full[i], 1); mbar_init(&v_empty[i], 1);
-      mbar_init(&d_full[i], 4); mbar_init(&d_empty[i], 12);
+      mbar_init(&d_full[i], 4); mbar_init(&d_empty[i], 8);
     }
-    mbar_init(sp_full, 1); mbar_init(sp_empty, 12);
-    mbar_init(ds_full, 12); mbar_init(ds_empty, 1);
+    mbar_init(sp_full, 1); mbar_init(sp_empty, 8);
+    mbar_init(ds_full, 8); mbar_init(ds_empty, 1);
     mbar_init(dq_full, 1); mbar_init(dq_empty, 4);
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 13) {
+  if (warp == 9) {
     tmem_alloc(tslot, 512);
     tmem_relinquish();
   }
@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
   const uint32_t tbase = *tslot;
   const int items = tiles * a.Hkv;
 
-  if (warp == 12) {
+  if (warp == 8) {
     // ---------------- TMA producer ----------------
     if (lane == 0) {
       tma_prefetch_map(&tm_q);
@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
         for (uint32_t i = nv > VS ? nv - VS : 0; i < nv; ++i) wait_landed(&v_full[i % VS], (i / VS) & 1);
       }
     }
-  } else if (warp == 13) {
+  } else if (warp == 9) {
     // ---------------- MMA issuer (the whole warp; one elected lane issues) ----------------
     constexpr uint32_t DQ_IDESC = idesc_bf16(128, DQK, false, true);
     const uint32_t sb = smem_u32(smem), tb = (uint32_t)uniform((int)tbase);
@@ -280,11 +280,11 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     umma_commit_warp(drain);
     wait_landed(drain, 0);
     __syncwarp();
-  } else if (warp >= 14) {
+  } else if (warp >= 10) {
     // ---------------- helpers: the next item's D, lse and borders; the last item's dq ----------------
     constexpr int LR = DV / 8, RW = 32 / LR, U = 8;   // lanes a row; rows a step; steps in flight together
     const uint32_t lanes = tmem_lane_base(warp);
-    const int rb = (warp - 14) * 32;                  // D: the warp's rows
+    const int rb = (warp - 10) * 32;                  // D: the warp's rows
     const int orq = (rb + lane) / a.G;                // the lane's own one
     const int orow = orq * a.Hq + (rb + lane) - orq * a.G;
     uint32_t ni = 0;
@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
         dst[4 * (rb + lane) + 1] = l * kLog2e;
         dst[4 * (rb + lane) + 2] = __int_as_float(max(ds, t - a.window + 1));
         dst[4 * (rb + lane) + 3] = __int_as_float(ds);
-        if (warp == 14 && lane == 0) {
+        if (warp == 10 && lane == 0) {
           volatile int* h = head + 8 * slot;
           h[0] = m.klo;
           h[1] = m.ns;
@@ -394,8 +394,8 @@ __global__ void __launch_bounds__(kDqThreads, 1)
       prev = item;
     }
   } else {
-    // ---------------- score warps: row = TMEM lane, a piece of 32 keys each ----------------
-    const int k32 = (warp >> 2) * 32;
+    // ---------------- score warps: row = TMEM lane, half of the block's keys each ----------------
+    const int half = warp >> 2;
     const int r = (warp & 3) * 32 + lane;
     const int rq = r / a.G;
     const uint32_t lanes = tmem_lane_base(warp);
@@ -422,54 +422,59 @@ __global__ void __launch_bounds__(kDqThreads, 1)
       const int early = min(ds + a.sinks, lo);
       const bool live = rq < qt && t < a.T;
       for (int j = 0; j < m.nbt; ++j, ++nsp) {
-        const int kb = dq_key<BLK>(m, j) + k32, cols = dq_cols<BLK>(m, j);
-        const bool any = k32 < cols;                       // the block reaches this piece
+        const int cols = dq_cols<BLK>(m, j), pieces = cols >> 5, c0 = half * (cols >> 1);   // 16-key pieces, first key
+        const int kb = dq_key<BLK>(m, j) + c0;
         const bool sink_blk = j < m.sb;
-        const bool border = sink_blk || kb < lo_last || kb + 31 > m.t0;
-        uint32_t seen = ~0u;
+        const bool border = sink_blk || kb < lo_last || kb + (cols >> 1) - 1 > m.t0;
+        uint64_t seen = ~0ull;
         if (border) {
-          seen = bit_range32(lo - kb, t + 1 - kb) | bit_range32(ds - kb, early - kb);
-          if (sink_blk) seen = ds == m.ds0 ? bit_range32(0, m.ns - BLK * j - k32) : 0u;
-          if (!live) seen = 0u;
+          seen = bit_range(lo - kb, t + 1 - kb) | bit_range(ds - kb, early - kb);
+          if (sink_blk) seen = ds == m.ds0 ? bit_range(0, m.ns - BLK * j - c0) : 0ull;
+          if (!live) seen = 0ull;
         }
         if (!__all_sync(0xffffffffu, mbar_wait(sp_full, nsp & 1, abort_flag, a.err))) { alive = false; break; }
         tc_fence_after();
-        float s[32], p[32];
-        if (any) {
-          tmem_ld32(tbase + C::S0 + lanes + k32, s);
-          tmem_ld32(tbase + C::P0 + lanes + k32, p);
-          tmem_ld_wait_regs(s);
-          tmem_ld_wait_regs(p);
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(sp_empty);   // the next block's products can start
-        float w[16];
-        if (any) {
-          const uint64_t sc2 = pack2(a.scale_log2, a.scale_log2), l22 = pack2(-l2, -l2), d2 = pack2(-D, -D);
+        // 16 keys at a time: a spilled register costs a trip to L2 (the tiles leave L1 nothing)
+        float w[3][8];
+        const uint64_t sc2 = pack2(a.scale_log2, a.scale_log2), l22 = pack2(-l2, -l2), d2 = pack2(-D, -D);
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            const float2 e = unpack2(ffma2(pack2(s[i], s[i + 1]), sc2, l22));
-            const float2 y = unpack2(fadd2(pack2(p[i], p[i + 1]), d2));
-            s[i] = ex2_approx(e.x) * y.x;
-            s[i + 1] = ex2_approx(e.y) * y.y;
-          }
-          if (border) {
+        for (int c = 0; c < 3; ++c) {
+          if (c < pieces) {
+            float s[16], p[16];
+            tmem_ld16(tbase + C::S0 + lanes + c0 + 16 * c, s);
+            tmem_ld16(tbase + C::P0 + lanes + c0 + 16 * c, p);
+            tmem_ld_wait_regs(s);
+            tmem_ld_wait_regs(p);
+            if (c + 1 == pieces) {   // the next block's products can start
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(sp_empty);
+            }
 #pragma unroll
-            for (int i = 0; i < 32; ++i) s[i] = (seen >> i) & 1u ? s[i] : 0.f;
-          }
+            for (int i = 0; i < 16; i += 2) {
+              const float2 e = unpack2(ffma2(pack2(s[i], s[i + 1]), sc2, l22));
+              const float2 y = unpack2(fadd2(pack2(p[i], p[i + 1]), d2));
+              s[i] = ex2_approx(e.x) * y.x;
+              s[i + 1] = ex2_approx(e.y) * y.y;
+            }
+            if (border) {
+              const uint32_t bits = (uint32_t)(seen >> (16 * c));
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            const __nv_bfloat162 b = __floats2bfloat162_rn(s[i], s[i + 1]);
-            w[i >> 1] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&b));
+              for (int i = 0; i < 16; ++i) s[i] = (bits >> i) & 1u ? s[i] : 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+              const __nv_bfloat162 b = __floats2bfloat162_rn(s[i], s[i + 1]);
+              w[c][i >> 1] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&b));
+            }
           }
         }
         // dS of the block before must have been read by its product before it is replaced
         if (nsp > 0 && !__all_sync(0xffffffffu, mbar_wait(ds_empty, (nsp - 1) & 1, abort_flag, a.err))) { alive = false; break; }
-        if (any) {
-          tmem_st16(tbase + C::DS0 + lanes + (k32 >> 1), w);
-          tmem_st_wait();
-        }
+#pragma unroll
+        for (int c = 0; c < 3; ++c)
+          if (c < pieces) tmem_st8(tbase + C::DS0 + lanes + ((c0 + 16 * c) >> 1), w[c]);
+        tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(ds_full);
@@ -478,7 +483,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 13) {
+  if (warp == 9) {
     tc_fence_after();
     tmem_dealloc(tbase, 512);
   }
