@@ -1106,8 +1106,8 @@ irs_status irs_window_gqa_attn_fwd(const void* q, int64_t q_stride_t, int64_t q_
   if (!window_has_maps(a)) return launch_status(irs::launch_window_fwd_rows(a, st), "launching window attention (rows)");
   irs::WinMaps m;
   if ((s = make_packed_map(&m.q, q, Dqk, Hq, T, q_stride_h, q_stride_t, a.G, 128 / a.G)) != IRS_OK) return s;
-  if ((s = make_packed_map(&m.k, k, Dqk, Hkv, T, k_stride_h, k_stride_t, 1, irs::window_fwd_block(Dqk, Dv))) != IRS_OK) return s;
-  if ((s = make_packed_map(&m.v, v, Dv, Hkv, T, v_stride_h, v_stride_t, 1, irs::window_fwd_block(Dqk, Dv))) != IRS_OK) return s;
+  if ((s = make_packed_map(&m.k, k, Dqk, Hkv, T, k_stride_h, k_stride_t, 1, irs::window_fwd_block())) != IRS_OK) return s;
+  if ((s = make_packed_map(&m.v, v, Dv, Hkv, T, v_stride_h, v_stride_t, 1, irs::window_fwd_block())) != IRS_OK) return s;
   std::lock_guard<std::mutex> lk(g_dev_mu);
   return launch_status(irs::launch_window_fwd_tc(m, a, dev->num_sms, dev->window_fwd_configured, st),
                        "launching window attention");
@@ -1154,7 +1154,7 @@ irs_status irs_window_gqa_attn_bwd(const void* q, int64_t q_stride_t, int64_t q_
   if ((s = make_packed_map(&m.dout2, dout, Dv, Hq, T, Dv, (int64_t)Hq * Dv, hc, 64 / hc)) != IRS_OK) return s;
   if ((s = make_packed_map(&m.k, k, Dqk, Hkv, T, k_stride_h, k_stride_t, 1, 128)) != IRS_OK) return s;
   if ((s = make_packed_map(&m.v, v, Dv, Hkv, T, v_stride_h, v_stride_t, 1, 128)) != IRS_OK) return s;
-  const int blk = irs::window_dq_block(Dqk, Dv);
+  const int blk = irs::window_dq_block();
   if ((s = make_packed_map(&m.kq, k, Dqk, Hkv, T, k_stride_h, k_stride_t, 1, blk)) != IRS_OK) return s;
   if ((s = make_packed_map(&m.vq, v, Dv, Hkv, T, v_stride_h, v_stride_t, 1, blk)) != IRS_OK) return s;
   std::lock_guard<std::mutex> lk(g_dev_mu);

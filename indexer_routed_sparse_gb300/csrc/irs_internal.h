@@ -259,7 +259,7 @@ size_t window_bwd_workspace_bytes(int T, int Hq, int Hkv, int Dqk, int Dv, int n
 struct WinMaps {
   CUtensorMap q, k, v;
 };
-int window_fwd_block(int Dqk, int Dv);   // keys a block of the forward: the box of its k and v maps
+int window_fwd_block();   // keys a block of the forward: the box of its k and v maps
 constexpr int kWindowKinds = 6;   // kernels, by head dims
 // configured[kWindowKinds]: whose shared-memory limit has been raised on this device
 cudaError_t launch_window_fwd_tc(const WinMaps& m, const WinArgs& a, int num_sms, bool* configured, cudaStream_t stream);
@@ -282,7 +282,7 @@ struct WinSinks {
 struct WinBwdMaps {
   CUtensorMap q, dout, q2, dout2, k, v, kq, vq;
 };
-int window_dq_block(int Dqk, int Dv);
+int window_dq_block();
 size_t window_bwd_layout(uint8_t* ws, int T, int Hq, int Hkv, int Dqk, int Dv, int ndocs, int window, int sinks, WinSinks* s);
 cudaError_t launch_window_bwd_tc(const WinBwdMaps& m, const WinArgs& a, const WinSinks& sk, int num_sms, bool* configured,
                                  cudaStream_t stream);

@@ -467,6 +467,16 @@ __device__ __forceinline__ void store_rows32(const uint32_t (&w)[16], void* dst,
   }
 }
 
+// One float of shared memory by its 32-bit address (half the registers of a pointer).
+__device__ __forceinline__ void st_shared(uint32_t addr, float x) {
+  asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(x) : "memory");
+}
+__device__ __forceinline__ float ld_shared(uint32_t addr) {
+  float x;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(addr) : "memory");
+  return x;
+}
+
 // Byte offset of element (row, col) of a SW128 atom-tiled operand whose rows are 128 B
 // per atom (col = element index along the contiguous dimension, bf16).
 __host__ __device__ __forceinline__ uint32_t sw128_offset(uint32_t row, uint32_t col, uint32_t rows_per_atom) {

@@ -920,16 +920,7 @@ __global__ void __launch_bounds__(128) window_join_kernel(WinArgs a, WinSinks sk
 }  // namespace
 
 // Keys a block of the dq kernel: the box of its k and v maps.
-int window_dq_block(int Dqk, int Dv) {
-  switch ((Dqk / 64 - 1) * 2 + (Dv / 64 - 1)) {
-    case 0: return DqCfg<64, 64>::BLK;
-    case 1: return DqCfg<64, 128>::BLK;
-    case 2: return DqCfg<128, 64>::BLK;
-    case 3: return DqCfg<128, 128>::BLK;
-    case 4: return DqCfg<192, 64>::BLK;
-    default: return DqCfg<192, 128>::BLK;
-  }
-}
+int window_dq_block() { return DqCfg<128, 128>::BLK; }
 
 namespace {
 

@@ -45,9 +45,9 @@ template <int DQK, int DV>
 struct FwdCfg {
   static constexpr int QA = DQK / 64, VA = DV / 64;
   static constexpr uint32_t q_bytes = QA * kAtom;          // one tile's queries
-  // Keys a block: 128 where two stages of keys and of values fit beside the queries, else 96
-  // (192/128). One stage of 128 values exposed its load every block: 2.45 ms for 65536 tokens.
-  static constexpr int BLK = 2 * q_bytes + 2 * (QA + VA) * kAtom <= 224u * 1024u ? 128 : 96;
+  // Keys a block: two stages of 96 keys and values fit beside two tiles' queries at every head
+  // dim; 128 would leave 192/128 one stage of values, and a softmax thread too few registers.
+  static constexpr int BLK = 96;
   static constexpr uint32_t kv_atom = BLK * 128;           // BLK rows x 64 bf16
   static constexpr uint32_t k_bytes = QA * kv_atom, v_bytes = VA * kv_atom;
   static constexpr int KS = 2, VS = 2;
@@ -306,8 +306,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const int rq = r / a.G, rh = r - rq * a.G;            // its query and head
     const uint32_t s_addr = tbase + C::S0 + 128 * x + tmem_lane_base(warp);
     const uint32_t o_addr = tbase + C::O0 + x * DV + tmem_lane_base(warp);
-    volatile float* mine = reinterpret_cast<volatile float*>(smem + C::x_off) + (x * 2 + half) * kRows + r;
-    volatile float* other = reinterpret_cast<volatile float*>(smem + C::x_off) + (x * 2 + (half ^ 1)) * kRows + r;
+    const uint32_t mine = smem_u32(smem) + C::x_off + (uint32_t)((x * 2 + half) * kRows + r) * 4u;
+    const uint32_t other = smem_u32(smem) + C::x_off + (uint32_t)((x * 2 + (half ^ 1)) * kRows + r) * 4u;
     uint32_t nsf = 0, nof = 0;
     bool alive = true;
     for (int item = blockIdx.x; item < items && alive; item += gridDim.x) {
@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         float ln = 0.f;
         auto weights = [&]() {
           const float off = mx == -INFINITY ? 0.f : -mx;
-          float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f, big = 0.f;
+          float l0 = 0.f, l1 = 0.f, big = 0.f;
 #pragma unroll
           for (int c = 0; c < C::BLK / 32; ++c) {
             if (c < pieces) {
@@ -363,8 +363,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 const float p3 = ex2_approx(fmaf(v[i + 3], a.scale_log2, off));
                 l0 += p0;
                 l1 += p1;
-                l2 += p2;
-                l3 += p3;
+                l0 += p2;
+                l1 += p3;
                 big = fmaxf(fmaxf(big, p0), p1);
                 big = fmaxf(fmaxf(big, p2), p3);
                 const __nv_bfloat162 b0 = __floats2bfloat162_rn(p0, p1), b1 = __floats2bfloat162_rn(p2, p3);
@@ -373,11 +373,15 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
               }
             }
           }
-          ln = (l0 + l1) + (l2 + l3);
+          ln = l0 + l1;
           return big;
         };
         bool slow = !settled;
-        if (!slow) slow = named_bar_or(bar_id, 64, weights() > kRaise || !alive);
+        if (!slow) {
+          const float big = weights();
+          // a row that is none (its queries were never loaded) has no vote
+          slow = named_bar_or(bar_id, 64, (live && big > kRaise) || !alive);
+        }
         if (slow) {
           float top = -INFINITY;
           for (int c = 0; c < pieces; ++c) {
@@ -389,22 +393,22 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             for (int i = 0; i < 16; ++i) top = fmaxf(top, v[i]);
           }
           top *= a.scale_log2;
-          *mine = top;
+          st_shared(mine, top);
           alive = named_bar_and(bar_id, 64, alive);   // both halves leave together after a wait that gave up
-          const float nm = fmaxf(mx, fmaxf(top, *other));
+          const float nm = fmaxf(mx, fmaxf(top, ld_shared(other)));
           const float c = nm == -INFINITY ? 1.f : ex2_approx(mx - nm);
           mx = nm;
           l *= c;
           if (j > jf && alive) {
             // the scores' barrier also covers the products before them: O is complete so far
 #pragma unroll 1
-            for (int d = half * (DV / 2); d < (half + 1) * (DV / 2); d += 32) {
-              float o[32];
-              tmem_ld32(o_addr + d, o);
+            for (int d = half * (DV / 2); d < (half + 1) * (DV / 2); d += 16) {
+              float o[16];
+              tmem_ld16(o_addr + d, o);
               tmem_ld_wait_regs(o);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] *= c;
-              tmem_st32(o_addr + d, o);
+              for (int i = 0; i < 16; ++i) o[i] *= c;
+              tmem_st16(o_addr + d, o);
             }
           }
           weights();
@@ -423,26 +427,29 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       if (alive) alive = __all_sync(0xffffffffu, mbar_wait(&o_full[x], nof & 1, abort_flag, a.err));
       ++nof;
       tc_fence_after();
-      *mine = l;
+      st_shared(mine, l);
       alive = named_bar_and(bar_id, 64, alive);
       if (!alive) break;
-      l += *other;
+      l += ld_shared(other);
       const float inv = 1.f / l;
       const int h = g * a.G + rh;
       const int64_t row = (int64_t)t * a.Hq + h;
       float odd = fmaf(mx, 0.f, l * 0.f);                 // NaN where anything is not finite
 #pragma unroll 1
       for (int d = half * (DV / 2); d < (half + 1) * (DV / 2); d += 32) {
-        float o[32];
-        tmem_ld32(o_addr + d, o);
-        tmem_ld_wait_regs(o);
         uint32_t w[16];
 #pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-          odd = fmaf(o[i], 0.f, odd);
-          odd = fmaf(o[i + 1], 0.f, odd);
-          const __nv_bfloat162 b = __floats2bfloat162_rn(o[i] * inv, o[i + 1] * inv);
-          w[i >> 1] = *reinterpret_cast<const uint32_t*>(&b);
+        for (int e = 0; e < 2; ++e) {
+          float o[16];
+          tmem_ld16(o_addr + d + 16 * e, o);
+          tmem_ld_wait_regs(o);
+#pragma unroll
+          for (int i = 0; i < 16; i += 2) {
+            odd = fmaf(o[i], 0.f, odd);
+            odd = fmaf(o[i + 1], 0.f, odd);
+            const __nv_bfloat162 b = __floats2bfloat162_rn(o[i] * inv, o[i + 1] * inv);
+            w[8 * e + (i >> 1)] = *reinterpret_cast<const uint32_t*>(&b);
+          }
         }
         store_rows32(w, live ? a.out + row * DV + d : nullptr, lane);
       }
@@ -452,9 +459,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       if (half == 0 && live && a.lse != nullptr) a.lse[row] = fmaf(mx, 0.6931471805599453f, logf(l));
       // rows to do again: by the first half's warp, after both halves have stored
       if (named_bar_or(bar_id, 64, live && odd != 0.f)) {   // NaN compares unequal
-        *mine = odd;
+        st_shared(mine, odd);
         named_bar_sync(bar_id, 64);
-        unsigned again = __ballot_sync(0xffffffffu, live && half == 0 && (odd != 0.f || *other != 0.f));
+        unsigned again = __ballot_sync(0xffffffffu, live && half == 0 && (odd != 0.f || ld_shared(other) != 0.f));
         while (again) {
           const int src = __ffs((int)again) - 1;
           again &= again - 1;
@@ -474,11 +481,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 }  // namespace
 
 // Keys a block of the forward: the box of its k and v maps.
-int window_fwd_block(int Dqk, int Dv) { return Dqk == 192 && Dv == 128 ? FwdCfg<192, 128>::BLK : 128; }
+int window_fwd_block() { return FwdCfg<128, 128>::BLK; }
 
 namespace {
 
-static_assert(FwdCfg<192, 64>::BLK == 128 && FwdCfg<128, 128>::BLK == 128, "window_fwd_block");
+
 
 template <int DQK, int DV>
 cudaError_t launch_fwd(const WinMaps& m, const WinArgs& a, int num_sms, bool* configured, cudaStream_t stream) {
