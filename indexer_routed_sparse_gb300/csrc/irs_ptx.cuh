@@ -442,16 +442,14 @@ __device__ __forceinline__ void umma_commit(uint64_t* bar) {
                : "memory");
 }
 
-// Each lane holds 64 bytes (four 16-byte pieces, w) of its own row at dst (nullptr: not stored).
-// Four neighbouring lanes exchange pieces, so that a store instruction covers 64 contiguous
-// bytes of eight rows and not 16 of 32: an L1 line each costs a cycle.
-__device__ __forceinline__ void store_rows32(const uint32_t (&w)[16], void* dst, int lane) {
-  uint64_t base[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) base[k] = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(dst), (lane & ~3) + k);
+// Each lane holds 64 bytes (four 16-byte pieces, w) of its own row `rel` (-1: not stored), rows
+// `ld` elements apart from dst. Four neighbouring lanes exchange pieces, so that a store
+// instruction covers 64 contiguous bytes of eight rows and not 16 of 32: an L1 line each
+// costs a cycle.
+__device__ __forceinline__ void store_rows32(const uint32_t (&w)[16], __nv_bfloat16* dst, int rel, int ld, int lane) {
 #pragma unroll
   for (int s = 0; s < 4; ++s) {
-    // send piece (lane ^ s) & 3 of the own row to lane ^ s; receive that lane's piece `lane & 3`
+    // send the own row's piece (lane ^ s) & 3 to lane ^ s; receive that lane's piece lane & 3
     const int to = (lane ^ s) & 3;
     uint4 v;
     uint32_t* vw = reinterpret_cast<uint32_t*>(&v);
@@ -460,10 +458,8 @@ __device__ __forceinline__ void store_rows32(const uint32_t (&w)[16], void* dst,
       const uint32_t a = to & 1 ? w[4 + i] : w[i], b = to & 1 ? w[12 + i] : w[8 + i];
       vw[i] = __shfl_xor_sync(0xffffffffu, to & 2 ? b : a, s);
     }
-    const int from = (lane ^ s) & 3;   // whose row this piece belongs to
-    const uint64_t lo = from & 1 ? base[1] : base[0], hi = from & 1 ? base[3] : base[2];
-    uint4* p = reinterpret_cast<uint4*>(from & 2 ? hi : lo);
-    if (p != nullptr) p[lane & 3] = v;
+    const int row = __shfl_xor_sync(0xffffffffu, rel, s);
+    if (row >= 0) reinterpret_cast<uint4*>(dst + (int64_t)row * ld)[lane & 3] = v;
   }
 }
 

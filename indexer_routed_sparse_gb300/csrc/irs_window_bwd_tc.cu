@@ -362,7 +362,6 @@ __global__ void __launch_bounds__(kDqThreads, 1)
         const int tile = prev / a.Hkv, g = prev - tile * a.Hkv;
         const int r = (warp & 3) * 32 + lane, rq = r / a.G, t = tile * qt + rq, h = g * a.G + (r - rq * a.G);
         const bool live = rq < qt && t < a.T;
-        const int64_t row = (int64_t)t * a.Hq + h;
         if (!__all_sync(0xffffffffu, mbar_wait(dq_full, (ni - 1) & 1, abort_flag, a.err))) break;
         tc_fence_after();
         float odd = 0.f;
@@ -378,7 +377,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
             const __nv_bfloat162 b = __floats2bfloat162_rn(o[i] * a.scale, o[i + 1] * a.scale);
             w[i >> 1] = *reinterpret_cast<const uint32_t*>(&b);
           }
-          store_rows32(w, live ? a.dq + row * DQK + d : nullptr, lane);
+          store_rows32(w, a.dq + ((int64_t)tile * qt * a.Hq + g * a.G) * DQK + d, live ? rq * a.Hq + r - rq * a.G : -1, DQK, lane);
         }
         tc_fence_before();
         __syncwarp();

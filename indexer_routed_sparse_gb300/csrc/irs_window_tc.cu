@@ -10,9 +10,9 @@
 // * The 128 rows of a product are the G query heads of a KV head for 128 / G queries, so a
 //   tile spans few queries and the keys it needs beyond one window are few: window 512 and
 //   G = 16 give tiles of 8 queries over 519 keys.
-// * An item is two such tiles of neighbouring queries over the same key blocks (128 keys, by
-//   TMA, 96 where shared memory asks for it): while one tile's scores go through the softmax, the tensor cores work for the
-//   other. A persistent CTA an SM walks the items; the next item's queries and keys load
+// * An item is two such tiles of neighbouring queries over the same key blocks (64 keys, by
+//   TMA), each with an issuing warp of its own that runs two blocks' scores ahead of the
+//   weights' products: the softmax finds its scores ready. A persistent CTA an SM walks the items; the next item's queries and keys load
 //   while the last one drains.
 // * Two threads share a row, 64 keys of a block each (16 softmax warps). With one thread a
 //   row (8 warps of 128 values) a warp's own latency was the bound: 4 to 5 cycles an
@@ -38,25 +38,26 @@ namespace {
 
 constexpr int kRows = 128;           // rows a tile
 constexpr uint32_t kAtom = 128 * 128;   // 128 rows x 64 bf16
-constexpr int kFwdThreads = 576;     // warps 0-7, 8-15: softmax of the two tiles; 16: TMA; 17: MMA
+constexpr int kFwdThreads = 608;     // warps 0-7, 8-15: softmax of the two tiles; 16: TMA; 17, 18: MMA of the two tiles
 constexpr float kRaise = 256.f;      // a weight past this raises the maximum
 
 template <int DQK, int DV>
 struct FwdCfg {
   static constexpr int QA = DQK / 64, VA = DV / 64;
   static constexpr uint32_t q_bytes = QA * kAtom;          // one tile's queries
-  // Keys a block: two stages of 96 keys and values fit beside two tiles' queries at every head
-  // dim; 128 would leave 192/128 one stage of values, and a softmax thread too few registers.
-  static constexpr int BLK = 96;
+  // 64 keys a block: two blocks' scores of both tiles (4 x 64 columns) lie in TMEM beside both
+  // outputs, so a block's scores are there when the block before has its weights.
+  static constexpr int BLK = 64;
   static constexpr uint32_t kv_atom = BLK * 128;           // BLK rows x 64 bf16
   static constexpr uint32_t k_bytes = QA * kv_atom, v_bytes = VA * kv_atom;
-  static constexpr int KS = 2, VS = 2;
+  static constexpr int KS = 3, VS = 3;
   static constexpr uint32_t k_off = 2 * q_bytes, v_off = k_off + KS * k_bytes, x_off = v_off + VS * v_bytes;
   static constexpr uint32_t bar_off = x_off + 2 * 2 * kRows * 4;   // a word a row, half and tile
-  static constexpr uint32_t cu_off = bar_off + 24 * 8 + 16 + 2 * 16;
+  static constexpr uint32_t plan_off = bar_off + 32 * 8 + 16;   // [4][8] an item's blocks and borders
+  static constexpr uint32_t cu_off = plan_off + 4 * 32;
   static constexpr int cu_cap = (int)((232448u - cu_off) / 4u) < 2048 ? (int)((232448u - cu_off) / 4u) : 2048;
   static constexpr uint32_t total = cu_off + 4u * cu_cap;   // 226.3 KB at 192/128: none to spare for aligning
-  static constexpr uint32_t S0 = 0, O0 = 256;              // TMEM: S of tile x at 128 x, O at 256 + x DV
+  static constexpr uint32_t S0 = 0, O0 = 256;              // TMEM: S of tile x, buffer b at 128 x + 64 b; O at 256 + x DV
 };
 
 // The keys of one item: two tiles of `qt` queries from t0 on. The first `sb` blocks hold the
@@ -64,7 +65,7 @@ struct FwdCfg {
 // the second [f1, nbt).
 struct Item {
   int t0, last, lastA;   // first query; last query of the item and of its first tile
-  int ds0, klo, ns;      // document start of the first query; first key of the range; first tokens before it
+  int ds0, de0, klo, ns; // document of the first query; first key of the range; first tokens before it
   int sb, nbt, l0, f1;
   bool hasB;
 };
@@ -75,7 +76,9 @@ __device__ __forceinline__ Item window_item(const WinArgs& a, const int32_t* cu,
   m.last = min(t0 + 2 * qt, a.T) - 1;
   m.lastA = min(t0 + qt, a.T) - 1;
   m.hasB = t0 + qt < a.T;
-  m.ds0 = window_doc(cu, a.ndocs, a.T, t0).start;
+  const WinDoc d0 = window_doc(cu, a.ndocs, a.T, t0);
+  m.ds0 = d0.start;
+  m.de0 = d0.end;
   m.klo = max(m.ds0, t0 - a.window + 1);
   m.ns = max(0, min(m.ds0 + a.sinks, m.klo) - m.ds0);
   m.sb = (m.ns + kBlk - 1) / kBlk;
@@ -83,7 +86,7 @@ __device__ __forceinline__ Item window_item(const WinArgs& a, const int32_t* cu,
   m.l0 = (m.lastA - m.klo) / kBlk + m.sb;
   m.f1 = 0;
   if (m.hasB) {
-    const int tb = t0 + qt, dsB = window_doc(cu, a.ndocs, a.T, tb).start;
+    const int tb = t0 + qt, dsB = tb < m.de0 ? m.ds0 : window_doc(cu, a.ndocs, a.T, tb).start;
     // blocks before the second tile's window are left out; with first tokens, only theirs
     if (a.sinks == 0) m.f1 = (max(dsB, tb - a.window + 1) - m.klo) / kBlk;
     else m.f1 = dsB != m.ds0 ? m.sb : 0;
@@ -119,9 +122,7 @@ __device__ __forceinline__ void pv_any(int cols, uint32_t d, uint32_t p, uint32_
                                        bool accumulate) {
   switch (cols >> 5) {
     case 1: pv_run<2>(d, p, vb, atom, idesc, accumulate); break;
-    case 2: pv_run<4>(d, p, vb, atom, idesc, accumulate); break;
-    case 3: pv_run<6>(d, p, vb, atom, idesc, accumulate); break;
-    default: pv_run<8>(d, p, vb, atom, idesc, accumulate); break;
+    default: pv_run<4>(d, p, vb, atom, idesc, accumulate); break;
   }
 }
 
@@ -139,28 +140,30 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::bar_off);   // [2]
   uint64_t* q_empty = q_full + 2;     // [2]
   uint64_t* k_full = q_empty + 2;     // [KS]
-  uint64_t* k_empty = k_full + 2;
-  uint64_t* v_full = k_empty + 2;     // [VS]
-  uint64_t* v_empty = v_full + 2;
-  uint64_t* s_full = v_empty + 2;     // [2] scores of the tile's next block
-  uint64_t* p_full = s_full + 2;      // [2] its weights
-  uint64_t* o_full = p_full + 2;      // [2] the tile's output
+  uint64_t* k_empty = k_full + KS;
+  uint64_t* v_full = k_empty + KS;    // [VS]
+  uint64_t* v_empty = v_full + VS;
+  uint64_t* s_full = v_empty + VS;    // [2][2] scores of a tile's next block, by buffer
+  uint64_t* p_full = s_full + 4;      // [2][2] the block's weights
+  uint64_t* pv_done = p_full + 4;     // [2] ... have been multiplied
+  uint64_t* o_full = pv_done + 2;     // [2] the tile's output
   uint64_t* o_empty = o_full + 2;     // [2]
-  uint64_t* drain = o_empty + 2;
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* drain = o_empty + 2;      // [2]
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(drain + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
-  volatile int* plan = reinterpret_cast<volatile int*>(tslot + 4);     // [2][4]: an item's blocks, for the MMA warp
+  volatile int* plan = reinterpret_cast<volatile int*>(smem + C::plan_off);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
+    for (int i = 0; i < KS; ++i) { mbar_init(&k_full[i], 1); mbar_init(&k_empty[i], 2); }
+    for (int i = 0; i < VS; ++i) { mbar_init(&v_full[i], 1); mbar_init(&v_empty[i], 2); }
+    for (int i = 0; i < 4; ++i) { mbar_init(&s_full[i], 1); mbar_init(&p_full[i], 8); }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&q_full[i], 1); mbar_init(&q_empty[i], 1);
-      mbar_init(&k_full[i], 1); mbar_init(&k_empty[i], 1);
-      mbar_init(&v_full[i], 1); mbar_init(&v_empty[i], 1);
-      mbar_init(&s_full[i], 1); mbar_init(&p_full[i], 8);
+      mbar_init(&pv_done[i], 1);
       mbar_init(&o_full[i], 1); mbar_init(&o_empty[i], 8);
+      mbar_init(&drain[i], 1);
     }
-    mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -194,21 +197,29 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       bool ok = true;
       auto load_q = [&](int x, const Item& m, int g) {
         if (nq[x] > 0 && !mbar_wait(&q_empty[x], (nq[x] - 1) & 1, abort_flag, a.err)) return false;
+        ++nq[x];
+        if (x == 1 && !m.hasB) {   // the second tile's warp still learns of the item
+          mbar_arrive(&q_full[1]);
+          return true;
+        }
         mbar_arrive_expect_tx(&q_full[x], q_box);
         for (int c = 0; c < C::QA; ++c)
           tma_load_3d(smem + x * C::q_bytes + c * kAtom, &tm_q, c * 64, g * a.G, m.t0 + x * qt, &q_full[x]);
-        ++nq[x];
         return true;
       };
       for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
         const int pair = item / a.Hkv, g = item - pair * a.Hkv;
         const Item m = window_item<C::BLK>(a, cu, pair * 2 * qt, qt);
-        // two slots: this one was read before the first tile's last scores of two items ago
-        volatile int* pl = plan + 4 * (nq[0] & 1);
+        // four slots: this one's reader, three items behind at most, is done with it
+        volatile int* pl = plan + 8 * (nq[0] & 3);
         pl[0] = m.nbt;
         pl[1] = m.l0;
         pl[2] = m.hasB ? m.f1 : m.nbt;
         pl[3] = (m.sb > 0 ? item_cols<C::BLK>(m, m.sb - 1) : 0) | item_cols<C::BLK>(m, m.nbt - 1) << 8 | m.sb << 16;
+        pl[4] = m.klo;
+        pl[5] = m.ns;
+        pl[6] = m.ds0;
+        pl[7] = m.de0;
         if (!(ok = load_q(0, m, g))) break;
         for (int j = 0; j < m.nbt && ok; ++j) {
           const int kb = item_key<C::BLK>(m, j);
@@ -218,7 +229,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           for (int c = 0; c < C::QA; ++c)
             tma_load_3d(smem + C::k_off + ks * C::k_bytes + c * C::kv_atom, &tm_k, c * 64, g, kb, &k_full[ks]);
           ++nk;
-          if (j == 0 && m.hasB && !(ok = load_q(1, m, g))) break;
+          if (j == 0 && !(ok = load_q(1, m, g))) break;
           if (nv >= VS && !mbar_wait(&v_empty[vs], (nv / VS - 1) & 1, abort_flag, a.err)) { ok = false; break; }
           mbar_arrive_expect_tx(&v_full[vs], C::v_bytes);
           for (int c = 0; c < C::VA; ++c)
@@ -237,98 +248,152 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         for (uint32_t i = nv > VS ? nv - VS : 0; i < nv; ++i) landed(&v_full[i % VS], (i / VS) & 1);
       }
     }
-  } else if (warp == 17) {
-    // ---------------- MMA issuer (the whole warp; one elected lane issues) ----------------
+  } else if (warp >= 17) {
+    // ---------------- MMA issuer of a tile (the whole warp; one elected lane issues) ----------------
+    // One warp for both tiles left the tensor cores idle for a third of its time: a wait that
+    // succeeds costs 115 cycles, and one tile's softmax held up the other tile's products.
     constexpr uint32_t PV_IDESC = idesc_bf16(kRows, DV, false, true);
-    const uint32_t tb = (uint32_t)uniform((int)tbase);
-    const uint32_t sb = smem_u32(smem);
+    // Scores run two blocks ahead of the weights' products, into the next item too.
+    const int x = uniform(warp - 17);
+    const uint32_t tb = (uint32_t)uniform((int)tbase), sb = smem_u32(smem);
+    const uint32_t s_tm = tb + C::S0 + 128 * x, o_tm = tb + C::O0 + x * DV;
+    const uint64_t a0 = sdesc_sw128(sb + x * C::q_bytes, 16, 1024);
     auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, a.err)); };
-    uint32_t nk = 0, nv = 0, np[2] = {0, 0}, nq[2] = {0, 0}, no[2] = {0, 0};
+    struct Place {   // a place in the tile's list of blocks
+      int item, j, nbt, fx, lx, colsS, colsL, sb1;
+      uint32_t ni, st, ph, k, n;   // items so far; ring stage and its phase; blocks, active blocks so far
+    };
+    auto open = [&](Place& c) {
+      const volatile int* pl = plan + 8 * (c.ni & 3);
+      const int pc = uniform(pl[3]);
+      c.nbt = uniform(pl[0]);
+      c.fx = x == 0 ? 0 : uniform(pl[2]);
+      c.lx = x == 0 ? uniform(pl[1]) : c.nbt - 1;
+      c.colsS = pc & 0xff;
+      c.colsL = pc >> 8 & 0xff;
+      c.sb1 = (pc >> 16) - 1;
+      c.j = 0;
+    };
+    auto cols_of = [&](const Place& c) { return c.j == c.sb1 ? c.colsS : c.j == c.nbt - 1 ? c.colsL : C::BLK; };
     bool alive = true;
-    for (int item = blockIdx.x; item < items && alive; item += gridDim.x) {
-      if (!wait(&q_full[0], nq[0] & 1)) break;
-      const volatile int* pl = plan + 4 * (nq[0] & 1);
-      const int nbt = uniform(pl[0]), l0 = uniform(pl[1]), f1 = uniform(pl[2]), pc = uniform(pl[3]);
-      const int colsS = pc & 0xff, colsL = pc >> 8 & 0xff, sb1 = (pc >> 16) - 1;   // columns of the last first-token block (sb1) and of the last
-      ++nq[0];
-      int pcols = 0;
-      for (int j = 0; j <= nbt && alive; ++j) {
-        const bool more = j < nbt;
-        const int cols = j == sb1 ? colsS : j == nbt - 1 ? colsL : C::BLK;
-        const uint32_t kst = nk & 1, vst = nv & 1;
-        if (more && !wait(&k_full[kst], (nk >> 1) & 1)) { alive = false; break; }
-        if (j > 0 && !wait(&v_full[vst], (nv >> 1) & 1)) { alive = false; break; }
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int fx = x == 0 ? 0 : f1, lx = x == 0 ? l0 : nbt - 1;
-          if (j - 1 >= fx && j - 1 <= lx) {   // the block before: its weights times its values
-            if (!wait(&p_full[x], np[x] & 1)) { alive = false; break; }
-            ++np[x];
-            if (j - 1 == fx && no[x] > 0 && !wait(&o_empty[x], (no[x] - 1) & 1)) { alive = false; break; }
+    Place s{(int)blockIdx.x, 0, 0, 0, -1, 0, 0, -1, 0, 0, 0, 0, 0}, w = s;   // scores; weights' products
+    // The scores of the next active block; false where there is none, or none yet: block k's
+    // keys are loaded after block k - 1's values, into the stage that block k - 4's leave, so
+    // scores may not wait for more than three blocks past the values this warp still holds.
+    auto next_scores = [&]() {
+      while (alive && s.item < items) {
+        if (s.k > w.k + VS) return false;
+        if (s.j == 0) {   // the item's queries, and with them its plan
+          if (!(alive = wait(&q_full[x], s.ni & 1))) return false;
+          open(s);
+        }
+        bool act = false;
+        while (!act && s.j < s.nbt) {
+          if (s.k > w.k + VS) return false;
+          if (!(alive = wait(&k_full[s.st], s.ph))) return false;
+          act = s.j >= s.fx && s.j <= s.lx;
+          if (act) {
             tc_fence_after();
-            pv_any(pcols, tb + C::O0 + x * DV, tb + C::S0 + 128 * x, sb + C::v_off + vst * C::v_bytes, C::kv_atom, PV_IDESC,
-                   j - 1 > fx);
-            if (j - 1 == lx) { umma_commit_warp(&o_full[x]); ++no[x]; }
-          }
-          if (more && j >= fx && j <= lx) {
-            if (x == 1 && j == fx) {
-              if (!wait(&q_full[1], nq[1] & 1)) { alive = false; break; }
-              ++nq[1];
-            }
-            tc_fence_after();
-            const uint32_t idesc = idesc_bf16(kRows, cols, false, false);
-            const uint64_t a0 = sdesc_sw128(sb + x * C::q_bytes, 16, 1024);
-            const uint64_t b0 = sdesc_sw128(sb + C::k_off + kst * C::k_bytes, 16, 1024);
+            const uint32_t d = s_tm + 64 * (s.n & 1), idesc = idesc_bf16(kRows, cols_of(s), false, false);
+            const uint64_t b0 = sdesc_sw128(sb + C::k_off + s.st * C::k_bytes, 16, 1024);
 #pragma unroll
             for (int ks = 0; ks < 4 * C::QA; ++ks)
-              umma_bf16_warp(tb + C::S0 + 128 * x, a0 + (uint64_t)(((ks >> 2) * kAtom + (ks & 3) * 32) >> 4),
+              umma_bf16_warp(d, a0 + (uint64_t)(((ks >> 2) * kAtom + (ks & 3) * 32) >> 4),
                              b0 + (uint64_t)(((ks >> 2) * C::kv_atom + (ks & 3) * 32) >> 4), idesc, ks > 0);
-            umma_commit_warp(&s_full[x]);
-            if (j == lx) umma_commit_warp(&q_empty[x]);
+            umma_commit_warp(&s_full[2 * x + (s.n & 1)]);
+            umma_commit_warp(&k_empty[s.st]);
+            if (s.j == s.lx) umma_commit_warp(&q_empty[x]);
+            ++s.n;
+          } else if (lane == 0) {
+            mbar_arrive(&k_empty[s.st]);
           }
+          if (++s.st == KS) { s.st = 0; s.ph ^= 1u; }
+          ++s.j;
+          ++s.k;
         }
-        if (!alive) break;
-        if (j > 0) { umma_commit_warp(&v_empty[vst]); ++nv; }
-        if (more) { umma_commit_warp(&k_empty[kst]); ++nk; }
-        pcols = cols;
+        if (s.j == s.nbt) {
+          if (s.fx > s.lx && lane == 0) mbar_arrive(&q_empty[x]);   // an item without this tile
+          s.item += gridDim.x;
+          ++s.ni;
+          s.j = 0;
+        }
+        if (act) return true;
+      }
+      return false;
+    };
+    uint32_t no = 0;
+    while (alive && w.item < items) {
+      while (s.n - w.n < 2 && next_scores()) {}
+      if (!alive) break;
+      if (w.j == 0) open(w);   // the scores' place has been there
+      if (!(alive = wait(&v_full[w.st], w.ph))) break;
+      if (w.j >= w.fx && w.j <= w.lx) {
+        if (!(alive = wait(&p_full[2 * x + (w.n & 1)], (w.n >> 1) & 1))) break;
+        if (w.j == w.fx && no > 0 && !(alive = wait(&o_empty[x], (no - 1) & 1))) break;
+        tc_fence_after();
+        pv_any(cols_of(w), o_tm, s_tm + 64 * (w.n & 1), sb + C::v_off + w.st * C::v_bytes, C::kv_atom, PV_IDESC, w.j > w.fx);
+        umma_commit_warp(&pv_done[x]);
+        if (w.j == w.lx) { umma_commit_warp(&o_full[x]); ++no; }
+        umma_commit_warp(&v_empty[w.st]);
+        ++w.n;
+      } else if (lane == 0) {
+        mbar_arrive(&v_empty[w.st]);
+      }
+      if (++w.st == VS) { w.st = 0; w.ph ^= 1u; }
+      ++w.k;
+      if (++w.j == w.nbt) {
+        w.item += gridDim.x;
+        ++w.ni;
+        w.j = 0;
       }
     }
     // every issued product completes before the CTA releases its tensor memory
-    umma_commit_warp(drain);
+    umma_commit_warp(&drain[x]);
     const unsigned long long w0 = globaltimer_ns();
-    while (!mbar_try_wait(drain, 0) && globaltimer_ns() - w0 < kWaitLimitNs) {}
+    while (!mbar_try_wait(&drain[x], 0) && globaltimer_ns() - w0 < kWaitLimitNs) {}
     __syncwarp();
   } else {
     // ---------------- softmax: warps 0-7 the first tile, 8-15 the second ----------------
     const int x = warp >> 3, half = (warp >> 2) & 1;
     const int bar_id = 1 + x * 4 + (warp & 3);            // the two warps of these rows
     const int r = (warp & 3) * 32 + lane;                 // row of the tile = TMEM lane
-    const int rq = r / a.G, rh = r - rq * a.G;            // its query and head
-    const uint32_t s_addr = tbase + C::S0 + 128 * x + tmem_lane_base(warp);
+    const int rq = r / a.G;                               // its query
+    // its row of out, relative to the tile's first, and those of the four lanes that store together
+    const int rel = rq < qt ? rq * a.Hq + r - rq * a.G : -1;
+    const uint32_t s_base = tbase + C::S0 + 128 * x + tmem_lane_base(warp);
     const uint32_t o_addr = tbase + C::O0 + x * DV + tmem_lane_base(warp);
     const uint32_t mine = smem_u32(smem) + C::x_off + (uint32_t)((x * 2 + half) * kRows + r) * 4u;
     const uint32_t other = smem_u32(smem) + C::x_off + (uint32_t)((x * 2 + (half ^ 1)) * kRows + r) * 4u;
-    uint32_t nsf = 0, nof = 0;
+    uint32_t nsf = 0, nof = 0, ni = 0;
     bool alive = true;
-    for (int item = blockIdx.x; item < items && alive; item += gridDim.x) {
-      const int pair = item / a.Hkv, g = item - pair * a.Hkv;
-      const Item m = window_item<C::BLK>(a, cu, pair * 2 * qt, qt);
-      if (x == 1 && !m.hasB) continue;
-      const int t = m.t0 + x * qt + rq;
+    for (int item = blockIdx.x; item < items && alive; item += gridDim.x, ++ni) {
+      const int pair = item / a.Hkv, g = item - pair * a.Hkv, t0 = pair * 2 * qt;
+      const int t_first = t0 + x * qt, t_last = min(t_first + qt, a.T) - 1, t = t_first + rq;
+      if (t_first >= a.T) continue;
       const bool live = rq < qt && t < a.T;
-      const int t_first = m.t0 + x * qt, t_last = x == 0 ? m.lastA : m.last;
-      const int ds = window_doc(cu, a.ndocs, a.T, min(t, a.T - 1)).start;
+      // the first block's scores come after the item's plan
+      alive = __all_sync(0xffffffffu, mbar_wait(&s_full[2 * x + (nsf & 1)], (nsf >> 1) & 1, abort_flag, a.err));
+      const volatile int* pl = plan + 8 * (ni & 3);
+      Item m;
+      m.nbt = pl[0];
+      m.klo = pl[4];
+      m.ns = pl[5];
+      m.sb = pl[3] >> 16;
+      m.ds0 = pl[6];
+      m.last = min(t0 + 2 * qt, a.T) - 1;
+      const int jf = x == 0 ? 0 : pl[2], jl = x == 0 ? pl[1] : m.nbt - 1, de0 = pl[7];
+      const int ds = t < de0 ? m.ds0 : window_doc(cu, a.ndocs, a.T, min(t, a.T - 1)).start;
       const int lo = max(ds, t - a.window + 1);
       const int early = min(ds + a.sinks, lo);            // first tokens: [ds, early)
-      const int lo_last = max(window_doc(cu, a.ndocs, a.T, t_last).start, t_last - a.window + 1);
+      const int lo_last = max(t_last < de0 ? m.ds0 : window_doc(cu, a.ndocs, a.T, t_last).start, t_last - a.window + 1);
       float mx = -INFINITY, l = 0.f;
       bool settled = false;                               // every row of the warps has a maximum
-      const int jf = x == 0 ? 0 : m.f1, jl = x == 0 ? m.l0 : m.nbt - 1;
       for (int j = jf; j <= jl && alive; ++j) {
         const int kb = item_key<C::BLK>(m, j), cols = item_cols<C::BLK>(m, j);
         const bool sink_blk = j < m.sb;
         const int pieces = cols >> 5, c0 = half * (cols >> 1);   // 16-key pieces of this half, its first column
-        alive = __all_sync(0xffffffffu, mbar_wait(&s_full[x], nsf & 1, abort_flag, a.err));
+        if (j > jf) alive = __all_sync(0xffffffffu, mbar_wait(&s_full[2 * x + (nsf & 1)], (nsf >> 1) & 1, abort_flag, a.err));
+        const uint32_t s_addr = s_base + 64 * (nsf & 1);
         ++nsf;
         tc_fence_after();
         // border: key k0 + i is seen for i in [w0, w1) (the window) or [e0, e1) (first tokens)
@@ -399,8 +464,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           const float c = nm == -INFINITY ? 1.f : ex2_approx(mx - nm);
           mx = nm;
           l *= c;
+          // O has the products of the block before (these scores came after those of two before)
+          if (j > jf && alive) alive = __all_sync(0xffffffffu, mbar_wait(&pv_done[x], (nsf - 2) & 1, abort_flag, a.err));
           if (j > jf && alive) {
-            // the scores' barrier also covers the products before them: O is complete so far
+            tc_fence_after();
 #pragma unroll 1
             for (int d = half * (DV / 2); d < (half + 1) * (DV / 2); d += 16) {
               float o[16];
@@ -421,7 +488,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[x]);
+        if (lane == 0) mbar_arrive(&p_full[2 * x + ((nsf - 1) & 1)]);
       }
       // ---- the tile's rows, half the dims a thread ----
       if (alive) alive = __all_sync(0xffffffffu, mbar_wait(&o_full[x], nof & 1, abort_flag, a.err));
@@ -432,8 +499,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       if (!alive) break;
       l += ld_shared(other);
       const float inv = 1.f / l;
-      const int h = g * a.G + rh;
-      const int64_t row = (int64_t)t * a.Hq + h;
+      const int64_t row0 = (int64_t)t_first * a.Hq + g * a.G;
       float odd = fmaf(mx, 0.f, l * 0.f);                 // NaN where anything is not finite
 #pragma unroll 1
       for (int d = half * (DV / 2); d < (half + 1) * (DV / 2); d += 32) {
@@ -451,12 +517,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             w[8 * e + (i >> 1)] = *reinterpret_cast<const uint32_t*>(&b);
           }
         }
-        store_rows32(w, live ? a.out + row * DV + d : nullptr, lane);
+        store_rows32(w, a.out + row0 * DV + d, live ? rel : -1, DV, lane);
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&o_empty[x]);
-      if (half == 0 && live && a.lse != nullptr) a.lse[row] = fmaf(mx, 0.6931471805599453f, logf(l));
+      if (half == 0 && live && a.lse != nullptr) a.lse[row0 + rel] = fmaf(mx, 0.6931471805599453f, logf(l));
       // rows to do again: by the first half's warp, after both halves have stored
       if (named_bar_or(bar_id, 64, live && odd != 0.f)) {   // NaN compares unequal
         st_shared(mine, odd);
@@ -465,7 +531,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         while (again) {
           const int src = __ffs((int)again) - 1;
           again &= again - 1;
-          fwd_row<DQK / 64, DV / 64>(a, __shfl_sync(0xffffffffu, t, src), __shfl_sync(0xffffffffu, h, src), lane);
+          fwd_row<DQK / 64, DV / 64>(a, __shfl_sync(0xffffffffu, t, src), g * a.G + __shfl_sync(0xffffffffu, r - rq * a.G, src), lane);
         }
       }
     }
