@@ -49,9 +49,9 @@ struct FwdCfg {
   // outputs, so a block's scores are there when the block before has its weights.
   static constexpr int BLK = 64;
   static constexpr uint32_t kv_atom = BLK * 128;           // BLK rows x 64 bf16
-  static constexpr uint32_t k_bytes = QA * kv_atom, v_bytes = VA * kv_atom;
-  static constexpr int KS = 3, VS = 3;
-  static constexpr uint32_t k_off = 2 * q_bytes, v_off = k_off + KS * k_bytes, x_off = v_off + VS * v_bytes;
+  static constexpr uint32_t k_bytes = QA * kv_atom, v_bytes = VA * kv_atom, st_bytes = k_bytes + v_bytes;
+  static constexpr int ST = 3;                             // stages: block t's keys and block t - 2's values
+  static constexpr uint32_t st_off = 2 * q_bytes, x_off = st_off + ST * st_bytes;
   static constexpr uint32_t bar_off = x_off + 2 * 2 * kRows * 4;   // a word a row, half and tile
   static constexpr uint32_t plan_off = bar_off + 32 * 8 + 16;   // [4][8] an item's blocks and borders
   static constexpr uint32_t cu_off = plan_off + 4 * 32;
@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     window_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, WinArgs a, int qt, int pairs) {
   using C = FwdCfg<DQK, DV>;
-  constexpr int KS = C::KS, VS = C::VS;
+  constexpr int ST = C::ST;
   extern __shared__ __align__(1024) uint8_t smem[];
   if ((smem_u32(smem) & 1023u) != 0) {   // the attribute asks for it; the tiles need it
     record_error(a.err, IRS_DEVERR_TIMEOUT);
@@ -139,11 +139,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   }
   uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::bar_off);   // [2]
   uint64_t* q_empty = q_full + 2;     // [2]
-  uint64_t* k_full = q_empty + 2;     // [KS]
-  uint64_t* k_empty = k_full + KS;
-  uint64_t* v_full = k_empty + KS;    // [VS]
-  uint64_t* v_empty = v_full + VS;
-  uint64_t* s_full = v_empty + VS;    // [2][2] scores of a tile's next block, by buffer
+  uint64_t* st_full = q_empty + 2;    // [ST]
+  uint64_t* st_empty = st_full + ST;
+  uint64_t* s_full = st_empty + ST;    // [2][2] scores of a tile's next block, by buffer
   uint64_t* p_full = s_full + 4;      // [2][2] the block's weights
   uint64_t* pv_done = p_full + 4;     // [2] ... have been multiplied
   uint64_t* o_full = pv_done + 2;     // [2] the tile's output
@@ -155,8 +153,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
-    for (int i = 0; i < KS; ++i) { mbar_init(&k_full[i], 1); mbar_init(&k_empty[i], 2); }
-    for (int i = 0; i < VS; ++i) { mbar_init(&v_full[i], 1); mbar_init(&v_empty[i], 2); }
+    for (int i = 0; i < ST; ++i) { mbar_init(&st_full[i], 1); mbar_init(&st_empty[i], 2); }
     for (int i = 0; i < 4; ++i) { mbar_init(&s_full[i], 1); mbar_init(&p_full[i], 8); }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&q_full[i], 1); mbar_init(&q_empty[i], 1);
@@ -193,7 +190,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       tma_prefetch_map(&tm_k);
       tma_prefetch_map(&tm_v);
       const uint32_t q_box = (uint32_t)(qt * a.G) * 128u * C::QA;
-      uint32_t nq[2] = {0, 0}, nk = 0, nv = 0;
+      uint32_t nq[2] = {0, 0}, ns = 0, st = 0, ph = 0;
       bool ok = true;
       auto load_q = [&](int x, const Item& m, int g) {
         if (nq[x] > 0 && !mbar_wait(&q_empty[x], (nq[x] - 1) & 1, abort_flag, a.err)) return false;
@@ -221,20 +218,19 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         pl[6] = m.ds0;
         pl[7] = m.de0;
         if (!(ok = load_q(0, m, g))) break;
-        for (int j = 0; j < m.nbt && ok; ++j) {
-          const int kb = item_key<C::BLK>(m, j);
-          const uint32_t ks = nk % KS, vs = nv % VS;
-          if (nk >= KS && !mbar_wait(&k_empty[ks], (nk / KS - 1) & 1, abort_flag, a.err)) { ok = false; break; }
-          mbar_arrive_expect_tx(&k_full[ks], C::k_bytes);
-          for (int c = 0; c < C::QA; ++c)
-            tma_load_3d(smem + C::k_off + ks * C::k_bytes + c * C::kv_atom, &tm_k, c * 64, g, kb, &k_full[ks]);
-          ++nk;
+        for (int j = 0; j < m.nbt + 2; ++j) {   // block j's keys, block j - 2's values
+          if (ns >= (uint32_t)ST && !mbar_wait(&st_empty[st], ph ^ 1u, abort_flag, a.err)) { ok = false; break; }
+          mbar_arrive_expect_tx(&st_full[st], (j < m.nbt ? C::k_bytes : 0u) + (j >= 2 ? C::v_bytes : 0u));
+          uint8_t* dst = smem + C::st_off + st * C::st_bytes;
+          if (j < m.nbt)
+            for (int c = 0; c < C::QA; ++c)
+              tma_load_3d(dst + c * C::kv_atom, &tm_k, c * 64, g, item_key<C::BLK>(m, j), &st_full[st]);
+          if (j >= 2)
+            for (int c = 0; c < C::VA; ++c)
+              tma_load_3d(dst + C::k_bytes + c * C::kv_atom, &tm_v, c * 64, g, item_key<C::BLK>(m, j - 2), &st_full[st]);
+          ++ns;
+          if (++st == (uint32_t)ST) { st = 0; ph ^= 1u; }
           if (j == 0 && !(ok = load_q(1, m, g))) break;
-          if (nv >= VS && !mbar_wait(&v_empty[vs], (nv / VS - 1) & 1, abort_flag, a.err)) { ok = false; break; }
-          mbar_arrive_expect_tx(&v_full[vs], C::v_bytes);
-          for (int c = 0; c < C::VA; ++c)
-            tma_load_3d(smem + C::v_off + vs * C::v_bytes + c * C::kv_atom, &tm_v, c * 64, g, kb, &v_full[vs]);
-          ++nv;
         }
       }
       if (*abort_flag) {
@@ -244,8 +240,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           while (!mbar_try_wait(bar, parity) && globaltimer_ns() - w0 < kWaitLimitNs) {}
         };
         for (int x = 0; x < 2; ++x) if (nq[x] > 0) landed(&q_full[x], (nq[x] - 1) & 1);
-        for (uint32_t i = nk > KS ? nk - KS : 0; i < nk; ++i) landed(&k_full[i % KS], (i / KS) & 1);
-        for (uint32_t i = nv > VS ? nv - VS : 0; i < nv; ++i) landed(&v_full[i % VS], (i / VS) & 1);
+        for (uint32_t i = ns > (uint32_t)ST ? ns - ST : 0; i < ns; ++i) landed(&st_full[i % ST], (i / ST) & 1);
       }
     }
   } else if (warp >= 17) {
@@ -253,99 +248,53 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     // One warp for both tiles left the tensor cores idle for a third of its time: a wait that
     // succeeds costs 115 cycles, and one tile's softmax held up the other tile's products.
     constexpr uint32_t PV_IDESC = idesc_bf16(kRows, DV, false, true);
-    // Scores run two blocks ahead of the weights' products, into the next item too.
+    // A step is block t's scores and block t - 2's weights times its values: scores are two
+    // blocks ahead of the softmax, and one wait covers both operands. The loop is kept this
+    // plain because a lone warp takes ten cycles an instruction where the flow is not straight.
     const int x = uniform(warp - 17);
     const uint32_t tb = (uint32_t)uniform((int)tbase), sb = smem_u32(smem);
     const uint32_t s_tm = tb + C::S0 + 128 * x, o_tm = tb + C::O0 + x * DV;
     const uint64_t a0 = sdesc_sw128(sb + x * C::q_bytes, 16, 1024);
     auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, a.err)); };
-    struct Place {   // a place in the tile's list of blocks
-      int item, j, nbt, fx, lx, colsS, colsL, sb1;
-      uint32_t ni, st, ph, k, n;   // items so far; ring stage and its phase; blocks, active blocks so far
-    };
-    auto open = [&](Place& c) {
-      const volatile int* pl = plan + 8 * (c.ni & 3);
-      const int pc = uniform(pl[3]);
-      c.nbt = uniform(pl[0]);
-      c.fx = x == 0 ? 0 : uniform(pl[2]);
-      c.lx = x == 0 ? uniform(pl[1]) : c.nbt - 1;
-      c.colsS = pc & 0xff;
-      c.colsL = pc >> 8 & 0xff;
-      c.sb1 = (pc >> 16) - 1;
-      c.j = 0;
-    };
-    auto cols_of = [&](const Place& c) { return c.j == c.sb1 ? c.colsS : c.j == c.nbt - 1 ? c.colsL : C::BLK; };
+    uint32_t ni = 0, no = 0, st = 0, ph = 0, ns = 0, nw = 0;   // items, outputs; ring; blocks scored, weighted
     bool alive = true;
-    Place s{(int)blockIdx.x, 0, 0, 0, -1, 0, 0, -1, 0, 0, 0, 0, 0}, w = s;   // scores; weights' products
-    // The scores of the next active block; false where there is none, or none yet: block k's
-    // keys are loaded after block k - 1's values, into the stage that block k - 4's leave, so
-    // scores may not wait for more than three blocks past the values this warp still holds.
-    auto next_scores = [&]() {
-      while (alive && s.item < items) {
-        if (s.k > w.k + VS) return false;
-        if (s.j == 0) {   // the item's queries, and with them its plan
-          if (!(alive = wait(&q_full[x], s.ni & 1))) return false;
-          open(s);
+    for (int item = blockIdx.x; item < items && alive; item += gridDim.x, ++ni) {
+      if (!wait(&q_full[x], ni & 1)) break;
+      const volatile int* pl = plan + 8 * (ni & 3);
+      const int nbt = uniform(pl[0]), pc = uniform(pl[3]);
+      const int fx = x == 0 ? 0 : uniform(pl[2]), lx = x == 0 ? uniform(pl[1]) : nbt - 1;
+      const int colsS = pc & 0xff, colsL = pc >> 8 & 0xff, sb1 = (pc >> 16) - 1;   // columns of the last first-token block (sb1) and of the last
+      for (int t = 0; t < nbt + 2; ++t) {
+        if (!wait(&st_full[st], ph)) { alive = false; break; }
+        const uint32_t kv = sb + C::st_off + st * C::st_bytes;
+        const int b = t - 2;
+        if (b >= fx && b <= lx) {
+          if (!wait(&p_full[2 * x + (nw & 1)], (nw >> 1) & 1)) { alive = false; break; }
+          if (b == fx && no > 0 && !wait(&o_empty[x], (no - 1) & 1)) { alive = false; break; }
+          tc_fence_after();
+          pv_any(b == sb1 ? colsS : b == nbt - 1 ? colsL : C::BLK, o_tm, s_tm + 64 * (nw & 1), kv + C::k_bytes, C::kv_atom,
+                 PV_IDESC, b > fx);
+          if (b == lx) { umma_commit_warp(&o_full[x]); ++no; }
+          umma_commit_warp(&pv_done[x]);
+          ++nw;
         }
-        bool act = false;
-        while (!act && s.j < s.nbt) {
-          if (s.k > w.k + VS) return false;
-          if (!(alive = wait(&k_full[s.st], s.ph))) return false;
-          act = s.j >= s.fx && s.j <= s.lx;
-          if (act) {
-            tc_fence_after();
-            const uint32_t d = s_tm + 64 * (s.n & 1), idesc = idesc_bf16(kRows, cols_of(s), false, false);
-            const uint64_t b0 = sdesc_sw128(sb + C::k_off + s.st * C::k_bytes, 16, 1024);
+        if (t >= fx && t <= lx) {
+          tc_fence_after();
+          const uint32_t d = s_tm + 64 * (ns & 1);
+          const uint32_t idesc = idesc_bf16(kRows, t == sb1 ? colsS : t == nbt - 1 ? colsL : C::BLK, false, false);
+          const uint64_t b0 = sdesc_sw128(kv, 16, 1024);
 #pragma unroll
-            for (int ks = 0; ks < 4 * C::QA; ++ks)
-              umma_bf16_warp(d, a0 + (uint64_t)(((ks >> 2) * kAtom + (ks & 3) * 32) >> 4),
-                             b0 + (uint64_t)(((ks >> 2) * C::kv_atom + (ks & 3) * 32) >> 4), idesc, ks > 0);
-            umma_commit_warp(&s_full[2 * x + (s.n & 1)]);
-            umma_commit_warp(&k_empty[s.st]);
-            if (s.j == s.lx) umma_commit_warp(&q_empty[x]);
-            ++s.n;
-          } else if (lane == 0) {
-            mbar_arrive(&k_empty[s.st]);
-          }
-          if (++s.st == KS) { s.st = 0; s.ph ^= 1u; }
-          ++s.j;
-          ++s.k;
+          for (int ks = 0; ks < 4 * C::QA; ++ks)
+            umma_bf16_warp(d, a0 + (uint64_t)(((ks >> 2) * kAtom + (ks & 3) * 32) >> 4),
+                           b0 + (uint64_t)(((ks >> 2) * C::kv_atom + (ks & 3) * 32) >> 4), idesc, ks > 0);
+          umma_commit_warp(&s_full[2 * x + (ns & 1)]);
+          if (t == lx) umma_commit_warp(&q_empty[x]);
+          ++ns;
         }
-        if (s.j == s.nbt) {
-          if (s.fx > s.lx && lane == 0) mbar_arrive(&q_empty[x]);   // an item without this tile
-          s.item += gridDim.x;
-          ++s.ni;
-          s.j = 0;
-        }
-        if (act) return true;
+        umma_commit_warp(&st_empty[st]);   // arrives at once where the tile had nothing to do
+        if (++st == (uint32_t)ST) { st = 0; ph ^= 1u; }
       }
-      return false;
-    };
-    uint32_t no = 0;
-    while (alive && w.item < items) {
-      while (s.n - w.n < 2 && next_scores()) {}
-      if (!alive) break;
-      if (w.j == 0) open(w);   // the scores' place has been there
-      if (!(alive = wait(&v_full[w.st], w.ph))) break;
-      if (w.j >= w.fx && w.j <= w.lx) {
-        if (!(alive = wait(&p_full[2 * x + (w.n & 1)], (w.n >> 1) & 1))) break;
-        if (w.j == w.fx && no > 0 && !(alive = wait(&o_empty[x], (no - 1) & 1))) break;
-        tc_fence_after();
-        pv_any(cols_of(w), o_tm, s_tm + 64 * (w.n & 1), sb + C::v_off + w.st * C::v_bytes, C::kv_atom, PV_IDESC, w.j > w.fx);
-        umma_commit_warp(&pv_done[x]);
-        if (w.j == w.lx) { umma_commit_warp(&o_full[x]); ++no; }
-        umma_commit_warp(&v_empty[w.st]);
-        ++w.n;
-      } else if (lane == 0) {
-        mbar_arrive(&v_empty[w.st]);
-      }
-      if (++w.st == VS) { w.st = 0; w.ph ^= 1u; }
-      ++w.k;
-      if (++w.j == w.nbt) {
-        w.item += gridDim.x;
-        ++w.ni;
-        w.j = 0;
-      }
+      if (alive && fx > lx && lane == 0) mbar_arrive(&q_empty[x]);   // an item without this tile
     }
     // every issued product completes before the CTA releases its tensor memory
     umma_commit_warp(&drain[x]);
