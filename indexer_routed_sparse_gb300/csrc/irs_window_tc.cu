@@ -347,38 +347,37 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         tc_fence_after();
         // border: key k0 + i is seen for i in [w0, w1) (the window) or [e0, e1) (first tokens)
         const bool border = sink_blk || kb < lo_last || kb + cols - 1 > t_first;
-        uint64_t seen = ~0ull;
+        uint32_t seen = ~0u;
         if (border) {
           const int k0 = kb + c0;
-          seen = bit_range(lo - k0, t + 1 - k0) | bit_range(ds - k0, early - k0);
-          if (sink_blk) seen = ds == m.ds0 ? bit_range(0, m.ns - C::BLK * j - c0) : 0ull;
-          if (!live) seen = 0ull;
+          seen = bit_range32(lo - k0, t + 1 - k0) | bit_range32(ds - k0, early - k0);
+          if (sink_blk) seen = ds == m.ds0 ? bit_range32(0, m.ns - C::BLK * j - c0) : 0u;
+          if (!live) seen = 0u;
         }
         // One pass: the weights under the present maximum, and whether one passes 2^8. They
         // wait in registers for the two halves' vote; where it asks for it (and for the first
         // blocks, before every row has a maximum) the scores are read again.
-        uint32_t w[C::BLK / 32][8];
+        uint32_t w[2][8];
         float ln = 0.f;
         auto weights = [&]() {
           const float off = mx == -INFINITY ? 0.f : -mx;
-          float l0 = 0.f, l1 = 0.f, big = 0.f;
+          const uint64_t sc2 = pack2(a.scale_log2, a.scale_log2), off2 = pack2(off, off);
+          uint64_t sum0 = 0ull, sum1 = 0ull;   // FP32 pairs
+          float big = 0.f;
 #pragma unroll
-          for (int c = 0; c < C::BLK / 32; ++c) {
+          for (int c = 0; c < 2; ++c) {
             if (c < pieces) {
               float v[16];
               tmem_ld16(s_addr + c0 + 16 * c, v);
               tmem_ld_wait_regs(v);
-              if (border) mask16(v, (uint32_t)(seen >> (16 * c)));
+              if (border) mask16(v, seen >> (16 * c));
 #pragma unroll
               for (int i = 0; i < 16; i += 4) {
-                const float p0 = ex2_approx(fmaf(v[i], a.scale_log2, off));
-                const float p1 = ex2_approx(fmaf(v[i + 1], a.scale_log2, off));
-                const float p2 = ex2_approx(fmaf(v[i + 2], a.scale_log2, off));
-                const float p3 = ex2_approx(fmaf(v[i + 3], a.scale_log2, off));
-                l0 += p0;
-                l1 += p1;
-                l0 += p2;
-                l1 += p3;
+                const float2 x0 = unpack2(ffma2(pack2(v[i], v[i + 1]), sc2, off2));
+                const float2 x1 = unpack2(ffma2(pack2(v[i + 2], v[i + 3]), sc2, off2));
+                const float p0 = ex2_approx(x0.x), p1 = ex2_approx(x0.y), p2 = ex2_approx(x1.x), p3 = ex2_approx(x1.y);
+                sum0 = fadd2(sum0, pack2(p0, p1));
+                sum1 = fadd2(sum1, pack2(p2, p3));
                 big = fmaxf(fmaxf(big, p0), p1);
                 big = fmaxf(fmaxf(big, p2), p3);
                 const __nv_bfloat162 b0 = __floats2bfloat162_rn(p0, p1), b1 = __floats2bfloat162_rn(p2, p3);
@@ -387,7 +386,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
               }
             }
           }
-          ln = l0 + l1;
+          const float2 s2 = unpack2(fadd2(sum0, sum1));
+          ln = s2.x + s2.y;
           return big;
         };
         bool slow = !settled;
@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             float v[16];
             tmem_ld16(s_addr + c0 + 16 * c, v);
             tmem_ld_wait_regs(v);
-            if (border) mask16(v, (uint32_t)(seen >> (16 * c)));
+            if (border) mask16(v, seen >> (16 * c));
 #pragma unroll
             for (int i = 0; i < 16; ++i) top = fmaxf(top, v[i]);
           }
@@ -432,7 +432,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         }
         l += ln;
 #pragma unroll
-        for (int c = 0; c < C::BLK / 32; ++c)
+        for (int c = 0; c < 2; ++c)
           if (c < pieces) tmem_st8(s_addr + c0 + 8 * c, reinterpret_cast<const float(&)[8]>(w[c]));
         tmem_st_wait();
         tc_fence_before();
@@ -466,22 +466,24 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             w[8 * e + (i >> 1)] = *reinterpret_cast<const uint32_t*>(&b);
           }
         }
-        store_rows32(w, a.out + row0 * DV + d, live ? rel : -1, DV, lane);
+        if (live) {
+          uint4* dst = reinterpret_cast<uint4*>(a.out + (row0 + rel) * DV + d);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) dst[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        }
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&o_empty[x]);
       if (half == 0 && live && a.lse != nullptr) a.lse[row0 + rel] = fmaf(mx, 0.6931471805599453f, logf(l));
-      // rows to do again: by the first half's warp, after both halves have stored
-      if (named_bar_or(bar_id, 64, live && odd != 0.f)) {   // NaN compares unequal
-        st_shared(mine, odd);
-        named_bar_sync(bar_id, 64);
-        unsigned again = __ballot_sync(0xffffffffu, live && half == 0 && (odd != 0.f || ld_shared(other) != 0.f));
-        while (again) {
-          const int src = __ffs((int)again) - 1;
-          again &= again - 1;
-          fwd_row<DQK / 64, DV / 64>(a, __shfl_sync(0xffffffffu, t, src), g * a.G + __shfl_sync(0xffffffffu, r - rq * a.G, src), lane);
-        }
+      // rows to do again, each half its own columns (NaN compares unequal), after the stores above
+      __syncwarp();
+      unsigned again = __ballot_sync(0xffffffffu, live && odd != 0.f);
+      while (again) {
+        const int src = __ffs((int)again) - 1;
+        again &= again - 1;
+        fwd_row<DQK / 64, DV / 64>(a, __shfl_sync(0xffffffffu, t, src), g * a.G + __shfl_sync(0xffffffffu, r - rq * a.G, src),
+                                   lane, half * (DV / 2), DV / 2, half == 0);
       }
     }
   }
