@@ -39,7 +39,7 @@ constexpr int kCols = 64;               // (query, head) rows a block (dk, dv)
 constexpr uint32_t kAtom = 128 * 128;   // 128 rows x 64 bf16
 constexpr uint32_t kAtom64 = 64 * 128;  // 64 rows x 64 bf16
 constexpr int kDqThreads = 448;         // warps 0-7: score warps; 8: TMA; 9: MMA; 10-13: helpers
-constexpr int kBwdThreads = 320;        // warps 0-7: score warps; 8: TMA; 9: MMA
+constexpr int kDkvThreads = 576;        // warps 0-15: score warps; 16: TMA; 17: MMA
 
 __device__ __forceinline__ void wait_landed(uint64_t* bar, uint32_t parity) {
   const unsigned long long t0 = globaltimer_ns();
@@ -546,7 +546,7 @@ __device__ __forceinline__ DkvItem dkv_item(const WinArgs& a, const WinSinks& sk
 }
 
 template <int DQK, int DV>
-__global__ void __launch_bounds__(kBwdThreads, 1)
+__global__ void __launch_bounds__(kDkvThreads, 1)
     window_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
                       const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, WinArgs a,
                       WinSinks sk, int tiles) {
@@ -575,21 +575,21 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const int nhc = (a.G + kCols - 1) / kCols;     // blocks that share their queries
   // stage rows that no copy writes (64 not a multiple of the heads) meet weights of 0
   if (qt * hc < kCols) {
-    for (uint32_t i = tid; i < ST * C::st_bytes / 16u; i += kBwdThreads)
+    for (uint32_t i = tid; i < ST * C::st_bytes / 16u; i += kDkvThreads)
       reinterpret_cast<uint4*>(smem + C::st_off)[i] = make_uint4(0, 0, 0, 0);
     fence_proxy_async_smem();
   }
   if (tid == 0) {
     mbar_init(kv_full, 1); mbar_init(kv_empty, 1);
     for (int i = 0; i < 4; ++i) { mbar_init(&st_full[i], 33); mbar_init(&st_empty[i], 1); }
-    mbar_init(sp_full, 1); mbar_init(sp_empty, 8);
-    mbar_init(pd_full, 8); mbar_init(pd_empty, 1);
-    mbar_init(acc_full, 1); mbar_init(acc_empty, 8);
+    mbar_init(sp_full, 1); mbar_init(sp_empty, 16);
+    mbar_init(pd_full, 16); mbar_init(pd_empty, 1);
+    mbar_init(acc_full, 1); mbar_init(acc_empty, 16);
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 9) {
+  if (warp == 17) {
     tmem_alloc(tslot, 512);
     tmem_relinquish();
   }
@@ -600,7 +600,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const int units = tiles + (a.sinks > 0 && sk.slots > 0 ? min(sk.chunk0[a.ndocs], sk.chunks) : 0);
   const int items = units * a.Hkv;
 
-  if (warp == 8) {
+  if (warp == 16) {
     // ---------------- producer: TMA by lane 0, lse and D by all ----------------
     if (lane == 0) {
       tma_prefetch_map(&tm_q);
@@ -652,7 +652,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       if (ni > 0) wait_landed(kv_full, (ni - 1) & 1);
       for (uint32_t i = ns > ST ? ns - ST : 0; i < ns; ++i) wait_landed(&st_full[i % ST], (i / ST) & 1);
     }
-  } else if (warp == 9) {
+  } else if (warp == 17) {
     // ---------------- MMA issuer (the whole warp; one elected lane issues) ----------------
     constexpr uint32_t S_IDESC = idesc_bf16(128, kCols, false, false);
     constexpr uint32_t DV_IDESC = idesc_bf16(128, DV, false, true), DK_IDESC = idesc_bf16(128, DQK, false, true);
@@ -700,8 +700,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     wait_landed(drain, 0);
     __syncwarp();
   } else {
-    // ---------------- score warps: key = TMEM lane, 32 of a block's 64 rows each ----------------
-    const int half = warp >> 2;
+    // ---------------- score warps: key = TMEM lane, 16 of a block's 64 rows each ----------------
+    const int quart = warp >> 2;
     const int r = (warp & 3) * 32 + lane;
     const uint32_t lanes = tmem_lane_base(warp);
     uint32_t nb = 0, ni = 0;
@@ -741,18 +741,18 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           break;
         }
         tc_fence_after();
-        float sc[32], dp[32];
-        tmem_ld32(tbase + C::S0 + lanes + 32 * half, sc);
-        tmem_ld32(tbase + C::P0 + lanes + 32 * half, dp);
+        float sc[16], dp[16];
+        tmem_ld16(tbase + C::S0 + lanes + 16 * quart, sc);
+        tmem_ld16(tbase + C::P0 + lanes + 16 * quart, dp);
         tmem_ld_wait_regs(sc);
         tmem_ld_wait_regs(dp);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(sp_empty);
-        const float4* l4 = reinterpret_cast<const float4*>(ld + st * 2 * kCols + 32 * half);
-        const float4* d4 = reinterpret_cast<const float4*>(ld + st * 2 * kCols + kCols + 32 * half);
+        const float4* l4 = reinterpret_cast<const float4*>(ld + st * 2 * kCols + 16 * quart);
+        const float4* d4 = reinterpret_cast<const float4*>(ld + st * 2 * kCols + kCols + 16 * quart);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 4; ++i) {
           const float4 l = l4[i], d = d4[i];
           const float lv[4] = {l.x, l.y, l.z, l.w}, dv[4] = {d.x, d.y, d.z, d.w};
 #pragma unroll
@@ -763,23 +763,23 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           }
         }
         if (!whole) {
+          const uint32_t in = bit_range32(c0 - 16 * quart, min(c1 - 16 * quart, 16));
 #pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            const bool in = c + 32 * half >= c0 && c + 32 * half < c1;
-            sc[c] = in ? sc[c] : 0.f;
-            dp[c] = in ? dp[c] : 0.f;
+          for (int c = 0; c < 16; ++c) {
+            sc[c] = (in >> c) & 1u ? sc[c] : 0.f;
+            dp[c] = (in >> c) & 1u ? dp[c] : 0.f;
           }
         }
-        float w[16], x[16];
+        float w[8], x[8];
 #pragma unroll
-        for (int c = 0; c < 32; c += 2) {
+        for (int c = 0; c < 16; c += 2) {
           const __nv_bfloat162 p = __floats2bfloat162_rn(sc[c], sc[c + 1]), q = __floats2bfloat162_rn(dp[c], dp[c + 1]);
           w[c >> 1] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&p));
           x[c >> 1] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&q));
         }
         if (nb > 0 && !__all_sync(0xffffffffu, mbar_wait(pd_empty, (nb - 1) & 1, abort_flag, a.err))) { alive = false; break; }
-        tmem_st16(tbase + C::PW0 + lanes + 16 * half, w);
-        tmem_st16(tbase + C::DS0 + lanes + 16 * half, x);
+        tmem_st8(tbase + C::PW0 + lanes + 8 * quart, w);
+        tmem_st8(tbase + C::DS0 + lanes + 8 * quart, x);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -788,34 +788,36 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       if (!alive) break;
       if (!__all_sync(0xffffffffu, mbar_wait(acc_full, ni & 1, abort_flag, a.err))) break;
       tc_fence_after();
-      // ---- this key's sums: half 0 dv, half 1 dk ----
+      // ---- this key's sums [dk | dv], pieces of 32 columns in turn ----
       const bool far = m.chunk >= 0 || (s - doc.start < a.sinks && doc.end - doc.start > a.window && sk.slots > 0);
-      float* part = nullptr;   // FP32 rows [DQK | DV] of first tokens
+      float* part = nullptr;   // FP32 rows of first tokens
       if (m.chunk >= 0) part = sk.part + (((int64_t)m.chunk * a.Hkv + m.g) * a.sinks + r) * (DQK + DV);
       else if (live && far) part = sk.base + (((int64_t)sk.slot[di] * a.Hkv + m.g) * a.sinks + (s - doc.start)) * (DQK + DV);
       const int64_t row = (int64_t)s * a.Hkv + m.g;
-      float odd = 0.f;
+      float odd_k = 0.f, odd_v = 0.f;
 #pragma unroll 1
-      for (int d = 0; d < (half == 0 ? DV : DQK); d += 32) {
+      for (int d = 32 * quart; d < DQK + DV; d += 128) {
+        const bool is_k = d < DQK;
         float o[32];
-        tmem_ld32(tbase + (half == 0 ? C::DV0 : C::DK0) + lanes + d, o);
+        tmem_ld32(tbase + (is_k ? C::DK0 + d : C::DV0 + (d - DQK)) + lanes, o);
         tmem_ld_wait_regs(o);
-        const float f = half == 0 ? 1.f : a.scale;
+        const float f = is_k ? a.scale : 1.f;
         if (live && far) {
-          float* dst = part + (half == 0 ? DQK : 0) + d;
 #pragma unroll
           for (int i = 0; i < 32; i += 4)
-            *reinterpret_cast<float4*>(dst + i) = make_float4(o[i] * f, o[i + 1] * f, o[i + 2] * f, o[i + 3] * f);
+            *reinterpret_cast<float4*>(part + d + i) = make_float4(o[i] * f, o[i + 1] * f, o[i + 2] * f, o[i + 3] * f);
         } else {
           uint32_t w[16];
+          float odd = 0.f;
 #pragma unroll
           for (int i = 0; i < 32; i += 2) {
             odd = fmaf(o[i], 0.f, fmaf(o[i + 1], 0.f, odd));
             const __nv_bfloat162 b = __floats2bfloat162_rn(o[i] * f, o[i + 1] * f);
             w[i >> 1] = *reinterpret_cast<const uint32_t*>(&b);
           }
+          if (is_k) odd_k += odd; else odd_v += odd;
           if (live) {
-            uint4* dst = reinterpret_cast<uint4*>(half == 0 ? a.dv + row * DV + d : a.dk + row * DQK + d);
+            uint4* dst = reinterpret_cast<uint4*>(is_k ? a.dk + row * DQK + d : a.dv + row * DV + (d - DQK));
 #pragma unroll
             for (int i = 0; i < 4; ++i) dst[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
           }
@@ -824,18 +826,19 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(acc_empty);
-      // a key is done again by the half whose sums are not finite, each its own output
-      unsigned again = __ballot_sync(0xffffffffu, live && !far && odd != 0.f);
+      // keys whose sums are not finite (NaN compares unequal) are done again, each warp the
+      // columns it stored
+      unsigned again = __ballot_sync(0xffffffffu, live && !far && (odd_k != 0.f || odd_v != 0.f));
       while (again) {
         const int src = __ffs((int)again) - 1;
         again &= again - 1;
-        dkv_row<DQK / 64, DV / 64>(a, __shfl_sync(0xffffffffu, s, src), m.g, lane, half == 1, half == 0);
+        dkv_row<DQK / 64, DV / 64>(a, __shfl_sync(0xffffffffu, s, src), m.g, lane, 32 * quart, 128);
       }
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == 17) {
     tc_fence_after();
     tmem_dealloc(tbase, 512);
   }
@@ -913,7 +916,7 @@ __global__ void __launch_bounds__(128) window_join_kernel(WinArgs a, WinSinks sk
     if (x < DQK) a.dk[row * DQK + x] = __float2bfloat16_rn(s);
     else a.dv[row * DV + x - DQK] = __float2bfloat16_rn(s);
   }
-  if (__syncthreads_or(odd != 0.f) && threadIdx.x < 32) dkv_row<DQK / 64, DV / 64>(a, start + i, g, threadIdx.x, true, true);
+  if (__syncthreads_or(odd != 0.f) && threadIdx.x < 32) dkv_row<DQK / 64, DV / 64>(a, start + i, g, threadIdx.x);
 }
 
 }  // namespace
@@ -945,7 +948,7 @@ cudaError_t launch_bwd(const WinBwdMaps& m, const WinArgs& a, const WinSinks& sk
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   const int64_t kitems = ((int64_t)ktiles + sk.chunks) * a.Hkv;
-  window_dkv_kernel<DQK, DV><<<kitems < num_sms ? (int)kitems : num_sms, kBwdThreads, K::total, stream>>>(m.q2, m.dout2, m.k, m.v, a, sk, ktiles);
+  window_dkv_kernel<DQK, DV><<<kitems < num_sms ? (int)kitems : num_sms, kDkvThreads, K::total, stream>>>(m.q2, m.dout2, m.k, m.v, a, sk, ktiles);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if (sk.slots > 0)
     window_join_kernel<DQK, DV><<<(unsigned)(sk.slots * a.Hkv * a.sinks), 128, 0, stream>>>(a, sk);

@@ -127,8 +127,10 @@ __device__ __noinline__ void dq_row(const WinArgs& a, int t, int h, int lane) {
   store_row<NQ>(acc, a.scale, a.dq + row * (64 * NQ), lane);
 }
 
+// Writes the columns of [dk | dv] whose piece of 32 is `first`'s, or lies `step` columns from it
+// and so on; by default all.
 template <int NQ, int NV>
-__device__ __noinline__ void dkv_row(const WinArgs& a, int s, int g, int lane, bool want_dk = true, bool want_dv = true) {
+__device__ __noinline__ void dkv_row(const WinArgs& a, int s, int g, int lane, int first = 0, int step = 32) {
   const WinDoc doc = window_doc(a.cu, a.ndocs, a.T, s);
   const int64_t last = (int64_t)s + a.window;   // first query past the window
   const int end = s - doc.start < a.sinks || last > doc.end ? doc.end : (int)last;
@@ -152,8 +154,18 @@ __device__ __noinline__ void dkv_row(const WinArgs& a, int s, int g, int lane, b
     }
   }
   const int64_t row = (int64_t)s * a.Hkv + g;
-  if (want_dk) store_row<NQ>(dk, a.scale, a.dk + row * (64 * NQ), lane);
-  if (want_dv) store_row<NV>(dv, 1.f, a.dv + row * (64 * NV), lane);
+#pragma unroll
+  for (int i = 0; i < NQ; ++i) {
+    const int d = 64 * i + 2 * lane;
+    if (((d & ~31) - first) % step == 0)
+      *reinterpret_cast<__nv_bfloat162*>(a.dk + row * (64 * NQ) + d) = __floats2bfloat162_rn(dk[i].x * a.scale, dk[i].y * a.scale);
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int d = 64 * i + 2 * lane;
+    if ((((64 * NQ + d) & ~31) - first) % step == 0)
+      *reinterpret_cast<__nv_bfloat162*>(a.dv + row * (64 * NV) + d) = __floats2bfloat162_rn(dv[i].x, dv[i].y);
+  }
 }
 
 }  // namespace
