@@ -19,7 +19,14 @@
 // * dk, dv: rows are 128 keys, columns the rows (query, head) that see them, 64 at a time:
 //   S^T = K Q^T, dP^T = V dO^T; P^T and dS^T return to TMEM as bf16, first operands of
 //   dV += P^T dO and dK += dS^T Q. With Dqk = 192 and Dv = 128 the TMEM is full to the last
-//   column: 64 + 64 scores, 32 + 32 weights, 128 + 192 sums.
+//   column: 64 + 64 scores, 32 + 32 weights, 128 + 192 sums. One warp issues the scores,
+//   another the sums: a wait that succeeds at once still costs the issuer 115 cycles, and so
+//   one's waits lie under the other's products. Copies, and the loads of lse and D, have a
+//   warp each: together in one warp the loads' 1,300 cycles a block held the copies up.
+//   Each tile starts at another of its query blocks (dkv_item). At T 32768, 64 / 4 heads of
+//   192 / 128, window 512, 4 first tokens: one issuer and one loading warp 1.63 ms, split
+//   1.56, tiles in step 1.46 (4.1 GB from DRAM); the products alone, at the rates measured
+//   for these shapes, take 1.14.
 // * First tokens are seen by every later query of their document, so their sums are long.
 //   Queries beyond the window are cut into stretches, each an item of its own (one tile of
 //   first-token keys) with FP32 partial sums in the workspace; a small kernel adds a first
@@ -39,7 +46,7 @@ constexpr int kCols = 64;               // (query, head) rows a block (dk, dv)
 constexpr uint32_t kAtom = 128 * 128;   // 128 rows x 64 bf16
 constexpr uint32_t kAtom64 = 64 * 128;  // 64 rows x 64 bf16
 constexpr int kDqThreads = 448;         // warps 0-7: score warps; 8: TMA; 9: MMA; 10-13: helpers
-constexpr int kDkvThreads = 576;        // warps 0-15: score warps; 16: TMA; 17: MMA
+constexpr int kDkvThreads = 640;        // warps 0-15: score warps; 16: lse and D; 17, 18: MMA; 19: TMA
 
 __device__ __forceinline__ void wait_landed(uint64_t* bar, uint32_t parity) {
   const unsigned long long t0 = globaltimer_ns();
@@ -509,6 +516,22 @@ struct DkvItem {
   int t0, t1;       // queries
   int g, chunk;     // KV head; stretch of far queries of first tokens, or -1
   int nblk;
+  int off;          // the block of queries to start with
+};
+
+// The blocks of an item in turn: `tb` its first query, `hb` its first head of the group. From
+// query block `off` on, around the end: key tiles in flight stand at the same place of a period
+// as long as their range, so that the tiles that see a query load it at about the same time.
+struct DkvWalk {
+  int tb, hb;
+  __device__ __forceinline__ DkvWalk(const DkvItem& m, int qt) : tb(m.t0 + m.off * qt), hb(0) {}
+  __device__ __forceinline__ void next(const DkvItem& m, int qt, int hc, int G) {
+    hb += hc;
+    if (hb < G) return;
+    hb = 0;
+    tb += qt;
+    if (tb >= m.t1) tb = m.t0;
+  }
 };
 
 // Queries of one stretch beyond the window.
@@ -541,7 +564,11 @@ __device__ __forceinline__ DkvItem dkv_item(const WinArgs& a, const WinSinks& sk
     m.t1 = min(end, m.t0 + n);
   }
   m.t1 = max(m.t1, m.t0 + 1);   // only where cu_seqlens is malformed
-  m.nblk = (m.t1 - m.t0 + qt - 1) / qt * nhc;
+  const int nq = (m.t1 - m.t0 + qt - 1) / qt;
+  m.nblk = nq * nhc;
+  const int period = (int)min((int64_t)a.window + kBlk - 1, (int64_t)a.T) / qt + 1;
+  const int at = m.t0 / qt % period;
+  m.off = m.chunk < 0 && at > 0 && period - at < nq ? period - at : 0;
   return m;
 }
 
@@ -565,8 +592,8 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
   uint64_t* pd_empty = pd_full + 1;    // ... have been read by the products
   uint64_t* acc_full = pd_empty + 1;
   uint64_t* acc_empty = acc_full + 1;
-  uint64_t* drain = acc_empty + 1;
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* drain = acc_empty + 1;     // [2]
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(drain + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -585,7 +612,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     mbar_init(sp_full, 1); mbar_init(sp_empty, 16);
     mbar_init(pd_full, 16); mbar_init(pd_empty, 1);
     mbar_init(acc_full, 1); mbar_init(acc_empty, 16);
-    mbar_init(drain, 1);
+    mbar_init(&drain[0], 1); mbar_init(&drain[1], 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -601,103 +628,118 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
   const int items = units * a.Hkv;
 
   if (warp == 16) {
-    // ---------------- producer: TMA by lane 0, lse and D by all ----------------
+    // ---------------- lse and D of each stage's rows ----------------
+    // (a warp of its own: the copies below need not wait for what these loads take)
+    uint32_t ns = 0, st = 0, ph = 0;
+    // the lane's two rows of a block: query, head, and row of lse relative to the block's first (-1: none)
+    int cq[2], ch[2], crow[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int c = lane + 32 * i;
+      cq[i] = c / hc;
+      ch[i] = c - cq[i] * hc;
+      crow[i] = c < qt * hc ? cq[i] * a.Hq + ch[i] : -1;
+    }
+    bool ok = true;
+    for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
+      const DkvItem m = dkv_item(a, sk, item, tiles, qt, nhc);
+      DkvWalk at(m, qt);
+      for (int b = 0; b < m.nblk; ++b, ++ns, at.next(m, qt, hc, a.G)) {
+        const int64_t base = (int64_t)at.tb * a.Hq + m.g * a.G + at.hb;
+        float v[4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const bool in = crow[i] >= 0 && at.tb + cq[i] < a.T && at.hb + ch[i] < a.G;
+          v[2 * i] = in ? a.lse_in[base + crow[i]] : 0.f;   // scaled where it is stored: nothing waits for it here
+          v[2 * i + 1] = in ? a.delta[base + crow[i]] : 0.f;
+        }
+        if (ns >= ST && !__all_sync(0xffffffffu, mbar_wait(&st_empty[st], ph ^ 1u, abort_flag, a.err))) { ok = false; break; }
+        float* l = ld + st * 2 * kCols;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          l[lane + 32 * i] = v[2 * i] * kLog2e;
+          l[kCols + lane + 32 * i] = v[2 * i + 1];
+        }
+        mbar_arrive(&st_full[st]);
+        if (++st == ST) { st = 0; ph ^= 1u; }
+      }
+    }
+  } else if (warp == 19) {
+    // ---------------- copies, by lane 0 ----------------
     if (lane == 0) {
       tma_prefetch_map(&tm_q);
       tma_prefetch_map(&tm_do);
       tma_prefetch_map(&tm_k);
       tma_prefetch_map(&tm_v);
-    }
-    const uint32_t box = (uint32_t)(qt * hc) * 128u * (C::QA + C::VA);
-    uint32_t ni = 0, ns = 0;
-    bool ok = true;
-    for (int item = blockIdx.x; item < items && ok; item += gridDim.x, ++ni) {
-      const DkvItem m = dkv_item(a, sk, item, tiles, qt, nhc);
-      if (ni > 0 && !__all_sync(0xffffffffu, mbar_wait(kv_empty, (ni - 1) & 1, abort_flag, a.err))) break;
-      if (lane == 0) {
+      const uint32_t box = (uint32_t)(qt * hc) * 128u * (C::QA + C::VA);
+      uint32_t ni = 0, ns = 0, st = 0, ph = 0;
+      bool ok = true;
+      for (int item = blockIdx.x; item < items && ok; item += gridDim.x, ++ni) {
+        const DkvItem m = dkv_item(a, sk, item, tiles, qt, nhc);
+        if (ni > 0 && !mbar_wait(kv_empty, (ni - 1) & 1, abort_flag, a.err)) break;
         mbar_arrive_expect_tx(kv_full, C::k_bytes + C::v_bytes);
         for (int c = 0; c < C::QA; ++c) tma_load_3d(smem + c * kAtom, &tm_k, c * 64, m.g, m.s0, kv_full);
         for (int c = 0; c < C::VA; ++c) tma_load_3d(smem + C::k_bytes + c * kAtom, &tm_v, c * 64, m.g, m.s0, kv_full);
-      }
-      for (int b = 0; b < m.nblk; ++b, ++ns) {
-        const uint32_t st = ns % ST;
-        const int tb = m.t0 + b / nhc * qt, hb = b % nhc * hc;
-        float v[4];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int c = lane + 32 * i, t = tb + c / hc, h = hb + c % hc;
-          const bool in = c < qt * hc && t < a.T && h < a.G;
-          const int64_t row = (int64_t)t * a.Hq + m.g * a.G + h;
-          v[2 * i] = in ? a.lse_in[row] * kLog2e : 0.f;
-          v[2 * i + 1] = in ? a.delta[row] : 0.f;
-        }
-        if (ns >= ST && !__all_sync(0xffffffffu, mbar_wait(&st_empty[st], (ns / ST - 1) & 1, abort_flag, a.err))) { ok = false; break; }
-        if (lane == 0) {
+        DkvWalk at(m, qt);
+        for (int b = 0; b < m.nblk; ++b, ++ns, at.next(m, qt, hc, a.G)) {
+          if (ns >= ST && !mbar_wait(&st_empty[st], ph ^ 1u, abort_flag, a.err)) { ok = false; break; }
           mbar_arrive_expect_tx(&st_full[st], box);
           uint8_t* dst = smem + C::st_off + st * C::st_bytes;
-          for (int c = 0; c < C::QA; ++c) tma_load_3d(dst + c * kAtom64, &tm_q, c * 64, m.g * a.G + hb, tb, &st_full[st]);
+          for (int c = 0; c < C::QA; ++c) tma_load_3d(dst + c * kAtom64, &tm_q, c * 64, m.g * a.G + at.hb, at.tb, &st_full[st]);
           for (int c = 0; c < C::VA; ++c)
-            tma_load_3d(dst + C::q_bytes + c * kAtom64, &tm_do, c * 64, m.g * a.G + hb, tb, &st_full[st]);
+            tma_load_3d(dst + C::q_bytes + c * kAtom64, &tm_do, c * 64, m.g * a.G + at.hb, at.tb, &st_full[st]);
+          if (++st == ST) { st = 0; ph ^= 1u; }
         }
-        float* l = ld + st * 2 * kCols;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          l[lane + 32 * i] = v[2 * i];
-          l[kCols + lane + 32 * i] = v[2 * i + 1];
-        }
-        mbar_arrive(&st_full[st]);
+      }
+      if (*abort_flag) {
+        if (ni > 0) wait_landed(kv_full, (ni - 1) & 1);
+        for (uint32_t i = ns > ST ? ns - ST : 0; i < ns; ++i) wait_landed(&st_full[i % ST], (i / ST) & 1);
       }
     }
-    if (*abort_flag && lane == 0) {
-      if (ni > 0) wait_landed(kv_full, (ni - 1) & 1);
-      for (uint32_t i = ns > ST ? ns - ST : 0; i < ns; ++i) wait_landed(&st_full[i % ST], (i / ST) & 1);
-    }
-  } else if (warp == 17) {
-    // ---------------- MMA issuer (the whole warp; one elected lane issues) ----------------
-    constexpr uint32_t S_IDESC = idesc_bf16(128, kCols, false, false);
-    constexpr uint32_t DV_IDESC = idesc_bf16(128, DV, false, true), DK_IDESC = idesc_bf16(128, DQK, false, true);
+  } else if (warp > 16) {
+    // ---------------- MMA issuers (a whole warp each; one elected lane issues) ----------------
+    // One warp issues the scores and dP, another dv and dk: each one's waits (115 cycles even
+    // where nothing is waited for) lie under the other's products.
     const uint32_t sb = smem_u32(smem), tb = (uint32_t)uniform((int)tbase);
     auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, a.err)); };
-    uint32_t nsc = 0, npd = 0, ni = 0, sst = 0, sph = 0, pst = 0;   // blocks scored, blocks summed, items; ring places
+    uint32_t n = 0, ni = 0, st = 0, ph = 0;   // blocks, items; ring
     bool alive = true;
-    auto scores = [&]() {
-      if (!wait(&st_full[sst], sph)) return false;
-      if (nsc > 0 && !wait(sp_empty, (nsc - 1) & 1)) return false;
-      tc_fence_after();
-      const uint32_t q = sb + C::st_off + sst * C::st_bytes;
-      ss_run<C::QA>(tb + C::S0, sb, kAtom, q, kAtom64, S_IDESC);
-      ss_run<C::VA>(tb + C::P0, sb + C::k_bytes, kAtom, q + C::q_bytes, kAtom64, S_IDESC);
-      umma_commit_warp(sp_full);
-      ++nsc;
-      if (++sst == ST) { sst = 0; sph ^= 1u; }
-      return true;
-    };
-    for (int item = blockIdx.x; item < items && alive; item += gridDim.x, ++ni) {
-      const int nblk = uniform(dkv_item(a, sk, item, tiles, qt, nhc).nblk);
-      if (!wait(kv_full, ni & 1)) break;
-      if (!scores()) break;
-      if (nblk == 1) umma_commit_warp(kv_empty);
-      for (int b = 0; b < nblk; ++b) {
-        if (b + 1 < nblk) {
-          if (!scores()) { alive = false; break; }
-          if (b + 2 == nblk) umma_commit_warp(kv_empty);
+    if (warp == 17) {
+      constexpr uint32_t S_IDESC = idesc_bf16(128, kCols, false, false);
+      for (int item = blockIdx.x; item < items && alive; item += gridDim.x, ++ni) {
+        const int nblk = uniform(dkv_item(a, sk, item, tiles, qt, nhc).nblk);
+        if (!wait(kv_full, ni & 1)) break;
+        for (int b = 0; b < nblk; ++b, ++n) {
+          if (!wait(&st_full[st], ph) || (n > 0 && !wait(sp_empty, (n - 1) & 1))) { alive = false; break; }
+          tc_fence_after();
+          const uint32_t q = sb + C::st_off + st * C::st_bytes;
+          ss_run<C::QA>(tb + C::S0, sb, kAtom, q, kAtom64, S_IDESC);
+          ss_run<C::VA>(tb + C::P0, sb + C::k_bytes, kAtom, q + C::q_bytes, kAtom64, S_IDESC);
+          umma_commit_warp(sp_full);
+          if (++st == ST) { st = 0; ph ^= 1u; }
         }
-        if (!wait(pd_full, npd & 1)) { alive = false; break; }
-        if (b == 0 && ni > 0 && !wait(acc_empty, (ni - 1) & 1)) { alive = false; break; }
-        tc_fence_after();
-        const uint32_t q = sb + C::st_off + pst * C::st_bytes;
-        ts_run<4>(tb + C::DV0, tb + C::PW0, q + C::q_bytes, kAtom64, DV_IDESC, b > 0);
-        ts_run<4>(tb + C::DK0, tb + C::DS0, q, kAtom64, DK_IDESC, b > 0);
-        umma_commit_warp(pd_empty);
-        umma_commit_warp(&st_empty[pst]);
-        ++npd;
-        if (++pst == ST) pst = 0;
+        umma_commit_warp(kv_empty);
       }
-      if (!alive) break;
-      umma_commit_warp(acc_full);
+    } else {
+      constexpr uint32_t DV_IDESC = idesc_bf16(128, DV, false, true), DK_IDESC = idesc_bf16(128, DQK, false, true);
+      for (int item = blockIdx.x; item < items && alive; item += gridDim.x, ++ni) {
+        const int nblk = uniform(dkv_item(a, sk, item, tiles, qt, nhc).nblk);
+        for (int b = 0; b < nblk; ++b, ++n) {
+          if (!wait(pd_full, n & 1) || (b == 0 && ni > 0 && !wait(acc_empty, (ni - 1) & 1))) { alive = false; break; }
+          tc_fence_after();
+          const uint32_t q = sb + C::st_off + st * C::st_bytes;
+          ts_run<4>(tb + C::DV0, tb + C::PW0, q + C::q_bytes, kAtom64, DV_IDESC, b > 0);
+          ts_run<4>(tb + C::DK0, tb + C::DS0, q, kAtom64, DK_IDESC, b > 0);
+          umma_commit_warp(pd_empty);
+          umma_commit_warp(&st_empty[st]);
+          if (++st == ST) st = 0;
+        }
+        if (!alive) break;
+        umma_commit_warp(acc_full);
+      }
     }
-    umma_commit_warp(drain);
-    wait_landed(drain, 0);
+    umma_commit_warp(&drain[warp - 17]);
+    wait_landed(&drain[warp - 17], 0);
     __syncwarp();
   } else {
     // ---------------- score warps: key = TMEM lane, 16 of a block's 64 rows each ----------------
@@ -713,28 +755,26 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
       int di = 0;
       const WinDoc doc = window_doc(a.cu, a.ndocs, a.T, min(s, a.T - 1), &di);
       // this key's queries of the item: [from, to)
-      const int64_t past = (int64_t)s + a.window;
-      const int from = m.chunk < 0 ? s : (int)min(past, (int64_t)m.t1);
-      const int to = m.chunk < 0 ? (int)min(past, (int64_t)doc.end) : m.t1;
+      const int past = (int)min((int64_t)s + a.window, (int64_t)(m.chunk < 0 ? doc.end : m.t1));
+      const int from = m.chunk < 0 ? s : past;
+      const int to = m.chunk < 0 ? past : m.t1;
       // a block is whole when every key of the tile sees every row
       int all0, all1;
       if (m.chunk < 0) {
         const WinDoc d0 = window_doc(a.cu, a.ndocs, a.T, m.s0);
         all0 = m.s0 + m.keys - 1;
-        all1 = (int)min((int64_t)m.s0 + a.window, (int64_t)d0.end);
+        all1 = (int)min((int64_t)m.s0 + a.window, (int64_t)d0.end) - qt;
       } else {
         all0 = (int)min((int64_t)m.s0 + m.keys - 1 + a.window, (int64_t)m.t1);
-        all1 = m.t1;
+        all1 = m.t1 - qt;
       }
-      for (int b = 0; b < m.nblk; ++b, ++nb) {
+      DkvWalk at(m, qt);
+      for (int b = 0; b < m.nblk; ++b, ++nb, at.next(m, qt, hc, a.G)) {
         const uint32_t st = nb % ST;
-        const int tb = m.t0 + b / nhc * qt, valid = min(qt * hc, a.G - b % nhc * hc < hc ? a.G - b % nhc * hc : qt * hc);
-        const bool whole = tb >= all0 && tb + qt <= all1 && valid == kCols;
-        int c0 = 0, c1 = kCols;
-        if (!whole) {
-          c0 = max(from - tb, 0) * hc;
-          c1 = min(valid, max(min(to - tb, qt), 0) * hc);
-        }
+        const int tb = at.tb, valid = a.G - at.hb < hc ? a.G - at.hb : qt * hc;
+        uint32_t in = 0xffffu;   // which of this warp's rows the key sees
+        if (!(tb >= all0 && tb <= all1 && valid == kCols))
+          in = bit_range32(max(from - tb, 0) * hc - 16 * quart, min(min(valid, max(min(to - tb, qt), 0) * hc) - 16 * quart, 16));
         if (!__all_sync(0xffffffffu, mbar_wait(&st_full[st], (nb / ST) & 1, abort_flag, a.err) &&
                                          mbar_wait(sp_full, nb & 1, abort_flag, a.err))) {
           alive = false;
@@ -762,8 +802,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
             dp[c] = sc[c] * (dp[c] - dv[k]);
           }
         }
-        if (!whole) {
-          const uint32_t in = bit_range32(c0 - 16 * quart, min(c1 - 16 * quart, 16));
+        if (in != 0xffffu) {
 #pragma unroll
           for (int c = 0; c < 16; ++c) {
             sc[c] = (in >> c) & 1u ? sc[c] : 0.f;
