@@ -542,12 +542,15 @@ cudaError_t launch_decode(const PagedArgs& a, int num_sms, bool* configured, cud
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // few pairs may have hundreds of parts each: a row a block, the parts over 1024 threads;
-  // many pairs have a few parts: rows over the threads
+  // many pairs have a few parts: every row at once, up to 512 threads
   const int pairs = a.B * a.Hkv * nhb;
   const bool few = pairs < num_sms;
+  const int rows = a.G < kHeads ? a.G : kHeads;
+  int threads = few ? 1024 : (rows * (DV / 4) + 31) / 32 * 32;
+  if (!few && threads > 512) threads = 512;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)pairs, few ? (unsigned)(a.G < kHeads ? a.G : kHeads) : 1u);
-  cfg.blockDim = dim3(few ? 1024 : 256);
+  cfg.gridDim = dim3((unsigned)pairs, few ? (unsigned)rows : 1u);
+  cfg.blockDim = dim3((unsigned)threads);
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
