@@ -447,3 +447,95 @@ def test_prompt_then_steps_together(irs):
     R.check(out, ref[0], ref[2], "routed step")
     assert ((out.cpu().double() - dense.cpu().double()).abs() <= 2 * ref[2]).all()
     assert (lse - dense_l).abs().max() <= 1e-4
+
+
+@pytest.mark.parametrize("Dqk,Dv,n,start,layout", [(64, 256, 32, 16, "half"), (8, 24, 0, 0, "half"), (200, 8, 16, 8, "interleaved"),
+                                                   (16, 1000, 16, 0, "half"), (256, 64, 256, 0, "interleaved")])
+@pytest.mark.parametrize("new", [[1, 1, 1], [30, 1, 9]])
+def test_append_values_of_other_widths(irs, Dqk, Dv, n, start, layout, new):
+    """Value rows wider and narrower than key rows, odd numbers of 16-byte pieces."""
+    g = torch.Generator().manual_seed(Dqk + Dv)
+    before, page, Hq, Hkv = [0, 17, 31], 16, 3, 2
+    kc, vc, table = _pool(g, [a + m for a, m in zip(before, new)], page, Hkv, Dqk, Dv)
+    T = sum(new)
+    q, k, v = _normal(g, T, Hq, Dqk), _normal(g, T, Hkv, Dqk), _normal(g, T, Hkv, Dv)
+    kd, vd = kc.to(DEV), vc.to(DEV)
+    f = irs.rope_frequencies(n)[0] if n else None
+    cu = None if T == 3 else torch.tensor([0] + new).cumsum(0).to(torch.int32).to(DEV)
+    q_out = irs.paged_rope_append(q.to(DEV), k.to(DEV), v.to(DEV), kd, vd, table.to(DEV),
+                                  torch.tensor(before, dtype=torch.int32, device=DEV), f.to(DEV) if n else None,
+                                  cu_new=cu, layout=layout, start=start)
+    irs.check_device_errors(DEV)
+    pos = torch.cat([torch.arange(a, a + m) for a, m in zip(before, new)])
+    seq = torch.cat([torch.full((m,), b) for b, m in enumerate(new)])
+    slots = (table[seq, pos // page].long(), pos % page)
+    rot = (lambda x: R.rotate(x, pos, f, layout, start, 1.0)) if n else (lambda x: (x.double(), torch.zeros(x.shape)))
+    R.check(q_out, *rot(q), "queries")
+    R.check(kd.cpu()[slots], *rot(k), "keys")
+    assert torch.equal(vd.cpu()[slots], v)
+    kn, vn = kd.cpu(), vd.cpu()
+    kn[slots], vn[slots] = kc[slots], vc[slots]              # nothing else changed
+    assert torch.equal(kn, kc) and torch.equal(vn, vc)
+
+
+def test_append_more_sequences_than_shared_memory_holds(irs):
+    """The sequence of a token is then searched in global memory; some sequences have no new token."""
+    g = torch.Generator().manual_seed(8)
+    B = 5000
+    new = (torch.arange(B) % 3).tolist()
+    T = sum(new)
+    table = torch.randperm(B, generator=g).to(torch.int32)[:, None]
+    kc = torch.zeros(B, 8, 1, 64, dtype=torch.bfloat16)
+    k, v = _normal(g, T, 1, 64), _normal(g, T, 1, 64)
+    cu = torch.tensor([0] + new).cumsum(0).to(torch.int32)
+    before = torch.arange(B, dtype=torch.int32) % 6
+    kd, vd = kc.to(DEV), kc.to(DEV)
+    irs.paged_rope_append(None, k.to(DEV), v.to(DEV), kd, vd, table.to(DEV), before.to(DEV), cu_new=cu.to(DEV))
+    irs.check_device_errors(DEV)
+    seq = torch.repeat_interleave(torch.arange(B), torch.tensor(new))
+    pos = before[seq].long() + torch.arange(T) - cu[seq].long()
+    want_k, want_v = kc.clone(), kc.clone()
+    want_k[table[seq, 0].long(), pos], want_v[table[seq, 0].long(), pos] = k, v
+    assert torch.equal(kd.cpu(), want_k) and torch.equal(vd.cpu(), want_v)
+
+
+def test_decode_more_sequences_than_threads(irs):
+    """Many short sequences: each thread of a block counts the tiles of several, with empty ones among them."""
+    g = torch.Generator().manual_seed(21)
+    lens = torch.randint(0, 40, (1500,), generator=g).tolist()
+    _decode_case(irs, lens, 4, 2, 64, 64, 16)
+
+
+def test_decode_on_two_streams_at_once(irs):
+    g = torch.Generator().manual_seed(14)
+    lens = [3000, 1, 900, 0, 64]
+    kc, vc, table = _pool(g, lens, 16, 2, 128, 128)
+    args = [kc.to(DEV), vc.to(DEV), table.to(DEV), torch.tensor(lens, dtype=torch.int32, device=DEV)]
+    qs = [_normal(g, 5, 8, 128).to(DEV) for _ in range(2)]
+    alone = [irs.paged_gqa_attn_decode(q, *args) for q in qs]
+    streams = [torch.cuda.Stream(DEV) for _ in qs]
+    torch.cuda.synchronize()
+    runs = []
+    for _ in range(6):
+        for s, q in zip(streams, qs):
+            with torch.cuda.stream(s):
+                runs.append(irs.paged_gqa_attn_decode(q, *args))
+    torch.cuda.synchronize()
+    for i, (o, l) in enumerate(runs):
+        assert torch.equal(o, alone[i % 2][0]) and torch.equal(l, alone[i % 2][1])
+    irs.check_device_errors(DEV)
+
+
+def test_decode_one_workspace_for_calls_in_order(irs):
+    """Calls of one stream may share a workspace, whatever their sizes; a short one is replaced."""
+    g = torch.Generator().manual_seed(15)
+    ws = torch.empty(64 << 20, dtype=torch.uint8, device=DEV)
+    for lens in ([2000, 5], [1] * 50, [700] * 9):
+        kc, vc, table = _pool(g, lens, 16, 2, 64, 64)
+        args = [_normal(g, len(lens), 4, 64).to(DEV), kc.to(DEV), vc.to(DEV), table.to(DEV),
+                torch.tensor(lens, dtype=torch.int32, device=DEV)]
+        want = irs.paged_gqa_attn_decode(*args)
+        ws.fill_(255)                                        # NaN, were it read
+        for w in (ws, ws[:64]):
+            got = irs.paged_gqa_attn_decode(*args, workspace=w)
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

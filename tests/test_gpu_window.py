@@ -181,3 +181,79 @@ def test_training_step_captured(irs):
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, step()))
     irs.check_device_errors(DEV)
+
+
+@pytest.mark.parametrize("Hq,Hkv,Dqk,Dv", [(100, 1, 64, 64), (130, 2, 128, 64), (24, 2, 64, 128)])
+def test_groups_that_do_not_fill_tiles(irs, Hq, Hkv, Dqk, Dv):
+    """More query heads a KV head than a block of columns holds, and numbers that do not divide it."""
+    _case(irs, *_inputs(160, Hq, Hkv, Dqk, Dv, [100, 60]), window=33, sinks=3)
+
+
+@pytest.mark.parametrize("Hq,Hkv,Dqk,Dv,window,sinks,longest", [
+    (4, 4, 64, 64, 20, 3, 90), (6, 3, 192, 128, 100, 4, 700), (16, 2, 128, 128, 64, 0, 300), (5, 5, 128, 128, 300, 40, 900)])
+def test_many_tiles_a_block(irs, Hq, Hkv, Dqk, Dv, window, sinks, longest):
+    """Tokens enough that every block of the kernels works through several tiles, over documents of
+    mixed lengths; a sample of the documents, the first and the last among them, is checked."""
+    g = torch.Generator().manual_seed(longest)
+    docs = []
+    while sum(docs) < 24000:
+        docs.append(int(torch.randint(1, longest + 1, (1,), generator=g)))
+    T = sum(docs)
+    q, k, v, do, cu = _inputs(T, Hq, Hkv, Dqk, Dv, docs)
+    dev = [t.to(DEV) for t in (q, k, v, cu, do)]
+    qd, kd, vd, cd, dd = dev
+    out, lse = irs.window_gqa_attn_fwd(qd, kd, vd, cd, window, sinks=sinks)
+    got = irs.window_gqa_attn_bwd(qd, kd, vd, cd, window, out, lse, dd, sinks=sinks)
+    irs.check_device_errors(DEV)
+    oc, lc, gc = out.cpu(), lse.cpu(), [t.cpu() for t in got]
+    scale = 1 / math.sqrt(Dqk)
+    picks = {0, len(docs) - 1} | {int(i) for i in torch.randint(0, len(docs), (18,), generator=g)}
+    for d in sorted(picks):
+        a, b = int(cu[d]), int(cu[d + 1])
+        one = torch.tensor([0, b - a], dtype=torch.int32)
+        x = (q[a:b], k[a:b], v[a:b], one, window, sinks, scale)
+        ref = R.window_fwd(*x)
+        R.check(oc[a:b], ref[0], ref[2], (d, "out"))
+        R.check(lc[a:b], ref[1], ref[3], (d, "lse"))
+        want = R.window_bwd(*x, oc[a:b], lc[a:b], do[a:b])
+        for name, t in zip(("dq", "dk", "dv"), gc):
+            R.check(t[a:b], *want[name], (d, name))
+    for _ in range(3):   # and every run gives the same bits
+        again = irs.window_gqa_attn_fwd(qd, kd, vd, cd, window, sinks=sinks)
+        grads = irs.window_gqa_attn_bwd(qd, kd, vd, cd, window, out, lse, dd, sinks=sinks)
+        assert all(torch.equal(a, b) for a, b in zip((out, lse) + tuple(got), tuple(again) + tuple(grads)))
+
+
+def test_calls_on_two_streams_at_once(irs):
+    q, k, v, do, cu = _inputs(2000, 8, 2, 128, 128, [900, 1100])
+    qd, kd, vd, cd, dd = (t.to(DEV) for t in (q, k, v, cu, do))
+
+    def step(x):
+        out, lse = irs.window_gqa_attn_fwd(x, kd, vd, cd, 200, sinks=4)
+        return (out, lse) + tuple(irs.window_gqa_attn_bwd(x, kd, vd, cd, 200, out, lse, dd, sinks=4))
+
+    xs = [qd, qd.flip(0).contiguous()]
+    alone = [step(x) for x in xs]
+    streams = [torch.cuda.Stream(DEV) for _ in xs]
+    torch.cuda.synchronize()
+    runs = []
+    for _ in range(4):
+        for s, x in zip(streams, xs):
+            with torch.cuda.stream(s):
+                runs.append(step(x))
+    torch.cuda.synchronize()
+    for i, r in enumerate(runs):
+        assert all(torch.equal(a, b) for a, b in zip(r, alone[i % 2]))
+    irs.check_device_errors(DEV)
+
+
+def test_columns_of_a_wider_tensor_and_one_head_of_many(irs):
+    """Rows of one token, and of one head, whose other strides are any number."""
+    q, k, v, do, cu = _inputs(1, 2, 1, 64, 64, [1])
+    wide = lambda t: torch.zeros(t.shape[0], t.shape[1], 200, dtype=t.dtype, device=DEV)  # noqa: E731
+    gpu = []
+    for t in (q, k, v):
+        w = wide(t)
+        w[:, :, 8:72] = t.to(DEV)
+        gpu.append(w[:, :, 8:72])
+    _case(irs, q, k, v, do, cu, 5, 1, gpu=tuple(gpu))
