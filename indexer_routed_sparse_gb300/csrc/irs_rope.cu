@@ -17,7 +17,7 @@
 // and 512 of them an SM have 128 KB on the way. Measured at 16384 tokens of 64 heads of 128:
 // 86 us, 6.3 TB/s (eight heads ahead, 4096 threads an SM in the launch; four heads 93 us,
 // two 97; 2048 threads 87, 8192 103, as the angles are then worked out for few heads each);
-// 12,000 new tokens of 64 / 4 heads of 192 / 128, a third rotated, into pages of 16: 125 us.
+// 14,000 new tokens of 64 / 4 heads of 192 / 128, a third rotated, into pages of 16: 125 us.
 #include "irs_internal.h"
 #include "irs_ptx.cuh"
 
