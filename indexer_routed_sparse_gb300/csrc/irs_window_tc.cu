@@ -50,7 +50,7 @@ namespace {
 constexpr int kRows = 128;           // rows a tile
 constexpr uint32_t kAtom = 128 * 128;   // 128 rows x 64 bf16
 constexpr int kFwdThreads = 608;     // warps 0-7, 8-15: softmax of the two tiles; 16: TMA; 17, 18: MMA of the two tiles
-constexpr float kRaise = 256.f;      // a weight past this raises the maximum
+constexpr float kRaise = 256.f;      // a half row's weights of a block with a sum past this raise the maximum
 
 template <int DQK, int DV>
 struct FwdCfg {
@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           if (sink_blk) seen = ds == m.ds0 ? bit_range32(0, m.ns - C::BLK * j - c0) : 0u;
           if (!live) seen = 0u;
         }
-        // One pass: the weights under the present maximum, and whether one passes 2^8. They
+        // One pass: the weights under the present maximum, and whether their sum passes 2^8. They
         // wait in registers for the two halves' vote; where it asks for it (and for the first
         // blocks, before every row has a maximum) the scores are read again.
         uint32_t w[2][8];
@@ -374,7 +374,6 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           const float off = mx == -INFINITY ? 0.f : -mx;
           const uint64_t sc2 = pack2(a.scale_log2, a.scale_log2), off2 = pack2(off, off);
           uint64_t sum0 = 0ull, sum1 = 0ull;   // FP32 pairs
-          float big = 0.f;
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             if (c < pieces) {
@@ -389,8 +388,6 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 const float p0 = ex2_approx(x0.x), p1 = ex2_approx(x0.y), p2 = ex2_approx(x1.x), p3 = ex2_approx(x1.y);
                 sum0 = fadd2(sum0, pack2(p0, p1));
                 sum1 = fadd2(sum1, pack2(p2, p3));
-                big = fmaxf(fmaxf(big, p0), p1);
-                big = fmaxf(fmaxf(big, p2), p3);
                 const __nv_bfloat162 b0 = __floats2bfloat162_rn(p0, p1), b1 = __floats2bfloat162_rn(p2, p3);
                 w[c][i >> 1] = *reinterpret_cast<const uint32_t*>(&b0);
                 w[c][(i >> 1) + 1] = *reinterpret_cast<const uint32_t*>(&b1);
@@ -399,13 +396,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           }
           const float2 s2 = unpack2(fadd2(sum0, sum1));
           ln = s2.x + s2.y;
-          return big;
         };
         bool slow = !settled;
         if (!slow) {
-          const float big = weights();
+          weights();
           // a row that is none (its queries were never loaded) has no vote
-          slow = named_bar_or(bar_id, 64, (live && big > kRaise) || !alive);
+          slow = named_bar_or(bar_id, 64, (live && ln > kRaise) || !alive);
         }
         if (slow) {
           float top = -INFINITY;
