@@ -699,12 +699,13 @@ def sparse_gqa_attn_fwd_grouped(q: torch.Tensor, k: torch.Tensor, v: torch.Tenso
 # ---------------------------------------------------------------------------------------
 ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
 _raw_stream = torch._C._cuda_getCurrentRawStream   # current_stream() without its Python object: 0.1 us for 2
+_current_device = torch._C._cuda_getDevice
 _BF16, _F32, _F64, _I32 = torch.bfloat16, torch.float32, torch.float64, torch.int32
 
 
 def _call(index: int, what: str, fn, *args) -> None:
     """fn(*args, current stream) with GPU `index` current (the library launches on the current one)."""
-    if torch.cuda.current_device() == index:
+    if _current_device() == index:
         st = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
@@ -727,14 +728,15 @@ def _first(t: torch.Tensor, name: str, dtype: torch.dtype) -> int:
 
 def _look(t: torch.Tensor, name: str, dtype: torch.dtype, ndim: int, index: int):
     """(shape, strides) of a tensor whose last dim is contiguous, its type and place checked."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index:
+        shape, strides = t.shape, t.stride()
+        if len(shape) == ndim and (strides[-1] == 1 or shape[-1] <= 1):
+            return shape, strides
     if _first(t, name, dtype) != index:
         raise ValueError(f"{name} is on {t.device}, not cuda:{index}")
-    shape, strides = t.shape, t.stride()
-    if len(shape) != ndim:
-        raise ValueError(f"{name} must have {ndim} dims, got shape {tuple(shape)}")
-    if strides[-1] != 1 and shape[-1] > 1:
-        raise ValueError(f"{name} must have unit inner stride")
-    return shape, strides
+    if t.dim() != ndim:
+        raise ValueError(f"{name} must have {ndim} dims, got shape {tuple(t.shape)}")
+    raise ValueError(f"{name} must have unit inner stride")
 
 
 def _result(t: torch.Tensor | None, name: str, shape: tuple, dtype: torch.dtype, index: int) -> torch.Tensor:
