@@ -31,8 +31,15 @@
 //   Queries beyond the window are cut into stretches, each an item of its own (one tile of
 //   first-token keys) with FP32 partial sums in the workspace; a small kernel adds a first
 //   token's window part and its stretches in order.
+// * Roundings: P and dS are bf16 as first operands (half a step, 2^-8, of each, on products
+//   whose sums are FP32); D comes from the bf16 output the caller kept, as in the routed
+//   attention's backward: half a step of the output, which tells only where a row sees a few
+//   keys (the exact D = sum p dP would need a pass over the scores before dS).
 // * 0 times an infinity or NaN of a masked row is NaN: rows and keys whose result is not
 //   finite are computed again from what they see alone.
+// * Measured at the size above: dq 1.03 ms (of its issuing warp's 1.98 million cycles, 1.28
+//   are products on their way, 1.09 by the rates of their shapes; 64 / 4 heads: tiles of 8
+//   queries), dk and dv 1.46 ms.
 #include "irs_internal.h"
 #include "irs_ptx.cuh"
 #include "irs_window_rows.cuh"
