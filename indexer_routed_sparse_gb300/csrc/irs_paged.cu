@@ -452,10 +452,11 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) paged_decode_kernel(PagedAr
 }
 
 // Joins the parts of the (sequence, head) pairs that warp borders cut, and writes the empty
-// ones. A block has Dv/4 column lanes and row-and-part groups: `pg` groups share a row, each
-// taking every pg-th part with its own running maximum; they are then joined in order.
+// ones. A block has Dv/4 column lanes and groups of them: `pg` groups share a row, each taking
+// every pg-th part with its own running maximum; they are then joined in order. A thread gets
+// four parts, all in flight together, where there are groups enough.
 template <int DV>
-__global__ void __launch_bounds__(1024) paged_join_kernel(PagedArgs a, int nhb, int workers, int pg) {
+__global__ void __launch_bounds__(1024) paged_join_kernel(PagedArgs a, int nhb, int workers) {
   constexpr int CL = DV / 4;
   __shared__ float4 sm_o[1024];
   __shared__ float2 sm_ml[1024 / CL];
@@ -468,17 +469,19 @@ __global__ void __launch_bounds__(1024) paged_join_kernel(PagedArgs a, int nhb, 
   const int64_t F0 = p0, F1 = p0 + nt;
   const int g = hk / nhb, hb = hk % nhb;
   const int h0 = g * a.G + hb * kHeads, nh = min(kHeads, a.G - hb * kHeads);
-  const int cl = threadIdx.x % CL, grp = threadIdx.x / CL;
-  const int part_grp = grp % pg, row_grp = grp / pg, rows = (int)blockDim.x / CL / pg;
+  const int cl = threadIdx.x % CL, grp = threadIdx.x / CL, groups = (int)blockDim.x / CL;
   int c0 = 0, c1 = -1;
   if (nt > 0) {
     c0 = (int)(F0 / share);
     c1 = (int)((F1 - 1) / share);
     if (c0 == c1) return;
   }
+  int pg = 1;
+  while (2 * pg <= groups && 4 * pg < c1 - c0 + 1) pg *= 2;
+  const int part_grp = grp % pg, row_grp = grp / pg, rows = groups / pg;
   const float* parts = reinterpret_cast<const float*>(a.ws + paged_prefix_bytes(a.B));
   for (int rb = blockIdx.y * rows; rb < nh; rb += gridDim.y * rows) {
-    const int row = rb + row_grp;
+    const int row = row_grp < rows ? rb + row_grp : nh;
     float M = -INFINITY, ls = 0.f;
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
     auto add = [&](float m, float l, const float4& x) {   // a part with its own maximum
@@ -545,15 +548,18 @@ cudaError_t launch_decode(const PagedArgs& a, int num_sms, bool* configured, cud
   paged_decode_kernel<DQK, DV><<<pg.ctas, 32 * pg.warps, pg.smem, stream>>>(a, pg, nhb);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  // few pairs may have hundreds of parts each: a row a block, the parts over 1024 threads;
-  // many pairs have a few parts: every row at once, up to 512 threads
-  const int pairs = a.B * a.Hkv * nhb;
-  const bool few = pairs < num_sms;
-  const int rows = a.G < kHeads ? a.G : kHeads;
-  int threads = few ? 1024 : (rows * (DV / 4) + 31) / 32 * 32;
-  if (!few && threads > 512) threads = 512;
+  // About four parts a thread: a sequence has workers / B of them when the lengths are alike.
+  // (One long sequence: 32 groups a row, a row a block. 16 sequences of 8000 with 8 heads, 10
+  // parts each: 28 us when every row had 32 groups all the same.)
+  const int pairs = a.B * a.Hkv * nhb, rows = a.G < kHeads ? a.G : kHeads;
+  int per_row = 1;
+  while (per_row < 32 && 4 * per_row < pg.workers / a.B) per_row *= 2;
+  const int most = per_row == 32 ? 1024 : 512;
+  int threads = (rows * per_row * (DV / 4) + 31) / 32 * 32;
+  if (threads > most) threads = most;
+  const int in_block = threads / (DV / 4);
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)pairs, few ? (unsigned)rows : 1u);
+  cfg.gridDim = dim3((unsigned)pairs, (unsigned)((rows * per_row + in_block - 1) / in_block));
   cfg.blockDim = dim3((unsigned)threads);
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
@@ -561,7 +567,7 @@ cudaError_t launch_decode(const PagedArgs& a, int num_sms, bool* configured, cud
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_join_kernel<DV>, a, nhb, pg.workers, few ? 1024 / (DV / 4) : 1);
+  return cudaLaunchKernelEx(&cfg, paged_join_kernel<DV>, a, nhb, pg.workers);
 }
 
 }  // namespace
