@@ -26,7 +26,7 @@
 //   and are the first operand of O += P V straight from TMEM (V read MN-major from its
 //   [key][dim] tile). No register may be spilled: shared memory leaves no L1, and a spilled
 //   word is a trip to L2 (12 words in the loop: 1.53 -> 1.73 ms).
-// * The running maximum is raised only where a weight under it passes 2^8 (sums are FP32), so
+// * The running maximum is raised only where a half row's weights under it sum past 2^8 (sums are FP32), so
 //   that after a tile's first block the scores are read once and O in TMEM is hardly ever
 //   rescaled.
 // * Documents are not aligned to tiles: a tile's keys are one range of the packed sequence,
@@ -34,8 +34,8 @@
 //   masked element by element. First tokens before the range are one more (narrow) block.
 // * A masked weight is 0, but 0 times an infinity or NaN in a masked value row is NaN. Rows
 //   whose sum or output is not finite are computed again from their visible keys alone.
-// * Measured: 1.53 ms at the size above (880 TFLOP/s of the pairs that are seen). Of a softmax
-//   warp's 29,600 cycles an item (ten blocks) 17,400 are its work on them, 5,600 its waits for
+// * Measured: 1.52 ms at the size above (885 TFLOP/s of the pairs that are seen). Of a softmax
+//   warp's 29,300 cycles an item (ten blocks) 17,000 are its work on them, 5,600 its waits for
 //   scores (115 cycles each where nothing is waited for) and 6,500 the item's output; the
 //   products at the rates of their shapes (64 columns read at the limit of shared memory:
 //   48.6 cycles for 16 dims, 32 if it were not) would take 17,000.
