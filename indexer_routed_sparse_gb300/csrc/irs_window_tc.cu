@@ -63,7 +63,11 @@ struct FwdCfg {
   static constexpr uint32_t k_bytes = QA * kv_atom, v_bytes = VA * kv_atom, st_bytes = k_bytes + v_bytes;
   static constexpr int ST = 3;                             // stages: block t's keys and block t - 2's values
   static constexpr uint32_t st_off = 2 * q_bytes, x_off = st_off + ST * st_bytes;
-  static constexpr uint32_t bar_off = x_off + 2 * 2 * kRows * 4;   // a word a row, half and tile
+  // Two words a row, half and tile, by which the two threads of a row exchange maxima and sums. A
+  // maximum's word is written again behind the barrier that ends its block's slow path; the sum's,
+  // read last in an item, behind those of the next item's first block, which is always slow.
+  static constexpr uint32_t x_bytes = 2 * 2 * kRows * 4;
+  static constexpr uint32_t bar_off = x_off + 2 * x_bytes;
   static constexpr uint32_t plan_off = bar_off + 32 * 8 + 16;   // [4][8] an item's blocks and borders
   static constexpr uint32_t cu_off = plan_off + 4 * 32;
   static constexpr int cu_cap = (int)((232448u - cu_off) / 4u) < 2048 ? (int)((232448u - cu_off) / 4u) : 2048;
@@ -450,10 +454,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       if (alive) alive = __all_sync(0xffffffffu, mbar_wait(&o_full[x], nof & 1, abort_flag, a.err));
       ++nof;
       tc_fence_after();
-      st_shared(mine, l);
+      st_shared(mine + C::x_bytes, l);
       alive = named_bar_and(bar_id, 64, alive);
       if (!alive) break;
-      l += ld_shared(other);
+      l += ld_shared(other + C::x_bytes);
       const float inv = 1.f / l;
       const int64_t row0 = (int64_t)t_first * a.Hq + g * a.G;
       float odd = fmaf(mx, 0.f, l * 0.f);                 // NaN where anything is not finite

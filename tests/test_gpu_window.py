@@ -257,3 +257,21 @@ def test_columns_of_a_wider_tensor_and_one_head_of_many(irs):
         w[:, :, 8:72] = t.to(DEV)
         gpu.append(w[:, :, 8:72])
     _case(irs, q, k, v, do, cu, 5, 1, gpu=tuple(gpu))
+
+
+@pytest.mark.parametrize("Hq,Hkv,Dqk,Dv", [(8, 8, 64, 64), (32, 2, 192, 128)])
+def test_short_items_follow_one_another(irs, Hq, Hkv, Dqk, Dv):
+    """Window 1: a tile has hardly any work between its row sums and the next tile's first maxima, which the
+    same threads exchange, many times a block. A row's output is its own value, its lse its own score."""
+    T = 30000
+    g = torch.Generator(device=DEV).manual_seed(5)
+    n = lambda *s: torch.randn(*s, generator=g, device=DEV).to(torch.bfloat16)  # noqa: E731
+    q, k, v = n(T, Hq, Dqk), n(T, Hkv, Dqk), n(T, Hkv, Dv)
+    cu = torch.tensor([0, 7, T], dtype=torch.int32, device=DEV)
+    x = q.double() * k.double().repeat_interleave(Hq // Hkv, 1)
+    bound = (Dqk + 8) * R.U32 * x.abs().sum(-1) / 8 + 2.0 ** -21   # an FP32 sum of products, then a rounded scale and sum
+    for _ in range(20):
+        out, lse = irs.window_gqa_attn_fwd(q, k, v, cu, 1, 0.125)
+        assert torch.equal(out, v.repeat_interleave(Hq // Hkv, 1))
+        assert ((lse.double() - x.sum(-1) / 8).abs() <= bound).all()
+    irs.check_device_errors(DEV)
