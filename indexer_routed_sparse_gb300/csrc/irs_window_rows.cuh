@@ -68,10 +68,8 @@ __device__ __forceinline__ void check_documents(const WinArgs& a) {
   if (bad) record_error(a.err, IRS_DEVERR_CU_SEQLENS);
 }
 
-// Writes the output's columns [d0, d0 + dn) and, where it is wanted, lse.
 template <int NQ, int NV>
-__device__ __noinline__ void fwd_row(const WinArgs& a, int t, int h, int lane, int d0 = 0, int dn = 64 * NV,
-                                     bool want_lse = true) {
+__device__ __noinline__ void fwd_row(const WinArgs& a, int t, int h, int lane) {
   const int g = h / a.G;
   const WinDoc doc = window_doc(a.cu, a.ndocs, a.T, t);
   const int lo = max(doc.start, t - a.window + 1);
@@ -81,7 +79,8 @@ __device__ __noinline__ void fwd_row(const WinArgs& a, int t, int h, int lane, i
 #pragma unroll
   for (int i = 0; i < NV; ++i) o[i] = make_float2(0.f, 0.f);
   float m = -INFINITY, l = 0.f;
-  for (int s = doc.start < early ? doc.start : lo; s <= t; s = s + 1 == early ? lo : s + 1) {
+  // once a weight is NaN, so are the sum and every column: the remaining keys change nothing
+  for (int s = doc.start < early ? doc.start : lo; s <= t && l == l; s = s + 1 == early ? lo : s + 1) {
     float2 x[NQ], y[NV];
     load_row<NQ>(x, a.k + (int64_t)s * a.k_st + (int64_t)g * a.k_sh, lane);
     load_row<NV>(y, a.v + (int64_t)s * a.v_st + (int64_t)g * a.v_sh, lane);
@@ -94,14 +93,8 @@ __device__ __noinline__ void fwd_row(const WinArgs& a, int t, int h, int lane, i
     for (int i = 0; i < NV; ++i) { o[i].x *= c; o[i].y *= c; }
     axpy_row<NV>(o, p, y);
   }
-  __nv_bfloat16* out = a.out + ((int64_t)t * a.Hq + h) * (64 * NV);
-  const float inv = 1.f / l;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int d = 64 * i + 2 * lane;
-    if (d >= d0 && d < d0 + dn) *reinterpret_cast<__nv_bfloat162*>(out + d) = __floats2bfloat162_rn(o[i].x * inv, o[i].y * inv);
-  }
-  if (want_lse && a.lse != nullptr && lane == 0) a.lse[(int64_t)t * a.Hq + h] = fmaf(m, kLn2, logf(l));
+  store_row<NV>(o, 1.f / l, a.out + ((int64_t)t * a.Hq + h) * (64 * NV), lane);
+  if (a.lse != nullptr && lane == 0) a.lse[(int64_t)t * a.Hq + h] = fmaf(m, kLn2, logf(l));
 }
 
 template <int NQ, int NV>

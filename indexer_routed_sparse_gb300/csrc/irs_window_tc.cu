@@ -33,12 +33,16 @@
 //   and each row masks by its own document's start. Only blocks at a border of the range are
 //   masked element by element. First tokens before the range are one more (narrow) block.
 // * A masked weight is 0, but 0 times an infinity or NaN in a masked value row is NaN. Rows
-//   whose sum or output is not finite are computed again from their visible keys alone.
+//   whose sum or output is not finite are marked (a NaN in the output, the item in shared memory)
+//   and computed again from their visible keys alone when the CTA is through with its items: a
+//   row takes as long as its window, and the pipeline's waits have a limit.
 // * Measured: 1.52 ms at the size above (885 TFLOP/s of the pairs that are seen). Of a softmax
 //   warp's 29,300 cycles an item (ten blocks) 17,000 are its work on them, 5,600 its waits for
 //   scores (115 cycles each where nothing is waited for) and 6,500 the item's output; the
 //   products at the rates of their shapes (64 columns read at the limit of shared memory:
 //   48.6 cycles for 16 dims, 32 if it were not) would take 17,000.
+#include <climits>
+
 #include "irs_internal.h"
 #include "irs_ptx.cuh"
 #include "irs_window_rows.cuh"
@@ -69,7 +73,8 @@ struct FwdCfg {
   static constexpr uint32_t x_bytes = 2 * 2 * kRows * 4;
   static constexpr uint32_t bar_off = x_off + 2 * x_bytes;
   static constexpr uint32_t plan_off = bar_off + 32 * 8 + 16;   // [4][8] an item's blocks and borders
-  static constexpr uint32_t cu_off = plan_off + 4 * 32;
+  static constexpr uint32_t redo_off = plan_off + 4 * 32;       // [16][2] first and last item of a softmax warp with marked rows
+  static constexpr uint32_t cu_off = redo_off + 16 * 8;
   static constexpr int cu_cap = (int)((232448u - cu_off) / 4u) < 2048 ? (int)((232448u - cu_off) / 4u) : 2048;
   static constexpr uint32_t total = cu_off + 4u * cu_cap;   // 226.3 KB at 192/128: none to spare for aligning
   static constexpr uint32_t S0 = 0, O0 = 256;              // TMEM: S of tile x, buffer b at 128 x + 64 b; O at 256 + x DV
@@ -165,6 +170,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   uint32_t* tslot = reinterpret_cast<uint32_t*>(drain + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
   volatile int* plan = reinterpret_cast<volatile int*>(smem + C::plan_off);
+  int* redo = reinterpret_cast<int*>(smem + C::redo_off);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
@@ -182,6 +188,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   if (warp == 17) {
     tmem_alloc(tslot, 512);
     tmem_relinquish();
+  }
+  if (tid < 16) {
+    redo[2 * tid] = INT_MAX;
+    redo[2 * tid + 1] = -1;
   }
   check_documents(a);
   // document borders are searched for every item by every row: in shared memory where they fit
@@ -487,14 +497,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&o_empty[x]);
       if (half == 0 && live && a.lse != nullptr) a.lse[row0 + rel] = fmaf(mx, 0.6931471805599453f, logf(l));
-      // rows to do again, each half its own columns (NaN compares unequal), after the stores above
-      __syncwarp();
-      unsigned again = __ballot_sync(0xffffffffu, live && odd != 0.f);
-      while (again) {
-        const int src = __ffs((int)again) - 1;
-        again &= again - 1;
-        fwd_row<DQK / 64, DV / 64>(a, __shfl_sync(0xffffffffu, t, src), g * a.G + __shfl_sync(0xffffffffu, r - rq * a.G, src),
-                                   lane, half * (DV / 2), DV / 2, half == 0);
+      // rows to do again (NaN compares unequal): a NaN over the half's first column marks them
+      const bool bad = live && odd != 0.f;
+      if (bad) a.out[(row0 + rel) * DV + half * (DV / 2)] = __ushort_as_bfloat16(0x7fff);
+      if (__any_sync(0xffffffffu, bad) && lane == 0) {
+        if (redo[2 * warp + 1] < 0) redo[2 * warp] = item;
+        redo[2 * warp + 1] = item;
       }
     }
   }
@@ -503,6 +511,33 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   if (warp == 17) {
     tc_fence_after();
     tmem_dealloc(tbase, 512);
+  }
+  // ---- marked rows, by all warps in turn: nothing waits for them any more ----
+  if (*abort_flag) return;
+  const int first = __reduce_min_sync(0xffffffffu, lane < 16 ? redo[2 * lane] : INT_MAX);
+  const int last = __reduce_max_sync(0xffffffffu, lane < 16 ? redo[2 * lane + 1] : -1);
+  int turn = 0;
+  for (int item = first; item <= last; item += gridDim.x) {
+    const int pair = item / a.Hkv, g = item - pair * a.Hkv, t0 = pair * 2 * qt;
+    if (warp < 8) {   // which of 32 rows of a tile are marked; the plans' words are free by now
+      const int r = (warp & 3) * 32 + lane, rq = r / a.G, t = t0 + (warp >> 2) * qt + rq;
+      bool bad = false;
+      if (rq < qt && t < a.T) {
+        const __nv_bfloat16* o = a.out + ((int64_t)t * a.Hq + g * a.G + r - rq * a.G) * DV;
+        bad = __hisnan(o[0]) || __hisnan(o[DV / 2]);
+      }
+      const unsigned marks = __ballot_sync(0xffffffffu, bad);
+      if (lane == 0) plan[warp] = (int)marks;
+    }
+    __syncthreads();
+    for (int i = 0; i < 8; ++i) {
+      for (unsigned m = (unsigned)plan[i]; m; m &= m - 1) {
+        const int r = (i & 3) * 32 + __ffs((int)m) - 1, rq = r / a.G;
+        if (turn == warp) fwd_row<DQK / 64, DV / 64>(a, t0 + (i >> 2) * qt + rq, g * a.G + r - rq * a.G, lane);
+        if (++turn == kFwdThreads / 32) turn = 0;
+      }
+    }
+    __syncthreads();
   }
 }
 

@@ -275,3 +275,57 @@ def test_short_items_follow_one_another(irs, Hq, Hkv, Dqk, Dv):
         assert torch.equal(out, v.repeat_interleave(Hq // Hkv, 1))
         assert ((lse.double() - x.sum(-1) / 8).abs() <= bound).all()
     irs.check_device_errors(DEV)
+
+
+def _rows(cu, rows, window, sinks):
+    """(row, the keys it sees) of some rows."""
+    for t in rows:
+        start = int(cu[torch.searchsorted(cu, t, right=True) - 1])
+        lo = max(start, t - window + 1)
+        yield t, torch.cat((torch.arange(start, max(start, min(start + sinks, lo))), torch.arange(lo, t + 1)))
+
+
+def _same(got, ref, bound, what):
+    """NaN where the definition has NaN, within its bound elsewhere."""
+    got, nan = got.cpu().double(), torch.isnan(ref)
+    assert torch.equal(torch.isnan(got), nan), (what, "NaN in other places")
+    R.check(got.masked_fill(nan, 0.0), ref.masked_fill(nan, 0.0), bound.masked_fill(nan, 1.0), what)
+
+
+def _check_fwd_rows(q, k, v, cu, window, sinks, out, lse, rows):
+    Hkv = k.shape[1]
+    for t, at in _rows(cu, rows, window, sinks):
+        o, l, eo, el = R._attend(q[t].double().view(Hkv, -1, q.shape[2]), k[at].double(), v[at].double(), 1 / math.sqrt(q.shape[2]))
+        _same(out[t].view(o.shape), o, eo, (t, "out"))
+        _same(lse[t].view(l.shape), l, el, (t, "lse"))
+
+
+def test_forward_rows_that_see_nan_and_their_neighbours(irs):
+    """Long windows, several tiles a block: rows that see a NaN or an infinity hold what the definition does, also in
+    the columns that it does not reach, and the rows that share their tiles stay within their bounds."""
+    window, sinks = 6000, 2
+    q, k, v, _, cu = _inputs(16400, 16, 1, 64, 64, [9000, 7400])
+    v[50, 0, 3], v[9100, 0, 5], k[9500], q[4000, 2] = math.nan, math.inf, math.nan, math.nan
+    out, lse = irs.window_gqa_attn_fwd(*(t.to(DEV) for t in (q, k, v, cu)), window, sinks=sinks)
+    irs.check_device_errors(DEV)
+    _check_fwd_rows(q, k, v, cu, window, sinks, out, lse, [
+        0, 40, 49, 50, 51, 60, 3999, 4000, 4001, 6049, 6050, 6051, 6070, 8999, 9000, 9096, 9099, 9100, 9101, 9490, 9499,
+        9500, 9501, 15098, 15099, 15100, 15101, 15499, 15500, 15501, 16399])
+
+
+def test_forward_repairs_do_not_hold_up_the_pipeline(irs):
+    """A NaN in a long document's last value row meets the rows before it in that tile with weight 0. Each of them has
+    450,000 keys: computed again while the block's next tiles wait, they outlast the limit of those waits (2 s by the
+    time of a key, some 0.5 us a warp, and 32 rows a warp)."""
+    A, T = 450_000, 470_000
+    g = torch.Generator(device=DEV).manual_seed(3)
+    n = lambda *s: torch.randn(*s, generator=g, device=DEV).to(torch.bfloat16)  # noqa: E731
+    q, k, v = n(T, 16, 64), n(T, 1, 64), n(T, 1, 64)
+    v[A - 1] = math.nan
+    cu = torch.tensor([0, A, T], dtype=torch.int32)
+    out, lse = irs.window_gqa_attn_fwd(q, k, v, cu.to(DEV), T)
+    irs.check_device_errors(DEV)
+    nan = torch.isnan(out).flatten(1).sum(1).nonzero()[:, 0].tolist()
+    assert nan == [A - 1] and torch.isnan(out[A - 1]).all() and not torch.isnan(lse).any()
+    _check_fwd_rows(*(t.cpu() for t in (q, k, v)), cu, T, 0, out, lse,
+                    [0, 1000, A - 17, A - 16, A - 9, A - 2, A - 1, A, A + 9, T - 3000, T - 1])
