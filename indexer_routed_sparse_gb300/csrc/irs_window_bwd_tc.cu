@@ -36,10 +36,14 @@
 //   attention's backward: half a step of the output, which tells only where a row sees a few
 //   keys (the exact D = sum p dP would need a pass over the scores before dS).
 // * 0 times an infinity or NaN of a masked row is NaN: rows and keys whose result is not
-//   finite are computed again from what they see alone.
+//   finite are computed again from what they see alone. Rows of dq are marked (a NaN in the
+//   first column, the item in shared memory) and done when the CTA is through with its items:
+//   a row takes as long as its window, and the pipeline's waits have a limit.
 // * Measured at the size above: dq 1.03 ms (of its issuing warp's 1.98 million cycles, 1.28
 //   are products on their way, 1.09 by the rates of their shapes; 64 / 4 heads: tiles of 8
 //   queries), dk and dv 1.46 ms.
+#include <climits>
+
 #include "irs_internal.h"
 #include "irs_ptx.cuh"
 #include "irs_window_rows.cuh"
@@ -99,7 +103,8 @@ struct DqCfg {
   static constexpr uint32_t hdr_off = row_off + 2 * 128 * 16;   // [2][8] of an item: range and borders
   static constexpr uint32_t plan_off = hdr_off + 2 * 32;        // [2][4] its blocks, for the MMA warp
   static constexpr uint32_t bar_off = plan_off + 2 * 16;
-  static constexpr uint32_t cu_off = bar_off + 24 * 8 + 16;
+  static constexpr uint32_t redo_off = bar_off + 24 * 8 + 16;   // [4][2] first and last item of a helper warp with marked rows
+  static constexpr uint32_t cu_off = redo_off + 4 * 8;
   static constexpr int cu_cap = 2048;
   static constexpr uint32_t total = cu_off + 4 * cu_cap + 1024;
   static constexpr uint32_t S0 = 0, P0 = 128, DS0 = 256, DQ0 = 320;   // TMEM columns
@@ -144,6 +149,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
   volatile float* rows = reinterpret_cast<volatile float*>(smem + C::row_off);
   volatile int* head = reinterpret_cast<volatile int*>(smem + C::hdr_off);
   volatile int* plan = reinterpret_cast<volatile int*>(smem + C::plan_off);
+  int* redo = reinterpret_cast<int*>(smem + C::redo_off);
   uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::bar_off);
   uint64_t* q_empty = q_full + 1;
   uint64_t* k_full = q_empty + 1;    // [3]
@@ -180,6 +186,10 @@ __global__ void __launch_bounds__(kDqThreads, 1)
   if (warp == 9) {
     tmem_alloc(tslot, 512);
     tmem_relinquish();
+  }
+  if (tid < 4) {
+    redo[2 * tid] = INT_MAX;
+    redo[2 * tid + 1] = -1;
   }
   check_documents(a);
   const int32_t* cu = a.cu;
@@ -369,7 +379,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
           h[5] = m.last;
         }
         __syncwarp();
-        if (in) a.delta[base + orow] = dst[4 * (rb + lane)];
+        if (in) a.delta[base + orow] = dst[4 * (rb + lane)];   // for later kernels, and this one's end
         if (lane == 0) mbar_arrive(&d_full[slot]);
       }
       if (prev >= 0) {
@@ -396,11 +406,13 @@ __global__ void __launch_bounds__(kDqThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(dq_empty);
-        unsigned again = __ballot_sync(0xffffffffu, live && odd != 0.f);   // NaN compares unequal
-        while (again) {
-          const int src = __ffs((int)again) - 1;
-          again &= again - 1;
-          dq_row<DQK / 64, DV / 64>(a, __shfl_sync(0xffffffffu, t, src), __shfl_sync(0xffffffffu, h, src), lane);
+        // rows to do again (NaN compares unequal): a NaN in the first column marks them (the lane
+        // that stored the column did so before the __syncwarp)
+        const bool bad = live && odd != 0.f;
+        if (bad) a.dq[((int64_t)t * a.Hq + h) * DQK] = __ushort_as_bfloat16(0x7fff);
+        if (__any_sync(0xffffffffu, bad) && lane == 0) {
+          if (redo[2 * (warp & 3) + 1] < 0) redo[2 * (warp & 3)] = prev;
+          redo[2 * (warp & 3) + 1] = prev;
         }
       }
       if (item >= items) break;
@@ -499,6 +511,29 @@ __global__ void __launch_bounds__(kDqThreads, 1)
   if (warp == 9) {
     tc_fence_after();
     tmem_dealloc(tbase, 512);
+  }
+  // ---- marked rows, by all warps in turn: nothing waits for them any more ----
+  if (*abort_flag) return;
+  const int first = __reduce_min_sync(0xffffffffu, lane < 4 ? redo[2 * lane] : INT_MAX);
+  const int last = __reduce_max_sync(0xffffffffu, lane < 4 ? redo[2 * lane + 1] : -1);
+  int turn = 0;
+  for (int item = first; item <= last; item += gridDim.x) {
+    const int tile = item / a.Hkv, g = item - tile * a.Hkv, t0 = tile * qt;
+    if (warp < 4) {   // which of 32 rows are marked; the plans' words are free by now
+      const int r = warp * 32 + lane, rq = r / a.G, t = t0 + rq;
+      const bool bad = rq < qt && t < a.T && __hisnan(a.dq[((int64_t)t * a.Hq + g * a.G + r - rq * a.G) * DQK]);
+      const unsigned marks = __ballot_sync(0xffffffffu, bad);
+      if (lane == 0) plan[warp] = (int)marks;
+    }
+    __syncthreads();
+    for (int i = 0; i < 4; ++i) {
+      for (unsigned m = (unsigned)plan[i]; m; m &= m - 1) {
+        const int r = i * 32 + __ffs((int)m) - 1, rq = r / a.G;
+        if (turn == warp) dq_row<DQK / 64, DV / 64>(a, t0 + rq, g * a.G + r - rq * a.G, lane);
+        if (++turn == kDqThreads / 32) turn = 0;
+      }
+    }
+    __syncthreads();
   }
 }
 

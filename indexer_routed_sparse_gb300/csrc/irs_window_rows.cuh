@@ -110,12 +110,13 @@ __device__ __noinline__ void dq_row(const WinArgs& a, int t, int h, int lane) {
 #pragma unroll
   for (int i = 0; i < NQ; ++i) acc[i] = make_float2(0.f, 0.f);
   const float l2 = a.lse_in[row] * kLog2e, D = a.delta[row];
-  for (int s = doc.start < early ? doc.start : lo; s <= t; s = s + 1 == early ? lo : s + 1) {
+  float ds = 0.f;   // once it is NaN, so is every column: the remaining keys change nothing
+  for (int s = doc.start < early ? doc.start : lo; s <= t && ds == ds; s = s + 1 == early ? lo : s + 1) {
     float2 x[NQ], y[NV];
     load_row<NQ>(x, a.k + (int64_t)s * a.k_st + (int64_t)g * a.k_sh, lane);
     load_row<NV>(y, a.v + (int64_t)s * a.v_st + (int64_t)g * a.v_sh, lane);
-    const float p = ex2_approx(fmaf(dot_row<NQ>(q, x), a.scale_log2, -l2));
-    axpy_row<NQ>(acc, p * (dot_row<NV>(d, y) - D), x);
+    ds = ex2_approx(fmaf(dot_row<NQ>(q, x), a.scale_log2, -l2)) * (dot_row<NV>(d, y) - D);
+    axpy_row<NQ>(acc, ds, x);
   }
   store_row<NQ>(acc, a.scale, a.dq + row * (64 * NQ), lane);
 }

@@ -329,3 +329,55 @@ def test_forward_repairs_do_not_hold_up_the_pipeline(irs):
     assert nan == [A - 1] and torch.isnan(out[A - 1]).all() and not torch.isnan(lse).any()
     _check_fwd_rows(*(t.cpu() for t in (q, k, v)), cu, T, 0, out, lse,
                     [0, 1000, A - 17, A - 16, A - 9, A - 2, A - 1, A, A + 9, T - 3000, T - 1])
+
+
+def _check_dq_rows(q, k, v, cu, window, sinks, out, lse, do, dq, rows):
+    """Some rows of dq against the formula, with the roundings that serving_ref.window_bwd counts."""
+    Hkv, Dq, Dv = k.shape[1], q.shape[2], v.shape[2]
+    scale, G = 1 / math.sqrt(Dq), q.shape[1] // k.shape[1]
+    for t, at in _rows(cu, rows, window, sinks):
+        qt, dt, ot = (x[t].double().view(Hkv, G, -1) for x in (q, do, out))
+        l = lse[t].double().view(Hkv, G, 1)
+        kt, vt = k[at].double(), v[at].double()
+        x = torch.einsum("hgd,shd->hgs", qt, kt) * scale
+        p = torch.exp(x - l)
+        D = (dt * ot).sum(-1, keepdim=True)
+        y = torch.einsum("hgd,shd->hgs", dt, vt) - D
+        ymag = torch.einsum("hgd,shd->hgs", dt.abs(), vt.abs()) + (dt.abs() * ot.abs()).sum(-1, keepdim=True)
+        ds = p * y
+        ep = p * ((Dq + 4) * R.U32 * torch.einsum("hgd,shd->hgs", qt.abs(), kt.abs()) * scale + 2.0 ** -21 + 4 * R.U32 * l.abs())
+        e = ep * y.abs() + p * (Dv + 4) * R.U32 * ymag + (R.U16 + 64 * R.U32) * ds.abs()
+        r = torch.einsum("hgs,shd->hgd", ds, kt) * scale
+        bound = R.U16 * r.abs() + torch.einsum("hgs,shd->hgd", e, kt.abs()) * scale + 1e-30
+        _same(dq[t].view(r.shape), r, bound, (t, "dq"))
+
+
+def test_dq_rows_that_see_nan_and_their_neighbours(irs):
+    window, sinks = 6000, 2
+    q, k, v, do, cu = _inputs(16400, 16, 1, 64, 64, [9000, 7400])
+    dev = [t.to(DEV) for t in (q, k, v, cu)]
+    out, lse = irs.window_gqa_attn_fwd(*dev, window, sinks=sinks)
+    kb, vb = k.clone(), v.clone()
+    kb[8990], vb[9100, 0, 5], vb[16390, 0, 3] = math.nan, math.inf, math.nan
+    dq = irs.window_gqa_attn_bwd(dev[0], kb.to(DEV), vb.to(DEV), dev[3], window, out, lse, do.to(DEV), sinks=sinks)[0]
+    irs.check_device_errors(DEV)
+    _check_dq_rows(q, kb, vb, cu, window, sinks, out.cpu(), lse.cpu(), do, dq, [
+        0, 1, 4000, 8983, 8984, 8988, 8989, 8990, 8991, 8999, 9000, 9001, 9099, 9100, 9101, 15099, 15100, 15101, 15110,
+        16384, 16389, 16390, 16391, 16399])
+
+
+def test_dq_repairs_do_not_hold_up_the_pipeline(irs):
+    """As for the forward: rows of 250,000 keys beside one that sees a NaN, and tiles behind them."""
+    A, T = 250_000, 270_000
+    g = torch.Generator(device=DEV).manual_seed(4)
+    n = lambda *s: torch.randn(*s, generator=g, device=DEV).to(torch.bfloat16)  # noqa: E731
+    q, k, v, do = n(T, 16, 64), n(T, 1, 64), n(T, 1, 64), n(T, 16, 64)
+    cu = torch.tensor([0, A, T], dtype=torch.int32)
+    out, lse = irs.window_gqa_attn_fwd(q, k, v, cu.to(DEV), T)
+    k[A - 1] = math.nan
+    dq, dk, dv = irs.window_gqa_attn_bwd(q, k, v, cu.to(DEV), T, out, lse, do)
+    irs.check_device_errors(DEV)
+    for t in (dq, dk, dv):
+        assert torch.isnan(t).flatten(1).sum(1).nonzero()[:, 0].tolist() == [A - 1]
+    _check_dq_rows(*(t.cpu() for t in (q, k, v)), cu, T, 0, out.cpu(), lse.cpu(), do.cpu(), dq,
+                   [0, 1000, A - 17, A - 9, A - 8, A - 2, A - 1, A, A + 9, T - 3000, T - 1])
