@@ -1140,12 +1140,11 @@ irs_status irs_window_gqa_attn_bwd(const void* q, int64_t q_stride_t, int64_t q_
   a.out = bf(const_cast<void*>(out));
   a.lse_in = lse;
   a.dout = bf(dout);
-  a.delta = static_cast<float*>(workspace);
   a.dq = bf(dq); a.dk = bf(dk); a.dv = bf(dv);
+  irs::WinSinks sk;
+  irs::window_bwd_layout(static_cast<uint8_t*>(workspace), T, Hq, Hkv, Dqk, Dv, ndocs, window, sinks, &a, &sk);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (!window_has_maps(a)) return launch_status(irs::launch_window_bwd_rows(a, st), "launching the window backward (rows)");
-  irs::WinSinks sk;
-  irs::window_bwd_layout(static_cast<uint8_t*>(workspace), T, Hq, Hkv, Dqk, Dv, ndocs, window, sinks, &sk);
   const int hc = a.G < 64 ? a.G : 64;
   irs::WinBwdMaps m;
   if ((s = make_packed_map(&m.q, q, Dqk, Hq, T, q_stride_h, q_stride_t, a.G, 128 / a.G)) != IRS_OK) return s;

@@ -248,6 +248,7 @@ struct WinArgs {
   const float* lse_in;        // [T, Hq] (backward)
   const __nv_bfloat16* dout;
   float* delta;               // [T, Hq] scratch: dout . out
+  uint32_t* redo;             // scratch: whether any, then a bit a (token, KV head): dk and dv to compute again
   __nv_bfloat16* dq;
   __nv_bfloat16* dk;
   __nv_bfloat16* dv;
@@ -283,7 +284,8 @@ struct WinBwdMaps {
   CUtensorMap q, dout, q2, dout2, k, v, kq, vq;
 };
 int window_dq_block();
-size_t window_bwd_layout(uint8_t* ws, int T, int Hq, int Hkv, int Dqk, int Dv, int ndocs, int window, int sinks, WinSinks* s);
+size_t window_bwd_layout(uint8_t* ws, int T, int Hq, int Hkv, int Dqk, int Dv, int ndocs, int window, int sinks, WinArgs* a,
+                         WinSinks* s);
 cudaError_t launch_window_bwd_tc(const WinBwdMaps& m, const WinArgs& a, const WinSinks& sk, int num_sms, bool* configured,
                                  cudaStream_t stream);
 

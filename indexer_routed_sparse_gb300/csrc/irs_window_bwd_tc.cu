@@ -36,9 +36,11 @@
 //   attention's backward: half a step of the output, which tells only where a row sees a few
 //   keys (the exact D = sum p dP would need a pass over the scores before dS).
 // * 0 times an infinity or NaN of a masked row is NaN: rows and keys whose result is not
-//   finite are computed again from what they see alone. Rows of dq are marked (a NaN in the
-//   first column, the item in shared memory) and done when the CTA is through with its items:
-//   a row takes as long as its window, and the pipeline's waits have a limit.
+//   finite are computed again from what they see alone, outside the pipelines, whose waits have
+//   a limit: a row or key takes as long as its window. Rows of dq are marked (a NaN in the
+//   first column, the item in shared memory) and done when the CTA is through with its items.
+//   A bad query reaches all 128 keys of every tile that loads it, so marked keys (a bit each in
+//   the workspace) are spread over the GPU by a last small kernel, a block a key.
 // * Measured at the size above: dq 1.03 ms (of its issuing warp's 1.98 million cycles, 1.28
 //   are products on their way, 1.09 by the rates of their shapes; 64 / 4 heads: tiles of 8
 //   queries), dk and dv 1.46 ms.
@@ -58,6 +60,18 @@ constexpr uint32_t kAtom = 128 * 128;   // 128 rows x 64 bf16
 constexpr uint32_t kAtom64 = 64 * 128;  // 64 rows x 64 bf16
 constexpr int kDqThreads = 448;         // warps 0-7: score warps; 8: TMA; 9: MMA; 10-13: helpers
 constexpr int kDkvThreads = 640;        // warps 0-15: score warps; 16: lse and D; 17, 18: MMA; 19: TMA
+
+// A word that says whether any key is marked, then a bit a key.
+__host__ __device__ inline int64_t redo_words(int T, int Hkv) { return 1 + ((int64_t)T * Hkv + 31) / 32; }
+// (out of line: inlined into the dq kernel it costs that eight spilled registers)
+__device__ __noinline__ void redo_clear(const WinArgs& a) {
+  const int64_t words = redo_words(a.T, a.Hkv);
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < words; i += (int64_t)gridDim.x * blockDim.x) a.redo[i] = 0u;
+}
+__device__ __forceinline__ void redo_mark(const WinArgs& a, int64_t row) {
+  atomicOr(a.redo + 1 + (row >> 5), 1u << (row & 31));   // a set: the order does not matter
+  a.redo[0] = 1u;
+}
 
 __device__ __forceinline__ void wait_landed(uint64_t* bar, uint32_t parity) {
   const unsigned long long t0 = globaltimer_ns();
@@ -512,6 +526,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     tc_fence_after();
     tmem_dealloc(tbase, 512);
   }
+  redo_clear(a);   // for the kernel behind this one
   // ---- marked rows, by all warps in turn: nothing waits for them any more ----
   if (*abort_flag) return;
   const int first = __reduce_min_sync(0xffffffffu, lane < 4 ? redo[2 * lane] : INT_MAX);
@@ -907,14 +922,8 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(acc_empty);
-      // keys whose sums are not finite (NaN compares unequal) are done again, each warp the
-      // columns it stored
-      unsigned again = __ballot_sync(0xffffffffu, live && !far && (odd_k != 0.f || odd_v != 0.f));
-      while (again) {
-        const int src = __ffs((int)again) - 1;
-        again &= again - 1;
-        dkv_row<DQK / 64, DV / 64>(a, __shfl_sync(0xffffffffu, s, src), m.g, lane, 32 * quart, 128);
-      }
+      // keys whose sums are not finite (NaN compares unequal) are done again
+      if (live && !far && (odd_k != 0.f || odd_v != 0.f)) redo_mark(a, row);
     }
   }
   tc_fence_before();
@@ -997,7 +1006,60 @@ __global__ void __launch_bounds__(128) window_join_kernel(WinArgs a, WinSinks sk
     if (x < DQK) a.dk[row * DQK + x] = __float2bfloat16_rn(s);
     else a.dv[row * DV + x - DQK] = __float2bfloat16_rn(s);
   }
-  if (__syncthreads_or(odd != 0.f) && threadIdx.x < 32) dkv_row<DQK / 64, DV / 64>(a, start + i, g, threadIdx.x);
+  if (odd != 0.f) redo_mark(a, row);
+}
+
+// dk and dv of the marked keys. Block b looks at every gridDim-th key; its warps share a marked
+// key's queries and join their sums in order. With no key marked it costs its launch.
+constexpr int kRedoThreads = 512;
+template <int DQK, int DV>
+__global__ void __launch_bounds__(kRedoThreads, 2) window_redo_kernel(WinArgs a) {
+  constexpr int W = kRedoThreads / 32, D = DQK + DV;
+  __shared__ float sums[W][D];
+  __shared__ unsigned marks[W];
+  __shared__ volatile int nan;
+  if (a.redo[0] == 0u) return;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int64_t rows = (int64_t)a.T * a.Hkv;
+  for (int64_t c0 = blockIdx.x; c0 < rows; c0 += (int64_t)kRedoThreads * gridDim.x) {
+    const int64_t mine = c0 + (int64_t)tid * gridDim.x;
+    const unsigned m = __ballot_sync(0xffffffffu, mine < rows && (a.redo[1 + (mine >> 5)] >> (mine & 31) & 1u));
+    if (lane == 0) marks[warp] = m;
+    __syncthreads();
+    for (int w = 0; w < W; ++w) {
+      for (unsigned left = marks[w]; left; left &= left - 1) {
+        const int64_t row = c0 + (int64_t)(w * 32 + __ffs((int)left) - 1) * gridDim.x;
+        const int s = (int)(row / a.Hkv), g = (int)(row % a.Hkv), end = key_end(a, s);
+        // a NaN in lse makes every column NaN: looked for first, a lane a row
+        bool bad = false;
+        for (int64_t i = tid; i < (int64_t)(end - s) * a.G && !bad; i += kRedoThreads) {
+          const float l = a.lse_in[(s + i / a.G) * a.Hq + g * a.G + i % a.G];
+          bad = l != l;
+        }
+        if (tid == 0) nan = 0;
+        bad = __syncthreads_or(bad);
+        if (bad) {
+          for (int d = tid; d < D; d += kRedoThreads) sums[0][d] = __int_as_float(0x7fffffff);
+        } else {
+          float2 dk[DQK / 64], dv[DV / 64];
+          dkv_sums<DQK / 64, DV / 64>(a, s, g, lane, warp, W, &nan, dk, dv);
+#pragma unroll
+          for (int i = 0; i < DQK / 64; ++i) *reinterpret_cast<float2*>(&sums[warp][64 * i + 2 * lane]) = dk[i];
+#pragma unroll
+          for (int i = 0; i < DV / 64; ++i) *reinterpret_cast<float2*>(&sums[warp][DQK + 64 * i + 2 * lane]) = dv[i];
+        }
+        __syncthreads();
+        for (int d = tid; d < D; d += kRedoThreads) {
+          float x = sums[0][d];
+          for (int i = 1; i < W && !bad; ++i) x += sums[i][d];
+          if (d < DQK) a.dk[row * DQK + d] = __float2bfloat16_rn(x * a.scale);
+          else a.dv[row * DV + d - DQK] = __float2bfloat16_rn(x);
+        }
+        __syncthreads();
+      }
+    }
+    __syncthreads();
+  }
 }
 
 }  // namespace
@@ -1031,26 +1093,33 @@ cudaError_t launch_bwd(const WinBwdMaps& m, const WinArgs& a, const WinSinks& sk
   const int64_t kitems = ((int64_t)ktiles + sk.chunks) * a.Hkv;
   window_dkv_kernel<DQK, DV><<<kitems < num_sms ? (int)kitems : num_sms, kDkvThreads, K::total, stream>>>(m.q2, m.dout2, m.k, m.v, a, sk, ktiles);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  if (sk.slots > 0)
+  if (sk.slots > 0) {
     window_join_kernel<DQK, DV><<<(unsigned)(sk.slots * a.Hkv * a.sinks), 128, 0, stream>>>(a, sk);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  window_redo_kernel<DQK, DV><<<2 * num_sms, kRedoThreads, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-// Workspace: D of every row; then, with first tokens, the plan and the FP32 sums.
+// Workspace: D of every row and the marks of keys; then, with first tokens, the plan and the FP32 sums.
 size_t window_bwd_workspace_bytes(int T, int Hq, int Hkv, int Dqk, int Dv, int ndocs, int window, int sinks) {
+  WinArgs a;
   WinSinks s;
-  return window_bwd_layout(nullptr, T, Hq, Hkv, Dqk, Dv, ndocs, window, sinks, &s);
+  return window_bwd_layout(nullptr, T, Hq, Hkv, Dqk, Dv, ndocs, window, sinks, &a, &s);
 }
 
-size_t window_bwd_layout(uint8_t* ws, int T, int Hq, int Hkv, int Dqk, int Dv, int ndocs, int window, int sinks, WinSinks* s) {
-  size_t off = ((size_t)T * Hq * 4 + 255) & ~size_t(255);
+size_t window_bwd_layout(uint8_t* ws, int T, int Hq, int Hkv, int Dqk, int Dv, int ndocs, int window, int sinks, WinArgs* a,
+                         WinSinks* s) {
+  size_t off = 0;
   auto take = [&](size_t bytes) {
     uint8_t* p = ws + off;
     off += (bytes + 255) & ~size_t(255);
     return p;
   };
+  a->delta = reinterpret_cast<float*>(take((size_t)T * Hq * 4));
+  a->redo = reinterpret_cast<uint32_t*>(take((size_t)redo_words(T, Hkv) * 4));
   *s = WinSinks{};
   const int64_t longer = (int64_t)T / ((int64_t)window + 1);   // documents that can be longer than the window
   s->slots = sinks > 0 ? (int)(longer < ndocs ? longer : ndocs) : 0;

@@ -121,45 +121,53 @@ __device__ __noinline__ void dq_row(const WinArgs& a, int t, int h, int lane) {
   store_row<NQ>(acc, a.scale, a.dq + row * (64 * NQ), lane);
 }
 
-// Writes the columns of [dk | dv] whose piece of 32 is `first`'s, or lies `step` columns from it
-// and so on; by default all.
-template <int NQ, int NV>
-__device__ __noinline__ void dkv_row(const WinArgs& a, int s, int g, int lane, int first = 0, int step = 32) {
+// The first query past those that see key s.
+__device__ __forceinline__ int key_end(const WinArgs& a, int s) {
   const WinDoc doc = window_doc(a.cu, a.ndocs, a.T, s);
-  const int64_t last = (int64_t)s + a.window;   // first query past the window
-  const int end = s - doc.start < a.sinks || last > doc.end ? doc.end : (int)last;
-  float2 k[NQ], v[NV], dk[NQ], dv[NV];
+  const int64_t last = (int64_t)s + a.window;
+  return s - doc.start < a.sinks || last > doc.end ? doc.end : (int)last;
+}
+
+// Sums [dk | dv] of a key over the queries `first`, `first` + `step`, ... of those that see it.
+// Once a weight is NaN, so is every column; warps that share a key say so in *nan.
+template <int NQ, int NV>
+__device__ __forceinline__ void dkv_sums(const WinArgs& a, int s, int g, int lane, int first, int step, volatile int* nan,
+                                         float2 (&dk)[NQ], float2 (&dv)[NV]) {
+  const int end = key_end(a, s);
+  float2 k[NQ], v[NV];
   load_row<NQ>(k, a.k + (int64_t)s * a.k_st + (int64_t)g * a.k_sh, lane);
   load_row<NV>(v, a.v + (int64_t)s * a.v_st + (int64_t)g * a.v_sh, lane);
 #pragma unroll
   for (int i = 0; i < NQ; ++i) dk[i] = make_float2(0.f, 0.f);
 #pragma unroll
   for (int i = 0; i < NV; ++i) dv[i] = make_float2(0.f, 0.f);
-  for (int t = s; t < end; ++t) {
-    for (int h = g * a.G; h < (g + 1) * a.G; ++h) {
+  for (int t = s + first; t < end; t += step) {
+    float p = 0.f;
+    for (int h = g * a.G; h < (g + 1) * a.G && p == p; ++h) {
       const int64_t row = (int64_t)t * a.Hq + h;
       float2 q[NQ], d[NV];
       load_row<NQ>(q, a.q + (int64_t)t * a.q_st + (int64_t)h * a.q_sh, lane);
       load_row<NV>(d, a.dout + row * (64 * NV), lane);
-      const float p = ex2_approx(fmaf(dot_row<NQ>(q, k), a.scale_log2, -a.lse_in[row] * kLog2e));
+      p = ex2_approx(fmaf(dot_row<NQ>(q, k), a.scale_log2, -a.lse_in[row] * kLog2e));
       const float ds = p * (dot_row<NV>(d, v) - a.delta[row]);
       axpy_row<NQ>(dk, ds, q);
       axpy_row<NV>(dv, p, d);
     }
+    if (p != p) {
+      if (nan != nullptr) *nan = 1;
+      return;
+    }
+    if (nan != nullptr && *nan) return;
   }
+}
+
+template <int NQ, int NV>
+__device__ __noinline__ void dkv_row(const WinArgs& a, int s, int g, int lane) {
+  float2 dk[NQ], dv[NV];
+  dkv_sums<NQ, NV>(a, s, g, lane, 0, 1, nullptr, dk, dv);
   const int64_t row = (int64_t)s * a.Hkv + g;
-#pragma unroll
-  for (int i = 0; i < NQ; ++i) {
-    const int d = 64 * i + 2 * lane;
-    if (((d & ~31) - first) % step == 0)
-      *reinterpret_cast<__nv_bfloat162*>(a.dk + row * (64 * NQ) + d) = __floats2bfloat162_rn(dk[i].x * a.scale, dk[i].y * a.scale);
-  }
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int d = 64 * i + 2 * lane;
-    if ((((64 * NQ + d) & ~31) - first) % step == 0)
-      *reinterpret_cast<__nv_bfloat162*>(a.dv + row * (64 * NV) + d) = __floats2bfloat162_rn(dv[i].x, dv[i].y);
-  }
+  store_row<NQ>(dk, a.scale, a.dk + row * (64 * NQ), lane);
+  store_row<NV>(dv, 1.f, a.dv + row * (64 * NV), lane);
 }
 
 }  // namespace

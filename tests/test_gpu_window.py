@@ -381,3 +381,69 @@ def test_dq_repairs_do_not_hold_up_the_pipeline(irs):
         assert torch.isnan(t).flatten(1).sum(1).nonzero()[:, 0].tolist() == [A - 1]
     _check_dq_rows(*(t.cpu() for t in (q, k, v)), cu, T, 0, out.cpu(), lse.cpu(), do.cpu(), dq,
                    [0, 1000, A - 17, A - 9, A - 8, A - 2, A - 1, A, A + 9, T - 3000, T - 1])
+
+
+def _check_key_rows(q, k, v, cu, window, sinks, out, lse, do, dk, dv, keys):
+    """Some rows of dk and dv (one KV head) against the formula in 64 bits on the GPU, with the roundings that
+    serving_ref.window_bwd counts."""
+    Dq, Dv, G = q.shape[2], v.shape[2], q.shape[1]
+    scale = 1 / math.sqrt(Dq)
+    for s in keys:
+        b = int(torch.searchsorted(cu, s, right=True)) - 1
+        start, end = int(cu[b]), int(cu[b + 1])
+        end = end if s - start < sinks else min(end, s + window)
+        qs, ds_, os_ = (x[s:end].double().flatten(0, 1) for x in (q, do, out))
+        l, kt, vt = lse[s:end].double().flatten(), k[s, 0].double(), v[s, 0].double()
+        p = torch.exp(qs @ kt * scale - l)
+        y = ds_ @ vt - (ds_ * os_).sum(-1)
+        ymag = ds_.abs() @ vt.abs() + (ds_ * os_).abs().sum(-1)
+        ep = p * ((Dq + 4) * R.U32 * (qs.abs() @ kt.abs()) * scale + 2.0 ** -21 + 4 * R.U32 * l.abs())
+        w = p * y * scale
+        ew = (ep * y.abs() + p * (Dv + 4) * R.U32 * ymag) * scale + R.U16 * w.abs()
+        for got, x, e, a, what in ((dk, w, ew, qs, "dk"), (dv, p, ep + R.U16 * p, ds_, "dv")):
+            r = x @ a
+            bound = R.U16 * r.abs() + (e + 64 * R.U32 * x.abs()) @ a.abs() + 1e-30
+            _same(got[s, 0], r.cpu(), bound.cpu(), (s, what))
+
+
+@pytest.mark.parametrize("window,sinks", [(40_000, 0), (300, 3), (5000, 64)])
+@pytest.mark.parametrize("which", ["q", "dout", "lse"])
+def test_keys_repaired_outside_the_pipeline(irs, window, sinks, which):
+    """A NaN in one head of a query reaches every key of the tiles that load it. Those that do not see it are computed
+    again; with a window of 40,000 and 16 heads a key that is done by one warp while its tile's block waits takes longer
+    than the waits last (32 keys of 640,000 rows of some 0.3 us). First tokens that see it and first tokens that do not
+    are summed over stretches."""
+    A, T = 40_000, 60_000
+    g = torch.Generator(device=DEV).manual_seed(window)
+    n = lambda *s: torch.randn(*s, generator=g, device=DEV).to(torch.bfloat16)  # noqa: E731
+    q, k, v, do = n(T, 16, 64), n(T, 1, 64), n(T, 1, 64), n(T, 16, 64)
+    cu = torch.tensor([0, A, T], dtype=torch.int32)
+    out, lse = irs.window_gqa_attn_fwd(q, k, v, cu.to(DEV), window, sinks=sinks)
+    for t in (10, 29_000):
+        {"q": q, "dout": do, "lse": lse}[which][t, 2] = math.nan
+    dq, dk, dv = irs.window_gqa_attn_bwd(q, k, v, cu.to(DEV), window, out, lse, do, sinks=sinks)
+    irs.check_device_errors(DEV)
+    seen = {s for t in (10, 29_000) for s in (*range(min(sinks, t + 1)), *range(max(0, t - window + 1), t + 1))}
+    for t in (dk, dv):
+        assert set(torch.isnan(t).flatten(1).any(1).nonzero()[:, 0].tolist()) == seen
+    _check_key_rows(q, k, v, cu, window, sinks, out, lse, do, dk, dv,
+                    [0, 1, 2, 3, 10, 11, 12, 63, 64, 127, 128, 130, 28_000, 28_672, 28_701, 28_999, 29_000, 29_001, 29_055,
+                     29_100, 39_999, A, A + 1, A + 70, T - 1])
+    again = irs.window_gqa_attn_bwd(q, k, v, cu.to(DEV), window, out, lse, do, sinks=sinks)
+    for a, b in zip((dq, dk, dv), again):
+        assert torch.equal(a.view(torch.int16), b.view(torch.int16))   # NaN as well
+
+
+def test_everything_nan_and_the_next_call(irs):
+    """A step that has diverged gives NaN everywhere, and the same workspace then serves a clean one."""
+    q, k, v, do, cu = (t.to(DEV) for t in _inputs(3000, 8, 2, 128, 128, [1700, 1, 1299]))
+    ws = torch.full((64 << 20,), 255, dtype=torch.uint8, device=DEV)
+    out, lse = irs.window_gqa_attn_fwd(q, k, v, cu, 500, sinks=4)
+    want = irs.window_gqa_attn_bwd(q, k, v, cu, 500, out, lse, do, sinks=4, workspace=ws)
+    bad = torch.full_like(q, math.nan)
+    o, l = irs.window_gqa_attn_fwd(bad, k, v, cu, 500, sinks=4)
+    got = irs.window_gqa_attn_bwd(bad, k, v, cu, 500, o, l, do, sinks=4, workspace=ws)
+    assert all(torch.isnan(t).all() for t in (o, l) + tuple(got))
+    again = irs.window_gqa_attn_bwd(q, k, v, cu, 500, out, lse, do, sinks=4, workspace=ws)
+    assert all(torch.equal(a, b) for a, b in zip(want, again))
+    irs.check_device_errors(DEV)
