@@ -30,8 +30,8 @@
 // * The maximum is raised, and the output rescaled, only where a score passes it by 2^8:
 //   weights then stay below 2^8 and sums below 2^8 n, harmless in FP32, and the rescaling of
 //   Dv/2 registers a thread leaves the loop almost entirely.
-// * A weight enters the second product as two bf16 terms (its rounding and the rest), which
-//   keeps 16 bits of it; the extra product costs tensor time that HBM-bound code has.
+// * A weight enters the second product as two bf16 terms (its first eight bits and the rest),
+//   which keeps 16 bits of it; the extra product costs tensor time that HBM-bound code has.
 // * Measured: 64 sequences of 20,000 to 50,000 positions, 64 / 8 heads of 128: 1.30 ms, 7.0
 //   TB/s; 2051 routes of 96 sequences, 32 / 8 heads of 128: 132 us, 6.1 TB/s; 512 + 4
 //   positions of 128 sequences, 64 / 4 heads of 192 / 128: 35 us for 120 MB, where the start
@@ -112,12 +112,15 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// x and y as bf16 pairs: the rounded values, and what the rounding left.
+// Weights x and y (>= 0) as two bf16 pairs: cut to eight bits, and what the cut left, rounded: 2^-16
+// of the weight is lost at most. Neither term is negative, and the second is never 0 (2^-126 where
+// nothing is left, which no sum notices): times an infinite value both give that infinity, where a
+// rest of 0 or of the other sign would make it NaN. Masked rows are 0 in shared memory.
 __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
-  const float2 f = __bfloat1622float2(h);
-  const __nv_bfloat162 l = __floats2bfloat162_rn(x - f.x, y - f.y);
-  hi = *reinterpret_cast<const uint32_t*>(&h);
+  const uint32_t xi = __float_as_uint(x), yi = __float_as_uint(y);
+  hi = __byte_perm(xi, yi, 0x7632);
+  const __nv_bfloat162 l = __hmax2(__floats2bfloat162_rn(x - __uint_as_float(xi & 0xffff0000u), y - __uint_as_float(yi & 0xffff0000u)),
+                                   __halves2bfloat162(__ushort_as_bfloat16(0x0080), __ushort_as_bfloat16(0x0080)));
   lo = *reinterpret_cast<const uint32_t*>(&l);
 }
 

@@ -539,3 +539,30 @@ def test_decode_one_workspace_for_calls_in_order(irs):
         for w in (ws, ws[:64]):
             got = irs.paged_gqa_attn_decode(*args, workspace=w)
             assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_decode_attended_infinities(irs):
+    """An infinite value under a positive weight gives that infinity, two of opposite sign NaN, and the other columns and
+    heads are as ever: in sequences that one run holds and in ones that are cut, with the largest weight exactly 1."""
+    g = torch.Generator().manual_seed(31)
+    lens = [1, 9, 40, 3000, 700, 17]
+    kc, vc, table = _pool(g, lens, 16, 2, 128, 128)
+    q = _normal(g, 6, 8, 128)
+    at = lambda b, p: (int(table[b, p // 16]), p % 16)  # noqa: E731
+    vc[at(0, 0)][0, 3] = math.inf                            # the only position
+    vc[at(1, 8)][1, 7] = -math.inf
+    for p, x in ((2, math.inf), (30, -math.inf)):            # opposite signs in one column
+        vc[at(2, p)][0, 60] = x
+    for p in (5, 1400, 2999):
+        vc[at(3, p)][0, 100] = math.inf
+    vc[at(4, 699)][1, 0] = -math.inf
+    vc[at(5, 16)][0, 127] = math.nan
+    ln = torch.tensor(lens, dtype=torch.int32)
+    ref = R.decode(q, kc, vc, table, ln, 0.1)
+    out, lse = irs.paged_gqa_attn_decode(q.to(DEV), kc.to(DEV), vc.to(DEV), table.to(DEV), ln.to(DEV), 0.1)
+    irs.check_device_errors(DEV)
+    nan = torch.isnan(ref[0])
+    assert torch.isinf(ref[0]).any() and nan.any()
+    assert torch.equal(torch.isnan(out.cpu()), nan)
+    R.check(out.cpu().masked_fill(nan, 0), ref[0].masked_fill(nan, 0), ref[2].masked_fill(nan, 1), "out")
+    R.check(lse, ref[1], ref[3], "lse")
