@@ -528,8 +528,8 @@ irs_status irs_rope(const void* x, int64_t x_stride_t, int64_t x_stride_h, const
  * p % page_size. The new tokens are rows of q, k and v: sequence b's are
  * [cu_new[b], cu_new[b+1]) at the positions cache_lens[b], cache_lens[b] + 1, ...
  * (cu_new NULL: row b is sequence b's only new token, T == B). cache_lens holds the lengths
- * BEFORE the call and is not changed. Rows behind cu_new[B] are left as they were, in q_out
- * and k_out too.
+ * BEFORE the call and is not changed. Rows behind cu_new[B], and rows before a first entry that
+ * is not 0, belong to no sequence: they are left as they were, in q_out and k_out too.
  *
  * q          bf16 [T, Hq, Dqk] by strides, q_out likewise (may be q); Hq = 0: no queries
  * k, v       bf16 [T, Hkv, Dqk], [T, Hkv, Dv] by strides
@@ -539,7 +539,8 @@ irs_status irs_rope(const void* x, int64_t x_stride_t, int64_t x_stride_h, const
  * k_out      NULL, or bf16 by strides: the rotated keys a second time, contiguous use
  * A token whose length or page lies outside the pool (IRS_DEVERR_PAGE) is not written to the
  * cache. Two tokens of one call must not share a slot: a page that new tokens fall in
- * belongs to one sequence. A cu_new that falls or passes T sets IRS_DEVERR_CU_SEQLENS.
+ * belongs to one sequence. A cu_new that does not start at 0, falls or passes T sets
+ * IRS_DEVERR_CU_SEQLENS.
  * max_pages * page_size <= 2^30.
  */
 irs_status irs_paged_rope_append(const void* q, int64_t q_stride_t, int64_t q_stride_h, const void* k,

@@ -68,7 +68,7 @@ __device__ __forceinline__ void rotate8(uint4& a, uint4& b, const float (&cs)[8]
   }
 }
 
-// The sequence of token t: the last b with cu[b] <= t (sequences may be empty).
+// The sequence of token t: the last b with cu[b] <= t (sequences may be empty), or 0.
 __device__ __forceinline__ int sequence_of(const int32_t* cu, int B, int t) {
   int lo = 0, hi = B;   // cu[lo] <= t < cu[hi] where cu is well formed
   while (hi - lo > 1) {
@@ -131,8 +131,10 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_kernel(RopeArgs a) {
     int64_t kslot = -1, vslot = -1;   // element offsets of the token's cache rows
     if (paged) {
       const int b = cu != nullptr ? sequence_of(cu, a.B, (int)t) : (int)t;
+      const int row0 = cu != nullptr ? cu[b] : (int)t;
+      if (row0 < 0 || row0 > t) continue;   // a cu_new that does not start at 0: the row is no sequence's
       const int len = a.cache_lens[b];
-      pos = len + (cu != nullptr ? (int)t - cu[b] : 0);
+      pos = len + ((int)t - row0);
       const int pg = pos / a.page_size;
       int page = -1;
       if (len >= 0 && pos >= 0 && pg < a.max_pages) page = a.page_table[(int64_t)b * a.table_stride + pg];

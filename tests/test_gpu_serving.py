@@ -566,3 +566,27 @@ def test_decode_attended_infinities(irs):
     assert torch.equal(torch.isnan(out.cpu()), nan)
     R.check(out.cpu().masked_fill(nan, 0), ref[0].masked_fill(nan, 0), ref[2].masked_fill(nan, 1), "out")
     R.check(lse, ref[1], ref[3], "lse")
+
+
+@pytest.mark.parametrize("cu", [[2, 4, 6], [3, 3, 6], [-2, 3, 6], [-(2**31), 3, 6]])
+def test_append_leaves_rows_before_the_first_sequence(irs, cu):
+    """A cu_new that does not start at 0 is reported; rows that belong to no sequence are written nowhere, least of all
+    over the sequence's older keys."""
+    g = torch.Generator().manual_seed(41)
+    lens = [20, 33]
+    kc, vc, table = _pool(g, [48, 48], 16, 1, 64, 64)
+    k, v, q = _normal(g, 6, 1, 64), _normal(g, 6, 1, 64), _normal(g, 6, 2, 64)
+    kd, vd = kc.to(DEV), vc.to(DEV)
+    q_out = torch.full((6, 2, 64), 7.0, dtype=torch.bfloat16, device=DEV)
+    k_out = torch.full((6, 1, 64), 7.0, dtype=torch.bfloat16, device=DEV)
+    irs.read_device_errors(DEV)
+    irs.paged_rope_append(q.to(DEV), k.to(DEV), v.to(DEV), kd, vd, table.to(DEV), torch.tensor(lens, dtype=torch.int32, device=DEV),
+                          cu_new=torch.tensor(cu, dtype=torch.int32, device=DEV), q_out=q_out, k_out=k_out)
+    assert irs.read_device_errors(DEV) == irs.DEVERR_CU_SEQLENS
+    for b in range(2):
+        for i in range(max(cu[b], 0) if cu[b] >= 0 else cu[b + 1], cu[b + 1]):
+            p = lens[b] + i - cu[b]
+            kc[int(table[b, p // 16]), p % 16], vc[int(table[b, p // 16]), p % 16] = k[i], v[i]
+    assert torch.equal(kd.cpu(), kc) and torch.equal(vd.cpu(), vc)
+    none = cu[0] if cu[0] >= 0 else cu[1]
+    assert (q_out[:none] == 7).all() and (k_out[:none] == 7).all() and torch.equal(q_out[none:].cpu(), q[none:])
