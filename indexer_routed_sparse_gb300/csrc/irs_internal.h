@@ -268,7 +268,7 @@ cudaError_t launch_window_fwd_tc(const WinMaps& m, const WinArgs& a, int num_sms
 cudaError_t launch_window_fwd_rows(const WinArgs& a, cudaStream_t stream);
 cudaError_t launch_window_bwd_rows(const WinArgs& a, cudaStream_t stream);
 
-// First tokens with queries beyond the window (backward): the documents that have them, cut
+// First tokens with many queries beyond the window (backward): the documents that have them, cut
 // into stretches of queries, and FP32 sums [Dqk | Dv] of each first token and KV head.
 struct WinSinks {
   int slots, chunks;   // upper bounds of the documents and stretches

@@ -30,7 +30,10 @@
 // * First tokens are seen by every later query of their document, so their sums are long.
 //   Queries beyond the window are cut into stretches, each an item of its own (one tile of
 //   first-token keys) with FP32 partial sums in the workspace; a small kernel adds a first
-//   token's window part and its stretches in order.
+//   token's window part and its stretches in order. Documents with one stretch's queries or
+//   fewer beyond the window leave them to the window's tile: partial sums then grow with the
+//   tokens, not with the documents (4000 documents of 16 tokens, window 8, 64 first tokens, 8
+//   heads of 192 / 128 would have 5.4 GB of them).
 // * Roundings: P and dS are bf16 as first operands (half a step, 2^-8, of each, on products
 //   whose sums are FP32); D comes from the bf16 output the caller kept, as in the routed
 //   attention's backward: half a step of the output, which tells only where a row sees a few
@@ -591,8 +594,18 @@ struct DkvWalk {
   }
 };
 
-// Queries of one stretch beyond the window.
-__host__ __device__ inline int sink_stretch(int window) { return window < 256 ? 256 : window > 4096 ? 4096 : window; }
+// Queries of one stretch beyond the window. At least eight a first token, so that the stretches' FP32
+// rows stay a small part of the batch's (3 / 8 of one a key at most).
+__host__ __device__ inline int sink_stretch(int window, int sinks) {
+  const int n = window > 8 * sinks ? window : 8 * sinks;
+  return n < 256 ? 256 : n > 4096 ? 4096 : n;
+}
+// Whether a document of `len` tokens has stretches of its own. With no more than one stretch's
+// queries beyond the window, its first tokens' window tile takes those as well: as many blocks,
+// and no partial sums.
+__device__ __forceinline__ bool sink_far(const WinArgs& a, int len) {
+  return a.sinks > 0 && len - a.window > sink_stretch(a.window, a.sinks);
+}
 
 __device__ __forceinline__ DkvItem dkv_item(const WinArgs& a, const WinSinks& sk, int item, int tiles, int qt, int nhc) {
   DkvItem m;
@@ -605,7 +618,7 @@ __device__ __forceinline__ DkvItem dkv_item(const WinArgs& a, const WinSinks& sk
     m.t0 = m.s0;
     const int sl = m.s0 + m.keys - 1;
     const WinDoc d = window_doc(a.cu, a.ndocs, a.T, sl);
-    m.t1 = (int)min((int64_t)sl + a.window, (int64_t)d.end);
+    m.t1 = max(m.s0 - d.start, 0) < a.sinks && !sink_far(a, d.end - d.start) ? d.end : (int)min((int64_t)sl + a.window, (int64_t)d.end);
   } else {
     m.chunk = u - tiles;
     int lo = 0, hi = a.ndocs;   // chunk0[lo] <= chunk < chunk0[hi]
@@ -616,7 +629,7 @@ __device__ __forceinline__ DkvItem dkv_item(const WinArgs& a, const WinSinks& sk
     const int start = min(max(a.cu[lo], 0), a.T - 1), end = max(min(a.cu[lo + 1], a.T), start + 1);
     m.s0 = start;
     m.keys = min(a.sinks, end - start);
-    const int n = sink_stretch(a.window);
+    const int n = sink_stretch(a.window, a.sinks);
     m.t0 = (int)min((int64_t)end, (int64_t)start + a.window + (int64_t)(m.chunk - sk.chunk0[lo]) * n);
     m.t1 = min(end, m.t0 + n);
   }
@@ -812,7 +825,8 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
       int di = 0;
       const WinDoc doc = window_doc(a.cu, a.ndocs, a.T, min(s, a.T - 1), &di);
       // this key's queries of the item: [from, to)
-      const int past = (int)min((int64_t)s + a.window, (int64_t)(m.chunk < 0 ? doc.end : m.t1));
+      const int past = s - doc.start < a.sinks && !sink_far(a, doc.end - doc.start)
+                           ? doc.end : (int)min((int64_t)s + a.window, (int64_t)(m.chunk < 0 ? doc.end : m.t1));
       const int from = m.chunk < 0 ? s : past;
       const int to = m.chunk < 0 ? past : m.t1;
       // a block is whole when every key of the tile sees every row
@@ -885,7 +899,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
       if (!__all_sync(0xffffffffu, mbar_wait(acc_full, ni & 1, abort_flag, a.err))) break;
       tc_fence_after();
       // ---- this key's sums [dk | dv], pieces of 32 columns in turn ----
-      const bool far = m.chunk >= 0 || (s - doc.start < a.sinks && doc.end - doc.start > a.window && sk.slots > 0);
+      const bool far = m.chunk >= 0 || (s - doc.start < a.sinks && sink_far(a, doc.end - doc.start) && sk.slots > 0);
       float* part = nullptr;   // FP32 rows of first tokens
       if (m.chunk >= 0) part = sk.part + (((int64_t)m.chunk * a.Hkv + m.g) * a.sinks + r) * (DQK + DV);
       else if (live && far) part = sk.base + (((int64_t)sk.slot[di] * a.Hkv + m.g) * a.sinks + (s - doc.start)) * (DQK + DV);
@@ -939,18 +953,17 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
 // ---------------------------------------------------------------------------------------
 constexpr int kPlanThreads = 1024;
 
-// slot[d]: the document's place among those longer than the window; chunk0[d]: its first
+// slot[d]: the document's place among those with stretches; chunk0[d]: its first
 // stretch; doc[slot]. One block.
 __global__ void __launch_bounds__(kPlanThreads) window_plan_kernel(WinArgs a, WinSinks sk) {
   __shared__ int s_slot[kPlanThreads], s_chunk[kPlanThreads];
   const int tid = threadIdx.x;
   const int per = (a.ndocs + kPlanThreads - 1) / kPlanThreads;
   const int b = min(a.ndocs, tid * per), e = min(a.ndocs, b + per);
-  const int n = sink_stretch(a.window);
+  const int n = sink_stretch(a.window, a.sinks);
   auto chunks_of = [&](int d) {
     const int start = min(max(a.cu[d], 0), a.T - 1), end = max(min(a.cu[d + 1], a.T), start + 1);
-    const int far = end - start - a.window;
-    return far > 0 ? (far + n - 1) / n : 0;
+    return sink_far(a, end - start) ? (end - start - a.window + n - 1) / n : 0;
   };
   int slots = 0, chunks = 0;
   for (int d = b; d < e; ++d) {
@@ -1121,10 +1134,10 @@ size_t window_bwd_layout(uint8_t* ws, int T, int Hq, int Hkv, int Dqk, int Dv, i
   a->delta = reinterpret_cast<float*>(take((size_t)T * Hq * 4));
   a->redo = reinterpret_cast<uint32_t*>(take((size_t)redo_words(T, Hkv) * 4));
   *s = WinSinks{};
-  const int64_t longer = (int64_t)T / ((int64_t)window + 1);   // documents that can be longer than the window
+  const int64_t longer = (int64_t)T / ((int64_t)window + sink_stretch(window, sinks) + 1);   // documents that can have stretches
   s->slots = sinks > 0 ? (int)(longer < ndocs ? longer : ndocs) : 0;
   if (s->slots > 0) {
-    s->chunks = T / sink_stretch(window) + s->slots;
+    s->chunks = T / sink_stretch(window, sinks) + s->slots;
     s->slot = reinterpret_cast<int*>(take((size_t)ndocs * 4));
     s->chunk0 = reinterpret_cast<int*>(take((size_t)(ndocs + 1) * 4));
     s->doc = reinterpret_cast<int*>(take((size_t)(s->slots + 1) * 4));

@@ -447,3 +447,12 @@ def test_everything_nan_and_the_next_call(irs):
     again = irs.window_gqa_attn_bwd(q, k, v, cu, 500, out, lse, do, sinks=4, workspace=ws)
     assert all(torch.equal(a, b) for a, b in zip(want, again))
     irs.check_device_errors(DEV)
+
+
+@pytest.mark.parametrize("docs,window,sinks", [
+    ([21, 22, 100, 275, 276, 277, 278, 300, 700], 20, 5), ([31, 349, 350, 351, 352, 40, 700], 30, 40),
+    ([600, 1, 1030, 1156, 1157], 130, 128), ([17] * 60 + [9, 8, 300], 8, 64), ([5, 520, 519, 515, 3], 259, 3)])
+def test_first_tokens_just_past_the_window(irs, docs, window, sinks):
+    """Documents with as many queries beyond the window as their first tokens' tile takes, one fewer and one more, and
+    first tokens in two tiles."""
+    _case(irs, *_inputs(sum(docs), 4, 2, 64, 64, docs), window=window, sinks=sinks)

@@ -230,3 +230,12 @@ def test_reference_decode_is_the_windows_last_row():
         assert torch.allclose(w[0][-1], d[0][0], atol=1e-14) and torch.allclose(w[1][-1], d[1][0], atol=1e-14)
     r = R.decode(q[-1:], kc, vc, table, torch.tensor([n]), 0.125, routes=torch.arange(n)[None])
     assert torch.allclose(r[0], R.decode(q[-1:], kc, vc, table, torch.tensor([n]), 0.125)[0], atol=1e-14)
+
+
+@pytest.mark.parametrize("T,ndocs,window,sinks", [(131072, 1000, 128, 128), (65536, 4000, 8, 64), (65536, 1, 1, 1),
+                                                  (1 << 20, 1 << 19, 1, 128), (32768, 11, 512, 4), (50, 50, 1, 128), (9000, 3, 8000, 128)])
+def test_window_backward_workspace_grows_with_tokens(lib, T, ndocs, window, sinks):
+    """However many documents there are: D and the marks of keys, and FP32 rows for 3 of 8 keys at most."""
+    Hq, Hkv, Dqk, Dv = 16, 8, 192, 128
+    got = lib.irs_window_gqa_attn_bwd_workspace_bytes(T, Hq, Hkv, Dqk, Dv, ndocs, window, sinks)
+    assert got <= 4 * T * Hq + T * Hkv // 8 + 12 * ndocs + 4096 + 3 * T // 8 * Hkv * (Dqk + Dv) * 4
