@@ -508,7 +508,8 @@ irs_status irs_sparse_gqa_attn_bwd(const void* q, int64_t q_stride_t, int64_t q_
  * inv_freq  fp64 [rope_dims / 2] DEVICE, radians per token (finite)
  * out       bf16 by strides; out may be x with x's strides, and no other overlap
  * sizes: D % 8 == 0, rope_dims a multiple of 16 in [0, D], start % 8 == 0, start + rope_dims
- *        <= D; strides and pointers keep rows 16-byte aligned; T = 0 does nothing
+ *        <= D; strides and pointers keep rows 16-byte aligned; rows of out do not overlap;
+ *        T = 0 does nothing
  */
 #define IRS_ROPE_HALF 0
 #define IRS_ROPE_INTERLEAVED 1
@@ -536,7 +537,9 @@ irs_status irs_rope(const void* x, int64_t x_stride_t, int64_t x_stride_h, const
  * cu_new     NULL or int32 [B + 1] DEVICE, from 0, never falling, at most T
  * page_table int32 [B, max_pages] DEVICE; only the new tokens' entries are read
  * rope_dims  0: nothing is rotated (inv_freq may be NULL)
- * k_out      NULL, or bf16 by strides: the rotated keys a second time, contiguous use
+ * k_out      NULL, or bf16 by strides: the rotated keys a second time, contiguous use (may be k)
+ * Strides of 0 (one row for several) are for q, k and v alone: rows of the caches and outputs
+ * do not overlap.
  * A token whose length or page lies outside the pool (IRS_DEVERR_PAGE) is not written to the
  * cache. Two tokens of one call must not share a slot: a page that new tokens fall in
  * belongs to one sequence. A cu_new that does not start at 0, falls or passes T sets

@@ -845,6 +845,9 @@ bool bad_stride(std::initializer_list<int64_t> strides) {
   return false;
 }
 
+// Whether rows of `row` elements `stride` apart along a dim of n entries are written over one another.
+bool rows_meet(int n, int64_t stride, int row) { return n > 1 && stride < row; }
+
 irs_status check_rope(const double* inv_freq, int D, int rope_dims, int start, int layout, float amplitude) {
   if (D < 8 || D % 8 != 0 || D > 4096) return fail(IRS_ERR_VALUE, "the head dim must be a multiple of 8 in [8, 4096] (got %d)", D);
   if (rope_dims < 0 || rope_dims % 16 != 0) return fail(IRS_ERR_VALUE, "rope_dims must be a multiple of 16 (got %d)", rope_dims);
@@ -887,6 +890,8 @@ irs_status irs_rope(const void* x, int64_t x_stride_t, int64_t x_stride_h, const
     return fail(IRS_ERR_VALUE, "strides must be non-negative multiples of 8 elements (16 bytes)");
   if (x == out && (x_stride_t != out_stride_t || x_stride_h != out_stride_h))
     return fail(IRS_ERR_VALUE, "out may be x only with x's strides");
+  if (rows_meet(T, out_stride_t, D) || rows_meet(H, out_stride_h, D))
+    return fail(IRS_ERR_VALUE, "rows of out overlap: strides of at least D are needed");
   DeviceInfo* dev = nullptr;
   if ((s = current_device(&dev)) != IRS_OK) return s;
   irs::RopeArgs a{};
@@ -933,6 +938,14 @@ irs_status irs_paged_rope_append(const void* q, int64_t q_stride_t, int64_t q_st
     return fail(IRS_ERR_VALUE, "strides must be non-negative multiples of 8 elements (16 bytes)");
   if (Hq > 0 && q == q_out && (q_stride_t != qo_stride_t || q_stride_h != qo_stride_h))
     return fail(IRS_ERR_VALUE, "q_out may be q only with q's strides");
+  if (k == k_out && (k_stride_t != ko_stride_t || k_stride_h != ko_stride_h))
+    return fail(IRS_ERR_VALUE, "k_out may be k only with k's strides");
+  if (rows_meet(num_pages, kc_stride_p, Dqk) || rows_meet(page_size, kc_stride_t, Dqk) || rows_meet(Hkv, kc_stride_h, Dqk) ||
+      rows_meet(num_pages, vc_stride_p, Dv) || rows_meet(page_size, vc_stride_t, Dv) || rows_meet(Hkv, vc_stride_h, Dv))
+    return fail(IRS_ERR_VALUE, "rows of a cache overlap: strides of at least the head dim are needed");
+  if ((Hq > 0 && (rows_meet(T, qo_stride_t, Dqk) || rows_meet(Hq, qo_stride_h, Dqk))) ||
+      (k_out != nullptr && (rows_meet(T, ko_stride_t, Dqk) || rows_meet(Hkv, ko_stride_h, Dqk))))
+    return fail(IRS_ERR_VALUE, "rows of q_out or k_out overlap: strides of at least Dqk are needed");
   DeviceInfo* dev = nullptr;
   if ((s = current_device(&dev)) != IRS_OK) return s;
   irs::RopeArgs a{};

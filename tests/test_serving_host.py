@@ -239,3 +239,27 @@ def test_window_backward_workspace_grows_with_tokens(lib, T, ndocs, window, sink
     Hq, Hkv, Dqk, Dv = 16, 8, 192, 128
     got = lib.irs_window_gqa_attn_bwd_workspace_bytes(T, Hq, Hkv, Dqk, Dv, ndocs, window, sinks)
     assert got <= 4 * T * Hq + T * Hkv // 8 + 12 * ndocs + 4096 + 3 * T // 8 * Hkv * (Dqk + Dv) * 4
+
+
+@pytest.mark.parametrize("ot,oh", [(0, 128), (256, 0), (64, 128), (256, 120)])
+def test_rope_refuses_outputs_that_overlap_themselves(lib, p, ot, oh):
+    """Tokens or heads that share a row of the output would be written over one another in any order."""
+    _refused(lib, lib.irs_rope(p, 256, 128, p, p, 4, 2, 128, 64, 0, 0, 1.0, 0, p + 512, ot, oh, None), b"overlap")
+
+
+@pytest.mark.parametrize("which", range(6))
+@pytest.mark.parametrize("stride", [0, 64])
+def test_append_refuses_caches_that_overlap_themselves(lib, p, which, stride):
+    st = [4096, 256, 128, 4096, 256, 128]
+    st[which] = stride
+    _refused(lib, lib.irs_paged_rope_append(None, 0, 0, p, 256, 128, p, 256, 128, p, 4, 2, 0, 2, 128, 128, p, 8, 8, 9, 16, p, p, 64,
+                                            0, 1, 1.0, p, *st[:3], p, *st[3:], None, 0, 0, None, 0, 0, None, None), b"overlap")
+
+
+@pytest.mark.parametrize("qo,ko,word", [((0, 128), (256, 128), b"overlap"), ((512, 0), (256, 128), b"overlap"),
+                                        ((512, 128), (0, 128), b"overlap"), ((512, 128), (256, 0), b"overlap"),
+                                        ((512, 128), (512, 128), b"k's strides")])
+def test_append_refuses_outputs_that_overlap(lib, p, qo, ko, word):
+    k_out = p if word == b"k's strides" else p + 256
+    _refused(lib, lib.irs_paged_rope_append(p, 512, 128, p, 256, 128, p, 256, 128, p, 4, 2, 4, 2, 128, 128, p, 8, 8, 9, 16, p, p, 64,
+                                            0, 1, 1.0, p, 4096, 256, 128, p, 4096, 256, 128, p + 512, *qo, k_out, *ko, None, None), word)
