@@ -615,7 +615,7 @@ irs_status irs_paged_gqa_attn_decode(const void* q, int64_t q_stride_b, int64_t 
  *             otherwise: outputs are then undefined)
  * sizes: Hq % Hkv == 0, Hq / Hkv <= 128, Dqk in {64, 128, 192}, Dv in {64, 128}, window >= 1,
  *        0 <= sinks <= 128, scale > 0 (finite); T = 0 does nothing
- * out  bf16 [T, Hq, Dv] contiguous;  lse  fp32 [T, Hq] contiguous (may be NULL)
+ * out  bf16 [T, Hq, Dv] contiguous, apart from q, k and v;  lse  fp32 [T, Hq] contiguous (may be NULL)
  */
 irs_status irs_window_gqa_attn_fwd(const void* q, int64_t q_stride_t, int64_t q_stride_h, const void* k,
                                    int64_t k_stride_t, int64_t k_stride_h, const void* v, int64_t v_stride_t,
@@ -631,7 +631,7 @@ irs_status irs_window_gqa_attn_fwd(const void* q, int64_t q_stride_t, int64_t q_
  *
  * out, dout  bf16 [T, Hq, Dv] contiguous;  lse  fp32 [T, Hq] contiguous
  * dq  bf16 [T, Hq, Dqk], dk  bf16 [T, Hkv, Dqk], dv  bf16 [T, Hkv, Dv]: contiguous, 16-byte
- *     aligned, overwritten (sums in FP32, rounded once)
+ *     aligned, overwritten (sums in FP32, rounded once); apart from the inputs and one another
  * workspace  irs_window_gqa_attn_bwd_workspace_bytes(...) bytes, 256-byte aligned; nothing
  *            in it outlives the call, and calls that may overlap need one each. 4 T Hq bytes, and
  *            with first tokens FP32 sums of 3 T / 8 key and value rows at most

@@ -1062,6 +1062,22 @@ bool window_has_maps(const irs::WinArgs& a) {
   return ok(a.q_st, a.q_sh, a.Hq) && ok(a.k_st, a.k_sh, a.Hkv) && ok(a.v_st, a.v_sh, a.Hkv);
 }
 
+// The bytes that a [T, heads, row] bf16 tensor reaches over.
+struct Span {
+  uintptr_t from, to;
+};
+Span span_of(const void* p, int T, int64_t stride_t, int heads, int64_t stride_h, int row) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+  return Span{a, a + 2 * (uintptr_t)((T - 1) * stride_t + (heads - 1) * stride_h + row)};
+}
+Span span_of(const void* p, int T, int heads, int row) { return span_of(p, T, (int64_t)heads * row, heads, row, row); }
+// Kernels read their inputs again after the first outputs are written.
+bool meets(const Span& out, std::initializer_list<Span> others) {
+  for (const Span& o : others)
+    if (out.from < o.to && o.from < out.to) return true;
+  return false;
+}
+
 // Checks shared by the window forward and backward; fills the arguments both need.
 irs_status window_args(irs::WinArgs* a, const void* q, int64_t q_stride_t, int64_t q_stride_h, const void* k,
                        int64_t k_stride_t, int64_t k_stride_h, const void* v, int64_t v_stride_t, int64_t v_stride_h,
@@ -1111,6 +1127,8 @@ irs_status irs_window_gqa_attn_fwd(const void* q, int64_t q_stride_t, int64_t q_
                              cu_seqlens, ndocs, window, sinks, T, Hq, Hkv, Dqk, Dv, scale, err_flag);
   if (s != IRS_OK || T == 0) return s;
   if (!out || !aligned16(out)) return fail(IRS_ERR_VALUE, "out must be a 16-byte aligned buffer");
+  const Span in[] = {span_of(q, T, a.q_st, Hq, a.q_sh, Dqk), span_of(k, T, a.k_st, Hkv, a.k_sh, Dqk), span_of(v, T, a.v_st, Hkv, a.v_sh, Dv)};
+  if (meets(span_of(out, T, Hq, Dv), {in[0], in[1], in[2]})) return fail(IRS_ERR_VALUE, "out overlaps q, k or v");
   DeviceInfo* dev = nullptr;
   if ((s = current_device(&dev)) != IRS_OK) return s;
   a.out = bf(out);
@@ -1148,6 +1166,12 @@ irs_status irs_window_gqa_attn_bwd(const void* q, int64_t q_stride_t, int64_t q_
   if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return fail(IRS_ERR_VALUE, "workspace must be 256-byte aligned");
   const size_t need = irs::window_bwd_workspace_bytes(T, Hq, Hkv, Dqk, Dv, ndocs, window, sinks);
   if (workspace_bytes < need) return fail(IRS_ERR_VALUE, "workspace too small: %zu < %zu bytes", workspace_bytes, need);
+  const Span in[] = {span_of(q, T, a.q_st, Hq, a.q_sh, Dqk), span_of(k, T, a.k_st, Hkv, a.k_sh, Dqk),
+                     span_of(v, T, a.v_st, Hkv, a.v_sh, Dv), span_of(out, T, Hq, Dv), span_of(dout, T, Hq, Dv)};
+  const Span grads[] = {span_of(dq, T, Hq, Dqk), span_of(dk, T, Hkv, Dqk), span_of(dv, T, Hkv, Dv)};
+  for (const Span& g : grads)
+    if (meets(g, {in[0], in[1], in[2], in[3], in[4]})) return fail(IRS_ERR_VALUE, "dq, dk or dv overlaps q, k, v, out or dout");
+  if (meets(grads[0], {grads[1], grads[2]}) || meets(grads[1], {grads[2]})) return fail(IRS_ERR_VALUE, "dq, dk and dv overlap");
   DeviceInfo* dev = nullptr;
   if ((s = current_device(&dev)) != IRS_OK) return s;
   a.out = bf(const_cast<void*>(out));

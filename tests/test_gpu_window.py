@@ -456,3 +456,28 @@ def test_first_tokens_just_past_the_window(irs, docs, window, sinks):
     """Documents with as many queries beyond the window as their first tokens' tile takes, one fewer and one more, and
     first tokens in two tiles."""
     _case(irs, *_inputs(sum(docs), 4, 2, 64, 64, docs), window=window, sinks=sinks)
+
+
+def test_tensors_side_by_side_in_one_buffer(irs):
+    """Inputs and outputs that touch but do not overlap."""
+    q, k, v, do, cu = _inputs(70, 4, 2, 128, 64, [30, 40])
+    dev = [t.to(DEV) for t in (q, k, v, cu)]
+    out, lse = irs.window_gqa_attn_fwd(*dev, 20, sinks=2)
+    want = irs.window_gqa_attn_bwd(*dev, 20, out, lse, do.to(DEV), sinks=2)
+    buf = torch.zeros(2 * sum(t.numel() for t in (q, k, v, do)), dtype=torch.bfloat16, device=DEV)
+    at, mine = 0, []
+    for t in (out, q, v, do, want[1], k, want[0], want[2]):
+        mine.append(buf[at:at + t.numel()].view(t.shape))
+        at += t.numel()
+    for d, t in zip(mine, (None, q, v, do, None, k)):
+        if t is not None:
+            d.copy_(t)
+    o, qm, vm, dm, dk, km, dq, dv = mine
+    _, l = irs.window_gqa_attn_fwd(qm, km, vm, dev[3], 20, sinks=2, out=o)
+    irs.window_gqa_attn_bwd(qm, km, vm, dev[3], 20, o, l, dm, sinks=2, dq=dq, dk=dk, dv=dv)
+    assert torch.equal(o, out) and all(torch.equal(a, b) for a, b in zip((dq, dk, dv), want))
+    with pytest.raises(ValueError, match="overlap"):
+        irs.window_gqa_attn_bwd(qm, km, vm, dev[3], 20, o, l, dm, sinks=2, dq=qm)
+    with pytest.raises(ValueError, match="overlap"):
+        irs.window_gqa_attn_fwd(qm, km, vm, dev[3], 20, out=buf[64:64 + o.numel()].view(o.shape))
+    irs.check_device_errors(DEV)

@@ -263,3 +263,14 @@ def test_append_refuses_outputs_that_overlap(lib, p, qo, ko, word):
     k_out = p if word == b"k's strides" else p + 256
     _refused(lib, lib.irs_paged_rope_append(p, 512, 128, p, 256, 128, p, 256, 128, p, 4, 2, 4, 2, 128, 128, p, 8, 8, 9, 16, p, p, 64,
                                             0, 1, 1.0, p, 4096, 256, 128, p, 4096, 256, 128, p + 512, *qo, k_out, *ko, None, None), word)
+
+
+@pytest.mark.parametrize("bwd,kw", [(False, dict(out=q)) for q in "qkv"] + [
+    (True, {o: i}) for o in ("dq", "dk", "dv") for i in ("q", "k", "v", "out", "dout")] + [(True, dict(dk="dq")), (True, dict(dv="dk"))])
+@pytest.mark.parametrize("by", [0, 256])
+def test_window_refuses_outputs_over_inputs(lib, p, bwd, kw, by):
+    """Rows that are computed again, and dk and dv, read inputs after the first outputs are written. One output lies at
+    or just behind the start of another tensor; all the others are apart."""
+    at = {n: p + (i << 20) for i, n in enumerate(("q", "k", "v", "cu", "out", "lse", "dout", "dq", "dk", "dv", "ws"))}
+    at.update({o: at[i] + by for o, i in kw.items()})
+    _refused(lib, _window(lib, p, bwd, **at), b"overlap")
