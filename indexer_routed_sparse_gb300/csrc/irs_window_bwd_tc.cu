@@ -308,8 +308,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
         switch (cols_of(j) >> 5) {
           case 1: ts_run<2>(tb + C::DQ0, tb + C::DS0, kb, C::kv_atom, DQ_IDESC, j > 0); break;
           case 2: ts_run<4>(tb + C::DQ0, tb + C::DS0, kb, C::kv_atom, DQ_IDESC, j > 0); break;
-          case 3: ts_run<6>(tb + C::DQ0, tb + C::DS0, kb, C::kv_atom, DQ_IDESC, j > 0); break;
-          default: ts_run<8>(tb + C::DQ0, tb + C::DS0, kb, C::kv_atom, DQ_IDESC, j > 0); break;
+          default: ts_run<6>(tb + C::DQ0, tb + C::DS0, kb, C::kv_atom, DQ_IDESC, j > 0); break;
         }
         umma_commit_warp(ds_empty);
         umma_commit_warp(&k_empty[kd]);

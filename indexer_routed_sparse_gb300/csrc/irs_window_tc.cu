@@ -4,7 +4,8 @@
 // max(s_d, t - window + 1), and the first tokens s_d <= s < min(s_d + sinks, lo).
 //
 // What bounds it. 2 (Dqk + Dv) flops a (query, head, key) pair on operands that stay in L2:
-// the tensor cores, with the exponentials (one a pair) close behind.
+// the tensor cores by count. As it runs no unit is full (tensor pipe 41% active, issue 48%, the
+// exponential unit 17% at T 8192): the softmax's and the products' turns are.
 //
 // Design.
 // * The 128 rows of a product are the G query heads of a KV head for 128 / G queries, so a
@@ -26,9 +27,9 @@
 //   and are the first operand of O += P V straight from TMEM (V read MN-major from its
 //   [key][dim] tile). No register may be spilled: shared memory leaves no L1, and a spilled
 //   word is a trip to L2 (12 words in the loop: 1.53 -> 1.73 ms).
-// * The running maximum is raised only where a half row's weights under it sum past 2^8 (sums are FP32), so
-//   that after a tile's first block the scores are read once and O in TMEM is hardly ever
-//   rescaled.
+// * The running maximum is raised only where a half row's weights under it sum past 2^8 (sums
+//   are FP32), so that after a tile's first block the scores are read once and O in TMEM is
+//   hardly ever rescaled.
 // * Documents are not aligned to tiles: a tile's keys are one range of the packed sequence,
 //   and each row masks by its own document's start. Only blocks at a border of the range are
 //   masked element by element. First tokens before the range are one more (narrow) block.
@@ -76,7 +77,7 @@ struct FwdCfg {
   static constexpr uint32_t redo_off = plan_off + 4 * 32;       // [16][2] first and last item of a softmax warp with marked rows
   static constexpr uint32_t cu_off = redo_off + 16 * 8;
   static constexpr int cu_cap = (int)((232448u - cu_off) / 4u) < 2048 ? (int)((232448u - cu_off) / 4u) : 2048;
-  static constexpr uint32_t total = cu_off + 4u * cu_cap;   // 226.3 KB at 192/128: none to spare for aligning
+  static constexpr uint32_t total = cu_off + 4u * cu_cap;   // all of 227 KB at 192/128: none to spare for aligning
   static constexpr uint32_t S0 = 0, O0 = 256;              // TMEM: S of tile x, buffer b at 128 x + 64 b; O at 256 + x DV
 };
 
@@ -332,7 +333,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const int bar_id = 1 + x * 4 + (warp & 3);            // the two warps of these rows
     const int r = (warp & 3) * 32 + lane;                 // row of the tile = TMEM lane
     const int rq = r / a.G;                               // its query
-    // its row of out, relative to the tile's first, and those of the four lanes that store together
+    // its row of out, relative to the tile's first
     const int rel = rq < qt ? rq * a.Hq + r - rq * a.G : -1;
     const uint32_t s_base = tbase + C::S0 + 128 * x + tmem_lane_base(warp);
     const uint32_t o_addr = tbase + C::O0 + x * DV + tmem_lane_base(warp);
@@ -547,8 +548,6 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 int window_fwd_block() { return FwdCfg<128, 128>::BLK; }
 
 namespace {
-
-
 
 template <int DQK, int DV>
 cudaError_t launch_fwd(const WinMaps& m, const WinArgs& a, int num_sms, bool* configured, cudaStream_t stream) {
