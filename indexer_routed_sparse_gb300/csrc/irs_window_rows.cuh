@@ -84,15 +84,16 @@ __device__ __noinline__ void fwd_row(const WinArgs& a, int t, int h, int lane) {
     float2 x[NQ], y[NV];
     load_row<NQ>(x, a.k + (int64_t)s * a.k_st + (int64_t)g * a.k_sh, lane);
     load_row<NV>(y, a.v + (int64_t)s * a.v_st + (int64_t)g * a.v_sh, lane);
-    const float sc = dot_row<NQ>(q, x) * a.scale_log2;
-    const float mn = fmaxf(m, sc);
-    const float c = ex2_approx(m - mn), p = ex2_approx(sc - mn);
-    m = mn;
+    const float sc = dot_row<NQ>(q, x) * a.scale_log2, was = m;
+    m = fmaxf(m, sc);
+    const float off = m == -INFINITY ? 0.f : m;   // scores of -inf so far: weights of 0
+    const float c = ex2_approx(was - off), p = ex2_approx(sc - off);
     l = fmaf(l, c, p);
 #pragma unroll
     for (int i = 0; i < NV; ++i) { o[i].x *= c; o[i].y *= c; }
     axpy_row<NV>(o, p, y);
   }
+  if (l == 0.f) l = NAN;   // no score above -inf: 0 / 0
   store_row<NV>(o, 1.f / l, a.out + ((int64_t)t * a.Hq + h) * (64 * NV), lane);
   if (a.lse != nullptr && lane == 0) a.lse[(int64_t)t * a.Hq + h] = fmaf(m, kLn2, logf(l));
 }

@@ -481,3 +481,25 @@ def test_tensors_side_by_side_in_one_buffer(irs):
     with pytest.raises(ValueError, match="overlap"):
         irs.window_gqa_attn_fwd(qm, km, vm, dev[3], 20, out=buf[64:64 + o.numel()].view(o.shape))
     irs.check_device_errors(DEV)
+
+
+@pytest.mark.parametrize("shared", [True, False])
+def test_scores_of_minus_infinity(irs, shared):
+    """A visible key with a score of -inf has weight 0, also as the first that a row sees; a row that sees no other key
+    is NaN, as the formula's 0 / 0. On the path for shared key rows, and where a NaN in a masked value row makes the
+    rows be computed again."""
+    q, k, v, _, cu = _inputs(90, 4, 2, 64, 64, [40, 50])
+    q[:, :, 0] = 1.0
+    k[40, :, 0], v[39] = -math.inf, math.nan                 # the second document's first key; the first one's last value
+    if shared:
+        k, v = (t[:, :1].expand(90, 2, 64) for t in (k, v))
+    dev = [t.to(DEV) for t in (q, cu)]
+    kd, vd = ((t[:, :1].to(DEV).expand(90, 2, 64) if shared else t.to(DEV)) for t in (k, v))
+    out, lse = irs.window_gqa_attn_fwd(dev[0], kd, vd, dev[1], 30, sinks=2)
+    irs.check_device_errors(DEV)
+    assert torch.isnan(out[40]).all() and torch.isnan(lse[40]).all() and torch.isnan(out[39]).all()
+    for t, at in _rows(cu, [0, 30, 38, *range(41, 90)], 30, 2):
+        at = at[at != 40]
+        o, l, eo, el = R._attend(q[t].double().view(2, 2, 64), k[at].double(), v[at].double(), 0.125)
+        _same(out[t].view(o.shape), o, eo, (t, "out"))
+        _same(lse[t].view(l.shape), l, el, (t, "lse"))
