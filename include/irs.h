@@ -572,9 +572,10 @@ irs_status irs_paged_rope_append(const void* q, int64_t q_stride_t, int64_t q_st
  * With KV head g = h / (Hq/Hkv) and that set R:
  *   s_r = scale * q[b,h,:] . k_r[g,:],  out = sum_r e^{s_r - m} v_r[g,:] / sum_r e^{s_r - m},
  *   lse = m + ln sum_r e^{s_r - m}
- * A sequence with no position (L = 0, or all routes padding) gives out = 0, lse = -inf.
- * Route entries other than -1 outside [0, L) are padding and set IRS_DEVERR_ROUTE_ID; entries
- * must be distinct. A length below 0 or past max_pages * page_size reads as 0 and a position
+ * A sequence with no position (L = 0, or all routes padding) gives out = 0, lse = -inf; one
+ * whose scores are all -inf gives NaN, as the formula does.
+ * Route entries other than -1 outside [0, L) are padding and (where L > 0) set
+ * IRS_DEVERR_ROUTE_ID; entries must be distinct. A length below 0 or past max_pages * page_size reads as 0 and a position
  * whose page lies outside the pool is skipped; both set IRS_DEVERR_PAGE. Rows of the pool
  * that no position points at are never read.
  *

@@ -331,6 +331,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) paged_decode_kernel(PagedAr
 #pragma unroll
       for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
     float mx[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};   // rows g4 and g4 + 8
+    uint32_t seen = 0u;                                        // whether any position was attended
 
     for (int it = 0; it < tiles; ++it) {
       cp_async_wait_pending(S - 2);
@@ -340,6 +341,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) paged_decode_kernel(PagedAr
       step_a();
       const uint32_t kd = ring + (uint32_t)slot * kStage, vd = kd + kTile * DQK * 2;
       const uint32_t mask = masks[warp * S + slot];
+      seen |= mask;
       slot = slot + 1 == S ? 0 : slot + 1;
       // S = Q K^T: two halves of 8 positions
       float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
@@ -414,6 +416,8 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) paged_decode_kernel(PagedAr
     for (int i = 0; i < 2; ++i) {
       l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
       l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+      // attended, and every score -inf: 0 / 0; in a part -1, which a finite maximum wipes out
+      if (l[i] == 0.f && seen != 0u) l[i] = tiles == cc.nt ? NAN : -1.f;
     }
     if (tiles == cc.nt) {
 #pragma unroll
@@ -491,7 +495,7 @@ __global__ void __launch_bounds__(1024) paged_join_kernel(PagedArgs a, int nhb, 
       const float n = fmaxf(M, m);
       const float u = n == -INFINITY ? 0.f : ex2_approx(M - n), v = n == -INFINITY ? 0.f : ex2_approx(m - n);
       M = n;
-      ls = fmaf(ls, u, l * v);
+      ls = n == -INFINITY ? ls + l : fmaf(ls, u, l * v);
       s.x = fmaf(s.x, u, x.x * v);
       s.y = fmaf(s.y, u, x.y * v);
       s.z = fmaf(s.z, u, x.z * v);
@@ -529,6 +533,7 @@ __global__ void __launch_bounds__(1024) paged_join_kernel(PagedArgs a, int nhb, 
       __syncthreads();
     }
     if (part_grp == 0 && row < nh) {
+      if (ls < 0.f) ls = NAN;
       const float inv = ls == 0.f ? 0.f : 1.f / ls;
       const int64_t r = (int64_t)b * a.Hq + h0 + row;
       __nv_bfloat162 y[2] = {__floats2bfloat162_rn(s.x * inv, s.y * inv), __floats2bfloat162_rn(s.z * inv, s.w * inv)};

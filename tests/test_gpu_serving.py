@@ -590,3 +590,31 @@ def test_append_leaves_rows_before_the_first_sequence(irs, cu):
     assert torch.equal(kd.cpu(), kc) and torch.equal(vd.cpu(), vc)
     none = cu[0] if cu[0] >= 0 else cu[1]
     assert (q_out[:none] == 7).all() and (k_out[:none] == 7).all() and torch.equal(q_out[none:].cpu(), q[none:])
+
+
+def test_decode_scores_of_minus_infinity(irs):
+    """Positions whose score is -inf have weight 0; a sequence whose positions all have it is NaN, as the formula's
+    0 / 0, in one run or cut into parts, while one with no position stays 0."""
+    g = torch.Generator().manual_seed(51)
+    lens = [1, 40, 3000, 3000, 0, 500, 17]
+    kc, vc, table = _pool(g, lens, 16, 2, 64, 64)
+    q = _normal(g, 7, 4, 64)
+    q[:, :, 0] = 1.0
+    gone = [range(1), range(40), range(1000, 3000), range(3000), (), range(200), [16]]
+    clean = kc.clone()
+    for b, ps in enumerate(gone):
+        for p in ps:
+            kc[int(table[b, p // 16]), p % 16, :, 0] = -math.inf
+    routes = torch.full((7, 3000), -1, dtype=torch.int32)    # the definition without those positions
+    for b, n in enumerate(lens):
+        at = [p for p in range(n) if p not in set(gone[b])]
+        routes[b, :len(at)] = torch.tensor(at, dtype=torch.int32)
+    ln = torch.tensor(lens, dtype=torch.int32)
+    ref = R.decode(q, clean, vc, table, ln, 0.125, routes=routes)
+    out, lse = irs.paged_gqa_attn_decode(q.to(DEV), kc.to(DEV), vc.to(DEV), table.to(DEV), ln.to(DEV), 0.125)
+    irs.check_device_errors(DEV)
+    for b in (0, 1, 3):
+        assert torch.isnan(out[b]).all() and torch.isnan(lse[b]).all(), b
+    rest = [2, 4, 5, 6]
+    R.check(out[rest], ref[0][rest], ref[2][rest], "out")
+    R.check(lse[rest], ref[1][rest], ref[3][rest], "lse")
