@@ -32,9 +32,9 @@
 //   Dv/2 registers a thread leaves the loop almost entirely.
 // * A weight enters the second product as two bf16 terms (its first eight bits and the rest),
 //   which keeps 16 bits of it; the extra product costs tensor time that HBM-bound code has.
-// * Measured: 64 sequences of 20,000 to 50,000 positions, 64 / 8 heads of 128: 1.30 ms, 7.0
+// * Measured: 64 sequences of 20,000 to 50,000 positions, 64 / 8 heads of 128: 1.31 ms, 7.0
 //   TB/s; 2051 routes of 96 sequences, 32 / 8 heads of 128: 132 us, 6.1 TB/s; 512 + 4
-//   positions of 128 sequences, 64 / 4 heads of 192 / 128: 35 us for 120 MB, where the start
+//   positions of 128 sequences, 64 / 4 heads of 192 / 128: 36 us for 120 MB, where the start
 //   (lengths, pages, first copies) and the join count.
 #include "irs_internal.h"
 #include "irs_ptx.cuh"

@@ -46,7 +46,7 @@
 //   the workspace) are spread over the GPU by a last small kernel, a block a key.
 // * Measured at the size above: dq 1.03 ms (of its issuing warp's 1.98 million cycles, 1.28
 //   are products on their way, 1.09 by the rates of their shapes; 64 / 4 heads: tiles of 8
-//   queries), dk and dv 1.46 ms.
+//   queries), dk and dv 1.47 ms; looking for marked keys 2 us where there are none.
 #include <climits>
 
 #include "irs_internal.h"

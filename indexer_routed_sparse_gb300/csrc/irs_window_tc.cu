@@ -4,7 +4,7 @@
 // max(s_d, t - window + 1), and the first tokens s_d <= s < min(s_d + sinks, lo).
 //
 // What bounds it. 2 (Dqk + Dv) flops a (query, head, key) pair on operands that stay in L2:
-// the tensor cores by count. As it runs no unit is full (tensor pipe 41% active, issue 48%, the
+// the tensor cores by count. As it runs no unit is full (tensor pipe 41% active, issue 47%, the
 // exponential unit 17% at T 8192): the softmax's and the products' turns are.
 //
 // Design.
@@ -37,7 +37,7 @@
 //   whose sum or output is not finite are marked (a NaN in the output, the item in shared memory)
 //   and computed again from their visible keys alone when the CTA is through with its items: a
 //   row takes as long as its window, and the pipeline's waits have a limit.
-// * Measured: 1.52 ms at the size above (885 TFLOP/s of the pairs that are seen). Of a softmax
+// * Measured: 1.51 ms at the size above (890 TFLOP/s of the pairs that are seen). Of a softmax
 //   warp's 29,300 cycles an item (ten blocks) 17,000 are its work on them, 5,600 its waits for
 //   scores (115 cycles each where nothing is waited for) and 6,500 the item's output; the
 //   products at the rates of their shapes (64 columns read at the limit of shared memory:
