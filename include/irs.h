@@ -632,7 +632,8 @@ irs_status irs_window_gqa_attn_fwd(const void* q, int64_t q_stride_t, int64_t q_
  *
  * out, dout  bf16 [T, Hq, Dv] contiguous;  lse  fp32 [T, Hq] contiguous
  * dq  bf16 [T, Hq, Dqk], dk  bf16 [T, Hkv, Dqk], dv  bf16 [T, Hkv, Dv]: contiguous, 16-byte
- *     aligned, overwritten (sums in FP32, rounded once); apart from the inputs and one another
+ *     aligned, overwritten (sums in FP32, rounded once); apart from q, k, v, dout and one another
+ *     (dq may be out where Dqk = Dv, and dk and dv may lie over it)
  * workspace  irs_window_gqa_attn_bwd_workspace_bytes(...) bytes, 256-byte aligned; nothing
  *            in it outlives the call, and calls that may overlap need one each. 4 T Hq bytes, and
  *            with first tokens FP32 sums of 3 T / 8 key and value rows at most

@@ -1167,10 +1167,12 @@ irs_status irs_window_gqa_attn_bwd(const void* q, int64_t q_stride_t, int64_t q_
   const size_t need = irs::window_bwd_workspace_bytes(T, Hq, Hkv, Dqk, Dv, ndocs, window, sinks);
   if (workspace_bytes < need) return fail(IRS_ERR_VALUE, "workspace too small: %zu < %zu bytes", workspace_bytes, need);
   const Span in[] = {span_of(q, T, a.q_st, Hq, a.q_sh, Dqk), span_of(k, T, a.k_st, Hkv, a.k_sh, Dqk),
-                     span_of(v, T, a.v_st, Hkv, a.v_sh, Dv), span_of(out, T, Hq, Dv), span_of(dout, T, Hq, Dv)};
+                     span_of(v, T, a.v_st, Hkv, a.v_sh, Dv), span_of(dout, T, Hq, Dv)};
   const Span grads[] = {span_of(dq, T, Hq, Dqk), span_of(dk, T, Hkv, Dqk), span_of(dv, T, Hkv, Dv)};
   for (const Span& g : grads)
-    if (meets(g, {in[0], in[1], in[2], in[3], in[4]})) return fail(IRS_ERR_VALUE, "dq, dk or dv overlaps q, k, v, out or dout");
+    if (meets(g, {in[0], in[1], in[2], in[3]})) return fail(IRS_ERR_VALUE, "dq, dk or dv overlaps q, k, v or dout");
+  // a row of out is read for the last time before its row of dq is written, and all before dk and dv
+  if (!(dq == out && Dqk == Dv) && meets(grads[0], {span_of(out, T, Hq, Dv)})) return fail(IRS_ERR_VALUE, "dq overlaps out row by other row");
   if (meets(grads[0], {grads[1], grads[2]}) || meets(grads[1], {grads[2]})) return fail(IRS_ERR_VALUE, "dq, dk and dv overlap");
   DeviceInfo* dev = nullptr;
   if ((s = current_device(&dev)) != IRS_OK) return s;

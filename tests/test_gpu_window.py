@@ -503,3 +503,22 @@ def test_scores_of_minus_infinity(irs, shared):
         o, l, eo, el = R._attend(q[t].double().view(2, 2, 64), k[at].double(), v[at].double(), 0.125)
         _same(out[t].view(o.shape), o, eo, (t, "out"))
         _same(lse[t].view(l.shape), l, el, (t, "lse"))
+
+
+@pytest.mark.parametrize("window,sinks", [(60, 3), (2000, 0)])
+def test_gradients_over_the_output(irs, window, sinks):
+    """dq in out's place, and dk and dv over out: it is not read again, also where rows are computed again."""
+    q, k, v, do, cu = (t.to(DEV) for t in _inputs(3000, 8, 2, 64, 64, [1400, 1600]))
+    out, lse = irs.window_gqa_attn_fwd(q, k, v, cu, window, sinks=sinks)
+    k[700, 0], do[2500, 3] = math.nan, math.nan
+    want = irs.window_gqa_attn_bwd(q, k, v, cu, window, out, lse, do, sinks=sinks)
+    same = lambda a, b: torch.equal(a.view(torch.int16), b.view(torch.int16))  # noqa: E731
+    o = out.clone()
+    got = irs.window_gqa_attn_bwd(q, k, v, cu, window, o, lse, do, sinks=sinks, dq=o)
+    assert got[0] is o and all(same(a, b) for a, b in zip(got, want))
+    o = out.clone()
+    n = k.numel()
+    dk, dv = o.view(-1)[64:64 + n].view(k.shape), o.view(-1)[64 + n:64 + 2 * n].view(v.shape)
+    got = irs.window_gqa_attn_bwd(q, k, v, cu, window, o, lse, do, sinks=sinks, dk=dk, dv=dv)
+    assert all(same(a, b) for a, b in zip(got, want))
+    irs.check_device_errors(DEV)

@@ -266,7 +266,7 @@ def test_append_refuses_outputs_that_overlap(lib, p, qo, ko, word):
 
 
 @pytest.mark.parametrize("bwd,kw", [(False, dict(out=q)) for q in "qkv"] + [
-    (True, {o: i}) for o in ("dq", "dk", "dv") for i in ("q", "k", "v", "out", "dout")] + [(True, dict(dk="dq")), (True, dict(dv="dk"))])
+    (True, {o: i}) for o in ("dq", "dk", "dv") for i in ("q", "k", "v", "dout")] + [(True, dict(dk="dq")), (True, dict(dv="dk"))])
 @pytest.mark.parametrize("by", [0, 256])
 def test_window_refuses_outputs_over_inputs(lib, p, bwd, kw, by):
     """Rows that are computed again, and dk and dv, read inputs after the first outputs are written. One output lies at
@@ -274,3 +274,10 @@ def test_window_refuses_outputs_over_inputs(lib, p, bwd, kw, by):
     at = {n: p + (i << 20) for i, n in enumerate(("q", "k", "v", "cu", "out", "lse", "dout", "dq", "dk", "dv", "ws"))}
     at.update({o: at[i] + by for o, i in kw.items()})
     _refused(lib, _window(lib, p, bwd, **at), b"overlap")
+
+
+@pytest.mark.parametrize("kw", [dict(by=256), dict(Dqk=64), dict(Dv=64)])
+def test_window_backward_refuses_dq_over_other_rows_of_out(lib, p, kw):
+    at = {n: p + (i << 20) for i, n in enumerate(("q", "k", "v", "cu", "out", "lse", "dout", "dk", "dv", "ws"))}
+    kw = dict(kw)
+    _refused(lib, _window(lib, p, True, dq=at["out"] + kw.pop("by", 0), **kw, **at), b"overlaps out")
