@@ -130,7 +130,8 @@ __device__ __forceinline__ int key_end(const WinArgs& a, int s) {
 }
 
 // Sums [dk | dv] of a key over the queries `first`, `first` + `step`, ... of those that see it.
-// Once a weight is NaN, so is every column; warps that share a key say so in *nan.
+// Once every column is NaN (as with the first weight that is) the rest changes nothing; warps that
+// share a key say so in *nan.
 template <int NQ, int NV>
 __device__ __forceinline__ void dkv_sums(const WinArgs& a, int s, int g, int lane, int first, int step, volatile int* nan,
                                          float2 (&dk)[NQ], float2 (&dv)[NV]) {
@@ -142,6 +143,7 @@ __device__ __forceinline__ void dkv_sums(const WinArgs& a, int s, int g, int lan
   for (int i = 0; i < NQ; ++i) dk[i] = make_float2(0.f, 0.f);
 #pragma unroll
   for (int i = 0; i < NV; ++i) dv[i] = make_float2(0.f, 0.f);
+  bool dk_nan = false;
   for (int t = s + first; t < end; t += step) {
     float p = 0.f;
     for (int h = g * a.G; h < (g + 1) * a.G && p == p; ++h) {
@@ -153,8 +155,16 @@ __device__ __forceinline__ void dkv_sums(const WinArgs& a, int s, int g, int lan
       const float ds = p * (dot_row<NV>(d, v) - a.delta[row]);
       axpy_row<NQ>(dk, ds, q);
       axpy_row<NV>(dv, p, d);
+      dk_nan |= ds != ds;
     }
-    if (p != p) {
+    bool over = p != p;
+    if (dk_nan && !over) {
+      over = true;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) over &= dv[i].x != dv[i].x && dv[i].y != dv[i].y;
+      over = __all_sync(0xffffffffu, over);
+    }
+    if (over) {
       if (nan != nullptr) *nan = 1;
       return;
     }
