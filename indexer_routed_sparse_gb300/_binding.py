@@ -139,8 +139,28 @@ def device_error_flag(device=None) -> torch.Tensor:
     """The per-device int32 word the kernels OR IRS_DEVERR_* bits into."""
     dev = torch.device("cuda", torch.cuda.current_device() if device is None else torch.device(device).index)
     if dev.index not in _err_flags:
-        _err_flags[dev.index] = torch.zeros(1, dtype=torch.int32, device=dev)
+        with torch.cuda.device(dev):
+            capturing = torch.cuda.is_current_stream_capturing()
+            flag = _uncaptured_zero(dev) if capturing else torch.zeros(1, dtype=torch.int32, device=dev)
+        _err_flags.setdefault(dev.index, flag)
     return _err_flags[dev.index]
+
+
+def _uncaptured_zero(dev: torch.device) -> torch.Tensor:
+    """An int32 0 that exists now, although the current stream is being captured: made in the graph it would be
+    cleared by every replay, and not before the first."""
+    driver = ctypes.CDLL("libcuda.so.1")
+    mode = ctypes.c_int(2)   # CU_STREAM_CAPTURE_MODE_RELAXED: this thread may wait for another stream meanwhile
+    if driver.cuThreadExchangeStreamCaptureMode(ctypes.byref(mode)):
+        raise RuntimeError("cuThreadExchangeStreamCaptureMode failed")
+    try:
+        side = torch.cuda.Stream(dev)
+        with torch.cuda.stream(side):
+            word = torch.zeros(1, dtype=torch.int32, device=dev)
+        side.synchronize()
+    finally:
+        driver.cuThreadExchangeStreamCaptureMode(ctypes.byref(mode))
+    return word
 
 
 def read_device_errors(device=None, reset: bool = True) -> int:

@@ -522,3 +522,33 @@ def test_gradients_over_the_output(irs, window, sinks):
     got = irs.window_gqa_attn_bwd(q, k, v, cu, window, o, lse, do, sinks=sinks, dk=dk, dv=dv)
     assert all(same(a, b) for a, b in zip(got, want))
     irs.check_device_errors(DEV)
+
+
+def test_first_call_of_a_process_captured(irs):
+    """The device's error word is made outside the graph: it is clear before the first replay, and a replay does not
+    clear what another call reported."""
+    import os
+    import subprocess
+    import sys
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = """
+import torch
+import indexer_routed_sparse_gb300 as irs
+q = torch.ones(40, 2, 64, dtype=torch.bfloat16, device="cuda")
+cu = torch.tensor([0, 40], dtype=torch.int32, device="cuda")
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    out, lse = irs.window_gqa_attn_fwd(q, q, q, cu, 8)
+assert irs.read_device_errors() == 0
+g.replay()
+torch.cuda.synchronize()
+assert (out == 1).all()
+irs.window_gqa_attn_fwd(q, q, q, torch.tensor([0, 41], dtype=torch.int32, device="cuda"), 8)
+g.replay()
+assert irs.read_device_errors() == irs.DEVERR_CU_SEQLENS
+g.replay()
+assert irs.read_device_errors() == 0
+"""
+    done = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300, cwd=root)
+    assert done.returncode == 0, done.stderr[-2000:]
