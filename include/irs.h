@@ -649,6 +649,107 @@ irs_status irs_window_gqa_attn_bwd(const void* q, int64_t q_stride_t, int64_t q_
                                    size_t workspace_bytes, int32_t* err_flag, irs_stream_t stream);
 
 /*
+ * A serving step's page tables, token positions and slots, from the requests' lengths.
+ *
+ * Sequence b holds n = cache_lens[b] tokens and takes m = new_lens[b] more. Its pages are
+ * page_table[b, 0 .. ceil(n / page_size)); the call gives it those that n + m tokens need
+ * beyond them, in the order of the sequences from the end of the list of free pages: the i-th
+ * page given is free_pages[*free_count - 1 - i]. With groups (P > 0: group g has the sequences
+ * cu_groups[g] .. cu_groups[g+1], whose first prefix_lens[g] tokens are the same) every
+ * sequence behind its group's first takes that one's entries of the pages that the prefix
+ * fills, prefix_lens[g] / page_size of them, where the first has them and the sequence's own n
+ * covers the prefix; a page that a prefix fills in part is each sequence's own.
+ * Results, beside the entries of page_table:
+ *   cu_new    int32 [B + 1]     exclusive sums of new_lens, as irs_paged_rope_append takes them
+ *   positions int32 [tokens]    of each new token in its sequence
+ *   slots     int64 [tokens]    page * page_size + place in the page: the token's row of a pool
+ *   lens_out  int32 [B]         n + m
+ *   free_left int32 [1]         pages still free: the first free_left entries of free_pages
+ * positions and slots behind the last new token are -1. Inputs are not changed, so the same call
+ * gives the same results again.
+ * A sequence that finds too few pages gets none: its new entries and its slots are -1, its
+ * length stays n, and IRS_DEVERR_PAGE is set. So it is for a length or number of new tokens
+ * below 0, and for n + m past max_pages * page_size, which read as m = 0; and for a free_count
+ * outside [0, free_size], which is cut to it. More than `tokens` new ones: the rest has no
+ * position or slot (IRS_DEVERR_CU_SEQLENS); borders of groups that fall, or do not lie in
+ * [0, B] from 0 on, set it too and are cut.
+ * page_table int32 [B, max_pages], rows table_stride apart; B >= 1; max_pages * page_size <=
+ * 2^30. Outputs and page_table overlap neither inputs nor one another.
+ */
+irs_status irs_paged_plan(const int32_t* cache_lens, const int32_t* new_lens, int B, int32_t* page_table,
+                          int64_t table_stride, int max_pages, int page_size, const int32_t* free_pages, int free_size,
+                          const int32_t* free_count, const int32_t* cu_groups, const int32_t* prefix_lens, int P,
+                          int tokens, int32_t* cu_new, int32_t* positions, int64_t* slots, int32_t* lens_out,
+                          int32_t* free_left, int32_t* err_flag, irs_stream_t stream);
+
+/*
+ * shared_prefix_gqa_attn_fwd: attention of prompt tokens over a cached prefix that their
+ * group shares.
+ *
+ * QSA page, `gathered_qsa_gqa_attention` (the same softmax over a set of cached positions), for
+ * a set that many rows share: the prefix's keys and values are read once for all of them. The
+ * tokens cu_rows[g] .. cu_rows[g+1] attend every position of [0, prefix_lens[g]) of prefix g,
+ * whose pages are row g of page_table:
+ *   out, lse as for irs_paged_gqa_attn_decode over that set (an empty one: 0 and -inf)
+ * and with own_out and own_lse, the attention of the same tokens over other keys (their own
+ * prompt: irs_window_gqa_attn_fwd with a window that covers it), the two are joined:
+ *   lse = ln(e^lse_p + e^own_lse),  out = e^(lse_p - lse) out_p + e^(own_lse - lse) own_out
+ * A part whose lse is -inf does not count, whatever its output holds.
+ * Rows behind cu_rows[P] belong to no group and are left as they were.
+ *
+ * q           bf16 [T, Hq, Dqk] by strides;  caches as for irs_paged_rope_append
+ * page_table  int32 [P, max_pages]
+ * cu_rows     int32 [P + 1] DEVICE, from 0, never falling, at most T (IRS_DEVERR_CU_SEQLENS
+ *             otherwise: outputs are then undefined)
+ * prefix_lens int32 [P] DEVICE; one below 0 or past max_pages * page_size reads as 0 and sets
+ *             IRS_DEVERR_PAGE, as does a page outside the pool, with which its group's outputs
+ *             are undefined
+ * own_out     NULL, or bf16 [T, Hq, Dv] contiguous (may be out); own_lse fp32 [T, Hq] (may be lse)
+ * sizes: P >= 1, Hq % Hkv == 0, Hq / Hkv <= 128, Dqk in {64, 128, 192}, Dv in {64, 128}, rows
+ *        16-byte aligned, max_pages * page_size <= 2^30, scale > 0 (finite); T = 0 does nothing
+ * out         bf16 [T, Hq, Dv] contiguous, apart from q;  lse  fp32 [T, Hq] (may be NULL)
+ * workspace   irs_shared_prefix_gqa_attn_fwd_workspace_bytes(...) bytes, 256-byte aligned; nothing
+ *             in it outlives the call, and calls that may overlap need one each
+ * Results do not depend on the run: the split over the prefixes is fixed by the sizes and
+ * lengths, and its parts are joined in order.
+ */
+size_t irs_shared_prefix_gqa_attn_fwd_workspace_bytes(int T, int P, int Hq, int Hkv, int Dv);
+irs_status irs_shared_prefix_gqa_attn_fwd(const void* q, int64_t q_stride_t, int64_t q_stride_h, const void* k_cache,
+                                          int64_t kc_stride_p, int64_t kc_stride_t, int64_t kc_stride_h,
+                                          const void* v_cache, int64_t vc_stride_p, int64_t vc_stride_t,
+                                          int64_t vc_stride_h, const int32_t* page_table, int64_t table_stride,
+                                          int max_pages, int num_pages, int page_size, const int32_t* cu_rows,
+                                          const int32_t* prefix_lens, int P, const void* own_out, const float* own_lse,
+                                          int T, int Hq, int Hkv, int Dqk, int Dv, float scale, void* out, float* lse,
+                                          void* workspace, size_t workspace_bytes, int32_t* err_flag,
+                                          irs_stream_t stream);
+
+/*
+ * shared_prefix_gqa_attn_decode: irs_paged_gqa_attn_decode (every position) of sequences that
+ * share prefixes, each prefix read once for its group.
+ *
+ * Group g has the sequences cu_groups[g] .. cu_groups[g+1]. Their first prefix_lens[g] positions
+ * hold the same keys and values and are read through the page table's row of the group's first
+ * sequence; the positions behind them through each sequence's own row. cache_lens counts both.
+ * Sequences behind cu_groups[P] share nothing. A length of 0 (an idle slot) gives out = 0 and
+ * lse = -inf; so does one below 0, past max_pages * page_size or shorter than its group's
+ * prefix, which sets IRS_DEVERR_PAGE.
+ * An own position whose page lies outside the pool is skipped (IRS_DEVERR_PAGE); with such a page
+ * in a prefix its group's outputs are undefined. prefix_lens, cu_groups, errors, sizes, results and
+ * the workspace as for irs_shared_prefix_gqa_attn_fwd; page_table int32 [B, max_pages]; B * Hq < 2^24,
+ * Hkv * ceil(Hq / Hkv / 16) <= 1024.
+ */
+size_t irs_shared_prefix_gqa_attn_decode_workspace_bytes(int B, int P, int Hq, int Hkv, int Dv);
+irs_status irs_shared_prefix_gqa_attn_decode(const void* q, int64_t q_stride_b, int64_t q_stride_h, const void* k_cache,
+                                             int64_t kc_stride_p, int64_t kc_stride_t, int64_t kc_stride_h,
+                                             const void* v_cache, int64_t vc_stride_p, int64_t vc_stride_t,
+                                             int64_t vc_stride_h, const int32_t* page_table, int64_t table_stride,
+                                             int max_pages, int num_pages, int page_size, const int32_t* cache_lens,
+                                             const int32_t* cu_groups, const int32_t* prefix_lens, int P, int B, int Hq,
+                                             int Hkv, int Dqk, int Dv, float scale, void* out, float* lse, void* workspace,
+                                             size_t workspace_bytes, int32_t* err_flag, irs_stream_t stream);
+
+/*
  * Failure-detection self-test (no counterpart on the reference pages). Launches one
  * bounded on-device wait on a barrier phase that nothing completes: after limit_ns
  * (1e6 .. 2e9) the wait gives up, ORs IRS_DEVERR_TIMEOUT into *err_flag and the kernel

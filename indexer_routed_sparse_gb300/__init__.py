@@ -17,6 +17,9 @@ this package is its thin Python binding. Names follow the C entry points:
 * ``rope`` / ``rope_frequencies``: rotary positions of the attention heads
 * ``paged_rope_append``: new tokens, rotated, into a paged key/value cache
 * ``paged_gqa_attn_decode``: one new token per sequence over that cache
+* ``paged_plan``: page tables, positions and slots of a serving step, from the requests' lengths
+* ``shared_prefix_gqa_attn_fwd`` / ``shared_prefix_gqa_attn_decode``: prompt tokens, and one new
+  token per sequence, over a cached prefix that is read once for all that share it
 """
 from ._binding import (  # noqa: F401
     DEVERR_CU_SEQLENS,
@@ -24,6 +27,7 @@ from ._binding import (  # noqa: F401
     DEVERR_ROUTE_ID,
     DEVERR_TIMEOUT,
     LIB_PATH,
+    PagedPlan,
     check_bounded_wait,
     check_device_errors,
     compose_window_routes,
@@ -34,11 +38,14 @@ from ._binding import (  # noqa: F401
     indexer_projection,
     lib,
     paged_gqa_attn_decode,
+    paged_plan,
     paged_rope_append,
     read_device_errors,
     region_summaries,
     rope,
     rope_frequencies,
+    shared_prefix_gqa_attn_decode,
+    shared_prefix_gqa_attn_fwd,
     sparse_gqa_attn_bwd,
     sparse_gqa_attn_fwd,
     sparse_gqa_attn_fwd_grouped,

@@ -12,6 +12,7 @@ import functools
 import math
 import os
 import threading
+import typing
 
 import torch
 
@@ -78,6 +79,13 @@ _SIGNATURES = {
     "irs_window_gqa_attn_bwd_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I, _I, _I, _I]),
     "irs_window_gqa_attn_bwd": (_I, [_P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _I, _I, _I, _P, _P, _P, _I, _I,
                                      _I, _I, _I, _F, _P, _P, _P, _P, _SZ, _P, _P]),
+    "irs_paged_plan": (_I, [_P, _P, _I, _P, _I64, _I, _I, _P, _I, _P, _P, _P, _I, _I, _P, _P, _P, _P, _P, _P, _P]),
+    "irs_shared_prefix_gqa_attn_fwd_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I]),
+    "irs_shared_prefix_gqa_attn_fwd": (_I, [_P, _I64, _I64, _P, _I64, _I64, _I64, _P, _I64, _I64, _I64, _P, _I64, _I, _I,
+                                            _I, _P, _P, _I, _P, _P, _I, _I, _I, _I, _I, _F, _P, _P, _P, _SZ, _P, _P]),
+    "irs_shared_prefix_gqa_attn_decode_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I]),
+    "irs_shared_prefix_gqa_attn_decode": (_I, [_P, _I64, _I64, _P, _I64, _I64, _I64, _P, _I64, _I64, _I64, _P, _I64, _I,
+                                               _I, _I, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _P, _P, _P, _SZ, _P, _P]),
     "irs_check_bounded_wait": (_I, [ctypes.c_uint64, _P, _P]),
 }
 
@@ -983,6 +991,171 @@ def paged_gqa_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
     _call(index, "paged_gqa_attn_decode", lib().irs_paged_gqa_attn_decode, q.data_ptr(), qb, qh, k_cache.data_ptr(),
           kcs[0], kcs[1], kcs[2], v_cache.data_ptr(), vcs[0], vcs[1], vcs[2], page_table.data_ptr(), ts, max_pages, pages,
           page, cache_lens.data_ptr(), rp, rs, W, window, sinks, B, Hq, Hkv, Dqk, Dv, scale, out.data_ptr(), lp,
+          workspace.data_ptr(), workspace.numel(), _err(err, index))
+    return out, lse
+
+
+class PagedPlan(typing.NamedTuple):
+    """What `paged_plan` returns, beside the entries that it writes into the page table."""
+
+    cu_new: torch.Tensor       # int32 [B + 1]
+    positions: torch.Tensor    # int32 [tokens]
+    slots: torch.Tensor        # int64 [tokens]
+    cache_lens: torch.Tensor   # int32 [B], with the new tokens
+    free_count: torch.Tensor   # int32 [1], pages still free
+
+
+def _packed(t: torch.Tensor, name: str, shape: tuple, index: int) -> int:
+    """The address of a contiguous int32 tensor of this shape."""
+    got, _ = _look(t, name, _I32, len(shape), index)
+    if tuple(got) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor {shape}, got {tuple(got)}")
+    return t.data_ptr()
+
+
+def _groups(cu: torch.Tensor, prefix_lens: torch.Tensor, name: str, index: int) -> tuple[int, int, int]:
+    """(address of the borders, of the prefix lengths, number of groups)."""
+    P = _look(prefix_lens, "prefix_lens", _I32, 1, index)[0][0]
+    return _packed(cu, name, (P + 1,), index), _packed(prefix_lens, "prefix_lens", (P,), index), P
+
+
+def paged_plan(cache_lens: torch.Tensor, new_lens: torch.Tensor, page_table: torch.Tensor, free_pages: torch.Tensor,
+               free_count: torch.Tensor, page_size: int, tokens: int, *, cu_groups: torch.Tensor | None = None,
+               prefix_lens: torch.Tensor | None = None, out: PagedPlan | None = None,
+               err: torch.Tensor | None = None) -> PagedPlan:
+    """A serving step's page tables, token positions and slots, from the requests' lengths.
+
+    cache_lens int32 [B], the lengths BEFORE the step, and new_lens int32 [B], the tokens that
+    each sequence takes; page_table int32 [B, max_pages], in which the pages that the new tokens
+    need are entered; free_pages int32 [n], of which the first free_count (int32 [1]) are free
+    and are given out from the end; tokens: rows of the results for tokens, at least the sum of
+    new_lens (a padded batch has more: -1). With cu_groups int32 [P + 1] and prefix_lens int32
+    [P] the sequences behind a group's first take its entries of the pages that the prefix fills.
+
+    Returns cu_new and positions, which `paged_rope_append` and `rope` take, slots (rows of a
+    pool seen as [pages * page_size, ...]), and the lengths and free pages after the step. The
+    inputs are not changed, so results replace them by the caller's hand. A sequence that finds
+    too few free pages gets none, keeps its length and sets DEVERR_PAGE.
+    """
+    index = _first(cache_lens, "cache_lens", _I32)
+    B = _look(cache_lens, "cache_lens", _I32, 1, index)[0][0]
+    lens, new = _packed(cache_lens, "cache_lens", (B,), index), _packed(new_lens, "new_lens", (B,), index)
+    (rows, max_pages), ts = _look(page_table, "page_table", _I32, 2, index)
+    if rows != B:
+        raise ValueError(f"page_table must have {B} rows, got {rows}")
+    free = _look(free_pages, "free_pages", _I32, 1, index)[0][0]
+    _packed(free_pages, "free_pages", (free,), index)
+    cu = pl = P = 0
+    if (cu_groups is None) != (prefix_lens is None):
+        raise ValueError("cu_groups and prefix_lens come together")
+    if cu_groups is not None:
+        cu, pl, P = _groups(cu_groups, prefix_lens, "cu_groups", index)
+    if tokens < 0:
+        raise ValueError("tokens must not be negative")
+    got = out if out is not None else (None,) * 5
+    got = PagedPlan(_result(got[0], "cu_new", (B + 1,), _I32, index), _result(got[1], "positions", (tokens,), _I32, index),
+                    _result(got[2], "slots", (tokens,), torch.int64, index), _result(got[3], "cache_lens", (B,), _I32, index),
+                    _result(got[4], "free_count", (1,), _I32, index))
+    _call(index, "paged_plan", lib().irs_paged_plan, lens, new, B, page_table.data_ptr(), ts[0], max_pages, page_size,
+          free_pages.data_ptr(), free, _packed(free_count, "free_count", (1,), index), cu, pl, P, tokens,
+          got.cu_new.data_ptr(), got.positions.data_ptr(), got.slots.data_ptr(), got.cache_lens.data_ptr(),
+          got.free_count.data_ptr(), _err(err, index))
+    return got
+
+
+@functools.lru_cache(maxsize=4096)
+def _prefix_bytes(decode: bool, *sizes: int) -> int:
+    name = "decode" if decode else "fwd"
+    return int(getattr(lib(), f"irs_shared_prefix_gqa_attn_{name}_workspace_bytes")(*sizes))
+
+
+def _prefix_pool(k_cache, v_cache, page_table, index: int):
+    """(shape of the key pool, Dv, its strides, the value pool's, page table shape, row stride)."""
+    ks, kst = _look(k_cache, "k_cache", _BF16, 4, index)
+    vs, vst = _look(v_cache, "v_cache", _BF16, 4, index)
+    if ks[:3] != vs[:3]:
+        raise ValueError(f"shape mismatch: k_cache {tuple(ks)} v_cache {tuple(vs)}")
+    ts, tst = _look(page_table, "page_table", _I32, 2, index)
+    return ks, vs[3], kst, vst, ts, tst[0] if ts[0] > 1 else ts[1]
+
+
+def shared_prefix_gqa_attn_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor,
+                               cu_rows: torch.Tensor, prefix_lens: torch.Tensor, scale: float | None = None, *,
+                               own: tuple[torch.Tensor, torch.Tensor] | None = None, out: torch.Tensor | None = None,
+                               lse: torch.Tensor | None = None, want_lse: bool = True,
+                               workspace: torch.Tensor | None = None,
+                               err: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor | None]:
+    """Attention of prompt tokens over a cached prefix that their group shares: (out bf16
+    [T, Hq, Dv], lse fp32 [T, Hq]).
+
+    q bf16 [T, Hq, Dqk]; the cache as for `paged_rope_append`; page_table int32 [P, max_pages], a
+    row a prefix; cu_rows int32 [P + 1]: the tokens cu_rows[g] .. cu_rows[g+1] attend all of
+    prefix g's prefix_lens[g] (int32 [P]) positions. own: (out, lse) of the same tokens over
+    other keys, such as `window_gqa_attn_fwd` over their own prompts; the result is then the
+    attention over both sets. out and lse may be own's. Rows behind cu_rows[P] are left alone.
+    """
+    index = _first(q, "q", _BF16)
+    (T, Hq, Dqk), (qt, qh, _) = _look(q, "q", _BF16, 3, index)
+    (pages, page, Hkv, D), Dv, kcs, vcs, (rows, max_pages), ts = _prefix_pool(k_cache, v_cache, page_table, index)
+    if D != Dqk:
+        raise ValueError(f"shape mismatch: q {tuple(q.shape)} for a cache of head dim {D}")
+    cu, pl, P = _groups(cu_rows, prefix_lens, "cu_rows", index)
+    if rows != P:
+        raise ValueError(f"page_table must have a row for each of {P} prefixes, got {rows}")
+    op = ol = 0
+    if own is not None:
+        if own[0] is None or own[1] is None:
+            raise TypeError("own must be (out, lse)")
+        op = _result(own[0], "own[0]", (T, Hq, Dv), _BF16, index).data_ptr()
+        ol = _result(own[1], "own[1]", (T, Hq), _F32, index).data_ptr()
+    if scale is None:
+        scale = 1.0 / math.sqrt(Dqk)
+    out = _result(out, "out", (T, Hq, Dv), _BF16, index)
+    lp = 0
+    if lse is not None or want_lse:
+        lse = _result(lse, "lse", (T, Hq), _F32, index)
+        lp = lse.data_ptr()
+    workspace = _scratch(workspace, _prefix_bytes(False, T, P, Hq, Hkv, Dv), index)
+    _call(index, "shared_prefix_gqa_attn_fwd", lib().irs_shared_prefix_gqa_attn_fwd, q.data_ptr(), qt, qh,
+          k_cache.data_ptr(), kcs[0], kcs[1], kcs[2], v_cache.data_ptr(), vcs[0], vcs[1], vcs[2], page_table.data_ptr(), ts,
+          max_pages, pages, page, cu, pl, P, op, ol, T, Hq, Hkv, Dqk, Dv, scale, out.data_ptr(), lp, workspace.data_ptr(),
+          workspace.numel(), _err(err, index))
+    return out, lse
+
+
+def shared_prefix_gqa_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                  page_table: torch.Tensor, cache_lens: torch.Tensor, cu_groups: torch.Tensor,
+                                  prefix_lens: torch.Tensor, scale: float | None = None, *,
+                                  out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                                  want_lse: bool = True, workspace: torch.Tensor | None = None,
+                                  err: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor | None]:
+    """`paged_gqa_attn_decode` of sequences that share prefixes, each read once for its group:
+    (out bf16 [B, Hq, Dv], lse fp32 [B, Hq]).
+
+    cu_groups int32 [P + 1]: the sequences cu_groups[g] .. cu_groups[g+1] hold the same keys and
+    values at their first prefix_lens[g] (int32 [P]) positions, which are read through the page
+    table's row of the group's first sequence; the positions behind them through each sequence's
+    own. cache_lens counts both. Sequences behind the last group share nothing. A length of 0 (an
+    idle slot) gives out = 0 and lse = -inf.
+    """
+    index = _first(q, "q", _BF16)
+    qshape, (qb, qh, _) = _look(q, "q", _BF16, 3, index)
+    (pages, page, Hkv, Dqk), Dv, kcs, vcs, (B, max_pages), ts = _pool(k_cache, v_cache, page_table, cache_lens, index)
+    Hq = qshape[1]
+    if qshape != (B, Hq, Dqk):
+        raise ValueError(f"shape mismatch: q {tuple(qshape)} for {B} sequences of head dim {Dqk}")
+    cu, pl, P = _groups(cu_groups, prefix_lens, "cu_groups", index)
+    if scale is None:
+        scale = 1.0 / math.sqrt(Dqk)
+    out = _result(out, "out", (B, Hq, Dv), _BF16, index)
+    lp = 0
+    if lse is not None or want_lse:
+        lse = _result(lse, "lse", (B, Hq), _F32, index)
+        lp = lse.data_ptr()
+    workspace = _scratch(workspace, _prefix_bytes(True, B, P, Hq, Hkv, Dv), index)
+    _call(index, "shared_prefix_gqa_attn_decode", lib().irs_shared_prefix_gqa_attn_decode, q.data_ptr(), qb, qh,
+          k_cache.data_ptr(), kcs[0], kcs[1], kcs[2], v_cache.data_ptr(), vcs[0], vcs[1], vcs[2], page_table.data_ptr(), ts,
+          max_pages, pages, page, cache_lens.data_ptr(), cu, pl, P, B, Hq, Hkv, Dqk, Dv, scale, out.data_ptr(), lp,
           workspace.data_ptr(), workspace.numel(), _err(err, index))
     return out, lse
 

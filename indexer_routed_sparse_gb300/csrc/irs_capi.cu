@@ -1070,6 +1070,10 @@ Span span_of(const void* p, int T, int64_t stride_t, int heads, int64_t stride_h
   const uintptr_t a = reinterpret_cast<uintptr_t>(p);
   return Span{a, a + 2 * (uintptr_t)((T - 1) * stride_t + (heads - 1) * stride_h + row)};
 }
+Span bytes_of(const void* p, int64_t n) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+  return Span{a, a + (uintptr_t)n};
+}
 Span span_of(const void* p, int T, int heads, int row) { return span_of(p, T, (int64_t)heads * row, heads, row, row); }
 // Kernels read their inputs again after the first outputs are written.
 bool meets(const Span& out, std::initializer_list<Span> others) {
@@ -1198,6 +1202,162 @@ irs_status irs_window_gqa_attn_bwd(const void* q, int64_t q_stride_t, int64_t q_
   std::lock_guard<std::mutex> lk(g_dev_mu);
   return launch_status(irs::launch_window_bwd_tc(m, a, sk, dev->num_sms, dev->window_bwd_configured, st),
                        "launching the window attention backward");
+}
+
+irs_status irs_paged_plan(const int32_t* cache_lens, const int32_t* new_lens, int B, int32_t* page_table,
+                          int64_t table_stride, int max_pages, int page_size, const int32_t* free_pages, int free_size,
+                          const int32_t* free_count, const int32_t* cu_groups, const int32_t* prefix_lens, int P,
+                          int tokens, int32_t* cu_new, int32_t* positions, int64_t* slots, int32_t* lens_out,
+                          int32_t* free_left, int32_t* err_flag, irs_stream_t stream) {
+  if (B < 1 || P < 0 || tokens < 0 || free_size < 0) return fail(IRS_ERR_VALUE, "bad sizes (B=%d P=%d tokens=%d free_size=%d)", B, P, tokens, free_size);
+  if (max_pages < 1 || page_size < 1) return fail(IRS_ERR_VALUE, "bad pool sizes (max_pages=%d page_size=%d)", max_pages, page_size);
+  if ((long long)max_pages * page_size > (1LL << 30)) return fail(IRS_ERR_VALUE, "max_pages * page_size must be at most 2^30");
+  if (B > 1 && table_stride < max_pages) return fail(IRS_ERR_VALUE, "table_stride must be >= max_pages");
+  if (!cache_lens || !new_lens || !page_table || !free_count || !cu_new || !lens_out || !free_left)
+    return fail(IRS_ERR_VALUE, "NULL tensor pointer");
+  if ((tokens > 0 && (!positions || !slots)) || (free_size > 0 && !free_pages) || (P > 0 && (!cu_groups || !prefix_lens)))
+    return fail(IRS_ERR_VALUE, "NULL tensor pointer");
+  const Span out[] = {bytes_of(cu_new, 4 * ((int64_t)B + 1)), bytes_of(positions, 4 * (int64_t)tokens), bytes_of(slots, 8 * (int64_t)tokens),
+                      bytes_of(lens_out, 4 * (int64_t)B), bytes_of(free_left, 4),
+                      bytes_of(page_table, 4 * ((B - 1) * (B > 1 ? table_stride : 0) + max_pages))};
+  const Span in[] = {bytes_of(cache_lens, 4 * (int64_t)B), bytes_of(new_lens, 4 * (int64_t)B), bytes_of(free_pages, 4 * (int64_t)free_size),
+                     bytes_of(free_count, 4), bytes_of(cu_groups, P > 0 ? 4 * ((int64_t)P + 1) : 0), bytes_of(prefix_lens, 4 * (int64_t)P)};
+  // every CTA reads all inputs, some after others have written
+  for (int i = 0; i < 6; ++i) {
+    if (meets(out[i], {in[0], in[1], in[2], in[3], in[4], in[5]})) return fail(IRS_ERR_VALUE, "an output overlaps an input");
+    for (int j = 0; j < i; ++j)
+      if (meets(out[i], {out[j]})) return fail(IRS_ERR_VALUE, "outputs overlap");
+  }
+  DeviceInfo* dev = nullptr;
+  irs_status s = current_device(&dev);
+  if (s != IRS_OK) return s;
+  irs::PlanArgs a{};
+  a.cache_lens = cache_lens; a.new_lens = new_lens;
+  a.page_table = page_table; a.table_stride = table_stride;
+  a.free_pages = free_pages; a.free_count = free_count;
+  a.cu_groups = cu_groups; a.prefix_lens = prefix_lens;
+  a.cu_new = cu_new; a.positions = positions; a.slots = slots;
+  a.lens_out = lens_out; a.free_left = free_left;
+  a.err = err_flag;
+  a.B = B; a.P = P; a.max_pages = max_pages; a.page_size = page_size; a.free_size = free_size; a.tokens = tokens;
+  return launch_status(irs::launch_plan(a, dev->num_sms, reinterpret_cast<cudaStream_t>(stream)), "launching the page plan");
+}
+
+}  // extern "C"
+
+namespace {
+
+// Checks shared by the two forms of shared-prefix attention; fills the arguments both need.
+irs_status prefix_args(irs::PrefixArgs* a, const void* q, int64_t q_stride_t, int64_t q_stride_h, const void* k_cache,
+                       int64_t kc_stride_p, int64_t kc_stride_t, int64_t kc_stride_h, const void* v_cache,
+                       int64_t vc_stride_p, int64_t vc_stride_t, int64_t vc_stride_h, const int32_t* page_table,
+                       int64_t table_stride, int max_pages, int num_pages, int page_size, const int32_t* cu,
+                       const int32_t* prefix_lens, int P, int T, int Hq, int Hkv, int Dqk, int Dv, float scale, void* out,
+                       float* lse, void* workspace, size_t workspace_bytes, size_t need, bool decode, int32_t* err_flag) {
+  if (T < 0 || P < 0 || Hq < 1 || Hkv < 1) return fail(IRS_ERR_VALUE, "bad sizes (T=%d P=%d Hq=%d Hkv=%d)", T, P, Hq, Hkv);
+  if (Hq % Hkv != 0) return fail(IRS_ERR_VALUE, "Hq (%d) must be a multiple of Hkv (%d)", Hq, Hkv);
+  if (Hq / Hkv > 128) return fail(IRS_ERR_VALUE, "at most 128 query heads a KV head (got %d)", Hq / Hkv);
+  if (Dqk != 64 && Dqk != 128 && Dqk != 192) return fail(IRS_ERR_VALUE, "Dqk must be 64, 128 or 192 (got %d)", Dqk);
+  if (Dv != 64 && Dv != 128) return fail(IRS_ERR_VALUE, "Dv must be 64 or 128 (got %d)", Dv);
+  if ((long long)T * Hq >= (1LL << 31)) return fail(IRS_ERR_VALUE, "T * Hq must be below 2^31");
+  if (decode && (long long)T * Hq >= (1LL << 24)) return fail(IRS_ERR_VALUE, "B * Hq must be below 2^24");
+  if (decode && (long long)Hkv * ((Hq / Hkv + 15) / 16) > 1024)
+    return fail(IRS_ERR_VALUE, "at most 1024 KV heads times blocks of 16 query heads");
+  if (!(scale > 0.f) || !std::isfinite(scale)) return fail(IRS_ERR_VALUE, "scale must be positive and finite");
+  if (T == 0) return IRS_OK;
+  if (P < 1) return fail(IRS_ERR_VALUE, "at least one group is needed");
+  irs_status s = check_pool(k_cache, v_cache, page_table, page_table, table_stride, max_pages, num_pages, page_size);
+  if (s != IRS_OK) return s;
+  if (!q || !out || !workspace || !cu || !prefix_lens) return fail(IRS_ERR_VALUE, "NULL tensor pointer");
+  if (!aligned16(q) || !aligned16(out)) return fail(IRS_ERR_VALUE, "q and out must be 16-byte aligned");
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return fail(IRS_ERR_VALUE, "workspace must be 256-byte aligned");
+  if (workspace_bytes < need) return fail(IRS_ERR_VALUE, "workspace too small: %zu < %zu bytes", workspace_bytes, need);
+  one_entry(T, q_stride_t); one_entry(Hq, q_stride_h);
+  one_entry(num_pages, kc_stride_p); one_entry(num_pages, vc_stride_p);
+  one_entry(page_size, kc_stride_t); one_entry(page_size, vc_stride_t);
+  one_entry(Hkv, kc_stride_h); one_entry(Hkv, vc_stride_h);
+  if (bad_stride({q_stride_t, q_stride_h, kc_stride_p, kc_stride_t, kc_stride_h, vc_stride_p, vc_stride_t, vc_stride_h}))
+    return fail(IRS_ERR_VALUE, "strides must be non-negative multiples of 8 elements (16 bytes)");
+  if (meets(span_of(out, T, Hq, Dv), {span_of(q, T, q_stride_t, Hq, q_stride_h, Dqk)})) return fail(IRS_ERR_VALUE, "out overlaps q");
+  a->q = bf(q); a->q_st = q_stride_t; a->q_sh = q_stride_h;
+  a->k = bf(k_cache); a->k_sp = kc_stride_p; a->k_st = kc_stride_t; a->k_sh = kc_stride_h;
+  a->v = bf(v_cache); a->v_sp = vc_stride_p; a->v_st = vc_stride_t; a->v_sh = vc_stride_h;
+  a->page_table = page_table; a->table_stride = table_stride;
+  a->cu = cu; a->prefix_lens = prefix_lens;
+  a->out = bf(out); a->lse = lse;
+  a->ws = static_cast<uint8_t*>(workspace);
+  a->err = err_flag;
+  a->T = T; a->P = P; a->Hq = Hq; a->Hkv = Hkv; a->G = Hq / Hkv; a->Dqk = Dqk; a->Dv = Dv;
+  a->max_pages = max_pages; a->num_pages = num_pages; a->page_size = page_size;
+  a->scale_log2 = scale * 1.4426950408889634f;
+  return IRS_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t irs_shared_prefix_gqa_attn_fwd_workspace_bytes(int T, int P, int Hq, int Hkv, int Dv) {
+  if (T < 0 || P < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Dv < 64) return 0;
+  return irs::prefix_workspace_bytes(T, P, Hq, Hkv, Dv, false);
+}
+
+irs_status irs_shared_prefix_gqa_attn_fwd(const void* q, int64_t q_stride_t, int64_t q_stride_h, const void* k_cache,
+                                          int64_t kc_stride_p, int64_t kc_stride_t, int64_t kc_stride_h,
+                                          const void* v_cache, int64_t vc_stride_p, int64_t vc_stride_t,
+                                          int64_t vc_stride_h, const int32_t* page_table, int64_t table_stride,
+                                          int max_pages, int num_pages, int page_size, const int32_t* cu_rows,
+                                          const int32_t* prefix_lens, int P, const void* own_out, const float* own_lse,
+                                          int T, int Hq, int Hkv, int Dqk, int Dv, float scale, void* out, float* lse,
+                                          void* workspace, size_t workspace_bytes, int32_t* err_flag,
+                                          irs_stream_t stream) {
+  irs::PrefixArgs a{};
+  const size_t need = irs_shared_prefix_gqa_attn_fwd_workspace_bytes(T, P, Hq, Hkv, Dv);
+  irs_status s = prefix_args(&a, q, q_stride_t, q_stride_h, k_cache, kc_stride_p, kc_stride_t, kc_stride_h, v_cache,
+                             vc_stride_p, vc_stride_t, vc_stride_h, page_table, table_stride, max_pages, num_pages, page_size,
+                             cu_rows, prefix_lens, P, T, Hq, Hkv, Dqk, Dv, scale, out, lse, workspace, workspace_bytes, need,
+                             false, err_flag);
+  if (s != IRS_OK || T == 0) return s;
+  if ((own_out == nullptr) != (own_lse == nullptr)) return fail(IRS_ERR_VALUE, "own_out and own_lse come together");
+  if (!aligned16(own_out)) return fail(IRS_ERR_VALUE, "own_out must be 16-byte aligned");
+  // a row of own_out is read by the thread that writes that row of out, and nothing else reads it
+  if (own_out != nullptr && own_out != out && meets(span_of(out, T, Hq, Dv), {span_of(own_out, T, Hq, Dv)}))
+    return fail(IRS_ERR_VALUE, "out overlaps own_out row by other row");
+  if (own_lse != nullptr && lse != nullptr && own_lse != lse &&
+      meets(bytes_of(lse, 4LL * T * Hq), {bytes_of(own_lse, 4LL * T * Hq)}))
+    return fail(IRS_ERR_VALUE, "lse overlaps own_lse row by other row");
+  DeviceInfo* dev = nullptr;
+  if ((s = current_device(&dev)) != IRS_OK) return s;
+  a.own_out = static_cast<const __nv_bfloat16*>(own_out);
+  a.own_lse = own_lse;
+  return launch_status(irs::launch_prefix_rows(a, reinterpret_cast<cudaStream_t>(stream)), "launching shared-prefix attention");
+}
+
+size_t irs_shared_prefix_gqa_attn_decode_workspace_bytes(int B, int P, int Hq, int Hkv, int Dv) {
+  if (B < 0 || P < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Dv < 64) return 0;
+  return irs::prefix_workspace_bytes(B, P, Hq, Hkv, Dv, true);
+}
+
+irs_status irs_shared_prefix_gqa_attn_decode(const void* q, int64_t q_stride_b, int64_t q_stride_h, const void* k_cache,
+                                             int64_t kc_stride_p, int64_t kc_stride_t, int64_t kc_stride_h,
+                                             const void* v_cache, int64_t vc_stride_p, int64_t vc_stride_t,
+                                             int64_t vc_stride_h, const int32_t* page_table, int64_t table_stride,
+                                             int max_pages, int num_pages, int page_size, const int32_t* cache_lens,
+                                             const int32_t* cu_groups, const int32_t* prefix_lens, int P, int B, int Hq,
+                                             int Hkv, int Dqk, int Dv, float scale, void* out, float* lse, void* workspace,
+                                             size_t workspace_bytes, int32_t* err_flag, irs_stream_t stream) {
+  irs::PrefixArgs a{};
+  const size_t need = irs_shared_prefix_gqa_attn_decode_workspace_bytes(B, P, Hq, Hkv, Dv);
+  irs_status s = prefix_args(&a, q, q_stride_b, q_stride_h, k_cache, kc_stride_p, kc_stride_t, kc_stride_h, v_cache,
+                             vc_stride_p, vc_stride_t, vc_stride_h, page_table, table_stride, max_pages, num_pages, page_size,
+                             cu_groups, prefix_lens, P, B, Hq, Hkv, Dqk, Dv, scale, out, lse, workspace, workspace_bytes,
+                             need, true, err_flag);
+  if (s != IRS_OK || B == 0) return s;
+  if (!cache_lens) return fail(IRS_ERR_VALUE, "NULL cache pointer");
+  DeviceInfo* dev = nullptr;
+  if ((s = current_device(&dev)) != IRS_OK) return s;
+  a.cache_lens = cache_lens;
+  return launch_status(irs::launch_prefix_rows(a, reinterpret_cast<cudaStream_t>(stream)), "launching shared-prefix decoding");
 }
 
 }  // extern "C"

@@ -234,6 +234,51 @@ size_t paged_workspace_bytes(int B, int Dv);
 // configured[kPagedKinds]: whose shared-memory limit has been raised on this device
 cudaError_t launch_paged_decode(const PagedArgs& a, int num_sms, bool* configured, cudaStream_t stream);
 
+// A serving step's page tables, token positions and slots.
+struct PlanArgs {
+  const int32_t* cache_lens;   // [B]
+  const int32_t* new_lens;     // [B]
+  int32_t* page_table;         // [B, max_pages] by rows of table_stride
+  int64_t table_stride;
+  const int32_t* free_pages;   // [free_size]
+  const int32_t* free_count;
+  const int32_t* cu_groups;    // [P + 1] (P > 0)
+  const int32_t* prefix_lens;  // [P]
+  int32_t* cu_new;             // [B + 1]
+  int32_t* positions;          // [tokens]
+  int64_t* slots;              // [tokens]
+  int32_t* lens_out;           // [B]
+  int32_t* free_left;
+  int32_t* err;
+  int B, P, max_pages, page_size, free_size, tokens;
+};
+cudaError_t launch_plan(const PlanArgs& a, int num_sms, cudaStream_t stream);
+
+// Attention of many rows over the prefix that their group shares, in a paged cache. Rows are
+// (token, query head) pairs; group g has the tokens cu[g] .. cu[g+1].
+struct PrefixArgs {
+  const __nv_bfloat16* q;     // [T, Hq, Dqk] by strides
+  const __nv_bfloat16* k;     // pool [num_pages, page_size, Hkv, Dqk] by strides
+  const __nv_bfloat16* v;
+  int64_t q_st, q_sh, k_sp, k_st, k_sh, v_sp, v_st, v_sh;
+  const int32_t* page_table;  // prompts: a row a group; decoding: a row a sequence (cache_lens given)
+  int64_t table_stride;
+  const int32_t* cu;          // [P + 1]
+  const int32_t* prefix_lens; // [P]
+  const int32_t* cache_lens;  // decoding: [T] lengths, the prefix's positions among them; else nullptr
+  const __nv_bfloat16* own_out;   // prompts: [T, Hq, Dv] and [T, Hq], joined; or nullptr
+  const float* own_lse;
+  __nv_bfloat16* out;         // [T, Hq, Dv]
+  float* lse;                 // [T, Hq] or nullptr
+  uint8_t* ws;
+  int32_t* err;
+  int T, P, Hq, Hkv, G, Dqk, Dv;
+  int max_pages, num_pages, page_size;
+  float scale_log2;
+};
+size_t prefix_workspace_bytes(int T, int P, int Hq, int Hkv, int Dv, bool decode);
+cudaError_t launch_prefix_rows(const PrefixArgs& a, cudaStream_t stream);
+
 // Attention of packed documents over a sliding window and the documents' first tokens.
 struct WinArgs {
   const __nv_bfloat16* q;
@@ -304,6 +349,36 @@ __device__ __forceinline__ WinDoc window_doc(const int32_t* cu, int ndocs, int T
   return WinDoc{min(max(cu[lo], 0), t), max(min(cu[lo + 1], T), t + 1)};
 }
 
+// Group g of shared-prefix attention: its tokens [first, last) and the positions of its prefix. Borders
+// that fall or pass T are cut, a prefix past the page table's reach reads as none; both are reported
+// by prefix_check.
+struct PrefixGroup {
+  int first, last, n;
+};
+__device__ __forceinline__ PrefixGroup prefix_group(const PrefixArgs& a, int g) {
+  PrefixGroup x;
+  x.first = min(max(__ldg(a.cu + g), 0), a.T);
+  x.last = min(max(__ldg(a.cu + g + 1), x.first), a.T);
+  x.n = __ldg(a.prefix_lens + g);
+  if (x.n < 0 || x.n > a.max_pages * a.page_size) x.n = 0;   // the product is at most 2^30
+  return x;
+}
+// The group of token t, or -1.
+__device__ __forceinline__ int prefix_group_of(const PrefixArgs& a, int t) {
+  if (t < __ldg(a.cu) || t >= __ldg(a.cu + a.P)) return -1;
+  int lo = 0, hi = a.P;   // cu[lo] <= t < cu[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(a.cu + mid) <= t) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+// Positions that the new token of sequence t attends, when n of them are its group's: all of [0, L),
+// none where the length is 0, shorter than the prefix or past the page table's reach.
+__device__ __forceinline__ int prefix_length(const PrefixArgs& a, int t, int n) {
+  const int L = __ldg(a.cache_lens + t);
+  return L < n || L > a.max_pages * a.page_size ? 0 : L;
+}
 // The positions that sequence b's new token attends, in order: `early` first tokens, then
 // `recent` tokens from `first` on, then W routed entries (those inside the first two parts
 // do not count again). A length below 0 or past the page table's reach is reported and read
