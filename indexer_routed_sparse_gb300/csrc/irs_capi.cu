@@ -36,6 +36,7 @@ struct DeviceInfo {
   size_t score_smem = 0, topk_smem = 0, attn_smem = 0, mla_smem = 0, bwd_smem = 0;   // largest configured so far
   bool proj_configured = false;
   bool paged_configured[irs::kPagedKinds] = {};
+  bool prefix_configured[irs::kPrefixKinds] = {}, prefix_own_configured[irs::kPrefixKinds] = {};
   bool window_fwd_configured[irs::kWindowKinds] = {}, window_bwd_configured[irs::kWindowKinds] = {};
 };
 constexpr int kMaxDevices = 64;
@@ -1297,6 +1298,51 @@ irs_status prefix_args(irs::PrefixArgs* a, const void* q, int64_t q_stride_t, in
 
 extern "C" {
 
+}  // extern "C"
+
+namespace {
+
+// 4-D bf16 map of a pool [pages][heads][positions][D], boxes of 64 dims x `chunk` positions; false where
+// a stride cannot be a map's.
+irs_status make_pool_map(CUtensorMap* m, const void* base, int D, const irs::PrefixArgs& a, int64_t sp, int64_t st, int64_t sh,
+                         int chunk, bool* made) {
+  auto ok = [](int n, int64_t s) { return n == 1 || (s > 0 && s < (1LL << 38)); };
+  *made = ok(a.num_pages, sp) && ok(a.page_size, st) && ok(a.Hkv, sh);
+  if (!*made) return IRS_OK;
+  auto fn = encode_fn();
+  if (fn == nullptr) return fail(IRS_ERR_RUNTIME, "cuTensorMapEncodeTiled is unavailable");
+  cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)a.page_size, (cuuint64_t)a.Hkv, (cuuint64_t)a.num_pages};
+  // the stride of a dim with one entry is never used, but has to be a valid one
+  cuuint64_t strides[3] = {(cuuint64_t)(a.page_size > 1 ? st : D) * 2, (cuuint64_t)(a.Hkv > 1 ? sh : D) * 2,
+                           (cuuint64_t)(a.num_pages > 1 ? sp : D) * 2};
+  cuuint32_t box[4] = {64, (cuuint32_t)chunk, 1, 1};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, es,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(IRS_ERR_RUNTIME, "cuTensorMapEncodeTiled (pool) failed (%d)", (int)r);
+  return IRS_OK;
+}
+
+irs_status prefix_maps(irs::PrefixMaps* m, const irs::PrefixArgs& a) {
+  *m = irs::PrefixMaps{};
+  irs_status s;
+  m->has_q = (a.T == 1 || a.q_st > 0) && (a.Hq == 1 || a.q_sh > 0);
+  if (m->has_q && (s = make_packed_map(&m->q, a.q, a.Dqk, a.Hq, a.T, a.q_sh, a.q_st, a.G, 128 / a.G)) != IRS_OK) return s;
+  m->chunk = irs::prefix_chunk(a.Dqk, a.page_size);
+  if (m->chunk > 0) {
+    bool k = false, v = false;
+    if ((s = make_pool_map(&m->k, a.k, a.Dqk, a, a.k_sp, a.k_st, a.k_sh, m->chunk, &k)) != IRS_OK) return s;
+    if ((s = make_pool_map(&m->v, a.v, a.Dv, a, a.v_sp, a.v_st, a.v_sh, m->chunk, &v)) != IRS_OK) return s;
+    if (!k || !v) m->chunk = 0;
+  }
+  return IRS_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
 size_t irs_shared_prefix_gqa_attn_fwd_workspace_bytes(int T, int P, int Hq, int Hkv, int Dv) {
   if (T < 0 || P < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Dv < 64) return 0;
   return irs::prefix_workspace_bytes(T, P, Hq, Hkv, Dv, false);
@@ -1330,7 +1376,11 @@ irs_status irs_shared_prefix_gqa_attn_fwd(const void* q, int64_t q_stride_t, int
   if ((s = current_device(&dev)) != IRS_OK) return s;
   a.own_out = static_cast<const __nv_bfloat16*>(own_out);
   a.own_lse = own_lse;
-  return launch_status(irs::launch_prefix_rows(a, reinterpret_cast<cudaStream_t>(stream)), "launching shared-prefix attention");
+  irs::PrefixMaps m;
+  if ((s = prefix_maps(&m, a)) != IRS_OK) return s;
+  std::lock_guard<std::mutex> lk(g_dev_mu);
+  return launch_status(irs::launch_prefix_fwd(m, a, dev->num_sms, dev->prefix_configured, reinterpret_cast<cudaStream_t>(stream)),
+                       "launching shared-prefix attention");
 }
 
 size_t irs_shared_prefix_gqa_attn_decode_workspace_bytes(int B, int P, int Hq, int Hkv, int Dv) {
@@ -1357,7 +1407,12 @@ irs_status irs_shared_prefix_gqa_attn_decode(const void* q, int64_t q_stride_b, 
   DeviceInfo* dev = nullptr;
   if ((s = current_device(&dev)) != IRS_OK) return s;
   a.cache_lens = cache_lens;
-  return launch_status(irs::launch_prefix_rows(a, reinterpret_cast<cudaStream_t>(stream)), "launching shared-prefix decoding");
+  irs::PrefixMaps m;
+  if ((s = prefix_maps(&m, a)) != IRS_OK) return s;
+  std::lock_guard<std::mutex> lk(g_dev_mu);
+  return launch_status(irs::launch_prefix_decode(m, a, dev->num_sms, dev->prefix_configured, dev->prefix_own_configured,
+                                                 reinterpret_cast<cudaStream_t>(stream)),
+                       "launching shared-prefix decoding");
 }
 
 }  // extern "C"

@@ -210,50 +210,6 @@ struct RopeArgs {
 };
 cudaError_t launch_rope(RopeArgs a, bool half, int num_sms, cudaStream_t stream);
 
-// Attention of one new token per sequence over a paged cache.
-struct PagedArgs {
-  const __nv_bfloat16* q;
-  const __nv_bfloat16* k;     // pool [num_pages, page_size, Hkv, Dqk] by strides
-  const __nv_bfloat16* v;
-  int64_t q_sb, q_sh, k_sp, k_st, k_sh, v_sp, v_st, v_sh;
-  const int32_t* page_table;
-  int64_t table_stride;
-  const int32_t* cache_lens;
-  const int32_t* route;       // [B, W] positions or nullptr
-  int64_t route_stride;
-  __nv_bfloat16* out;         // [B, Hq, Dv]
-  float* lse;                 // [B, Hq] or nullptr
-  uint8_t* ws;
-  int32_t* err;
-  int B, Hq, Hkv, G, Dqk, Dv, W, window, sinks;
-  int max_pages, num_pages, page_size;
-  float scale_log2;
-};
-constexpr int kPagedKinds = 12;   // kernels, by head dims
-size_t paged_workspace_bytes(int B, int Dv);
-// configured[kPagedKinds]: whose shared-memory limit has been raised on this device
-cudaError_t launch_paged_decode(const PagedArgs& a, int num_sms, bool* configured, cudaStream_t stream);
-
-// A serving step's page tables, token positions and slots.
-struct PlanArgs {
-  const int32_t* cache_lens;   // [B]
-  const int32_t* new_lens;     // [B]
-  int32_t* page_table;         // [B, max_pages] by rows of table_stride
-  int64_t table_stride;
-  const int32_t* free_pages;   // [free_size]
-  const int32_t* free_count;
-  const int32_t* cu_groups;    // [P + 1] (P > 0)
-  const int32_t* prefix_lens;  // [P]
-  int32_t* cu_new;             // [B + 1]
-  int32_t* positions;          // [tokens]
-  int64_t* slots;              // [tokens]
-  int32_t* lens_out;           // [B]
-  int32_t* free_left;
-  int32_t* err;
-  int B, P, max_pages, page_size, free_size, tokens;
-};
-cudaError_t launch_plan(const PlanArgs& a, int num_sms, cudaStream_t stream);
-
 // Attention of many rows over the prefix that their group shares, in a paged cache. Rows are
 // (token, query head) pairs; group g has the tokens cu[g] .. cu[g+1].
 struct PrefixArgs {
@@ -276,8 +232,69 @@ struct PrefixArgs {
   int max_pages, num_pages, page_size;
   float scale_log2;
 };
+// TMA maps: queries [T][heads][Dqk] in boxes of 64 dims x G heads x 128/G tokens; the pools
+// [pages][heads][positions][dims] in boxes of 64 dims x `chunk` positions of one head and page.
+struct PrefixMaps {
+  CUtensorMap q, k, v;
+  bool has_q;    // no map where a stride is 0: rows are copied by address
+  int chunk;     // 0: no map, rows are copied by address
+};
+// Positions a TMA copy: the largest power of two that divides a page and a block of keys, if it is 8 or more.
+int prefix_chunk(int Dqk, int page_size);
+constexpr int kPrefixKinds = 6;   // kernels, by head dims
 size_t prefix_workspace_bytes(int T, int P, int Hq, int Hkv, int Dv, bool decode);
-cudaError_t launch_prefix_rows(const PrefixArgs& a, cudaStream_t stream);
+// configured, own_configured [kPrefixKinds]: whose shared-memory limit has been raised on this device
+cudaError_t launch_prefix_fwd(const PrefixMaps& m, const PrefixArgs& a, int num_sms, bool* configured, cudaStream_t stream);
+cudaError_t launch_prefix_decode(const PrefixMaps& m, const PrefixArgs& a, int num_sms, bool* configured, bool* own_configured,
+                                 cudaStream_t stream);
+
+// Attention of one new token per sequence over a paged cache.
+struct PagedArgs {
+  const __nv_bfloat16* q;
+  const __nv_bfloat16* k;     // pool [num_pages, page_size, Hkv, Dqk] by strides
+  const __nv_bfloat16* v;
+  int64_t q_sb, q_sh, k_sp, k_st, k_sh, v_sp, v_st, v_sh;
+  const int32_t* page_table;
+  int64_t table_stride;
+  const int32_t* cache_lens;
+  const int32_t* route;       // [B, W] positions or nullptr
+  int64_t route_stride;
+  __nv_bfloat16* out;         // [B, Hq, Dv]
+  float* lse;                 // [B, Hq] or nullptr
+  uint8_t* ws;
+  int32_t* err;
+  int B, Hq, Hkv, G, Dqk, Dv, W, window, sinks;
+  int max_pages, num_pages, page_size;
+  float scale_log2;
+  PrefixArgs shared;          // of sequences that share prefixes: cu, prefix_lens, cache_lens and sizes
+  float* rows;                // ... FP32 sums of the rows that no run's border cuts
+};
+constexpr int kPagedKinds = 12;   // kernels, by head dims
+size_t paged_workspace_bytes(int B, int Dv);
+// configured[kPagedKinds]: whose shared-memory limit has been raised on this device
+cudaError_t launch_paged_decode(const PagedArgs& a, int num_sms, bool* configured, cudaStream_t stream);
+// The own positions of sequences that share prefixes (kPrefixKinds kernels); *workers: runs of a head's list
+cudaError_t launch_paged_shared(const PagedArgs& a, int num_sms, bool* configured, int* workers, cudaStream_t stream);
+
+// A serving step's page tables, token positions and slots.
+struct PlanArgs {
+  const int32_t* cache_lens;   // [B]
+  const int32_t* new_lens;     // [B]
+  int32_t* page_table;         // [B, max_pages] by rows of table_stride
+  int64_t table_stride;
+  const int32_t* free_pages;   // [free_size]
+  const int32_t* free_count;
+  const int32_t* cu_groups;    // [P + 1] (P > 0)
+  const int32_t* prefix_lens;  // [P]
+  int32_t* cu_new;             // [B + 1]
+  int32_t* positions;          // [tokens]
+  int64_t* slots;              // [tokens]
+  int32_t* lens_out;           // [B]
+  int32_t* free_left;
+  int32_t* err;
+  int B, P, max_pages, page_size, free_size, tokens;
+};
+cudaError_t launch_plan(const PlanArgs& a, int num_sms, cudaStream_t stream);
 
 // Attention of packed documents over a sliding window and the documents' first tokens.
 struct WinArgs {
@@ -372,6 +389,11 @@ __device__ __forceinline__ int prefix_group_of(const PrefixArgs& a, int t) {
     if (__ldg(a.cu + mid) <= t) lo = mid; else hi = mid;
   }
   return lo;
+}
+// Positions that sequence t's group shares (0: it is of no group).
+__device__ __forceinline__ int prefix_positions(const PrefixArgs& a, int t) {
+  const int g = prefix_group_of(a, t);
+  return g < 0 ? 0 : prefix_group(a, g).n;
 }
 // Positions that the new token of sequence t attends, when n of them are its group's: all of [0, L),
 // none where the length is 0, shorter than the prefix or past the page table's reach.

@@ -37,19 +37,14 @@
 //   positions of 128 sequences, 64 / 4 heads of 192 / 128: 36 us for 120 MB, where the start
 //   (lengths, pages, first copies) and the join count.
 #include "irs_internal.h"
+#include "irs_paged.cuh"
 #include "irs_ptx.cuh"
 
 namespace irs {
 
 namespace {
 
-constexpr int kTile = 16;              // positions a tile (two 8-column halves of the score product)
-constexpr int kHeads = 16;             // query heads a tile (rows of the products)
-constexpr int kMaxPagedCtas = 160;
-constexpr int kMaxWarps = 8;
 constexpr float kRaise = 8.f;          // raise the maximum only where a score passes it by 2^8
-
-constexpr int kMinTiles = 4;           // a warp's run has at least this many: a part is as large as two tiles
 constexpr uint32_t kRingBytes = 223u * 1024u;
 
 // How a launch lays out its warps: `groups` groups of CTAs take `heads` heads each; `per_head`
@@ -83,20 +78,24 @@ inline PagedGrid paged_grid(int Dqk, int Dv, int HK, int num_sms) {
   return g;
 }
 
-// Workspace: prefix sums of the sequences' tile counts, then two parts for every run and head
-// (the sequence it starts in, the one it ends in): rows of Dv sums, then maxima, then sums.
-__host__ __device__ inline size_t paged_prefix_bytes(int B) { return ((size_t)(B + 1) * 8 + 255) & ~size_t(255); }
-__host__ __device__ inline size_t paged_part_floats(int Dv) { return (size_t)kHeads * (Dv + 2); }
-
-__device__ __forceinline__ int tiles_of(const PagedArgs& a, int L) {
-  const PagedSet s = paged_set(a, L);
-  return (s.n + kTile - 1) / kTile;
+// The positions that sequence b's new token attends here; SHARED: those behind its group's prefix.
+template <bool SHARED>
+__device__ __forceinline__ PagedSet set_of(const PagedArgs& a, int b) {
+  const int L = __ldg(a.cache_lens + b);
+  if constexpr (SHARED) {
+    PagedSet s{};
+    const int n = prefix_positions(a.shared, b);
+    s.L = prefix_length(a.shared, b, n);
+    s.first = s.L > 0 ? n : 0;
+    s.recent = s.n = s.L - s.first;
+    return s;
+  } else {
+    return paged_set(a, L);
+  }
 }
-
-// Tiles of a run.
-__device__ __forceinline__ int64_t paged_share(int64_t total, int workers) {
-  const int64_t q = (total + workers - 1) / workers;
-  return q < kMinTiles ? kMinTiles : q;
+template <bool SHARED>
+__device__ __forceinline__ int tiles_of(const PagedArgs& a, int b) {
+  return (set_of<SHARED>(a, b).n + kTile - 1) / kTile;
 }
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
@@ -129,20 +128,24 @@ struct Cursor {
   int b, tile, nt;   // sequence, tile of it, its tile count
   PagedSet set;
 };
+template <bool SHARED>
 __device__ __forceinline__ void cursor_open(const PagedArgs& a, Cursor& c) {
-  c.set = paged_set(a, __ldg(a.cache_lens + c.b));
+  c.set = set_of<SHARED>(a, c.b);
   c.nt = (c.set.n + kTile - 1) / kTile;
 }
 // Move on to the sequence that holds c.tile; the list must go on that far.
+template <bool SHARED>
 __device__ __forceinline__ void cursor_settle(const PagedArgs& a, Cursor& c) {
   while (c.tile >= c.nt) {
     c.tile -= c.nt;
     if (++c.b >= a.B) { c.b = a.B - 1; c.tile = 0; return; }   // not reached on a list of the right length
-    cursor_open(a, c);
+    cursor_open<SHARED>(a, c);
   }
 }
 
-template <int DQK, int DV>
+// SHARED: the own positions of sequences that share prefixes. Nothing is written but FP32 sums: parts as
+// ever, and rows of a sequence that no border cuts, for the join with the prefixes' (irs_prefix_tc.cu).
+template <int DQK, int DV, bool SHARED>
 __global__ void __launch_bounds__(32 * kMaxWarps, 1) paged_decode_kernel(PagedArgs a, PagedGrid pg, int nhb) {
   constexpr int KS = DQK / 16, NV = DV / 8;
   constexpr uint32_t kStage = kTile * (DQK + DV) * 2;
@@ -166,9 +169,11 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) paged_decode_kernel(PagedAr
   {
     int64_t n = 0;
     for (int b = bs; b < be; ++b) {
-      const int L = __ldg(a.cache_lens + b);
-      if (blockIdx.x == 0 && (L < 0 || L > a.max_pages * a.page_size)) record_error(a.err, IRS_DEVERR_PAGE);
-      n += tiles_of(a, L);
+      if (blockIdx.x == 0) {
+        const int L = __ldg(a.cache_lens + b);
+        if (SHARED ? L != 0 && set_of<SHARED>(a, b).L == 0 : L < 0 || L > a.max_pages * a.page_size) record_error(a.err, IRS_DEVERR_PAGE);
+      }
+      n += tiles_of<SHARED>(a, b);
     }
     int64_t x = n;
 #pragma unroll
@@ -195,7 +200,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) paged_decode_kernel(PagedAr
     int64_t* pre = reinterpret_cast<int64_t*>(a.ws);
     int64_t n = scan[tid];
     for (int b = bs; b < be; ++b) {
-      const int64_t next = n + tiles_of(a, __ldg(a.cache_lens + b));
+      const int64_t next = n + tiles_of<SHARED>(a, b);
       if (blockIdx.x == 0) pre[b] = n;
       for (int w = 0; w < pg.per_head; ++w) {
         const int64_t f = (worker0 + w) * share;
@@ -208,13 +213,17 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) paged_decode_kernel(PagedAr
   __syncthreads();
   const int sub = warp % pg.per_head, worker = worker0 + sub;
   const int64_t f0 = worker * share, f1 = min(total, f0 + share);
-  if (f0 >= f1 || start_b[sub] < 0 || hk >= HK) return;
+  // SHARED: launched early and waited for by the join, which then may rely on the kernel before this one
+  if (f0 >= f1 || start_b[sub] < 0 || hk >= HK) {
+    if constexpr (SHARED) asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
   const int g = hk / nhb, hb = hk % nhb;
   const int h0 = g * a.G + hb * kHeads, nh = min(kHeads, a.G - hb * kHeads);
 
   Cursor cc;                                            // the tile being computed
   cc.b = start_b[sub];
-  cursor_open(a, cc);
+  cursor_open<SHARED>(a, cc);
   cc.tile = (int)(f0 - start_pre[sub]);
 
   // ---- loads: A looks up positions or routes, B pages, C issues the copies ----
@@ -230,7 +239,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) paged_decode_kernel(PagedAr
     a_pos = -1;
     a_route = false;
     if (a_live) {
-      cursor_settle(a, lc);
+      cursor_settle<SHARED>(a, lc);
       a_b = lc.b;
       int j = lc.tile * kTile + key;
       if (j < lc.set.n) {
@@ -310,7 +319,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) paged_decode_kernel(PagedAr
   int slot = 0;
   int64_t f = f0;
   while (f < f1) {
-    cursor_settle(a, cc);
+    cursor_settle<SHARED>(a, cc);
     const int tiles = (int)min(f1 - f, (int64_t)(cc.nt - cc.tile));
     const __nv_bfloat16* qrow = a.q + (int64_t)cc.b * a.q_sb;
     auto load_q = [&](uint32_t (&f)[4], int ks) {
@@ -417,9 +426,21 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) paged_decode_kernel(PagedAr
       l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
       l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
       // attended, and every score -inf: 0 / 0; in a part -1, which a finite maximum wipes out
-      if (l[i] == 0.f && seen != 0u) l[i] = tiles == cc.nt ? NAN : -1.f;
+      if (l[i] == 0.f && seen != 0u) l[i] = !SHARED && tiles == cc.nt ? NAN : -1.f;
     }
-    if (tiles == cc.nt) {
+    if (SHARED && tiles == cc.nt) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int row = g4 + 8 * i;
+        if (row < nh) {
+          const int64_t r = (int64_t)cc.b * a.Hq + h0 + row;
+#pragma unroll
+          for (int n = 0; n < NV; ++n)
+            *reinterpret_cast<float2*>(a.rows + r * DV + n * 8 + 2 * t4) = make_float2(o[n][2 * i], o[n][2 * i + 1]);
+          if (t4 == 0) *reinterpret_cast<float2*>(a.rows + (int64_t)a.B * a.Hq * DV + 2 * r) = make_float2(mx[i], l[i]);
+        }
+      }
+    } else if (tiles == cc.nt) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int row = g4 + 8 * i;
@@ -456,6 +477,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) paged_decode_kernel(PagedAr
   cp_async_wait_pending(0);
   if (bad_route) record_error(a.err, IRS_DEVERR_ROUTE_ID);
   if (bad_page) record_error(a.err, IRS_DEVERR_PAGE);
+  if constexpr (SHARED) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // Joins the parts of the (sequence, head) pairs that warp borders cut, and writes the empty
@@ -546,14 +568,14 @@ __global__ void __launch_bounds__(1024) paged_join_kernel(PagedArgs a, int nhb, 
 template <int DQK, int DV>
 cudaError_t launch_decode(const PagedArgs& a, int num_sms, bool* configured, cudaStream_t stream) {
   if (!*configured) {
-    const cudaError_t e = cudaFuncSetAttribute(paged_decode_kernel<DQK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    const cudaError_t e = cudaFuncSetAttribute(paged_decode_kernel<DQK, DV, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                (int)(kRingBytes + 256));
     if (e != cudaSuccess) return e;
     *configured = true;
   }
   const int nhb = (a.G + kHeads - 1) / kHeads;
   const PagedGrid pg = paged_grid(DQK, DV, a.Hkv * nhb, num_sms);
-  paged_decode_kernel<DQK, DV><<<pg.ctas, 32 * pg.warps, pg.smem, stream>>>(a, pg, nhb);
+  paged_decode_kernel<DQK, DV, false><<<pg.ctas, 32 * pg.warps, pg.smem, stream>>>(a, pg, nhb);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // About four parts a thread: a sequence has workers / B of them when the lengths are alike.
@@ -578,6 +600,32 @@ cudaError_t launch_decode(const PagedArgs& a, int num_sms, bool* configured, cud
   return cudaLaunchKernelEx(&cfg, paged_join_kernel<DV>, a, nhb, pg.workers);
 }
 
+// The own positions of sequences that share prefixes: the next kernel of the stream may start before
+// the kernel before this one ends, and so may this one.
+template <int DQK, int DV>
+cudaError_t launch_shared(const PagedArgs& a, int num_sms, bool* configured, int* workers, cudaStream_t stream) {
+  if (!*configured) {
+    const cudaError_t e = cudaFuncSetAttribute(paged_decode_kernel<DQK, DV, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)(kRingBytes + 256));
+    if (e != cudaSuccess) return e;
+    *configured = true;
+  }
+  const int nhb = (a.G + kHeads - 1) / kHeads;
+  const PagedGrid pg = paged_grid(DQK, DV, a.Hkv * nhb, num_sms);
+  *workers = pg.workers;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)pg.ctas);
+  cfg.blockDim = dim3((unsigned)(32 * pg.warps));
+  cfg.dynamicSmemBytes = pg.smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_decode_kernel<DQK, DV, true>, a, pg, nhb);
+}
+
 }  // namespace
 
 size_t paged_workspace_bytes(int B, int Dv) {
@@ -599,6 +647,18 @@ cudaError_t launch_paged_decode(const PagedArgs& a, int num_sms, bool* configure
     case 9: return launch_decode<256, 64>(a, num_sms, configured + i, stream);
     case 10: return launch_decode<256, 128>(a, num_sms, configured + i, stream);
     default: return launch_decode<256, 256>(a, num_sms, configured + i, stream);
+  }
+}
+
+cudaError_t launch_paged_shared(const PagedArgs& a, int num_sms, bool* configured, int* workers, cudaStream_t stream) {
+  const int i = (a.Dqk / 64 - 1) * 2 + (a.Dv / 64 - 1);
+  switch (i) {
+    case 0: return launch_shared<64, 64>(a, num_sms, configured + i, workers, stream);
+    case 1: return launch_shared<64, 128>(a, num_sms, configured + i, workers, stream);
+    case 2: return launch_shared<128, 64>(a, num_sms, configured + i, workers, stream);
+    case 3: return launch_shared<128, 128>(a, num_sms, configured + i, workers, stream);
+    case 4: return launch_shared<192, 64>(a, num_sms, configured + i, workers, stream);
+    default: return launch_shared<192, 128>(a, num_sms, configured + i, workers, stream);
   }
 }
 

@@ -1,0 +1,949 @@
+// Attention over shared prefixes on the tensor cores (tcgen05 + TMEM + TMA).
+//
+// Mathematics as in irs_prefix.cuh. A prefix has no mask: every row of a group attends every
+// position, so this is two dense products with a softmax between them.
+//
+// What bounds it. 2 (Dqk + Dv) flops a (row, position) pair, and the prefix's keys and values once
+// for every 256 rows of a KV head: the tensor cores for prompts, HBM for a few rows.
+//
+// Design.
+// * A tile is 128 rows: the G query heads of a KV head for 128 / G tokens of one group. Two tiles
+//   of neighbouring tokens are one item over the same key blocks, so that the tensor cores work on
+//   one tile while the other's softmax runs.
+// * The items of a KV head, each as many blocks long as its prefix, form one list; it is cut into
+//   runs of equal length, one a CTA, so ragged prefixes and few rows load the SMs equally. The list
+//   comes from the lengths on the device; nothing is read back. The CTAs of neighbouring numbers
+//   take the same run for different heads, whose rows lie next to one another in the pool. An item
+//   that a border cuts leaves parts (running maximum, sum, FP32 output) that a second kernel joins
+//   in list order: every run gives the same bits.
+// * Keys and values come through the page table by TMA, a chunk that lies in one page at a time;
+//   where pages are not multiples of 8 positions, and for the positions behind the last whole
+//   chunk of a prefix, by 16-byte copies with zeros behind the end: no position past it is read,
+//   and 0 times whatever its value holds is never formed.
+// * S[128 x block] = Q K^T lies in TMEM; the weights return over it as bf16 and are the first operand
+//   of O += P V straight from TMEM. Two threads share a row. The running maximum is raised only where
+//   a half row's weights under it sum past 2^8, so that a block's scores are read once and O is hardly
+//   ever rescaled; the sums are FP32.
+#include <climits>
+
+#include "irs_internal.h"
+#include "irs_paged.cuh"
+#include "irs_prefix.cuh"
+#include "irs_ptx.cuh"
+
+namespace irs {
+
+namespace {
+
+constexpr int kRows = 128;              // rows a tile
+constexpr uint32_t kAtom = 128 * 128;   // 128 rows x 64 bf16
+// warps 0-7, 8-15: softmax of the two tiles; 16: plan, queries and keys; 17, 18: products of the two tiles; 19: values
+constexpr int kThreads = 640;
+constexpr float kRaise = 256.f;         // a half row's weights of a block with a sum past this raise the maximum
+constexpr int kPlanReaders = 19;        // warps that read an item's plan
+
+template <int DQK, int DV>
+struct Cfg {
+  static constexpr int QA = DQK / 64, VA = DV / 64;
+  static constexpr int BLK = prefix_block(DQK);            // positions a block
+  static constexpr uint32_t q_bytes = QA * kAtom;          // one tile's queries
+  static constexpr uint32_t atom = BLK * 128;              // BLK rows x 64 bf16
+  static constexpr uint32_t k_bytes = QA * atom, v_bytes = VA * atom;
+  static constexpr int KS = DQK == 64 ? 4 : DQK == 128 ? 3 : 2;                    // stages of keys
+  static constexpr int VS = DQK == 64 ? (DV == 64 ? 4 : 3) : (DV == 64 ? 3 : 2);   // and values
+  static constexpr uint32_t k_off = 2 * q_bytes, v_off = k_off + KS * k_bytes;
+  // a word a row, half and tile, by which the two threads of a row exchange maxima and sums
+  static constexpr uint32_t x_off = v_off + VS * v_bytes, x_bytes = 2 * 2 * kRows * 4;
+  static constexpr uint32_t bar_off = x_off + x_bytes;
+  static constexpr uint32_t plan_off = bar_off + 40 * 8 + 16;   // [4][8] the items' plans
+  static constexpr uint32_t total = plan_off + 4 * 32;
+  static_assert(total <= 232448, "227 KB");
+  static constexpr uint32_t S0 = 0, O0 = 256;              // TMEM: scores at 128 x, outputs at 256 + x DV
+};
+
+// D[128 x DV] (+)= P . V: P bf16 in TMEM, V a [position][dim] tile read MN-major; NK steps of 16
+// positions. Each half of the positions has its weights at the first of its own score columns.
+template <int NK>
+__device__ __forceinline__ void pv_run(uint32_t d, uint32_t p, uint32_t vb, uint32_t atom, uint32_t idesc, bool accumulate) {
+  const uint64_t b0 = sdesc_sw128(vb, atom, 1024);
+#pragma unroll
+  for (int ks = 0; ks < NK; ++ks)
+    umma_bf16_ts_warp(d, p + (ks < NK / 2 ? 8 * ks : 8 * NK + 8 * (ks - NK / 2)), b0 + (uint64_t)((ks * 2048) >> 4), idesc,
+                      (accumulate || ks > 0) ? 1u : 0u);
+}
+
+// Copies blocks of a prefix's keys or values into a ring; a whole warp.
+template <int ATOMS, int BLK, int ST>
+struct Loader {
+  const CUtensorMap* map;
+  const __nv_bfloat16* base;
+  int64_t sp, stt;            // strides: page, position in page
+  const int32_t* row;         // the prefix's page table row
+  int page_size, num_pages, chunk, head;   // chunk: positions a TMA copy (0: 16-byte copies)
+  uint64_t* full;
+  uint64_t* empty;
+  uint32_t smem;              // of the first stage
+  uint8_t* smem_p;
+  volatile int* abort_flag;
+  int32_t* err;
+  int lane;
+  uint32_t st, ph, ns, pending;
+  bool bad;
+
+  static constexpr uint32_t atom = BLK * 128, bytes = ATOMS * atom;
+
+  // The page of position p, or num_pages where it is none.
+  __device__ __forceinline__ int page_of(int p, int& off) {
+    const int pg = p / page_size;
+    off = p - pg * page_size;
+    const int page = __ldg(row + pg);
+    if (page >= 0 && page < num_pages) return page;
+    bad = true;
+    return num_pages;
+  }
+  // Copied blocks that are not yet announced: all but `keep` (0 or 1) of them.
+  __device__ __forceinline__ void announce(uint32_t keep) {
+    while (pending > keep) {
+      cp_async_wait_pending(pending - 1);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(full + (st + ST - pending) % ST);
+      --pending;
+    }
+  }
+  // Rows [r0, cols) of the block at position kb, those from `valid` on as zeros.
+  __device__ __forceinline__ void copy_rows(int kb, int r0, int valid, int cols, uint32_t dst) {
+    for (int r = r0; r < cols; r += 32) {
+      int64_t at = 0;
+      bool ok = r + lane < valid;
+      if (ok) {
+        int off;
+        const int page = page_of(kb + r + lane, off);
+        ok = page < num_pages;
+        at = ok ? (int64_t)page * sp + (int64_t)off * stt : 0;
+      }
+      const uint32_t m = __ballot_sync(0xffffffffu, ok);
+      const int c8 = lane & 7;
+#pragma unroll 4
+      for (int i = 0; i < 8; ++i) {   // eight lanes a row, four rows at a time
+        const int k = 4 * i + (lane >> 3), rr = r + k;
+        const __nv_bfloat16* src = base + __shfl_sync(0xffffffffu, at, k) + c8 * 8;
+        const uint32_t n = (m >> k) & 1u ? 16u : 0u;
+        const uint32_t d = dst + (uint32_t)rr * 128u + (uint32_t)((c8 ^ (rr & 7)) << 4);
+        if (rr < cols) {
+#pragma unroll
+          for (int c = 0; c < ATOMS; ++c) cp_async_16(d + c * atom, src + 64 * c, n);
+        }
+      }
+    }
+  }
+  // The block at position kb: `valid` positions, zeros up to cols. chunk_page: of the lane's chunk.
+  __device__ __forceinline__ bool load(int kb, int valid, int cols, int chunk_page, int chunk_off) {
+    if (ns >= (uint32_t)ST) {
+      if (!__all_sync(0xffffffffu, mbar_test(&empty[st], ph ^ 1u))) {
+        announce(0);
+        if (!__all_sync(0xffffffffu, mbar_wait(&empty[st], ph ^ 1u, abort_flag, err))) return false;
+      }
+    }
+    const uint32_t dst = smem + st * bytes;
+    if (chunk > 0) {
+      const int whole = valid / chunk;
+      if (whole > 0) {
+        if (lane == 0) mbar_expect_tx(&full[st], (uint32_t)(whole * chunk) * 128u * ATOMS);
+        __syncwarp();
+        if (lane < whole) {
+          uint8_t* d = smem_p + st * bytes + (uint32_t)(lane * chunk) * 128u;
+#pragma unroll
+          for (int c = 0; c < ATOMS; ++c) tma_load_4d(d + c * atom, map, c * 64, chunk_off, head, chunk_page, &full[st]);
+        }
+      }
+      if (whole * chunk < cols) {
+        copy_rows(kb, whole * chunk, valid, cols, dst);
+        cp_async_commit();
+        cp_async_wait_pending(0);
+        fence_proxy_async_smem();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&full[st]);
+      advance();
+    } else {
+      copy_rows(kb, 0, valid, cols, dst);
+      cp_async_commit();
+      ++pending;
+      advance();
+      announce(1);
+    }
+    return true;
+  }
+  __device__ __forceinline__ void advance() {
+    ++ns;
+    if (++st == (uint32_t)ST) { st = 0; ph ^= 1u; }
+  }
+  // The blocks [b0, b0 + nb) of a prefix of n positions.
+  __device__ __forceinline__ bool run(const int32_t* table_row, int b0, int nb, int n) {
+    row = table_row;
+    int page = 0, off = 0;
+    auto look = [&](int b) {   // the lane's chunk of block b, a block ahead of its copy
+      const int p = b * BLK + lane * chunk;
+      if (chunk > 0 && lane * chunk < BLK && p + chunk <= n) page = page_of(p, off);
+    };
+    look(b0);
+    for (int b = b0; b < b0 + nb; ++b) {
+      const int valid = min(BLK, n - b * BLK), p = page, o = off;
+      if (b + 1 < b0 + nb) look(b + 1);
+      if (!load(b * BLK, valid, (valid + 31) & ~31, p, o)) return false;
+    }
+    announce(0);
+    return true;
+  }
+  // Copies that are still in flight land before the CTA leaves.
+  __device__ __forceinline__ void drain() {
+    cp_async_wait_pending(0);
+    if (*abort_flag) {
+      for (uint32_t i = ns > (uint32_t)ST ? ns - ST : 0; i < ns; ++i) {
+        const unsigned long long w0 = globaltimer_ns();
+        while (!mbar_try_wait(&full[i % ST], (i / ST) & 1) && globaltimer_ns() - w0 < kWaitLimitNs) {}
+      }
+    }
+    if (bad) record_error(err, IRS_DEVERR_PAGE);
+  }
+};
+
+template <int DQK, int DV>
+__global__ void __launch_bounds__(kThreads, 1)
+    prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                  const __grid_constant__ CUtensorMap tm_v, PrefixArgs a, int runs, int chunk, int q_map) {
+  using C = Cfg<DQK, DV>;
+  constexpr int KS = C::KS, VS = C::VS, BLK = C::BLK;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if ((smem_u32(smem) & 1023u) != 0) {   // the attribute asks for it; the tiles need it
+    record_error(a.err, IRS_DEVERR_TIMEOUT);
+    return;
+  }
+  uint64_t* plan_full = reinterpret_cast<uint64_t*>(smem + C::bar_off);   // [4]
+  uint64_t* plan_empty = plan_full + 4;   // [4]
+  uint64_t* q_full = plan_empty + 4;      // [2]
+  uint64_t* q_empty = q_full + 2;         // [2]
+  uint64_t* k_full = q_empty + 2;         // [KS]
+  uint64_t* k_empty = k_full + 4;
+  uint64_t* v_full = k_empty + 4;         // [VS]
+  uint64_t* v_empty = v_full + 4;
+  uint64_t* s_full = v_empty + 4;         // [2] a tile's scores; all its earlier products are done too
+  uint64_t* p_full = s_full + 2;          // [2] its weights
+  uint64_t* o_full = p_full + 2;          // [2] its output
+  uint64_t* o_empty = o_full + 2;         // [2]
+  uint64_t* drain = o_empty + 2;          // [2]
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + C::bar_off + 40 * 8);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
+  volatile int* start_g = reinterpret_cast<volatile int*>(tslot + 2);   // group that this CTA's run starts in
+  volatile int* plan = reinterpret_cast<volatile int*>(smem + C::plan_off);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int head = (int)(blockIdx.x % (unsigned)a.Hkv), run = (int)(blockIdx.x / (unsigned)a.Hkv);
+  const int qt = kRows / a.G;
+  if (tid == 0) {
+    for (int i = 0; i < 4; ++i) { mbar_init(&plan_full[i], 1); mbar_init(&plan_empty[i], kPlanReaders); }
+    for (int i = 0; i < KS; ++i) { mbar_init(&k_full[i], 1); mbar_init(&k_empty[i], 2); }
+    for (int i = 0; i < VS; ++i) { mbar_init(&v_full[i], 1); mbar_init(&v_empty[i], 2); }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], 1); mbar_init(&q_empty[i], 1);
+      mbar_init(&s_full[i], 1); mbar_init(&p_full[i], 8);
+      mbar_init(&o_full[i], 1); mbar_init(&o_empty[i], 8);
+      mbar_init(&drain[i], 1);
+    }
+    *abort_flag = 0;
+    *start_g = -1;
+    fence_mbar_init();
+  }
+  if (warp == 17) {
+    tmem_alloc(tslot, 512);
+    tmem_relinquish();
+  }
+  // ---- the list of a head's blocks: its length, and where this CTA's run starts ----
+  int64_t* sums = reinterpret_cast<int64_t*>(smem);   // [kThreads / 32] + total + start, before the tiles are loaded
+  const int per = (a.P + kThreads - 1) / kThreads;
+  const int gs = min(a.P, tid * per), ge = min(a.P, gs + per);
+  int64_t mine = 0;
+  for (int g = gs; g < ge; ++g) mine += prefix_units(prefix_group(a, g), qt, BLK);
+  int64_t before = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before += y;
+  }
+  if (lane == 31) sums[warp] = before;
+  __syncthreads();
+  before -= mine;
+  int64_t total = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += sums[w];
+    total += sums[w];
+  }
+  const int64_t share = prefix_share(total, runs);
+  const int64_t f0 = run * share, f1 = min(total, f0 + share);
+  {
+    int64_t* pre = reinterpret_cast<int64_t*>(a.ws);
+    int64_t n = before;
+    for (int g = gs; g < ge; ++g) {
+      const int64_t next = n + prefix_units(prefix_group(a, g), qt, BLK);
+      if (blockIdx.x == 0) pre[g] = n;
+      if (f0 >= n && f0 < next) {
+        *start_g = g;
+        sums[kThreads / 32] = n;
+      }
+      n = next;
+    }
+    if (blockIdx.x == 0 && tid == 0) pre[a.P] = total;
+  }
+  if (blockIdx.x == 0) prefix_check(a);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = *tslot;
+  const int64_t start_pre = sums[kThreads / 32];
+  fence_proxy_async_smem();
+  __syncthreads();                        // the words are read before the first tile is loaded over them
+  const bool any = f0 < f1 && *start_g >= 0;
+
+  auto wait_all = [&](uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, a.err));
+  };
+  // An item as its readers take it from its plan.
+  struct Item {
+    int nb, t0, t1, part, b0, n, row;   // part: 0 the whole item, 1 or 2 the run's first or second part
+  };
+  uint32_t items = 0;                     // read so far
+  auto next_item = [&](Item& m) {
+    if (!wait_all(&plan_full[items & 3], (items >> 2) & 1)) return false;
+    const volatile int* pl = plan + 8 * (items & 3);
+    m.nb = pl[0];
+    m.t0 = pl[1];
+    m.t1 = pl[2];
+    m.part = pl[3];
+    m.b0 = pl[4];
+    m.n = pl[5];
+    m.row = pl[6];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&plan_empty[items & 3]);
+    ++items;
+    return m.nb > 0;
+  };
+
+  if (warp == 16) {
+    // ---------------- plan, queries and keys ----------------
+    Loader<C::QA, BLK, KS> ld{};
+    ld.map = &tm_k; ld.base = a.k + (int64_t)head * a.k_sh; ld.sp = a.k_sp; ld.stt = a.k_st;
+    ld.page_size = a.page_size; ld.num_pages = a.num_pages; ld.chunk = chunk; ld.head = head;
+    ld.full = k_full; ld.empty = k_empty; ld.smem_p = smem + C::k_off; ld.smem = smem_u32(smem) + C::k_off;
+    ld.abort_flag = abort_flag; ld.err = a.err; ld.lane = lane;
+    if (lane == 0) {
+      tma_prefetch_map(&tm_q);
+      tma_prefetch_map(&tm_k);
+      tma_prefetch_map(&tm_v);
+    }
+    uint32_t np = 0, nq[2] = {0, 0};
+    bool ok = true;
+    auto publish = [&](const Item& m) {
+      if (np >= 4 && !wait_all(&plan_empty[np & 3], ((np >> 2) - 1) & 1)) return false;
+      if (lane == 0) {
+        volatile int* pl = plan + 8 * (np & 3);
+        pl[0] = m.nb;
+        pl[1] = m.t0;
+        pl[2] = m.t1;
+        pl[3] = m.part;
+        pl[4] = m.b0;
+        pl[5] = m.n;
+        pl[6] = m.row;
+        mbar_arrive(&plan_full[np & 3]);
+      }
+      __syncwarp();
+      ++np;
+      return true;
+    };
+    auto load_q = [&](int x, const Item& m) {
+      if (nq[x] > 0 && !wait_all(&q_empty[x], (nq[x] - 1) & 1)) return false;
+      ++nq[x];
+      const int t = m.t0 + x * qt;
+      if (q_map) {
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&q_full[x], (uint32_t)(qt * a.G) * 128u * C::QA);
+          for (int c = 0; c < C::QA; ++c)
+            tma_load_3d(smem + x * C::q_bytes + c * kAtom, &tm_q, c * 64, head * a.G, t, &q_full[x]);
+        }
+      } else {
+        // rows by address: strides that no map can have
+        ld.announce(0);
+        const uint32_t dst = smem_u32(smem) + x * C::q_bytes;
+        const int c8 = lane & 7;
+        for (int r = lane >> 3; r < kRows; r += 4) {
+          const int tq = t + r / a.G;
+          const bool live = r < qt * a.G && tq < a.T;
+          const __nv_bfloat16* src = a.q + (live ? (int64_t)tq * a.q_st + (int64_t)(head * a.G + r % a.G) * a.q_sh : 0) + c8 * 8;
+          const uint32_t d = dst + (uint32_t)r * 128u + (uint32_t)((c8 ^ (r & 7)) << 4);
+#pragma unroll
+          for (int c = 0; c < C::QA; ++c) cp_async_16(d + c * kAtom, src + 64 * c, live ? 16u : 0u);
+        }
+        cp_async_commit();
+        cp_async_wait_pending(0);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_full[x]);
+      }
+      __syncwarp();
+      return true;
+    };
+    int g = any ? *start_g : 0;
+    int64_t pre = start_pre, f = f0;
+    while (any && ok && f < f1) {
+      const PrefixGroup grp = prefix_group(a, g);
+      const int64_t units = prefix_units(grp, qt, BLK);
+      if (f >= pre + units) {               // the next group that has any
+        pre += units;
+        if (++g >= a.P) break;              // not reached on a list of the right length
+        continue;
+      }
+      const int nbg = (grp.n + BLK - 1) / BLK;
+      const int pair = (int)((f - pre) / nbg);
+      Item m;
+      m.b0 = (int)((f - pre) - (int64_t)pair * nbg);
+      m.nb = (int)min(f1 - f, (int64_t)(nbg - m.b0));
+      m.t0 = grp.first + pair * 2 * qt;
+      m.t1 = grp.last;
+      m.part = m.nb == nbg ? 0 : f == f0 ? 1 : 2;
+      m.n = grp.n;
+      m.row = a.cache_lens != nullptr ? grp.first : g;
+      ok = publish(m) && load_q(0, m) && (m.t0 + qt >= m.t1 || load_q(1, m)) &&
+           ld.run(a.page_table + (int64_t)m.row * a.table_stride, m.b0, m.nb, m.n);
+      f += m.nb;
+    }
+    if (ok) {
+      Item end{};
+      publish(end);
+    }
+    ld.drain();
+    if (*abort_flag && q_map) {
+      for (int x = 0; x < 2; ++x)
+        if (nq[x] > 0) {
+          const unsigned long long w0 = globaltimer_ns();
+          while (!mbar_try_wait(&q_full[x], (nq[x] - 1) & 1) && globaltimer_ns() - w0 < kWaitLimitNs) {}
+        }
+    }
+  } else if (warp == 19) {
+    // ---------------- values ----------------
+    Loader<C::VA, BLK, VS> ld{};
+    ld.map = &tm_v; ld.base = a.v + (int64_t)head * a.v_sh; ld.sp = a.v_sp; ld.stt = a.v_st;
+    ld.page_size = a.page_size; ld.num_pages = a.num_pages; ld.chunk = chunk; ld.head = head;
+    ld.full = v_full; ld.empty = v_empty; ld.smem_p = smem + C::v_off; ld.smem = smem_u32(smem) + C::v_off;
+    ld.abort_flag = abort_flag; ld.err = a.err; ld.lane = lane;
+    Item m;
+    while (next_item(m))
+      if (!ld.run(a.page_table + (int64_t)m.row * a.table_stride, m.b0, m.nb, m.n)) break;
+    ld.drain();
+  } else if (warp >= 17) {
+    // ---------------- the products of a tile (the whole warp; one elected lane issues) ----------------
+    constexpr uint32_t PV_IDESC = idesc_bf16(kRows, DV, false, true);
+    const int x = uniform(warp - 17);
+    const uint32_t tb = (uint32_t)uniform((int)tbase), sb = smem_u32(smem);
+    const uint32_t s_tm = tb + C::S0 + 128 * x, o_tm = tb + C::O0 + x * DV;
+    const uint64_t a0 = sdesc_sw128(sb + x * C::q_bytes, 16, 1024);
+    uint32_t nq = 0, no = 0, np = 0, ks = 0, kph = 0, vs = 0, vph = 0;
+    bool alive = true;
+    Item m;
+    while (alive && next_item(m)) {
+      const int nb = uniform(m.nb), b0 = uniform(m.b0), n = uniform(m.n);
+      if (x == 1 && m.t0 + qt >= m.t1) {       // an item of one tile: its blocks pass by
+        for (int j = 0; j < nb && alive; ++j) {
+          alive = wait_all(&k_full[ks], kph) && wait_all(&v_full[vs], vph);
+          if (lane == 0) { mbar_arrive(&k_empty[ks]); mbar_arrive(&v_empty[vs]); }
+          __syncwarp();
+          if (++ks == (uint32_t)KS) { ks = 0; kph ^= 1u; }
+          if (++vs == (uint32_t)VS) { vs = 0; vph ^= 1u; }
+        }
+        continue;
+      }
+      if (!wait_all(&q_full[x], nq & 1)) break;
+      ++nq;
+      int cols = 0;
+      for (int j = 0; j <= nb; ++j) {
+        if (j > 0) {
+          // O += P V of the block before
+          if (!wait_all(&v_full[vs], vph) || !wait_all(&p_full[x], np & 1)) { alive = false; break; }
+          if (j == 1 && no > 0 && !wait_all(&o_empty[x], (no - 1) & 1)) { alive = false; break; }
+          ++np;
+          tc_fence_after();
+          const uint32_t vb = sb + C::v_off + vs * C::v_bytes;
+          switch (cols >> 5) {
+            case 1: pv_run<2>(o_tm, s_tm, vb, C::atom, PV_IDESC, j > 1); break;
+            case 2: pv_run<4>(o_tm, s_tm, vb, C::atom, PV_IDESC, j > 1); break;
+            case 3: pv_run<6>(o_tm, s_tm, vb, C::atom, PV_IDESC, j > 1); break;
+            default: pv_run<BLK / 16>(o_tm, s_tm, vb, C::atom, PV_IDESC, j > 1); break;
+          }
+          if (j == nb) { umma_commit_warp(&o_full[x]); ++no; }
+          umma_commit_warp(&v_empty[vs]);
+          if (++vs == (uint32_t)VS) { vs = 0; vph ^= 1u; }
+        }
+        if (j < nb) {
+          if (!wait_all(&k_full[ks], kph)) { alive = false; break; }
+          tc_fence_after();
+          cols = min(BLK, (n - (b0 + j) * BLK + 31) & ~31);
+          const uint32_t idesc = idesc_bf16(kRows, cols, false, false);
+          const uint64_t b = sdesc_sw128(sb + C::k_off + ks * C::k_bytes, 16, 1024);
+#pragma unroll
+          for (int i = 0; i < 4 * C::QA; ++i)
+            umma_bf16_warp(s_tm, a0 + (uint64_t)(((i >> 2) * kAtom + (i & 3) * 32) >> 4),
+                           b + (uint64_t)(((i >> 2) * C::atom + (i & 3) * 32) >> 4), idesc, i > 0);
+          umma_commit_warp(&s_full[x]);
+          umma_commit_warp(&k_empty[ks]);
+          if (j == nb - 1) umma_commit_warp(&q_empty[x]);
+          if (++ks == (uint32_t)KS) { ks = 0; kph ^= 1u; }
+        }
+      }
+    }
+    // every issued product completes before the CTA releases its tensor memory
+    umma_commit_warp(&drain[x]);
+    const unsigned long long w0 = globaltimer_ns();
+    while (!mbar_try_wait(&drain[x], 0) && globaltimer_ns() - w0 < kWaitLimitNs) {}
+    __syncwarp();
+  } else {
+    // ---------------- softmax: warps 0-7 the first tile, 8-15 the second ----------------
+    const int x = warp >> 3, half = (warp >> 2) & 1;
+    const int bar_id = 1 + x * 4 + (warp & 3);            // the two warps of these rows
+    const int r = (warp & 3) * 32 + lane;                 // row of the tile = TMEM lane
+    const int rq = r / a.G;                               // its token
+    const int rel = rq * a.Hq + head * a.G + r - rq * a.G;   // its row of out, relative to the tile's first token's
+    const uint32_t s_addr = tbase + C::S0 + 128 * x + tmem_lane_base(warp);
+    const uint32_t o_addr = tbase + C::O0 + x * DV + tmem_lane_base(warp);
+    const uint32_t mine_w = smem_u32(smem) + C::x_off + (uint32_t)((x * 2 + half) * kRows + r) * 4u;
+    const uint32_t other_w = smem_u32(smem) + C::x_off + (uint32_t)((x * 2 + (half ^ 1)) * kRows + r) * 4u;
+    uint32_t ns = 0, no = 0;
+    bool alive = true;
+    Item m;
+    while (alive && next_item(m)) {
+      const int t0 = m.t0 + x * qt, t = t0 + rq;
+      if (t0 >= m.t1) continue;
+      const bool live = rq < qt && t < m.t1;
+      float mx = -INFINITY, l = 0.f;
+      bool settled = false;                               // every row of the warps has a maximum
+      for (int j = 0; j < m.nb && alive; ++j) {
+        const int left = m.n - (m.b0 + j) * BLK;          // positions from the block's first on
+        const int cols = min(BLK, (left + 31) & ~31), pieces = cols >> 5, c0 = half * (cols >> 1);
+        const bool border = left < cols;
+        alive = wait_all(&s_full[x], ns & 1);
+        ++ns;
+        tc_fence_after();
+        // One pass: the weights under the present maximum, and whether their sum passes 2^8. They
+        // wait in registers for the two halves' vote; where it asks for it (and for the first
+        // block, before every row has a maximum) the scores are read again.
+        constexpr int NP = BLK / 32;
+        uint32_t w[NP][8];
+        float ln = 0.f;
+        auto scores = [&](int c, float (&v)[16]) {
+          tmem_ld16(s_addr + c0 + 16 * c, v);
+          tmem_ld_wait_regs(v);
+          if (border) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = c0 + 16 * c + i < left ? v[i] : -INFINITY;
+          }
+        };
+        auto weights = [&]() {
+          const float off = mx == -INFINITY ? 0.f : -mx;
+          const uint64_t sc2 = pack2(a.scale_log2, a.scale_log2), off2 = pack2(off, off);
+          uint64_t sum0 = 0ull, sum1 = 0ull;   // FP32 pairs
+#pragma unroll
+          for (int c = 0; c < NP; ++c) {
+            if (c < pieces) {
+              float v[16];
+              scores(c, v);
+#pragma unroll
+              for (int i = 0; i < 16; i += 4) {
+                const float2 x0 = unpack2(ffma2(pack2(v[i], v[i + 1]), sc2, off2));
+                const float2 x1 = unpack2(ffma2(pack2(v[i + 2], v[i + 3]), sc2, off2));
+                const float p0 = ex2_approx(x0.x), p1 = ex2_approx(x0.y), p2 = ex2_approx(x1.x), p3 = ex2_approx(x1.y);
+                sum0 = fadd2(sum0, pack2(p0, p1));
+                sum1 = fadd2(sum1, pack2(p2, p3));
+                const __nv_bfloat162 y0 = __floats2bfloat162_rn(p0, p1), y1 = __floats2bfloat162_rn(p2, p3);
+                w[c][i >> 1] = *reinterpret_cast<const uint32_t*>(&y0);
+                w[c][(i >> 1) + 1] = *reinterpret_cast<const uint32_t*>(&y1);
+              }
+            }
+          }
+          const float2 s2 = unpack2(fadd2(sum0, sum1));
+          ln = s2.x + s2.y;
+        };
+        bool slow = !settled;
+        if (!slow) {
+          weights();
+          // a row that is none has no vote; NaN compares false and goes on
+          slow = named_bar_or(bar_id, 64, (live && ln > kRaise) || !alive);
+        }
+        if (slow) {
+          float top = -INFINITY;
+          for (int c = 0; c < pieces; ++c) {
+            float v[16];
+            scores(c, v);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) top = fmaxf(top, v[i]);
+          }
+          top *= a.scale_log2;
+          st_shared(mine_w, top);
+          alive = named_bar_and(bar_id, 64, alive);   // both halves leave together after a wait that gave up
+          const float nm = fmaxf(mx, fmaxf(top, ld_shared(other_w)));
+          const float c = nm == -INFINITY ? 1.f : ex2_approx(mx - nm);
+          mx = nm;
+          l *= c;
+          // O has every earlier product: these scores were issued behind them
+          if (j > 0 && alive) {
+#pragma unroll 1
+            for (int d = half * (DV / 2); d < (half + 1) * (DV / 2); d += 16) {
+              float o[16];
+              tmem_ld16(o_addr + d, o);
+              tmem_ld_wait_regs(o);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] *= c;
+              tmem_st16(o_addr + d, o);
+            }
+          }
+          weights();
+          settled = named_bar_and(bar_id, 64, !live || mx > -INFINITY);   // and both have read the words
+        }
+        l += ln;
+#pragma unroll
+        for (int c = 0; c < NP; ++c)
+          if (c < pieces) tmem_st8(s_addr + c0 + 8 * c, reinterpret_cast<const float(&)[8]>(w[c]));
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[x]);
+      }
+      // ---- the tile's rows, half the dims a thread ----
+      if (alive) alive = wait_all(&o_full[x], no & 1);
+      ++no;
+      tc_fence_after();
+      st_shared(mine_w, l);
+      alive = named_bar_and(bar_id, 64, alive);
+      if (!alive) break;
+      l += ld_shared(other_w);
+      named_bar_sync(bar_id, 64);                         // both have read the words
+      if (l == 0.f) l = -1.f;                             // attended, and every score -inf: in a part, a finite maximum wipes it out
+      const int64_t row = (int64_t)t0 * a.Hq + rel;
+      if (m.part != 0 || a.cache_lens != nullptr) {
+        // a part, or the prefix's share of a decoding row: FP32, joined by the next kernel
+        float* dst;
+        float* ml;
+        if (m.part != 0) {
+          float* part = prefix_part(a, run, head, m.part - 1);
+          dst = part + (size_t)(x * kRows + r) * DV;
+          ml = part + 2 * kRows * DV + 2 * (x * kRows + r);
+        } else {
+          dst = prefix_rows(a) + row * DV;
+          ml = prefix_rows(a) + (size_t)a.T * a.Hq * DV + 2 * row;
+        }
+#pragma unroll 1
+        for (int d = half * (DV / 2); d < (half + 1) * (DV / 2); d += 16) {
+          float o[16];
+          tmem_ld16(o_addr + d, o);
+          tmem_ld_wait_regs(o);
+          if (live) {
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) *reinterpret_cast<float4*>(dst + d + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+          }
+        }
+        if (live && half == 0) *reinterpret_cast<float2*>(ml) = make_float2(mx, l);
+      } else {
+        const PrefixJoin jn = live ? prefix_join_own(a, row, mx, l) : PrefixJoin{0.f, 0.f, 0.f};
+        named_bar_sync(bar_id, 64);                       // lse may be own_lse: both have read it
+#pragma unroll 1
+        for (int d = half * (DV / 2); d < (half + 1) * (DV / 2); d += 16) {
+          float o[16];
+          tmem_ld16(o_addr + d, o);
+          tmem_ld_wait_regs(o);
+          if (live) {
+#pragma unroll
+            for (int i = 0; i < 16; i += 8) prefix_store8(a, row * DV + d + i, jn, o + i);
+          }
+        }
+        if (half == 0 && live && a.lse != nullptr) a.lse[row] = jn.lse;
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&o_empty[x]);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 17) {
+    tc_fence_after();
+    tmem_dealloc(tbase, 512);
+  }
+}
+
+// Prompts: joins the parts of the items that runs' borders cut, with the rows' other parts too, and
+// writes the rows of empty prefixes. A block takes 32 rows of the item that holds border blockIdx.x of
+// a head's list, if that is the item's first; eight columns a thread.
+constexpr int kJoinThreads = 256;
+template <int DV>
+__global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(PrefixArgs a, int runs) {
+  constexpr int CL = DV / 8, R = kJoinThreads / CL;   // threads a row, rows at a time
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int head = blockIdx.y, qt = kRows / a.G;
+  const int cl = threadIdx.x % CL, lane = threadIdx.x & 31;
+  const uint32_t row_mask = (CL == 16 ? 0xffffu : 0xffu) << (lane / CL * CL);
+  auto store = [&](int64_t row, float m, float l, const float* o) {
+    const PrefixJoin jn = prefix_join_own(a, row, m, l);
+    __syncwarp(row_mask);                             // lse may be own_lse: the row's threads have read it
+    if (cl == 0 && a.lse != nullptr) a.lse[row] = jn.lse;
+    prefix_store8(a, row * DV + 8 * cl, jn, o);
+  };
+  const int64_t* pre = reinterpret_cast<const int64_t*>(a.ws);
+  const int64_t total = pre[a.P], share = prefix_share(total, runs);
+  const int64_t f = (int64_t)(blockIdx.x + 1) * share;
+  if (f < total) {
+    const int g = prefix_find(pre, a.P, f);
+    const PrefixGroup grp = prefix_group(a, g);
+    const int nbg = prefix_blocks(a, grp.n);
+    const int pair = (int)((f - pre[g]) / nbg);
+    const int64_t s = pre[g] + (int64_t)pair * nbg;
+    if (s != f && s >= f - share) {                   // cut, and by no earlier border
+      const int c0 = (int)blockIdx.x, c1 = (int)((s + nbg - 1) / share);
+      for (int r = blockIdx.z * 32 + threadIdx.x / CL; r < (int)blockIdx.z * 32 + 32; r += R) {
+        const int x = r / kRows, rr = r % kRows, rq = rr / a.G;
+        const int t = grp.first + pair * 2 * qt + x * qt + rq;
+        if (rq >= qt || t >= grp.last) continue;
+        PrefixSum<8> sum;
+        sum.clear();
+        for (int c = c0; c <= c1; ++c) {
+          // the item's first part is its run's second, unless the run starts with it
+          const float* part = prefix_part(a, c, head, c == c0 && s != (int64_t)c0 * share ? 1 : 0);
+          const float2 ml = *reinterpret_cast<const float2*>(part + kPrefixRows * DV + 2 * r);
+          float o[8];
+          prefix_load8(o, part + (size_t)r * DV + 8 * cl);
+          sum.add(ml.x, ml.y, o);
+        }
+        store((int64_t)t * a.Hq + head * a.G + rr - rq * a.G, sum.m, sum.l, sum.o);
+      }
+    }
+  }
+  bool none = false;
+  for (int g = threadIdx.x; g < a.P; g += kJoinThreads) none |= prefix_group(a, g).n == 0;
+  if (!__syncthreads_or(none)) return;
+  const float zero[8] = {};
+  const int64_t blocks = (int64_t)gridDim.x * gridDim.z, me = (int64_t)blockIdx.x * gridDim.z + blockIdx.z;
+  for (int g = 0; g < a.P; ++g) {
+    const PrefixGroup grp = prefix_group(a, g);
+    if (grp.n != 0) continue;
+    const int64_t rows = (int64_t)(grp.last - grp.first) * a.G;
+    for (int64_t r = me * R + threadIdx.x / CL; r < rows; r += blocks * R)
+      store((grp.first + r / a.G) * a.Hq + head * a.G + r % a.G, -INFINITY, 0.f, zero);
+  }
+}
+
+// Decoding: a row's parts over its group's prefix, then those over its own positions, joined in the
+// order of the two lists. A block takes the rows of one (sequence, KV head), eight columns a thread;
+// `pg` groups of threads share a row, each taking every pg-th part, and are then joined in order.
+constexpr int kStepThreads = 512;
+template <int DV>
+__global__ void __launch_bounds__(kStepThreads) prefix_step_join_kernel(PrefixArgs a, const uint8_t* own_ws, const float* own_rows, int runs, int workers) {
+  constexpr int CL = DV / 8, groups = kStepThreads / CL;
+  __shared__ float sm[kStepThreads][9];
+  __shared__ float2 sm_ml[groups];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int t = blockIdx.x / a.Hkv, head = blockIdx.x % a.Hkv;
+  const int cl = threadIdx.x % CL, grp = threadIdx.x / CL;
+  const int g = prefix_group_of(a, t);
+  PrefixGroup gr{0, 0, 0};
+  if (g >= 0) gr = prefix_group(a, g);
+  const bool live = prefix_length(a, t, gr.n) > 0;
+  // ---- the prefix's parts: runs c0 .. c1 of the head's list, or one row ----
+  const int qt = kRows / a.G;
+  int c0 = 0, np = 0, first_slot = 0, x = 0, rq = 0;
+  if (live && gr.n > 0) {
+    const int64_t* pre = reinterpret_cast<const int64_t*>(a.ws);
+    const int64_t share = prefix_share(pre[a.P], runs);
+    const int nbg = prefix_blocks(a, gr.n), pair = (t - gr.first) / (2 * qt);
+    const int64_t s = pre[g] + (int64_t)pair * nbg;
+    c0 = (int)(s / share);
+    np = (int)((s + nbg - 1) / share) - c0 + 1;
+    first_slot = s != (int64_t)c0 * share ? 1 : 0;
+    x = (t - gr.first) / qt % 2;
+    rq = (t - gr.first) % qt;
+  }
+  // ---- the own positions' parts: by blocks of 16 query heads ----
+  const int nhb = (a.G + kHeads - 1) / kHeads, HK = a.Hkv * nhb;
+  int d0 = 0, no = 0, own_slot = 0;
+  if (live) {
+    const int64_t* pre = reinterpret_cast<const int64_t*>(own_ws);
+    const int64_t F0 = pre[t], F1 = pre[t + 1];
+    if (F1 > F0) {
+      const int64_t share = paged_share(pre[a.T], workers);
+      d0 = (int)(F0 / share);
+      no = (int)((F1 - 1) / share) - d0 + 1;
+      own_slot = F0 != (int64_t)d0 * share ? 1 : 0;
+    }
+  }
+  const float* own_parts = reinterpret_cast<const float*>(own_ws + paged_prefix_bytes(a.T));
+  const int parts = np + no;
+  int pg = 1;
+  while (2 * pg <= groups && 4 * pg < parts) pg *= 2;
+  const int part_grp = grp % pg, row_grp = grp / pg, rows = groups / pg;
+  for (int rb = blockIdx.y * rows; rb < a.G; rb += gridDim.y * rows) {
+    const int h = rb + row_grp;                         // head of the KV head's
+    const int64_t row = (int64_t)t * a.Hq + head * a.G + h;
+    PrefixSum<8> sum;
+    sum.clear();
+    if (h < a.G) {
+      const int r = x * kRows + rq * a.G + h;
+      constexpr int U = 4;
+      for (int p = part_grp; p < parts; p += U * pg) {
+        float2 ml[U];
+        float o[U][8];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int i = p + u * pg;
+          ml[u] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) o[u][k] = 0.f;
+          if (i < parts) {
+            if (i < np) {
+              const float* part = np == 1 ? prefix_rows(a) + row * DV
+                                          : prefix_part(a, c0 + i, head, i == 0 ? first_slot : 0) + (size_t)r * DV;
+              ml[u] = *reinterpret_cast<const float2*>(np == 1 ? prefix_rows(a) + (size_t)a.T * a.Hq * DV + 2 * row
+                                                               : part + (size_t)(kPrefixRows - r) * DV + 2 * r);
+              prefix_load8(o[u], part + 8 * cl);
+            } else if (no == 1) {
+              ml[u] = *reinterpret_cast<const float2*>(own_rows + (size_t)a.T * a.Hq * DV + 2 * row);
+              prefix_load8(o[u], own_rows + row * DV + 8 * cl);
+            } else {
+              const int j = i - np, hk = head * nhb + h / kHeads, hr = h % kHeads;
+              const float* part = own_parts + (((size_t)(d0 + j) * HK + hk) * 2 + (j == 0 ? own_slot : 0)) * paged_part_floats(DV);
+              ml[u] = make_float2(part[kHeads * DV + hr], part[kHeads * DV + kHeads + hr]);
+              prefix_load8(o[u], part + hr * DV + 8 * cl);
+            }
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) sum.add(ml[u].x, ml[u].y, o[u]);
+      }
+    }
+    if (pg > 1) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) sm[threadIdx.x][k] = sum.o[k];
+      if (cl == 0) sm_ml[grp] = make_float2(sum.m, sum.l);
+      __syncthreads();
+      if (part_grp == 0)
+        for (int i = 1; i < pg; ++i) {
+          float o[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) o[k] = sm[threadIdx.x + i * CL][k];
+          sum.add(sm_ml[grp + i].x, sm_ml[grp + i].y, o);
+        }
+      __syncthreads();
+    }
+    if (part_grp == 0 && h < a.G) {
+      const PrefixJoin jn = prefix_join_own(a, row, sum.m, sum.l);
+      if (cl == 0 && a.lse != nullptr) a.lse[row] = jn.lse;
+      prefix_store8(a, row * DV + 8 * cl, jn, sum.o);
+    }
+  }
+}
+
+template <int DQK, int DV>
+cudaError_t launch_prefix(const PrefixMaps& m, const PrefixArgs& a, int runs, bool* configured, cudaStream_t stream) {
+  using C = Cfg<DQK, DV>;
+  if (!*configured) {
+    const cudaError_t e = cudaFuncSetAttribute(prefix_kernel<DQK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::total);
+    if (e != cudaSuccess) return e;
+    *configured = true;
+  }
+  prefix_kernel<DQK, DV><<<runs * a.Hkv, kThreads, C::total, stream>>>(m.q, m.k, m.v, a, runs, m.chunk, m.has_q ? 1 : 0);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_prefix_any(const PrefixMaps& m, const PrefixArgs& a, int runs, bool* configured, cudaStream_t stream) {
+  const int i = (a.Dqk / 64 - 1) * 2 + (a.Dv / 64 - 1);
+  switch (i) {
+    case 0: return launch_prefix<64, 64>(m, a, runs, configured + i, stream);
+    case 1: return launch_prefix<64, 128>(m, a, runs, configured + i, stream);
+    case 2: return launch_prefix<128, 64>(m, a, runs, configured + i, stream);
+    case 3: return launch_prefix<128, 128>(m, a, runs, configured + i, stream);
+    case 4: return launch_prefix<192, 64>(m, a, runs, configured + i, stream);
+    default: return launch_prefix<192, 128>(m, a, runs, configured + i, stream);
+  }
+}
+
+// A launch that may start before the kernel before it in the stream ends.
+cudaLaunchConfig_t early(dim3 grid, int threads, cudaStream_t stream, cudaLaunchAttribute* at) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.stream = stream;
+  at->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at->val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cfg;
+}
+
+// Runs of a head's list: a CTA each, as many as there are SMs for all heads.
+int prefix_runs(int Hkv, int num_sms) {
+  const int ctas = num_sms < kMaxPrefixCtas ? num_sms : kMaxPrefixCtas;
+  return ctas / Hkv > 1 ? ctas / Hkv : 1;
+}
+
+}  // namespace
+
+int prefix_chunk(int Dqk, int page_size) {
+  int c = Dqk == 192 ? 32 : 128;   // a divisor of prefix_block(Dqk)
+  while (page_size % c != 0) c /= 2;
+  return c < 8 ? 0 : c;
+}
+
+size_t prefix_workspace_bytes(int T, int P, int Hq, int Hkv, int Dv, bool decode) {
+  size_t n = prefix_pre_bytes(P) + prefix_parts_bytes(Dv);
+  if (decode) n += 2 * prefix_rows_bytes(T, Hq, Dv) + paged_workspace_bytes(T, Dv);
+  return n;
+}
+
+cudaError_t launch_prefix_fwd(const PrefixMaps& m, const PrefixArgs& a, int num_sms, bool* configured, cudaStream_t stream) {
+  const int runs = prefix_runs(a.Hkv, num_sms);
+  const cudaError_t e = launch_prefix_any(m, a, runs, configured, stream);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute at[1];
+  const cudaLaunchConfig_t cfg = early(dim3((unsigned)runs, (unsigned)a.Hkv, kPrefixRows / 32), kJoinThreads, stream, at);
+  return a.Dv == 64 ? cudaLaunchKernelEx(&cfg, prefix_join_kernel<64>, a, runs)
+                    : cudaLaunchKernelEx(&cfg, prefix_join_kernel<128>, a, runs);
+}
+
+cudaError_t launch_prefix_decode(const PrefixMaps& m, const PrefixArgs& a, int num_sms, bool* configured, bool* own_configured,
+                                 cudaStream_t stream) {
+  const int runs = prefix_runs(a.Hkv, num_sms);
+  cudaError_t e = launch_prefix_any(m, a, runs, configured, stream);
+  if (e != cudaSuccess) return e;
+  uint8_t* ws = a.ws + prefix_pre_bytes(a.P) + prefix_parts_bytes(a.Dv) + prefix_rows_bytes(a.T, a.Hq, a.Dv);
+  PagedArgs o{};
+  o.q = a.q; o.q_sb = a.q_st; o.q_sh = a.q_sh;
+  o.k = a.k; o.k_sp = a.k_sp; o.k_st = a.k_st; o.k_sh = a.k_sh;
+  o.v = a.v; o.v_sp = a.v_sp; o.v_st = a.v_st; o.v_sh = a.v_sh;
+  o.page_table = a.page_table; o.table_stride = a.table_stride;
+  o.cache_lens = a.cache_lens;
+  o.rows = reinterpret_cast<float*>(ws);
+  o.ws = ws + prefix_rows_bytes(a.T, a.Hq, a.Dv);
+  o.err = a.err;
+  o.B = a.T; o.Hq = a.Hq; o.Hkv = a.Hkv; o.G = a.G; o.Dqk = a.Dqk; o.Dv = a.Dv;
+  o.max_pages = a.max_pages; o.num_pages = a.num_pages; o.page_size = a.page_size;
+  o.scale_log2 = a.scale_log2;
+  o.shared = a;
+  int workers = 0;
+  if ((e = launch_paged_shared(o, num_sms, own_configured, &workers, stream)) != cudaSuccess) return e;
+  const int64_t pairs = (int64_t)a.T * a.Hkv;
+  int y = (int)(2 * num_sms / pairs);
+  y = y < 1 ? 1 : y > a.G ? a.G : y;
+  cudaLaunchAttribute at[1];
+  const cudaLaunchConfig_t cfg = early(dim3((unsigned)pairs, (unsigned)y), kStepThreads, stream, at);
+  const uint8_t* own_ws = o.ws;
+  const float* own_rows = o.rows;
+  return a.Dv == 64 ? cudaLaunchKernelEx(&cfg, prefix_step_join_kernel<64>, a, own_ws, own_rows, runs, workers)
+                    : cudaLaunchKernelEx(&cfg, prefix_step_join_kernel<128>, a, own_ws, own_rows, runs, workers);
+}
+
+}  // namespace irs
