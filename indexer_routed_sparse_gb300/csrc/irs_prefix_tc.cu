@@ -21,8 +21,8 @@
 //   chunk of a prefix, by 16-byte copies with zeros behind the end: no position past it is read,
 //   and 0 times whatever its value holds is never formed.
 // * S[128 x block] = Q K^T lies in TMEM; the weights return over it as bf16 and are the first operand
-//   of O += P V straight from TMEM. Two threads share a row. The running maximum is raised only where
-//   a half row's weights under it sum past 2^8, so that a block's scores are read once and O is hardly
+//   of O += P V straight from TMEM. A thread has a row. The running maximum is raised only where a
+//   row's weights under it sum past 2^8, so that a block's scores are read once and O is hardly
 //   ever rescaled; the sums are FP32.
 #include <climits>
 
@@ -37,10 +37,12 @@ namespace {
 
 constexpr int kRows = 128;              // rows a tile
 constexpr uint32_t kAtom = 128 * 128;   // 128 rows x 64 bf16
-// warps 0-7, 8-15: softmax of the two tiles; 16: plan, queries and keys; 17, 18: products of the two tiles; 19: values
-constexpr int kThreads = 640;
-constexpr float kRaise = 256.f;         // a half row's weights of a block with a sum past this raise the maximum
-constexpr int kPlanReaders = 19;        // warps that read an item's plan
+// warps 0-3, 4-7: softmax of the two tiles, a thread a row; 8: plan, queries and keys; 9: values; 10, 11: products
+// of the two tiles. Registers: 384 x 168 at launch, of which the softmax's threads take 208
+// and the others keep 88: 256 x 208 + 128 x 88 = 384 x 168.
+constexpr int kThreads = 384;
+constexpr float kRaise = 256.f;         // a row's weights of a block with a sum past this raise the maximum
+constexpr int kPlanReaders = 11;        // warps that read an item's plan
 
 template <int DQK, int DV>
 struct Cfg {
@@ -52,24 +54,71 @@ struct Cfg {
   static constexpr int KS = DQK == 64 ? 4 : DQK == 128 ? 3 : 2;                    // stages of keys
   static constexpr int VS = DQK == 64 ? (DV == 64 ? 4 : 3) : (DV == 64 ? 3 : 2);   // and values
   static constexpr uint32_t k_off = 2 * q_bytes, v_off = k_off + KS * k_bytes;
-  // a word a row, half and tile, by which the two threads of a row exchange maxima and sums
-  static constexpr uint32_t x_off = v_off + VS * v_bytes, x_bytes = 2 * 2 * kRows * 4;
-  static constexpr uint32_t bar_off = x_off + x_bytes;
+  static constexpr uint32_t bar_off = v_off + VS * v_bytes;
   static constexpr uint32_t plan_off = bar_off + 40 * 8 + 16;   // [4][8] the items' plans
   static constexpr uint32_t total = plan_off + 4 * 32;
   static_assert(total <= 232448, "227 KB");
   static constexpr uint32_t S0 = 0, O0 = 256;              // TMEM: scores at 128 x, outputs at 256 + x DV
 };
 
-// D[128 x DV] (+)= P . V: P bf16 in TMEM, V a [position][dim] tile read MN-major; NK steps of 16
-// positions. Each half of the positions has its weights at the first of its own score columns.
+// D[128 x DV] (+)= P . V: P bf16 in TMEM, V a [position][dim] tile read MN-major; NK steps of 16 positions.
 template <int NK>
 __device__ __forceinline__ void pv_run(uint32_t d, uint32_t p, uint32_t vb, uint32_t atom, uint32_t idesc, bool accumulate) {
   const uint64_t b0 = sdesc_sw128(vb, atom, 1024);
 #pragma unroll
   for (int ks = 0; ks < NK; ++ks)
-    umma_bf16_ts_warp(d, p + (ks < NK / 2 ? 8 * ks : 8 * NK + 8 * (ks - NK / 2)), b0 + (uint64_t)((ks * 2048) >> 4), idesc,
-                      (accumulate || ks > 0) ? 1u : 0u);
+    umma_bf16_ts_warp(d, p + 8 * ks, b0 + (uint64_t)((ks * 2048) >> 4), idesc, (accumulate || ks > 0) ? 1u : 0u);
+}
+
+// A row's weights of a whole block, 2^(score * scale + off), as bf16 pairs, and their sum. The loads of the
+// second half run behind the first half's work. Written in the order of issue: a piece's exponentials, then the
+// sums and roundings of the piece before, so that a lone warp does not wait for each result in turn (pair by
+// pair a block took 2300 cycles).
+template <int NP>
+__device__ __forceinline__ void row_weights(uint32_t s_addr, float scale, float off, uint32_t (&w)[NP][8], float& ln) {
+  constexpr int HP = NP / 2;
+  const uint64_t sc2 = pack2(scale, scale), off2 = pack2(off, off);
+  uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};   // FP32 pairs
+  float v[NP][16], p[2][16];
+#pragma unroll
+  for (int c = 0; c < HP; ++c) tmem_ld16(s_addr + 16 * c, v[c]);
+  auto finish = [&](int c) {
+    float(&q)[16] = p[c & 1];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum[i & 3] = fadd2(sum[i & 3], pack2(q[2 * i], q[2 * i + 1]));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(q[2 * i], q[2 * i + 1]);
+      w[c][i] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+  };
+#pragma unroll
+  for (int c = 0; c < NP; ++c) {
+    if (c == 0 || c == HP) {
+      tmem_ld_wait();
+#pragma unroll
+      for (int k = c; k < c + HP; ++k)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) asm volatile("" : "+f"(v[k][i]));   // no use before the wait
+      if (c == 0) {
+#pragma unroll
+        for (int k = HP; k < NP; ++k) tmem_ld16(s_addr + 16 * k, v[k]);
+      }
+    }
+    float z[16];
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) {
+      const float2 f = unpack2(ffma2(pack2(v[c][i], v[c][i + 1]), sc2, off2));
+      z[i] = f.x;
+      z[i + 1] = f.y;
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(p[c & 1][i]) : "f"(z[i]));
+    if (c > 0) finish(c - 1);
+  }
+  finish(NP - 1);
+  const float2 s2 = unpack2(fadd2(fadd2(sum[0], sum[1]), fadd2(sum[2], sum[3])));
+  ln = s2.x + s2.y;
 }
 
 // Copies blocks of a prefix's keys or values into a ring; a whole warp.
@@ -233,7 +282,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* p_full = s_full + 2;          // [2] its weights
   uint64_t* o_full = p_full + 2;          // [2] its output
   uint64_t* o_empty = o_full + 2;         // [2]
-  uint64_t* drain = o_empty + 2;          // [2]
+  uint64_t* turn = o_empty + 2;           // [2] the tile's products may be issued
+  uint64_t* drain = turn + 2;             // [2]
   uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + C::bar_off + 40 * 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
   volatile int* start_g = reinterpret_cast<volatile int*>(tslot + 2);   // group that this CTA's run starts in
@@ -248,15 +298,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < VS; ++i) { mbar_init(&v_full[i], 1); mbar_init(&v_empty[i], 2); }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&q_full[i], 1); mbar_init(&q_empty[i], 1);
-      mbar_init(&s_full[i], 1); mbar_init(&p_full[i], 8);
-      mbar_init(&o_full[i], 1); mbar_init(&o_empty[i], 8);
-      mbar_init(&drain[i], 1);
+      mbar_init(&s_full[i], 1); mbar_init(&p_full[i], 4);
+      mbar_init(&o_full[i], 1); mbar_init(&o_empty[i], 4);
+      mbar_init(&turn[i], 1); mbar_init(&drain[i], 1);
     }
     *abort_flag = 0;
     *start_g = -1;
     fence_mbar_init();
   }
-  if (warp == 17) {
+  if (warp == 10) {
     tmem_alloc(tslot, 512);
     tmem_relinquish();
   }
@@ -330,7 +380,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     return m.nb > 0;
   };
 
-  if (warp == 16) {
+  if (warp >= 8) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+  if (warp == 8) {
     // ---------------- plan, queries and keys ----------------
     Loader<C::QA, BLK, KS> ld{};
     ld.map = &tm_k; ld.base = a.k + (int64_t)head * a.k_sh; ld.sp = a.k_sp; ld.stt = a.k_st;
@@ -429,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           while (!mbar_try_wait(&q_full[x], (nq[x] - 1) & 1) && globaltimer_ns() - w0 < kWaitLimitNs) {}
         }
     }
-  } else if (warp == 19) {
+  } else if (warp == 9) {
     // ---------------- values ----------------
     Loader<C::VA, BLK, VS> ld{};
     ld.map = &tm_v; ld.base = a.v + (int64_t)head * a.v_sh; ld.sp = a.v_sp; ld.stt = a.v_st;
@@ -440,19 +492,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (next_item(m))
       if (!ld.run(a.page_table + (int64_t)m.row * a.table_stride, m.b0, m.nb, m.n)) break;
     ld.drain();
-  } else if (warp >= 17) {
+  } else {
     // ---------------- the products of a tile (the whole warp; one elected lane issues) ----------------
+    // A turn is a tile's weights of the block before times their values, then its scores of the next block.
+    // The tiles take turns, so that one's softmax has the other's turn to run in. A warp each, because waits and
+    // commits cost the issuing warp 100 to 300 cycles apiece, which the other warp's products fill; and one
+    // commit a turn, whose reader releases the operands.
     constexpr uint32_t PV_IDESC = idesc_bf16(kRows, DV, false, true);
-    const int x = uniform(warp - 17);
+    const int x = uniform(warp - 10);
     const uint32_t tb = (uint32_t)uniform((int)tbase), sb = smem_u32(smem);
     const uint32_t s_tm = tb + C::S0 + 128 * x, o_tm = tb + C::O0 + x * DV;
-    const uint64_t a0 = sdesc_sw128(sb + x * C::q_bytes, 16, 1024);
-    uint32_t nq = 0, no = 0, np = 0, ks = 0, kph = 0, vs = 0, vph = 0;
+    const uint64_t q0 = sdesc_sw128(sb + x * C::q_bytes, 16, 1024);
+    uint32_t nq = 0, no = 0, np = 0, nt = 0, ks = 0, kph = 0, vs = 0, vph = 0;
     bool alive = true;
     Item m;
     while (alive && next_item(m)) {
       const int nb = uniform(m.nb), b0 = uniform(m.b0), n = uniform(m.n);
-      if (x == 1 && m.t0 + qt >= m.t1) {       // an item of one tile: its blocks pass by
+      const bool two = m.t0 + qt < m.t1;
+      if (x == 1 && !two) {                    // an item of one tile: its blocks pass by, every phase in turn
         for (int j = 0; j < nb && alive; ++j) {
           alive = wait_all(&k_full[ks], kph) && wait_all(&v_full[vs], vph);
           if (lane == 0) { mbar_arrive(&k_empty[ks]); mbar_arrive(&v_empty[vs]); }
@@ -466,12 +523,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++nq;
       int cols = 0;
       for (int j = 0; j <= nb; ++j) {
+        if (j < nb && !wait_all(&k_full[ks], kph)) { alive = false; break; }
+        if (j > 0 && !(wait_all(&v_full[vs], vph) && (j > 1 || no == 0 || wait_all(&o_empty[x], (no - 1) & 1)) &&
+                       wait_all(&p_full[x], np & 1))) { alive = false; break; }
+        if (two) {
+          if ((x == 1 || nt > 0) && !wait_all(&turn[x], (x == 1 ? nt : nt - 1) & 1)) { alive = false; break; }
+          ++nt;
+        }
+        tc_fence_after();
         if (j > 0) {
-          // O += P V of the block before
-          if (!wait_all(&v_full[vs], vph) || !wait_all(&p_full[x], np & 1)) { alive = false; break; }
-          if (j == 1 && no > 0 && !wait_all(&o_empty[x], (no - 1) & 1)) { alive = false; break; }
-          ++np;
-          tc_fence_after();
           const uint32_t vb = sb + C::v_off + vs * C::v_bytes;
           switch (cols >> 5) {
             case 1: pv_run<2>(o_tm, s_tm, vb, C::atom, PV_IDESC, j > 1); break;
@@ -479,152 +539,150 @@ __global__ void __launch_bounds__(kThreads, 1)
             case 3: pv_run<6>(o_tm, s_tm, vb, C::atom, PV_IDESC, j > 1); break;
             default: pv_run<BLK / 16>(o_tm, s_tm, vb, C::atom, PV_IDESC, j > 1); break;
           }
-          if (j == nb) { umma_commit_warp(&o_full[x]); ++no; }
-          umma_commit_warp(&v_empty[vs]);
+          ++np;
           if (++vs == (uint32_t)VS) { vs = 0; vph ^= 1u; }
         }
         if (j < nb) {
-          if (!wait_all(&k_full[ks], kph)) { alive = false; break; }
-          tc_fence_after();
           cols = min(BLK, (n - (b0 + j) * BLK + 31) & ~31);
           const uint32_t idesc = idesc_bf16(kRows, cols, false, false);
           const uint64_t b = sdesc_sw128(sb + C::k_off + ks * C::k_bytes, 16, 1024);
 #pragma unroll
           for (int i = 0; i < 4 * C::QA; ++i)
-            umma_bf16_warp(s_tm, a0 + (uint64_t)(((i >> 2) * kAtom + (i & 3) * 32) >> 4),
+            umma_bf16_warp(s_tm, q0 + (uint64_t)(((i >> 2) * kAtom + (i & 3) * 32) >> 4),
                            b + (uint64_t)(((i >> 2) * C::atom + (i & 3) * 32) >> 4), idesc, i > 0);
-          umma_commit_warp(&s_full[x]);
-          umma_commit_warp(&k_empty[ks]);
-          if (j == nb - 1) umma_commit_warp(&q_empty[x]);
           if (++ks == (uint32_t)KS) { ks = 0; kph ^= 1u; }
         }
+        if (two && lane == 0) mbar_arrive(&turn[x ^ 1]);
+        __syncwarp();
+        umma_commit_warp(j < nb ? &s_full[x] : &o_full[x]);
       }
+      ++no;
     }
     // every issued product completes before the CTA releases its tensor memory
     umma_commit_warp(&drain[x]);
     const unsigned long long w0 = globaltimer_ns();
     while (!mbar_try_wait(&drain[x], 0) && globaltimer_ns() - w0 < kWaitLimitNs) {}
     __syncwarp();
+  }
   } else {
-    // ---------------- softmax: warps 0-7 the first tile, 8-15 the second ----------------
-    const int x = warp >> 3, half = (warp >> 2) & 1;
-    const int bar_id = 1 + x * 4 + (warp & 3);            // the two warps of these rows
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    // ---------------- softmax: warps 0-3 the first tile, 4-7 the second, a thread a row ----------------
+    const int x = warp >> 2;
     const int r = (warp & 3) * 32 + lane;                 // row of the tile = TMEM lane
     const int rq = r / a.G;                               // its token
     const int rel = rq * a.Hq + head * a.G + r - rq * a.G;   // its row of out, relative to the tile's first token's
     const uint32_t s_addr = tbase + C::S0 + 128 * x + tmem_lane_base(warp);
     const uint32_t o_addr = tbase + C::O0 + x * DV + tmem_lane_base(warp);
-    const uint32_t mine_w = smem_u32(smem) + C::x_off + (uint32_t)((x * 2 + half) * kRows + r) * 4u;
-    const uint32_t other_w = smem_u32(smem) + C::x_off + (uint32_t)((x * 2 + (half ^ 1)) * kRows + r) * 4u;
-    uint32_t ns = 0, no = 0;
+    uint32_t ns = 0, no = 0, ks = 0, vs = 0;              // blocks, items; stages to release next
     bool alive = true;
     Item m;
     while (alive && next_item(m)) {
       const int t0 = m.t0 + x * qt, t = t0 + rq;
-      if (t0 >= m.t1) continue;
+      if (t0 >= m.t1) {                                   // an item of one tile
+        ks = (ks + m.nb) % KS;
+        vs = (vs + m.nb) % VS;
+        continue;
+      }
       const bool live = rq < qt && t < m.t1;
+      // Scores that are there say that the products before them are done: the tile's first warp then releases
+      // their operands.
+      const bool release = (warp & 3) == 0 && lane == 0;
+      auto free_stage = [&](uint64_t* empty, uint32_t& st, int stages) {
+        mbar_arrive(&empty[st]);
+        if (++st == (uint32_t)stages) st = 0;
+      };
       float mx = -INFINITY, l = 0.f;
-      bool settled = false;                               // every row of the warps has a maximum
-      for (int j = 0; j < m.nb && alive; ++j) {
+      bool settled = false;                               // every row of the warp has a maximum
+      for (int j = 0; j < m.nb; ++j) {
         const int left = m.n - (m.b0 + j) * BLK;          // positions from the block's first on
-        const int cols = min(BLK, (left + 31) & ~31), pieces = cols >> 5, c0 = half * (cols >> 1);
-        const bool border = left < cols;
-        alive = wait_all(&s_full[x], ns & 1);
+        if (!(alive = wait_all(&s_full[x], ns & 1))) break;
         ++ns;
-        tc_fence_after();
-        // One pass: the weights under the present maximum, and whether their sum passes 2^8. They
-        // wait in registers for the two halves' vote; where it asks for it (and for the first
-        // block, before every row has a maximum) the scores are read again.
-        constexpr int NP = BLK / 32;
-        uint32_t w[NP][8];
-        float ln = 0.f;
-        auto scores = [&](int c, float (&v)[16]) {
-          tmem_ld16(s_addr + c0 + 16 * c, v);
-          tmem_ld_wait_regs(v);
-          if (border) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = c0 + 16 * c + i < left ? v[i] : -INFINITY;
-          }
-        };
-        auto weights = [&]() {
-          const float off = mx == -INFINITY ? 0.f : -mx;
-          const uint64_t sc2 = pack2(a.scale_log2, a.scale_log2), off2 = pack2(off, off);
-          uint64_t sum0 = 0ull, sum1 = 0ull;   // FP32 pairs
-#pragma unroll
-          for (int c = 0; c < NP; ++c) {
-            if (c < pieces) {
-              float v[16];
-              scores(c, v);
-#pragma unroll
-              for (int i = 0; i < 16; i += 4) {
-                const float2 x0 = unpack2(ffma2(pack2(v[i], v[i + 1]), sc2, off2));
-                const float2 x1 = unpack2(ffma2(pack2(v[i + 2], v[i + 3]), sc2, off2));
-                const float p0 = ex2_approx(x0.x), p1 = ex2_approx(x0.y), p2 = ex2_approx(x1.x), p3 = ex2_approx(x1.y);
-                sum0 = fadd2(sum0, pack2(p0, p1));
-                sum1 = fadd2(sum1, pack2(p2, p3));
-                const __nv_bfloat162 y0 = __floats2bfloat162_rn(p0, p1), y1 = __floats2bfloat162_rn(p2, p3);
-                w[c][i >> 1] = *reinterpret_cast<const uint32_t*>(&y0);
-                w[c][(i >> 1) + 1] = *reinterpret_cast<const uint32_t*>(&y1);
-              }
-            }
-          }
-          const float2 s2 = unpack2(fadd2(sum0, sum1));
-          ln = s2.x + s2.y;
-        };
-        bool slow = !settled;
-        if (!slow) {
-          weights();
-          // a row that is none has no vote; NaN compares false and goes on
-          slow = named_bar_or(bar_id, 64, (live && ln > kRaise) || !alive);
+        if (release) {
+          free_stage(k_empty, ks, KS);
+          if (j > 0) free_stage(v_empty, vs, VS);
+          if (j == m.nb - 1) mbar_arrive(&q_empty[x]);
         }
+        __syncwarp();
+        tc_fence_after();
+        // The common case, one pass: the weights under the present maximum, and whether their sum passes
+        // 2^8. They wait in registers for the warp's vote.
+        constexpr int NP = BLK / 16;                      // pieces of 16 columns
+        bool slow = !settled || left < BLK;
+        if (!slow) {
+          uint32_t w[NP][8];
+          float ln = 0.f;
+          row_weights<NP>(s_addr, a.scale_log2, -mx, w, ln);
+          slow = __any_sync(0xffffffffu, live && ln > kRaise);   // a row that is none has no vote; NaN goes on
+          if (!slow) {
+            l += ln;
+#pragma unroll
+            for (int c = 0; c < NP; ++c) tmem_st8(s_addr + 8 * c, reinterpret_cast<const float(&)[8]>(w[c]));
+          }
+        }
+        // An item's first block (no row has a maximum yet), a prefix's last (it may end inside) and blocks that
+        // raise a maximum: two passes.
         if (slow) {
+          const int pieces = min(BLK, (left + 31) & ~31) >> 4;
+          auto scores = [&](int c, float (&v)[16]) {
+            tmem_ld16(s_addr + 16 * c, v);
+            tmem_ld_wait_regs(v);
+            if (left < 16 * c + 16) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) v[i] = 16 * c + i < left ? v[i] : -INFINITY;
+            }
+          };
           float top = -INFINITY;
+#pragma unroll 1
           for (int c = 0; c < pieces; ++c) {
             float v[16];
             scores(c, v);
 #pragma unroll
             for (int i = 0; i < 16; ++i) top = fmaxf(top, v[i]);
           }
-          top *= a.scale_log2;
-          st_shared(mine_w, top);
-          alive = named_bar_and(bar_id, 64, alive);   // both halves leave together after a wait that gave up
-          const float nm = fmaxf(mx, fmaxf(top, ld_shared(other_w)));
-          const float c = nm == -INFINITY ? 1.f : ex2_approx(mx - nm);
+          const float nm = fmaxf(mx, top * a.scale_log2);
+          const float f = nm == -INFINITY ? 1.f : ex2_approx(mx - nm);
           mx = nm;
-          l *= c;
+          l *= f;
           // O has every earlier product: these scores were issued behind them
-          if (j > 0 && alive) {
+          if (j > 0 && __any_sync(0xffffffffu, f != 1.f)) {
 #pragma unroll 1
-            for (int d = half * (DV / 2); d < (half + 1) * (DV / 2); d += 16) {
+            for (int d = 0; d < DV; d += 16) {
               float o[16];
               tmem_ld16(o_addr + d, o);
               tmem_ld_wait_regs(o);
 #pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] *= c;
+              for (int i = 0; i < 16; ++i) o[i] *= f;
               tmem_st16(o_addr + d, o);
             }
           }
-          weights();
-          settled = named_bar_and(bar_id, 64, !live || mx > -INFINITY);   // and both have read the words
-        }
-        l += ln;
+          const float off = mx == -INFINITY ? 0.f : -mx;
+#pragma unroll 1
+          for (int c = 0; c < pieces; ++c) {
+            float v[16];
+            uint32_t w[8];
+            scores(c, v);
 #pragma unroll
-        for (int c = 0; c < NP; ++c)
-          if (c < pieces) tmem_st8(s_addr + c0 + 8 * c, reinterpret_cast<const float(&)[8]>(w[c]));
+            for (int i = 0; i < 16; i += 2) {
+              const float p0 = ex2_approx(fmaf(v[i], a.scale_log2, off)), p1 = ex2_approx(fmaf(v[i + 1], a.scale_log2, off));
+              l += p0 + p1;
+              const __nv_bfloat162 b = __floats2bfloat162_rn(p0, p1);
+              w[i >> 1] = *reinterpret_cast<const uint32_t*>(&b);
+            }
+            tmem_st8(s_addr + 8 * c, reinterpret_cast<const float(&)[8]>(w));   // over columns that have been read
+          }
+          settled = __all_sync(0xffffffffu, !live || mx > -INFINITY);
+        }
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[x]);
       }
-      // ---- the tile's rows, half the dims a thread ----
-      if (alive) alive = wait_all(&o_full[x], no & 1);
+      // ---- the tile's rows ----
+      if (!alive || !(alive = wait_all(&o_full[x], no & 1))) break;
       ++no;
+      if (release) free_stage(v_empty, vs, VS);
+      __syncwarp();
       tc_fence_after();
-      st_shared(mine_w, l);
-      alive = named_bar_and(bar_id, 64, alive);
-      if (!alive) break;
-      l += ld_shared(other_w);
-      named_bar_sync(bar_id, 64);                         // both have read the words
       if (l == 0.f) l = -1.f;                             // attended, and every score -inf: in a part, a finite maximum wipes it out
       const int64_t row = (int64_t)t0 * a.Hq + rel;
       if (m.part != 0 || a.cache_lens != nullptr) {
@@ -634,36 +692,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (m.part != 0) {
           float* part = prefix_part(a, run, head, m.part - 1);
           dst = part + (size_t)(x * kRows + r) * DV;
-          ml = part + 2 * kRows * DV + 2 * (x * kRows + r);
+          ml = part + kPrefixRows * DV + 2 * (x * kRows + r);
         } else {
           dst = prefix_rows(a) + row * DV;
           ml = prefix_rows(a) + (size_t)a.T * a.Hq * DV + 2 * row;
         }
 #pragma unroll 1
-        for (int d = half * (DV / 2); d < (half + 1) * (DV / 2); d += 16) {
-          float o[16];
-          tmem_ld16(o_addr + d, o);
+        for (int d = 0; d < DV; d += 32) {
+          float o[32];
+          tmem_ld32(o_addr + d, o);
           tmem_ld_wait_regs(o);
           if (live) {
 #pragma unroll
-            for (int i = 0; i < 16; i += 4) *reinterpret_cast<float4*>(dst + d + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+            for (int i = 0; i < 32; i += 4) *reinterpret_cast<float4*>(dst + d + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
           }
         }
-        if (live && half == 0) *reinterpret_cast<float2*>(ml) = make_float2(mx, l);
+        if (live) *reinterpret_cast<float2*>(ml) = make_float2(mx, l);
       } else {
         const PrefixJoin jn = live ? prefix_join_own(a, row, mx, l) : PrefixJoin{0.f, 0.f, 0.f};
-        named_bar_sync(bar_id, 64);                       // lse may be own_lse: both have read it
 #pragma unroll 1
-        for (int d = half * (DV / 2); d < (half + 1) * (DV / 2); d += 16) {
-          float o[16];
-          tmem_ld16(o_addr + d, o);
+        for (int d = 0; d < DV; d += 32) {
+          float o[32];
+          tmem_ld32(o_addr + d, o);
           tmem_ld_wait_regs(o);
           if (live) {
 #pragma unroll
-            for (int i = 0; i < 16; i += 8) prefix_store8(a, row * DV + d + i, jn, o + i);
+            for (int i = 0; i < 32; i += 8) prefix_store8(a, row * DV + d + i, jn, o + i);
           }
         }
-        if (half == 0 && live && a.lse != nullptr) a.lse[row] = jn.lse;
+        if (live && a.lse != nullptr) a.lse[row] = jn.lse;
       }
       tc_fence_before();
       __syncwarp();
@@ -672,7 +729,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 17) {
+  if (warp == 10) {
     tc_fence_after();
     tmem_dealloc(tbase, 512);
   }
@@ -680,8 +737,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Prompts: joins the parts of the items that runs' borders cut, with the rows' other parts too, and
 // writes the rows of empty prefixes. A block takes 32 rows of the item that holds border blockIdx.x of
-// a head's list, if that is the item's first; eight columns a thread.
-constexpr int kJoinThreads = 256;
+// a head's list, if that is the item's first; eight columns a thread, four parts in flight.
+constexpr int kJoinThreads = 512;
 template <int DV>
 __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(PrefixArgs a, int runs) {
   constexpr int CL = DV / 8, R = kJoinThreads / CL;   // threads a row, rows at a time
@@ -712,13 +769,24 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(PrefixArgs a,
         if (rq >= qt || t >= grp.last) continue;
         PrefixSum<8> sum;
         sum.clear();
-        for (int c = c0; c <= c1; ++c) {
-          // the item's first part is its run's second, unless the run starts with it
-          const float* part = prefix_part(a, c, head, c == c0 && s != (int64_t)c0 * share ? 1 : 0);
-          const float2 ml = *reinterpret_cast<const float2*>(part + kPrefixRows * DV + 2 * r);
-          float o[8];
-          prefix_load8(o, part + (size_t)r * DV + 8 * cl);
-          sum.add(ml.x, ml.y, o);
+        constexpr int U = 4;
+        for (int c = c0; c <= c1; c += U) {
+          float2 ml[U];
+          float o[U][8];
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            ml[u] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) o[u][k] = 0.f;
+            if (c + u <= c1) {
+              // the item's first part is its run's second, unless the run starts with it
+              const float* part = prefix_part(a, c + u, head, c + u == c0 && s != (int64_t)c0 * share ? 1 : 0);
+              ml[u] = *reinterpret_cast<const float2*>(part + kPrefixRows * DV + 2 * r);
+              prefix_load8(o[u], part + (size_t)r * DV + 8 * cl);
+            }
+          }
+#pragma unroll
+          for (int u = 0; u < U; ++u) sum.add(ml[u].x, ml[u].y, o[u]);
         }
         store((int64_t)t * a.Hq + head * a.G + rr - rq * a.G, sum.m, sum.l, sum.o);
       }
