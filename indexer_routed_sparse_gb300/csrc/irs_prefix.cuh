@@ -14,9 +14,8 @@ namespace irs {
 
 namespace {
 
-// Positions a block of keys: 128 columns of scores a product where shared memory has room for the
-// stages; beside queries of 192 dims it has for 96.
-__host__ __device__ constexpr int prefix_block(int Dqk) { return Dqk == 192 ? 96 : 128; }
+// Positions a block: both tiles' scores, weights (half as wide) and outputs lie in the 512 columns of TMEM.
+__host__ __device__ constexpr int prefix_block(int Dv) { return Dv == 64 ? 128 : 80; }
 constexpr int kPrefixRows = 256;      // rows an item (two tiles)
 constexpr int kMaxPrefixCtas = 160;
 constexpr int kMinBlocks = 1;         // a run has at least this many blocks
@@ -24,7 +23,9 @@ constexpr int kMinBlocks = 1;         // a run has at least this many blocks
 __host__ __device__ inline size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
 
 // Workspace: sums of the groups' blocks; two parts a CTA (the item its run starts in, the one it ends
-// in): rows of Dv sums, then (maximum, sum) pairs; decoding, the same a row for rows that no border cuts.
+// in); decoding, the same a row for rows that no border cuts. Sums of n rows lie as [Dv / 4][n][4], then
+// [n] pairs of maximum and sum: a warp's 32 rows are 512 bytes a store, where rows of Dv columns made
+// a store touch 32 lines and an item's end take 8,000 cycles.
 __host__ __device__ inline size_t prefix_pre_bytes(int P) { return align256(((size_t)P + 1) * 8); }
 __host__ __device__ inline size_t prefix_part_floats(int Dv) { return (size_t)kPrefixRows * (Dv + 2); }
 __host__ __device__ inline size_t prefix_parts_bytes(int Dv) { return (size_t)kMaxPrefixCtas * 2 * prefix_part_floats(Dv) * 4; }
@@ -37,12 +38,24 @@ __device__ __forceinline__ float* prefix_rows(const PrefixArgs& a) {
   return reinterpret_cast<float*>(a.ws + prefix_pre_bytes(a.P) + prefix_parts_bytes(a.Dv));
 }
 
+__device__ __forceinline__ float4& prefix_sums4(float* sums, int64_t n, int64_t row, int d) {
+  return *reinterpret_cast<float4*>(sums + ((int64_t)(d / 4) * n + row) * 4);
+}
+__device__ __forceinline__ float2& prefix_sums_ml(float* sums, int64_t n, int64_t row, int Dv) {
+  return *reinterpret_cast<float2*>(sums + n * Dv + 2 * row);
+}
+__device__ __forceinline__ void prefix_sums8(float (&o)[8], float* sums, int64_t n, int64_t row, int d) {
+  const float4 x = prefix_sums4(sums, n, row, d), y = prefix_sums4(sums, n, row, d + 4);
+  o[0] = x.x; o[1] = x.y; o[2] = x.z; o[3] = x.w;
+  o[4] = y.x; o[5] = y.y; o[6] = y.z; o[7] = y.w;
+}
+
 // Blocks of a group in a head's list: its pairs of tiles (qt tokens each), each over the whole prefix.
 __device__ __forceinline__ int64_t prefix_units(const PrefixGroup& g, int qt, int blk) {
   return (int64_t)((g.last - g.first + 2 * qt - 1) / (2 * qt)) * ((g.n + blk - 1) / blk);
 }
 __device__ __forceinline__ int prefix_blocks(const PrefixArgs& a, int n) {
-  const int blk = prefix_block(a.Dqk);
+  const int blk = prefix_block(a.Dv);
   return (n + blk - 1) / blk;
 }
 // Blocks of a run.
@@ -60,14 +73,14 @@ __device__ __forceinline__ int prefix_find(const int64_t* pre, int P, int64_t f)
   return lo;
 }
 
-// Malformed borders and prefix lengths, by one block.
-__device__ __forceinline__ void prefix_check(const PrefixArgs& a) {
+// Malformed borders and prefix lengths, by threads 0 .. n - 1.
+__device__ __forceinline__ void prefix_check(const PrefixArgs& a, int i, int n) {
   int errors = 0;
-  if (threadIdx.x == 0 && (a.cu[0] != 0 || a.cu[a.P] > a.T)) errors |= IRS_DEVERR_CU_SEQLENS;
-  for (int g = threadIdx.x; g < a.P; g += blockDim.x) {
+  if (i == 0 && (a.cu[0] != 0 || a.cu[a.P] > a.T)) errors |= IRS_DEVERR_CU_SEQLENS;
+  for (int g = i; g < a.P; g += n) {
     if (a.cu[g + 1] < a.cu[g]) errors |= IRS_DEVERR_CU_SEQLENS;
-    const int n = a.prefix_lens[g];
-    if (n < 0 || n > a.max_pages * a.page_size) errors |= IRS_DEVERR_PAGE;
+    const int len = a.prefix_lens[g];
+    if (len < 0 || len > a.max_pages * a.page_size) errors |= IRS_DEVERR_PAGE;
   }
   if (errors) record_error(a.err, errors);
 }
@@ -120,25 +133,27 @@ __device__ __forceinline__ PrefixJoin prefix_join_own(const PrefixArgs& a, int64
   }
   return j;
 }
-// Eight columns of the result, from element `at` of out on.
-__device__ __forceinline__ void prefix_store8(const PrefixArgs& a, int64_t at, const PrefixJoin& j, const float* o) {
-  float y[8];
+// Eight columns of the result as bf16 pairs; z: those of the other part (not looked at where it does not count).
+__device__ __forceinline__ void prefix_mix8(uint32_t* w, const PrefixJoin& j, const float* o, const uint4& z) {
+  const __nv_bfloat162* zz = reinterpret_cast<const __nv_bfloat162*>(&z);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) y[i] = j.mine == 0.f ? 0.f : o[i] * j.mine;
-  if (j.theirs != 0.f) {
-    const uint4 z = *reinterpret_cast<const uint4*>(a.own_out + at);
-    const __nv_bfloat162* zz = reinterpret_cast<const __nv_bfloat162*>(&z);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 4; ++i) {
+    float x = j.mine == 0.f ? 0.f : o[2 * i] * j.mine, y = j.mine == 0.f ? 0.f : o[2 * i + 1] * j.mine;
+    if (j.theirs != 0.f) {
       const float2 f = __bfloat1622float2(zz[i]);
-      y[2 * i] = fmaf(j.theirs, f.x, y[2 * i]);
-      y[2 * i + 1] = fmaf(j.theirs, f.y, y[2 * i + 1]);
+      x = fmaf(j.theirs, f.x, x);
+      y = fmaf(j.theirs, f.y, y);
     }
+    const __nv_bfloat162 b = __floats2bfloat162_rn(x, y);
+    w[i] = *reinterpret_cast<const uint32_t*>(&b);
   }
-  __nv_bfloat162 b[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) b[i] = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
-  *reinterpret_cast<uint4*>(a.out + at) = *reinterpret_cast<const uint4*>(b);
+}
+// ... to element `at` of out on.
+__device__ __forceinline__ void prefix_store8(const PrefixArgs& a, int64_t at, const PrefixJoin& j, const float* o) {
+  uint4 z = make_uint4(0u, 0u, 0u, 0u), y;
+  if (j.theirs != 0.f) z = *reinterpret_cast<const uint4*>(a.own_out + at);
+  prefix_mix8(reinterpret_cast<uint32_t*>(&y), j, o, z);
+  *reinterpret_cast<uint4*>(a.out + at) = y;
 }
 
 }  // namespace

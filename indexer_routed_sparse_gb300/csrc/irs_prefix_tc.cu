@@ -20,10 +20,14 @@
 //   where pages are not multiples of 8 positions, and for the positions behind the last whole
 //   chunk of a prefix, by 16-byte copies with zeros behind the end: no position past it is read,
 //   and 0 times whatever its value holds is never formed.
-// * S[128 x block] = Q K^T lies in TMEM; the weights return over it as bf16 and are the first operand
-//   of O += P V straight from TMEM. A thread has a row. The running maximum is raised only where a
-//   row's weights under it sum past 2^8, so that a block's scores are read once and O is hardly
-//   ever rescaled; the sums are FP32.
+// * S[128 x block] = Q K^T lies in TMEM, and the weights return beside it as bf16, the first operand of
+//   O += P V straight from TMEM. A thread has a row: it takes a block's scores into registers, which
+//   frees them for the next block's product, and works from there. With the weights over the scores a
+//   tile's next product waited for its whole softmax: 3440 cycles for 2 x 128 rows and 128 positions
+//   at 128 / 128, where the products take 2050.
+// * The running maximum is raised only where a score passes it by 2^8 (weights stay below 2^8 and sums,
+//   in FP32, far from their limits), so O is hardly ever rescaled in TMEM.
+// * A weight is rounded once to bf16, as the operand that the tensor cores take.
 #include <climits>
 
 #include "irs_internal.h"
@@ -37,28 +41,30 @@ namespace {
 
 constexpr int kRows = 128;              // rows a tile
 constexpr uint32_t kAtom = 128 * 128;   // 128 rows x 64 bf16
-// warps 0-3, 4-7: softmax of the two tiles, a thread a row; 8: plan, queries and keys; 9: values; 10, 11: products
+// warps 0-3, 4-7: softmax of the two tiles, a thread a row; 8: list, queries and keys; 9: values; 10, 11: products
 // of the two tiles. Registers: 384 x 168 at launch, of which the softmax's threads take 208
 // and the others keep 88: 256 x 208 + 128 x 88 = 384 x 168.
 constexpr int kThreads = 384;
-constexpr float kRaise = 256.f;         // a row's weights of a block with a sum past this raise the maximum
+constexpr float kRaise = 8.f;           // a score (base 2) that passes the maximum by this raises it
 constexpr int kPlanReaders = 11;        // warps that read an item's plan
 
 template <int DQK, int DV>
 struct Cfg {
   static constexpr int QA = DQK / 64, VA = DV / 64;
-  static constexpr int BLK = prefix_block(DQK);            // positions a block
+  static constexpr int BLK = prefix_block(DV);             // positions a block
   static constexpr uint32_t q_bytes = QA * kAtom;          // one tile's queries
   static constexpr uint32_t atom = BLK * 128;              // BLK rows x 64 bf16
   static constexpr uint32_t k_bytes = QA * atom, v_bytes = VA * atom;
-  static constexpr int KS = DQK == 64 ? 4 : DQK == 128 ? 3 : 2;                    // stages of keys
-  static constexpr int VS = DQK == 64 ? (DV == 64 ? 4 : 3) : (DV == 64 ? 3 : 2);   // and values
+  static constexpr int KS = DQK < 128 ? 4 : DQK == 128 ? (DV == 64 ? 3 : 4) : (DV == 64 ? 2 : 3);   // stages of keys
+  static constexpr int VS = DQK < 192 ? 4 : 2;                                                      // and values
   static constexpr uint32_t k_off = 2 * q_bytes, v_off = k_off + KS * k_bytes;
   static constexpr uint32_t bar_off = v_off + VS * v_bytes;
-  static constexpr uint32_t plan_off = bar_off + 40 * 8 + 16;   // [4][8] the items' plans
+  static constexpr uint32_t plan_off = bar_off + 44 * 8 + 16;   // [4][8] the items' plans
   static constexpr uint32_t total = plan_off + 4 * 32;
   static_assert(total <= 232448, "227 KB");
-  static constexpr uint32_t S0 = 0, O0 = 256;              // TMEM: scores at 128 x, outputs at 256 + x DV
+  // TMEM: scores, weights, outputs of the two tiles
+  static constexpr uint32_t S0 = 0, P0 = 2 * BLK, PS = (BLK / 2 + 15) & ~15, O0 = 512 - 2 * DV;
+  static_assert(BLK % 16 == 0 && P0 + PS + BLK / 2 <= O0, "512 columns");
 };
 
 // D[128 x DV] (+)= P . V: P bf16 in TMEM, V a [position][dim] tile read MN-major; NK steps of 16 positions.
@@ -70,18 +76,14 @@ __device__ __forceinline__ void pv_run(uint32_t d, uint32_t p, uint32_t vb, uint
     umma_bf16_ts_warp(d, p + 8 * ks, b0 + (uint64_t)((ks * 2048) >> 4), idesc, (accumulate || ks > 0) ? 1u : 0u);
 }
 
-// A row's weights of a whole block, 2^(score * scale + off), as bf16 pairs, and their sum. The loads of the
-// second half run behind the first half's work. Written in the order of issue: a piece's exponentials, then the
-// sums and roundings of the piece before, so that a lone warp does not wait for each result in turn (pair by
-// pair a block took 2300 cycles).
+// A row's weights of a block, 2^(score * scale + off), as bf16 pairs, and their sum. Written in the order of
+// issue: a piece's exponentials, then the sums and roundings of the piece before, so that a lone warp does
+// not wait for each result in turn (pair by pair a block of 128 took 2300 cycles, so 770).
 template <int NP>
-__device__ __forceinline__ void row_weights(uint32_t s_addr, float scale, float off, uint32_t (&w)[NP][8], float& ln) {
-  constexpr int HP = NP / 2;
+__device__ __forceinline__ float row_weights(const float (&v)[NP][16], float scale, float off, uint32_t (&w)[NP][8]) {
   const uint64_t sc2 = pack2(scale, scale), off2 = pack2(off, off);
   uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};   // FP32 pairs
-  float v[NP][16], p[2][16];
-#pragma unroll
-  for (int c = 0; c < HP; ++c) tmem_ld16(s_addr + 16 * c, v[c]);
+  float p[2][16];
   auto finish = [&](int c) {
     float(&q)[16] = p[c & 1];
 #pragma unroll
@@ -94,17 +96,6 @@ __device__ __forceinline__ void row_weights(uint32_t s_addr, float scale, float 
   };
 #pragma unroll
   for (int c = 0; c < NP; ++c) {
-    if (c == 0 || c == HP) {
-      tmem_ld_wait();
-#pragma unroll
-      for (int k = c; k < c + HP; ++k)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) asm volatile("" : "+f"(v[k][i]));   // no use before the wait
-      if (c == 0) {
-#pragma unroll
-        for (int k = HP; k < NP; ++k) tmem_ld16(s_addr + 16 * k, v[k]);
-      }
-    }
     float z[16];
 #pragma unroll
     for (int i = 0; i < 16; i += 2) {
@@ -118,7 +109,7 @@ __device__ __forceinline__ void row_weights(uint32_t s_addr, float scale, float 
   }
   finish(NP - 1);
   const float2 s2 = unpack2(fadd2(fadd2(sum[0], sum[1]), fadd2(sum[2], sum[3])));
-  ln = s2.x + s2.y;
+  return s2.x + s2.y;
 }
 
 // Copies blocks of a prefix's keys or values into a ring; a whole warp.
@@ -240,7 +231,7 @@ struct Loader {
     for (int b = b0; b < b0 + nb; ++b) {
       const int valid = min(BLK, n - b * BLK), p = page, o = off;
       if (b + 1 < b0 + nb) look(b + 1);
-      if (!load(b * BLK, valid, (valid + 31) & ~31, p, o)) return false;
+      if (!load(b * BLK, valid, (valid + 15) & ~15, p, o)) return false;
     }
     announce(0);
     return true;
@@ -278,15 +269,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* k_empty = k_full + 4;
   uint64_t* v_full = k_empty + 4;         // [VS]
   uint64_t* v_empty = v_full + 4;
-  uint64_t* s_full = v_empty + 4;         // [2] a tile's scores; all its earlier products are done too
-  uint64_t* p_full = s_full + 2;          // [2] its weights
-  uint64_t* o_full = p_full + 2;          // [2] its output
-  uint64_t* o_empty = o_full + 2;         // [2]
-  uint64_t* turn = o_empty + 2;           // [2] the tile's products may be issued
-  uint64_t* drain = turn + 2;             // [2]
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + C::bar_off + 40 * 8);
+  uint64_t* s_full = v_empty + 4;         // [2] a tile's scores
+  uint64_t* s_free = s_full + 2;          // [2] they have been read
+  uint64_t* p_full = s_free + 2;          // [2] its weights
+  uint64_t* pv_done = p_full + 2;         // [2] they have been multiplied
+  uint64_t* o_empty = pv_done + 2;        // [2] its output has been read
+  uint64_t* drain = o_empty + 2;          // [2]
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + C::bar_off + 44 * 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
-  volatile int* start_g = reinterpret_cast<volatile int*>(tslot + 2);   // group that this CTA's run starts in
   volatile int* plan = reinterpret_cast<volatile int*>(smem + C::plan_off);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -298,63 +288,60 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < VS; ++i) { mbar_init(&v_full[i], 1); mbar_init(&v_empty[i], 2); }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&q_full[i], 1); mbar_init(&q_empty[i], 1);
-      mbar_init(&s_full[i], 1); mbar_init(&p_full[i], 4);
-      mbar_init(&o_full[i], 1); mbar_init(&o_empty[i], 4);
-      mbar_init(&turn[i], 1); mbar_init(&drain[i], 1);
+      mbar_init(&s_full[i], 1); mbar_init(&s_free[i], 4);
+      mbar_init(&p_full[i], 4); mbar_init(&pv_done[i], 1);
+      mbar_init(&o_empty[i], 4); mbar_init(&drain[i], 1);
     }
     *abort_flag = 0;
-    *start_g = -1;
     fence_mbar_init();
   }
   if (warp == 10) {
     tmem_alloc(tslot, 512);
     tmem_relinquish();
   }
-  // ---- the list of a head's blocks: its length, and where this CTA's run starts ----
-  int64_t* sums = reinterpret_cast<int64_t*>(smem);   // [kThreads / 32] + total + start, before the tiles are loaded
-  const int per = (a.P + kThreads - 1) / kThreads;
-  const int gs = min(a.P, tid * per), ge = min(a.P, gs + per);
-  int64_t mine = 0;
-  for (int g = gs; g < ge; ++g) mine += prefix_units(prefix_group(a, g), qt, BLK);
-  int64_t before = mine;
+  if (warp == 9 && lane == 0) {
+    tma_prefetch_map(&tm_q);
+    tma_prefetch_map(&tm_k);
+    tma_prefetch_map(&tm_v);
+  }
+  // ---- the list of a head's blocks: its length, and where this CTA's run starts (one warp) ----
+  PrefixGroup mine{0, 0, 0};              // the lane's group of the 32 from g0 on
+  int64_t units = 0, pre = 0, f0 = 0, f1 = 0;   // its blocks, the blocks before it; the run
+  int g0 = 0;
+  auto look = [&](int base, int64_t before) {   // groups base .. base + 31; returns the blocks up to their end
+    g0 = base;
+    mine = PrefixGroup{0, 0, 0};
+    if (base + lane < a.P) mine = prefix_group(a, base + lane);
+    units = prefix_units(mine, qt, BLK);
+    int64_t x = units;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, before, o);
-    if (lane >= o) before += y;
-  }
-  if (lane == 31) sums[warp] = before;
-  __syncthreads();
-  before -= mine;
-  int64_t total = 0;
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) before += sums[w];
-    total += sums[w];
-  }
-  const int64_t share = prefix_share(total, runs);
-  const int64_t f0 = run * share, f1 = min(total, f0 + share);
-  {
-    int64_t* pre = reinterpret_cast<int64_t*>(a.ws);
-    int64_t n = before;
-    for (int g = gs; g < ge; ++g) {
-      const int64_t next = n + prefix_units(prefix_group(a, g), qt, BLK);
-      if (blockIdx.x == 0) pre[g] = n;
-      if (f0 >= n && f0 < next) {
-        *start_g = g;
-        sums[kThreads / 32] = n;
-      }
-      n = next;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
     }
-    if (blockIdx.x == 0 && tid == 0) pre[a.P] = total;
+    pre = before + x - units;
+    return before + __shfl_sync(0xffffffffu, x, 31);
+  };
+  if (warp == 8) {
+    int64_t* sums = reinterpret_cast<int64_t*>(a.ws);
+    int64_t total = 0;
+    for (int base = 0; base < a.P; base += 32) {
+      total = look(base, total);
+      if (blockIdx.x == 0 && base + lane < a.P) sums[base + lane] = pre;
+    }
+    if (blockIdx.x == 0 && lane == 0) sums[a.P] = total;
+    const int64_t share = prefix_share(total, runs);
+    f0 = run * share;
+    f1 = min(total, f0 + share);
+    if (a.P > 32) {
+      int64_t before = 0;
+      for (int base = 0; base < a.P && before <= f0; base += 32) before = look(base, before);
+    }
   }
-  if (blockIdx.x == 0) prefix_check(a);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *tslot;
-  const int64_t start_pre = sums[kThreads / 32];
-  fence_proxy_async_smem();
-  __syncthreads();                        // the words are read before the first tile is loaded over them
-  const bool any = f0 < f1 && *start_g >= 0;
 
   auto wait_all = [&](uint64_t* bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, a.err));
@@ -381,199 +368,194 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   if (warp >= 8) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-  if (warp == 8) {
-    // ---------------- plan, queries and keys ----------------
-    Loader<C::QA, BLK, KS> ld{};
-    ld.map = &tm_k; ld.base = a.k + (int64_t)head * a.k_sh; ld.sp = a.k_sp; ld.stt = a.k_st;
-    ld.page_size = a.page_size; ld.num_pages = a.num_pages; ld.chunk = chunk; ld.head = head;
-    ld.full = k_full; ld.empty = k_empty; ld.smem_p = smem + C::k_off; ld.smem = smem_u32(smem) + C::k_off;
-    ld.abort_flag = abort_flag; ld.err = a.err; ld.lane = lane;
-    if (lane == 0) {
-      tma_prefetch_map(&tm_q);
-      tma_prefetch_map(&tm_k);
-      tma_prefetch_map(&tm_v);
-    }
-    uint32_t np = 0, nq[2] = {0, 0};
-    bool ok = true;
-    auto publish = [&](const Item& m) {
-      if (np >= 4 && !wait_all(&plan_empty[np & 3], ((np >> 2) - 1) & 1)) return false;
-      if (lane == 0) {
-        volatile int* pl = plan + 8 * (np & 3);
-        pl[0] = m.nb;
-        pl[1] = m.t0;
-        pl[2] = m.t1;
-        pl[3] = m.part;
-        pl[4] = m.b0;
-        pl[5] = m.n;
-        pl[6] = m.row;
-        mbar_arrive(&plan_full[np & 3]);
-      }
-      __syncwarp();
-      ++np;
-      return true;
-    };
-    auto load_q = [&](int x, const Item& m) {
-      if (nq[x] > 0 && !wait_all(&q_empty[x], (nq[x] - 1) & 1)) return false;
-      ++nq[x];
-      const int t = m.t0 + x * qt;
-      if (q_map) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp == 8) {
+      // ---------------- the list, queries and keys ----------------
+      Loader<C::QA, BLK, KS> ld{};
+      ld.map = &tm_k; ld.base = a.k + (int64_t)head * a.k_sh; ld.sp = a.k_sp; ld.stt = a.k_st;
+      ld.page_size = a.page_size; ld.num_pages = a.num_pages; ld.chunk = chunk; ld.head = head;
+      ld.full = k_full; ld.empty = k_empty; ld.smem_p = smem + C::k_off; ld.smem = smem_u32(smem) + C::k_off;
+      ld.abort_flag = abort_flag; ld.err = a.err; ld.lane = lane;
+      uint32_t np = 0, nq[2] = {0, 0};
+      bool ok = true;
+      auto publish = [&](const Item& m) {
+        if (np >= 4 && !wait_all(&plan_empty[np & 3], ((np >> 2) - 1) & 1)) return false;
         if (lane == 0) {
-          mbar_arrive_expect_tx(&q_full[x], (uint32_t)(qt * a.G) * 128u * C::QA);
-          for (int c = 0; c < C::QA; ++c)
-            tma_load_3d(smem + x * C::q_bytes + c * kAtom, &tm_q, c * 64, head * a.G, t, &q_full[x]);
+          volatile int* pl = plan + 8 * (np & 3);
+          pl[0] = m.nb;
+          pl[1] = m.t0;
+          pl[2] = m.t1;
+          pl[3] = m.part;
+          pl[4] = m.b0;
+          pl[5] = m.n;
+          pl[6] = m.row;
+          mbar_arrive(&plan_full[np & 3]);
         }
-      } else {
-        // rows by address: strides that no map can have
-        ld.announce(0);
-        const uint32_t dst = smem_u32(smem) + x * C::q_bytes;
-        const int c8 = lane & 7;
-        for (int r = lane >> 3; r < kRows; r += 4) {
-          const int tq = t + r / a.G;
-          const bool live = r < qt * a.G && tq < a.T;
-          const __nv_bfloat16* src = a.q + (live ? (int64_t)tq * a.q_st + (int64_t)(head * a.G + r % a.G) * a.q_sh : 0) + c8 * 8;
-          const uint32_t d = dst + (uint32_t)r * 128u + (uint32_t)((c8 ^ (r & 7)) << 4);
-#pragma unroll
-          for (int c = 0; c < C::QA; ++c) cp_async_16(d + c * kAtom, src + 64 * c, live ? 16u : 0u);
-        }
-        cp_async_commit();
-        cp_async_wait_pending(0);
-        fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&q_full[x]);
-      }
-      __syncwarp();
-      return true;
-    };
-    int g = any ? *start_g : 0;
-    int64_t pre = start_pre, f = f0;
-    while (any && ok && f < f1) {
-      const PrefixGroup grp = prefix_group(a, g);
-      const int64_t units = prefix_units(grp, qt, BLK);
-      if (f >= pre + units) {               // the next group that has any
-        pre += units;
-        if (++g >= a.P) break;              // not reached on a list of the right length
-        continue;
-      }
-      const int nbg = (grp.n + BLK - 1) / BLK;
-      const int pair = (int)((f - pre) / nbg);
-      Item m;
-      m.b0 = (int)((f - pre) - (int64_t)pair * nbg);
-      m.nb = (int)min(f1 - f, (int64_t)(nbg - m.b0));
-      m.t0 = grp.first + pair * 2 * qt;
-      m.t1 = grp.last;
-      m.part = m.nb == nbg ? 0 : f == f0 ? 1 : 2;
-      m.n = grp.n;
-      m.row = a.cache_lens != nullptr ? grp.first : g;
-      ok = publish(m) && load_q(0, m) && (m.t0 + qt >= m.t1 || load_q(1, m)) &&
-           ld.run(a.page_table + (int64_t)m.row * a.table_stride, m.b0, m.nb, m.n);
-      f += m.nb;
-    }
-    if (ok) {
-      Item end{};
-      publish(end);
-    }
-    ld.drain();
-    if (*abort_flag && q_map) {
-      for (int x = 0; x < 2; ++x)
-        if (nq[x] > 0) {
-          const unsigned long long w0 = globaltimer_ns();
-          while (!mbar_try_wait(&q_full[x], (nq[x] - 1) & 1) && globaltimer_ns() - w0 < kWaitLimitNs) {}
-        }
-    }
-  } else if (warp == 9) {
-    // ---------------- values ----------------
-    Loader<C::VA, BLK, VS> ld{};
-    ld.map = &tm_v; ld.base = a.v + (int64_t)head * a.v_sh; ld.sp = a.v_sp; ld.stt = a.v_st;
-    ld.page_size = a.page_size; ld.num_pages = a.num_pages; ld.chunk = chunk; ld.head = head;
-    ld.full = v_full; ld.empty = v_empty; ld.smem_p = smem + C::v_off; ld.smem = smem_u32(smem) + C::v_off;
-    ld.abort_flag = abort_flag; ld.err = a.err; ld.lane = lane;
-    Item m;
-    while (next_item(m))
-      if (!ld.run(a.page_table + (int64_t)m.row * a.table_stride, m.b0, m.nb, m.n)) break;
-    ld.drain();
-  } else {
-    // ---------------- the products of a tile (the whole warp; one elected lane issues) ----------------
-    // A turn is a tile's weights of the block before times their values, then its scores of the next block.
-    // The tiles take turns, so that one's softmax has the other's turn to run in. A warp each, because waits and
-    // commits cost the issuing warp 100 to 300 cycles apiece, which the other warp's products fill; and one
-    // commit a turn, whose reader releases the operands.
-    constexpr uint32_t PV_IDESC = idesc_bf16(kRows, DV, false, true);
-    const int x = uniform(warp - 10);
-    const uint32_t tb = (uint32_t)uniform((int)tbase), sb = smem_u32(smem);
-    const uint32_t s_tm = tb + C::S0 + 128 * x, o_tm = tb + C::O0 + x * DV;
-    const uint64_t q0 = sdesc_sw128(sb + x * C::q_bytes, 16, 1024);
-    uint32_t nq = 0, no = 0, np = 0, nt = 0, ks = 0, kph = 0, vs = 0, vph = 0;
-    bool alive = true;
-    Item m;
-    while (alive && next_item(m)) {
-      const int nb = uniform(m.nb), b0 = uniform(m.b0), n = uniform(m.n);
-      const bool two = m.t0 + qt < m.t1;
-      if (x == 1 && !two) {                    // an item of one tile: its blocks pass by, every phase in turn
-        for (int j = 0; j < nb && alive; ++j) {
-          alive = wait_all(&k_full[ks], kph) && wait_all(&v_full[vs], vph);
-          if (lane == 0) { mbar_arrive(&k_empty[ks]); mbar_arrive(&v_empty[vs]); }
-          __syncwarp();
-          if (++ks == (uint32_t)KS) { ks = 0; kph ^= 1u; }
-          if (++vs == (uint32_t)VS) { vs = 0; vph ^= 1u; }
-        }
-        continue;
-      }
-      if (!wait_all(&q_full[x], nq & 1)) break;
-      ++nq;
-      int cols = 0;
-      for (int j = 0; j <= nb; ++j) {
-        if (j < nb && !wait_all(&k_full[ks], kph)) { alive = false; break; }
-        if (j > 0 && !(wait_all(&v_full[vs], vph) && (j > 1 || no == 0 || wait_all(&o_empty[x], (no - 1) & 1)) &&
-                       wait_all(&p_full[x], np & 1))) { alive = false; break; }
-        if (two) {
-          if ((x == 1 || nt > 0) && !wait_all(&turn[x], (x == 1 ? nt : nt - 1) & 1)) { alive = false; break; }
-          ++nt;
-        }
-        tc_fence_after();
-        if (j > 0) {
-          const uint32_t vb = sb + C::v_off + vs * C::v_bytes;
-          switch (cols >> 5) {
-            case 1: pv_run<2>(o_tm, s_tm, vb, C::atom, PV_IDESC, j > 1); break;
-            case 2: pv_run<4>(o_tm, s_tm, vb, C::atom, PV_IDESC, j > 1); break;
-            case 3: pv_run<6>(o_tm, s_tm, vb, C::atom, PV_IDESC, j > 1); break;
-            default: pv_run<BLK / 16>(o_tm, s_tm, vb, C::atom, PV_IDESC, j > 1); break;
+        ++np;
+        return true;
+      };
+      auto load_q = [&](int x, const Item& m) {
+        if (nq[x] > 0 && !wait_all(&q_empty[x], (nq[x] - 1) & 1)) return false;
+        ++nq[x];
+        const int t = m.t0 + x * qt;
+        if (q_map) {
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&q_full[x], (uint32_t)(qt * a.G) * 128u * C::QA);
+            for (int c = 0; c < C::QA; ++c)
+              tma_load_3d(smem + x * C::q_bytes + c * kAtom, &tm_q, c * 64, head * a.G, t, &q_full[x]);
           }
-          ++np;
-          if (++vs == (uint32_t)VS) { vs = 0; vph ^= 1u; }
-        }
-        if (j < nb) {
-          cols = min(BLK, (n - (b0 + j) * BLK + 31) & ~31);
-          const uint32_t idesc = idesc_bf16(kRows, cols, false, false);
-          const uint64_t b = sdesc_sw128(sb + C::k_off + ks * C::k_bytes, 16, 1024);
+        } else {
+          // rows by address: strides that no map can have
+          ld.announce(0);
+          const uint32_t dst = smem_u32(smem) + x * C::q_bytes;
+          const int c8 = lane & 7;
+          for (int r = lane >> 3; r < kRows; r += 4) {
+            const int tq = t + r / a.G;
+            const bool live = r < qt * a.G && tq < a.T;
+            const __nv_bfloat16* src = a.q + (live ? (int64_t)tq * a.q_st + (int64_t)(head * a.G + r % a.G) * a.q_sh : 0) + c8 * 8;
+            const uint32_t d = dst + (uint32_t)r * 128u + (uint32_t)((c8 ^ (r & 7)) << 4);
 #pragma unroll
-          for (int i = 0; i < 4 * C::QA; ++i)
-            umma_bf16_warp(s_tm, q0 + (uint64_t)(((i >> 2) * kAtom + (i & 3) * 32) >> 4),
-                           b + (uint64_t)(((i >> 2) * C::atom + (i & 3) * 32) >> 4), idesc, i > 0);
-          if (++ks == (uint32_t)KS) { ks = 0; kph ^= 1u; }
+            for (int c = 0; c < C::QA; ++c) cp_async_16(d + c * kAtom, src + 64 * c, live ? 16u : 0u);
+          }
+          cp_async_commit();
+          cp_async_wait_pending(0);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&q_full[x]);
         }
-        if (two && lane == 0) mbar_arrive(&turn[x ^ 1]);
         __syncwarp();
-        umma_commit_warp(j < nb ? &s_full[x] : &o_full[x]);
+        return true;
+      };
+      int64_t f = f0;
+      while (ok && f < f1) {
+        const unsigned has = __ballot_sync(0xffffffffu, f >= pre && f < pre + units);
+        if (has == 0) {                       // a later group
+          if (g0 + 32 >= a.P) break;          // not reached on a list of the right length
+          const int64_t end = __shfl_sync(0xffffffffu, pre + units, 31);
+          look(g0 + 32, end);
+          continue;
+        }
+        const int src = __ffs((int)has) - 1;
+        const int first = __shfl_sync(0xffffffffu, mine.first, src), last = __shfl_sync(0xffffffffu, mine.last, src);
+        const int n = __shfl_sync(0xffffffffu, mine.n, src);
+        const int64_t before = __shfl_sync(0xffffffffu, pre, src);
+        const int nbg = (n + BLK - 1) / BLK;
+        const int pair = (int)((f - before) / nbg);
+        Item m;
+        m.b0 = (int)((f - before) - (int64_t)pair * nbg);
+        m.nb = (int)min(f1 - f, (int64_t)(nbg - m.b0));
+        m.t0 = first + pair * 2 * qt;
+        m.t1 = last;
+        m.part = m.nb == nbg ? 0 : f == f0 ? 1 : 2;
+        m.n = n;
+        m.row = a.cache_lens != nullptr ? first : g0 + src;
+        ok = publish(m) && load_q(0, m) && (m.t0 + qt >= m.t1 || load_q(1, m)) &&
+             ld.run(a.page_table + (int64_t)m.row * a.table_stride, m.b0, m.nb, m.n);
+        f += m.nb;
       }
-      ++no;
+      if (ok) {
+        Item end{};
+        publish(end);
+      }
+      ld.drain();
+      if (*abort_flag && q_map) {
+        for (int x = 0; x < 2; ++x)
+          if (nq[x] > 0) {
+            const unsigned long long w0 = globaltimer_ns();
+            while (!mbar_try_wait(&q_full[x], (nq[x] - 1) & 1) && globaltimer_ns() - w0 < kWaitLimitNs) {}
+          }
+      }
+    } else if (warp == 9) {
+      // ---------------- values ----------------
+      Loader<C::VA, BLK, VS> ld{};
+      ld.map = &tm_v; ld.base = a.v + (int64_t)head * a.v_sh; ld.sp = a.v_sp; ld.stt = a.v_st;
+      ld.page_size = a.page_size; ld.num_pages = a.num_pages; ld.chunk = chunk; ld.head = head;
+      ld.full = v_full; ld.empty = v_empty; ld.smem_p = smem + C::v_off; ld.smem = smem_u32(smem) + C::v_off;
+      ld.abort_flag = abort_flag; ld.err = a.err; ld.lane = lane;
+      Item m;
+      while (next_item(m))
+        if (!ld.run(a.page_table + (int64_t)m.row * a.table_stride, m.b0, m.nb, m.n)) break;
+      ld.drain();
+    } else {
+      // ---------------- the products of a tile (the whole warp; one elected lane issues) ----------------
+      // The scores of block j + 1, then the weights of block j times their values. A warp a tile, because
+      // waits and commits cost the issuing warp 100 to 300 cycles apiece, which the other's products fill. Its
+      // readers release the operands: a commit more a block costs as much again.
+      constexpr uint32_t PV_IDESC = idesc_bf16(kRows, DV, false, true);
+      const int x = uniform(warp - 10);
+      const uint32_t tb = (uint32_t)uniform((int)tbase), sb = smem_u32(smem);
+      const uint32_t s_tm = tb + C::S0 + BLK * x, p_tm = tb + C::P0 + C::PS * x, o_tm = tb + C::O0 + x * DV;
+      const uint64_t q0 = sdesc_sw128(sb + x * C::q_bytes, 16, 1024);
+      uint32_t nq = 0, no = 0, np = 0, nsc = 0, ks = 0, kph = 0, vs = 0, vph = 0;
+      bool alive = true;
+      Item m;
+      while (alive && next_item(m)) {
+        const int nb = uniform(m.nb), b0 = uniform(m.b0), n = uniform(m.n);
+        if (x == 1 && m.t0 + qt >= m.t1) {       // an item of one tile: its blocks pass by, every phase in turn
+          for (int j = 0; j < nb && alive; ++j) {
+            alive = wait_all(&k_full[ks], kph) && wait_all(&v_full[vs], vph);
+            if (lane == 0) { mbar_arrive(&k_empty[ks]); mbar_arrive(&v_empty[vs]); }
+            __syncwarp();
+            if (++ks == (uint32_t)KS) { ks = 0; kph ^= 1u; }
+            if (++vs == (uint32_t)VS) { vs = 0; vph ^= 1u; }
+          }
+          continue;
+        }
+        if (!wait_all(&q_full[x], nq & 1)) break;
+        ++nq;
+        for (int j = -1; j < nb; ++j) {
+          if (j + 1 < nb) {
+            if (!wait_all(&k_full[ks], kph) || (nsc > 0 && !wait_all(&s_free[x], (nsc - 1) & 1))) { alive = false; break; }
+            ++nsc;
+            tc_fence_after();
+            const uint32_t idesc = idesc_bf16(kRows, min(BLK, (n - (b0 + j + 1) * BLK + 15) & ~15), false, false);
+            const uint64_t b = sdesc_sw128(sb + C::k_off + ks * C::k_bytes, 16, 1024);
+#pragma unroll
+            for (int i = 0; i < 4 * C::QA; ++i)
+              umma_bf16_warp(s_tm, q0 + (uint64_t)(((i >> 2) * kAtom + (i & 3) * 32) >> 4),
+                             b + (uint64_t)(((i >> 2) * C::atom + (i & 3) * 32) >> 4), idesc, i > 0);
+            umma_commit_warp(&s_full[x]);
+            if (++ks == (uint32_t)KS) { ks = 0; kph ^= 1u; }
+          }
+          if (j >= 0) {
+            if (!(wait_all(&v_full[vs], vph) && (j > 0 || no == 0 || wait_all(&o_empty[x], (no - 1) & 1)) &&
+                  wait_all(&p_full[x], np & 1))) { alive = false; break; }
+            ++np;
+            tc_fence_after();
+            const uint32_t vb = sb + C::v_off + vs * C::v_bytes;
+            const int steps = (min(BLK, n - (b0 + j) * BLK) + 15) >> 4;
+            if (steps == BLK / 16) {
+              pv_run<BLK / 16>(o_tm, p_tm, vb, C::atom, PV_IDESC, j > 0);
+            } else {
+              for (int k = 0; k < steps; ++k) pv_run<1>(o_tm, p_tm + 8 * k, vb + 2048 * k, C::atom, PV_IDESC, j > 0 || k > 0);
+            }
+            umma_commit_warp(&pv_done[x]);
+            if (++vs == (uint32_t)VS) { vs = 0; vph ^= 1u; }
+          }
+        }
+        ++no;
+      }
+      // every issued product completes before the CTA releases its tensor memory
+      umma_commit_warp(&drain[x]);
+      const unsigned long long w0 = globaltimer_ns();
+      while (!mbar_try_wait(&drain[x], 0) && globaltimer_ns() - w0 < kWaitLimitNs) {}
+      __syncwarp();
     }
-    // every issued product completes before the CTA releases its tensor memory
-    umma_commit_warp(&drain[x]);
-    const unsigned long long w0 = globaltimer_ns();
-    while (!mbar_try_wait(&drain[x], 0) && globaltimer_ns() - w0 < kWaitLimitNs) {}
-    __syncwarp();
-  }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     // ---------------- softmax: warps 0-3 the first tile, 4-7 the second, a thread a row ----------------
+    if (blockIdx.x == 0 && warp == 7) prefix_check(a, lane, 32);
+    constexpr int NP = BLK / 16;                          // pieces of 16 columns
     const int x = warp >> 2;
     const int r = (warp & 3) * 32 + lane;                 // row of the tile = TMEM lane
     const int rq = r / a.G;                               // its token
     const int rel = rq * a.Hq + head * a.G + r - rq * a.G;   // its row of out, relative to the tile's first token's
-    const uint32_t s_addr = tbase + C::S0 + 128 * x + tmem_lane_base(warp);
+    const uint32_t s_addr = tbase + C::S0 + BLK * x + tmem_lane_base(warp);
+    const uint32_t p_addr = tbase + C::P0 + C::PS * x + tmem_lane_base(warp);
     const uint32_t o_addr = tbase + C::O0 + x * DV + tmem_lane_base(warp);
-    uint32_t ns = 0, no = 0, ks = 0, vs = 0;              // blocks, items; stages to release next
+    const bool release = (warp & 3) == 0 && lane == 0;    // says for the tile that operands are free
+    uint32_t ns = 0, nv = 0, ks = 0, vs = 0;              // blocks; products; stages to release next
     bool alive = true;
     Item m;
     while (alive && next_item(m)) {
@@ -584,67 +566,61 @@ __global__ void __launch_bounds__(kThreads, 1)
         continue;
       }
       const bool live = rq < qt && t < m.t1;
-      // Scores that are there say that the products before them are done: the tile's first warp then releases
-      // their operands.
-      const bool release = (warp & 3) == 0 && lane == 0;
-      auto free_stage = [&](uint64_t* empty, uint32_t& st, int stages) {
-        mbar_arrive(&empty[st]);
-        if (++st == (uint32_t)stages) st = 0;
+      auto multiplied = [&]() {                           // the weights of the block before are done with
+        if (!wait_all(&pv_done[x], nv & 1)) return false;
+        ++nv;
+        if (release) {
+          mbar_arrive(&v_empty[vs]);
+          if (++vs == (uint32_t)VS) vs = 0;
+        }
+        __syncwarp();
+        tc_fence_after();
+        return true;
       };
       float mx = -INFINITY, l = 0.f;
-      bool settled = false;                               // every row of the warp has a maximum
       for (int j = 0; j < m.nb; ++j) {
         const int left = m.n - (m.b0 + j) * BLK;          // positions from the block's first on
         if (!(alive = wait_all(&s_full[x], ns & 1))) break;
         ++ns;
+        tc_fence_after();
+        float v[NP][16];
+#pragma unroll
+        for (int c = 0; c < NP; ++c) tmem_ld16(s_addr + 16 * c, v[c]);
         if (release) {
-          free_stage(k_empty, ks, KS);
-          if (j > 0) free_stage(v_empty, vs, VS);
+          mbar_arrive(&k_empty[ks]);
+          if (++ks == (uint32_t)KS) ks = 0;
           if (j == m.nb - 1) mbar_arrive(&q_empty[x]);
         }
         __syncwarp();
-        tc_fence_after();
-        // The common case, one pass: the weights under the present maximum, and whether their sum passes
-        // 2^8. They wait in registers for the warp's vote.
-        constexpr int NP = BLK / 16;                      // pieces of 16 columns
-        bool slow = !settled || left < BLK;
-        if (!slow) {
-          uint32_t w[NP][8];
-          float ln = 0.f;
-          row_weights<NP>(s_addr, a.scale_log2, -mx, w, ln);
-          slow = __any_sync(0xffffffffu, live && ln > kRaise);   // a row that is none has no vote; NaN goes on
-          if (!slow) {
-            l += ln;
+        tmem_ld_wait();
 #pragma unroll
-            for (int c = 0; c < NP; ++c) tmem_st8(s_addr + 8 * c, reinterpret_cast<const float(&)[8]>(w[c]));
-          }
+        for (int c = 0; c < NP; ++c)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) asm volatile("" : "+f"(v[c][i]));   // no use before the wait
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_free[x]);
+        if (left < BLK) {                                 // the prefix ends inside: columns behind it are left from before
+#pragma unroll
+          for (int c = 0; c < NP; ++c)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[c][i] = 16 * c + i < left ? v[c][i] : -INFINITY;
         }
-        // An item's first block (no row has a maximum yet), a prefix's last (it may end inside) and blocks that
-        // raise a maximum: two passes.
-        if (slow) {
-          const int pieces = min(BLK, (left + 31) & ~31) >> 4;
-          auto scores = [&](int c, float (&v)[16]) {
-            tmem_ld16(s_addr + 16 * c, v);
-            tmem_ld_wait_regs(v);
-            if (left < 16 * c + 16) {
+        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-              for (int i = 0; i < 16; ++i) v[i] = 16 * c + i < left ? v[i] : -INFINITY;
-            }
-          };
-          float top = -INFINITY;
-#pragma unroll 1
-          for (int c = 0; c < pieces; ++c) {
-            float v[16];
-            scores(c, v);
+        for (int c = 0; c < NP; ++c)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) top = fmaxf(top, v[i]);
-          }
-          const float nm = fmaxf(mx, top * a.scale_log2);
+          for (int i = 0; i < 16; i += 2) top[(i >> 1) & 3] = fmaxf(top[(i >> 1) & 3], fmaxf(v[c][i], v[c][i + 1]));
+        const float tm = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.scale_log2;
+        bool waited = false;
+        if (__any_sync(0xffffffffu, live && tm > mx + kRaise)) {   // a row that is none has no vote
+          const float nm = fmaxf(mx, tm);
           const float f = nm == -INFINITY ? 1.f : ex2_approx(mx - nm);
           mx = nm;
           l *= f;
-          // O has every earlier product: these scores were issued behind them
-          if (j > 0 && __any_sync(0xffffffffu, f != 1.f)) {
+          if (j > 0) {
+            if (!(alive = multiplied())) break;
+            waited = true;
 #pragma unroll 1
             for (int d = 0; d < DV; d += 16) {
               float o[16];
@@ -655,48 +631,32 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_st16(o_addr + d, o);
             }
           }
-          const float off = mx == -INFINITY ? 0.f : -mx;
-#pragma unroll 1
-          for (int c = 0; c < pieces; ++c) {
-            float v[16];
-            uint32_t w[8];
-            scores(c, v);
-#pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-              const float p0 = ex2_approx(fmaf(v[i], a.scale_log2, off)), p1 = ex2_approx(fmaf(v[i + 1], a.scale_log2, off));
-              l += p0 + p1;
-              const __nv_bfloat162 b = __floats2bfloat162_rn(p0, p1);
-              w[i >> 1] = *reinterpret_cast<const uint32_t*>(&b);
-            }
-            tmem_st8(s_addr + 8 * c, reinterpret_cast<const float(&)[8]>(w));   // over columns that have been read
-          }
-          settled = __all_sync(0xffffffffu, !live || mx > -INFINITY);
         }
+        uint32_t w[NP][8];
+        l += row_weights<NP>(v, a.scale_log2, mx == -INFINITY ? 0.f : -mx, w);
+        if (j > 0 && !waited && !(alive = multiplied())) break;
+#pragma unroll
+        for (int c = 0; c < NP; ++c) tmem_st8(p_addr + 8 * c, reinterpret_cast<const float(&)[8]>(w[c]));
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[x]);
       }
+      if (!alive) break;
       // ---- the tile's rows ----
-      if (!alive || !(alive = wait_all(&o_full[x], no & 1))) break;
-      ++no;
-      if (release) free_stage(v_empty, vs, VS);
-      __syncwarp();
-      tc_fence_after();
-      if (l == 0.f) l = -1.f;                             // attended, and every score -inf: in a part, a finite maximum wipes it out
+      const bool sums = m.part != 0 || a.cache_lens != nullptr;   // FP32 sums, joined by the next kernel
+      const bool joined = !sums && live && a.own_out != nullptr;
       const int64_t row = (int64_t)t0 * a.Hq + rel;
-      if (m.part != 0 || a.cache_lens != nullptr) {
-        // a part, or the prefix's share of a decoding row: FP32, joined by the next kernel
-        float* dst;
-        float* ml;
-        if (m.part != 0) {
-          float* part = prefix_part(a, run, head, m.part - 1);
-          dst = part + (size_t)(x * kRows + r) * DV;
-          ml = part + kPrefixRows * DV + 2 * (x * kRows + r);
-        } else {
-          dst = prefix_rows(a) + row * DV;
-          ml = prefix_rows(a) + (size_t)a.T * a.Hq * DV + 2 * row;
-        }
+      uint4 own[DV / 8];                                  // the row's other part, fetched while the last products run
+      if (joined) {
+#pragma unroll
+        for (int i = 0; i < DV / 8; ++i) own[i] = *reinterpret_cast<const uint4*>(a.own_out + row * DV + 8 * i);
+      }
+      if (!(alive = multiplied())) break;
+      if (l == 0.f) l = -1.f;                             // attended, and every score -inf: in a part, a finite maximum wipes it out
+      if (sums) {
+        float* part = m.part != 0 ? prefix_part(a, run, head, m.part - 1) : prefix_rows(a);
+        const int64_t rows = m.part != 0 ? kPrefixRows : (int64_t)a.T * a.Hq, at = m.part != 0 ? x * kRows + r : row;
 #pragma unroll 1
         for (int d = 0; d < DV; d += 32) {
           float o[32];
@@ -704,21 +664,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld_wait_regs(o);
           if (live) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) *reinterpret_cast<float4*>(dst + d + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+            for (int i = 0; i < 32; i += 4) prefix_sums4(part, rows, at, d + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
           }
         }
-        if (live) *reinterpret_cast<float2*>(ml) = make_float2(mx, l);
+        if (live) prefix_sums_ml(part, rows, at, DV) = make_float2(mx, l);
       } else {
         const PrefixJoin jn = live ? prefix_join_own(a, row, mx, l) : PrefixJoin{0.f, 0.f, 0.f};
-#pragma unroll 1
+#pragma unroll
         for (int d = 0; d < DV; d += 32) {
           float o[32];
           tmem_ld32(o_addr + d, o);
           tmem_ld_wait_regs(o);
-          if (live) {
+          uint32_t w[16];
 #pragma unroll
-            for (int i = 0; i < 32; i += 8) prefix_store8(a, row * DV + d + i, jn, o + i);
-          }
+          for (int i = 0; i < 4; ++i) prefix_mix8(w + 4 * i, jn, o + 8 * i, own[d / 8 + i]);
+          store_rows32(w, a.out + (int64_t)t0 * a.Hq * DV + d, live ? rel : -1, DV, lane);
         }
         if (live && a.lse != nullptr) a.lse[row] = jn.lse;
       }
@@ -736,22 +696,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Prompts: joins the parts of the items that runs' borders cut, with the rows' other parts too, and
-// writes the rows of empty prefixes. A block takes 32 rows of the item that holds border blockIdx.x of
-// a head's list, if that is the item's first; eight columns a thread, four parts in flight.
+// writes the rows of empty prefixes. The borders that cut one item share its rows: 8 blocks a border, and
+// where these leave a block fewer than 32 rows, several groups of threads take a row's parts in
+// turn and are then joined in order. Neighbouring threads have neighbouring rows, as the sums lie.
 constexpr int kJoinThreads = 512;
 template <int DV>
 __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(PrefixArgs a, int runs) {
-  constexpr int CL = DV / 8, R = kJoinThreads / CL;   // threads a row, rows at a time
+  constexpr int CL = DV / 8;                          // threads a row, eight columns each
+  __shared__ float sm[kJoinThreads][9];
+  __shared__ float2 sm_ml[kJoinThreads];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int head = blockIdx.y, qt = kRows / a.G;
-  const int cl = threadIdx.x % CL, lane = threadIdx.x & 31;
-  const uint32_t row_mask = (CL == 16 ? 0xffffu : 0xffu) << (lane / CL * CL);
-  auto store = [&](int64_t row, float m, float l, const float* o) {
-    const PrefixJoin jn = prefix_join_own(a, row, m, l);
-    __syncwarp(row_mask);                             // lse may be own_lse: the row's threads have read it
-    if (cl == 0 && a.lse != nullptr) a.lse[row] = jn.lse;
-    prefix_store8(a, row * DV + 8 * cl, jn, o);
-  };
   const int64_t* pre = reinterpret_cast<const int64_t*>(a.ws);
   const int64_t total = pre[a.P], share = prefix_share(total, runs);
   const int64_t f = (int64_t)(blockIdx.x + 1) * share;
@@ -761,34 +716,60 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(PrefixArgs a,
     const int nbg = prefix_blocks(a, grp.n);
     const int pair = (int)((f - pre[g]) / nbg);
     const int64_t s = pre[g] + (int64_t)pair * nbg;
-    if (s != f && s >= f - share) {                   // cut, and by no earlier border
-      const int c0 = (int)blockIdx.x, c1 = (int)((s + nbg - 1) / share);
-      for (int r = blockIdx.z * 32 + threadIdx.x / CL; r < (int)blockIdx.z * 32 + 32; r += R) {
-        const int x = r / kRows, rr = r % kRows, rq = rr / a.G;
-        const int t = grp.first + pair * 2 * qt + x * qt + rq;
-        if (rq >= qt || t >= grp.last) continue;
-        PrefixSum<8> sum;
-        sum.clear();
+    if (s != f) {                                     // an item is cut here
+      const int c0 = (int)(s / share), c1 = (int)((s + nbg - 1) / share);   // its runs: borders c0 .. c1 - 1
+      const int blocks = (c1 - c0) * (int)gridDim.z, me = ((int)blockIdx.x - c0) * (int)gridDim.z + (int)blockIdx.z;
+      int rpb = 32;                                   // rows a block
+      while (rpb > 1 && rpb / 2 * blocks >= kPrefixRows) rpb /= 2;
+      const int row_in = threadIdx.x % rpb, cl = threadIdx.x / rpb % CL, part_grp = threadIdx.x / (rpb * CL);
+      const int pg = kJoinThreads / (rpb * CL);
+      const int r = me * rpb + row_in, x = r / kRows, rr = r % kRows, rq = rr / a.G;
+      const int t = grp.first + pair * 2 * qt + x * qt + rq;
+      const bool live = r < kPrefixRows && rq < qt && t < grp.last;
+      PrefixSum<8> sum;
+      sum.clear();
+      if (live) {
         constexpr int U = 4;
-        for (int c = c0; c <= c1; c += U) {
+        for (int c = c0 + part_grp; c <= c1; c += U * pg) {
           float2 ml[U];
           float o[U][8];
 #pragma unroll
           for (int u = 0; u < U; ++u) {
+            const int ci = c + u * pg;
             ml[u] = make_float2(-INFINITY, 0.f);
 #pragma unroll
             for (int k = 0; k < 8; ++k) o[u][k] = 0.f;
-            if (c + u <= c1) {
+            if (ci <= c1) {
               // the item's first part is its run's second, unless the run starts with it
-              const float* part = prefix_part(a, c + u, head, c + u == c0 && s != (int64_t)c0 * share ? 1 : 0);
-              ml[u] = *reinterpret_cast<const float2*>(part + kPrefixRows * DV + 2 * r);
-              prefix_load8(o[u], part + (size_t)r * DV + 8 * cl);
+              float* part = prefix_part(a, ci, head, ci == c0 && s != (int64_t)c0 * share ? 1 : 0);
+              ml[u] = prefix_sums_ml(part, kPrefixRows, r, DV);
+              prefix_sums8(o[u], part, kPrefixRows, r, 8 * cl);
             }
           }
 #pragma unroll
           for (int u = 0; u < U; ++u) sum.add(ml[u].x, ml[u].y, o[u]);
         }
-        store((int64_t)t * a.Hq + head * a.G + rr - rq * a.G, sum.m, sum.l, sum.o);
+      }
+      if (pg > 1) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) sm[threadIdx.x][k] = sum.o[k];
+        sm_ml[threadIdx.x] = make_float2(sum.m, sum.l);
+        __syncthreads();
+        if (part_grp == 0)
+          for (int i = threadIdx.x + rpb * CL; i < kJoinThreads; i += rpb * CL) {
+            float o[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) o[k] = sm[i][k];
+            sum.add(sm_ml[i].x, sm_ml[i].y, o);
+          }
+      }
+      const int64_t row = (int64_t)t * a.Hq + head * a.G + rr - rq * a.G;
+      const bool mine = live && part_grp == 0;
+      const PrefixJoin jn = mine ? prefix_join_own(a, row, sum.m, sum.l) : PrefixJoin{0.f, 0.f, 0.f};
+      __syncthreads();                                // lse may be own_lse: the row's threads have read it
+      if (mine) {
+        if (cl == 0 && a.lse != nullptr) a.lse[row] = jn.lse;
+        prefix_store8(a, row * DV + 8 * cl, jn, sum.o);
       }
     }
   }
@@ -796,33 +777,42 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(PrefixArgs a,
   for (int g = threadIdx.x; g < a.P; g += kJoinThreads) none |= prefix_group(a, g).n == 0;
   if (!__syncthreads_or(none)) return;
   const float zero[8] = {};
+  constexpr int R = kJoinThreads / CL;
+  const int cl = threadIdx.x % CL;
   const int64_t blocks = (int64_t)gridDim.x * gridDim.z, me = (int64_t)blockIdx.x * gridDim.z + blockIdx.z;
   for (int g = 0; g < a.P; ++g) {
     const PrefixGroup grp = prefix_group(a, g);
     if (grp.n != 0) continue;
     const int64_t rows = (int64_t)(grp.last - grp.first) * a.G;
-    for (int64_t r = me * R + threadIdx.x / CL; r < rows; r += blocks * R)
-      store((grp.first + r / a.G) * a.Hq + head * a.G + r % a.G, -INFINITY, 0.f, zero);
+    for (int64_t base = me * R; base < rows; base += blocks * R) {
+      const int64_t i = base + threadIdx.x / CL;
+      const int64_t row = (grp.first + i / a.G) * a.Hq + head * a.G + i % a.G;
+      const PrefixJoin jn = i < rows ? prefix_join_own(a, row, -INFINITY, 0.f) : PrefixJoin{0.f, 0.f, 0.f};
+      __syncthreads();
+      if (i < rows) {
+        if (cl == 0 && a.lse != nullptr) a.lse[row] = jn.lse;
+        prefix_store8(a, row * DV + 8 * cl, jn, zero);
+      }
+    }
   }
 }
 
 // Decoding: a row's parts over its group's prefix, then those over its own positions, joined in the
-// order of the two lists. A block takes the rows of one (sequence, KV head), eight columns a thread;
-// `pg` groups of threads share a row, each taking every pg-th part, and are then joined in order.
-constexpr int kStepThreads = 512;
+// order of the two lists. A block takes rows of one (sequence, KV head), eight columns a thread; `pg`
+// groups of threads share a row, each taking every pg-th part, and are then joined in order.
+constexpr int kStepThreads = 256;
 template <int DV>
 __global__ void __launch_bounds__(kStepThreads) prefix_step_join_kernel(PrefixArgs a, const uint8_t* own_ws, const float* own_rows, int runs, int workers) {
   constexpr int CL = DV / 8, groups = kStepThreads / CL;
   __shared__ float sm[kStepThreads][9];
-  __shared__ float2 sm_ml[groups];
+  __shared__ float2 sm_ml[kStepThreads];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int t = blockIdx.x / a.Hkv, head = blockIdx.x % a.Hkv;
-  const int cl = threadIdx.x % CL, grp = threadIdx.x / CL;
   const int g = prefix_group_of(a, t);
   PrefixGroup gr{0, 0, 0};
   if (g >= 0) gr = prefix_group(a, g);
   const bool live = prefix_length(a, t, gr.n) > 0;
-  // ---- the prefix's parts: runs c0 .. c1 of the head's list, or one row ----
+  // ---- the prefix's parts: runs c0 .. of the head's list, or one row ----
   const int qt = kRows / a.G;
   int c0 = 0, np = 0, first_slot = 0, x = 0, rq = 0;
   if (live && gr.n > 0) {
@@ -851,11 +841,13 @@ __global__ void __launch_bounds__(kStepThreads) prefix_step_join_kernel(PrefixAr
   }
   const float* own_parts = reinterpret_cast<const float*>(own_ws + paged_prefix_bytes(a.T));
   const int parts = np + no;
+  // four parts a thread, and no more rows at once than the KV head has
   int pg = 1;
-  while (2 * pg <= groups && 4 * pg < parts) pg *= 2;
-  const int part_grp = grp % pg, row_grp = grp / pg, rows = groups / pg;
+  while (2 * pg <= groups && (4 * pg < parts || groups / (2 * pg) >= a.G)) pg *= 2;
+  const int rows = groups / pg;
+  const int row_in = threadIdx.x % rows, cl = threadIdx.x / rows % CL, part_grp = threadIdx.x / (rows * CL);
   for (int rb = blockIdx.y * rows; rb < a.G; rb += gridDim.y * rows) {
-    const int h = rb + row_grp;                         // head of the KV head's
+    const int h = rb + row_in;                          // head of the KV head's
     const int64_t row = (int64_t)t * a.Hq + head * a.G + h;
     PrefixSum<8> sum;
     sum.clear();
@@ -873,11 +865,10 @@ __global__ void __launch_bounds__(kStepThreads) prefix_step_join_kernel(PrefixAr
           for (int k = 0; k < 8; ++k) o[u][k] = 0.f;
           if (i < parts) {
             if (i < np) {
-              const float* part = np == 1 ? prefix_rows(a) + row * DV
-                                          : prefix_part(a, c0 + i, head, i == 0 ? first_slot : 0) + (size_t)r * DV;
-              ml[u] = *reinterpret_cast<const float2*>(np == 1 ? prefix_rows(a) + (size_t)a.T * a.Hq * DV + 2 * row
-                                                               : part + (size_t)(kPrefixRows - r) * DV + 2 * r);
-              prefix_load8(o[u], part + 8 * cl);
+              float* part = np == 1 ? prefix_rows(a) : prefix_part(a, c0 + i, head, i == 0 ? first_slot : 0);
+              const int64_t n = np == 1 ? (int64_t)a.T * a.Hq : kPrefixRows, at = np == 1 ? row : r;
+              ml[u] = prefix_sums_ml(part, n, at, DV);
+              prefix_sums8(o[u], part, n, at, 8 * cl);
             } else if (no == 1) {
               ml[u] = *reinterpret_cast<const float2*>(own_rows + (size_t)a.T * a.Hq * DV + 2 * row);
               prefix_load8(o[u], own_rows + row * DV + 8 * cl);
@@ -896,14 +887,14 @@ __global__ void __launch_bounds__(kStepThreads) prefix_step_join_kernel(PrefixAr
     if (pg > 1) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) sm[threadIdx.x][k] = sum.o[k];
-      if (cl == 0) sm_ml[grp] = make_float2(sum.m, sum.l);
+      sm_ml[threadIdx.x] = make_float2(sum.m, sum.l);
       __syncthreads();
       if (part_grp == 0)
-        for (int i = 1; i < pg; ++i) {
+        for (int i = threadIdx.x + rows * CL; i < kStepThreads; i += rows * CL) {
           float o[8];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) o[k] = sm[threadIdx.x + i * CL][k];
-          sum.add(sm_ml[grp + i].x, sm_ml[grp + i].y, o);
+          for (int k = 0; k < 8; ++k) o[k] = sm[i][k];
+          sum.add(sm_ml[i].x, sm_ml[i].y, o);
         }
       __syncthreads();
     }
@@ -960,8 +951,8 @@ int prefix_runs(int Hkv, int num_sms) {
 
 }  // namespace
 
-int prefix_chunk(int Dqk, int page_size) {
-  int c = Dqk == 192 ? 32 : 128;   // a divisor of prefix_block(Dqk)
+int prefix_chunk(int Dv, int page_size) {
+  int c = Dv == 64 ? 128 : 16;   // a divisor of prefix_block(Dv)
   while (page_size % c != 0) c /= 2;
   return c < 8 ? 0 : c;
 }
