@@ -1329,7 +1329,7 @@ irs_status prefix_maps(irs::PrefixMaps* m, const irs::PrefixArgs& a) {
   irs_status s;
   m->has_q = (a.T == 1 || a.q_st > 0) && (a.Hq == 1 || a.q_sh > 0);
   if (m->has_q && (s = make_packed_map(&m->q, a.q, a.Dqk, a.Hq, a.T, a.q_sh, a.q_st, a.G, 128 / a.G)) != IRS_OK) return s;
-  m->chunk = irs::prefix_chunk(a.Dv, a.page_size);
+  m->chunk = irs::prefix_chunk(a.Dqk, a.page_size);
   if (m->chunk > 0) {
     bool k = false, v = false;
     if ((s = make_pool_map(&m->k, a.k, a.Dqk, a, a.k_sp, a.k_st, a.k_sh, m->chunk, &k)) != IRS_OK) return s;

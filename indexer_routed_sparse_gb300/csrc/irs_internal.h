@@ -240,7 +240,7 @@ struct PrefixMaps {
   int chunk;     // 0: no map, rows are copied by address
 };
 // Positions a TMA copy: the largest power of two that divides a page and a block of keys, if it is 8 or more.
-int prefix_chunk(int Dv, int page_size);
+int prefix_chunk(int Dqk, int page_size);
 constexpr int kPrefixKinds = 6;   // kernels, by head dims
 size_t prefix_workspace_bytes(int T, int P, int Hq, int Hkv, int Dv, bool decode);
 // configured, own_configured [kPrefixKinds]: whose shared-memory limit has been raised on this device

@@ -14,8 +14,9 @@ namespace irs {
 
 namespace {
 
-// Positions a block: both tiles' scores, weights (half as wide) and outputs lie in the 512 columns of TMEM.
-__host__ __device__ constexpr int prefix_block(int Dv) { return Dv == 64 ? 128 : 80; }
+// Positions a block: 128 columns of scores a product where shared memory has room for the stages; beside queries
+// of 192 dims it has for 96.
+__host__ __device__ constexpr int prefix_block(int Dqk) { return Dqk == 192 ? 96 : 128; }
 constexpr int kPrefixRows = 256;      // rows an item (two tiles)
 constexpr int kMaxPrefixCtas = 160;
 constexpr int kMinBlocks = 1;         // a run has at least this many blocks
@@ -55,7 +56,7 @@ __device__ __forceinline__ int64_t prefix_units(const PrefixGroup& g, int qt, in
   return (int64_t)((g.last - g.first + 2 * qt - 1) / (2 * qt)) * ((g.n + blk - 1) / blk);
 }
 __device__ __forceinline__ int prefix_blocks(const PrefixArgs& a, int n) {
-  const int blk = prefix_block(a.Dv);
+  const int blk = prefix_block(a.Dqk);
   return (n + blk - 1) / blk;
 }
 // Blocks of a run.

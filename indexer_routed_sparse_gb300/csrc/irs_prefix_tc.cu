@@ -20,11 +20,13 @@
 //   where pages are not multiples of 8 positions, and for the positions behind the last whole
 //   chunk of a prefix, by 16-byte copies with zeros behind the end: no position past it is read,
 //   and 0 times whatever its value holds is never formed.
-// * S[128 x block] = Q K^T lies in TMEM, and the weights return beside it as bf16, the first operand of
-//   O += P V straight from TMEM. A thread has a row: it takes a block's scores into registers, which
-//   frees them for the next block's product, and works from there. With the weights over the scores a
-//   tile's next product waited for its whole softmax: 3440 cycles for 2 x 128 rows and 128 positions
-//   at 128 / 128, where the products take 2050.
+// * S[128 x block] = Q K^T lies in TMEM; the weights return over it as bf16 and are the first operand
+//   of O += P V straight from TMEM. A thread has a row.
+// * The tiles' products take turns: what a tile waits for is its own softmax, which the other's
+//   products fill. Left to themselves both tiles' products ran at once, and then both softmaxes.
+//   Blocks of 80 positions, whose weights find room beside the scores so that the next scores need
+//   not wait for them, were slower (128 / 128: 2450 cycles a block of 80 for 3440 a block of 128): what
+//   a softmax warp spends on a block of any size, its waits, loads and votes, is 1000 cycles.
 // * The running maximum is raised only where a score passes it by 2^8 (weights stay below 2^8 and sums,
 //   in FP32, far from their limits), so O is hardly ever rescaled in TMEM.
 // * A weight is rounded once to bf16, as the operand that the tensor cores take.
@@ -45,26 +47,28 @@ constexpr uint32_t kAtom = 128 * 128;   // 128 rows x 64 bf16
 // of the two tiles. Registers: 384 x 168 at launch, of which the softmax's threads take 208
 // and the others keep 88: 256 x 208 + 128 x 88 = 384 x 168.
 constexpr int kThreads = 384;
-constexpr float kRaise = 8.f;           // a score (base 2) that passes the maximum by this raises it
+constexpr float kRaise = 8.f, kRaiseSum = 256.f;   // a score (base 2) that passes the maximum by this, or half a block's weights with a sum past this, raise it
 constexpr int kPlanReaders = 11;        // warps that read an item's plan
 
 template <int DQK, int DV>
 struct Cfg {
   static constexpr int QA = DQK / 64, VA = DV / 64;
-  static constexpr int BLK = prefix_block(DV);             // positions a block
+  static constexpr int BLK = prefix_block(DQK);            // positions a block
   static constexpr uint32_t q_bytes = QA * kAtom;          // one tile's queries
   static constexpr uint32_t atom = BLK * 128;              // BLK rows x 64 bf16
   static constexpr uint32_t k_bytes = QA * atom, v_bytes = VA * atom;
-  static constexpr int KS = DQK < 128 ? 4 : DQK == 128 ? (DV == 64 ? 3 : 4) : (DV == 64 ? 2 : 3);   // stages of keys
-  static constexpr int VS = DQK < 192 ? 4 : 2;                                                      // and values
+  static constexpr int KS = DQK == 64 ? 4 : DQK == 128 ? 3 : 2;                    // stages of keys
+  static constexpr int VS = DQK == 64 ? (DV == 64 ? 4 : 3) : (DV == 64 ? 3 : 2);   // and values
+  // Whether a block's first half of weights is announced before its second: where a tile's softmax is longer than
+  // the other's products (2 x 1024 cycles a block at 128 / 128: 333 -> 318 us for three prefixes of 2000 to 8000);
+  // at 192 / 128 (2 x 1060 for 96 positions) the wait inside a turn costs more than it gains.
+  static constexpr bool SPLIT = DQK < 192;
   static constexpr uint32_t k_off = 2 * q_bytes, v_off = k_off + KS * k_bytes;
   static constexpr uint32_t bar_off = v_off + VS * v_bytes;
   static constexpr uint32_t plan_off = bar_off + 44 * 8 + 16;   // [4][8] the items' plans
   static constexpr uint32_t total = plan_off + 4 * 32;
   static_assert(total <= 232448, "227 KB");
-  // TMEM: scores, weights, outputs of the two tiles
-  static constexpr uint32_t S0 = 0, P0 = 2 * BLK, PS = (BLK / 2 + 15) & ~15, O0 = 512 - 2 * DV;
-  static_assert(BLK % 16 == 0 && P0 + PS + BLK / 2 <= O0, "512 columns");
+  static constexpr uint32_t S0 = 0, O0 = 256;              // TMEM: scores (and weights) at 128 x, outputs at 256 + x DV
 };
 
 // D[128 x DV] (+)= P . V: P bf16 in TMEM, V a [position][dim] tile read MN-major; NK steps of 16 positions.
@@ -76,11 +80,11 @@ __device__ __forceinline__ void pv_run(uint32_t d, uint32_t p, uint32_t vb, uint
     umma_bf16_ts_warp(d, p + 8 * ks, b0 + (uint64_t)((ks * 2048) >> 4), idesc, (accumulate || ks > 0) ? 1u : 0u);
 }
 
-// A row's weights of a block, 2^(score * scale + off), as bf16 pairs, and their sum. Written in the order of
-// issue: a piece's exponentials, then the sums and roundings of the piece before, so that a lone warp does
-// not wait for each result in turn (pair by pair a block of 128 took 2300 cycles, so 770).
-template <int NP>
-__device__ __forceinline__ float row_weights(const float (&v)[NP][16], float scale, float off, uint32_t (&w)[NP][8]) {
+// A row's weights of N pieces of a block, 2^(score * scale + off), as bf16 pairs, and their sum. Written in the
+// order of issue: a piece's exponentials, then the sums and roundings of the piece before, so that a lone warp
+// does not wait for each result in turn (pair by pair a block of 128 took 2300 cycles, so 770).
+template <int N>
+__device__ __forceinline__ float row_weights(const float (*v)[16], float scale, float off, uint32_t (&w)[N][8]) {
   const uint64_t sc2 = pack2(scale, scale), off2 = pack2(off, off);
   uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};   // FP32 pairs
   float p[2][16];
@@ -95,7 +99,7 @@ __device__ __forceinline__ float row_weights(const float (&v)[NP][16], float sca
     }
   };
 #pragma unroll
-  for (int c = 0; c < NP; ++c) {
+  for (int c = 0; c < N; ++c) {
     float z[16];
 #pragma unroll
     for (int i = 0; i < 16; i += 2) {
@@ -107,9 +111,15 @@ __device__ __forceinline__ float row_weights(const float (&v)[NP][16], float sca
     for (int i = 0; i < 16; ++i) asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(p[c & 1][i]) : "f"(z[i]));
     if (c > 0) finish(c - 1);
   }
-  finish(NP - 1);
+  finish(N - 1);
   const float2 s2 = unpack2(fadd2(fadd2(sum[0], sum[1]), fadd2(sum[2], sum[3])));
   return s2.x + s2.y;
+}
+// The largest of three.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 
 // Copies blocks of a prefix's keys or values into a ring; a whole warp.
@@ -269,12 +279,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* k_empty = k_full + 4;
   uint64_t* v_full = k_empty + 4;         // [VS]
   uint64_t* v_empty = v_full + 4;
-  uint64_t* s_full = v_empty + 4;         // [2] a tile's scores
-  uint64_t* s_free = s_full + 2;          // [2] they have been read
-  uint64_t* p_full = s_free + 2;          // [2] its weights
-  uint64_t* pv_done = p_full + 2;         // [2] they have been multiplied
-  uint64_t* o_empty = pv_done + 2;        // [2] its output has been read
-  uint64_t* drain = o_empty + 2;          // [2]
+  uint64_t* s_full = v_empty + 4;         // [2] a tile's scores; all its earlier products are done too
+  uint64_t* p_full = s_full + 2;          // [2][2] its weights, by halves of the block
+  uint64_t* o_full = p_full + 4;          // [2] its output
+  uint64_t* o_empty = o_full + 2;         // [2]
+  uint64_t* turn = o_empty + 2;           // [2] its products may be issued
+  uint64_t* drain = turn + 2;             // [2]
   uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + C::bar_off + 44 * 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
   volatile int* plan = reinterpret_cast<volatile int*>(smem + C::plan_off);
@@ -288,9 +298,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < VS; ++i) { mbar_init(&v_full[i], 1); mbar_init(&v_empty[i], 2); }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&q_full[i], 1); mbar_init(&q_empty[i], 1);
-      mbar_init(&s_full[i], 1); mbar_init(&s_free[i], 4);
-      mbar_init(&p_full[i], 4); mbar_init(&pv_done[i], 1);
-      mbar_init(&o_empty[i], 4); mbar_init(&drain[i], 1);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[2 * i], 4); mbar_init(&p_full[2 * i + 1], 4);
+      mbar_init(&o_full[i], 1); mbar_init(&o_empty[i], 4);
+      mbar_init(&turn[i], 1); mbar_init(&drain[i], 1);
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -479,20 +490,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       ld.drain();
     } else {
       // ---------------- the products of a tile (the whole warp; one elected lane issues) ----------------
-      // The scores of block j + 1, then the weights of block j times their values. A warp a tile, because
-      // waits and commits cost the issuing warp 100 to 300 cycles apiece, which the other's products fill. Its
-      // readers release the operands: a commit more a block costs as much again.
+      // A turn is a tile's weights of the block before times their values, then its scores of the next block. A
+      // warp a tile, because waits and commits cost the issuing warp 100 to 300 cycles apiece, which the other's
+      // products fill; and one commit a turn, whose readers release the operands.
       constexpr uint32_t PV_IDESC = idesc_bf16(kRows, DV, false, true);
+      constexpr int HS = BLK / 32;               // steps of 16 positions in half a block
       const int x = uniform(warp - 10);
       const uint32_t tb = (uint32_t)uniform((int)tbase), sb = smem_u32(smem);
-      const uint32_t s_tm = tb + C::S0 + BLK * x, p_tm = tb + C::P0 + C::PS * x, o_tm = tb + C::O0 + x * DV;
+      const uint32_t s_tm = tb + C::S0 + 128 * x, o_tm = tb + C::O0 + x * DV;
       const uint64_t q0 = sdesc_sw128(sb + x * C::q_bytes, 16, 1024);
-      uint32_t nq = 0, no = 0, np = 0, nsc = 0, ks = 0, kph = 0, vs = 0, vph = 0;
+      uint32_t nq = 0, no = 0, np = 0, nt = 0, ks = 0, kph = 0, vs = 0, vph = 0;
       bool alive = true;
       Item m;
       while (alive && next_item(m)) {
         const int nb = uniform(m.nb), b0 = uniform(m.b0), n = uniform(m.n);
-        if (x == 1 && m.t0 + qt >= m.t1) {       // an item of one tile: its blocks pass by, every phase in turn
+        const bool two = m.t0 + qt < m.t1;
+        if (x == 1 && !two) {                    // an item of one tile: its blocks pass by, every phase in turn
           for (int j = 0; j < nb && alive; ++j) {
             alive = wait_all(&k_full[ks], kph) && wait_all(&v_full[vs], vph);
             if (lane == 0) { mbar_arrive(&k_empty[ks]); mbar_arrive(&v_empty[vs]); }
@@ -504,35 +517,45 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!wait_all(&q_full[x], nq & 1)) break;
         ++nq;
-        for (int j = -1; j < nb; ++j) {
-          if (j + 1 < nb) {
-            if (!wait_all(&k_full[ks], kph) || (nsc > 0 && !wait_all(&s_free[x], (nsc - 1) & 1))) { alive = false; break; }
-            ++nsc;
-            tc_fence_after();
-            const uint32_t idesc = idesc_bf16(kRows, min(BLK, (n - (b0 + j + 1) * BLK + 15) & ~15), false, false);
+        for (int j = 0; j <= nb; ++j) {
+          if (j < nb && !wait_all(&k_full[ks], kph)) { alive = false; break; }
+          if (j > 0 && !(wait_all(&v_full[vs], vph) && (j > 1 || no == 0 || wait_all(&o_empty[x], (no - 1) & 1)) &&
+                         wait_all(&p_full[2 * x], np & 1))) { alive = false; break; }
+          if (two) {
+            if ((x == 1 || nt > 0) && !wait_all(&turn[x], (x == 1 ? nt : nt - 1) & 1)) { alive = false; break; }
+            ++nt;
+          }
+          tc_fence_after();
+          if (j > 0) {
+            const uint32_t vb = sb + C::v_off + vs * C::v_bytes;
+            const int steps = (min(BLK, n - (b0 + j - 1) * BLK) + 15) >> 4;
+            if (steps < 2 * HS) {
+              if (C::SPLIT && !wait_all(&p_full[2 * x + 1], np & 1)) { alive = false; break; }
+              tc_fence_after();
+              for (int k = 0; k < steps; ++k) pv_run<1>(o_tm, s_tm + 8 * k, vb + 2048 * k, C::atom, PV_IDESC, j > 1 || k > 0);
+            } else if constexpr (C::SPLIT) {
+              pv_run<HS>(o_tm, s_tm, vb, C::atom, PV_IDESC, j > 1);
+              if (!wait_all(&p_full[2 * x + 1], np & 1)) { alive = false; break; }
+              tc_fence_after();
+              pv_run<HS>(o_tm, s_tm + 8 * HS, vb + 2048 * HS, C::atom, PV_IDESC, true);
+            } else {
+              pv_run<2 * HS>(o_tm, s_tm, vb, C::atom, PV_IDESC, j > 1);
+            }
+            ++np;
+            if (++vs == (uint32_t)VS) { vs = 0; vph ^= 1u; }
+          }
+          if (j < nb) {
+            const uint32_t idesc = idesc_bf16(kRows, min(BLK, (n - (b0 + j) * BLK + 15) & ~15), false, false);
             const uint64_t b = sdesc_sw128(sb + C::k_off + ks * C::k_bytes, 16, 1024);
 #pragma unroll
             for (int i = 0; i < 4 * C::QA; ++i)
               umma_bf16_warp(s_tm, q0 + (uint64_t)(((i >> 2) * kAtom + (i & 3) * 32) >> 4),
                              b + (uint64_t)(((i >> 2) * C::atom + (i & 3) * 32) >> 4), idesc, i > 0);
-            umma_commit_warp(&s_full[x]);
             if (++ks == (uint32_t)KS) { ks = 0; kph ^= 1u; }
           }
-          if (j >= 0) {
-            if (!(wait_all(&v_full[vs], vph) && (j > 0 || no == 0 || wait_all(&o_empty[x], (no - 1) & 1)) &&
-                  wait_all(&p_full[x], np & 1))) { alive = false; break; }
-            ++np;
-            tc_fence_after();
-            const uint32_t vb = sb + C::v_off + vs * C::v_bytes;
-            const int steps = (min(BLK, n - (b0 + j) * BLK) + 15) >> 4;
-            if (steps == BLK / 16) {
-              pv_run<BLK / 16>(o_tm, p_tm, vb, C::atom, PV_IDESC, j > 0);
-            } else {
-              for (int k = 0; k < steps; ++k) pv_run<1>(o_tm, p_tm + 8 * k, vb + 2048 * k, C::atom, PV_IDESC, j > 0 || k > 0);
-            }
-            umma_commit_warp(&pv_done[x]);
-            if (++vs == (uint32_t)VS) { vs = 0; vph ^= 1u; }
-          }
+          if (two && lane == 0) mbar_arrive(&turn[x ^ 1]);
+          __syncwarp();
+          umma_commit_warp(j < nb ? &s_full[x] : &o_full[x]);
         }
         ++no;
       }
@@ -546,16 +569,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     // ---------------- softmax: warps 0-3 the first tile, 4-7 the second, a thread a row ----------------
     if (blockIdx.x == 0 && warp == 7) prefix_check(a, lane, 32);
-    constexpr int NP = BLK / 16;                          // pieces of 16 columns
+    constexpr int NP = BLK / 16, HP = NP / 2;             // pieces of 16 columns; in half a block
     const int x = warp >> 2;
     const int r = (warp & 3) * 32 + lane;                 // row of the tile = TMEM lane
     const int rq = r / a.G;                               // its token
     const int rel = rq * a.Hq + head * a.G + r - rq * a.G;   // its row of out, relative to the tile's first token's
-    const uint32_t s_addr = tbase + C::S0 + BLK * x + tmem_lane_base(warp);
-    const uint32_t p_addr = tbase + C::P0 + C::PS * x + tmem_lane_base(warp);
+    const uint32_t s_addr = tbase + C::S0 + 128 * x + tmem_lane_base(warp);
     const uint32_t o_addr = tbase + C::O0 + x * DV + tmem_lane_base(warp);
     const bool release = (warp & 3) == 0 && lane == 0;    // says for the tile that operands are free
-    uint32_t ns = 0, nv = 0, ks = 0, vs = 0;              // blocks; products; stages to release next
+    uint32_t ns = 0, no = 0, ks = 0, vs = 0;              // blocks, items; stages to release next
     bool alive = true;
     Item m;
     while (alive && next_item(m)) {
@@ -566,61 +588,111 @@ __global__ void __launch_bounds__(kThreads, 1)
         continue;
       }
       const bool live = rq < qt && t < m.t1;
-      auto multiplied = [&]() {                           // the weights of the block before are done with
-        if (!wait_all(&pv_done[x], nv & 1)) return false;
-        ++nv;
-        if (release) {
-          mbar_arrive(&v_empty[vs]);
-          if (++vs == (uint32_t)VS) vs = 0;
-        }
-        __syncwarp();
-        tc_fence_after();
-        return true;
+      auto free_values = [&]() {                          // the products before the scores (or output) that came are done
+        mbar_arrive(&v_empty[vs]);
+        if (++vs == (uint32_t)VS) vs = 0;
       };
       float mx = -INFINITY, l = 0.f;
+      bool settled = false;                               // every row of the warp has a maximum
       for (int j = 0; j < m.nb; ++j) {
         const int left = m.n - (m.b0 + j) * BLK;          // positions from the block's first on
         if (!(alive = wait_all(&s_full[x], ns & 1))) break;
         ++ns;
         tc_fence_after();
-        float v[NP][16];
+        // The common case: the first half's weights under the present maximum, while the second half loads. Where
+        // a half's sum passes 2^8 (SPLIT: or a score of the second half passes the maximum by as much, which has to
+        // be known before the first half is announced), both are done again.
+        auto store_weights = [&](int c0, const uint32_t (&y)[HP][8]) {
 #pragma unroll
-        for (int c = 0; c < NP; ++c) tmem_ld16(s_addr + 16 * c, v[c]);
+          for (int c = 0; c < HP; ++c) tmem_st8(s_addr + 8 * (c0 + c), reinterpret_cast<const float(&)[8]>(y[c]));
+        };
+        auto announce = [&](int h) {                      // weights are there: a half's, or the block's
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[2 * x + h]);
+        };
+        bool slow = !settled || left < BLK;
+        float lo[HP][16], hi[HP][16];
+        uint32_t w[HP][8];
+        const float off = -mx;
+        if (!slow) {
+#pragma unroll
+          for (int c = 0; c < HP; ++c) tmem_ld16(s_addr + 16 * c, lo[c]);
+        }
         if (release) {
           mbar_arrive(&k_empty[ks]);
           if (++ks == (uint32_t)KS) ks = 0;
+          if (j > 0) free_values();
           if (j == m.nb - 1) mbar_arrive(&q_empty[x]);
         }
         __syncwarp();
-        tmem_ld_wait();
+        if (!slow) {
+          tmem_ld_wait();
 #pragma unroll
-        for (int c = 0; c < NP; ++c)
+          for (int c = 0; c < HP; ++c)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) asm volatile("" : "+f"(v[c][i]));   // no use before the wait
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s_free[x]);
-        if (left < BLK) {                                 // the prefix ends inside: columns behind it are left from before
+            for (int i = 0; i < 16; ++i) asm volatile("" : "+f"(lo[c][i]));   // no use before the wait
 #pragma unroll
-          for (int c = 0; c < NP; ++c)
+          for (int c = 0; c < HP; ++c) tmem_ld16(s_addr + 16 * (HP + c), hi[c]);
+          const float ln = row_weights<HP>(lo, a.scale_log2, off, w);
+          tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v[c][i] = 16 * c + i < left ? v[c][i] : -INFINITY;
+          for (int c = 0; c < HP; ++c)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) asm volatile("" : "+f"(hi[c][i]));
+          // a row that is none has no vote; NaN goes on
+          if constexpr (C::SPLIT) {
+            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int c = 0; c < HP; ++c)
+#pragma unroll
+              for (int i = 0; i < 16; i += 2) top[(i >> 1) & 3] = max3(top[(i >> 1) & 3], hi[c][i], hi[c][i + 1]);
+            const float tm = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.scale_log2;
+            slow = __any_sync(0xffffffffu, live && (ln > kRaiseSum || tm > mx + kRaise));
+            if (!slow) {
+              l += ln;
+              store_weights(0, w);
+              announce(0);
+              l += row_weights<HP>(hi, a.scale_log2, off, w);
+              store_weights(HP, w);
+            }
+          } else {
+            uint32_t u[HP][8];
+            const float hn = row_weights<HP>(hi, a.scale_log2, off, u);
+            slow = __any_sync(0xffffffffu, live && (ln > kRaiseSum || hn > kRaiseSum));
+            if (!slow) {
+              l += ln + hn;
+              store_weights(0, w);
+              store_weights(HP, u);
+            }
+          }
         }
-        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        // An item's first block (no row has a maximum yet), a prefix's last (it may end inside) and blocks that
+        // raise a maximum: two passes.
+        if (slow) {
+          const int pieces = (min(BLK, left) + 15) >> 4;
+          auto scores = [&](int c, float (&y)[16]) {
+            tmem_ld16(s_addr + 16 * c, y);
+            tmem_ld_wait_regs(y);
+            if (left < 16 * c + 16) {
 #pragma unroll
-        for (int c = 0; c < NP; ++c)
+              for (int i = 0; i < 16; ++i) y[i] = 16 * c + i < left ? y[i] : -INFINITY;
+            }
+          };
+          float top = -INFINITY;
+#pragma unroll 2
+          for (int c = 0; c < pieces; ++c) {
+            float y[16];
+            scores(c, y);
 #pragma unroll
-          for (int i = 0; i < 16; i += 2) top[(i >> 1) & 3] = fmaxf(top[(i >> 1) & 3], fmaxf(v[c][i], v[c][i + 1]));
-        const float tm = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.scale_log2;
-        bool waited = false;
-        if (__any_sync(0xffffffffu, live && tm > mx + kRaise)) {   // a row that is none has no vote
-          const float nm = fmaxf(mx, tm);
+            for (int i = 0; i < 16; i += 2) top = max3(top, y[i], y[i + 1]);
+          }
+          const float nm = fmaxf(mx, top * a.scale_log2);
           const float f = nm == -INFINITY ? 1.f : ex2_approx(mx - nm);
           mx = nm;
           l *= f;
-          if (j > 0) {
-            if (!(alive = multiplied())) break;
-            waited = true;
+          if (j > 0 && __any_sync(0xffffffffu, f != 1.f)) {   // O has every earlier product: these scores were issued behind them
 #pragma unroll 1
             for (int d = 0; d < DV; d += 16) {
               float o[16];
@@ -631,28 +703,38 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_st16(o_addr + d, o);
             }
           }
+          const float o2 = mx == -INFINITY ? 0.f : -mx;
+#pragma unroll 1
+          for (int c = 0; c < pieces; ++c) {
+            float y[1][16];
+            uint32_t u[1][8];
+            scores(c, y[0]);
+            l += row_weights<1>(y, a.scale_log2, o2, u);
+            tmem_st8(s_addr + 8 * c, reinterpret_cast<const float(&)[8]>(u[0]));   // over columns that have been read
+          }
+          settled = __all_sync(0xffffffffu, !live || mx > -INFINITY);
         }
-        uint32_t w[NP][8];
-        l += row_weights<NP>(v, a.scale_log2, mx == -INFINITY ? 0.f : -mx, w);
-        if (j > 0 && !waited && !(alive = multiplied())) break;
-#pragma unroll
-        for (int c = 0; c < NP; ++c) tmem_st8(p_addr + 8 * c, reinterpret_cast<const float(&)[8]>(w[c]));
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[x]);
+        if (C::SPLIT && slow) announce(0);
+        announce(C::SPLIT ? 1 : 0);
       }
       if (!alive) break;
       // ---- the tile's rows ----
       const bool sums = m.part != 0 || a.cache_lens != nullptr;   // FP32 sums, joined by the next kernel
       const bool joined = !sums && live && a.own_out != nullptr;
       const int64_t row = (int64_t)t0 * a.Hq + rel;
-      uint4 own[DV / 8];                                  // the row's other part, fetched while the last products run
-      if (joined) {
+      uint4 own[2][4];                                    // 32 columns of the row's other part, fetched ahead
+      auto fetch = [&](uint4 (&o)[4], int d) {
+        if (joined) {
 #pragma unroll
-        for (int i = 0; i < DV / 8; ++i) own[i] = *reinterpret_cast<const uint4*>(a.own_out + row * DV + 8 * i);
-      }
-      if (!(alive = multiplied())) break;
+          for (int i = 0; i < 4; ++i) o[i] = *reinterpret_cast<const uint4*>(a.own_out + row * DV + d + 8 * i);
+        }
+      };
+      fetch(own[0], 0);
+      if (!(alive = wait_all(&o_full[x], no & 1))) break;
+      ++no;
+      if (release) free_values();
+      __syncwarp();
+      tc_fence_after();
       if (l == 0.f) l = -1.f;                             // attended, and every score -inf: in a part, a finite maximum wipes it out
       if (sums) {
         float* part = m.part != 0 ? prefix_part(a, run, head, m.part - 1) : prefix_rows(a);
@@ -674,10 +756,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int d = 0; d < DV; d += 32) {
           float o[32];
           tmem_ld32(o_addr + d, o);
+          if (d + 32 < DV) fetch(own[(d / 32 + 1) & 1], d + 32);
           tmem_ld_wait_regs(o);
           uint32_t w[16];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) prefix_mix8(w + 4 * i, jn, o + 8 * i, own[d / 8 + i]);
+          for (int i = 0; i < 4; ++i) prefix_mix8(w + 4 * i, jn, o + 8 * i, own[(d / 32) & 1][i]);
           store_rows32(w, a.out + (int64_t)t0 * a.Hq * DV + d, live ? rel : -1, DV, lane);
         }
         if (live && a.lse != nullptr) a.lse[row] = jn.lse;
@@ -696,12 +779,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Prompts: joins the parts of the items that runs' borders cut, with the rows' other parts too, and
-// writes the rows of empty prefixes. The borders that cut one item share its rows: 8 blocks a border, and
-// where these leave a block fewer than 32 rows, several groups of threads take a row's parts in
-// turn and are then joined in order. Neighbouring threads have neighbouring rows, as the sums lie.
-constexpr int kJoinThreads = 512;
+// writes the rows of empty prefixes. The borders that cut one item share its rows, kJoinBlocks blocks a border;
+// where a block has fewer than 32 rows, several groups of threads take a row's parts in turn and are then
+// joined in order. Neighbouring threads have neighbouring rows, as the sums lie.
+constexpr int kJoinThreads = 512, kJoinBlocks = 2;
 template <int DV>
-__global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(PrefixArgs a, int runs) {
+__global__ void __launch_bounds__(kJoinThreads, 2) prefix_join_kernel(PrefixArgs a, int runs) {
   constexpr int CL = DV / 8;                          // threads a row, eight columns each
   __shared__ float sm[kJoinThreads][9];
   __shared__ float2 sm_ml[kJoinThreads];
@@ -718,58 +801,61 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(PrefixArgs a,
     const int64_t s = pre[g] + (int64_t)pair * nbg;
     if (s != f) {                                     // an item is cut here
       const int c0 = (int)(s / share), c1 = (int)((s + nbg - 1) / share);   // its runs: borders c0 .. c1 - 1
-      const int blocks = (c1 - c0) * (int)gridDim.z, me = ((int)blockIdx.x - c0) * (int)gridDim.z + (int)blockIdx.z;
-      int rpb = 32;                                   // rows a block
+      const int blocks = (c1 - c0) * kJoinBlocks, me = ((int)blockIdx.x - c0) * kJoinBlocks + (int)blockIdx.z;
+      int rpb = kPrefixRows / kJoinBlocks;            // rows a block
       while (rpb > 1 && rpb / 2 * blocks >= kPrefixRows) rpb /= 2;
-      const int row_in = threadIdx.x % rpb, cl = threadIdx.x / rpb % CL, part_grp = threadIdx.x / (rpb * CL);
-      const int pg = kJoinThreads / (rpb * CL);
-      const int r = me * rpb + row_in, x = r / kRows, rr = r % kRows, rq = rr / a.G;
-      const int t = grp.first + pair * 2 * qt + x * qt + rq;
-      const bool live = r < kPrefixRows && rq < qt && t < grp.last;
-      PrefixSum<8> sum;
-      sum.clear();
-      if (live) {
-        constexpr int U = 4;
-        for (int c = c0 + part_grp; c <= c1; c += U * pg) {
-          float2 ml[U];
-          float o[U][8];
+      const int chunk = min(rpb, 32), pg = kJoinThreads / (chunk * CL);
+      const int row_in = threadIdx.x % chunk, cl = threadIdx.x / chunk % CL, part_grp = threadIdx.x / (chunk * CL);
+      const int64_t row0 = (int64_t)(grp.first + pair * 2 * qt) * a.Hq + head * a.G;
+      const int tokens = grp.last - grp.first - pair * 2 * qt;
+      const int slot0 = s != (int64_t)c0 * share ? 1 : 0;   // the item's first part is its run's second, unless the run starts with it
+      for (int r = me * rpb + row_in; r - row_in < (me + 1) * rpb; r += chunk) {
+        const int x = r / kRows, rr = r % kRows, rq = rr / a.G;
+        const bool live = r < kPrefixRows && rq < qt && x * qt + rq < tokens;
+        PrefixSum<8> sum;
+        sum.clear();
+        if (live) {
+          constexpr int U = 2;
+          for (int c = c0 + part_grp; c <= c1; c += U * pg) {
+            float2 ml[U];
+            float o[U][8];
 #pragma unroll
-          for (int u = 0; u < U; ++u) {
-            const int ci = c + u * pg;
-            ml[u] = make_float2(-INFINITY, 0.f);
+            for (int u = 0; u < U; ++u) {
+              const int ci = c + u * pg;
+              ml[u] = make_float2(-INFINITY, 0.f);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) o[u][k] = 0.f;
-            if (ci <= c1) {
-              // the item's first part is its run's second, unless the run starts with it
-              float* part = prefix_part(a, ci, head, ci == c0 && s != (int64_t)c0 * share ? 1 : 0);
-              ml[u] = prefix_sums_ml(part, kPrefixRows, r, DV);
-              prefix_sums8(o[u], part, kPrefixRows, r, 8 * cl);
+              for (int k = 0; k < 8; ++k) o[u][k] = 0.f;
+              if (ci <= c1) {
+                float* part = prefix_part(a, ci, head, ci == c0 ? slot0 : 0);
+                ml[u] = prefix_sums_ml(part, kPrefixRows, r, DV);
+                prefix_sums8(o[u], part, kPrefixRows, r, 8 * cl);
+              }
             }
-          }
 #pragma unroll
-          for (int u = 0; u < U; ++u) sum.add(ml[u].x, ml[u].y, o[u]);
+            for (int u = 0; u < U; ++u) sum.add(ml[u].x, ml[u].y, o[u]);
+          }
         }
-      }
-      if (pg > 1) {
+        if (pg > 1) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) sm[threadIdx.x][k] = sum.o[k];
-        sm_ml[threadIdx.x] = make_float2(sum.m, sum.l);
-        __syncthreads();
-        if (part_grp == 0)
-          for (int i = threadIdx.x + rpb * CL; i < kJoinThreads; i += rpb * CL) {
-            float o[8];
+          for (int k = 0; k < 8; ++k) sm[threadIdx.x][k] = sum.o[k];
+          sm_ml[threadIdx.x] = make_float2(sum.m, sum.l);
+          __syncthreads();
+          if (part_grp == 0)
+            for (int i = threadIdx.x + chunk * CL; i < kJoinThreads; i += chunk * CL) {
+              float o[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) o[k] = sm[i][k];
-            sum.add(sm_ml[i].x, sm_ml[i].y, o);
-          }
-      }
-      const int64_t row = (int64_t)t * a.Hq + head * a.G + rr - rq * a.G;
-      const bool mine = live && part_grp == 0;
-      const PrefixJoin jn = mine ? prefix_join_own(a, row, sum.m, sum.l) : PrefixJoin{0.f, 0.f, 0.f};
-      __syncthreads();                                // lse may be own_lse: the row's threads have read it
-      if (mine) {
-        if (cl == 0 && a.lse != nullptr) a.lse[row] = jn.lse;
-        prefix_store8(a, row * DV + 8 * cl, jn, sum.o);
+              for (int k = 0; k < 8; ++k) o[k] = sm[i][k];
+              sum.add(sm_ml[i].x, sm_ml[i].y, o);
+            }
+        }
+        const int64_t row = row0 + (int64_t)(x * qt + rq) * a.Hq + rr - rq * a.G;
+        const bool mine = live && part_grp == 0;
+        const PrefixJoin jn = mine ? prefix_join_own(a, row, sum.m, sum.l) : PrefixJoin{0.f, 0.f, 0.f};
+        __syncthreads();                              // lse may be own_lse: the row's threads have read it; and the sums
+        if (mine) {
+          if (cl == 0 && a.lse != nullptr) a.lse[row] = jn.lse;
+          prefix_store8(a, row * DV + 8 * cl, jn, sum.o);
+        }
       }
     }
   }
@@ -951,8 +1037,8 @@ int prefix_runs(int Hkv, int num_sms) {
 
 }  // namespace
 
-int prefix_chunk(int Dv, int page_size) {
-  int c = Dv == 64 ? 128 : 16;   // a divisor of prefix_block(Dv)
+int prefix_chunk(int Dqk, int page_size) {
+  int c = Dqk == 192 ? 32 : 128;   // a divisor of prefix_block(Dqk)
   while (page_size % c != 0) c /= 2;
   return c < 8 ? 0 : c;
 }
@@ -968,7 +1054,7 @@ cudaError_t launch_prefix_fwd(const PrefixMaps& m, const PrefixArgs& a, int num_
   const cudaError_t e = launch_prefix_any(m, a, runs, configured, stream);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute at[1];
-  const cudaLaunchConfig_t cfg = early(dim3((unsigned)runs, (unsigned)a.Hkv, kPrefixRows / 32), kJoinThreads, stream, at);
+  const cudaLaunchConfig_t cfg = early(dim3((unsigned)runs, (unsigned)a.Hkv, kJoinBlocks), kJoinThreads, stream, at);
   return a.Dv == 64 ? cudaLaunchKernelEx(&cfg, prefix_join_kernel<64>, a, runs)
                     : cudaLaunchKernelEx(&cfg, prefix_join_kernel<128>, a, runs);
 }
