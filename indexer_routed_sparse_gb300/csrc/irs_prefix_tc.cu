@@ -47,7 +47,7 @@ constexpr uint32_t kAtom = 128 * 128;   // 128 rows x 64 bf16
 // of the two tiles. Registers: 384 x 168 at launch, of which the softmax's threads take 208
 // and the others keep 88: 256 x 208 + 128 x 88 = 384 x 168.
 constexpr int kThreads = 384;
-constexpr float kRaise = 8.f, kRaiseSum = 256.f;   // a score (base 2) that passes the maximum by this, or half a block's weights with a sum past this, raise it
+constexpr float kRaise = 256.f;         // half a block's weights of a row with a sum past this raise its maximum
 constexpr int kPlanReaders = 11;        // warps that read an item's plan
 
 template <int DQK, int DV>
@@ -59,10 +59,6 @@ struct Cfg {
   static constexpr uint32_t k_bytes = QA * atom, v_bytes = VA * atom;
   static constexpr int KS = DQK == 64 ? 4 : DQK == 128 ? 3 : 2;                    // stages of keys
   static constexpr int VS = DQK == 64 ? (DV == 64 ? 4 : 3) : (DV == 64 ? 3 : 2);   // and values
-  // Whether a block's first half of weights is announced before its second: where a tile's softmax is longer than
-  // the other's products (2 x 1024 cycles a block at 128 / 128: 333 -> 318 us for three prefixes of 2000 to 8000);
-  // at 192 / 128 (2 x 1060 for 96 positions) the wait inside a turn costs more than it gains.
-  static constexpr bool SPLIT = DQK < 192;
   static constexpr uint32_t k_off = 2 * q_bytes, v_off = k_off + KS * k_bytes;
   static constexpr uint32_t bar_off = v_off + VS * v_bytes;
   static constexpr uint32_t plan_off = bar_off + 44 * 8 + 16;   // [4][8] the items' plans
@@ -280,8 +276,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* v_full = k_empty + 4;         // [VS]
   uint64_t* v_empty = v_full + 4;
   uint64_t* s_full = v_empty + 4;         // [2] a tile's scores; all its earlier products are done too
-  uint64_t* p_full = s_full + 2;          // [2][2] its weights, by halves of the block
-  uint64_t* o_full = p_full + 4;          // [2] its output
+  uint64_t* p_full = s_full + 2;          // [2] its weights
+  uint64_t* o_full = p_full + 2;          // [2] its output
   uint64_t* o_empty = o_full + 2;         // [2]
   uint64_t* turn = o_empty + 2;           // [2] its products may be issued
   uint64_t* drain = turn + 2;             // [2]
@@ -298,8 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < VS; ++i) { mbar_init(&v_full[i], 1); mbar_init(&v_empty[i], 2); }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&q_full[i], 1); mbar_init(&q_empty[i], 1);
-      mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[2 * i], 4); mbar_init(&p_full[2 * i + 1], 4);
+      mbar_init(&s_full[i], 1); mbar_init(&p_full[i], 4);
       mbar_init(&o_full[i], 1); mbar_init(&o_empty[i], 4);
       mbar_init(&turn[i], 1); mbar_init(&drain[i], 1);
     }
@@ -494,7 +489,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       // warp a tile, because waits and commits cost the issuing warp 100 to 300 cycles apiece, which the other's
       // products fill; and one commit a turn, whose readers release the operands.
       constexpr uint32_t PV_IDESC = idesc_bf16(kRows, DV, false, true);
-      constexpr int HS = BLK / 32;               // steps of 16 positions in half a block
       const int x = uniform(warp - 10);
       const uint32_t tb = (uint32_t)uniform((int)tbase), sb = smem_u32(smem);
       const uint32_t s_tm = tb + C::S0 + 128 * x, o_tm = tb + C::O0 + x * DV;
@@ -519,27 +513,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++nq;
         for (int j = 0; j <= nb; ++j) {
           if (j < nb && !wait_all(&k_full[ks], kph)) { alive = false; break; }
-          if (j > 0 && !(wait_all(&v_full[vs], vph) && (j > 1 || no == 0 || wait_all(&o_empty[x], (no - 1) & 1)) &&
-                         wait_all(&p_full[2 * x], np & 1))) { alive = false; break; }
+          if (j > 0 && !(wait_all(&v_full[vs], vph) && (j > 1 || no == 0 || wait_all(&o_empty[x], (no - 1) & 1)))) { alive = false; break; }
+          // A wait costs 100 to 250 cycles even where nothing is waited for, so what comes last is waited for last:
+          // the weights, but at 192 dims, whose turns are longer than a softmax, the turn (294 against 306 us for
+          // three prefixes at 128 / 128; 3.53 against 3.59 ms for 8192 tokens over 16,384 positions at 192 / 128).
+          auto weights = [&]() { return j == 0 || wait_all(&p_full[x], np & 1); };
+          if (DQK == 192 && !weights()) { alive = false; break; }
           if (two) {
             if ((x == 1 || nt > 0) && !wait_all(&turn[x], (x == 1 ? nt : nt - 1) & 1)) { alive = false; break; }
             ++nt;
           }
+          if (DQK < 192 && !weights()) { alive = false; break; }
           tc_fence_after();
           if (j > 0) {
             const uint32_t vb = sb + C::v_off + vs * C::v_bytes;
             const int steps = (min(BLK, n - (b0 + j - 1) * BLK) + 15) >> 4;
-            if (steps < 2 * HS) {
-              if (C::SPLIT && !wait_all(&p_full[2 * x + 1], np & 1)) { alive = false; break; }
-              tc_fence_after();
-              for (int k = 0; k < steps; ++k) pv_run<1>(o_tm, s_tm + 8 * k, vb + 2048 * k, C::atom, PV_IDESC, j > 1 || k > 0);
-            } else if constexpr (C::SPLIT) {
-              pv_run<HS>(o_tm, s_tm, vb, C::atom, PV_IDESC, j > 1);
-              if (!wait_all(&p_full[2 * x + 1], np & 1)) { alive = false; break; }
-              tc_fence_after();
-              pv_run<HS>(o_tm, s_tm + 8 * HS, vb + 2048 * HS, C::atom, PV_IDESC, true);
+            if (steps == BLK / 16) {
+              pv_run<BLK / 16>(o_tm, s_tm, vb, C::atom, PV_IDESC, j > 1);
             } else {
-              pv_run<2 * HS>(o_tm, s_tm, vb, C::atom, PV_IDESC, j > 1);
+              for (int k = 0; k < steps; ++k) pv_run<1>(o_tm, s_tm + 8 * k, vb + 2048 * k, C::atom, PV_IDESC, j > 1 || k > 0);
             }
             ++np;
             if (++vs == (uint32_t)VS) { vs = 0; vph ^= 1u; }
@@ -600,18 +592,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++ns;
         tc_fence_after();
         // The common case: the first half's weights under the present maximum, while the second half loads. Where
-        // a half's sum passes 2^8 (SPLIT: or a score of the second half passes the maximum by as much, which has to
-        // be known before the first half is announced), both are done again.
-        auto store_weights = [&](int c0, const uint32_t (&y)[HP][8]) {
-#pragma unroll
-          for (int c = 0; c < HP; ++c) tmem_st8(s_addr + 8 * (c0 + c), reinterpret_cast<const float(&)[8]>(y[c]));
-        };
-        auto announce = [&](int h) {                      // weights are there: a half's, or the block's
-          tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&p_full[2 * x + h]);
-        };
+        // a half's sum passes 2^8 both are done again.
         bool slow = !settled || left < BLK;
         float lo[HP][16], hi[HP][16];
         uint32_t w[HP][8];
@@ -641,31 +622,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int c = 0; c < HP; ++c)
 #pragma unroll
             for (int i = 0; i < 16; ++i) asm volatile("" : "+f"(hi[c][i]));
+          uint32_t u[HP][8];
+          const float hn = row_weights<HP>(hi, a.scale_log2, off, u);
           // a row that is none has no vote; NaN goes on
-          if constexpr (C::SPLIT) {
-            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          slow = __any_sync(0xffffffffu, live && (ln > kRaise || hn > kRaise));
+          if (!slow) {
+            l += ln + hn;
 #pragma unroll
-            for (int c = 0; c < HP; ++c)
+            for (int c = 0; c < HP; ++c) tmem_st8(s_addr + 8 * c, reinterpret_cast<const float(&)[8]>(w[c]));
 #pragma unroll
-              for (int i = 0; i < 16; i += 2) top[(i >> 1) & 3] = max3(top[(i >> 1) & 3], hi[c][i], hi[c][i + 1]);
-            const float tm = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.scale_log2;
-            slow = __any_sync(0xffffffffu, live && (ln > kRaiseSum || tm > mx + kRaise));
-            if (!slow) {
-              l += ln;
-              store_weights(0, w);
-              announce(0);
-              l += row_weights<HP>(hi, a.scale_log2, off, w);
-              store_weights(HP, w);
-            }
-          } else {
-            uint32_t u[HP][8];
-            const float hn = row_weights<HP>(hi, a.scale_log2, off, u);
-            slow = __any_sync(0xffffffffu, live && (ln > kRaiseSum || hn > kRaiseSum));
-            if (!slow) {
-              l += ln + hn;
-              store_weights(0, w);
-              store_weights(HP, u);
-            }
+            for (int c = 0; c < HP; ++c) tmem_st8(s_addr + 8 * (HP + c), reinterpret_cast<const float(&)[8]>(u[c]));
           }
         }
         // An item's first block (no row has a maximum yet), a prefix's last (it may end inside) and blocks that
@@ -714,8 +680,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           settled = __all_sync(0xffffffffu, !live || mx > -INFINITY);
         }
-        if (C::SPLIT && slow) announce(0);
-        announce(C::SPLIT ? 1 : 0);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[x]);
       }
       if (!alive) break;
       // ---- the tile's rows ----
