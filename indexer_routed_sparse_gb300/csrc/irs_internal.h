@@ -293,8 +293,9 @@ struct PlanArgs {
   int32_t* free_left;
   int32_t* err;
   int B, P, max_pages, page_size, free_size, tokens;
+  int page_shift;              // set by launch_plan: log2 of page_size, or -1
 };
-cudaError_t launch_plan(const PlanArgs& a, int num_sms, cudaStream_t stream);
+cudaError_t launch_plan(PlanArgs a, int num_sms, cudaStream_t stream);
 
 // Attention of packed documents over a sliding window and the documents' first tokens.
 struct WinArgs {

@@ -12,7 +12,8 @@
 // Design. Every CTA sums over all sequences (a thread a run of them), so that nothing is handed from
 // one CTA to another and one launch does; a token finds its sequence among the 256 runs' sums in
 // shared memory and then inside the run. An entry that this call makes is worked out from the list of
-// free pages wherever it is needed, never read back from the table, so CTAs need no order.
+// free pages wherever it is needed, never read back from the table, so CTAs need no order. A thread
+// has four items in hand, so that their searches and loads run side by side.
 #include <climits>
 
 #include "irs_internal.h"
@@ -23,43 +24,45 @@ namespace irs {
 namespace {
 
 constexpr int kPlanThreads = 256;
+constexpr int kPlanItems = 4;        // items a thread has in hand
+constexpr int kPlanCached = 1024;    // sequences, and borders of groups, that a CTA keeps in shared memory; others are worked out again
 
 // What one sequence takes.
 struct PlanSeq {
   int n, m, held, need, shared;   // tokens, new ones; pages; entries that its group's first sequence gives
-  bool bad;
 };
 
 // The group of sequence b, or -1; *first its first sequence. Borders that fall or pass B are cut.
-__device__ __forceinline__ int plan_group(const PlanArgs& a, int b, int* first) {
-  int lo = 0, hi = a.P;   // cu[lo] <= b < cu[hi]
-  if (a.P == 0 || b < a.cu_groups[0] || b >= a.cu_groups[a.P]) return -1;
+__device__ __forceinline__ int plan_group(const int32_t* cu, int P, int b, int* first) {
+  if (P == 0 || b < cu[0] || b >= cu[P]) return -1;
+  int lo = 0, hi = P;   // cu[lo] <= b < cu[hi]
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (a.cu_groups[mid] <= b) lo = mid; else hi = mid;
+    if (cu[mid] <= b) lo = mid; else hi = mid;
   }
-  *first = min(max(a.cu_groups[lo], 0), b);
+  *first = min(max(cu[lo], 0), b);
   return lo;
 }
+__device__ __forceinline__ int plan_page(const PlanArgs& a, int pos) { return a.page_shift >= 0 ? pos >> a.page_shift : pos / a.page_size; }
 
-__device__ __forceinline__ PlanSeq plan_seq(const PlanArgs& a, int b) {
+__device__ __forceinline__ PlanSeq plan_seq(const PlanArgs& a, const int32_t* cu, int b, bool* bad) {
   PlanSeq s;
   const int reach = a.max_pages * a.page_size;   // at most 2^30
   s.n = __ldg(a.cache_lens + b);
   s.m = __ldg(a.new_lens + b);
-  s.bad = s.n < 0 || s.m < 0 || s.n > reach || s.m > reach - s.n;
   s.held = s.need = s.shared = 0;
-  if (s.bad) {
+  if (s.n < 0 || s.m < 0 || s.n > reach || s.m > reach - s.n) {
+    *bad = true;
     s.m = 0;
     return s;
   }
-  s.held = (s.n + a.page_size - 1) / a.page_size;
-  s.need = (s.n + s.m + a.page_size - 1) / a.page_size - s.held;
+  s.held = plan_page(a, s.n + a.page_size - 1);
+  s.need = plan_page(a, s.n + s.m + a.page_size - 1) - s.held;
   int first = 0;
-  const int g = plan_group(a, b, &first);
+  const int g = plan_group(cu, a.P, b, &first);
   if (g >= 0 && b > first) {
     const int n = __ldg(a.prefix_lens + g);
-    if (n > 0 && n <= s.n) s.shared = n / a.page_size;
+    if (n > 0 && n <= s.n) s.shared = plan_page(a, n);
   }
   return s;
 }
@@ -70,23 +73,33 @@ struct PlanSum {
 };
 
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
-  __shared__ PlanSum sums[kPlanThreads + 1];   // before each thread's run of sequences, and the whole
+  __shared__ PlanSum sums[kPlanThreads];       // before each thread's run of sequences
   __shared__ PlanSum warp_sums[kPlanThreads / 32];
+  __shared__ PlanSeq cached[kPlanCached];
+  __shared__ int32_t cached_cu[kPlanCached];
   __shared__ int sm_granted;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int per = (a.B + kPlanThreads - 1) / kPlanThreads;
   const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
   const int count = min(max(__ldg(a.free_count), 0), a.free_size);
-  int errors = 0;
+  const int32_t* cu = a.cu_groups;
+  if (a.P > 0 && a.P < kPlanCached) {
+    for (int i = tid; i <= a.P; i += kPlanThreads) cached_cu[i] = a.cu_groups[i];
+    cu = cached_cu;
+    __syncthreads();
+  }
+  bool bad = false;
+  auto seq = [&](int b) { return b < kPlanCached ? cached[b] : plan_seq(a, cu, b, &bad); };
 
   PlanSum n{0, 0, 0};
   for (int b = b0; b < b1; ++b) {
-    const PlanSeq s = plan_seq(a, b);
+    const PlanSeq s = plan_seq(a, cu, b, &bad);
+    if (b < kPlanCached) cached[b] = s;
     n.pages += s.need;
     n.tokens += s.m;
     n.shared += s.shared;
-    if (s.bad) errors |= IRS_DEVERR_PAGE;
   }
+  int errors = bad ? IRS_DEVERR_PAGE : 0;
   PlanSum x = n;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -97,23 +110,24 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
   if (lane == 31) warp_sums[warp] = x;
   if (tid == 0) sm_granted = 0;
   __syncthreads();
-  PlanSum base{x.pages - n.pages, x.tokens - n.tokens, x.shared - n.shared};
-  for (int w = 0; w < warp; ++w) {
-    base.pages += warp_sums[w].pages;
-    base.tokens += warp_sums[w].tokens;
-    base.shared += warp_sums[w].shared;
+  PlanSum base{x.pages - n.pages, x.tokens - n.tokens, x.shared - n.shared}, all{0, 0, 0};
+#pragma unroll
+  for (int w = 0; w < kPlanThreads / 32; ++w) {
+    const PlanSum s = warp_sums[w];
+    if (w < warp) { base.pages += s.pages; base.tokens += s.tokens; base.shared += s.shared; }
+    all.pages += s.pages;
+    all.tokens += s.tokens;
+    all.shared += s.shared;
   }
   sums[tid] = base;
-  if (tid == kPlanThreads - 1) sums[kPlanThreads] = PlanSum{base.pages + n.pages, base.tokens + n.tokens, base.shared + n.shared};
   __syncthreads();
-  const PlanSum all = sums[kPlanThreads];
 
   // ---- the small results, by the first CTA ----
   if (blockIdx.x == 0) {
     PlanSum at = base;
     int granted = 0;
     for (int b = b0; b < b1; ++b) {
-      const PlanSeq s = plan_seq(a, b);
+      const PlanSeq s = seq(b);
       a.cu_new[b] = (int)min(at.tokens, (int64_t)INT_MAX);
       const bool fits = s.need == 0 || at.pages + s.need <= count;
       if (!fits) errors |= IRS_DEVERR_PAGE;
@@ -127,10 +141,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
       a.cu_new[a.B] = (int)min(all.tokens, (int64_t)INT_MAX);
       if (all.tokens > a.tokens) errors |= IRS_DEVERR_CU_SEQLENS;
       if (count != *a.free_count) errors |= IRS_DEVERR_PAGE;
-      if (a.P > 0 && (a.cu_groups[0] != 0 || a.cu_groups[a.P] > a.B)) errors |= IRS_DEVERR_CU_SEQLENS;
+      if (a.P > 0 && (cu[0] != 0 || cu[a.P] > a.B)) errors |= IRS_DEVERR_CU_SEQLENS;
     }
     for (int g = tid; g < a.P; g += kPlanThreads) {
-      if (a.cu_groups[g + 1] < a.cu_groups[g]) errors |= IRS_DEVERR_CU_SEQLENS;
+      if (cu[g + 1] < cu[g]) errors |= IRS_DEVERR_CU_SEQLENS;
       if (a.prefix_lens[g] < 0) errors |= IRS_DEVERR_PAGE;
     }
     if (errors) record_error(a.err, errors);
@@ -140,19 +154,18 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
 
   // The sequence that holds item i of the pages, tokens or shared entries, and the sums before it.
   auto find = [&](int64_t i, int64_t PlanSum::*of, int PlanSeq::*own, PlanSeq& s, PlanSum& at) {
-    int lo = 0, hi = kPlanThreads;   // sums[lo] <= i < sums[hi]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (sums[mid].*of <= i) lo = mid; else hi = mid;
-    }
+    int lo = 0;   // the last run that starts at i or before
+#pragma unroll
+    for (int d = kPlanThreads / 2; d > 0; d >>= 1)
+      if (sums[lo + d].*of <= i) lo += d;
     at = sums[lo];
-    int b = lo * per;
-    s = plan_seq(a, b);
+    int b = min(lo * per, a.B - 1);
+    s = seq(b);
     while (i >= at.*of + s.*own && b < a.B - 1) {
       at.pages += s.need;
       at.tokens += s.m;
       at.shared += s.shared;
-      s = plan_seq(a, ++b);
+      s = seq(++b);
     }
     return b;
   };
@@ -164,52 +177,95 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
   };
   auto pages_before = [&](int b) {
     int64_t p = sums[b / per].pages;
-    for (int i = b / per * per; i < b; ++i) p += plan_seq(a, i).need;
+    for (int i = b / per * per; i < b; ++i) p += seq(i).need;
     return p;
   };
 
-  const int64_t step = (int64_t)gridDim.x * kPlanThreads, me = (int64_t)blockIdx.x * kPlanThreads + tid;
-  for (int64_t i = me; i < all.pages; i += step) {
-    PlanSeq s;
-    PlanSum at;
-    const int b = find(i, &PlanSum::pages, &PlanSeq::need, s, at);
-    const int j = s.held + (int)(i - at.pages);
-    a.page_table[(int64_t)b * a.table_stride + j] = entry(b, s, at.pages, j);
-  }
-  for (int64_t i = me; i < all.shared; i += step) {
-    PlanSeq s;
-    PlanSum at;
-    const int b = find(i, &PlanSum::shared, &PlanSeq::shared, s, at);
-    const int j = (int)(i - at.shared);
-    int first = 0;
-    plan_group(a, b, &first);
-    const PlanSeq f = plan_seq(a, first);
-    // entries that the first sequence has not, it does not give
-    if (j < f.held + f.need) a.page_table[(int64_t)b * a.table_stride + j] = entry(first, f, pages_before(first), j);
-  }
-  for (int64_t i = me; i < a.tokens; i += step) {
-    int pos = -1;
-    int64_t slot = -1;
-    if (i < all.tokens) {
-      PlanSeq s;
-      PlanSum at;
-      const int b = find(i, &PlanSum::tokens, &PlanSeq::m, s, at);
-      pos = s.n + (int)(i - at.tokens);
-      const int j = pos / a.page_size;
-      const int page = s.need > 0 && at.pages + s.need > count ? -1 : entry(b, s, at.pages, j);
-      if (page >= 0) slot = (int64_t)page * a.page_size + pos - j * a.page_size;
+  // A CTA takes kPlanItems x kPlanThreads items at a time, neighbouring threads neighbouring items.
+  constexpr int64_t kChunk = (int64_t)kPlanItems * kPlanThreads;
+  const int64_t step = gridDim.x * kChunk, me = blockIdx.x * kChunk + tid;
+  for (int64_t i0 = me; i0 < all.pages; i0 += step) {
+    int32_t* dst[kPlanItems];
+    int page[kPlanItems];
+#pragma unroll
+    for (int u = 0; u < kPlanItems; ++u) {
+      const int64_t i = i0 + u * kPlanThreads;
+      dst[u] = nullptr;
+      page[u] = -1;
+      if (i < all.pages) {
+        PlanSeq s;
+        PlanSum at;
+        const int b = find(i, &PlanSum::pages, &PlanSeq::need, s, at);
+        const int j = s.held + (int)(i - at.pages);
+        dst[u] = a.page_table + (int64_t)b * a.table_stride + j;
+        page[u] = entry(b, s, at.pages, j);
+      }
     }
-    a.positions[i] = pos;
-    a.slots[i] = slot;
+#pragma unroll
+    for (int u = 0; u < kPlanItems; ++u)
+      if (dst[u] != nullptr) *dst[u] = page[u];
+  }
+  for (int64_t i0 = me; i0 < all.shared; i0 += step) {
+    int32_t* dst[kPlanItems];
+    int page[kPlanItems];
+#pragma unroll
+    for (int u = 0; u < kPlanItems; ++u) {
+      const int64_t i = i0 + u * kPlanThreads;
+      dst[u] = nullptr;
+      page[u] = -1;
+      if (i < all.shared) {
+        PlanSeq s;
+        PlanSum at;
+        const int b = find(i, &PlanSum::shared, &PlanSeq::shared, s, at);
+        const int j = (int)(i - at.shared);
+        int first = 0;
+        plan_group(cu, a.P, b, &first);
+        const PlanSeq f = seq(first);
+        // entries that the first sequence has not, it does not give
+        if (j < f.held + f.need) {
+          dst[u] = a.page_table + (int64_t)b * a.table_stride + j;
+          page[u] = entry(first, f, j < f.held ? 0 : pages_before(first), j);
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kPlanItems; ++u)
+      if (dst[u] != nullptr) *dst[u] = page[u];
+  }
+  for (int64_t i0 = me; i0 < a.tokens; i0 += step) {
+    int pos[kPlanItems], page[kPlanItems];
+#pragma unroll
+    for (int u = 0; u < kPlanItems; ++u) {
+      const int64_t i = i0 + u * kPlanThreads;
+      pos[u] = page[u] = -1;
+      if (i < all.tokens && i < a.tokens) {
+        PlanSeq s;
+        PlanSum at;
+        const int b = find(i, &PlanSum::tokens, &PlanSeq::m, s, at);
+        pos[u] = s.n + (int)(i - at.tokens);
+        if (s.need == 0 || at.pages + s.need <= count) page[u] = entry(b, s, at.pages, plan_page(a, pos[u]));
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kPlanItems; ++u) {
+      const int64_t i = i0 + u * kPlanThreads;
+      if (i < a.tokens) {
+        a.positions[i] = pos[u];
+        a.slots[i] = page[u] < 0 ? -1 : (int64_t)page[u] * a.page_size + pos[u] - plan_page(a, pos[u]) * a.page_size;
+      }
+    }
   }
 }
 
 }  // namespace
 
-cudaError_t launch_plan(const PlanArgs& a, int num_sms, cudaStream_t stream) {
-  // a thread eight items; tables that are shared may have as many entries as they have places
+cudaError_t launch_plan(PlanArgs a, int num_sms, cudaStream_t stream) {
+  a.page_shift = -1;
+  if ((a.page_size & (a.page_size - 1)) == 0)
+    for (a.page_shift = 0; (1 << a.page_shift) < a.page_size; ++a.page_shift) {}
+  // tables that are shared may have as many entries as they have places
   const int64_t items = (int64_t)a.tokens + (a.P > 0 ? (int64_t)a.B * a.max_pages / 4 : 0);
-  int64_t grid = (items + 8 * kPlanThreads - 1) / (8 * kPlanThreads);
+  int64_t grid = (items + kPlanItems * kPlanThreads - 1) / (kPlanItems * kPlanThreads);
   grid = grid < 1 ? 1 : grid > 4 * num_sms ? 4 * num_sms : grid;
   plan_kernel<<<(unsigned)grid, kPlanThreads, 0, stream>>>(a);
   return cudaGetLastError();

@@ -147,7 +147,7 @@ struct Loader {
     bad = true;
     return num_pages;
   }
-  // Copied blocks that are not yet announced: all but `keep` (0 or 1) of them.
+  // Copied blocks that are not yet announced: all but `keep` of them.
   __device__ __forceinline__ void announce(uint32_t keep) {
     while (pending > keep) {
       cp_async_wait_pending(pending - 1);
@@ -157,42 +157,54 @@ struct Loader {
       --pending;
     }
   }
-  // Rows [r0, cols) of the block at position kb, those from `valid` on as zeros.
-  __device__ __forceinline__ void copy_rows(int kb, int r0, int valid, int cols, uint32_t dst) {
-    for (int r = r0; r < cols; r += 32) {
-      int64_t at = 0;
-      bool ok = r + lane < valid;
-      if (ok) {
-        int off;
-        const int page = page_of(kb + r + lane, off);
-        ok = page < num_pages;
-        at = ok ? (int64_t)page * sp + (int64_t)off * stt : 0;
-      }
-      const uint32_t m = __ballot_sync(0xffffffffu, ok);
-      const int c8 = lane & 7;
+  // Where the lane's row of rows r .. r + 31 of the block at position kb lies, or -1.
+  __device__ __forceinline__ int64_t row_at(int kb, int r, int valid) {
+    if (r + lane >= valid) return -1;
+    int off;
+    const int page = page_of(kb + r + lane, off);
+    return page < num_pages ? (int64_t)page * sp + (int64_t)off * stt : -1;
+  }
+  // Rows r .. r + 31 of a block, up to cols: eight lanes a row, four rows at a time; zeros where there is none.
+  __device__ __forceinline__ void copy_rows(int r, int64_t at, int cols, uint32_t dst) {
+    const int c8 = lane & 7;
 #pragma unroll 4
-      for (int i = 0; i < 8; ++i) {   // eight lanes a row, four rows at a time
-        const int k = 4 * i + (lane >> 3), rr = r + k;
-        const __nv_bfloat16* src = base + __shfl_sync(0xffffffffu, at, k) + c8 * 8;
-        const uint32_t n = (m >> k) & 1u ? 16u : 0u;
-        const uint32_t d = dst + (uint32_t)rr * 128u + (uint32_t)((c8 ^ (rr & 7)) << 4);
-        if (rr < cols) {
+    for (int i = 0; i < 8; ++i) {
+      const int k = 4 * i + (lane >> 3), rr = r + k;
+      const int64_t o = __shfl_sync(0xffffffffu, at, k);
+      const __nv_bfloat16* src = base + (o < 0 ? 0 : o) + c8 * 8;
+      const uint32_t d = dst + (uint32_t)rr * 128u + (uint32_t)((c8 ^ (rr & 7)) << 4);
+      if (rr < cols) {
 #pragma unroll
-          for (int c = 0; c < ATOMS; ++c) cp_async_16(d + c * atom, src + 64 * c, n);
-        }
+        for (int c = 0; c < ATOMS; ++c) cp_async_16(d + c * atom, src + 64 * c, o < 0 ? 0u : 16u);
       }
     }
   }
-  // The block at position kb: `valid` positions, zeros up to cols. chunk_page: of the lane's chunk.
-  __device__ __forceinline__ bool load(int kb, int valid, int cols, int chunk_page, int chunk_off) {
-    if (ns >= (uint32_t)ST) {
-      if (!__all_sync(0xffffffffu, mbar_test(&empty[st], ph ^ 1u))) {
-        announce(0);
-        if (!__all_sync(0xffffffffu, mbar_wait(&empty[st], ph ^ 1u, abort_flag, err))) return false;
-      }
-    }
-    const uint32_t dst = smem + st * bytes;
-    if (chunk > 0) {
+  // Waits for the next stage.
+  __device__ __forceinline__ bool stage() {
+    if (ns < (uint32_t)ST || __all_sync(0xffffffffu, mbar_test(&empty[st], ph ^ 1u))) return true;
+    announce(0);
+    return __all_sync(0xffffffffu, mbar_wait(&empty[st], ph ^ 1u, abort_flag, err));
+  }
+  __device__ __forceinline__ void advance() {
+    ++ns;
+    if (++st == (uint32_t)ST) { st = 0; ph ^= 1u; }
+  }
+  // The blocks [b0, b0 + nb) of a prefix of n positions. Pages are looked up a block ahead of the copies.
+  __device__ __forceinline__ bool run(const int32_t* table_row, int b0, int nb, int n) {
+    row = table_row;
+    return chunk > 0 ? run_chunks(b0, nb, n) : run_rows(b0, nb, n);
+  }
+  __device__ __forceinline__ bool run_chunks(int b0, int nb, int n) {
+    int page = 0, off = 0;
+    auto look = [&](int b) {   // the lane's chunk of block b
+      const int p = b * BLK + lane * chunk;
+      if (lane * chunk < BLK && p + chunk <= n) page = page_of(p, off);
+    };
+    look(b0);
+    for (int b = b0; b < b0 + nb; ++b) {
+      const int valid = min(BLK, n - b * BLK), cols = (valid + 15) & ~15, p = page, o = off;
+      if (b + 1 < b0 + nb) look(b + 1);
+      if (!stage()) return false;
       const int whole = valid / chunk;
       if (whole > 0) {
         if (lane == 0) mbar_expect_tx(&full[st], (uint32_t)(whole * chunk) * 128u * ATOMS);
@@ -200,11 +212,11 @@ struct Loader {
         if (lane < whole) {
           uint8_t* d = smem_p + st * bytes + (uint32_t)(lane * chunk) * 128u;
 #pragma unroll
-          for (int c = 0; c < ATOMS; ++c) tma_load_4d(d + c * atom, map, c * 64, chunk_off, head, chunk_page, &full[st]);
+          for (int c = 0; c < ATOMS; ++c) tma_load_4d(d + c * atom, map, c * 64, o, head, p, &full[st]);
         }
       }
       if (whole * chunk < cols) {
-        copy_rows(kb, whole * chunk, valid, cols, dst);
+        for (int r = whole * chunk; r < cols; r += 32) copy_rows(r, row_at(b * BLK, r, valid), cols, smem + st * bytes);
         cp_async_commit();
         cp_async_wait_pending(0);
         fence_proxy_async_smem();
@@ -212,32 +224,29 @@ struct Loader {
       __syncwarp();
       if (lane == 0) mbar_arrive(&full[st]);
       advance();
-    } else {
-      copy_rows(kb, 0, valid, cols, dst);
-      cp_async_commit();
-      ++pending;
-      advance();
-      announce(1);
     }
     return true;
   }
-  __device__ __forceinline__ void advance() {
-    ++ns;
-    if (++st == (uint32_t)ST) { st = 0; ph ^= 1u; }
-  }
-  // The blocks [b0, b0 + nb) of a prefix of n positions.
-  __device__ __forceinline__ bool run(const int32_t* table_row, int b0, int nb, int n) {
-    row = table_row;
-    int page = 0, off = 0;
-    auto look = [&](int b) {   // the lane's chunk of block b, a block ahead of its copy
-      const int p = b * BLK + lane * chunk;
-      if (chunk > 0 && lane * chunk < BLK && p + chunk <= n) page = page_of(p, off);
+  // Up to ST blocks are in flight; what has landed is announced when a block more has been issued, or the ring is full.
+  __device__ __forceinline__ bool run_rows(int b0, int nb, int n) {
+    constexpr int R = BLK / 32;
+    int64_t at[R];
+    auto look = [&](int b) {
+#pragma unroll
+      for (int i = 0; i < R; ++i) at[i] = row_at(b * BLK, 32 * i, min(BLK, n - b * BLK));
     };
     look(b0);
     for (int b = b0; b < b0 + nb; ++b) {
-      const int valid = min(BLK, n - b * BLK), p = page, o = off;
+      const int cols = (min(BLK, n - b * BLK) + 15) & ~15;
+      if (!stage()) return false;
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+        if (32 * i < cols) copy_rows(32 * i, at[i], cols, smem + st * bytes);
+      cp_async_commit();
+      ++pending;
+      advance();
       if (b + 1 < b0 + nb) look(b + 1);
-      if (!load(b * BLK, valid, (valid + 15) & ~15, p, o)) return false;
+      announce(ST - 1);
     }
     announce(0);
     return true;
