@@ -1005,18 +1005,19 @@ class PagedPlan(typing.NamedTuple):
     free_count: torch.Tensor   # int32 [1], pages still free
 
 
-def _packed(t: torch.Tensor, name: str, shape: tuple, index: int) -> int:
-    """The address of a contiguous int32 tensor of this shape."""
-    got, _ = _look(t, name, _I32, len(shape), index)
-    if tuple(got) != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 tensor {shape}, got {tuple(got)}")
+def _packed(t: torch.Tensor, name: str, n: int, index: int) -> int:
+    """The address of a contiguous int32 tensor [n]."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is _I32 and t.get_device() == index and t.shape == (n,)
+            and t.is_contiguous()):
+        got, _ = _look(t, name, _I32, 1, index)
+        raise ValueError(f"{name} must be a contiguous int32 tensor ({n},), got {tuple(got)}")
     return t.data_ptr()
 
 
 def _groups(cu: torch.Tensor, prefix_lens: torch.Tensor, name: str, index: int) -> tuple[int, int, int]:
     """(address of the borders, of the prefix lengths, number of groups)."""
     P = _look(prefix_lens, "prefix_lens", _I32, 1, index)[0][0]
-    return _packed(cu, name, (P + 1,), index), _packed(prefix_lens, "prefix_lens", (P,), index), P
+    return _packed(cu, name, P + 1, index), _packed(prefix_lens, "prefix_lens", P, index), P
 
 
 def paged_plan(cache_lens: torch.Tensor, new_lens: torch.Tensor, page_table: torch.Tensor, free_pages: torch.Tensor,
@@ -1038,29 +1039,34 @@ def paged_plan(cache_lens: torch.Tensor, new_lens: torch.Tensor, page_table: tor
     too few free pages gets none, keeps its length and sets DEVERR_PAGE.
     """
     index = _first(cache_lens, "cache_lens", _I32)
-    B = _look(cache_lens, "cache_lens", _I32, 1, index)[0][0]
-    lens, new = _packed(cache_lens, "cache_lens", (B,), index), _packed(new_lens, "new_lens", (B,), index)
+    (B,), _ = _look(cache_lens, "cache_lens", _I32, 1, index)
+    lens, new = _packed(cache_lens, "cache_lens", B, index), _packed(new_lens, "new_lens", B, index)
     (rows, max_pages), ts = _look(page_table, "page_table", _I32, 2, index)
     if rows != B:
         raise ValueError(f"page_table must have {B} rows, got {rows}")
     free = _look(free_pages, "free_pages", _I32, 1, index)[0][0]
-    _packed(free_pages, "free_pages", (free,), index)
+    free_at, count = _packed(free_pages, "free_pages", free, index), _packed(free_count, "free_count", 1, index)
     cu = pl = P = 0
-    if (cu_groups is None) != (prefix_lens is None):
-        raise ValueError("cu_groups and prefix_lens come together")
-    if cu_groups is not None:
+    if cu_groups is not None and prefix_lens is not None:
         cu, pl, P = _groups(cu_groups, prefix_lens, "cu_groups", index)
+    elif cu_groups is not prefix_lens:
+        raise ValueError("cu_groups and prefix_lens come together")
     if tokens < 0:
         raise ValueError("tokens must not be negative")
-    got = out if out is not None else (None,) * 5
-    got = PagedPlan(_result(got[0], "cu_new", (B + 1,), _I32, index), _result(got[1], "positions", (tokens,), _I32, index),
-                    _result(got[2], "slots", (tokens,), torch.int64, index), _result(got[3], "cache_lens", (B,), _I32, index),
-                    _result(got[4], "free_count", (1,), _I32, index))
+    if out is None:   # two allocations and a split: five allocations cost the host twice as much
+        whole = torch.empty(2 * B + 2 + tokens, dtype=_I32, device=index)
+        slots = torch.empty(tokens, dtype=torch.int64, device=index)
+        cu_new, lens_out, left, positions = whole.split_with_sizes((B + 1, B, 1, tokens))
+        out = PagedPlan(cu_new, positions, slots, lens_out, left)
+        at = whole.data_ptr()
+        to = (at, at + 4 * (2 * B + 2), slots.data_ptr(), at + 4 * (B + 1), at + 4 * (2 * B + 1))
+    else:
+        _result(out[2], "slots", (tokens,), torch.int64, index)
+        to = (_packed(out[0], "cu_new", B + 1, index), _packed(out[1], "positions", tokens, index), out[2].data_ptr(),
+              _packed(out[3], "cache_lens", B, index), _packed(out[4], "free_count", 1, index))
     _call(index, "paged_plan", lib().irs_paged_plan, lens, new, B, page_table.data_ptr(), ts[0], max_pages, page_size,
-          free_pages.data_ptr(), free, _packed(free_count, "free_count", (1,), index), cu, pl, P, tokens,
-          got.cu_new.data_ptr(), got.positions.data_ptr(), got.slots.data_ptr(), got.cache_lens.data_ptr(),
-          got.free_count.data_ptr(), _err(err, index))
-    return got
+          free_at, free, count, cu, pl, P, tokens, *to, _err(err, index))
+    return out
 
 
 @functools.lru_cache(maxsize=4096)

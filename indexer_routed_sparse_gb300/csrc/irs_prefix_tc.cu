@@ -644,26 +644,35 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         // An item's first block (no row has a maximum yet), a prefix's last (it may end inside) and blocks that
-        // raise a maximum: two passes.
+        // raise a maximum: all scores at once, the maximum, then the weights.
         if (slow) {
-          const int pieces = (min(BLK, left) + 15) >> 4;
-          auto scores = [&](int c, float (&y)[16]) {
-            tmem_ld16(s_addr + 16 * c, y);
-            tmem_ld_wait_regs(y);
-            if (left < 16 * c + 16) {
 #pragma unroll
-              for (int i = 0; i < 16; ++i) y[i] = 16 * c + i < left ? y[i] : -INFINITY;
+          for (int c = 0; c < HP; ++c) tmem_ld16(s_addr + 16 * c, lo[c]);
+#pragma unroll
+          for (int c = 0; c < HP; ++c) tmem_ld16(s_addr + 16 * (HP + c), hi[c]);
+          tmem_ld_wait();
+#pragma unroll
+          for (int c = 0; c < HP; ++c)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              asm volatile("" : "+f"(lo[c][i]));
+              asm volatile("" : "+f"(hi[c][i]));
             }
-          };
-          float top = -INFINITY;
-#pragma unroll 2
-          for (int c = 0; c < pieces; ++c) {
-            float y[16];
-            scores(c, y);
+          if (left < BLK) {                               // columns behind the end are left from before
 #pragma unroll
-            for (int i = 0; i < 16; i += 2) top = max3(top, y[i], y[i + 1]);
+            for (int c = 0; c < HP; ++c)
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                lo[c][i] = 16 * c + i < left ? lo[c][i] : -INFINITY;
+                hi[c][i] = 16 * (HP + c) + i < left ? hi[c][i] : -INFINITY;
+              }
           }
-          const float nm = fmaxf(mx, top * a.scale_log2);
+          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int c = 0; c < HP; ++c)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) top[i & 3] = max3(top[i & 3], lo[c][i], hi[c][i]);
+          const float nm = fmaxf(mx, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.scale_log2);
           const float f = nm == -INFINITY ? 1.f : ex2_approx(mx - nm);
           mx = nm;
           l *= f;
@@ -678,15 +687,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_st16(o_addr + d, o);
             }
           }
-          const float o2 = mx == -INFINITY ? 0.f : -mx;
-#pragma unroll 1
-          for (int c = 0; c < pieces; ++c) {
-            float y[1][16];
-            uint32_t u[1][8];
-            scores(c, y[0]);
-            l += row_weights<1>(y, a.scale_log2, o2, u);
-            tmem_st8(s_addr + 8 * c, reinterpret_cast<const float(&)[8]>(u[0]));   // over columns that have been read
-          }
+          const float now = mx == -INFINITY ? 0.f : -mx;
+          l += row_weights<HP>(lo, a.scale_log2, now, w);
+#pragma unroll
+          for (int c = 0; c < HP; ++c) tmem_st8(s_addr + 8 * c, reinterpret_cast<const float(&)[8]>(w[c]));
+          l += row_weights<HP>(hi, a.scale_log2, now, w);
+#pragma unroll
+          for (int c = 0; c < HP; ++c) tmem_st8(s_addr + 8 * (HP + c), reinterpret_cast<const float(&)[8]>(w[c]));
           settled = __all_sync(0xffffffffu, !live || mx > -INFINITY);
         }
         tmem_st_wait();
@@ -865,7 +872,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2) prefix_join_kernel(PrefixArgs
 // groups of threads share a row, each taking every pg-th part, and are then joined in order.
 constexpr int kStepThreads = 256;
 template <int DV>
-__global__ void __launch_bounds__(kStepThreads) prefix_step_join_kernel(PrefixArgs a, const uint8_t* own_ws, const float* own_rows, int runs, int workers) {
+__global__ void __launch_bounds__(kStepThreads, 4) prefix_step_join_kernel(PrefixArgs a, const uint8_t* own_ws, const float* own_rows, int runs, int workers) {
   constexpr int CL = DV / 8, groups = kStepThreads / CL;
   __shared__ float sm[kStepThreads][9];
   __shared__ float2 sm_ml[kStepThreads];
@@ -904,7 +911,7 @@ __global__ void __launch_bounds__(kStepThreads) prefix_step_join_kernel(PrefixAr
   }
   const float* own_parts = reinterpret_cast<const float*>(own_ws + paged_prefix_bytes(a.T));
   const int parts = np + no;
-  // four parts a thread, and no more rows at once than the KV head has
+  // up to four parts a thread, and no more rows at once than the KV head has
   int pg = 1;
   while (2 * pg <= groups && (4 * pg < parts || groups / (2 * pg) >= a.G)) pg *= 2;
   const int rows = groups / pg;
@@ -916,7 +923,7 @@ __global__ void __launch_bounds__(kStepThreads) prefix_step_join_kernel(PrefixAr
     sum.clear();
     if (h < a.G) {
       const int r = x * kRows + rq * a.G + h;
-      constexpr int U = 4;
+      constexpr int U = 2;
       for (int p = part_grp; p < parts; p += U * pg) {
         float2 ml[U];
         float o[U][8];
@@ -1058,7 +1065,7 @@ cudaError_t launch_prefix_decode(const PrefixMaps& m, const PrefixArgs& a, int n
   int workers = 0;
   if ((e = launch_paged_shared(o, num_sms, own_configured, &workers, stream)) != cudaSuccess) return e;
   const int64_t pairs = (int64_t)a.T * a.Hkv;
-  int y = (int)(2 * num_sms / pairs);
+  int y = (int)(8 * num_sms / pairs);   // blocks of four an SM, twice over: rows of many parts are taken one or two at a time
   y = y < 1 ? 1 : y > a.G ? a.G : y;
   cudaLaunchAttribute at[1];
   const cudaLaunchConfig_t cfg = early(dim3((unsigned)pairs, (unsigned)y), kStepThreads, stream, at);
