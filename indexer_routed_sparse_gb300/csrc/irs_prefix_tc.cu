@@ -135,7 +135,7 @@ struct Loader {
   volatile int* abort_flag;
   int32_t* err;
   int lane;
-  uint32_t st, ph, ns, pending;
+  uint32_t st, ph, ns;
   bool bad;
 
   static constexpr uint32_t atom = BLK * 128, bytes = ATOMS * atom;
@@ -148,16 +148,6 @@ struct Loader {
     if (page >= 0 && page < num_pages) return page;
     bad = true;
     return num_pages;
-  }
-  // Copied blocks that are not yet announced: all but `keep` of them.
-  __device__ __forceinline__ void announce(uint32_t keep) {
-    while (pending > keep) {
-      cp_async_wait_pending(pending - 1);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(full + (st + ST - pending) % ST);
-      --pending;
-    }
   }
   // The pages of the lane's rows (lane + 32 i) of the block at position kb; the lookups run side by side.
   static constexpr int R = BLK / 32;
@@ -194,9 +184,7 @@ struct Loader {
   }
   // Waits for the next stage.
   __device__ __forceinline__ bool stage() {
-    if (ns < (uint32_t)ST || __all_sync(0xffffffffu, mbar_test(&empty[st], ph ^ 1u))) return true;
-    announce(0);
-    return __all_sync(0xffffffffu, mbar_wait(&empty[st], ph ^ 1u, abort_flag, err));
+    return ns < (uint32_t)ST || __all_sync(0xffffffffu, mbar_wait(&empty[st], ph ^ 1u, abort_flag, err));
   }
   __device__ __forceinline__ void advance() {
     ++ns;
@@ -242,25 +230,22 @@ struct Loader {
     }
     return true;
   }
-  // Up to ST blocks are in flight; what has landed is announced when a block more has been issued, or the ring is full.
+  // Every lane's copies arrive on the stage's barrier when they have landed.
   __device__ __forceinline__ bool run_rows(int b0, int nb, int n) {
     int page[R], off[R];
     look_rows(b0 * BLK, min(BLK, n - b0 * BLK), page, off);
     for (int b = b0; b < b0 + nb; ++b) {
       if (!stage()) return false;
       copy_rows(0, min(BLK, n - b * BLK), page, off, smem + st * bytes);
-      cp_async_commit();
-      ++pending;
+      cp_async_mbar_arrive_noinc(&full[st]);
       advance();
       if (b + 1 < b0 + nb) look_rows((b + 1) * BLK, min(BLK, n - (b + 1) * BLK), page, off);
-      announce(ST - 1);
     }
-    announce(0);
     return true;
   }
   // Copies that are still in flight land before the CTA leaves.
   __device__ __forceinline__ void drain() {
-    cp_async_wait_pending(0);
+    asm volatile("cp.async.wait_all;" ::: "memory");
     if (*abort_flag) {
       for (uint32_t i = ns > (uint32_t)ST ? ns - ST : 0; i < ns; ++i) {
         const unsigned long long w0 = globaltimer_ns();
@@ -306,8 +291,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int qt = kRows / a.G;
   if (tid == 0) {
     for (int i = 0; i < 4; ++i) { mbar_init(&plan_full[i], 1); mbar_init(&plan_empty[i], kPlanReaders); }
-    for (int i = 0; i < KS; ++i) { mbar_init(&k_full[i], 1); mbar_init(&k_empty[i], 2); }
-    for (int i = 0; i < VS; ++i) { mbar_init(&v_full[i], 1); mbar_init(&v_empty[i], 2); }
+    for (int i = 0; i < KS; ++i) { mbar_init(&k_full[i], chunk > 0 ? 1 : 32); mbar_init(&k_empty[i], 2); }
+    for (int i = 0; i < VS; ++i) { mbar_init(&v_full[i], chunk > 0 ? 1 : 32); mbar_init(&v_empty[i], 2); }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&q_full[i], 1); mbar_init(&q_empty[i], 1);
       mbar_init(&s_full[i], 1); mbar_init(&p_full[i], 4);
@@ -430,8 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         } else {
           // rows by address: strides that no map can have
-          ld.announce(0);
-          const uint32_t dst = smem_u32(smem) + x * C::q_bytes;
+            const uint32_t dst = smem_u32(smem) + x * C::q_bytes;
           const int c8 = lane & 7;
           for (int r = lane >> 3; r < kRows; r += 4) {
             const int tq = t + r / a.G;
@@ -542,6 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++nt;
           }
           if (DQK < 192 && !weights()) { alive = false; break; }
+          if (chunk == 0) fence_proxy_async_smem();   // rows copied through the generic proxy
           tc_fence_after();
           if (j > 0) {
             const uint32_t vb = sb + C::v_off + vs * C::v_bytes;
