@@ -78,14 +78,13 @@ inline PagedGrid paged_grid(int Dqk, int Dv, int HK, int num_sms) {
   return g;
 }
 
-// The positions that sequence b's new token attends here; SHARED: those behind its group's prefix.
+// The positions that sequence b's new token attends here; SHARED: those behind the n that its group shares.
 template <bool SHARED>
-__device__ __forceinline__ PagedSet set_of(const PagedArgs& a, int b) {
+__device__ __forceinline__ PagedSet set_of(const PagedArgs& a, int b, int n) {
   const int L = __ldg(a.cache_lens + b);
   if constexpr (SHARED) {
     PagedSet s{};
-    const int n = prefix_positions(a.shared, b);
-    s.L = prefix_length(a.shared, b, n);
+    s.L = L < n || L > a.max_pages * a.page_size ? 0 : L;
     s.first = s.L > 0 ? n : 0;
     s.recent = s.n = s.L - s.first;
     return s;
@@ -93,10 +92,7 @@ __device__ __forceinline__ PagedSet set_of(const PagedArgs& a, int b) {
     return paged_set(a, L);
   }
 }
-template <bool SHARED>
-__device__ __forceinline__ int tiles_of(const PagedArgs& a, int b) {
-  return (set_of<SHARED>(a, b).n + kTile - 1) / kTile;
-}
+__device__ __forceinline__ int tiles_of(const PagedSet& s) { return (s.n + kTile - 1) / kTile; }
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -128,18 +124,24 @@ struct Cursor {
   int b, tile, nt;   // sequence, tile of it, its tile count
   PagedSet set;
 };
+// shared: how many positions sequence b shares with its group (kept for the first 32 kMaxWarps, else looked up).
 template <bool SHARED>
-__device__ __forceinline__ void cursor_open(const PagedArgs& a, Cursor& c) {
-  c.set = set_of<SHARED>(a, c.b);
-  c.nt = (c.set.n + kTile - 1) / kTile;
+__device__ __forceinline__ int shared_of(const PagedArgs& a, const int* shared, int b) {
+  if constexpr (SHARED) return b < 32 * kMaxWarps ? shared[b] : prefix_positions(a.shared, b);
+  else return 0;
+}
+template <bool SHARED>
+__device__ __forceinline__ void cursor_open(const PagedArgs& a, const int* shared, Cursor& c) {
+  c.set = set_of<SHARED>(a, c.b, shared_of<SHARED>(a, shared, c.b));
+  c.nt = tiles_of(c.set);
 }
 // Move on to the sequence that holds c.tile; the list must go on that far.
 template <bool SHARED>
-__device__ __forceinline__ void cursor_settle(const PagedArgs& a, Cursor& c) {
+__device__ __forceinline__ void cursor_settle(const PagedArgs& a, const int* shared, Cursor& c) {
   while (c.tile >= c.nt) {
     c.tile -= c.nt;
     if (++c.b >= a.B) { c.b = a.B - 1; c.tile = 0; return; }   // not reached on a list of the right length
-    cursor_open<SHARED>(a, c);
+    cursor_open<SHARED>(a, shared, c);
   }
 }
 
@@ -156,6 +158,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) paged_decode_kernel(PagedAr
   __shared__ int64_t scan[32 * kMaxWarps + 1];
   __shared__ int64_t start_pre[kMaxWarps];
   __shared__ int start_b[kMaxWarps];
+  __shared__ int shared[SHARED ? 32 * kMaxWarps : 1];
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -169,11 +172,14 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) paged_decode_kernel(PagedAr
   {
     int64_t n = 0;
     for (int b = bs; b < be; ++b) {
-      if (blockIdx.x == 0) {
-        const int L = __ldg(a.cache_lens + b);
-        if (SHARED ? L != 0 && set_of<SHARED>(a, b).L == 0 : L < 0 || L > a.max_pages * a.page_size) record_error(a.err, IRS_DEVERR_PAGE);
+      int prefix = 0;
+      if constexpr (SHARED) {
+        prefix = prefix_positions(a.shared, b);
+        if (b < 32 * kMaxWarps) shared[b] = prefix;
       }
-      n += tiles_of<SHARED>(a, b);
+      const PagedSet s = set_of<SHARED>(a, b, prefix);
+      if (blockIdx.x == 0 && s.L != __ldg(a.cache_lens + b)) record_error(a.err, IRS_DEVERR_PAGE);
+      n += tiles_of(s);
     }
     int64_t x = n;
 #pragma unroll
@@ -200,7 +206,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) paged_decode_kernel(PagedAr
     int64_t* pre = reinterpret_cast<int64_t*>(a.ws);
     int64_t n = scan[tid];
     for (int b = bs; b < be; ++b) {
-      const int64_t next = n + tiles_of<SHARED>(a, b);
+      const int64_t next = n + tiles_of(set_of<SHARED>(a, b, shared_of<SHARED>(a, shared, b)));
       if (blockIdx.x == 0) pre[b] = n;
       for (int w = 0; w < pg.per_head; ++w) {
         const int64_t f = (worker0 + w) * share;
@@ -223,7 +229,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) paged_decode_kernel(PagedAr
 
   Cursor cc;                                            // the tile being computed
   cc.b = start_b[sub];
-  cursor_open<SHARED>(a, cc);
+  cursor_open<SHARED>(a, shared, cc);
   cc.tile = (int)(f0 - start_pre[sub]);
 
   // ---- loads: A looks up positions or routes, B pages, C issues the copies ----
@@ -239,7 +245,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) paged_decode_kernel(PagedAr
     a_pos = -1;
     a_route = false;
     if (a_live) {
-      cursor_settle<SHARED>(a, lc);
+      cursor_settle<SHARED>(a, shared, lc);
       a_b = lc.b;
       int j = lc.tile * kTile + key;
       if (j < lc.set.n) {
@@ -319,7 +325,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) paged_decode_kernel(PagedAr
   int slot = 0;
   int64_t f = f0;
   while (f < f1) {
-    cursor_settle<SHARED>(a, cc);
+    cursor_settle<SHARED>(a, shared, cc);
     const int tiles = (int)min(f1 - f, (int64_t)(cc.nt - cc.tile));
     const __nv_bfloat16* qrow = a.q + (int64_t)cc.b * a.q_sb;
     auto load_q = [&](uint32_t (&f)[4], int ks) {

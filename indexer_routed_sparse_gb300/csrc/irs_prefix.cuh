@@ -19,7 +19,7 @@ namespace {
 __host__ __device__ constexpr int prefix_block(int Dqk) { return Dqk == 192 ? 96 : 128; }
 constexpr int kPrefixRows = 256;      // rows an item (two tiles)
 constexpr int kMaxPrefixCtas = 160;
-constexpr int kMinBlocks = 1;         // a run has at least this many blocks
+constexpr int kMinBlocks = 2;         // a run has at least this many blocks: fewer leave more parts to join than they save
 
 __host__ __device__ inline size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
 
@@ -61,8 +61,12 @@ __device__ __forceinline__ int prefix_blocks(const PrefixArgs& a, int n) {
 }
 // Blocks of a run.
 __device__ __forceinline__ int64_t prefix_share(int64_t total, int runs) {
-  const int64_t q = (total + runs - 1) / runs;
+  const int64_t q = total >> 30 == 0 ? (int64_t)(((uint32_t)total + (uint32_t)runs - 1u) / (uint32_t)runs) : (total + runs - 1) / runs;
   return q < kMinBlocks ? kMinBlocks : q;
+}
+// The run that holds unit f. (Divisions of 64 bits take a thread 100 instructions.)
+__device__ __forceinline__ int prefix_run(int64_t f, int64_t share) {
+  return ((f | share) >> 31) == 0 ? (int)((uint32_t)f / (uint32_t)share) : (int)(f / share);
 }
 // The group that holds unit f of a head's list.
 __device__ __forceinline__ int prefix_find(const int64_t* pre, int P, int64_t f) {

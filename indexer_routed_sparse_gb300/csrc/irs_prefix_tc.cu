@@ -862,111 +862,98 @@ __global__ void __launch_bounds__(kJoinThreads, 2) prefix_join_kernel(PrefixArgs
 }
 
 // Decoding: a row's parts over its group's prefix, then those over its own positions, joined in the
-// order of the two lists. A block takes rows of one (sequence, KV head), eight columns a thread; `pg`
-// groups of threads share a row, each taking every pg-th part, and are then joined in order.
-constexpr int kStepThreads = 256;
+// order of the two lists. Eight columns a thread, neighbouring threads neighbouring rows; where the rows
+// are few, pg groups of threads share a row, each taking every pg-th part, and are then joined in order.
+constexpr int kStepThreads = 256, kStepBlocks = 4;   // blocks an SM
 template <int DV>
-__global__ void __launch_bounds__(kStepThreads, 4) prefix_step_join_kernel(PrefixArgs a, const uint8_t* own_ws, const float* own_rows, int runs, int workers) {
-  constexpr int CL = DV / 8, groups = kStepThreads / CL;
+__global__ void __launch_bounds__(kStepThreads, kStepBlocks)
+    prefix_step_join_kernel(PrefixArgs a, const uint8_t* own_ws, const float* own_rows, int runs, int workers, int pg) {
+  constexpr int CL = DV / 8;
   __shared__ float sm[kStepThreads][9];
   __shared__ float2 sm_ml[kStepThreads];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int t = blockIdx.x / a.Hkv, head = blockIdx.x % a.Hkv;
+  const int R = kStepThreads / (CL * pg);              // rows a block
+  const int row_in = threadIdx.x % R, cl = threadIdx.x / R % CL, part_grp = threadIdx.x / (R * CL);
+  const int64_t row = (int64_t)blockIdx.x * R + row_in;
+  const bool there = row < (int64_t)a.T * a.Hq;
+  // what no kernel before this one writes is looked up before these have ended
+  const int t = there ? (int)(row / a.Hq) : 0, hq = (int)(row - (int64_t)t * a.Hq), head = there ? hq / a.G : 0, h = hq - head * a.G;
   const int g = prefix_group_of(a, t);
   PrefixGroup gr{0, 0, 0};
   if (g >= 0) gr = prefix_group(a, g);
-  const bool live = prefix_length(a, t, gr.n) > 0;
-  // ---- the prefix's parts: runs c0 .. of the head's list, or one row ----
-  const int qt = kRows / a.G;
-  int c0 = 0, np = 0, first_slot = 0, x = 0, rq = 0;
-  if (live && gr.n > 0) {
-    const int64_t* pre = reinterpret_cast<const int64_t*>(a.ws);
-    const int64_t share = prefix_share(pre[a.P], runs);
-    const int nbg = prefix_blocks(a, gr.n), pair = (t - gr.first) / (2 * qt);
-    const int64_t s = pre[g] + (int64_t)pair * nbg;
-    c0 = (int)(s / share);
-    np = (int)((s + nbg - 1) / share) - c0 + 1;
-    first_slot = s != (int64_t)c0 * share ? 1 : 0;
-    x = (t - gr.first) / qt % 2;
-    rq = (t - gr.first) % qt;
-  }
-  // ---- the own positions' parts: by blocks of 16 query heads ----
-  const int nhb = (a.G + kHeads - 1) / kHeads, HK = a.Hkv * nhb;
-  int d0 = 0, no = 0, own_slot = 0;
+  const bool live = there && prefix_length(a, t, gr.n) > 0;
+  const int qt = kRows / a.G, nhb = (a.G + kHeads - 1) / kHeads, HK = a.Hkv * nhb;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  int c0 = 0, np = 0, first_slot = 0, r = 0;            // the prefix's parts: runs c0 .. of the head's list, or one row
+  int d0 = 0, no = 0, own_slot = 0;                     // the own positions' parts, by blocks of 16 query heads
   if (live) {
-    const int64_t* pre = reinterpret_cast<const int64_t*>(own_ws);
-    const int64_t F0 = pre[t], F1 = pre[t + 1];
+    const int64_t* pre = reinterpret_cast<const int64_t*>(a.ws);
+    const int64_t* own_pre = reinterpret_cast<const int64_t*>(own_ws);
+    const int64_t total = pre[a.P], before = g >= 0 ? pre[g] : 0, F0 = own_pre[t], F1 = own_pre[t + 1], own_total = own_pre[a.T];
+    if (gr.n > 0) {
+      const int64_t share = prefix_share(total, runs);
+      const int nbg = prefix_blocks(a, gr.n), tt = t - gr.first;
+      const int64_t s = before + (int64_t)(tt / (2 * qt)) * nbg;
+      c0 = prefix_run(s, share);
+      np = prefix_run(s + nbg - 1, share) - c0 + 1;
+      first_slot = s != (int64_t)c0 * share ? 1 : 0;
+      r = tt / qt % 2 * kRows + tt % qt * a.G + h;
+    }
     if (F1 > F0) {
-      const int64_t share = paged_share(pre[a.T], workers);
-      d0 = (int)(F0 / share);
-      no = (int)((F1 - 1) / share) - d0 + 1;
+      const int64_t share = paged_share(own_total, workers);
+      d0 = prefix_run(F0, share);
+      no = prefix_run(F1 - 1, share) - d0 + 1;
       own_slot = F0 != (int64_t)d0 * share ? 1 : 0;
     }
   }
   const float* own_parts = reinterpret_cast<const float*>(own_ws + paged_prefix_bytes(a.T));
   const int parts = np + no;
-  // up to four parts a thread, and no more rows at once than the KV head has
-  int pg = 1;
-  while (2 * pg <= groups && (4 * pg < parts || groups / (2 * pg) >= a.G)) pg *= 2;
-  const int rows = groups / pg;
-  const int row_in = threadIdx.x % rows, cl = threadIdx.x / rows % CL, part_grp = threadIdx.x / (rows * CL);
-  for (int rb = blockIdx.y * rows; rb < a.G; rb += gridDim.y * rows) {
-    const int h = rb + row_in;                          // head of the KV head's
-    const int64_t row = (int64_t)t * a.Hq + head * a.G + h;
-    PrefixSum<8> sum;
-    sum.clear();
-    if (h < a.G) {
-      const int r = x * kRows + rq * a.G + h;
-      constexpr int U = 2;
-      for (int p = part_grp; p < parts; p += U * pg) {
-        float2 ml[U];
-        float o[U][8];
+  PrefixSum<8> sum;
+  sum.clear();
+  constexpr int U = 2;
+  for (int p = part_grp; p < parts; p += U * pg) {
+    float2 ml[U];
+    float o[U][8];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int i = p + u * pg;
-          ml[u] = make_float2(-INFINITY, 0.f);
+    for (int u = 0; u < U; ++u) {
+      const int i = p + u * pg;
+      ml[u] = make_float2(-INFINITY, 0.f);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) o[u][k] = 0.f;
-          if (i < parts) {
-            if (i < np) {
-              float* part = np == 1 ? prefix_rows(a) : prefix_part(a, c0 + i, head, i == 0 ? first_slot : 0);
-              const int64_t n = np == 1 ? (int64_t)a.T * a.Hq : kPrefixRows, at = np == 1 ? row : r;
-              ml[u] = prefix_sums_ml(part, n, at, DV);
-              prefix_sums8(o[u], part, n, at, 8 * cl);
-            } else if (no == 1) {
-              ml[u] = *reinterpret_cast<const float2*>(own_rows + (size_t)a.T * a.Hq * DV + 2 * row);
-              prefix_load8(o[u], own_rows + row * DV + 8 * cl);
-            } else {
-              const int j = i - np, hk = head * nhb + h / kHeads, hr = h % kHeads;
-              const float* part = own_parts + (((size_t)(d0 + j) * HK + hk) * 2 + (j == 0 ? own_slot : 0)) * paged_part_floats(DV);
-              ml[u] = make_float2(part[kHeads * DV + hr], part[kHeads * DV + kHeads + hr]);
-              prefix_load8(o[u], part + hr * DV + 8 * cl);
-            }
-          }
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) sum.add(ml[u].x, ml[u].y, o[u]);
+      for (int k = 0; k < 8; ++k) o[u][k] = 0.f;
+      if (i < np) {
+        float* part = np == 1 ? prefix_rows(a) : prefix_part(a, c0 + i, head, i == 0 ? first_slot : 0);
+        const int64_t n = np == 1 ? (int64_t)a.T * a.Hq : kPrefixRows, at = np == 1 ? row : r;
+        ml[u] = prefix_sums_ml(part, n, at, DV);
+        prefix_sums8(o[u], part, n, at, 8 * cl);
+      } else if (i < parts && no == 1) {
+        ml[u] = *reinterpret_cast<const float2*>(own_rows + (size_t)a.T * a.Hq * DV + 2 * row);
+        prefix_load8(o[u], own_rows + row * DV + 8 * cl);
+      } else if (i < parts) {
+        const int j = i - np, hk = head * nhb + h / kHeads, hr = h % kHeads;
+        const float* part = own_parts + (((size_t)(d0 + j) * HK + hk) * 2 + (j == 0 ? own_slot : 0)) * paged_part_floats(DV);
+        ml[u] = make_float2(part[kHeads * DV + hr], part[kHeads * DV + kHeads + hr]);
+        prefix_load8(o[u], part + hr * DV + 8 * cl);
       }
     }
-    if (pg > 1) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) sm[threadIdx.x][k] = sum.o[k];
-      sm_ml[threadIdx.x] = make_float2(sum.m, sum.l);
-      __syncthreads();
-      if (part_grp == 0)
-        for (int i = threadIdx.x + rows * CL; i < kStepThreads; i += rows * CL) {
-          float o[8];
+    for (int u = 0; u < U; ++u) sum.add(ml[u].x, ml[u].y, o[u]);
+  }
+  if (pg > 1) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) o[k] = sm[i][k];
-          sum.add(sm_ml[i].x, sm_ml[i].y, o);
-        }
-      __syncthreads();
+    for (int k = 0; k < 8; ++k) sm[threadIdx.x][k] = sum.o[k];
+    sm_ml[threadIdx.x] = make_float2(sum.m, sum.l);
+    __syncthreads();
+    if (part_grp > 0) return;
+    for (int i = threadIdx.x + R * CL; i < kStepThreads; i += R * CL) {
+      float o[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) o[k] = sm[i][k];
+      sum.add(sm_ml[i].x, sm_ml[i].y, o);
     }
-    if (part_grp == 0 && h < a.G) {
-      const PrefixJoin jn = prefix_join_own(a, row, sum.m, sum.l);
-      if (cl == 0 && a.lse != nullptr) a.lse[row] = jn.lse;
-      prefix_store8(a, row * DV + 8 * cl, jn, sum.o);
-    }
+  }
+  if (there) {
+    const PrefixJoin jn = prefix_join_own(a, row, sum.m, sum.l);
+    if (cl == 0 && a.lse != nullptr) a.lse[row] = jn.lse;
+    prefix_store8(a, row * DV + 8 * cl, jn, sum.o);
   }
 }
 
@@ -1058,15 +1045,15 @@ cudaError_t launch_prefix_decode(const PrefixMaps& m, const PrefixArgs& a, int n
   o.shared = a;
   int workers = 0;
   if ((e = launch_paged_shared(o, num_sms, own_configured, &workers, stream)) != cudaSuccess) return e;
-  const int64_t pairs = (int64_t)a.T * a.Hkv;
-  int y = (int)(8 * num_sms / pairs);   // blocks of four an SM, twice over: rows of many parts are taken one or two at a time
-  y = y < 1 ? 1 : y > a.G ? a.G : y;
+  const int64_t threads = (int64_t)a.T * a.Hq * (a.Dv / 8);
+  int pg = 1;   // as many threads as run at once
+  while (pg < 8 && 2 * pg * threads <= (int64_t)num_sms * kStepBlocks * kStepThreads) pg *= 2;
   cudaLaunchAttribute at[1];
-  const cudaLaunchConfig_t cfg = early(dim3((unsigned)pairs, (unsigned)y), kStepThreads, stream, at);
+  const cudaLaunchConfig_t cfg = early(dim3((unsigned)((threads * pg + kStepThreads - 1) / kStepThreads)), kStepThreads, stream, at);
   const uint8_t* own_ws = o.ws;
   const float* own_rows = o.rows;
-  return a.Dv == 64 ? cudaLaunchKernelEx(&cfg, prefix_step_join_kernel<64>, a, own_ws, own_rows, runs, workers)
-                    : cudaLaunchKernelEx(&cfg, prefix_step_join_kernel<128>, a, own_ws, own_rows, runs, workers);
+  return a.Dv == 64 ? cudaLaunchKernelEx(&cfg, prefix_step_join_kernel<64>, a, own_ws, own_rows, runs, workers, pg)
+                    : cudaLaunchKernelEx(&cfg, prefix_step_join_kernel<128>, a, own_ws, own_rows, runs, workers, pg);
 }
 
 }  // namespace irs
