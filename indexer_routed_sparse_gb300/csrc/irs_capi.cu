@@ -1258,6 +1258,7 @@ irs_status prefix_args(irs::PrefixArgs* a, const void* q, int64_t q_stride_t, in
   if (T < 0 || P < 0 || Hq < 1 || Hkv < 1) return fail(IRS_ERR_VALUE, "bad sizes (T=%d P=%d Hq=%d Hkv=%d)", T, P, Hq, Hkv);
   if (Hq % Hkv != 0) return fail(IRS_ERR_VALUE, "Hq (%d) must be a multiple of Hkv (%d)", Hq, Hkv);
   if (Hq / Hkv > 128) return fail(IRS_ERR_VALUE, "at most 128 query heads a KV head (got %d)", Hq / Hkv);
+  if (Hkv > 1024) return fail(IRS_ERR_VALUE, "at most 1024 KV heads (got %d)", Hkv);
   if (Dqk != 64 && Dqk != 128 && Dqk != 192) return fail(IRS_ERR_VALUE, "Dqk must be 64, 128 or 192 (got %d)", Dqk);
   if (Dv != 64 && Dv != 128) return fail(IRS_ERR_VALUE, "Dv must be 64 or 128 (got %d)", Dv);
   if ((long long)T * Hq >= (1LL << 31)) return fail(IRS_ERR_VALUE, "T * Hq must be below 2^31");
@@ -1327,7 +1328,7 @@ irs_status make_pool_map(CUtensorMap* m, const void* base, int D, const irs::Pre
 irs_status prefix_maps(irs::PrefixMaps* m, const irs::PrefixArgs& a) {
   *m = irs::PrefixMaps{};
   irs_status s;
-  m->has_q = (a.T == 1 || a.q_st > 0) && (a.Hq == 1 || a.q_sh > 0);
+  m->has_q = (a.T == 1 || (a.q_st > 0 && a.q_st < (1LL << 38))) && (a.Hq == 1 || (a.q_sh > 0 && a.q_sh < (1LL << 38)));
   if (m->has_q && (s = make_packed_map(&m->q, a.q, a.Dqk, a.Hq, a.T, a.q_sh, a.q_st, a.G, 128 / a.G)) != IRS_OK) return s;
   m->chunk = irs::prefix_chunk(a.Dqk, a.page_size);
   if (m->chunk > 0) {

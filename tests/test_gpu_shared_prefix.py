@@ -606,3 +606,64 @@ def test_plan_append_prompts_and_steps_together(irs):
         R.check(out[b][None], ref[0], ref[2] + 2.0 ** -18, "step out")
         R.check(lse[b][None], ref[1], ref[3] + 2.0 ** -18, "step lse")
     assert int(count) == 48 - len(set(table[table >= 0].tolist()))
+
+
+@pytest.mark.parametrize("decode", [False, True])
+def test_broadcast_pools_and_one_head_for_all(irs, decode):
+    """Pools whose heads, or whose positions, are one row: strides of 0."""
+    g = _gen(17)
+    kc, vc = _normal(g, 9, 16, 1, 128), _normal(g, 9, 16, 1, 64)
+    table = torch.arange(9, device=DEV, dtype=torch.int32)[None].repeat(3, 1)
+    q = _normal(g, 3, 8, 128)
+    for k, v in ((kc.expand(-1, -1, 4, -1), vc.expand(-1, -1, 4, -1)), (kc[:, :1].expand(-1, 16, 4, -1), vc.expand(-1, -1, 4, -1))):
+        if decode:
+            lens = [120, 0, 77]
+            out, lse = irs.shared_prefix_gqa_attn_decode(q, k, v, table, _i32(lens), _i32([0, 3]), _i32([70]))
+            ref = R.decode(q, k, v, table, lens, [0, 3], [70], 1 / math.sqrt(128))
+        else:
+            out, lse = irs.shared_prefix_gqa_attn_fwd(q, k, v, table[:2], _i32([0, 1, 3]), _i32([131, 70]))
+            ref = R.fwd(q, k, v, table, [0, 1, 3], [131, 70], 1 / math.sqrt(128))
+        irs.check_device_errors(DEV)
+        R.check(out, ref[0], ref[2], "out")
+        R.check(lse, ref[1], ref[3], "lse")
+
+
+def test_decode_every_sequence_a_group(irs):
+    """Many groups of one sequence, more than a list's first looks hold."""
+    g = torch.Generator().manual_seed(18)
+    n = 9000
+    prefix = torch.randint(0, 30, (n,), generator=g).tolist()
+    own = torch.randint(0, 4, (n,), generator=g).tolist()
+    q, kc, vc, table, lens, cu = _steps(_gen(18), [1] * n, prefix, own, 2, 1, 64, 64, 16)
+    out, lse = irs.shared_prefix_gqa_attn_decode(q, kc, vc, table, _i32(lens), _i32(cu), _i32(prefix))
+    irs.check_device_errors(DEV)
+    want, l = irs.paged_gqa_attn_decode(q, kc, vc, table, _i32(lens))
+    # the same attention by a kernel that is checked on its own: both within the roundings of weights and results
+    assert (out.double() - want.double()).abs().max() <= 3 * R.U16 * vc.double().abs().max()
+    assert torch.equal(lse == -math.inf, l == -math.inf)
+    assert (lse - l)[lse > -math.inf].abs().max() <= 2.0 ** -17
+
+
+def test_two_calls_at_once(irs):
+    """Calls of two host threads on two streams, each with a workspace of its own."""
+    import threading
+
+    args, out, lse = _decode(irs, [30, 9], [900, 300], list(range(39)), 16, 2, 128, 128, 16, seed=19)
+    got = [None, None]
+
+    def work(i):
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.default_stream())
+        with torch.cuda.stream(s):
+            for _ in range(20):
+                got[i] = irs.shared_prefix_gqa_attn_decode(*args)
+            s.synchronize()
+
+    torch.cuda.synchronize()
+    ts = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in ts:
+        t.start()
+    for t in ts:
+        t.join()
+    for o, l in got:
+        assert torch.equal(o, out) and torch.equal(l, lse)

@@ -87,7 +87,8 @@ def test_attention_refusals(lib, p, decode, kw, word):
 def test_attention_refusals_of_one_form(lib, p):
     _refused(lib, _prefix(lib, p, True, lens=None), b"NULL")
     _refused(lib, _prefix(lib, p, True, T=1 << 23), b"2^24")
-    _refused(lib, _prefix(lib, p, True, Hq=1025, Hkv=1025), b"1024")
+    _refused(lib, _prefix(lib, p, True, Hq=64 * 1024, Hkv=1024), b"1024")
+    _refused(lib, _prefix(lib, p, False, Hq=1025, Hkv=1025), b"1024")
     _refused(lib, _prefix(lib, p, False, T=1 << 30), b"2^31")
     _refused(lib, _prefix(lib, p, False, oo=p), b"come together")
     _refused(lib, _prefix(lib, p, False, oo=p + 8, ol=p), b"16-byte")
