@@ -330,48 +330,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     return before + __shfl_sync(0xffffffffu, x, 31);
   };
   if (warp == 8) {
-    // 32 groups a look. With more, four looks at once for the sum; where they end (the first 2 BLK of them) stays in
-    // the words where rows' offsets are left later, so that the run's first group is not looked for twice
     int64_t* sums = reinterpret_cast<int64_t*>(a.ws);
-    int64_t* ends = reinterpret_cast<int64_t*>(smem + C::offsets_off);
     int64_t total = 0;
-    if (a.P <= 32) {
-      total = look(0, 0);
-      if (blockIdx.x == 0 && lane < a.P) sums[lane] = pre;
-    } else {
-      for (int base = 0; base < a.P; base += 128) {
-        int64_t u[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int g = base + 32 * i + lane;
-          u[i] = g < a.P ? prefix_units(prefix_group(a, g), qt, BLK) : 0;
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int g = base + 32 * i + lane;
-          int64_t x = u[i];
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= o) x += y;
-          }
-          if (blockIdx.x == 0 && g < a.P) sums[g] = total + x - u[i];
-          total += __shfl_sync(0xffffffffu, x, 31);
-          if (lane == 0 && base / 32 + i < 2 * BLK) ends[base / 32 + i] = total;
-        }
-      }
-      __syncwarp();
+    for (int base = 0; base < a.P; base += 32) {
+      total = look(base, total);
+      if (blockIdx.x == 0 && base + lane < a.P) sums[base + lane] = pre;
     }
     if (blockIdx.x == 0 && lane == 0) sums[a.P] = total;
     const int64_t share = prefix_share(total, runs);
     f0 = run * share;
     f1 = min(total, f0 + share);
     if (a.P > 32) {
-      int at = 0;
       int64_t before = 0;
-      while (at < 2 * BLK - 1 && 32 * (at + 1) < a.P && ends[at] <= f0) before = ends[at++];
-      before = look(32 * at, before);
-      while (before <= f0 && g0 + 32 < a.P) before = look(g0 + 32, before);
+      for (int base = 0; base < a.P && before <= f0; base += 32) before = look(base, before);
     }
   }
   tc_fence_before();
