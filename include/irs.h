@@ -731,7 +731,8 @@ irs_status irs_shared_prefix_gqa_attn_fwd(const void* q, int64_t q_stride_t, int
  *
  * Group g has the sequences cu_groups[g] .. cu_groups[g+1]. Their first prefix_lens[g] positions
  * hold the same keys and values and are read through the page table's row of the group's first
- * sequence; the positions behind them through each sequence's own row. cache_lens counts both.
+ * sequence, which has to name the prefix's pages even where that sequence is idle; the positions
+ * behind them through each sequence's own row. cache_lens counts both.
  * Sequences behind cu_groups[P] share nothing. A length of 0 (an idle slot) gives out = 0 and
  * lse = -inf; so does one below 0, past max_pages * page_size or shorter than its group's
  * prefix, which sets IRS_DEVERR_PAGE.

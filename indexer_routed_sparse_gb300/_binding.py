@@ -1140,8 +1140,8 @@ def shared_prefix_gqa_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cach
 
     cu_groups int32 [P + 1]: the sequences cu_groups[g] .. cu_groups[g+1] hold the same keys and
     values at their first prefix_lens[g] (int32 [P]) positions, which are read through the page
-    table's row of the group's first sequence; the positions behind them through each sequence's
-    own. cache_lens counts both. Sequences behind the last group share nothing. A length of 0 (an
+    table's row of the group's first sequence (idle or not); the positions behind them through each
+    sequence's own. cache_lens counts both. Sequences behind the last group share nothing. A length of 0 (an
     idle slot) gives out = 0 and lse = -inf.
     """
     index = _first(q, "q", _BF16)

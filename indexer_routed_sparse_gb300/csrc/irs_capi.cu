@@ -1295,14 +1295,6 @@ irs_status prefix_args(irs::PrefixArgs* a, const void* q, int64_t q_stride_t, in
   return IRS_OK;
 }
 
-}  // namespace
-
-extern "C" {
-
-}  // extern "C"
-
-namespace {
-
 // 4-D bf16 map of a pool [pages][heads][positions][D], boxes of 64 dims x `chunk` positions; false where
 // a stride cannot be a map's.
 irs_status make_pool_map(CUtensorMap* m, const void* base, int D, const irs::PrefixArgs& a, int64_t sp, int64_t st, int64_t sh,

@@ -667,3 +667,11 @@ def test_two_calls_at_once(irs):
         t.join()
     for o, l in got:
         assert torch.equal(o, out) and torch.equal(l, lse)
+
+
+def test_decode_idle_first_sequence(irs):
+    """A group is read through its first sequence's row also where that one's own length is 0; a group without a
+    sequence that is not idle gives zeros."""
+    args, out, lse = _decode(irs, [3, 2, 1], [200, 64, 33], [None, 5, 40, None, None, 7], 8, 2, 128, 128, 16, seed=23)
+    assert (out[[0, 3, 4]] == 0).all() and (lse[[0, 3, 4]] == -math.inf).all()
+    assert torch.isfinite(lse[[1, 2, 5]]).all()
