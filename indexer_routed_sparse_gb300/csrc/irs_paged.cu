@@ -36,6 +36,8 @@
 //   TB/s; 2051 routes of 96 sequences, 32 / 8 heads of 128: 132 us, 6.1 TB/s; 512 + 4
 //   positions of 128 sequences, 64 / 4 heads of 192 / 128: 36 us for 120 MB, where the start
 //   (lengths, pages, first copies) and the join count.
+#include <type_traits>
+
 #include "irs_internal.h"
 #include "irs_paged.cuh"
 #include "irs_ptx.cuh"
@@ -78,10 +80,9 @@ inline PagedGrid paged_grid(int Dqk, int Dv, int HK, int num_sms) {
   return g;
 }
 
-// The positions that sequence b's new token attends here; SHARED: those behind the n that its group shares.
+// The positions that the new token of a sequence of length L attends here; SHARED: those behind the n that its group shares.
 template <bool SHARED>
-__device__ __forceinline__ PagedSet set_of(const PagedArgs& a, int b, int n) {
-  const int L = __ldg(a.cache_lens + b);
+__device__ __forceinline__ PagedSet set_of(const PagedArgs& a, int L, int n) {
   if constexpr (SHARED) {
     PagedSet s{};
     s.L = L < n || L > a.max_pages * a.page_size ? 0 : L;
@@ -126,29 +127,31 @@ struct Cursor {
 };
 // shared: how many positions sequence b shares with its group (kept for the first 32 kMaxWarps, else looked up).
 template <bool SHARED>
-__device__ __forceinline__ int shared_of(const PagedArgs& a, const int* shared, int b) {
-  if constexpr (SHARED) return b < 32 * kMaxWarps ? shared[b] : prefix_positions(a.shared, b);
+using PagedOthers = std::conditional_t<SHARED, PagedShared, PagedAlone>;
+template <bool SHARED>
+__device__ __forceinline__ int shared_of(const PagedOthers<SHARED>& sh, const int* shared, int b) {
+  if constexpr (SHARED) return b < 32 * kMaxWarps ? shared[b] : prefix_positions(sh.groups, b);
   else return 0;
 }
 template <bool SHARED>
-__device__ __forceinline__ void cursor_open(const PagedArgs& a, const int* shared, Cursor& c) {
-  c.set = set_of<SHARED>(a, c.b, shared_of<SHARED>(a, shared, c.b));
+__device__ __forceinline__ void cursor_open(const PagedArgs& a, const PagedOthers<SHARED>& sh, const int* shared, Cursor& c) {
+  c.set = set_of<SHARED>(a, __ldg(a.cache_lens + c.b), shared_of<SHARED>(sh, shared, c.b));
   c.nt = tiles_of(c.set);
 }
 // Move on to the sequence that holds c.tile; the list must go on that far.
 template <bool SHARED>
-__device__ __forceinline__ void cursor_settle(const PagedArgs& a, const int* shared, Cursor& c) {
+__device__ __forceinline__ void cursor_settle(const PagedArgs& a, const PagedOthers<SHARED>& sh, const int* shared, Cursor& c) {
   while (c.tile >= c.nt) {
     c.tile -= c.nt;
     if (++c.b >= a.B) { c.b = a.B - 1; c.tile = 0; return; }   // not reached on a list of the right length
-    cursor_open<SHARED>(a, shared, c);
+    cursor_open<SHARED>(a, sh, shared, c);
   }
 }
 
 // SHARED: the own positions of sequences that share prefixes. Nothing is written but FP32 sums: parts as
 // ever, and rows of a sequence that no border cuts, for the join with the prefixes' (irs_prefix_tc.cu).
 template <int DQK, int DV, bool SHARED>
-__global__ void __launch_bounds__(32 * kMaxWarps, 1) paged_decode_kernel(PagedArgs a, PagedGrid pg, int nhb) {
+__global__ void __launch_bounds__(32 * kMaxWarps, 1) paged_decode_kernel(PagedArgs a, PagedGrid pg, int nhb, PagedOthers<SHARED> sh) {
   constexpr int KS = DQK / 16, NV = DV / 8;
   constexpr uint32_t kStage = kTile * (DQK + DV) * 2;
   const int NW = pg.warps, S = pg.stages;
@@ -172,14 +175,14 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) paged_decode_kernel(PagedAr
   {
     int64_t n = 0;
     for (int b = bs; b < be; ++b) {
+      const int L = __ldg(a.cache_lens + b);
       int prefix = 0;
       if constexpr (SHARED) {
-        prefix = prefix_positions(a.shared, b);
+        prefix = prefix_positions(sh.groups, b);
         if (b < 32 * kMaxWarps) shared[b] = prefix;
       }
-      const PagedSet s = set_of<SHARED>(a, b, prefix);
-      if (blockIdx.x == 0 && s.L != __ldg(a.cache_lens + b)) record_error(a.err, IRS_DEVERR_PAGE);
-      n += tiles_of(s);
+      if (blockIdx.x == 0 && (L < prefix || L > a.max_pages * a.page_size) && (!SHARED || L != 0)) record_error(a.err, IRS_DEVERR_PAGE);
+      n += tiles_of(set_of<SHARED>(a, L, prefix));
     }
     int64_t x = n;
 #pragma unroll
@@ -206,7 +209,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) paged_decode_kernel(PagedAr
     int64_t* pre = reinterpret_cast<int64_t*>(a.ws);
     int64_t n = scan[tid];
     for (int b = bs; b < be; ++b) {
-      const int64_t next = n + tiles_of(set_of<SHARED>(a, b, shared_of<SHARED>(a, shared, b)));
+      const int64_t next = n + tiles_of(set_of<SHARED>(a, __ldg(a.cache_lens + b), shared_of<SHARED>(sh, shared, b)));
       if (blockIdx.x == 0) pre[b] = n;
       for (int w = 0; w < pg.per_head; ++w) {
         const int64_t f = (worker0 + w) * share;
@@ -229,7 +232,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) paged_decode_kernel(PagedAr
 
   Cursor cc;                                            // the tile being computed
   cc.b = start_b[sub];
-  cursor_open<SHARED>(a, shared, cc);
+  cursor_open<SHARED>(a, sh, shared, cc);
   cc.tile = (int)(f0 - start_pre[sub]);
 
   // ---- loads: A looks up positions or routes, B pages, C issues the copies ----
@@ -245,7 +248,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) paged_decode_kernel(PagedAr
     a_pos = -1;
     a_route = false;
     if (a_live) {
-      cursor_settle<SHARED>(a, shared, lc);
+      cursor_settle<SHARED>(a, sh, shared, lc);
       a_b = lc.b;
       int j = lc.tile * kTile + key;
       if (j < lc.set.n) {
@@ -325,7 +328,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) paged_decode_kernel(PagedAr
   int slot = 0;
   int64_t f = f0;
   while (f < f1) {
-    cursor_settle<SHARED>(a, shared, cc);
+    cursor_settle<SHARED>(a, sh, shared, cc);
     const int tiles = (int)min(f1 - f, (int64_t)(cc.nt - cc.tile));
     const __nv_bfloat16* qrow = a.q + (int64_t)cc.b * a.q_sb;
     auto load_q = [&](uint32_t (&f)[4], int ks) {
@@ -434,30 +437,25 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) paged_decode_kernel(PagedAr
       // attended, and every score -inf: 0 / 0; in a part -1, which a finite maximum wipes out
       if (l[i] == 0.f && seen != 0u) l[i] = !SHARED && tiles == cc.nt ? NAN : -1.f;
     }
-    if (SHARED && tiles == cc.nt) {
+    if (tiles == cc.nt) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int row = g4 + 8 * i;
         if (row < nh) {
           const int64_t r = (int64_t)cc.b * a.Hq + h0 + row;
+          if constexpr (SHARED) {
 #pragma unroll
-          for (int n = 0; n < NV; ++n)
-            *reinterpret_cast<float2*>(a.rows + r * DV + n * 8 + 2 * t4) = make_float2(o[n][2 * i], o[n][2 * i + 1]);
-          if (t4 == 0) *reinterpret_cast<float2*>(a.rows + (int64_t)a.B * a.Hq * DV + 2 * r) = make_float2(mx[i], l[i]);
-        }
-      }
-    } else if (tiles == cc.nt) {
+            for (int n = 0; n < NV; ++n)
+              *reinterpret_cast<float2*>(sh.rows + r * DV + n * 8 + 2 * t4) = make_float2(o[n][2 * i], o[n][2 * i + 1]);
+            if (t4 == 0) *reinterpret_cast<float2*>(sh.rows + (int64_t)a.B * a.Hq * DV + 2 * r) = make_float2(mx[i], l[i]);
+          } else {
+            const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];   // no position: 0; a NaN sum stays NaN
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int row = g4 + 8 * i;
-        if (row < nh) {
-          const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];   // no position: 0; a NaN sum stays NaN
-          const int64_t r = (int64_t)cc.b * a.Hq + h0 + row;
-#pragma unroll
-          for (int n = 0; n < NV; ++n)
-            *reinterpret_cast<__nv_bfloat162*>(a.out + r * DV + n * 8 + 2 * t4) =
-                __floats2bfloat162_rn(o[n][2 * i] * inv, o[n][2 * i + 1] * inv);
-          if (t4 == 0 && a.lse != nullptr) a.lse[r] = fmaf(mx[i], 0.6931471805599453f, logf(l[i]));
+            for (int n = 0; n < NV; ++n)
+              *reinterpret_cast<__nv_bfloat162*>(a.out + r * DV + n * 8 + 2 * t4) =
+                  __floats2bfloat162_rn(o[n][2 * i] * inv, o[n][2 * i + 1] * inv);
+            if (t4 == 0 && a.lse != nullptr) a.lse[r] = fmaf(mx[i], 0.6931471805599453f, logf(l[i]));
+          }
         }
       }
     } else {
@@ -581,7 +579,7 @@ cudaError_t launch_decode(const PagedArgs& a, int num_sms, bool* configured, cud
   }
   const int nhb = (a.G + kHeads - 1) / kHeads;
   const PagedGrid pg = paged_grid(DQK, DV, a.Hkv * nhb, num_sms);
-  paged_decode_kernel<DQK, DV, false><<<pg.ctas, 32 * pg.warps, pg.smem, stream>>>(a, pg, nhb);
+  paged_decode_kernel<DQK, DV, false><<<pg.ctas, 32 * pg.warps, pg.smem, stream>>>(a, pg, nhb, PagedAlone{});
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // About four parts a thread: a sequence has workers / B of them when the lengths are alike.
@@ -609,7 +607,7 @@ cudaError_t launch_decode(const PagedArgs& a, int num_sms, bool* configured, cud
 // The own positions of sequences that share prefixes: the next kernel of the stream may start before
 // the kernel before this one ends, and so may this one.
 template <int DQK, int DV>
-cudaError_t launch_shared(const PagedArgs& a, int num_sms, bool* configured, int* workers, cudaStream_t stream) {
+cudaError_t launch_shared(const PagedArgs& a, const PagedShared& sh, int num_sms, bool* configured, int* workers, cudaStream_t stream) {
   if (!*configured) {
     const cudaError_t e = cudaFuncSetAttribute(paged_decode_kernel<DQK, DV, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                (int)(kRingBytes + 256));
@@ -629,7 +627,7 @@ cudaError_t launch_shared(const PagedArgs& a, int num_sms, bool* configured, int
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_decode_kernel<DQK, DV, true>, a, pg, nhb);
+  return cudaLaunchKernelEx(&cfg, paged_decode_kernel<DQK, DV, true>, a, pg, nhb, sh);
 }
 
 }  // namespace
@@ -656,15 +654,15 @@ cudaError_t launch_paged_decode(const PagedArgs& a, int num_sms, bool* configure
   }
 }
 
-cudaError_t launch_paged_shared(const PagedArgs& a, int num_sms, bool* configured, int* workers, cudaStream_t stream) {
+cudaError_t launch_paged_shared(const PagedArgs& a, const PagedShared& sh, int num_sms, bool* configured, int* workers, cudaStream_t stream) {
   const int i = (a.Dqk / 64 - 1) * 2 + (a.Dv / 64 - 1);
   switch (i) {
-    case 0: return launch_shared<64, 64>(a, num_sms, configured + i, workers, stream);
-    case 1: return launch_shared<64, 128>(a, num_sms, configured + i, workers, stream);
-    case 2: return launch_shared<128, 64>(a, num_sms, configured + i, workers, stream);
-    case 3: return launch_shared<128, 128>(a, num_sms, configured + i, workers, stream);
-    case 4: return launch_shared<192, 64>(a, num_sms, configured + i, workers, stream);
-    default: return launch_shared<192, 128>(a, num_sms, configured + i, workers, stream);
+    case 0: return launch_shared<64, 64>(a, sh, num_sms, configured + i, workers, stream);
+    case 1: return launch_shared<64, 128>(a, sh, num_sms, configured + i, workers, stream);
+    case 2: return launch_shared<128, 64>(a, sh, num_sms, configured + i, workers, stream);
+    case 3: return launch_shared<128, 128>(a, sh, num_sms, configured + i, workers, stream);
+    case 4: return launch_shared<192, 64>(a, sh, num_sms, configured + i, workers, stream);
+    default: return launch_shared<192, 128>(a, sh, num_sms, configured + i, workers, stream);
   }
 }
 

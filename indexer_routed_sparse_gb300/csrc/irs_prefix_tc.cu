@@ -1036,22 +1036,21 @@ cudaError_t launch_prefix_decode(const PrefixMaps& m, const PrefixArgs& a, int n
   o.v = a.v; o.v_sp = a.v_sp; o.v_st = a.v_st; o.v_sh = a.v_sh;
   o.page_table = a.page_table; o.table_stride = a.table_stride;
   o.cache_lens = a.cache_lens;
-  o.rows = reinterpret_cast<float*>(ws);
   o.ws = ws + prefix_rows_bytes(a.T, a.Hq, a.Dv);
   o.err = a.err;
   o.B = a.T; o.Hq = a.Hq; o.Hkv = a.Hkv; o.G = a.G; o.Dqk = a.Dqk; o.Dv = a.Dv;
   o.max_pages = a.max_pages; o.num_pages = a.num_pages; o.page_size = a.page_size;
   o.scale_log2 = a.scale_log2;
-  o.shared = a;
+  const PagedShared sh{a, reinterpret_cast<float*>(ws)};
   int workers = 0;
-  if ((e = launch_paged_shared(o, num_sms, own_configured, &workers, stream)) != cudaSuccess) return e;
+  if ((e = launch_paged_shared(o, sh, num_sms, own_configured, &workers, stream)) != cudaSuccess) return e;
   const int64_t threads = (int64_t)a.T * a.Hq * (a.Dv / 8);
   int pg = 1;   // as many threads as run at once
   while (pg < 8 && 2 * pg * threads <= (int64_t)num_sms * kStepBlocks * kStepThreads) pg *= 2;
   cudaLaunchAttribute at[1];
   const cudaLaunchConfig_t cfg = early(dim3((unsigned)((threads * pg + kStepThreads - 1) / kStepThreads)), kStepThreads, stream, at);
   const uint8_t* own_ws = o.ws;
-  const float* own_rows = o.rows;
+  const float* own_rows = sh.rows;
   return a.Dv == 64 ? cudaLaunchKernelEx(&cfg, prefix_step_join_kernel<64>, a, own_ws, own_rows, runs, workers, pg)
                     : cudaLaunchKernelEx(&cfg, prefix_step_join_kernel<128>, a, own_ws, own_rows, runs, workers, pg);
 }
