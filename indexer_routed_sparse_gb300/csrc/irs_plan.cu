@@ -13,7 +13,12 @@
 // one CTA to another and one launch does; a token finds its sequence among the 256 runs' sums in
 // shared memory and then inside the run. An entry that this call makes is worked out from the list of
 // free pages wherever it is needed, never read back from the table, so CTAs need no order. A thread
-// has four items in hand, so that their searches and loads run side by side.
+// has four items in hand, so that their searches and loads run side by side. What is known of the first
+// 1024 sequences stays in shared memory (480 sequences that share 7 prompts: 23 us without, 12 with).
+//
+// Measured (device time, replayed from a graph): 64 sequences, one token each, 6.3 us; 480 that share 7
+// prompts 12.4; 48 prompts of 2000 to 60,000 tokens (16 MB) 14.4 us, 1.1 TB/s behind the
+// same chain of lengths, sums, search and page that is all of the first. Launched alone, the host's 30 us.
 #include <climits>
 
 #include "irs_internal.h"

@@ -19,7 +19,9 @@ namespace {
 __host__ __device__ constexpr int prefix_block(int Dqk) { return Dqk == 192 ? 96 : 128; }
 constexpr int kPrefixRows = 256;      // rows an item (two tiles)
 constexpr int kMaxPrefixCtas = 160;
-constexpr int kMinBlocks = 2;         // a run has at least this many blocks: fewer leave more parts to join than they save
+// A run has at least this many blocks: fewer leave more parts to join than they save. 77 tokens over 4099
+// positions, and a step of 8 sequences behind 2000: 2 blocks 22.7 and 22.6 us, 1 block 22.7 and 25.0, 4 blocks 26.7 and 22.8.
+constexpr int kMinBlocks = 2;
 
 __host__ __device__ inline size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
 
