@@ -675,3 +675,49 @@ def test_decode_idle_first_sequence(irs):
     args, out, lse = _decode(irs, [3, 2, 1], [200, 64, 33], [None, 5, 40, None, None, 7], 8, 2, 128, 128, 16, seed=23)
     assert (out[[0, 3, 4]] == 0).all() and (lse[[0, 3, 4]] == -math.inf).all()
     assert torch.isfinite(lse[[1, 2, 5]]).all()
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(200, 200), (160, 80), (1024, 1024)])
+def test_more_heads_than_run_at_once(irs, Hq, Hkv):
+    """KV heads past what has a CTA each at a time: a head's list is one run, or two."""
+    _prompts(irs, [3, 70], [150, 40], Hq, Hkv, 64, 64, 16, seed=Hkv)
+    _decode(irs, [2, 1], [140, 33], [3, 60, 0], Hq, Hkv, 64, 64, 16, seed=Hkv)
+
+
+@pytest.mark.parametrize("page,Dqk", [(128, 128), (256, 128), (512, 192), (1000, 64), (4096, 128)])
+def test_large_pages(irs, page, Dqk):
+    """Pages of a block and more, down to one page a sequence."""
+    _prompts(irs, [9, 70], [1033, 190], 8, 2, Dqk, 128, page, seed=page)
+    _decode(irs, [3, 2], [1033, 190], [1, 40, 900, 300, 0], 8, 2, Dqk, 128, page, seed=page)
+
+
+def test_calls_in_one_graph_share_a_workspace(irs):
+    """A step's calls in one graph, one workspace for all of them in turn, replayed with other lengths."""
+    q, kc, vc, table, lens, cu = _steps(_gen(29), [6, 3], [300, 90], [10, 4, 0, 70, 9, 33, 1, 2, 3], 8, 2, 128, 128, 16)
+    L, pl = _i32(lens), _i32([300, 90])
+    ws = torch.empty(128 << 20, dtype=torch.uint8, device=DEV)
+    firsts = table[[0, 6]].contiguous()
+
+    def step():
+        a = irs.shared_prefix_gqa_attn_decode(q, kc, vc, table, L, _i32_cu, pl, workspace=ws)
+        b = irs.shared_prefix_gqa_attn_fwd(q, kc, vc, firsts, _i32_cu, pl, own=a, workspace=ws)
+        c = irs.shared_prefix_gqa_attn_decode(q, kc, vc, table, L, _i32_cu, pl, workspace=ws)
+        return a, b, c
+
+    _i32_cu = _i32(cu)
+    step()
+    torch.cuda.synchronize()
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        got = step()
+    for n in ([300, 90], [17, 0], [256, 90]):
+        pl.copy_(_i32(n))
+        gr.replay()
+        torch.cuda.synchronize()
+        want = step()
+        for x, y in zip(got, want):
+            assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
+        assert torch.equal(got[0][0], got[2][0]) and torch.equal(got[0][1], got[2][1])
+        ref = R.decode(q, kc, vc, table, lens, cu, n, 1 / math.sqrt(128))
+        R.check(got[0][0], ref[0], ref[2], "out")
+    irs.check_device_errors(DEV)
