@@ -226,10 +226,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
         int first = 0;
         plan_group(cu, a.P, b, &first);
         const PlanSeq f = seq(first);
-        // entries that the first sequence has not, it does not give
-        if (j < f.held + f.need) {
+        // entries that the first sequence has not, or finds no page for, it does not give
+        const int64_t before = j < f.held ? 0 : pages_before(first);
+        if (j < f.held || (j < f.held + f.need && before + f.need <= count)) {
           dst[u] = a.page_table + (int64_t)b * a.table_stride + j;
-          page[u] = entry(first, f, j < f.held ? 0 : pages_before(first), j);
+          page[u] = entry(first, f, before, j);
         }
       }
     }

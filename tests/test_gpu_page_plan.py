@@ -1,0 +1,47 @@
+"""The page plan where pages run short and where a group's first sequence does not hold its prefix, on the GPU,
+against an allocator on the host."""
+import pytest
+import torch
+
+import plan_ref as R
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda", 0)
+
+
+@pytest.fixture(scope="module")
+def irs():
+    import indexer_routed_sparse_gb300 as m
+
+    m.lib()
+    return m
+
+
+def _i32(x):
+    return torch.tensor(x, dtype=torch.int32, device=DEV)
+
+
+def _check(irs, lens, new, table, free, page, groups=None, prefix=None, count=None, tokens=None):
+    """One plan, and the same again, equal to the definition in everything; returns the definition's results."""
+    count = len(free) if count is None else count
+    tokens = sum(max(m, 0) for m in new) if tokens is None else tokens
+    ref = R.plan(lens, new, table, free, count, page, tokens, groups, prefix)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    dt = _i32(table)
+    gr = {} if groups is None else dict(cu_groups=_i32(groups), prefix_lens=_i32(prefix))
+    for _ in range(2):
+        got = irs.paged_plan(_i32(lens), _i32(new), dt, _i32(free), _i32([count]), page, tokens, err=err, **gr)
+        assert dt.tolist() == ref[0]
+        assert got.cu_new.tolist() == ref[1] and got.positions.tolist() == ref[2] and got.slots.tolist() == ref[3]
+        assert got.cache_lens.tolist() == ref[4] and got.free_count.tolist() == [ref[5]]
+    assert int(err) == (irs.DEVERR_PAGE if ref[6] else 0)
+    return ref
+
+
+def test_a_refused_first_sequence_takes_nothing_from_the_others(irs):
+    """One free page for a first sequence that needs three: the others, which hold the prefix, keep their pages."""
+    ref = _check(irs, [0, 40], [40, 1], [[-1, -1, -1], [7, 8, 9]], [3], 16, [0, 2], [32])
+    assert ref[0][1] == [7, 8, 9] and ref[4] == [0, 41]
+    # it holds one page already, and gives that one only
+    ref = _check(irs, [16, 40, 0], [30, 1, 0], [[5, -1, -1], [7, 8, 9], [-1, -1, -1]], [3], 16, [0, 3], [32])
+    assert ref[0][1] == [5, 8, 9]
