@@ -656,9 +656,10 @@ irs_status irs_window_gqa_attn_bwd(const void* q, int64_t q_stride_t, int64_t q_
  * beyond them, in the order of the sequences from the end of the list of free pages: the i-th
  * page given is free_pages[*free_count - 1 - i]. With groups (P > 0: group g has the sequences
  * cu_groups[g] .. cu_groups[g+1], whose first prefix_lens[g] tokens are the same) every
- * sequence behind its group's first takes that one's entries of the pages that the prefix
- * fills, prefix_lens[g] / page_size of them, where the first has them and the sequence's own n
- * covers the prefix; a page that a prefix fills in part is each sequence's own.
+ * sequence behind its group's first whose own n covers the prefix takes that one's entries of
+ * the pages that the prefix fills, prefix_lens[g] / page_size of them: of these the pages that
+ * the first's tokens fill, this step's among them. Entries that it does not give stay as they
+ * are; a page that a prefix fills in part is each sequence's own.
  * Results, beside the entries of page_table:
  *   cu_new    int32 [B + 1]     exclusive sums of new_lens, as irs_paged_rope_append takes them
  *   positions int32 [tokens]    of each new token in its sequence

@@ -226,9 +226,15 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
         int first = 0;
         plan_group(cu, a.P, b, &first);
         const PlanSeq f = seq(first);
-        // entries that the first sequence has not, or finds no page for, it does not give
-        const int64_t before = j < f.held ? 0 : pages_before(first);
-        if (j < f.held || (j < f.held + f.need && before + f.need <= count)) {
+        // A page that the first sequence has not, finds none for or does not fill in this step it does not give.
+        const int end = (j + 1) * a.page_size;   // at most the prefix's length
+        bool gives = j < f.held && end <= f.n;
+        int64_t before = 0;
+        if (!gives && j < f.held + f.need && end <= f.n + f.m) {
+          before = pages_before(first);
+          gives = f.need == 0 || before + f.need <= count;
+        }
+        if (gives) {
           dst[u] = a.page_table + (int64_t)b * a.table_stride + j;
           page[u] = entry(first, f, before, j);
         }

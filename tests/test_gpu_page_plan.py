@@ -45,3 +45,12 @@ def test_a_refused_first_sequence_takes_nothing_from_the_others(irs):
     # it holds one page already, and gives that one only
     ref = _check(irs, [16, 40, 0], [30, 1, 0], [[5, -1, -1], [7, 8, 9], [-1, -1, -1]], [3], 16, [0, 3], [32])
     assert ref[0][1] == [5, 8, 9]
+
+
+@pytest.mark.parametrize("n,m,given", [(0, 20, 1), (20, 0, 1), (20, 1, 1), (20, 11, 1), (20, 12, 2), (31, 1, 2), (0, 32, 2), (15, 0, 0),
+                                       (0, 15, 0), (0, 48, 2), (33, 0, 2)])
+def test_pages_that_the_first_sequence_fills_in_part_are_not_given(irs, n, m, given):
+    """A first sequence that takes its prompt by and by gives the pages that are full after the step."""
+    row = [20, 21, 22][: -(-n // 16)]
+    ref = _check(irs, [n, 40], [m, 1], [row + [-1] * (4 - len(row)), [7, 8, 9, -1]], [1, 2, 3, 4], 16, [0, 2], [32])
+    assert ref[0][1] == ref[0][0][:given] + [7, 8, 9][given:] + [-1]
