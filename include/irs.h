@@ -669,8 +669,8 @@ irs_status irs_window_gqa_attn_bwd(const void* q, int64_t q_stride_t, int64_t q_
  * positions and slots behind the last new token are -1. Inputs are not changed, so the same call
  * gives the same results again.
  * A sequence that finds too few pages gets none: its new entries and its slots are -1, its
- * length stays n, and IRS_DEVERR_PAGE is set; the others of its group keep the entries that it
- * was to give. So it is for a length or number of new tokens
+ * length stays n, and IRS_DEVERR_PAGE is set; the sequences behind it may find enough, and the
+ * others of its group keep the entries that it was to give. So it is for a length or number of new tokens
  * below 0, and for n + m past max_pages * page_size, which read as m = 0; and for a free_count
  * outside [0, free_size], which is cut to it. More than `tokens` new ones: the rest has no
  * position or slot (IRS_DEVERR_CU_SEQLENS); borders of groups that fall, or do not lie in

@@ -1,7 +1,8 @@
 // A serving step's page tables, token positions and slots, from the requests' lengths.
 //
 // Mathematics. Sequence b holds n_b tokens and takes m_b more; pages hold p tokens:
-//   held_b = ceil(n_b / p),  need_b = ceil((n_b + m_b) / p) - held_b,  at_b = sum_{i<b} need_i
+//   held_b = ceil(n_b / p),  need_b = ceil((n_b + m_b) / p) - held_b
+//   b is given its pages where need_b <= count - at_b, at_b the sum of need_i over those i < b that are given theirs
 //   page_table[b, held_b + i] = free[count - 1 - at_b - i]   for 0 <= i < need_b
 //   token t = cu_b + i (cu the exclusive sums of m): position n_b + i, slot page * p + position % p
 // and the sequences behind a group's first take its entries of the pages that the prefix fills.
@@ -13,7 +14,8 @@
 // one CTA to another and one launch does; a token finds its sequence among the 256 runs' sums in
 // shared memory and then inside the run. An entry that this call makes is worked out from the list of
 // free pages wherever it is needed, never read back from the table, so CTAs need no order. A thread
-// has four items in hand, so that their searches and loads run side by side. What is known of the first
+// has four items in hand, so that their searches and loads run side by side. Where all together need more pages
+// than are free, a warp goes through the sequences in order, to know what is given before each run. What is known of the first
 // 1024 sequences stays in shared memory (480 sequences that share 7 prompts: 23 us without, 12 with).
 //
 // Measured (device time, replayed from a graph): 64 sequences, one token each, 6.3 us; 480 that share 7
@@ -72,9 +74,10 @@ __device__ __forceinline__ PlanSeq plan_seq(const PlanArgs& a, const int32_t* cu
   return s;
 }
 
-// Pages, tokens and shared entries of the sequences before a place.
+// Pages that the sequences before a place need, and that they are given; their tokens and shared entries.
 struct PlanSum {
   int64_t pages, tokens, shared;
+  int given;
 };
 
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
@@ -96,7 +99,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
   bool bad = false;
   auto seq = [&](int b) { return b < kPlanCached ? cached[b] : plan_seq(a, cu, b, &bad); };
 
-  PlanSum n{0, 0, 0};
+  PlanSum n{};
   for (int b = b0; b < b1; ++b) {
     const PlanSeq s = plan_seq(a, cu, b, &bad);
     if (b < kPlanCached) cached[b] = s;
@@ -115,7 +118,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
   if (lane == 31) warp_sums[warp] = x;
   if (tid == 0) sm_granted = 0;
   __syncthreads();
-  PlanSum base{x.pages - n.pages, x.tokens - n.tokens, x.shared - n.shared}, all{0, 0, 0};
+  PlanSum base{x.pages - n.pages, x.tokens - n.tokens, x.shared - n.shared, 0}, all{};
 #pragma unroll
   for (int w = 0; w < kPlanThreads / 32; ++w) {
     const PlanSum s = warp_sums[w];
@@ -124,8 +127,24 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
     all.tokens += s.tokens;
     all.shared += s.shared;
   }
+  base.given = (int)min(base.pages, (int64_t)count);
   sums[tid] = base;
   __syncthreads();
+  if (all.pages > count) {   // too few pages: what is given before each run of sequences, one after the other
+    if (warp == 0) {
+      int given = 0;
+      for (int c = 0; c < a.B; c += 32) {
+        const int need = c + lane < a.B ? seq(c + lane).need : 0;
+        for (int i = 0; i < 32 && c + i < a.B; ++i) {
+          if (lane == 0 && (c + i) % per == 0) sums[(c + i) / per].given = given;
+          const int x = __shfl_sync(0xffffffffu, need, i);
+          given += x <= count - given ? x : 0;
+        }
+      }
+    }
+    __syncthreads();
+    base.given = sums[tid].given;
+  }
 
   // ---- the small results, by the first CTA ----
   if (blockIdx.x == 0) {
@@ -134,12 +153,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
     for (int b = b0; b < b1; ++b) {
       const PlanSeq s = seq(b);
       a.cu_new[b] = (int)min(at.tokens, (int64_t)INT_MAX);
-      const bool fits = s.need == 0 || at.pages + s.need <= count;
+      const bool fits = s.need <= count - at.given;
       if (!fits) errors |= IRS_DEVERR_PAGE;
       a.lens_out[b] = fits ? s.n + s.m : s.n;
-      at.pages += s.need;
       at.tokens += s.m;
-      if (fits && s.need > 0) granted = (int)at.pages;
+      if (fits) granted = at.given += s.need;
     }
     if (granted > 0) atomicMax(&sm_granted, granted);
     if (tid == 0) {
@@ -170,19 +188,23 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
       at.pages += s.need;
       at.tokens += s.m;
       at.shared += s.shared;
+      at.given += s.need <= count - at.given ? s.need : 0;
       s = seq(++b);
     }
     return b;
   };
   // Entry j of sequence b's table after this call.
-  auto entry = [&](int b, const PlanSeq& s, int64_t pages_before, int j) {
+  auto entry = [&](int b, const PlanSeq& s, int given_before, int j) {
     if (j < s.held) return a.page_table[(int64_t)b * a.table_stride + j];
-    if (pages_before + s.need > count) return -1;
-    return a.free_pages[count - 1 - (pages_before + j - s.held)];
+    if (s.need > count - given_before) return -1;
+    return a.free_pages[count - 1 - given_before - (j - s.held)];
   };
-  auto pages_before = [&](int b) {
-    int64_t p = sums[b / per].pages;
-    for (int i = b / per * per; i < b; ++i) p += seq(i).need;
+  auto given_before = [&](int b) {
+    int p = sums[b / per].given;
+    for (int i = b / per * per; i < b; ++i) {
+      const int need = seq(i).need;
+      p += need <= count - p ? need : 0;
+    }
     return p;
   };
 
@@ -203,7 +225,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
         const int b = find(i, &PlanSum::pages, &PlanSeq::need, s, at);
         const int j = s.held + (int)(i - at.pages);
         dst[u] = a.page_table + (int64_t)b * a.table_stride + j;
-        page[u] = entry(b, s, at.pages, j);
+        page[u] = entry(b, s, at.given, j);
       }
     }
 #pragma unroll
@@ -212,12 +234,12 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
   }
   for (int64_t i0 = me; i0 < all.shared; i0 += step) {
     int32_t* dst[kPlanItems];
-    int page[kPlanItems];
+    const int32_t* src[kPlanItems];   // the first sequence's entry, in its row or in the list of free pages
 #pragma unroll
     for (int u = 0; u < kPlanItems; ++u) {
       const int64_t i = i0 + u * kPlanThreads;
+      src[u] = nullptr;
       dst[u] = nullptr;
-      page[u] = -1;
       if (i < all.shared) {
         PlanSeq s;
         PlanSum at;
@@ -226,23 +248,24 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
         int first = 0;
         plan_group(cu, a.P, b, &first);
         const PlanSeq f = seq(first);
+        const int32_t* row = a.page_table + (int64_t)first * a.table_stride + j;
+        dst[u] = a.page_table + (int64_t)b * a.table_stride + j;
         // A page that the first sequence has not, finds none for or does not fill in this step it does not give.
         const int end = (j + 1) * a.page_size;   // at most the prefix's length
-        bool gives = j < f.held && end <= f.n;
-        int64_t before = 0;
-        if (!gives && j < f.held + f.need && end <= f.n + f.m) {
-          before = pages_before(first);
-          gives = f.need == 0 || before + f.need <= count;
-        }
-        if (gives) {
-          dst[u] = a.page_table + (int64_t)b * a.table_stride + j;
-          page[u] = entry(first, f, before, j);
+        if (j < f.held && end <= f.n) {
+          src[u] = row;
+        } else if (j < f.held + f.need && end <= f.n + f.m) {
+          const int before = given_before(first);
+          if (f.need <= count - before) src[u] = j < f.held ? row : a.free_pages + count - 1 - before - (j - f.held);
         }
       }
     }
+    int page[kPlanItems];
+#pragma unroll
+    for (int u = 0; u < kPlanItems; ++u) page[u] = src[u] != nullptr ? *src[u] : -1;
 #pragma unroll
     for (int u = 0; u < kPlanItems; ++u)
-      if (dst[u] != nullptr) *dst[u] = page[u];
+      if (src[u] != nullptr) *dst[u] = page[u];
   }
   for (int64_t i0 = me; i0 < a.tokens; i0 += step) {
     int pos[kPlanItems], page[kPlanItems];
@@ -255,7 +278,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
         PlanSum at;
         const int b = find(i, &PlanSum::tokens, &PlanSeq::m, s, at);
         pos[u] = s.n + (int)(i - at.tokens);
-        if (s.need == 0 || at.pages + s.need <= count) page[u] = entry(b, s, at.pages, plan_page(a, pos[u]));
+        if (s.need <= count - at.given) page[u] = entry(b, s, at.given, plan_page(a, pos[u]));
       }
     }
 #pragma unroll

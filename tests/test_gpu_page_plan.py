@@ -54,3 +54,12 @@ def test_pages_that_the_first_sequence_fills_in_part_are_not_given(irs, n, m, gi
     row = [20, 21, 22][: -(-n // 16)]
     ref = _check(irs, [n, 40], [m, 1], [row + [-1] * (4 - len(row)), [7, 8, 9, -1]], [1, 2, 3, 4], 16, [0, 2], [32])
     assert ref[0][1] == ref[0][0][:given] + [7, 8, 9][given:] + [-1]
+
+
+def test_a_refused_sequence_takes_no_pages_from_those_behind_it(irs):
+    ref = _check(irs, [0, 16, 3, 15], [160, 1, 0, 40], [[-1] * 10, [9] + [-1] * 9, [8] + [-1] * 9, [7] + [-1] * 9], [1, 2, 3, 4, 5], 16)
+    assert ref[4] == [0, 17, 3, 55] and ref[5] == 1 and ref[0][1][:2] == [9, 5] and ref[0][3][:4] == [7, 4, 3, 2]
+    # refused ones between others, and one that finds none at all
+    _check(irs, [0, 0, 0, 0, 0], [33, 16, 65, 16, 1], [[-1] * 5] * 5, [1, 2, 3, 4, 5], 16)
+    # a follower whose first sequence is given its pages behind a refused one
+    _check(irs, [0, 0, 40], [100, 40, 1], [[-1] * 7, [-1] * 7, [7, 8, 9] + [-1] * 4], [1, 2, 3], 16, [0, 1, 3], [96, 32])
