@@ -32,6 +32,7 @@ namespace {
 
 constexpr int kPlanThreads = 256;
 constexpr int kPlanItems = 4;        // items a thread has in hand
+constexpr int kPlanCtas = 4;         // CTAs an SM
 constexpr int kPlanCached = 1024;    // sequences, and borders of groups, that a CTA keeps in shared memory; others are worked out again
 
 // What one sequence takes.
@@ -58,10 +59,14 @@ __device__ __forceinline__ PlanSeq plan_seq(const PlanArgs& a, const int32_t* cu
   s.n = __ldg(a.cache_lens + b);
   s.m = __ldg(a.new_lens + b);
   s.held = s.need = s.shared = 0;
-  if (s.n < 0 || s.m < 0 || s.n > reach || s.m > reach - s.n) {
+  if (s.n < 0 || s.n > reach) {   // holds nothing that is known
     *bad = true;
     s.m = 0;
     return s;
+  }
+  if (s.m < 0 || s.m > reach - s.n) {
+    *bad = true;
+    s.m = 0;
   }
   s.held = plan_page(a, s.n + a.page_size - 1);
   s.need = plan_page(a, s.n + s.m + a.page_size - 1) - s.held;
@@ -80,7 +85,7 @@ struct PlanSum {
   int given;
 };
 
-__global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
+__global__ void __launch_bounds__(kPlanThreads, kPlanCtas) plan_kernel(PlanArgs a) {
   __shared__ PlanSum sums[kPlanThreads];       // before each thread's run of sequences
   __shared__ PlanSum warp_sums[kPlanThreads / 32];
   __shared__ PlanSeq cached[kPlanCached];
@@ -301,7 +306,7 @@ cudaError_t launch_plan(PlanArgs a, int num_sms, cudaStream_t stream) {
   // tables that are shared may have as many entries as they have places
   const int64_t items = (int64_t)a.tokens + (a.P > 0 ? (int64_t)a.B * a.max_pages / 4 : 0);
   int64_t grid = (items + kPlanItems * kPlanThreads - 1) / (kPlanItems * kPlanThreads);
-  grid = grid < 1 ? 1 : grid > 4 * num_sms ? 4 * num_sms : grid;
+  grid = grid < 1 ? 1 : grid > kPlanCtas * num_sms ? kPlanCtas * num_sms : grid;
   plan_kernel<<<(unsigned)grid, kPlanThreads, 0, stream>>>(a);
   return cudaGetLastError();
 }

@@ -63,3 +63,10 @@ def test_a_refused_sequence_takes_no_pages_from_those_behind_it(irs):
     _check(irs, [0, 0, 0, 0, 0], [33, 16, 65, 16, 1], [[-1] * 5] * 5, [1, 2, 3, 4, 5], 16)
     # a follower whose first sequence is given its pages behind a refused one
     _check(irs, [0, 0, 40], [100, 40, 1], [[-1] * 7, [-1] * 7, [7, 8, 9] + [-1] * 4], [1, 2, 3], 16, [0, 1, 3], [96, 32])
+
+
+def test_a_length_past_the_table_refuses_new_tokens_and_nothing_else(irs):
+    """A sequence whose new tokens are refused for their number holds, gives and takes pages of a prefix as ever."""
+    table = [[4, 5, 6], [-1, -1, 9], [-1, -1, 8], [-1, -1, -1]]
+    ref = _check(irs, [40, 40, 40, 60], [20, 1, -3, 1], table, [1, 2], 16, [0, 4], [32])
+    assert [r[:2] for r in ref[0]] == [[4, 5], [4, 5], [4, 5], [-1, -1]] and ref[4] == [40, 41, 40, 60]
