@@ -658,8 +658,10 @@ irs_status irs_window_gqa_attn_bwd(const void* q, int64_t q_stride_t, int64_t q_
  * cu_groups[g] .. cu_groups[g+1], whose first prefix_lens[g] tokens are the same) every
  * sequence behind its group's first whose own n covers the prefix takes that one's entries of
  * the pages that the prefix fills, prefix_lens[g] / page_size of them: of these the pages that
- * the first's tokens fill, this step's among them. Entries that it does not give stay as they
- * are; a page that a prefix fills in part is each sequence's own.
+ * the first's tokens fill, this step's among them, or, where the first is idle (n = m = 0), those
+ * that its row names: irs_shared_prefix_gqa_attn_decode reads the prefix through that row too.
+ * Entries that it does not give, and those below 0, leave the others' as they are; a page that a
+ * prefix fills in part is each sequence's own.
  * Results, beside the entries of page_table:
  *   cu_new    int32 [B + 1]     exclusive sums of new_lens, as irs_paged_rope_append takes them
  *   positions int32 [tokens]    of each new token in its sequence

@@ -1031,12 +1031,15 @@ def paged_plan(cache_lens: torch.Tensor, new_lens: torch.Tensor, page_table: tor
     need are entered; free_pages int32 [n], of which the first free_count (int32 [1]) are free
     and are given out from the end; tokens: rows of the results for tokens, at least the sum of
     new_lens (a padded batch has more: -1). With cu_groups int32 [P + 1] and prefix_lens int32
-    [P] the sequences behind a group's first take its entries of the pages that the prefix fills.
+    [P] the sequences behind a group's first whose lengths cover the prefix take its entries of the
+    pages that the prefix fills: of those that its tokens fill with this step's, or, where it is
+    idle, that its row names.
 
     Returns cu_new and positions, which `paged_rope_append` and `rope` take, slots (rows of a
     pool seen as [pages * page_size, ...]), and the lengths and free pages after the step. The
     inputs are not changed, so results replace them by the caller's hand. A sequence that finds
-    too few free pages gets none, keeps its length and sets DEVERR_PAGE.
+    too few free pages gets none, keeps its length and sets DEVERR_PAGE; those behind it may find
+    enough.
     """
     index = _first(cache_lens, "cache_lens", _I32)
     (B,), _ = _look(cache_lens, "cache_lens", _I32, 1, index)

@@ -255,9 +255,10 @@ __global__ void __launch_bounds__(kPlanThreads, kPlanCtas) plan_kernel(PlanArgs 
         const PlanSeq f = seq(first);
         const int32_t* row = a.page_table + (int64_t)first * a.table_stride + j;
         dst[u] = a.page_table + (int64_t)b * a.table_stride + j;
-        // A page that the first sequence has not, finds none for or does not fill in this step it does not give.
+        // A page that the first sequence has not, finds none for or does not fill in this step it does not give; an
+        // idle one gives what its row names, as the decode reads it.
         const int end = (j + 1) * a.page_size;   // at most the prefix's length
-        if (j < f.held && end <= f.n) {
+        if ((j < f.held && end <= f.n) || (f.n == 0 && f.m == 0)) {
           src[u] = row;
         } else if (j < f.held + f.need && end <= f.n + f.m) {
           const int before = given_before(first);
@@ -270,7 +271,7 @@ __global__ void __launch_bounds__(kPlanThreads, kPlanCtas) plan_kernel(PlanArgs 
     for (int u = 0; u < kPlanItems; ++u) page[u] = src[u] != nullptr ? *src[u] : -1;
 #pragma unroll
     for (int u = 0; u < kPlanItems; ++u)
-      if (src[u] != nullptr) *dst[u] = page[u];
+      if (page[u] >= 0) *dst[u] = page[u];   // an entry below 0 is no page
   }
   for (int64_t i0 = me; i0 < a.tokens; i0 += step) {
     int pos[kPlanItems], page[kPlanItems];

@@ -70,3 +70,44 @@ def test_a_length_past_the_table_refuses_new_tokens_and_nothing_else(irs):
     table = [[4, 5, 6], [-1, -1, 9], [-1, -1, 8], [-1, -1, -1]]
     ref = _check(irs, [40, 40, 40, 60], [20, 1, -3, 1], table, [1, 2], 16, [0, 4], [32])
     assert [r[:2] for r in ref[0]] == [[4, 5], [4, 5], [4, 5], [-1, -1]] and ref[4] == [40, 41, 40, 60]
+
+
+def test_an_idle_first_sequence_gives_what_its_row_names(irs):
+    """As the decode reads a prefix: through the first sequence's row, idle or not; entries below 0 are not given."""
+    ref = _check(irs, [0, 40, 32], [0, 1, 20], [[3, 4, -1, -1], [-1, -1, 9, -1], [-1] * 4], [1, 2], 16, [0, 3], [32])
+    assert ref[0] == [[3, 4, -1, -1], [3, 4, 9, -1], [3, 4, 2, 1]]
+    ref = _check(irs, [0, 40], [0, 1], [[3, -1, -1], [7, 8, 9]], [1], 16, [0, 2], [32])
+    assert ref[0][1] == [3, 8, 9]
+
+
+@pytest.mark.parametrize("B,page,seed", [(1, 16, 0), (5, 16, 1), (7, 1, 2), (40, 16, 3), (257, 48, 4), (300, 4, 5), (1100, 16, 6),
+                                         (3000, 1, 7)])
+@pytest.mark.parametrize("groups", [0, 1, 6])
+def test_plans_that_run_short(irs, B, page, seed, groups):
+    """Ragged requests, idle and unknown ones among them, and pages for a third to all of them."""
+    g = torch.Generator().manual_seed(seed * 10 + groups)
+
+    def pick(lo, hi):
+        return int(torch.randint(lo, hi + 1, (1,), generator=g))
+
+    width = max(2, 120 // page)
+    reach = width * page
+    for share in (0.0, 0.35, 0.7, 1.0):
+        lens = [pick(0, reach * 3 // 4) if pick(0, 3) else 0 for _ in range(B)]
+        new = [min(pick(0, 2 if pick(0, 2) else reach // 2), reach - n) if pick(0, 3) else 0 for n in lens]
+        if B > 4:
+            lens[B // 2], new[B // 3], lens[B - 1] = -1, -2, reach + 1
+        held = [-(-n // page) if 0 <= n <= reach else 0 for n in lens]
+        need = sum(-(-(n + m) // page) - h for n, m, h in zip(lens, new, held) if 0 <= n and m >= 0 and n + m <= reach)
+        order = torch.randperm(sum(held) + need + 3, generator=g).tolist()
+        table = [[-1] * width for _ in lens]
+        at = 0
+        for row, h in zip(table, held):
+            row[:h] = order[at: at + h]
+            at += h
+        free = order[at:]
+        cuts = prefix = None
+        if groups:
+            cuts = [0] + sorted(pick(0, B) for _ in range(groups))
+            prefix = [pick(0, reach // 2) for _ in range(groups)]
+        _check(irs, lens, new, table, free, page, cuts, prefix, count=int(share * len(free)), tokens=sum(max(m, 0) for m in new) + 5)
