@@ -698,7 +698,8 @@ irs_status irs_paged_plan(const int32_t* cache_lens, const int32_t* new_lens, in
  * and with own_out and own_lse, the attention of the same tokens over other keys (their own
  * prompt: irs_window_gqa_attn_fwd with a window that covers it), the two are joined:
  *   lse = ln(e^lse_p + e^own_lse),  out = e^(lse_p - lse) out_p + e^(own_lse - lse) own_out
- * A part whose lse is -inf does not count, whatever its output holds.
+ * A part whose lse is -inf does not count, whatever its output holds; a prefix whose scores are
+ * all -inf neither, beside a part that counts (alone it gives NaN).
  * Rows behind cu_rows[P] belong to no group and are left as they were.
  *
  * q           bf16 [T, Hq, Dqk] by strides;  caches as for irs_paged_rope_append

@@ -124,19 +124,17 @@ struct PrefixJoin {
   float mine, theirs, lse;
 };
 __device__ __forceinline__ PrefixJoin prefix_join_own(const PrefixArgs& a, int64_t row, float m, float l) {
-  if (l < 0.f) l = NAN;
+  const float other = a.own_lse != nullptr ? a.own_lse[row] : -INFINITY;
+  if (l < 0.f) l = other != -INFINITY ? 0.f : NAN;   // beside a part that counts a weight of 0, alone 0 / 0
   PrefixJoin j;
   j.lse = l == 0.f ? -INFINITY : fmaf(m, 0.6931471805599453f, logf(l));
   j.mine = l == 0.f ? 0.f : 1.f / l;
   j.theirs = 0.f;
-  if (a.own_lse != nullptr) {
-    const float other = a.own_lse[row];
-    if (other != -INFINITY) {
-      const float M = fmaxf(j.lse, other), x = j.lse == -INFINITY ? 0.f : expf(j.lse - M), y = expf(other - M);
-      j.mine *= x / (x + y);
-      j.theirs = y / (x + y);
-      j.lse = M + logf(x + y);
-    }
+  if (other != -INFINITY) {
+    const float M = fmaxf(j.lse, other), x = j.lse == -INFINITY ? 0.f : expf(j.lse - M), y = expf(other - M);
+    j.mine *= x / (x + y);
+    j.theirs = y / (x + y);
+    j.lse = M + logf(x + y);
   }
   return j;
 }
