@@ -1,8 +1,11 @@
-"""Where shared-prefix attention joins a prefix's part with others, on the GPU: prefixes whose scores are all -inf."""
+"""Where shared-prefix attention joins a prefix's part with others, on the GPU: prefixes whose scores are all -inf, and
+results that take their other part's place in rows that runs' borders cut."""
 import math
 
 import pytest
 import torch
+
+import prefix_ref as R
 
 pytestmark = pytest.mark.gpu
 DEV = torch.device("cuda", 0)
@@ -54,3 +57,19 @@ def test_prompts_a_prefix_of_minus_infinity_leaves_the_own_part(irs, n, Dv):
     # weight 1 on the own part: its own bits
     assert torch.equal(out[~none], own[0][~none]) and torch.equal(lse[~none], own[1][~none])
     assert out[none].isnan().all() and lse[none].isnan().all()
+
+
+@pytest.mark.parametrize("Hq,Hkv,Dqk,Dv", [(16, 2, 128, 128), (16, 2, 64, 64), (32, 2, 192, 128), (5, 1, 128, 64)])
+def test_prompts_in_place_where_borders_cut_items(irs, Hq, Hkv, Dqk, Dv):
+    """out and lse in own's place: rows of items that several runs share, and of a group whose prefix is empty."""
+    rows, prefix = [700, 333, 900, 1], [3001, 0, 2500, 0]
+    q, kc, vc, table, cu, own = _inputs(Hq + Dv, rows, prefix, Hq, Hkv, Dqk, Dv)
+    out, lse = irs.shared_prefix_gqa_attn_fwd(q, kc, vc, table, _i32(cu), _i32(prefix), own=own)
+    ref = R.fwd(q, kc, vc, table, cu, prefix, 1 / math.sqrt(Dqk), own)
+    R.check(out, ref[0], ref[2], "out")
+    R.check(lse, ref[1], ref[3], "lse")
+    for _ in range(5):
+        a, b = own[0].clone(), own[1].clone()
+        irs.shared_prefix_gqa_attn_fwd(q, kc, vc, table, _i32(cu), _i32(prefix), own=(a, b), out=a, lse=b)
+        assert torch.equal(a, out) and torch.equal(b, lse)
+    irs.check_device_errors(DEV)
