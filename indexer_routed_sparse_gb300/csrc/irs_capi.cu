@@ -1079,7 +1079,7 @@ Span span_of(const void* p, int T, int heads, int row) { return span_of(p, T, (i
 // Kernels read their inputs again after the first outputs are written.
 bool meets(const Span& out, std::initializer_list<Span> others) {
   for (const Span& o : others)
-    if (out.from < o.to && o.from < out.to) return true;
+    if (out.from < out.to && o.from < o.to && out.from < o.to && o.from < out.to) return true;   // an empty one meets none
   return false;
 }
 
