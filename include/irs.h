@@ -713,9 +713,11 @@ irs_status irs_paged_plan(const int32_t* cache_lens, const int32_t* new_lens, in
  * sizes: P >= 1, Hq % Hkv == 0, Hq / Hkv <= 128, Hkv <= 1024, T * Hq < 2^31, Dqk in {64, 128, 192},
  *        Dv in {64, 128}, rows 16-byte aligned, max_pages * page_size <= 2^30, scale > 0 (finite);
  *        T = 0 does nothing
- * out         bf16 [T, Hq, Dv] contiguous, apart from q;  lse  fp32 [T, Hq] (may be NULL)
+ * out         bf16 [T, Hq, Dv] contiguous;  lse  fp32 [T, Hq] (may be NULL)
  * workspace   irs_shared_prefix_gqa_attn_fwd_workspace_bytes(...) bytes, 256-byte aligned; nothing
  *             in it outlives the call, and calls that may overlap need one each
+ * out, lse and the workspace overlap neither inputs (but for own_out and own_lse, as said) nor one
+ * another.
  * Results do not depend on the run: the split over the prefixes is fixed by the sizes and
  * lengths, and its parts are joined in order.
  */

@@ -1295,6 +1295,41 @@ irs_status prefix_args(irs::PrefixArgs* a, const void* q, int64_t q_stride_t, in
   return IRS_OK;
 }
 
+// CTAs read inputs while others write, and a call's kernels overlap: outputs and the workspace (`need` bytes of it) lie over
+// neither inputs nor one another. A row of own_out or own_lse is read by those who write that row, so out and lse may be these.
+irs_status prefix_apart(const irs::PrefixArgs& a, size_t need) {
+  struct Named {
+    const char* name;
+    Span span;
+  };
+  auto pool = [&](const void* p, int64_t sp, int64_t st, int64_t sh, int row) {
+    return bytes_of(p, 2 * ((a.num_pages - 1) * sp + (a.page_size - 1) * st + (a.Hkv - 1) * sh + row));
+  };
+  const int rows = a.cache_lens != nullptr ? a.T : a.P;   // of the page table
+  const int64_t n = (int64_t)a.T * a.Hq;
+  const Named in[] = {{"q", span_of(a.q, a.T, a.q_st, a.Hq, a.q_sh, a.Dqk)},
+                      {"k_cache", pool(a.k, a.k_sp, a.k_st, a.k_sh, a.Dqk)},
+                      {"v_cache", pool(a.v, a.v_sp, a.v_st, a.v_sh, a.Dv)},
+                      {"page_table", bytes_of(a.page_table, 4 * ((rows - 1) * a.table_stride + a.max_pages))},
+                      {"cu", bytes_of(a.cu, 4 * ((int64_t)a.P + 1))},
+                      {"prefix_lens", bytes_of(a.prefix_lens, 4 * (int64_t)a.P)},
+                      {"cache_lens", bytes_of(a.cache_lens, a.cache_lens != nullptr ? 4 * (int64_t)a.T : 0)},
+                      {"own_out", bytes_of(a.own_out, a.own_out != nullptr ? 2 * n * a.Dv : 0)},
+                      {"own_lse", bytes_of(a.own_lse, a.own_lse != nullptr ? 4 * n : 0)}};
+  const Named out[] = {{"out", bytes_of(a.out, 2 * n * a.Dv)},
+                       {"lse", bytes_of(a.lse, a.lse != nullptr ? 4 * n : 0)},
+                       {"workspace", bytes_of(a.ws, (int64_t)need)}};
+  for (int i = 0; i < 3; ++i) {
+    for (int k = 0; k < 9; ++k) {
+      const bool same = (i == 0 && k == 7 && a.out == a.own_out) || (i == 1 && k == 8 && a.lse == a.own_lse);
+      if (!same && meets(out[i].span, {in[k].span})) return fail(IRS_ERR_VALUE, "%s overlaps %s", out[i].name, in[k].name);
+    }
+    for (int j = 0; j < i; ++j)
+      if (meets(out[i].span, {out[j].span})) return fail(IRS_ERR_VALUE, "%s overlaps %s", out[i].name, out[j].name);
+  }
+  return IRS_OK;
+}
+
 // 4-D bf16 map of a pool [pages][heads][positions][D], boxes of 64 dims x `chunk` positions; false where
 // a stride cannot be a map's.
 irs_status make_pool_map(CUtensorMap* m, const void* base, int D, const irs::PrefixArgs& a, int64_t sp, int64_t st, int64_t sh,
@@ -1365,10 +1400,11 @@ irs_status irs_shared_prefix_gqa_attn_fwd(const void* q, int64_t q_stride_t, int
   if (own_lse != nullptr && lse != nullptr && own_lse != lse &&
       meets(bytes_of(lse, 4LL * T * Hq), {bytes_of(own_lse, 4LL * T * Hq)}))
     return fail(IRS_ERR_VALUE, "lse overlaps own_lse row by other row");
-  DeviceInfo* dev = nullptr;
-  if ((s = current_device(&dev)) != IRS_OK) return s;
   a.own_out = static_cast<const __nv_bfloat16*>(own_out);
   a.own_lse = own_lse;
+  if ((s = prefix_apart(a, need)) != IRS_OK) return s;
+  DeviceInfo* dev = nullptr;
+  if ((s = current_device(&dev)) != IRS_OK) return s;
   irs::PrefixMaps m;
   if ((s = prefix_maps(&m, a)) != IRS_OK) return s;
   std::lock_guard<std::mutex> lk(g_dev_mu);
@@ -1397,9 +1433,10 @@ irs_status irs_shared_prefix_gqa_attn_decode(const void* q, int64_t q_stride_b, 
                              need, true, err_flag);
   if (s != IRS_OK || B == 0) return s;
   if (!cache_lens) return fail(IRS_ERR_VALUE, "NULL cache pointer");
+  a.cache_lens = cache_lens;
+  if ((s = prefix_apart(a, need)) != IRS_OK) return s;
   DeviceInfo* dev = nullptr;
   if ((s = current_device(&dev)) != IRS_OK) return s;
-  a.cache_lens = cache_lens;
   irs::PrefixMaps m;
   if ((s = prefix_maps(&m, a)) != IRS_OK) return s;
   std::lock_guard<std::mutex> lk(g_dev_mu);
