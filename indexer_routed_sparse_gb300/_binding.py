@@ -1054,8 +1054,8 @@ def paged_plan(cache_lens: torch.Tensor, new_lens: torch.Tensor, page_table: tor
         cu, pl, P = _groups(cu_groups, prefix_lens, "cu_groups", index)
     elif cu_groups is not prefix_lens:
         raise ValueError("cu_groups and prefix_lens come together")
-    if tokens < 0:
-        raise ValueError("tokens must not be negative")
+    if not (0 <= tokens < 1 << 31 and 0 < page_size < 1 << 31):   # a C int cuts more bits off
+        raise ValueError(f"tokens must be in [0, 2^31) and page_size in [1, 2^31), got {tokens} and {page_size}")
     if out is None:   # two allocations and a split: five allocations cost the host twice as much
         whole = torch.empty(2 * B + 2 + tokens, dtype=_I32, device=index)
         slots = torch.empty(tokens, dtype=torch.int64, device=index)

@@ -111,3 +111,11 @@ def test_plans_that_run_short(irs, B, page, seed, groups):
             cuts = [0] + sorted(pick(0, B) for _ in range(groups))
             prefix = [pick(0, reach // 2) for _ in range(groups)]
         _check(irs, lens, new, table, free, page, cuts, prefix, count=int(share * len(free)), tokens=sum(max(m, 0) for m in new) + 5)
+
+
+def test_sizes_past_32_bits_are_refused(irs):
+    """Of 2^32 + 16 a C int keeps 16."""
+    args = _i32([3]), _i32([1]), _i32([[0, -1]]), _i32([5]), _i32([1])
+    for page, tokens in (((1 << 32) + 16, 1), (16, 1 << 40), (16, -1), (0, 1), (-16, 1)):
+        with pytest.raises(ValueError):
+            irs.paged_plan(*args, page, tokens)
