@@ -138,13 +138,28 @@ __global__ void __launch_bounds__(kPlanThreads, kPlanCtas) plan_kernel(PlanArgs 
   if (all.pages > count) {   // too few pages: what is given before each run of sequences, one after the other
     if (warp == 0) {
       int given = 0;
-      for (int c = 0; c < a.B; c += 32) {
-        const int need = c + lane < a.B ? seq(c + lane).need : 0;
-        for (int i = 0; i < 32 && c + i < a.B; ++i) {
-          if (lane == 0 && (c + i) % per == 0) sums[(c + i) / per].given = given;
-          const int x = __shfl_sync(0xffffffffu, need, i);
-          given += x <= count - given ? x : 0;
+      auto need_of = [&](int b) { return b < a.B ? seq(b).need : 0; };
+      int next = need_of(lane);
+      for (int c = 0; c < a.B; c += 32) {   // 32 sequences at a time; next: of the following ones, looked up ahead
+        const int need = next, b = c + lane;
+        next = need_of(b + 32);
+        int before = 0;
+        for (int from = 0; from < 32;) {    // those from `from` on up to the first that finds too few
+          const int left = count - given;
+          const int want = lane >= from && need <= left ? need : 0;
+          int64_t sum = want;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += y;
+          }
+          if (lane >= from) before = given + (int)min(sum - want, (int64_t)left);
+          const unsigned over = __ballot_sync(0xffffffffu, sum > left && want > 0);
+          const int stop = over != 0 ? __ffs((int)over) - 1 : 31;
+          given += (int)__shfl_sync(0xffffffffu, over != 0 ? sum - want : sum, stop);
+          from = stop + 1;
         }
+        if (b < a.B && b % per == 0) sums[b / per].given = before;
       }
     }
     __syncthreads();

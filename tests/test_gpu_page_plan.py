@@ -119,3 +119,11 @@ def test_sizes_past_32_bits_are_refused(irs):
     for page, tokens in (((1 << 32) + 16, 1), (16, 1 << 40), (16, -1), (0, 1), (-16, 1)):
         with pytest.raises(ValueError):
             irs.paged_plan(*args, page, tokens)
+
+
+@pytest.mark.parametrize("B", [31, 33, 64, 700, 2100])
+@pytest.mark.parametrize("free", [0, 1, 7, 40, 300])
+def test_many_that_find_too_few(irs, B, free):
+    """Needs in cycles, falling, scattered and alike: refusals lie among those that fit."""
+    for needs in ([1 + i % 5 for i in range(B)], [max(1, 60 - i) for i in range(B)], [1 + (i * 7919) % 60 for i in range(B)], [50] * B):
+        _check(irs, [0] * B, needs, [[-1] * max(needs)] * B, list(range(free)), 1)
