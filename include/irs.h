@@ -694,7 +694,8 @@ irs_status irs_paged_plan(const int32_t* cache_lens, const int32_t* new_lens, in
  * a set that many rows share: the prefix's keys and values are read once for all of them. The
  * tokens cu_rows[g] .. cu_rows[g+1] attend every position of [0, prefix_lens[g]) of prefix g,
  * whose pages are row g of page_table:
- *   out, lse as for irs_paged_gqa_attn_decode over that set (an empty one: 0 and -inf)
+ *   out, lse as for irs_paged_gqa_attn_decode over that set (an empty one: 0 and -inf), but for a
+ *   weight's rounding: to bf16 (8 bits) for its product with a value, where that one keeps 16 bits
  * and with own_out and own_lse, the attention of the same tokens over other keys (their own
  * prompt: irs_window_gqa_attn_fwd with a window that covers it), the two are joined:
  *   lse = ln(e^lse_p + e^own_lse),  out = e^(lse_p - lse) out_p + e^(own_lse - lse) own_out
@@ -715,7 +716,8 @@ irs_status irs_paged_plan(const int32_t* cache_lens, const int32_t* new_lens, in
  *        T = 0 does nothing
  * out         bf16 [T, Hq, Dv] contiguous;  lse  fp32 [T, Hq] (may be NULL)
  * workspace   irs_shared_prefix_gqa_attn_fwd_workspace_bytes(...) bytes, 256-byte aligned; nothing
- *             in it outlives the call, and calls that may overlap need one each
+ *             in it outlives the call, and calls that may overlap need one each. Two parts a CTA,
+ *             whatever T is: 21 MB with Dv = 64, 43 with 128
  * out, lse and the workspace overlap neither inputs (but for own_out and own_lse, as said) nor one
  * another.
  * Results do not depend on the run: the split over the prefixes is fixed by the sizes and
@@ -740,7 +742,13 @@ irs_status irs_shared_prefix_gqa_attn_fwd(const void* q, int64_t q_stride_t, int
  * hold the same keys and values and are read through the page table's row of the group's first
  * sequence, which has to name the prefix's pages even where that sequence is idle; the positions
  * behind them through each sequence's own row. cache_lens counts both.
- * Sequences behind cu_groups[P] share nothing. A length of 0 (an idle slot) gives out = 0 and
+ * Sequences behind cu_groups[P] share nothing; for a step without groups, P = 1 and cu_groups (0, 0).
+ * Weights of prefix positions are rounded to bf16 as above, those of own positions keep 16 bits.
+ * It pays where some 100 MB of keys and values or more need not be read again, 2 Hkv (Dqk + Dv) bytes a
+ * position of every sequence behind its group's first: 8 sequences behind 4000 positions of 8 KV heads
+ * of 128. Below that, with two sequences a group and with many groups of less than 1000
+ * positions irs_paged_gqa_attn_decode is as fast or faster (14 to 20 us for 17 to 23 at the smallest).
+ * A length of 0 (an idle slot) gives out = 0 and
  * lse = -inf; so does one below 0, past max_pages * page_size or shorter than its group's
  * prefix, which sets IRS_DEVERR_PAGE.
  * An own position whose page lies outside the pool is skipped (IRS_DEVERR_PAGE); with such a page

@@ -1102,6 +1102,7 @@ def shared_prefix_gqa_attn_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: 
     prefix g's prefix_lens[g] (int32 [P]) positions. own: (out, lse) of the same tokens over
     other keys, such as `window_gqa_attn_fwd` over their own prompts; the result is then the
     attention over both sets. out and lse may be own's. Rows behind cu_rows[P] are left alone.
+    Weights are rounded to bf16.
     """
     index = _first(q, "q", _BF16)
     (T, Hq, Dqk), (qt, qh, _) = _look(q, "q", _BF16, 3, index)
@@ -1144,8 +1145,12 @@ def shared_prefix_gqa_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cach
     cu_groups int32 [P + 1]: the sequences cu_groups[g] .. cu_groups[g+1] hold the same keys and
     values at their first prefix_lens[g] (int32 [P]) positions, which are read through the page
     table's row of the group's first sequence (idle or not); the positions behind them through each
-    sequence's own. cache_lens counts both. Sequences behind the last group share nothing. A length of 0 (an
-    idle slot) gives out = 0 and lse = -inf.
+    sequence's own. cache_lens counts both. Sequences behind the last group share nothing; in a step
+    without groups cu_groups is (0, 0). A length of 0 (an idle slot) gives out = 0 and lse = -inf.
+
+    Weights of prefix positions are rounded to bf16; `paged_gqa_attn_decode` keeps 16 bits of every weight. That
+    one, over each sequence's whole table, is as fast or faster where less than some 100 MB of keys and values need
+    not be read again, with two sequences a group, and with many groups of less than 1000 positions.
     """
     index = _first(q, "q", _BF16)
     qshape, (qb, qh, _) = _look(q, "q", _BF16, 3, index)

@@ -18,9 +18,10 @@
 // than are free, a warp goes through the sequences in order, to know what is given before each run. What is known of the first
 // 1024 sequences stays in shared memory (480 sequences that share 7 prompts: 23 us without, 12 with).
 //
-// Measured (device time, replayed from a graph): 64 sequences, one token each, 6.3 us; 480 that share 7
-// prompts 12.4; 48 prompts of 2000 to 60,000 tokens (16 MB) 14.4 us, 1.1 TB/s behind the
-// same chain of lengths, sums, search and page that is all of the first. Launched alone, the host's 30 us.
+// Measured (device time, replayed from a graph): 64 sequences, one token each, 6.2 us; 480 that share 7
+// prompts 12.3; 48 prompts of 2000 to 60,000 tokens (16 MB) 14.3 us, 1.1 TB/s behind the
+// same chain of lengths, sums, search and page that is all of the first. Launched alone, the host's 30 us. 480
+// sequences of 40 tokens each 10.3 us, and 14.5 where pages run out.
 #include <climits>
 
 #include "irs_internal.h"

@@ -57,7 +57,7 @@ constexpr int kRows = 128;              // rows a tile
 constexpr uint32_t kAtom = 128 * 128;   // 128 rows x 64 bf16
 // warps 0-3, 4-7: softmax of the two tiles, a thread a row; 8: list, queries and keys; 9: values; 10, 11: products
 // of the two tiles. Registers: 384 x 168 at launch, of which the softmax's threads take 208
-// and the others keep 88: 256 x 208 + 128 x 88 = 384 x 168.
+// and the others keep 88: 256 x 208 + 128 x 88 = 384 x 168. At 64 and 128 dims 28 to 36 bytes a thread are spilled all the same.
 constexpr int kThreads = 384;
 constexpr float kRaise = 256.f;         // half a block's weights of a row with a sum past this raise its maximum
 constexpr int kPlanReaders = 11;        // warps that read an item's plan
@@ -427,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         } else {
           // rows by address: strides that no map can have
-            const uint32_t dst = smem_u32(smem) + x * C::q_bytes;
+          const uint32_t dst = smem_u32(smem) + x * C::q_bytes;
           const int c8 = lane & 7;
           for (int r = lane >> 3; r < kRows; r += 4) {
             const int tq = t + r / a.G;
